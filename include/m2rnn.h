@@ -93,7 +93,8 @@ typedef struct {
 } m2rnn_shape;
 
 /* Library version (major*10000 + minor*100 + patch). */
-int m2rnn_version(void);  /* 200 and later: m2rnn_shape carries Nq; 201: M2RNN_ERR_BOUNDS */
+int m2rnn_version(void);  /* 200 and later: m2rnn_shape carries Nq; 201: M2RNN_ERR_BOUNDS;
+                                 202: the operators of m2rnn_block.h */
 
 /* 1 for the checked build (libm2rnn_check.so), 0 for the normal one.  The
  * checked build compiles the same kernels with an index check in front of

@@ -77,6 +77,15 @@ int check_shape(const m2rnn_shape* s) { return m2rnn::validate_shape(s); }
 }  // namespace
 
 namespace m2rnn {
+int host_device_info(int* dev, int** status, int* sms) { return device_info(dev, status, sms); }
+int host_check_ptr(const void* p, int dev, bool required) { return check_ptr(p, dev, required); }
+int host_check_elem_ptr(const void* p, int dev, size_t unit) {
+  if (p == nullptr) return M2RNN_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(p) % unit != 0) return M2RNN_ERR_MISALIGNED;
+  // the device test on the 16-byte block that holds the element
+  return check_ptr(reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t{15}),
+                   dev, true);
+}
 int validate_shape(const m2rnn_shape* s) {
   if (s == nullptr) return M2RNN_ERR_INVALID_ARG;
   if (s->B < 1 || s->N < 1 || s->T < 0 || s->ckpt_every < 0) return M2RNN_ERR_INVALID_ARG;
@@ -500,7 +509,7 @@ int decode_impl(const m2rnn_shape* s, const void* q, const void* k, const void* 
 
 extern "C" {
 
-int m2rnn_version(void) { return 201; }
+int m2rnn_version(void) { return 202; }
 
 int m2rnn_checked(void) { return M2RNN_CHECK ? 1 : 0; }
 

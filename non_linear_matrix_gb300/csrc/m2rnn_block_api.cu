@@ -1,0 +1,385 @@
+// m2rnn_block_api.cu -- the extern "C" entry points declared in
+// include/m2rnn_block.h: argument validation and launch planning of the
+// convolution, the q/k norm and the selective scan.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "m2rnn_block.h"
+#include "m2rnn_check.cuh"
+
+namespace {
+
+using m2rnn::host_check_ptr;
+using m2rnn::host_device_info;
+
+int status_from_cuda(cudaError_t e) { return e == cudaSuccess ? M2RNN_OK : M2RNN_ERR_CUDA; }
+
+bool is_dtype(int d) { return d == M2RNN_F32 || d == M2RNN_BF16; }
+size_t esize(int dtype) { return dtype == M2RNN_F32 ? 4 : 2; }
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// A row description (NULL: contiguous rows of `width` elements); distances
+// must keep rows on `unit`-byte boundaries.
+int read_rows(const m2rnn_rows* r, int T, long long width, int dtype, long long unit,
+              m2rnn_rows* out) {
+  if (r == nullptr) {
+    out->token = width;
+    out->batch = width * T;
+    return M2RNN_OK;
+  }
+  if (r->batch < 0 || r->token < 0) return M2RNN_ERR_INVALID_ARG;
+  const long long e = static_cast<long long>(esize(dtype));
+  if ((r->batch * e) % unit != 0 || (r->token * e) % unit != 0) return M2RNN_ERR_MISALIGNED;
+  *out = *r;
+  return M2RNN_OK;
+}
+
+bool overlap(const void* a, const void* b, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bytes && y < x + bytes;
+}
+
+int check_all(const void* const* ptrs, int n, int dev, bool required) {
+  for (int i = 0; i < n; ++i) {
+    const int rc = host_check_ptr(ptrs[i], dev, required);
+    if (rc != M2RNN_OK) return rc;
+  }
+  return M2RNN_OK;
+}
+template <int N>
+int require(const void* const (&ptrs)[N], int dev) {
+  return check_all(ptrs, N, dev, true);
+}
+template <int N>
+int allow(const void* const (&ptrs)[N], int dev) {
+  return check_all(ptrs, N, dev, false);
+}
+
+// ---- convolution ---------------------------------------------------------------
+
+int check_conv(const m2rnn_conv_shape* s, bool backward) {
+  if (s == nullptr) return M2RNN_ERR_INVALID_ARG;
+  if (s->B < 1 || s->T < 0 || s->C < 1) return M2RNN_ERR_INVALID_ARG;
+  if (!is_dtype(s->in_dtype) || (s->silu != 0 && s->silu != 1)) return M2RNN_ERR_INVALID_ARG;
+  if (backward && s->grad_dtype != M2RNN_F32 && s->grad_dtype != s->in_dtype)
+    return M2RNN_ERR_INVALID_ARG;
+  if (s->C % 8 != 0 || s->W < 2 || s->W > 4) return M2RNN_ERR_UNSUPPORTED_SHAPE;
+  if (static_cast<double>(s->B) * (static_cast<double>(s->T) + s->W) * s->C >= 1099511627776.0)
+    return M2RNN_ERR_UNSUPPORTED_SHAPE;  // 2^40
+  return M2RNN_OK;
+}
+
+size_t conv_state_bytes(const m2rnn_conv_shape* s) {
+  return static_cast<size_t>(s->B) * (s->W - 1) * s->C * esize(s->in_dtype);
+}
+
+m2rnn::ConvParams conv_params(const m2rnn_conv_shape* s, const m2rnn_rows& xr, const void* x,
+                              const void* w, const void* bias, const void* state, int* status) {
+  m2rnn::ConvParams p{};
+  p.x = x;
+  p.w = w;
+  p.bias = bias;
+  p.state = state;
+  p.xb = xr.batch;
+  p.xt = xr.token;
+  p.B = s->B;
+  p.T = s->T;
+  p.C = s->C;
+  p.W = s->W;
+  p.status = status;
+  return p;
+}
+
+// ---- q/k norm -----------------------------------------------------------------
+
+int check_qk(const m2rnn_qk_shape* s, bool backward) {
+  if (s == nullptr) return M2RNN_ERR_INVALID_ARG;
+  if (s->B < 1 || s->T < 0 || s->Nq < 1 || s->Nk < 0 || s->K < 1 || s->R < 0 || s->P < 0)
+    return M2RNN_ERR_INVALID_ARG;
+  if (!is_dtype(s->in_dtype) || (s->interleaved != 0 && s->interleaved != 1))
+    return M2RNN_ERR_INVALID_ARG;
+  if (backward && s->grad_dtype != M2RNN_F32 && s->grad_dtype != s->in_dtype)
+    return M2RNN_ERR_INVALID_ARG;
+  if (s->K % 8 != 0 || s->K > 256 || s->R > s->K || (s->R != 8 && s->R % 16 != 0))
+    return M2RNN_ERR_UNSUPPORTED_SHAPE;
+  if (s->Nq >= (1 << 20) || s->Nk >= (1 << 20)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
+  const double tokens = static_cast<double>(s->B) * s->T;
+  if (tokens >= 2147483648.0 ||
+      tokens * (static_cast<double>(s->Nq) + s->Nk) * s->K >= 1099511627776.0)
+    return M2RNN_ERR_UNSUPPORTED_SHAPE;  // 2^31 tokens, 2^40 elements
+  return M2RNN_OK;
+}
+
+// The arguments that both passes share.
+int qk_common(const m2rnn_qk_shape* s, const void* q, const m2rnn_rows* q_rows, const void* k,
+              const m2rnn_rows* k_rows, const void* wq, const void* wk, float eps,
+              const float* cs, const float* sn, const int* pos, bool backward,
+              m2rnn::QkParams* p, int* sms) {
+  int rc = check_qk(s, backward);
+  if (rc != M2RNN_OK) return rc;
+  if (!(eps >= 0.f)) return M2RNN_ERR_INVALID_ARG;  // also rejects NaN
+  m2rnn_rows qr, kr;
+  rc = read_rows(q_rows, s->T, static_cast<long long>(s->Nq) * s->K, s->in_dtype, 16, &qr);
+  if (rc != M2RNN_OK) return rc;
+  rc = read_rows(k_rows, s->T, static_cast<long long>(s->Nk) * s->K, s->in_dtype, 16, &kr);
+  if (rc != M2RNN_OK) return rc;
+  if (s->Nk == 0 && (k != nullptr || wk != nullptr)) return M2RNN_ERR_INVALID_ARG;
+  if (s->R > 0 && (cs == nullptr || sn == nullptr || s->P < 1)) return M2RNN_ERR_INVALID_ARG;
+  if (s->R > 0 && pos == nullptr && s->T > s->P) return M2RNN_ERR_INVALID_ARG;
+  int dev, *status;
+  rc = host_device_info(&dev, &status, sms);
+  if (rc != M2RNN_OK) return rc;
+  const void* opt[] = {wq, wk, cs, sn};
+  if ((rc = allow(opt, dev)) != M2RNN_OK) return rc;
+  if (s->T > 0) {
+    const void* req[] = {q};
+    if ((rc = require(req, dev)) != M2RNN_OK) return rc;
+    if ((rc = host_check_ptr(k, dev, s->Nk > 0)) != M2RNN_OK) return rc;
+    if ((rc = host_check_ptr(pos, dev, false)) != M2RNN_OK) return rc;
+  }
+  *p = m2rnn::QkParams{};
+  p->q = q;
+  p->k = k;
+  p->wq = wq;
+  p->wk = wk;
+  p->cs = cs;
+  p->sn = sn;
+  p->pos = pos;
+  p->qb = qr.batch;
+  p->qt = qr.token;
+  p->kb = kr.batch;
+  p->kt = kr.token;
+  p->tokens = static_cast<long long>(s->B) * s->T;
+  p->T = s->T;
+  p->Nq = s->Nq;
+  p->Nk = s->Nk;
+  p->K = s->K;
+  p->R = s->R;
+  p->P = s->P;
+  p->interleaved = s->interleaved;
+  p->split = m2rnn::qk_split(s);
+  p->eps = eps;
+  p->status = status;
+  return M2RNN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int m2rnn_conv_fwd(const m2rnn_conv_shape* s, const void* x, const m2rnn_rows* x_rows,
+                   const void* w, const void* bias, const void* state, void* y, void* state_out,
+                   void* stream) {
+  int rc = check_conv(s, false);
+  if (rc != M2RNN_OK) return rc;
+  m2rnn_rows xr;
+  if ((rc = read_rows(x_rows, s->T, s->C, s->in_dtype, 16, &xr)) != M2RNN_OK) return rc;
+  int dev, sms, *status;
+  if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
+  const void* req[] = {w};
+  const void* opt[] = {bias, state, state_out};
+  if ((rc = require(req, dev)) != M2RNN_OK || (rc = allow(opt, dev)) != M2RNN_OK) return rc;
+  const size_t sb = conv_state_bytes(s);
+  if (state != nullptr && state_out != nullptr && overlap(state, state_out, sb))
+    return M2RNN_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s->T == 0) {
+    if (state_out == nullptr) return M2RNN_OK;
+    return status_from_cuda(state ? cudaMemcpyAsync(state_out, state, sb, cudaMemcpyDeviceToDevice, st)
+                                  : cudaMemsetAsync(state_out, 0, sb, st));
+  }
+  const void* req2[] = {x, y};
+  if ((rc = require(req2, dev)) != M2RNN_OK) return rc;
+  m2rnn::ConvParams p = conv_params(s, xr, x, w, bias, state, status);
+  p.y = y;
+  p.state_out = state_out;
+  p.TT = m2rnn::conv_fwd_tokens(s, sms);
+  p.nT = (s->T + p.TT - 1) / p.TT;
+  return status_from_cuda(m2rnn::launch_conv_fwd(p, s->in_dtype == M2RNN_F32, s->silu != 0, st));
+}
+
+size_t m2rnn_conv_bwd_workspace_size(const m2rnn_conv_shape* s) {
+  if (check_conv(s, true) != M2RNN_OK || s->T == 0) return 0;
+  int TT, nT, nparts;
+  m2rnn::conv_bwd_plan(s, &TT, &nT, &nparts);
+  return align256(static_cast<size_t>(nparts) * s->C * (s->W + 1) * sizeof(float));
+}
+
+int m2rnn_conv_bwd(const m2rnn_conv_shape* s, const void* x, const m2rnn_rows* x_rows,
+                   const void* w, const void* bias, const void* state, const void* dy,
+                   const void* dstate_out, void* dx, float* dw, float* dbias, void* dstate,
+                   void* workspace, size_t ws_bytes, void* stream) {
+  int rc = check_conv(s, true);
+  if (rc != M2RNN_OK) return rc;
+  m2rnn_rows xr;
+  if ((rc = read_rows(x_rows, s->T, s->C, s->in_dtype, 16, &xr)) != M2RNN_OK) return rc;
+  int dev, sms, *status;
+  if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
+  const void* req[] = {w, dw};
+  const void* opt[] = {bias, state, dstate_out, dbias, dstate};
+  if ((rc = require(req, dev)) != M2RNN_OK || (rc = allow(opt, dev)) != M2RNN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s->T == 0) {  // no tokens: the state passes through
+    if (cudaMemsetAsync(dw, 0, static_cast<size_t>(s->C) * s->W * sizeof(float), st) != cudaSuccess)
+      return M2RNN_ERR_CUDA;
+    if (dbias != nullptr && cudaMemsetAsync(dbias, 0, s->C * sizeof(float), st) != cudaSuccess)
+      return M2RNN_ERR_CUDA;
+    if (dstate == nullptr) return M2RNN_OK;
+    const size_t sb = conv_state_bytes(s);
+    return status_from_cuda(dstate_out
+                                ? cudaMemcpyAsync(dstate, dstate_out, sb, cudaMemcpyDeviceToDevice, st)
+                                : cudaMemsetAsync(dstate, 0, sb, st));
+  }
+  const void* req2[] = {x, dy, dx};
+  if ((rc = require(req2, dev)) != M2RNN_OK) return rc;
+  if (workspace == nullptr || ws_bytes < m2rnn_conv_bwd_workspace_size(s)) return M2RNN_ERR_WORKSPACE;
+  const void* ws[] = {workspace};
+  if ((rc = require(ws, dev)) != M2RNN_OK) return rc;
+  m2rnn::ConvParams p = conv_params(s, xr, x, w, bias, state, status);
+  p.dy = dy;
+  p.dstate_out = dstate_out;
+  p.dx = dx;
+  p.dstate = dstate;
+  p.dw = dw;
+  p.dbias = dbias;
+  p.part = static_cast<float*>(workspace);
+  m2rnn::conv_bwd_plan(s, &p.TT, &p.nT, &p.nparts);
+  return status_from_cuda(m2rnn::launch_conv_bwd(p, s->in_dtype == M2RNN_F32,
+                                                 s->grad_dtype == M2RNN_F32, s->silu != 0, st));
+}
+
+int m2rnn_conv_step(const m2rnn_conv_shape* s, const void* x, const m2rnn_rows* x_rows,
+                    const void* w, const void* bias, const void* state, void* y, void* state_out,
+                    void* stream) {
+  int rc = check_conv(s, false);
+  if (rc != M2RNN_OK) return rc;
+  if (s->T != 1) return M2RNN_ERR_INVALID_ARG;
+  m2rnn_rows xr;
+  if ((rc = read_rows(x_rows, 1, s->C, s->in_dtype, 16, &xr)) != M2RNN_OK) return rc;
+  int dev, sms, *status;
+  if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
+  const void* req[] = {x, w, state, y, state_out};
+  const void* opt[] = {bias};
+  if ((rc = require(req, dev)) != M2RNN_OK || (rc = allow(opt, dev)) != M2RNN_OK) return rc;
+  if (state != state_out && overlap(state, state_out, conv_state_bytes(s)))
+    return M2RNN_ERR_INVALID_ARG;
+  m2rnn::ConvParams p = conv_params(s, xr, x, w, bias, state, status);
+  p.y = y;
+  p.state_out = state_out;
+  return status_from_cuda(m2rnn::launch_conv_step(p, s->in_dtype == M2RNN_F32, s->silu != 0,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+int m2rnn_qk_norm_fwd(const m2rnn_qk_shape* s, const void* q, const m2rnn_rows* q_rows,
+                      const void* k, const m2rnn_rows* k_rows, const void* wq, const void* wk,
+                      float eps, const float* cos, const float* sin, const int* pos, void* qo,
+                      void* ko, void* stream) {
+  m2rnn::QkParams p;
+  int sms;
+  int rc = qk_common(s, q, q_rows, k, k_rows, wq, wk, eps, cos, sin, pos, false, &p, &sms);
+  if (rc != M2RNN_OK || s->T == 0) return rc;
+  int dev, *status;
+  if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
+  if ((rc = host_check_ptr(qo, dev, true)) != M2RNN_OK) return rc;
+  if ((rc = host_check_ptr(ko, dev, s->Nk > 0)) != M2RNN_OK) return rc;
+  p.qo = qo;
+  p.ko = ko;
+  return status_from_cuda(m2rnn::launch_qk_fwd(p, s->in_dtype == M2RNN_F32, sms,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+size_t m2rnn_qk_norm_bwd_workspace_size(const m2rnn_qk_shape* s) {
+  if (check_qk(s, true) != M2RNN_OK || s->T == 0) return 0;
+  return align256(static_cast<size_t>(m2rnn::qk_bwd_parts(s)) * 2 * s->K * sizeof(float));
+}
+
+int m2rnn_qk_norm_bwd(const m2rnn_qk_shape* s, const void* q, const m2rnn_rows* q_rows,
+                      const void* k, const m2rnn_rows* k_rows, const void* wq, const void* wk,
+                      float eps, const float* cos, const float* sin, const int* pos,
+                      const void* dqo, const void* dko, void* dq, void* dk, float* dwq,
+                      float* dwk, void* workspace, size_t ws_bytes, void* stream) {
+  m2rnn::QkParams p;
+  int sms;
+  int rc = qk_common(s, q, q_rows, k, k_rows, wq, wk, eps, cos, sin, pos, true, &p, &sms);
+  if (rc != M2RNN_OK) return rc;
+  int dev, *status;
+  if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
+  const void* opt[] = {dwq, dwk};
+  if ((rc = allow(opt, dev)) != M2RNN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s->T == 0) {
+    for (float* d : {dwq, dwk})
+      if (d != nullptr && cudaMemsetAsync(d, 0, s->K * sizeof(float), st) != cudaSuccess)
+        return M2RNN_ERR_CUDA;
+    return M2RNN_OK;
+  }
+  const void* req[] = {dqo, dq};
+  if ((rc = require(req, dev)) != M2RNN_OK) return rc;
+  for (const void* x : {dko, static_cast<const void*>(dk)})
+    if ((rc = host_check_ptr(x, dev, s->Nk > 0)) != M2RNN_OK) return rc;
+  if (workspace == nullptr || ws_bytes < m2rnn_qk_norm_bwd_workspace_size(s))
+    return M2RNN_ERR_WORKSPACE;
+  if ((rc = host_check_ptr(workspace, dev, true)) != M2RNN_OK) return rc;
+  p.dqo = dqo;
+  p.dko = dko;
+  p.dq = dq;
+  p.dk = dk;
+  p.dwq = dwq;
+  p.dwk = dwk;
+  p.part = static_cast<float*>(workspace);
+  p.nparts = m2rnn::qk_bwd_parts(s);
+  return status_from_cuda(m2rnn::launch_qk_bwd(p, s->in_dtype == M2RNN_F32,
+                                               s->grad_dtype == M2RNN_F32, st));
+}
+
+int m2rnn_scan_step(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void* q,
+                    const void* k, const void* v, const void* a, const void* alpha,
+                    const void* beta, const void* w_r, const float* H_in, float* H_out, void* y,
+                    void* stream) {
+  int rc = m2rnn::validate_shape(s);
+  if (rc != M2RNN_OK) return rc;
+  if (s->T != 1) return M2RNN_ERR_INVALID_ARG;
+  const int Nq = s->Nq == 0 ? 1 : s->Nq;
+  m2rnn_rows qr, kr, vr, ar;
+  const long long qw = static_cast<long long>(Nq) * s->K, vw = static_cast<long long>(s->N) * s->V;
+  const long long e = static_cast<long long>(esize(s->in_dtype));
+  if ((rc = read_rows(rows ? &rows->q : nullptr, 1, qw, s->in_dtype, 16, &qr)) != M2RNN_OK ||
+      (rc = read_rows(rows ? &rows->k : nullptr, 1, qw, s->in_dtype, 16, &kr)) != M2RNN_OK ||
+      (rc = read_rows(rows ? &rows->v : nullptr, 1, vw, s->in_dtype, 16, &vr)) != M2RNN_OK ||
+      (rc = read_rows(rows ? &rows->a : nullptr, 1, s->N, s->in_dtype, e, &ar)) != M2RNN_OK)
+    return rc;
+  int dev, sms, *status;
+  if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
+  const void* req[] = {q, k, v, alpha, beta, H_in, H_out, y};
+  const void* opt[] = {w_r};
+  if ((rc = require(req, dev)) != M2RNN_OK || (rc = allow(opt, dev)) != M2RNN_OK) return rc;
+  if ((rc = m2rnn::host_check_elem_ptr(a, dev, static_cast<size_t>(e))) != M2RNN_OK) return rc;
+  if (H_out != H_in &&
+      overlap(H_in, H_out, static_cast<size_t>(s->B) * s->N * s->K * s->V * sizeof(float)))
+    return M2RNN_ERR_INVALID_ARG;
+  m2rnn::ScanStepParams p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.a = a;
+  p.alpha = alpha;
+  p.beta = beta;
+  p.w_r = w_r;
+  p.H_in = H_in;
+  p.H_out = H_out;
+  p.y = y;
+  p.qb = qr.batch;
+  p.kb = kr.batch;
+  p.vb = vr.batch;
+  p.ab = ar.batch;
+  p.B = s->B;
+  p.N = s->N;
+  p.Nq = Nq;
+  p.K = s->K;
+  p.status = status;
+  return status_from_cuda(m2rnn::launch_scan_step(p, s->V, s->in_dtype == M2RNN_F32,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

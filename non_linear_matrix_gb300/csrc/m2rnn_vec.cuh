@@ -1,0 +1,154 @@
+// m2rnn_vec.cuh -- vector loads and stores of the block operators' elements
+// (bf16 or fp32 in memory, fp32 in registers) and the fixed-order sum over
+// CTAs' partial results.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "m2rnn_check.cuh"
+#include "ptx.cuh"
+
+namespace m2rnn {
+
+template <bool F32>
+struct Elem {
+  using T = float;
+};
+template <>
+struct Elem<false> {
+  using T = __nv_bfloat16;
+};
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// VEC (4 or 8) consecutive elements as they lie in memory: 8 or 16 bytes of
+// bf16, 16 or 32 bytes of fp32.
+template <bool F32, int VEC>
+struct Raw {
+  uint32_t w[F32 ? VEC : VEC / 2];
+};
+
+template <bool F32, int VEC>
+__device__ __forceinline__ Raw<F32, VEC> raw_zero() {
+  Raw<F32, VEC> r;
+#pragma unroll
+  for (uint32_t& x : r.w) x = 0u;
+  return r;
+}
+
+template <bool F32, int VEC>
+__device__ __forceinline__ Raw<F32, VEC> raw_load(const typename Elem<F32>::T* src) {
+  Raw<F32, VEC> r;
+  if constexpr (sizeof(r.w) == 8) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
+    r.w[0] = u.x;
+    r.w[1] = u.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(r.w) / 16); ++i) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + i);
+      r.w[4 * i] = u.x;
+      r.w[4 * i + 1] = u.y;
+      r.w[4 * i + 2] = u.z;
+      r.w[4 * i + 3] = u.w;
+    }
+  }
+  return r;
+}
+
+template <bool F32, int VEC>
+__device__ __forceinline__ void raw_store(typename Elem<F32>::T* dst, const Raw<F32, VEC>& r) {
+  if constexpr (sizeof(r.w) == 8) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(r.w[0], r.w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(r.w) / 16); ++i)
+      reinterpret_cast<uint4*>(dst)[i] =
+          make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
+  }
+}
+
+template <bool F32, int VEC>
+__device__ __forceinline__ void raw_unpack(const Raw<F32, VEC>& r, float (&o)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    if constexpr (F32)
+      o[i] = __uint_as_float(r.w[i]);
+    else
+      o[i] = (i & 1) ? ptx::bf16x2_hi(r.w[i / 2]) : ptx::bf16x2_lo(r.w[i / 2]);
+  }
+}
+
+template <bool F32, int VEC>
+__device__ __forceinline__ Raw<F32, VEC> raw_pack(const float (&o)[VEC]) {
+  Raw<F32, VEC> r;
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) r.w[i] = __float_as_uint(o[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) r.w[i] = ptx::pack_bf16x2(o[2 * i], o[2 * i + 1]);
+  }
+  return r;
+}
+
+template <bool F32, int VEC>
+__device__ __forceinline__ void load_vec(const typename Elem<F32>::T* src, float (&o)[VEC]) {
+  raw_unpack<F32, VEC>(raw_load<F32, VEC>(src), o);
+}
+
+template <bool F32, int VEC>
+__device__ __forceinline__ void store_vec(typename Elem<F32>::T* dst, const float (&o)[VEC]) {
+  raw_store<F32, VEC>(dst, raw_pack<F32, VEC>(o));
+}
+
+// Sums part[nparts][n0 + n1 + n2] over the parts, always in the same order,
+// into up to three outputs (NULL: skipped).  A CTA takes 32 columns, its 32
+// warps every 32nd part each; the warps' sums are added in warp order.
+struct SumOut {
+  float* out[3];
+  int n[3];
+};
+
+static __global__ void __launch_bounds__(1024)
+    sum_parts_kernel(const float* part, int nparts, SumOut o, int* status, int site) {
+  __shared__ float acc[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = o.n[0] + o.n[1] + o.n[2];
+  const int col = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (col < n) {
+#pragma unroll 4
+    for (int r = warp; r < nparts; r += 32) {
+      const size_t at = static_cast<size_t>(r) * n + col;
+      if (in_range(status, at, 1, static_cast<size_t>(nparts) * n, site)) s += part[at];
+    }
+  }
+  acc[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || col >= n) return;
+  float t = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) t += acc[i][lane];
+  int at = col;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (at < o.n[i]) {
+      if (o.out[i] != nullptr) o.out[i][at] = t;
+      return;
+    }
+    at -= o.n[i];
+  }
+}
+
+static cudaError_t launch_sum_parts(const float* part, int nparts, const SumOut& o, int* status,
+                                    int site, cudaStream_t st) {
+  const int n = o.n[0] + o.n[1] + o.n[2];
+  sum_parts_kernel<<<(n + 31) / 32, 1024, 0, st>>>(part, nparts, o, status, site);
+  return cudaGetLastError();
+}
+
+}  // namespace m2rnn

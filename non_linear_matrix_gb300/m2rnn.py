@@ -1,4 +1,4 @@
-"""Thin ctypes binding of libm2rnn.so (include/m2rnn.h).
+"""Thin ctypes binding of libm2rnn.so (include/m2rnn.h and m2rnn_block.h).
 
 Argument marshalling only: it checks tensor placement and dtypes, allocates
 output tensors with torch, passes raw device pointers and the current CUDA
@@ -50,6 +50,15 @@ _EXPORTS = {
     "m2rnn_fwd_norm": (ctypes.c_int, [_VP] * 13 + [ctypes.c_float] + [_VP] * 6),
     "m2rnn_bwd_norm_workspace_size": (ctypes.c_size_t, [_VP, ctypes.c_int]),
     "m2rnn_bwd_norm": (ctypes.c_int, [_VP] * 31 + [ctypes.c_size_t, _VP]),
+    "m2rnn_conv_fwd": (ctypes.c_int, [_VP] * 9),
+    "m2rnn_conv_bwd_workspace_size": (ctypes.c_size_t, [_VP]),
+    "m2rnn_conv_bwd": (ctypes.c_int, [_VP] * 13 + [ctypes.c_size_t, _VP]),
+    "m2rnn_conv_step": (ctypes.c_int, [_VP] * 9),
+    "m2rnn_qk_norm_fwd": (ctypes.c_int, [_VP] * 7 + [ctypes.c_float] + [_VP] * 6),
+    "m2rnn_qk_norm_bwd_workspace_size": (ctypes.c_size_t, [_VP]),
+    "m2rnn_qk_norm_bwd": (ctypes.c_int, [_VP] * 7 + [ctypes.c_float] + [_VP] * 10 +
+                          [ctypes.c_size_t, _VP]),
+    "m2rnn_scan_step": (ctypes.c_int, [_VP] * 13),
 }
 
 
@@ -432,6 +441,261 @@ def bwd_norm(q, k, v, f, W, w_r, g, w_norm, y, rstd, dout, H0=None, ckpt=None, d
     if dck is not None:
         gr["dckpt"] = dck
     return gr
+
+
+# ---- the operators around the recurrence (include/m2rnn_block.h) -----------
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_longlong), ("token", ctypes.c_longlong)]
+
+
+class ConvShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("C", ctypes.c_int), ("W", ctypes.c_int),
+                ("in_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int), ("silu", ctypes.c_int)]
+
+
+class QkShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("Nq", ctypes.c_int),
+                ("Nk", ctypes.c_int), ("K", ctypes.c_int), ("R", ctypes.c_int),
+                ("P", ctypes.c_int), ("in_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
+
+
+class ScanRows(ctypes.Structure):
+    _fields_ = [("q", Rows), ("k", Rows), ("v", Rows), ("a", Rows)]
+
+
+def _rows(t, lead: int) -> Rows:
+    """Batch and token distances of a tensor whose first ``lead`` dimensions
+    are batch (and token) and whose remaining ones are packed."""
+    if not t.is_cuda:
+        raise ValueError("tensors passed to libm2rnn must be CUDA tensors")
+    inner = 1
+    for size, st in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
+        if size != 1 and st != inner:
+            raise ValueError("the dimensions after the token must be packed")
+        inner *= size
+    token = t.stride(1) if lead == 2 and t.shape[1] > 1 else inner
+    tokens = t.shape[1] if lead == 2 else 1
+    batch = t.stride(0) if t.shape[0] > 1 else token * tokens
+    return Rows(batch, token)
+
+
+def _at(t):
+    """Pointer of a tensor described by ``_rows`` (which checked its layout)."""
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _expect(name: str, t, shape, *dtypes):
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+
+
+def _out(t, shape, dtype, device, name: str = "out"):
+    if t is None:
+        return torch.empty(shape, device=device, dtype=dtype)
+    _expect(name, t, shape, dtype)
+    return t
+
+
+def _workspace(ws, need: int, device):
+    return torch.empty(max(need, 16), device=device, dtype=torch.uint8) if ws is None else ws
+
+
+def _nbytes(t):
+    return ctypes.c_size_t(t.numel() * t.element_size())
+
+
+def _grad_code(dy, x) -> int:
+    if dy.dtype not in (torch.float32, x.dtype):
+        raise TypeError("the incoming gradient must be float32 or of the inputs' dtype")
+    return _dtype_code(dy)
+
+
+def conv_fwd(x, w, bias=None, state=None, *, silu: bool = True, want_state: bool = True,
+             out=None, stream=None):
+    """Short causal convolution along time with SiLU (or none, silu=False).
+    Returns (y, state_out or None).
+
+    x [B,T,C] (its rows may be a slice of a wider buffer); w [C,W], W = 2..4;
+    bias [C] or None; state [B,W-1,C], the inputs before the call, or None
+    for zeros; one dtype (bf16 or f32).  ``out`` may supply y and state."""
+    B, T, C = x.shape
+    W = w.shape[1]
+    _expect("w", w, (C, W), x.dtype)
+    _expect("bias", bias, (C,), x.dtype)
+    _expect("state", state, (B, W - 1, C), x.dtype)
+    out = dict(out or {})
+    y = _out(out.get("y"), (B, T, C), x.dtype, x.device, "y")
+    so = out.get("state")
+    if so is not None or want_state:
+        so = _out(so, (B, W - 1, C), x.dtype, x.device, "state")
+    s, r = ConvShape(B, T, C, W, _dtype_code(x), 0, int(bool(silu))), _rows(x, 2)
+    rc = lib().m2rnn_conv_fwd(ctypes.byref(s), _at(x), ctypes.byref(r), _ptr(w), _ptr(bias),
+                              _ptr(state), _ptr(y), _ptr(so), _stream(stream))
+    _check(rc, "m2rnn_conv_fwd")
+    return y, so
+
+
+def conv_bwd(x, w, dy, bias=None, state=None, dstate_out=None, *, silu: bool = True,
+             want_dstate: bool = False, workspace=None, out=None, stream=None):
+    """Gradient of ``conv_fwd``: dict(dx, dw, dbias[, dstate]).  dy [B,T,C]
+    is float32 or of x's dtype; dstate_out [B,W-1,C] is the gradient of the
+    returned state (None = 0).  dx and dstate have x's dtype, dw and dbias
+    are fp32 (dbias None without a bias)."""
+    B, T, C = x.shape
+    W = w.shape[1]
+    _expect("w", w, (C, W), x.dtype)
+    _expect("bias", bias, (C,), x.dtype)
+    _expect("state", state, (B, W - 1, C), x.dtype)
+    _expect("dstate_out", dstate_out, (B, W - 1, C), x.dtype)
+    _expect("dy", dy, (B, T, C), torch.float32, x.dtype)
+    s = ConvShape(B, T, C, W, _dtype_code(x), _grad_code(dy, x), int(bool(silu)))
+    r, out, dev, f32 = _rows(x, 2), dict(out or {}), x.device, torch.float32
+    g = {"dx": _out(out.get("dx"), (B, T, C), x.dtype, dev, "dx"),
+         "dw": _out(out.get("dw"), (C, W), f32, dev, "dw"),
+         "dbias": None if bias is None else _out(out.get("dbias"), (C,), f32, dev, "dbias")}
+    ds = out.get("dstate")
+    if ds is not None or want_dstate:
+        ds = _out(ds, (B, W - 1, C), x.dtype, dev, "dstate")
+    ws = _workspace(workspace, int(lib().m2rnn_conv_bwd_workspace_size(ctypes.byref(s))), dev)
+    rc = lib().m2rnn_conv_bwd(ctypes.byref(s), _at(x), ctypes.byref(r), _ptr(w), _ptr(bias),
+                              _ptr(state), _ptr(dy), _ptr(dstate_out), _ptr(g["dx"]),
+                              _ptr(g["dw"]), _ptr(g["dbias"]), _ptr(ds), _ptr(ws), _nbytes(ws),
+                              _stream(stream))
+    _check(rc, "m2rnn_conv_bwd")
+    if ds is not None:
+        g["dstate"] = ds
+    return g
+
+
+def conv_step(x, w, state, bias=None, *, silu: bool = True, state_out=None, y=None, stream=None):
+    """One token of the convolution for B sequences: x [B,C], state
+    [B,W-1,C].  Returns (y, state_out); pass ``state_out=state`` to update
+    the state in place."""
+    B, C = x.shape
+    W = w.shape[1]
+    _expect("w", w, (C, W), x.dtype)
+    _expect("bias", bias, (C,), x.dtype)
+    _expect("state", state, (B, W - 1, C), x.dtype)
+    y = _out(y, (B, C), x.dtype, x.device, "y")
+    so = _out(state_out, (B, W - 1, C), x.dtype, x.device, "state_out")
+    s, r = ConvShape(B, 1, C, W, _dtype_code(x), 0, int(bool(silu))), _rows(x, 1)
+    rc = lib().m2rnn_conv_step(ctypes.byref(s), _at(x), ctypes.byref(r), _ptr(w), _ptr(bias),
+                               _ptr(state), _ptr(y), _ptr(so), _stream(stream))
+    _check(rc, "m2rnn_conv_step")
+    return y, so
+
+
+def _qk_args(q, k, wq, wk, cos, sin, pos, interleaved, grad_code):
+    """Shape, rows and checked arguments shared by both directions."""
+    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or
+                                           k.shape[3] != q.shape[3])):
+        raise ValueError("q must be [B,T,Nq,K] and k [B,T,Nk,K]")
+    if k is not None and k.dtype != q.dtype:
+        raise TypeError("q and k must share one dtype")
+    B, T, Nq, K = q.shape
+    Nk = 0 if k is None else k.shape[2]
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    R, P = (0, 0) if cos is None else (2 * cos.shape[1], cos.shape[0])
+    _expect("cos", cos, (P, R // 2), torch.float32)
+    _expect("sin", sin, (P, R // 2), torch.float32)
+    _expect("pos", pos, (B, T), torch.int32)
+    _expect("wq", wq, (K,), q.dtype)
+    _expect("wk", wk, (K,), q.dtype)
+    s = QkShape(B, T, Nq, Nk, K, R, P, _dtype_code(q), grad_code, int(bool(interleaved)))
+    rq = _rows(q, 2)
+    rk = rq if k is None else _rows(k, 2)
+    return s, rq, rk
+
+
+def qk_norm_fwd(q, k, wq=None, wk=None, eps: float = 1e-6, *, cos=None, sin=None, pos=None,
+                interleaved: bool = False, out=None, stream=None):
+    """RMS norm of every query and key head over its K features, times wq /
+    wk [K] (None = 1), with the first R = 2*cos.shape[1] features rotated by
+    the token's angles in the same pass.  Returns (q', k').
+
+    q [B,T,Nq,K], k [B,T,Nk,K] or None (rows may be slices); cos, sin [P,R/2]
+    fp32; pos [B,T] int32 (None: token t has position t); interleaved: pairs
+    (2i, 2i+1) instead of (i, i + R/2).  A position outside the table gives
+    NaN and sets M2RNN_ERR_BOUNDS in the device status."""
+    s, rq, rk = _qk_args(q, k, wq, wk, cos, sin, pos, interleaved, 0)
+    out = dict(out or {})
+    qo = _out(out.get("q"), tuple(q.shape), q.dtype, q.device, "q")
+    ko = None if k is None else _out(out.get("k"), tuple(k.shape), q.dtype, q.device, "k")
+    rc = lib().m2rnn_qk_norm_fwd(ctypes.byref(s), _at(q), ctypes.byref(rq), _at(k),
+                                 ctypes.byref(rk), _ptr(wq), _ptr(wk), ctypes.c_float(eps),
+                                 _ptr(cos), _ptr(sin), _ptr(pos), _ptr(qo), _ptr(ko),
+                                 _stream(stream))
+    _check(rc, "m2rnn_qk_norm_fwd")
+    return qo, ko
+
+
+def qk_norm_bwd(q, k, wq, wk, dqo, dko, eps: float = 1e-6, *, cos=None, sin=None, pos=None,
+                interleaved: bool = False, workspace=None, out=None, stream=None):
+    """Gradient of ``qk_norm_fwd``: dict(dq, dk, dwq, dwk); dqo, dko are
+    float32 or of q's dtype, dq and dk have q's dtype, dwq and dwk [K] are
+    fp32 (None without that weight)."""
+    s, rq, rk = _qk_args(q, k, wq, wk, cos, sin, pos, interleaved, _grad_code(dqo, q))
+    _expect("dqo", dqo, tuple(q.shape), torch.float32, q.dtype)
+    if (k is None) != (dko is None):
+        raise ValueError("dko goes with k")
+    if k is not None:
+        _expect("dko", dko, tuple(k.shape), dqo.dtype)
+    out, dev, K = dict(out or {}), q.device, q.shape[3]
+    g = {"dq": _out(out.get("dq"), tuple(q.shape), q.dtype, dev, "dq"),
+         "dk": None if k is None else _out(out.get("dk"), tuple(k.shape), q.dtype, dev, "dk"),
+         "dwq": None if wq is None else _out(out.get("dwq"), (K,), torch.float32, dev, "dwq"),
+         "dwk": None if wk is None else _out(out.get("dwk"), (K,), torch.float32, dev, "dwk")}
+    ws = _workspace(workspace, int(lib().m2rnn_qk_norm_bwd_workspace_size(ctypes.byref(s))), dev)
+    rc = lib().m2rnn_qk_norm_bwd(ctypes.byref(s), _at(q), ctypes.byref(rq), _at(k),
+                                 ctypes.byref(rk), _ptr(wq), _ptr(wk), ctypes.c_float(eps),
+                                 _ptr(cos), _ptr(sin), _ptr(pos), _ptr(dqo), _ptr(dko),
+                                 _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dwq"]), _ptr(g["dwk"]),
+                                 _ptr(ws), _nbytes(ws), _stream(stream))
+    _check(rc, "m2rnn_qk_norm_bwd")
+    return g
+
+
+def _scan_args(q, k, v, a, alpha, beta, w_r, lead: int):
+    """Shape and rows of a scan call; q, k may lack the group dimension."""
+    if q.dim() == lead + 1:
+        q, k = q.unsqueeze(lead), k.unsqueeze(lead)
+    B, (Nq, K), (N, V) = q.shape[0], q.shape[lead:], v.shape[lead:]
+    T = q.shape[1] if lead == 2 else 1
+    first = (B, T) if lead == 2 else (B,)
+    _expect("k", k, (*first, Nq, K), q.dtype)
+    _expect("v", v, (*first, N, V), q.dtype)
+    _expect("a", a, (*first, N), q.dtype)
+    _expect("alpha", alpha, (N,), q.dtype)
+    _expect("beta", beta, (N,), q.dtype)
+    _expect("w_r", w_r, (N, V), q.dtype)
+    rows = ScanRows(_rows(q, lead), _rows(k, lead), _rows(v, lead), _rows(a, lead))
+    return Shape(B, T, N, K, V, _dtype_code(q), 0, Nq), rows
+
+
+def scan_step(q, k, v, a, alpha, beta, H, w_r=None, *, H_out=None, y=None, stream=None):
+    """One token of the selective scan for B sequences.  Returns (y, H_out).
+
+    q, k [B,K] or [B,Nq,K]; v [B,N,V]; a [B,N] (rows may be slices); alpha,
+    beta [N]; w_r [N,V] or None; H [B,N,K,V] fp32 is the state before the
+    token.  Pass ``H_out=H`` to update it in place."""
+    s, rows = _scan_args(q, k, v, a, alpha, beta, w_r, 1)
+    state = (s.B, s.N, s.K, s.V)
+    _expect("H", H, state, torch.float32)
+    H_out = _out(H_out, state, torch.float32, q.device, "H_out")
+    y = _out(y, (s.B, s.N, s.V), q.dtype, q.device, "y")
+    rc = lib().m2rnn_scan_step(ctypes.byref(s), ctypes.byref(rows), _at(q), _at(k), _at(v),
+                               _at(a), _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(H), _ptr(H_out),
+                               _ptr(y), _stream(stream))
+    _check(rc, "m2rnn_scan_step")
+    return y, H_out
 
 
 def device_status(clear: bool = True, stream=None):
