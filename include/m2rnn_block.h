@@ -136,6 +136,35 @@ typedef struct {
     m2rnn_rows q, k, v, a;
 } m2rnn_scan_rows;
 
+/* Bytes of `saved`: what the forward pass can keep for the backward pass (the
+ * state before every 64th token and the gate's sums).  0 when T = 0. */
+size_t m2rnn_scan_saved_size(const m2rnn_shape *s);
+
+/* Bytes of workspace of m2rnn_scan_fwd; saved_given = 1 when `saved` is
+ * passed. */
+size_t m2rnn_scan_fwd_workspace_size(const m2rnn_shape *s, int saved_given);
+
+/* saved: m2rnn_scan_saved_size(s) bytes, or NULL. */
+int m2rnn_scan_fwd(const m2rnn_shape *s, const m2rnn_scan_rows *rows, const void *q,
+                   const void *k, const void *v, const void *a, const void *alpha,
+                   const void *beta, const void *w_r, const float *H0, void *y, float *H_T,
+                   void *saved, void *workspace, size_t ws_bytes, void *stream);
+
+size_t m2rnn_scan_bwd_workspace_size(const m2rnn_shape *s, int saved_given);
+
+/* Gradients for dL/dy = dy ([B,T,N,V] in_dtype) and dL/dH_T = dH_T (NULL = 0).
+ *   saved : from m2rnn_scan_fwd with the same inputs, or NULL (recomputed
+ *           into the workspace)
+ *   dq, dk [B,T,Nq,K] (summed over each group's heads), dv [B,T,N,V],
+ *   da [B,T,N] : in_dtype;  dalpha, dbeta [N], dw_r [N,V] : fp32 (dw_r NULL
+ *   exactly when w_r is);  dH0 [B,N,K,V] fp32 or NULL. */
+int m2rnn_scan_bwd(const m2rnn_shape *s, const m2rnn_scan_rows *rows, const void *q,
+                   const void *k, const void *v, const void *a, const void *alpha,
+                   const void *beta, const void *w_r, const float *H0, const void *saved,
+                   const void *dy, const float *dH_T, void *dq, void *dk, void *dv, void *da,
+                   float *dalpha, float *dbeta, float *dw_r, float *dH0, void *workspace,
+                   size_t ws_bytes, void *stream);
+
 /* One token for B sequences (s->T must be 1): q, k [B,Nq,K], v, y [B,N,V],
  * a [B,N]; of the rows only the batch distances are read.  H_out may be H_in
  * itself (in place), otherwise the two must not overlap. */

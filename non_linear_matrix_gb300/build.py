@@ -28,7 +28,9 @@ MICROBENCH = os.path.join(BUILD, "m2rnn_microbench")
 
 SOURCES = ["m2rnn_api.cu", "m2rnn_fwd.cu", "m2rnn_bwd.cu", "m2rnn_bwd_pipe.cu", "m2rnn_decode.cu",
            "m2rnn_noalloc.cu", "m2rnn_norm.cu", "m2rnn_block_api.cu", "m2rnn_conv.cu",
-           "m2rnn_qknorm.cu", "m2rnn_scan_step.cu"]
+           "m2rnn_qknorm.cu", "m2rnn_scan_step.cu", "m2rnn_scan_states.cu",
+           "m2rnn_scan_out.cu", "m2rnn_scan_bwd.cu", "m2rnn_scan_bwd_bf16_lo.cu",
+           "m2rnn_scan_bwd_bf16_hi.cu", "m2rnn_scan_bwd_f32_lo.cu", "m2rnn_scan_bwd_f32_hi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

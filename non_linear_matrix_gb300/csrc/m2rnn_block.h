@@ -4,6 +4,7 @@
 #pragma once
 #include <cstddef>
 #include <cstdint>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/m2rnn_block.h"
@@ -85,5 +86,38 @@ struct ScanStepParams {
   int* status;
 };
 cudaError_t launch_scan_step(const ScanStepParams& p, int V, bool f32, cudaStream_t st);
+
+// Selective scan over whole sequences (m2rnn_scan_*.cu).
+constexpr int kChunk = 64;    // tokens per chunk
+constexpr int kCols = 64;     // value columns per head block: 64 / V heads
+
+struct ScanParams {
+  const void *q, *k, *v, *a, *alpha, *beta, *w_r;
+  const float* H0;
+  void* y;
+  float* HT;
+  const void* dy;
+  const float* dHT;
+  void *dq, *dk, *dv, *da;
+  float *dalpha, *dbeta, *dw_r, *dH0;
+  long long qb, qt, kb, kt, vb, vt, ab, at;  // rows
+  int B, T, N, Nq, K, V;
+  int nc;         // chunks
+  int hpg, nhb;   // heads per group, head blocks per group
+  int nseg, cps;  // segments of a sequence in the state kernels, chunks in each
+  int hsplit;     // CTAs that share a chunk's head blocks
+  float2* sd;     // [B][N][nc * 64]: (log2 decay since the token's 16-block began, dt)
+  __nv_bfloat16* Hs;  // states before each chunk: [B][Nq * nhb][nc][terms][64 x K]
+  __nv_bfloat16* Rs;  // gradients of the states after each chunk, the same layout
+  float* segst;   // [B][Nq * nhb][nseg][64 x K]: states at the segments' ends
+  float* segdec;  // [B][N][nseg]: log2 decay over a segment
+  float* dqk;     // hsplit > 1: [hsplit][2][B][T][Nq][K] shares of dq, dk
+  float* part;    // [B * nc][N * (2 + V)] shares of dalpha, dbeta, dw_r
+  int* status;
+};
+int scan_state_terms(bool f32);
+cudaError_t launch_scan_states(const ScanParams& p, bool f32, bool reverse, cudaStream_t st);
+cudaError_t launch_scan_out(const ScanParams& p, bool f32, cudaStream_t st);
+cudaError_t launch_scan_bwd(const ScanParams& p, bool f32, cudaStream_t st);
 
 }  // namespace m2rnn

@@ -1,6 +1,7 @@
 // m2rnn_block_api.cu -- the extern "C" entry points declared in
 // include/m2rnn_block.h: argument validation and launch planning of the
 // convolution, the q/k norm and the selective scan.
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -163,6 +164,140 @@ int qk_common(const m2rnn_qk_shape* s, const void* q, const m2rnn_rows* q_rows, 
   p->status = status;
   return M2RNN_OK;
 }
+
+// ---- selective scan -------------------------------------------------------------
+
+struct ScanPlan {
+  int nc, hpg, nhb, nseg, cps, terms;
+  size_t sd, states, segst, segdec;  // bytes
+};
+
+// Segments of the state kernels: a sequence's chunks form a chain, so with
+// fewer (sequence, head block) pairs than 608 CTAs (four for each of 152 SMs)
+// it is cut, into runs of two chunks at least.
+ScanPlan scan_plan(const m2rnn_shape* s) {
+  ScanPlan q;
+  const int Nq = s->Nq == 0 ? 1 : s->Nq;
+  q.nc = (s->T + m2rnn::kChunk - 1) / m2rnn::kChunk;
+  q.hpg = s->N / Nq;
+  q.nhb = (q.hpg * s->V + m2rnn::kCols - 1) / m2rnn::kCols;
+  q.terms = m2rnn::scan_state_terms(s->in_dtype == M2RNN_F32);
+  const long long pairs = static_cast<long long>(s->B) * Nq * q.nhb;
+  long long seg = (608 + pairs - 1) / pairs;
+  if (seg > q.nc / 2) seg = q.nc / 2;
+  if (seg < 1) seg = 1;
+  q.cps = static_cast<int>((q.nc + seg - 1) / seg);
+  if (q.cps < 1) q.cps = 1;
+  q.nseg = (q.nc + q.cps - 1) / q.cps;
+  const size_t tile = static_cast<size_t>(m2rnn::kCols) * s->K;
+  const size_t heads = static_cast<size_t>(s->B) * s->N;
+  q.sd = align256(heads * q.nc * m2rnn::kChunk * sizeof(float2));
+  q.states = align256(pairs * q.nc * q.terms * tile * sizeof(__nv_bfloat16));
+  q.segst = q.nseg > 1 ? align256(pairs * q.nseg * tile * sizeof(float)) : 0;
+  q.segdec = q.nseg > 1 ? align256(heads * q.nseg * sizeof(float)) : 0;
+  return q;
+}
+
+// CTAs per chunk and group in the chunk-parallel kernels: the head blocks are
+// split where there are fewer than 1,216 chunks (two waves of 608 CTAs).
+int scan_hsplit(const m2rnn_shape* s, const ScanPlan& q) {
+  const long long chunks = static_cast<long long>(s->B) * (s->Nq == 0 ? 1 : s->Nq) * q.nc;
+  long long want = (1216 + chunks - 1) / chunks;
+  if (want > q.nhb) want = q.nhb;
+  const int per = static_cast<int>((q.nhb + want - 1) / want);
+  return (q.nhb + per - 1) / per;
+}
+
+// Workspace of the backward pass: fp32 shares of dq, dk where several CTAs add
+// to them, and the chunks' shares of the parameters' gradients.
+size_t scan_share_bytes(const m2rnn_shape* s, const ScanPlan& q) {
+  const int split = scan_hsplit(s, q);
+  if (split == 1) return 0;
+  return align256(static_cast<size_t>(split) * 2 * s->B * s->T * (s->Nq == 0 ? 1 : s->Nq) * s->K *
+                  sizeof(float));
+}
+size_t scan_part_bytes(const m2rnn_shape* s, const ScanPlan& q) {
+  return align256(static_cast<size_t>(s->B) * q.nc * s->N * (2 + s->V) * sizeof(float));
+}
+
+int check_scan(const m2rnn_shape* s) {
+  const int rc = m2rnn::validate_shape(s);
+  if (rc != M2RNN_OK) return rc;
+  if (s->T > (1 << 30)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
+  const ScanPlan q = scan_plan(s);
+  const double ctas = static_cast<double>(s->B) * q.nhb * (s->Nq == 0 ? 1 : s->Nq) * q.nc;
+  return ctas < 1073741824.0 ? M2RNN_OK : M2RNN_ERR_UNSUPPORTED_SHAPE;  // 2^30
+}
+
+// The arguments that both directions share, with rows and plan.
+int scan_common(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void* q, const void* k,
+                const void* v, const void* a, const void* alpha, const void* beta,
+                const void* w_r, const float* H0, m2rnn::ScanParams* p, ScanPlan* plan, int* dev) {
+  int rc = check_scan(s);
+  if (rc != M2RNN_OK) return rc;
+  const int Nq = s->Nq == 0 ? 1 : s->Nq;
+  const long long qw = static_cast<long long>(Nq) * s->K, vw = static_cast<long long>(s->N) * s->V;
+  const long long e = static_cast<long long>(esize(s->in_dtype));
+  m2rnn_rows qr, kr, vr, ar;
+  if ((rc = read_rows(rows ? &rows->q : nullptr, s->T, qw, s->in_dtype, 16, &qr)) != M2RNN_OK ||
+      (rc = read_rows(rows ? &rows->k : nullptr, s->T, qw, s->in_dtype, 16, &kr)) != M2RNN_OK ||
+      (rc = read_rows(rows ? &rows->v : nullptr, s->T, vw, s->in_dtype, 16, &vr)) != M2RNN_OK ||
+      (rc = read_rows(rows ? &rows->a : nullptr, s->T, s->N, s->in_dtype, e, &ar)) != M2RNN_OK)
+    return rc;
+  int sms, *status;
+  if ((rc = host_device_info(dev, &status, &sms)) != M2RNN_OK) return rc;
+  const void* req[] = {alpha, beta};
+  const void* opt[] = {w_r, H0};
+  if ((rc = require(req, *dev)) != M2RNN_OK || (rc = allow(opt, *dev)) != M2RNN_OK) return rc;
+  if (s->T > 0) {
+    const void* req2[] = {q, k, v};
+    if ((rc = require(req2, *dev)) != M2RNN_OK) return rc;
+    if ((rc = m2rnn::host_check_elem_ptr(a, *dev, static_cast<size_t>(e))) != M2RNN_OK) return rc;
+  }
+  *plan = scan_plan(s);
+  *p = m2rnn::ScanParams{};
+  p->q = q;
+  p->k = k;
+  p->v = v;
+  p->a = a;
+  p->alpha = alpha;
+  p->beta = beta;
+  p->w_r = w_r;
+  p->H0 = H0;
+  p->qb = qr.batch;
+  p->qt = qr.token;
+  p->kb = kr.batch;
+  p->kt = kr.token;
+  p->vb = vr.batch;
+  p->vt = vr.token;
+  p->ab = ar.batch;
+  p->at = ar.token;
+  p->B = s->B;
+  p->T = s->T;
+  p->N = s->N;
+  p->Nq = Nq;
+  p->K = s->K;
+  p->V = s->V;
+  p->nc = plan->nc;
+  p->hpg = plan->hpg;
+  p->nhb = plan->nhb;
+  p->nseg = plan->nseg;
+  p->cps = plan->cps;
+  p->hsplit = scan_hsplit(s, *plan);
+  p->status = status;
+  return M2RNN_OK;
+}
+
+// Hands out pieces of the workspace.
+struct Carve {
+  char* at;
+  template <class T>
+  T* take(size_t bytes) {
+    T* r = bytes ? reinterpret_cast<T*>(at) : nullptr;
+    at += bytes;
+    return r;
+  }
+};
 
 }  // namespace
 
@@ -331,6 +466,121 @@ int m2rnn_qk_norm_bwd(const m2rnn_qk_shape* s, const void* q, const m2rnn_rows* 
   p.nparts = m2rnn::qk_bwd_parts(s);
   return status_from_cuda(m2rnn::launch_qk_bwd(p, s->in_dtype == M2RNN_F32,
                                                s->grad_dtype == M2RNN_F32, st));
+}
+
+size_t m2rnn_scan_saved_size(const m2rnn_shape* s) {
+  if (check_scan(s) != M2RNN_OK || s->T == 0) return 0;
+  const ScanPlan q = scan_plan(s);
+  return q.sd + q.states;
+}
+
+size_t m2rnn_scan_fwd_workspace_size(const m2rnn_shape* s, int saved_given) {
+  if (check_scan(s) != M2RNN_OK || s->T == 0) return 0;
+  const ScanPlan q = scan_plan(s);
+  return (saved_given ? 0 : q.sd + q.states) + q.segst + q.segdec;
+}
+
+int m2rnn_scan_fwd(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void* q,
+                   const void* k, const void* v, const void* a, const void* alpha,
+                   const void* beta, const void* w_r, const float* H0, void* y, float* H_T,
+                   void* saved, void* workspace, size_t ws_bytes, void* stream) {
+  m2rnn::ScanParams p;
+  ScanPlan plan;
+  int dev;
+  int rc = scan_common(s, rows, q, k, v, a, alpha, beta, w_r, H0, &p, &plan, &dev);
+  if (rc != M2RNN_OK) return rc;
+  const void* opt[] = {H_T, saved};
+  if ((rc = allow(opt, dev)) != M2RNN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s->T == 0) {
+    if (H_T == nullptr) return M2RNN_OK;
+    const size_t bytes = static_cast<size_t>(s->B) * s->N * s->K * s->V * sizeof(float);
+    return status_from_cuda(H0 ? cudaMemcpyAsync(H_T, H0, bytes, cudaMemcpyDeviceToDevice, st)
+                               : cudaMemsetAsync(H_T, 0, bytes, st));
+  }
+  if ((rc = host_check_ptr(y, dev, true)) != M2RNN_OK) return rc;
+  const size_t need = m2rnn_scan_fwd_workspace_size(s, saved != nullptr);
+  if (need > 0) {
+    if (workspace == nullptr || ws_bytes < need) return M2RNN_ERR_WORKSPACE;
+    if ((rc = host_check_ptr(workspace, dev, true)) != M2RNN_OK) return rc;
+  }
+  Carve ws{static_cast<char*>(workspace)};
+  char* keep = saved ? static_cast<char*>(saved) : ws.take<char>(plan.sd + plan.states);
+  p.y = y;
+  p.HT = H_T;
+  p.sd = reinterpret_cast<float2*>(keep);
+  p.Hs = reinterpret_cast<__nv_bfloat16*>(keep + plan.sd);
+  p.segst = ws.take<float>(plan.segst);
+  p.segdec = ws.take<float>(plan.segdec);
+  const bool f32 = s->in_dtype == M2RNN_F32;
+  if (m2rnn::launch_scan_states(p, f32, false, st) != cudaSuccess) return M2RNN_ERR_CUDA;
+  return status_from_cuda(m2rnn::launch_scan_out(p, f32, st));
+}
+
+size_t m2rnn_scan_bwd_workspace_size(const m2rnn_shape* s, int saved_given) {
+  if (check_scan(s) != M2RNN_OK || s->T == 0) return 0;
+  const ScanPlan q = scan_plan(s);
+  return (saved_given ? 0 : q.sd + q.states) + q.states + q.segst + q.segdec +
+         scan_share_bytes(s, q) + scan_part_bytes(s, q);
+}
+
+int m2rnn_scan_bwd(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void* q,
+                   const void* k, const void* v, const void* a, const void* alpha,
+                   const void* beta, const void* w_r, const float* H0, const void* saved,
+                   const void* dy, const float* dH_T, void* dq, void* dk, void* dv, void* da,
+                   float* dalpha, float* dbeta, float* dw_r, float* dH0, void* workspace,
+                   size_t ws_bytes, void* stream) {
+  m2rnn::ScanParams p;
+  ScanPlan plan;
+  int dev;
+  int rc = scan_common(s, rows, q, k, v, a, alpha, beta, w_r, H0, &p, &plan, &dev);
+  if (rc != M2RNN_OK) return rc;
+  if ((w_r == nullptr) != (dw_r == nullptr)) return M2RNN_ERR_INVALID_ARG;
+  const void* req[] = {dalpha, dbeta};
+  const void* opt[] = {saved, dH_T, dw_r, dH0};
+  if ((rc = require(req, dev)) != M2RNN_OK || (rc = allow(opt, dev)) != M2RNN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s->T == 0) {  // no tokens: dH0 = dH_T
+    const size_t n = s->N * sizeof(float);
+    const size_t bytes = static_cast<size_t>(s->B) * s->N * s->K * s->V * sizeof(float);
+    if (cudaMemsetAsync(dalpha, 0, n, st) != cudaSuccess ||
+        cudaMemsetAsync(dbeta, 0, n, st) != cudaSuccess ||
+        (dw_r != nullptr && cudaMemsetAsync(dw_r, 0, n * s->V, st) != cudaSuccess))
+      return M2RNN_ERR_CUDA;
+    if (dH0 == nullptr) return M2RNN_OK;
+    return status_from_cuda(dH_T ? cudaMemcpyAsync(dH0, dH_T, bytes, cudaMemcpyDeviceToDevice, st)
+                                 : cudaMemsetAsync(dH0, 0, bytes, st));
+  }
+  const void* req2[] = {dy, dq, dk, dv, da};
+  if ((rc = require(req2, dev)) != M2RNN_OK) return rc;
+  if (workspace == nullptr || ws_bytes < m2rnn_scan_bwd_workspace_size(s, saved != nullptr))
+    return M2RNN_ERR_WORKSPACE;
+  if ((rc = host_check_ptr(workspace, dev, true)) != M2RNN_OK) return rc;
+  Carve ws{static_cast<char*>(workspace)};
+  char* keep = saved ? static_cast<char*>(const_cast<void*>(saved))  // read only
+                     : ws.take<char>(plan.sd + plan.states);
+  p.dy = dy;
+  p.dHT = dH_T;
+  p.dq = dq;
+  p.dk = dk;
+  p.dv = dv;
+  p.da = da;
+  p.dalpha = dalpha;
+  p.dbeta = dbeta;
+  p.dw_r = dw_r;
+  p.dH0 = dH0;
+  p.sd = reinterpret_cast<float2*>(keep);
+  p.Hs = reinterpret_cast<__nv_bfloat16*>(keep + plan.sd);
+  p.Rs = ws.take<__nv_bfloat16>(plan.states);
+  p.segst = ws.take<float>(plan.segst);
+  p.segdec = ws.take<float>(plan.segdec);
+  p.dqk = ws.take<float>(scan_share_bytes(s, plan));
+  p.part = ws.take<float>(scan_part_bytes(s, plan));
+  const bool f32 = s->in_dtype == M2RNN_F32;
+  if (saved == nullptr && m2rnn::launch_scan_states(p, f32, false, st) != cudaSuccess)
+    return M2RNN_ERR_CUDA;
+  if (m2rnn::launch_scan_states(p, f32, true, st) != cudaSuccess) return M2RNN_ERR_CUDA;
+  return status_from_cuda(m2rnn::launch_scan_bwd(p, f32, st));
 }
 
 int m2rnn_scan_step(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void* q,

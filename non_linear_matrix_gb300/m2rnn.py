@@ -58,6 +58,11 @@ _EXPORTS = {
     "m2rnn_qk_norm_bwd_workspace_size": (ctypes.c_size_t, [_VP]),
     "m2rnn_qk_norm_bwd": (ctypes.c_int, [_VP] * 7 + [ctypes.c_float] + [_VP] * 10 +
                           [ctypes.c_size_t, _VP]),
+    "m2rnn_scan_saved_size": (ctypes.c_size_t, [_VP]),
+    "m2rnn_scan_fwd_workspace_size": (ctypes.c_size_t, [_VP, ctypes.c_int]),
+    "m2rnn_scan_fwd": (ctypes.c_int, [_VP] * 14 + [ctypes.c_size_t, _VP]),
+    "m2rnn_scan_bwd_workspace_size": (ctypes.c_size_t, [_VP, ctypes.c_int]),
+    "m2rnn_scan_bwd": (ctypes.c_int, [_VP] * 22 + [ctypes.c_size_t, _VP]),
     "m2rnn_scan_step": (ctypes.c_int, [_VP] * 13),
 }
 
@@ -678,6 +683,77 @@ def _scan_args(q, k, v, a, alpha, beta, w_r, lead: int):
     _expect("w_r", w_r, (N, V), q.dtype)
     rows = ScanRows(_rows(q, lead), _rows(k, lead), _rows(v, lead), _rows(a, lead))
     return Shape(B, T, N, K, V, _dtype_code(q), 0, Nq), rows
+
+
+def scan_fwd(q, k, v, a, alpha, beta, w_r=None, H0=None, *, want_HT: bool = True,
+             save: bool = False, workspace=None, out=None, stream=None):
+    """Selective scan H_t = exp(-alpha dt_t) H_{t-1} + dt_t k_t v_t^T, dt =
+    softplus(a + beta), y_t = H_t^T q_t + w_r (.) v_t.  Returns (y, H_T or
+    None, saved or None).
+
+    q, k [B,T,K] or [B,T,Nq,K]; v [B,T,N,V]; a [B,T,N] (rows may be slices
+    of a wider buffer); alpha, beta [N]; w_r [N,V] or None; H0 [B,N,K,V] fp32
+    or None.  save=True keeps what ``scan_bwd`` would otherwise recompute (an
+    opaque buffer).  ``out`` may supply y, HT and saved."""
+    s, rows = _scan_args(q, k, v, a, alpha, beta, w_r, 2)
+    state, dev = (s.B, s.N, s.K, s.V), q.device
+    _expect("H0", H0, state, torch.float32)
+    out = dict(out or {})
+    y = _out(out.get("y"), (s.B, s.T, s.N, s.V), q.dtype, dev, "y")
+    HT, saved = out.get("HT"), out.get("saved")
+    if HT is not None or want_HT:
+        HT = _out(HT, state, torch.float32, dev, "HT")
+    L = lib()
+    if saved is None and save:
+        saved = torch.empty(max(int(L.m2rnn_scan_saved_size(ctypes.byref(s))), 16), device=dev,
+                            dtype=torch.uint8)
+    elif saved is not None and saved.numel() < int(L.m2rnn_scan_saved_size(ctypes.byref(s))):
+        raise ValueError("saved is smaller than m2rnn_scan_saved_size")
+    ws = _workspace(workspace, int(L.m2rnn_scan_fwd_workspace_size(ctypes.byref(s),
+                                                                   int(saved is not None))), dev)
+    rc = L.m2rnn_scan_fwd(ctypes.byref(s), ctypes.byref(rows), _at(q), _at(k), _at(v), _at(a),
+                          _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(H0), _ptr(y), _ptr(HT),
+                          _ptr(saved), _ptr(ws), _nbytes(ws), _stream(stream))
+    _check(rc, "m2rnn_scan_fwd")
+    return y, HT, saved
+
+
+def scan_bwd(q, k, v, a, alpha, beta, dy, w_r=None, H0=None, dHT=None, *, saved=None,
+             want_dH0: bool = False, workspace=None, out=None, stream=None):
+    """Gradient of ``scan_fwd`` for dL/dy = dy (v's dtype) and dL/dH_T = dHT
+    (fp32 or None): dict(dq, dk, dv, da (the inputs' dtype), dalpha, dbeta,
+    dw_r (fp32; None without w_r)[, dH0]).  ``saved`` comes from
+    ``scan_fwd(..., save=True)`` on the same inputs; without it the forward
+    states are computed again."""
+    s, rows = _scan_args(q, k, v, a, alpha, beta, w_r, 2)
+    state, dev, f32 = (s.B, s.N, s.K, s.V), q.device, torch.float32
+    _expect("H0", H0, state, f32)
+    _expect("dHT", dHT, state, f32)
+    _expect("dy", dy, (s.B, s.T, s.N, s.V), q.dtype)
+    out, L = dict(out or {}), lib()
+    g = {"dq": _out(out.get("dq"), tuple(q.shape), q.dtype, dev, "dq"),
+         "dk": _out(out.get("dk"), tuple(q.shape), q.dtype, dev, "dk"),
+         "dv": _out(out.get("dv"), (s.B, s.T, s.N, s.V), q.dtype, dev, "dv"),
+         "da": _out(out.get("da"), (s.B, s.T, s.N), q.dtype, dev, "da"),
+         "dalpha": _out(out.get("dalpha"), (s.N,), f32, dev, "dalpha"),
+         "dbeta": _out(out.get("dbeta"), (s.N,), f32, dev, "dbeta"),
+         "dw_r": None if w_r is None else _out(out.get("dw_r"), (s.N, s.V), f32, dev, "dw_r")}
+    dH0 = out.get("dH0")
+    if dH0 is not None or want_dH0:
+        dH0 = _out(dH0, state, f32, dev, "dH0")
+    if saved is not None and saved.numel() < int(L.m2rnn_scan_saved_size(ctypes.byref(s))):
+        raise ValueError("saved is smaller than m2rnn_scan_saved_size")
+    ws = _workspace(workspace, int(L.m2rnn_scan_bwd_workspace_size(ctypes.byref(s),
+                                                                   int(saved is not None))), dev)
+    rc = L.m2rnn_scan_bwd(ctypes.byref(s), ctypes.byref(rows), _at(q), _at(k), _at(v), _at(a),
+                          _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(H0), _ptr(saved), _ptr(dy),
+                          _ptr(dHT), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["da"]),
+                          _ptr(g["dalpha"]), _ptr(g["dbeta"]), _ptr(g["dw_r"]), _ptr(dH0),
+                          _ptr(ws), _nbytes(ws), _stream(stream))
+    _check(rc, "m2rnn_scan_bwd")
+    if dH0 is not None:
+        g["dH0"] = dH0
+    return g
 
 
 def scan_step(q, k, v, a, alpha, beta, H, w_r=None, *, H_out=None, y=None, stream=None):
