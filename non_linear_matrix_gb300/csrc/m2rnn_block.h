@@ -106,16 +106,21 @@ struct ScanParams {
   int hpg, nhb;   // heads per group, head blocks per group
   int nseg, cps;  // segments of a sequence in the state kernels, chunks in each
   int hsplit;     // CTAs that share a chunk's head blocks
-  float2* sd;     // [B][N][nc * 64]: (log2 decay since the token's 16-block began, dt)
-  __nv_bfloat16* Hs;  // states before each chunk: [B][Nq * nhb][nc][terms][64 x K]
-  __nv_bfloat16* Rs;  // gradients of the states after each chunk, the same layout
-  float* segst;   // [B][Nq * nhb][nseg][64 x K]: states at the segments' ends
-  float* segdec;  // [B][N][nseg]: log2 decay over a segment
+  // The gate's values of a chunk, [B][N][nc][3][64]: sums of log2 decay from the
+  // token's 16-block's start (loc); dt; the token's weight at its block's end,
+  // dt 2^(block's sum - loc).
+  float* gate;
+  float* cdec;    // [B][N][nc]: log2 decay from the segment's start to the chunk
+  float* Hl;      // [B][Nq * nhb][nc][64 x K]: states before each chunk, without what
+                  // came before their segment
+  float* Hseg;    // [B][Nq * nhb][nseg][64 x K]: states at the segments' ends
+  float* rdec;    // cdec, Hl and Hseg of the reverse states
+  float* Rl;
+  float* Rseg;
   float* dqk;     // hsplit > 1: [hsplit][2][B][T][Nq][K] shares of dq, dk
   float* part;    // [B * nc][N * (2 + V)] shares of dalpha, dbeta, dw_r
   int* status;
 };
-int scan_state_terms(bool f32);
 cudaError_t launch_scan_states(const ScanParams& p, bool f32, bool reverse, cudaStream_t st);
 cudaError_t launch_scan_out(const ScanParams& p, bool f32, cudaStream_t st);
 cudaError_t launch_scan_bwd(const ScanParams& p, bool f32, cudaStream_t st);

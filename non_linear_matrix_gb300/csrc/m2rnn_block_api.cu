@@ -1,7 +1,6 @@
 // m2rnn_block_api.cu -- the extern "C" entry points declared in
 // include/m2rnn_block.h: argument validation and launch planning of the
 // convolution, the q/k norm and the selective scan.
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -168,42 +167,54 @@ int qk_common(const m2rnn_qk_shape* s, const void* q, const m2rnn_rows* q_rows, 
 // ---- selective scan -------------------------------------------------------------
 
 struct ScanPlan {
-  int nc, hpg, nhb, nseg, cps, terms;
-  size_t sd, states, segst, segdec;  // bytes
+  int nc, hpg, nhb, nseg, cps;
+  size_t gate, dec, states, ends;  // bytes
+  size_t saved() const { return gate + one_way(); }
+  size_t one_way() const { return dec + states + ends; }
 };
 
-// Segments of the state kernels: a sequence's chunks form a chain, so with
-// fewer (sequence, head block) pairs than 608 CTAs (four for each of 152 SMs)
-// it is cut, into runs of two chunks at least.
+// Segments of the state kernel: a sequence's chunks form a chain, so it is cut
+// where there are fewer (sequence, head block) pairs than 912 CTAs (six, the
+// most that are resident, for each of 152 SMs), into runs of two chunks at least.
 ScanPlan scan_plan(const m2rnn_shape* s) {
   ScanPlan q;
   const int Nq = s->Nq == 0 ? 1 : s->Nq;
   q.nc = (s->T + m2rnn::kChunk - 1) / m2rnn::kChunk;
   q.hpg = s->N / Nq;
   q.nhb = (q.hpg * s->V + m2rnn::kCols - 1) / m2rnn::kCols;
-  q.terms = m2rnn::scan_state_terms(s->in_dtype == M2RNN_F32);
   const long long pairs = static_cast<long long>(s->B) * Nq * q.nhb;
-  long long seg = (608 + pairs - 1) / pairs;
+  long long seg = 912 / pairs;
   if (seg > q.nc / 2) seg = q.nc / 2;
   if (seg < 1) seg = 1;
   q.cps = static_cast<int>((q.nc + seg - 1) / seg);
   if (q.cps < 1) q.cps = 1;
   q.nseg = (q.nc + q.cps - 1) / q.cps;
-  const size_t tile = static_cast<size_t>(m2rnn::kCols) * s->K;
+  const size_t tile = static_cast<size_t>(m2rnn::kCols) * s->K * sizeof(float);
   const size_t heads = static_cast<size_t>(s->B) * s->N;
-  q.sd = align256(heads * q.nc * m2rnn::kChunk * sizeof(float2));
-  q.states = align256(pairs * q.nc * q.terms * tile * sizeof(__nv_bfloat16));
-  q.segst = q.nseg > 1 ? align256(pairs * q.nseg * tile * sizeof(float)) : 0;
-  q.segdec = q.nseg > 1 ? align256(heads * q.nseg * sizeof(float)) : 0;
+  q.gate = align256(heads * q.nc * 3 * m2rnn::kChunk * sizeof(float));
+  q.dec = align256(heads * (q.nc + q.nseg) * sizeof(float));
+  q.states = align256(pairs * q.nc * tile);
+  q.ends = q.nseg > 1 ? align256(pairs * q.nseg * tile) : 0;
   return q;
 }
 
-// CTAs per chunk and group in the chunk-parallel kernels: the head blocks are
-// split where there are fewer than 1,216 chunks (two waves of 608 CTAs).
-int scan_hsplit(const m2rnn_shape* s, const ScanPlan& q) {
+// CTAs that share a chunk's head blocks.  Outputs: enough CTAs (1,824, three
+// times what is resident) that they even out over the SMs; a CTA's own cost, its
+// q and k tiles and their product, is about 0.4 of a head block.
+int scan_out_split(const m2rnn_shape* s, const ScanPlan& q) {
   const long long chunks = static_cast<long long>(s->B) * (s->Nq == 0 ? 1 : s->Nq) * q.nc;
-  long long want = (1216 + chunks - 1) / chunks;
+  long long want = (1824 + chunks - 1) / chunks;
   if (want > q.nhb) want = q.nhb;
+  const int per = static_cast<int>((q.nhb + want - 1) / want);
+  return (q.nhb + per - 1) / per;
+}
+// Gradients: more than one costs shares of dq and dk in fp32, so only as many as
+// it takes to give each SM its two resident CTAs.
+int scan_bwd_split(const m2rnn_shape* s, const ScanPlan& q) {
+  const long long chunks = static_cast<long long>(s->B) * (s->Nq == 0 ? 1 : s->Nq) * q.nc;
+  long long want = 304 / chunks;
+  if (want > q.nhb) want = q.nhb;
+  if (want < 1) want = 1;
   const int per = static_cast<int>((q.nhb + want - 1) / want);
   return (q.nhb + per - 1) / per;
 }
@@ -211,7 +222,7 @@ int scan_hsplit(const m2rnn_shape* s, const ScanPlan& q) {
 // Workspace of the backward pass: fp32 shares of dq, dk where several CTAs add
 // to them, and the chunks' shares of the parameters' gradients.
 size_t scan_share_bytes(const m2rnn_shape* s, const ScanPlan& q) {
-  const int split = scan_hsplit(s, q);
+  const int split = scan_bwd_split(s, q);
   if (split == 1) return 0;
   return align256(static_cast<size_t>(split) * 2 * s->B * s->T * (s->Nq == 0 ? 1 : s->Nq) * s->K *
                   sizeof(float));
@@ -283,7 +294,6 @@ int scan_common(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void* q
   p->nhb = plan->nhb;
   p->nseg = plan->nseg;
   p->cps = plan->cps;
-  p->hsplit = scan_hsplit(s, *plan);
   p->status = status;
   return M2RNN_OK;
 }
@@ -291,9 +301,8 @@ int scan_common(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void* q
 // Hands out pieces of the workspace.
 struct Carve {
   char* at;
-  template <class T>
-  T* take(size_t bytes) {
-    T* r = bytes ? reinterpret_cast<T*>(at) : nullptr;
+  float* take(size_t bytes) {
+    float* r = bytes ? reinterpret_cast<float*>(at) : nullptr;
     at += bytes;
     return r;
   }
@@ -471,13 +480,13 @@ int m2rnn_qk_norm_bwd(const m2rnn_qk_shape* s, const void* q, const m2rnn_rows* 
 size_t m2rnn_scan_saved_size(const m2rnn_shape* s) {
   if (check_scan(s) != M2RNN_OK || s->T == 0) return 0;
   const ScanPlan q = scan_plan(s);
-  return q.sd + q.states;
+  return q.saved();
 }
 
 size_t m2rnn_scan_fwd_workspace_size(const m2rnn_shape* s, int saved_given) {
   if (check_scan(s) != M2RNN_OK || s->T == 0) return 0;
   const ScanPlan q = scan_plan(s);
-  return (saved_given ? 0 : q.sd + q.states) + q.segst + q.segdec;
+  return saved_given ? 0 : q.saved();
 }
 
 int m2rnn_scan_fwd(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void* q,
@@ -504,14 +513,14 @@ int m2rnn_scan_fwd(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void
     if (workspace == nullptr || ws_bytes < need) return M2RNN_ERR_WORKSPACE;
     if ((rc = host_check_ptr(workspace, dev, true)) != M2RNN_OK) return rc;
   }
-  Carve ws{static_cast<char*>(workspace)};
-  char* keep = saved ? static_cast<char*>(saved) : ws.take<char>(plan.sd + plan.states);
+  Carve keep{static_cast<char*>(saved ? saved : workspace)};
   p.y = y;
   p.HT = H_T;
-  p.sd = reinterpret_cast<float2*>(keep);
-  p.Hs = reinterpret_cast<__nv_bfloat16*>(keep + plan.sd);
-  p.segst = ws.take<float>(plan.segst);
-  p.segdec = ws.take<float>(plan.segdec);
+  p.gate = keep.take(plan.gate);
+  p.cdec = keep.take(plan.dec);
+  p.Hl = keep.take(plan.states);
+  p.Hseg = keep.take(plan.ends);
+  p.hsplit = scan_out_split(s, plan);
   const bool f32 = s->in_dtype == M2RNN_F32;
   if (m2rnn::launch_scan_states(p, f32, false, st) != cudaSuccess) return M2RNN_ERR_CUDA;
   return status_from_cuda(m2rnn::launch_scan_out(p, f32, st));
@@ -520,8 +529,7 @@ int m2rnn_scan_fwd(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void
 size_t m2rnn_scan_bwd_workspace_size(const m2rnn_shape* s, int saved_given) {
   if (check_scan(s) != M2RNN_OK || s->T == 0) return 0;
   const ScanPlan q = scan_plan(s);
-  return (saved_given ? 0 : q.sd + q.states) + q.states + q.segst + q.segdec +
-         scan_share_bytes(s, q) + scan_part_bytes(s, q);
+  return (saved_given ? 0 : q.saved()) + q.one_way() + scan_share_bytes(s, q) + scan_part_bytes(s, q);
 }
 
 int m2rnn_scan_bwd(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void* q,
@@ -557,8 +565,12 @@ int m2rnn_scan_bwd(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void
     return M2RNN_ERR_WORKSPACE;
   if ((rc = host_check_ptr(workspace, dev, true)) != M2RNN_OK) return rc;
   Carve ws{static_cast<char*>(workspace)};
-  char* keep = saved ? static_cast<char*>(const_cast<void*>(saved))  // read only
-                     : ws.take<char>(plan.sd + plan.states);
+  Carve keep{static_cast<char*>(const_cast<void*>(saved))};  // read only
+  Carve& fwd = saved ? keep : ws;
+  p.gate = fwd.take(plan.gate);
+  p.cdec = fwd.take(plan.dec);
+  p.Hl = fwd.take(plan.states);
+  p.Hseg = fwd.take(plan.ends);
   p.dy = dy;
   p.dHT = dH_T;
   p.dq = dq;
@@ -569,13 +581,12 @@ int m2rnn_scan_bwd(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void
   p.dbeta = dbeta;
   p.dw_r = dw_r;
   p.dH0 = dH0;
-  p.sd = reinterpret_cast<float2*>(keep);
-  p.Hs = reinterpret_cast<__nv_bfloat16*>(keep + plan.sd);
-  p.Rs = ws.take<__nv_bfloat16>(plan.states);
-  p.segst = ws.take<float>(plan.segst);
-  p.segdec = ws.take<float>(plan.segdec);
-  p.dqk = ws.take<float>(scan_share_bytes(s, plan));
-  p.part = ws.take<float>(scan_part_bytes(s, plan));
+  p.rdec = ws.take(plan.dec);
+  p.Rl = ws.take(plan.states);
+  p.Rseg = ws.take(plan.ends);
+  p.dqk = ws.take(scan_share_bytes(s, plan));
+  p.part = ws.take(scan_part_bytes(s, plan));
+  p.hsplit = scan_bwd_split(s, plan);
   const bool f32 = s->in_dtype == M2RNN_F32;
   if (saved == nullptr && m2rnn::launch_scan_states(p, f32, false, st) != cudaSuccess)
     return M2RNN_ERR_CUDA;

@@ -12,20 +12,28 @@
 // to a few 2^-24 of the sum itself, however long the sequence, never as
 // differences of two long sums.
 //
-// Operands.  Products run on the tensor cores in bf16 with fp32 accumulation.
-// A value that has more than 8 bits (a state, a decayed product, any fp32
-// input) enters as a sum of bf16 terms, largest first: two terms hold 16
-// bits (error at most 2^-18 of the value), three hold the whole fp32 value.  A
-// product of values with PA and PB terms multiplies the pairs whose sizes
-// matter, i + j < max(PA, PB).
+// Operands.  Products run on the tensor cores (mma.sync) in bf16 with fp32
+// accumulation.  A value of more than 8 bits enters as a sum of bf16 terms,
+// largest first; three terms hold a whole fp32 value.  A product of values
+// with PA and PB terms multiplies the pairs that matter, i + j < max(PA, PB).
+// bf16 inputs are one term.  What ends in fp32 (states, gradients of
+// parameters) is made from three-term operands; a weight or state that only
+// meets an output rounded to bf16 enters with one, an error of the size of that
+// rounding.
 //
 // Head blocks.  A CTA works on 64 value columns at a time: 64 / V heads of
 // one query/key group, which share q and k and the products q_i.k_j.
 //
-// States are kept transposed, as 8 x 8 blocks (value column, key row) of 128
-// contiguous bytes, block (v8, k8) at (v8 K/8 + k8): what an accumulator of
-// the state's product holds is a block's row, whole lines are written, and
-// both the block and its transpose are operands without bank conflicts.
+// States are kept transposed, as 8 x 8 blocks (value column, key row), block
+// (v8, k8) at (v8 K/8 + k8), fp32 in global memory, bf16 terms of 128
+// contiguous bytes in shared memory: what an accumulator of the state's product
+// holds is a row of a block, whole lines are written, and both the block and
+// its transpose are operands without bank conflicts.
+//
+// Segments.  Along the chunks the state is a chain.  It is cut into segments
+// that run at the same time, each from zero; a small kernel then carries the
+// states from segment to segment, and whoever reads a state adds
+// 2^S(segment's start, chunk) times the state at the segment's start.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -41,16 +49,47 @@
 namespace m2rnn {
 namespace scan {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;  // that fill a tile together
 constexpr int kVLd = kCols + 8;  // shared row of a value tile: 144 bytes, no bank conflicts
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <bool F32>
 struct Terms {
-  static constexpr int in = F32 ? 3 : 1;     // of an input
-  static constexpr int state = F32 ? 3 : 2;  // of a state or a decayed input
-  static constexpr int prob = F32 ? 3 : 1;   // of a weight that only meets outputs of in_dtype
+  static constexpr int in = F32 ? 3 : 1;   // of an input
+  static constexpr int state = 3;          // of a state or decayed input that ends in fp32
+  static constexpr int out = F32 ? 3 : 1;  // of a weight or state that only meets an output
 };
+
+// Pairs of fp32 values in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 pair(const float (&x)[4], int half) {
+  return make_float2(x[2 * half], x[2 * half + 1]);
+}
+__device__ __forceinline__ void set_pair(float (&x)[4], int half, float2 v) {
+  x[2 * half] = v.x;
+  x[2 * half + 1] = v.y;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -69,6 +108,14 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr));
 }
 
+// Barrier 1, of `threads` threads: some only announce themselves.
+__device__ __forceinline__ void bar_arrive(int threads) {
+  asm volatile("bar.arrive 1, %0;" ::"r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_wait(int threads) {
+  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+}
+
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool on) {
   const int n = on ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
@@ -79,15 +126,22 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
 // The P bf16 terms of a pair of values, packed.
 template <int P>
-__device__ __forceinline__ void split(float a, float b, uint32_t (&t)[P]) {
+__device__ __forceinline__ void split(float2 v, uint32_t (&t)[P]) {
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    t[i] = ptx::pack_bf16x2(a, b);
+    t[i] = ptx::pack_bf16x2(v.x, v.y);
+    // v - term is exact: the sign bit flips in both halves at once
     if (i + 1 < P) {
-      a -= ptx::bf16x2_lo(t[i]);
-      b -= ptx::bf16x2_hi(t[i]);
+      const uint32_t n = t[i] ^ 0x80008000u;
+      v = add2(v, make_float2(ptx::bf16x2_lo(n), ptx::bf16x2_hi(n)));
     }
   }
 }
@@ -118,6 +172,24 @@ __device__ __forceinline__ void mma_terms(float (&acc)[4], const uint32_t (&a)[P
     }
 }
 
+// The same for N accumulators that share A, term by term across them: a
+// product's result is ready about 20 clocks after its issue, so consecutive
+// products go to different accumulators.
+template <int PA, int PB, int N>
+__device__ __forceinline__ void mma_terms_n(float (&acc)[N][4], const uint32_t (&a)[PA][4],
+                                            const uint32_t (&b)[N][PB][2]) {
+  constexpr int most = (PA > PB ? PA : PB) - 1;
+#pragma unroll
+  for (int s = most; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < PA; ++i) {
+      const int j = s - i;
+      if (j >= 0 && j < PB)
+#pragma unroll
+        for (int n = 0; n < N; ++n) ptx::mma_bf16_16816(acc[n], a[i], b[n][j][0], b[n][j][1]);
+    }
+}
+
 // ---- tiles ------------------------------------------------------------------
 //
 // A tile holds 64 tokens' rows of up to `width` elements as P planes of
@@ -126,40 +198,38 @@ __device__ __forceinline__ void mma_terms(float (&acc)[4], const uint32_t (&a)[P
 
 // Fills a tile from global rows; rows at or past `rows` and columns at or past
 // `cols` become zero.  bf16 by asynchronous copies, fp32 through registers as
-// three terms.
-template <bool F32>
-__device__ __forceinline__ void load_tile(uint32_t dst, const void* src_, long long stride, int rows,
-                                          int cols, int width, int ld, int* status, int row_extent) {
+// three terms.  tid: the caller's place among kThreads threads.
+template <bool F32, int WIDTH>
+__device__ __forceinline__ void load_tile(int tid, uint32_t dst, const void* src_, long long stride,
+                                          int rows, int cols, int* status, int row_extent) {
   using E = typename Elem<F32>::T;
+  constexpr int per_row = WIDTH / 8, ld = WIDTH + 8, step = kThreads / per_row;  // rows per pass
+  const int r0 = tid / per_row, c = (tid % per_row) * 8;
+  const bool col_on = c < cols;
   const E* src = static_cast<const E*>(src_);
-  const int per_row = width / 8;
-  for (int e = threadIdx.x; e < kChunk * per_row; e += kThreads) {
-    const int r = e / per_row, c = (e - r * per_row) * 8;
-    bool on = r < rows && c < cols;
-    if (on) on = in_range(status, r, 1, row_extent, CHK_SCAN_IN);
-    const uint32_t d = dst + (r * ld + c) * 2;
-    const E* s = on ? src + r * stride + c : src;
+  const E* s = src + r0 * stride + c;
+  uint32_t d = dst + (r0 * ld + c) * 2;
+#pragma unroll
+  for (int i = 0; i < kChunk / step; ++i) {
+    const int r = r0 + i * step;
+    const bool on = col_on && r < rows && in_range(status, r, 1, row_extent, CHK_SCAN_IN);
     if constexpr (!F32) {
-      cp_async16_zfill(d, s, on);
+      cp_async16_zfill(d, on ? s : src, on);
     } else {
       float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if (on) load_vec<true, 8>(s, x);
       uint32_t t[4][3];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) split<3>(x[2 * i], x[2 * i + 1], t[i]);
+      for (int j = 0; j < 4; ++j) split<3>(make_float2(x[2 * j], x[2 * j + 1]), t[j]);
 #pragma unroll
       for (int p = 0; p < 3; ++p)
         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(d + p * kChunk * ld * 2),
                      "r"(t[0][p]), "r"(t[1][p]), "r"(t[2][p]), "r"(t[3][p])
                      : "memory");
     }
+    s += step * stride;
+    d += step * ld * 2;
   }
-}
-
-// Copies `bytes` (a multiple of 16) as they are.
-__device__ __forceinline__ void load_linear(uint32_t dst, const void* src, int bytes) {
-  for (int e = threadIdx.x * 16; e < bytes; e += kThreads * 16)
-    ptx::cp_async16(dst + e, static_cast<const char*>(src) + e);
 }
 
 // Address of a lane's row for ldmatrix of the 16 x 16 piece at (r0, c0) of a
@@ -244,25 +314,107 @@ __device__ __forceinline__ void state_bt2(uint32_t (&b0)[P][2], uint32_t (&b1)[P
   }
 }
 
+// The 16-row block of warp w of four.  The blocks differ in causal work and a
+// warp's place decides which quarter of its SM it runs on: the order turns from
+// CTA to CTA such that the CTAs that an SM holds at a time (152 apart) differ.
+__device__ __forceinline__ int row_block(int w) { return (w + (blockIdx.x >> 3)) & 3; }
+
 // ---- places -------------------------------------------------------------------
 
 struct Place {
   int b, group, hb;  // batch item, query/key group, head block within the group
   int head0, heads;  // first head of the block and how many it has
 };
-__device__ __forceinline__ Place place_of(const ScanParams& p, int b, int gb) {
+// Head block hb of a group (no division: this is done once per head block).
+__device__ __forceinline__ Place place_in(const ScanParams& p, int per, int b, int group, int hb) {
   Place w;
   w.b = b;
-  w.group = gb / p.nhb;
-  w.hb = gb - w.group * p.nhb;
-  const int per = kCols / p.V;
-  w.head0 = w.group * p.hpg + w.hb * per;
-  w.heads = min(per, p.hpg - w.hb * per);
+  w.group = group;
+  w.hb = hb;
+  w.head0 = group * p.hpg + hb * per;
+  w.heads = min(per, p.hpg - hb * per);
   return w;
 }
+__device__ __forceinline__ Place place_of(const ScanParams& p, int b, int gb) {
+  const int group = gb / p.nhb;
+  return place_in(p, kCols / p.V, b, group, gb - group * p.nhb);
+}
 
-__device__ __forceinline__ size_t state_at(const ScanParams& p, int terms, int b, int gb, int c) {
-  return ((static_cast<size_t>(b) * p.Nq * p.nhb + gb) * p.nc + c) * terms * kCols * p.K;
+// A segment's first state is the one its predecessor ended with; the first
+// segment starts from the given state itself.
+struct StateRef {
+  const float* own;    // 64 x K, before the chunk, from the segment's start
+  const float* start;  // 64 x K, at the segment's start (NULL: nothing to add)
+  const float* dec;    // [heads * nc]: log2 decay from there, head h's at h * nc
+};
+// seg: the segment that made the chunk's state.
+__device__ __forceinline__ StateRef state_ref(const ScanParams& p, const float* local,
+                                              const float* ends, const float* dec, const Place& w,
+                                              int c, int seg) {
+  const size_t pair = (static_cast<size_t>(w.b) * p.Nq + w.group) * p.nhb + w.hb, tile = kCols * p.K;
+  StateRef r;
+  r.own = local + (pair * p.nc + c) * tile;
+  r.start = seg == 0 ? nullptr : ends + (pair * p.nseg + seg - 1) * tile;
+  r.dec = dec + (static_cast<size_t>(w.b) * p.N + w.head0) * p.nc + c;
+  return r;
+}
+
+// Eight values of a state (a row of a block), element e of the tile: the loads,
+// and apart from them the sum, so that several rows' loads can be in flight.
+struct StateRow {
+  float4 a, b, s, t;
+  float dec;
+};
+template <int K, int V>
+__device__ __forceinline__ StateRow state_load(const ScanParams& p, const StateRef& r, int e) {
+  StateRow x;
+  x.a = __ldg(reinterpret_cast<const float4*>(r.own + e));
+  x.b = __ldg(reinterpret_cast<const float4*>(r.own + e) + 1);
+  x.s = x.t = make_float4(0.f, 0.f, 0.f, 0.f);
+  x.dec = 0.f;
+  if (r.start != nullptr) {
+    x.s = __ldg(reinterpret_cast<const float4*>(r.start + e));
+    x.t = __ldg(reinterpret_cast<const float4*>(r.start + e) + 1);
+    x.dec = __ldg(r.dec + static_cast<size_t>(e / (K * V)) * p.nc);
+  }
+  return x;
+}
+__device__ __forceinline__ void state_sum(const StateRow& r, float2 (&x)[4]) {
+  const float2 d = both(ex2(r.dec));
+  x[0] = fma2(make_float2(r.s.x, r.s.y), d, make_float2(r.a.x, r.a.y));
+  x[1] = fma2(make_float2(r.s.z, r.s.w), d, make_float2(r.a.z, r.a.w));
+  x[2] = fma2(make_float2(r.t.x, r.t.y), d, make_float2(r.b.x, r.b.y));
+  x[3] = fma2(make_float2(r.t.z, r.t.w), d, make_float2(r.b.z, r.b.w));
+}
+
+// Asks for a state's own tile to be in L2 by the time it is fetched.
+__device__ __forceinline__ void state_prefetch(int tid, const StateRef& r, int n) {
+  for (int e = tid * 32; e < n; e += kThreads * 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(r.own + e));
+}
+
+// Writes a state row's P terms into the shared tile.
+template <int P, int K>
+__device__ __forceinline__ void put_state_row(uint32_t tile, int e, const float2 (&x)[4]) {
+  uint32_t t[4][P];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) split<P>(x[j], t[j]);
+#pragma unroll
+  for (int q = 0; q < P; ++q)
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(tile + (q * kCols * K + e) * 2),
+                 "r"(t[0][q]), "r"(t[1][q]), "r"(t[2][q]), "r"(t[3][q])
+                 : "memory");
+}
+
+// A chunk's gate values of the block's heads: [heads][3][64] floats.
+__device__ __forceinline__ void load_gate(int tid, uint32_t dst, const ScanParams& p, const Place& w,
+                                          int c) {
+  for (int e = tid; e < w.heads * 48; e += kThreads) {
+    const int h = e / 48, o = (e - h * 48) * 4;
+    const size_t at = ((static_cast<size_t>(w.b) * p.N + w.head0 + h) * p.nc + c) * 192 + o;
+    if (in_range(p.status, at, 4, static_cast<size_t>(p.B) * p.N * p.nc * 192, CHK_SCAN_WS))
+      ptx::cp_async16(dst + (h * 192 + o) * 4, p.gate + at);
+  }
 }
 
 }  // namespace scan

@@ -15,17 +15,24 @@
 //     da_t = sigmoid(a + beta) ((Uin_t + sum_i D_it) / dt_t - alpha dl_t)
 //     dalpha = - sum dt dl,  dbeta = sum da,  dw_r = sum u (.) v
 //
-// (dl_t: with respect to the natural logarithm of the decay; the last sum
-// is the row sums of D from t on less its column sums from t on.)
+// (dl_t: with respect to the natural logarithm of the decay; its last sum is the
+// row sums of D from t on less its column sums from t on, both without the
+// diagonal, which would cancel and where the decay is strong is most of D.)
 //
 // A CTA takes one chunk of one group and walks over its head blocks: dq and
-// dk, and sum over heads of E L, stay in registers, so neither needs a sum
+// dk, and the sum over heads of E L, stay in registers, so neither needs a sum
 // over CTAs (unless the head blocks are shared out, then their shares are
-// added in order).  Warp w holds rows j = 16 w.. of everything indexed by j and
-// rows i = 16 w.. of dq; the products within the chunk are formed with j along
-// the rows, which leaves G L in the registers as the A operand of dv and the
-// sum of E L as that of dk.  States enter with two bf16 terms where a value
-// that stays in fp32 depends on them (dl) and with one for dv.
+// added in order).  Eight warps in two sides.  Warps 0 to 3 take dq and dk
+// through the states, 32 rows x half of the K columns each (a state's operand
+// then serves two products, and the shared-memory pipe is what this kernel loads
+// most), then the gate; warps 4 to 7 dv and everything within the chunk, 16 rows
+// j each, and the fetching of the next head block.  G and the sum of E L wait in
+// shared memory, in the order of the accumulators' lanes.  The products within
+// the chunk are formed with j along the rows, which leaves G L
+// in the registers as the A operand of dv.  Between different 16-token blocks L is a product of
+// a row's and a column's factor, as in the forward pass.  States enter with
+// three bf16 terms where a value that stays in fp32 depends on them (dl) and
+// with one for dv.
 #pragma once
 #include "m2rnn_scan.cuh"
 
@@ -38,44 +45,45 @@ struct BwdSmem {
   static constexpr int P = Terms<F32>::in, PS = Terms<F32>::state, K = 8 * KT, HB = kCols / V;
   static constexpr int key = P * kChunk * (K + 8) * 2, val = P * kChunk * kVLd * 2;
   static constexpr int state = PS * kCols * K * 2;
+  static constexpr int tri = 18 * 512;  // G, or the sum of E L: see tri_at
+  // D without its diagonal: column sums by row block (from column 16 w on), row
+  // sums; the diagonal
+  static constexpr int cols = 160 * HB, sums = (cols + 2 * HB * kChunk) * 4;
   static constexpr int q = 0, k = q + key, v = k + key, u = v + val, h = u + val;
   static constexpr int r = F32 ? h : h + state;  // fp32: R takes H's place
-  static constexpr int g = r + state;            // G, column tiles 2w.. of row block w only
-  static constexpr int arrays = g + 20 * 512;
-  // loc, locj, dts, Pin, Uin, Urow: [HB][64]; Pcol: [4][HB][64]; dw_r: [64]; <R,H>: [4]
-  static constexpr int floats = 10 * HB * kChunk + kCols + 4;
-  static constexpr int bytes = arrays + floats * 4;
+  static constexpr int KH = KT >= 4 ? 2 : 1;     // parts that the K columns are cut into
+  static constexpr int g = r + state, f = g + tri;
+  static constexpr int gate = f + (F32 ? 0 : tri);  // fp32 keeps the sum in registers
+  static constexpr int through = gate + HB * 192 * 4;       // Pin, Uin: [HB][64]
+  static constexpr int rh = through + 2 * HB * kChunk * 4;  // shares of <R, H>
+  static constexpr int chunk_sums = rh + 32 * 4;
+  static constexpr int bytes = chunk_sums + sums;
 };
 
-// First G tile of row block rt (rt has 8 - 2 rt column tiles).
-__device__ __forceinline__ int g_tile(int rt) { return rt * (9 - rt); }
+// Where row block rt keeps column tile nt (2 rt on) of a j by i matrix, in floats: 4 per lane,
+// of the first tile only the upper 8 rows' 2 (below, i < j).
+__device__ __forceinline__ int tri_at(int rt, int nt) {
+  const int first = rt * (960 - 128 * (rt - 1));  // sum of 64 + 128 (7 - 2 r) over r < rt
+  return nt == 2 * rt ? first : first + 64 + 128 * (nt - 2 * rt - 1);
+}
+
+__device__ __forceinline__ float4 tri_load(const float* m, int rt, int nt) {
+  const int lane = threadIdx.x & 31;
+  if (nt != 2 * rt) return *reinterpret_cast<const float4*>(m + tri_at(rt, nt) + 4 * lane);
+  const float2 x = *reinterpret_cast<const float2*>(m + tri_at(rt, nt) + 2 * lane);
+  return make_float4(x.x, x.y, 0.f, 0.f);
+}
+__device__ __forceinline__ void tri_store(float* m, int rt, int nt, float4 x) {
+  const int lane = threadIdx.x & 31;
+  if (nt != 2 * rt)
+    *reinterpret_cast<float4*>(m + tri_at(rt, nt) + 4 * lane) = x;
+  else
+    *reinterpret_cast<float2*>(m + tri_at(rt, nt) + 2 * lane) = make_float2(x.x, x.y);
+}
 
 __device__ __forceinline__ float quad_sum(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 1);
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
-}
-
-// v of 16 values c[id] per lane, summed over the eight lanes that share lane
-// mod 4: leaves sums 2 j, 2 j + 1 with j = lane / 4 (bit-reversed into halves,
-// quarters, eighths as below) in c[0], c[1]; returns that j.
-__device__ __forceinline__ int column_sums(float (&c)[16], int lane) {
-  const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float send = b4 ? c[k] : c[k + 8], keep = b4 ? c[k + 8] : c[k];
-    c[k] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float send = b3 ? c[k] : c[k + 4], keep = b3 ? c[k + 4] : c[k];
-    c[k] = keep + __shfl_xor_sync(0xffffffffu, send, 8);
-  }
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float send = b2 ? c[k] : c[k + 2], keep = b2 ? c[k + 2] : c[k];
-    c[k] = keep + __shfl_xor_sync(0xffffffffu, send, 4);
-  }
-  return (b4 ? 4 : 0) + (b3 ? 2 : 0) + (b2 ? 1 : 0);
 }
 
 // Two neighbouring values of an output in its element type.
@@ -88,28 +96,30 @@ __device__ __forceinline__ void store2(typename Elem<F32>::T* dst, float a, floa
 }
 
 template <bool F32, int KT, int V>
-__global__ void __launch_bounds__(kThreads, F32 || KT == 16 ? 1 : 2) bwd_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_kernel(const ScanParams p) {
   using E = typename Elem<F32>::T;
   using S = BwdSmem<F32, KT, V>;
-  constexpr int P = S::P, PS = S::PS, PW = Terms<F32>::prob, K = S::K, HB = S::HB, NT = V / 8;
+  constexpr int P = S::P, PS = S::PS, PO = Terms<F32>::out, K = S::K, HB = S::HB, NT = V / 8;
   constexpr int ld = K + 8;
-  constexpr int PR = F32 ? PS : 1;  // terms of R in dv
   extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t base = ptx::smem_addr(smem);
   const uint32_t qs = base + S::q, ks = base + S::k, vs = base + S::v, us = base + S::u,
                  hs = base + S::h, rs = base + S::r;
-  float4* gs = reinterpret_cast<float4*>(smem + S::g);
-  float* loc = reinterpret_cast<float*>(smem + S::arrays);
-  float* locj = loc + HB * kChunk;
-  float* dts = locj + HB * kChunk;
-  float* Pin = dts + HB * kChunk;
+  float* gs = reinterpret_cast<float*>(smem + S::g);
+  float* fs = reinterpret_cast<float*>(smem + S::f);
+  const float* gate = reinterpret_cast<const float*>(smem + S::gate);
+  float* Pin = reinterpret_cast<float*>(smem + S::through);
   float* Uin = Pin + HB * kChunk;
-  float* Urow = Uin + HB * kChunk;
-  float* Pcol = Urow + HB * kChunk;  // [4][HB][64]
-  float* wsum = Pcol + 4 * HB * kChunk;
-  float* rh = wsum + kCols;
+  float* rh = reinterpret_cast<float*>(smem + S::rh);
+  float* Pcol = reinterpret_cast<float*>(smem + S::chunk_sums);  // see col_at
+  float* Urow = Pcol + S::cols;                                  // [HB][64]
+  float* Ddiag = Urow + HB * kChunk;                             // [HB][64]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c2 = (lane & 3) * 2;
-  const int rt = warp;
+  const int rt = row_block(warp & 3);                  // its 16 rows (the chunk's side)
+  const bool sside = warp < 4;                         // the states' side
+  const int tid = threadIdx.x & (kThreads - 1);        // within the side
+  // column i of row block r's sums for head h (columns 16 r and on)
+  auto col_at = [&](int r, int h, int i) { return HB * (r * 64 - 8 * r * (r - 1)) + h * (64 - 16 * r) + i - 16 * r; };
   const int c = blockIdx.x % p.nc;
   const int rest = blockIdx.x / p.nc, share = rest % p.hsplit;
   const int group = (rest / p.hsplit) % p.Nq, b = rest / p.hsplit / p.Nq;
@@ -118,43 +128,337 @@ __global__ void __launch_bounds__(kThreads, F32 || KT == 16 ? 1 : 2) bwd_kernel(
   const int hb0 = share * per, hb1 = min(p.nhb, hb0 + per);
   const E* q = static_cast<const E*>(p.q) + b * p.qb + t0 * p.qt + static_cast<size_t>(group) * K;
   const E* k = static_cast<const E*>(p.k) + b * p.kb + t0 * p.kt + static_cast<size_t>(group) * K;
-  load_tile<F32>(qs, q, p.qt, rows, K, K, ld, p.status, p.T - t0);
-  load_tile<F32>(ks, k, p.kt, rows, K, K, ld, p.status, p.T - t0);
-  ptx::cp_async_commit();
+  if (sside) {
+    load_tile<F32, K>(tid, qs, q, p.qt, rows, K, p.status, p.T - t0);
+    load_tile<F32, K>(tid, ks, k, p.kt, rows, K, p.status, p.T - t0);
+    ptx::cp_async_commit();
+  }
 
-  const size_t sd_extent = static_cast<size_t>(p.B) * p.N * p.nc * kChunk;
-  const size_t st_extent = state_at(p, PS, p.B, 0, 0);
+  const size_t st_extent = static_cast<size_t>(p.B) * p.Nq * p.nhb * p.nc * kCols * K;
   const size_t tok_extent = static_cast<size_t>(p.B) * p.T * p.N;  // tokens x heads
   const long long ut = static_cast<long long>(p.N) * V;
-  auto fetch_state = [&](uint32_t dst, const __nv_bfloat16* src, int hb) {
-    const size_t at = state_at(p, PS, b, group * p.nhb + hb, c);
-    if (in_range(p.status, at, PS * kCols * K, st_extent, CHK_SCAN_WS))
-      load_linear(dst, src + at, PS * kCols * K * 2);
-    ptx::cp_async_commit();
+  const int hseg = c / p.cps, rseg = (p.nc - 1 - c) / p.cps;
+  auto ref_h = [&](const Place& w) { return state_ref(p, p.Hl, p.Hseg, p.cdec, w, c, hseg); };
+  auto ref_r = [&](const Place& w) { return state_ref(p, p.Rl, p.Rseg, p.rdec, w, c, rseg); };
+  // `threads` threads bring a state's tile, two rows each in flight.
+  auto fetch_state = [&](int thread, int threads, uint32_t dst, const float* base_of, const StateRef& r,
+                         int n) {
+    constexpr int U = 2;
+    const int step = threads * 8;
+#pragma unroll 1
+    for (int e0 = thread * 8; e0 < n; e0 += U * step) {
+      StateRow x[U];
+      bool on[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int e = e0 + u * step;
+        on[u] = e < n && in_range(p.status, (r.own - base_of) + e, 8, st_extent, CHK_SCAN_WS);
+        if (on[u]) x[u] = state_load<K, V>(p, r, e);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (on[u]) {
+          float2 z[4];
+          state_sum(x[u], z);
+          put_state_row<PS, K>(dst, e0 + u * step, z);
+        }
+    }
   };
-  auto fetch = [&](int hb) {
-    const Place w = place_of(p, b, group * p.nhb + hb);
+  auto fetch_h = [&](int hb, int thread, int threads) {
+    const Place w = place_in(p, HB, b, group, hb);
+    fetch_state(thread, threads, hs, p.Hl, ref_h(w), w.heads * V * K);
+  };
+  auto fetch_rest = [&](int hb) {
+    const Place w = place_in(p, HB, b, group, hb);
     const E* v = static_cast<const E*>(p.v) + b * p.vb + t0 * p.vt + static_cast<size_t>(w.head0) * V;
     const E* u = static_cast<const E*>(p.dy) + (static_cast<size_t>(b) * p.T + t0) * ut +
                  static_cast<size_t>(w.head0) * V;
-    load_tile<F32>(vs, v, p.vt, rows, w.heads * V, kCols, kVLd, p.status, p.T - t0);
-    load_tile<F32>(us, u, ut, rows, w.heads * V, kCols, kVLd, p.status, p.T - t0);
-    fetch_state(hs, p.Hs, hb);
-    if (!F32) fetch_state(rs, p.Rs, hb);
-    for (int e = threadIdx.x; e < w.heads * kChunk; e += kThreads) {
-      const size_t at = (static_cast<size_t>(b) * p.N + w.head0 + e / kChunk) * p.nc * kChunk + t0 + e % kChunk;
-      float2 s = make_float2(0.f, 0.f);
-      if (in_range(p.status, at, 1, sd_extent, CHK_SCAN_WS)) s = p.sd[at];
-      loc[e] = s.x;
-      locj[e] = F32 ? s.x : s.x - log2f(s.y);  // dt = 0: +inf, a weight of 0
-      dts[e] = s.y;
+    load_tile<F32, kCols>(tid, vs, v, p.vt, rows, w.heads * V, p.status, p.T - t0);
+    load_tile<F32, kCols>(tid, us, u, ut, rows, w.heads * V, p.status, p.T - t0);
+    load_gate(tid, base + S::gate, p, w, c);
+    ptx::cp_async_commit();
+    if (!F32) fetch_state(tid, kThreads, rs, p.Rl, ref_r(w), w.heads * V * K);
+  };
+  // fp32: R in H's place, and <R, H> with H from memory, in shares of 256
+  // elements (a warp's pass).
+  auto fetch_r_late = [&](int hb) {
+    const Place w = place_in(p, HB, b, group, hb);
+    const StateRef fh = ref_h(w), fr = ref_r(w);
+#pragma unroll 1
+    for (int e = tid * 8; e < w.heads * V * K; e += kThreads * 8) {
+      // (a warp's 256 elements together: its lanes sum below)
+      if (!in_range(p.status, (fh.own - p.Hl) + e / 256 * 256, 256, st_extent, CHK_SCAN_WS)) continue;
+      const StateRow xr = state_load<K, V>(p, fh, e), yr = state_load<K, V>(p, fr, e);
+      float2 x[4], y[4];
+      state_sum(xr, x);
+      state_sum(yr, y);
+      put_state_row<PS, K>(rs, e, y);
+      const float2 d = fma2(x[0], y[0], fma2(x[1], y[1], fma2(x[2], y[2], mul2(x[3], y[3]))));
+      float s = d.x + d.y;
+#pragma unroll
+      for (int m = 16; m >= 1; m /= 2) s += __shfl_xor_sync(0xffffffffu, s, m);
+      if (lane == 0) rh[e / 256] = s;
     }
   };
-  fetch(hb0);
-  cp_async_wait<F32 ? 1 : 2>();
+  if (sside) {
+    for (int e = tid; e < 2 * HB * kChunk; e += kThreads) Pin[e] = 0.f;  // and Uin
+    fetch_h(hb0, tid, kThreads);
+    cp_async_wait<0>();
+  } else {
+    fetch_rest(hb0);
+  }
   __syncthreads();
 
+  const E* w_r = static_cast<const E*>(p.w_r);
+  float* part = p.part + (static_cast<size_t>(b) * p.nc + c) * p.N * (2 + V);
+  const size_t part_extent = static_cast<size_t>(p.N) * (2 + V);
+  if (sside) {
+    constexpr int KH = S::KH, NK = KT / KH;  // column tiles of a warp
+    const int row0 = 32 * (warp & 1), n0 = NK * (warp >> 1);
+    const bool works = (warp >> 1) < KH;     // K = 16 has one part only
+    float dq[2][NK][4], dk[2][NK][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int nt = 0; nt < NK; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dq[m][nt][i] = dk[m][nt][i] = 0.f;
+    // Through a state: out += scale_row (A state^T), and the rows' products with
+    // `with`'s rows (q or k), for one head; scale[m]: of rows 16 m + g, + 8.
+    auto through = [&](uint32_t tile, uint32_t state, uint32_t with, int h, const float2 (&scale)[2],
+                       float (&out)[2][NK][4], float* sums) {
+      uint32_t a[2][V / 16][P][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int vv = 0; vv < V / 16; ++vv)
+          load_a<P>(a[m][vv], tile, kVLd, row0 + 16 * m, h * V + 16 * vv);
+      float d[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+      for (int nt = 0; nt < NK; nt += 2) {
+        uint32_t bb[V / 16][2][PS][2];
+#pragma unroll
+        for (int vv = 0; vv < V / 16; ++vv)
+          state_bt2<PS>(bb[vv][0], bb[vv][1], state, K, h * NT + 2 * vv, n0 + nt);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+          for (int vv = 0; vv < V / 16; ++vv) mma_terms_n<P, PS, 2>(x, a[m][vv], bb[vv]);
+          uint32_t y[P][4];
+          load_a<P>(y, with, ld, row0 + 16 * m, 8 * (n0 + nt));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {  // (row g, tile nt), (g + 8, nt), (g, nt + 1), (g + 8, nt + 1)
+            uint32_t t[P];
+#pragma unroll
+            for (int s = 0; s < P; ++s) t[s] = y[s][r];
+            const float2 z = pair(x[r >> 1], r & 1), f = join<P>(t);
+            float(&o)[4] = out[m][nt + (r >> 1)];
+            set_pair(o, r & 1, fma2(both((r & 1) ? scale[m].y : scale[m].x), z, pair(o, r & 1)));
+            d[m][r & 1] = fmaf(f.x, z.x, fmaf(f.y, z.y, d[m][r & 1]));
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const float y0 = quad_sum(d[m][0]) * scale[m].x, y1 = quad_sum(d[m][1]) * scale[m].y;
+        float* to = sums + h * kChunk + row0 + 16 * m + g;
+        if ((lane & 3) == 0) {  // at most two shares onto 0: their order does not matter
+          atomicAdd(to, y0);
+          atomicAdd(to + 8, y1);
+        }
+      }
+    };
+    for (int hb = hb0; hb < hb1; ++hb) {
+      const Place w = place_in(p, HB, b, group, hb);
+      __syncthreads();  // the head block is there
+      if (hb + 1 < hb1) {
+        const Place next = place_in(p, HB, b, group, hb + 1);
+        state_prefetch(tid, ref_h(next), next.heads * V * K);
+      }
+      // the gate of head `warp`: 2^S(start,end), and its two tokens' parts
+      float decay = 0.f, alpha = 0.f, dt[2], sg[2], ratio[2];
+      if (warp < w.heads) {
+        const int n = w.head0 + warp;
+        const float* lo = gate + warp * 192;
+        decay = ex2((lo[15] + lo[31]) + (lo[47] + lo[63]));
+        const E* a = static_cast<const E*>(p.a) + b * p.ab + n;
+        alpha = to_f32(static_cast<const E*>(p.alpha)[n]);
+        const float beta = to_f32(static_cast<const E*>(p.beta)[n]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = -INFINITY;
+          if (2 * lane + e < rows && in_range(p.status, t0 + 2 * lane + e, 1, p.T, CHK_SCAN_IN))
+            x = to_f32(a[(t0 + 2 * lane + e) * p.at]) + beta;
+          dt[e] = gate_softplus(x);
+          sg[e] = 1.f / (1.f + expf(-x));
+          // sigmoid / softplus -> 1 as both vanish; a token with dt = 0 has no part of U
+          ratio[e] = dt[e] > 0.f ? sg[e] / dt[e] : 1.f;
+        }
+      }
+      if (works) {
+#pragma unroll 1
+        for (int h = 0; h < w.heads; ++h) {  // dq through H: 2^S(start,i)
+          const float* lo = gate + h * 192;
+          float2 sc[2];
+          float off = row0 ? lo[15] + lo[31] : 0.f;
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            sc[m] = make_float2(ex2(off + lo[row0 + 16 * m + g]), ex2(off + lo[row0 + 16 * m + g + 8]));
+            off += lo[row0 + 15];
+          }
+          through(us, hs, qs, h, sc, dq, Pin);
+        }
+      }
+      if constexpr (F32) {  // R in H's place
+        __syncthreads();
+        __syncthreads();
+      } else if (16 * warp < w.heads * V) {  // <R, H> of the warp's 16 columns: the diagonal of H^T R
+        float z[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int kk = 0; kk < KT / 2; ++kk) {
+          uint32_t a[PS][4], bb[2][PS][2];
+          const int m = lane >> 3;
+          const uint32_t at = hs + (((2 * warp + (m & 1)) * KT + 2 * kk + (m >> 1)) * 64 + (lane & 7) * 8) * 2;
+#pragma unroll
+          for (int s = 0; s < PS; ++s) ldsm4(a[s], at + s * kCols * K * 2);
+          state_b2<PS>(bb[0], bb[1], rs, K, 2 * warp, kk);
+          mma_terms_n<PS, PS, 2>(z, a, bb);
+        }
+        float s = 0.f;
+        if ((lane & 3) == (g >> 1)) s = (g & 1) ? z[0][1] + z[1][3] : z[0][0] + z[1][2];
+#pragma unroll
+        for (int m = 16; m >= 1; m /= 2) s += __shfl_xor_sync(0xffffffffu, s, m);
+        if (lane == 0) rh[warp] = s;
+      }
+      if (!F32) bar_arrive(2 * kThreads);  // done with H
+      if (works) {
+#pragma unroll 1
+        for (int h = 0; h < w.heads; ++h) {  // dk through R: 2^S(j,end) dt_j
+          const float* lo = gate + h * 192;
+          float2 sc[2];
+          float off = row0 ? 0.f : lo[47] + lo[63];
+#pragma unroll
+          for (int m = 1; m >= 0; --m) {
+            const float f = ex2(off);
+            sc[m] = make_float2(lo[128 + row0 + 16 * m + g] * f, lo[128 + row0 + 16 * m + g + 8] * f);
+            off += lo[row0 + 31];
+          }
+          through(vs, rs, ks, h, sc, dk, Uin);
+        }
+      }
+      __syncthreads();  // done with it; the others' sums are there
+      if (F32 && hb + 1 < hb1) fetch_h(hb + 1, tid, kThreads);
+      if (warp < w.heads) {  // the gate: one warp per head, two tokens per lane
+        const int h = warp, n = w.head0 + h, t = 2 * lane, blk = lane >> 3;
+        float2& us2 = *reinterpret_cast<float2*>(Uin + h * kChunk + t);
+        float2& ps2 = *reinterpret_cast<float2*>(Pin + h * kChunk + t);
+        const float2 ui = us2, dd = *reinterpret_cast<const float2*>(Ddiag + h * kChunk + t);
+        float2 pi = ps2;
+        us2 = ps2 = make_float2(0.f, 0.f);  // for the next head block
+        const float2 ur = *reinterpret_cast<const float2*>(Urow + h * kChunk + t);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          if (s <= blk) pi = add2(pi, *reinterpret_cast<const float2*>(Pcol + col_at(s, h, t)));
+        const float2 bw = make_float2(pi.x - ur.x, pi.y - ur.y);
+        float inc = ui.x + ui.y, suf = bw.x + bw.y;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const float up = __shfl_up_sync(0xffffffffu, inc, d);
+          const float dn = __shfl_down_sync(0xffffffffu, suf, d);
+          if (lane >= d) inc += up;
+          if (lane + d < 32) suf += dn;
+        }
+        float before = __shfl_up_sync(0xffffffffu, inc, 1), behind = __shfl_down_sync(0xffffffffu, suf, 1);
+        if (lane == 0) before = 0.f;
+        if (lane == 31) behind = 0.f;
+        constexpr int shares = F32 ? K * V / 256 : V / 16;
+        float all = 0.f;
+#pragma unroll
+        for (int e = 0; e < shares; ++e) all += rh[h * shares + e];
+        all *= decay;
+        const float dl[2] = {all + before + (behind + bw.y + bw.x), all + (before + ui.x) + (behind + bw.y)};
+        const float uu[2] = {ui.x + ur.x + dd.x, ui.y + ur.y + dd.y};
+        float sa = 0.f, sb = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (t + e >= rows) continue;
+          const float da = fmaf(ratio[e], uu[e], -alpha * sg[e] * dl[e]);
+          sa = fmaf(-dt[e], dl[e], sa);
+          sb += da;
+          const size_t at = (static_cast<size_t>(b) * p.T + t0 + t + e) * p.N + n;
+          if (in_range(p.status, at, 1, tok_extent, CHK_SCAN_OUT)) {
+            if constexpr (F32)
+              static_cast<float*>(p.da)[at] = da;
+            else
+              static_cast<__nv_bfloat16*>(p.da)[at] = __float2bfloat16_rn(da);
+          }
+        }
+#pragma unroll
+        for (int m = 16; m >= 1; m /= 2) {
+          sa += __shfl_xor_sync(0xffffffffu, sa, m);
+          sb += __shfl_xor_sync(0xffffffffu, sb, m);
+        }
+        if (lane == 0 && in_range(p.status, p.N + n, 1, part_extent, CHK_SCAN_PARAM)) {
+          part[n] = sa;
+          part[p.N + n] = sb;
+        }
+      }
+    }
+    __syncthreads();
+    __syncthreads();  // the sum of E L is there
+    if (!works) return;
+    // dq and dk within the chunk
+    const size_t qk_extent = static_cast<size_t>(p.B) * p.T * p.Nq * K;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int rb = (row0 >> 4) + m;  // 16-row block
+#pragma unroll 1
+      for (int jb = 0; jb <= rb; ++jb) {
+        uint32_t a[PO][4];
+        load_a_t<PO>(a, vs, kVLd, 16 * jb, 16 * rb);
+#pragma unroll
+        for (int nt = 0; nt < NK; nt += 2) {
+          uint32_t b0[P][2], b1[P][2];
+          load_b2_t<P>(b0, b1, ks, ld, 16 * jb, 8 * (n0 + nt));
+          mma_terms<PO, P>(dq[m][nt], a, b0);
+          mma_terms<PO, P>(dq[m][nt + 1], a, b1);
+        }
+      }
+#pragma unroll 1
+      for (int ib = rb; ib < 4; ++ib) {
+        uint32_t a[PO][4];
+        load_a<PO>(a, vs, kVLd, 16 * rb, 16 * ib);
+#pragma unroll
+        for (int nt = 0; nt < NK; nt += 2) {
+          uint32_t b0[P][2], b1[P][2];
+          load_b2_t<P>(b0, b1, qs, ld, 16 * ib, 8 * (n0 + nt));
+          mma_terms<PO, P>(dk[m][nt], a, b0);
+          mma_terms<PO, P>(dk[m][nt + 1], a, b1);
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NK; ++nt)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int r = row0 + 16 * m + g + 8 * hh;
+          const size_t at = ((static_cast<size_t>(b) * p.T + t0 + r) * p.Nq + group) * K + 8 * (n0 + nt) + c2;
+          if (r >= rows || !in_range(p.status, at, 2, qk_extent, CHK_SCAN_OUT)) continue;
+          if (p.hsplit > 1) {
+            float* dst = p.dqk + static_cast<size_t>(share) * 2 * qk_extent + at;
+            *reinterpret_cast<float2*>(dst) = pair(dq[m][nt], hh);
+            *reinterpret_cast<float2*>(dst + qk_extent) = pair(dk[m][nt], hh);
+          } else {
+            store2<F32>(static_cast<E*>(p.dq) + at, dq[m][nt][2 * hh], dq[m][nt][2 * hh + 1]);
+            store2<F32>(static_cast<E*>(p.dk) + at, dk[m][nt][2 * hh], dk[m][nt][2 * hh + 1]);
+          }
+        }
+    }
+    return;
+  }
+
   // G with j along the rows, for the tiles with i >= j
+#pragma unroll 1
   for (int ib = rt; ib < 4; ++ib) {
     float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -165,138 +469,61 @@ __global__ void __launch_bounds__(kThreads, F32 || KT == 16 ? 1 : 2) bwd_kernel(
       mma_terms<P, P>(x0, a, b0);
       mma_terms<P, P>(x1, a, b1);
     }
-    const int at = (g_tile(rt) + 2 * (ib - rt)) * 32 + lane;
-    gs[at] = make_float4(x0[0], x0[1], x0[2], x0[3]);
-    gs[at + 32] = make_float4(x1[0], x1[1], x1[2], x1[3]);
+    tri_store(gs, rt, 2 * ib, make_float4(x0[0], x0[1], x0[2], x0[3]));
+    tri_store(gs, rt, 2 * ib + 1, make_float4(x1[0], x1[1], x1[2], x1[3]));
+    if (!F32) {
+      tri_store(fs, rt, 2 * ib, make_float4(0.f, 0.f, 0.f, 0.f));
+      tri_store(fs, rt, 2 * ib + 1, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
   }
-
-  float dq[KT][4], dk[KT][4], dsum[8][4];
-#pragma unroll
-  for (int nt = 0; nt < KT; ++nt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dq[nt][i] = dk[nt][i] = 0.f;
+  float dsum[8][4];  // sum over heads of E L, rows j
 #pragma unroll
   for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) dsum[nt][i] = 0.f;
-
-  const E* w_r = static_cast<const E*>(p.w_r);
-  float* part = p.part + (static_cast<size_t>(b) * p.nc + c) * p.N * (2 + V);
   for (int hb = hb0; hb < hb1; ++hb) {
-    const Place w = place_of(p, b, group * p.nhb + hb);
+    const Place w = place_in(p, HB, b, group, hb);
     cp_async_wait<0>();
     __syncthreads();
-
-    // Through a state: out += scale_row (A state^T) for 16 rows, and the rows'
-    // products with `with`'s rows (q or k), for one head.
-    auto through = [&](uint32_t tile, uint32_t state, uint32_t with, int h, float s0, float s1,
-                       float (&out)[KT][4], float* sums) {
-      uint32_t a[V / 16][P][4];
-#pragma unroll
-      for (int vv = 0; vv < V / 16; ++vv) load_a<P>(a[vv], tile, kVLd, 16 * rt, h * V + 16 * vv);
-      float d0 = 0.f, d1 = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < KT / 2; ++kk) {
-        float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int vv = 0; vv < V / 16; ++vv) {
-          uint32_t b0[PS][2], b1[PS][2];
-          state_bt2<PS>(b0, b1, state, K, h * NT + 2 * vv, 2 * kk);
-          mma_terms<P, PS>(x0, a[vv], b0);
-          mma_terms<P, PS>(x1, a[vv], b1);
-        }
-        uint32_t m[P][4];
-        load_a<P>(m, with, ld, 16 * rt, 16 * kk);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {  // (row g, tile 2kk), (g + 8, 2kk), (g, 2kk + 1), (g + 8, 2kk + 1)
-          uint32_t t[P];
-#pragma unroll
-          for (int s = 0; s < P; ++s) t[s] = m[s][r];
-          const float2 y = join<P>(t);
-          const float sc = (r & 1) ? s1 : s0;
-          const float z0 = sc * (r < 2 ? x0 : x1)[2 * (r & 1)], z1 = sc * (r < 2 ? x0 : x1)[2 * (r & 1) + 1];
-          out[2 * kk + (r >> 1)][2 * (r & 1)] += z0;
-          out[2 * kk + (r >> 1)][2 * (r & 1) + 1] += z1;
-          float& d = (r & 1) ? d1 : d0;
-          d = fmaf(y.x, z0, fmaf(y.y, z1, d));
-        }
-      }
-      d0 = quad_sum(d0);
-      d1 = quad_sum(d1);
-      if ((lane & 3) == 0) {
-        sums[h * kChunk + 16 * rt + g] = d0;
-        sums[h * kChunk + 16 * rt + g + 8] = d1;
-      }
-    };
-
-#pragma unroll 1
-    for (int h = 0; h < w.heads; ++h) {  // dq through H
-      const float* lo = loc + h * kChunk;
-      float off = 0.f;
-      for (int i4 = 0; i4 < rt; ++i4) off += lo[16 * i4 + 15];
-      through(us, hs, qs, h, ex2(off + lo[16 * rt + g]), ex2(off + lo[16 * rt + g + 8]), dq, Pin);
-    }
-    if (F32) {
+    if (F32) {  // R in H's place
       __syncthreads();
-      fetch_state(rs, p.Rs, hb);
-      cp_async_wait<0>();
+      fetch_r_late(hb);
       __syncthreads();
     }
-    // <R, H> of the warp's 16 columns
-    {
-      const __nv_bfloat16* hg = p.Hs + state_at(p, PS, b, group * p.nhb + hb, c);
-      float s = 0.f;
-      if (16 * warp / V < w.heads) {
-        for (int e = lane * 8; e < 2 * KT * 64; e += 256) {
-          const int at = 2 * warp * KT * 64 + e;
-          float x[8], y[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.f;
-#pragma unroll
-          for (int t = PS - 1; t >= 0; --t) {
-            const uint4 rr = ptx::lds_u32x4(rs + (t * kCols * K + at) * 2);
-            uint4 hh;
-            if (F32)
-              hh = __ldg(reinterpret_cast<const uint4*>(hg + t * kCols * K + at));
-            else
-              hh = ptx::lds_u32x4(hs + (t * kCols * K + at) * 2);
-            const uint32_t r4[4] = {rr.x, rr.y, rr.z, rr.w}, h4[4] = {hh.x, hh.y, hh.z, hh.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              x[2 * j] += ptx::bf16x2_lo(r4[j]);
-              x[2 * j + 1] += ptx::bf16x2_hi(r4[j]);
-              y[2 * j] += ptx::bf16x2_lo(h4[j]);
-              y[2 * j + 1] += ptx::bf16x2_hi(h4[j]);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s = fmaf(x[j], y[j], s);
-        }
-      }
-#pragma unroll
-      for (int m = 16; m >= 1; m /= 2) s += __shfl_xor_sync(0xffffffffu, s, m);
-      if (lane == 0) rh[warp] = s;
+    if (hb + 1 < hb1) {
+      const Place next = place_in(p, HB, b, group, hb + 1);
+      state_prefetch(tid, ref_r(next), next.heads * V * K);
     }
-
+    // dw_r: the diagonal of u^T v over the chunk, 16 columns per warp
+    if (w_r != nullptr && 16 * rt < w.heads * V) {
+      float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        uint32_t a[P][4], b0[P][2], b1[P][2];
+        load_a_t<P>(a, us, kVLd, 16 * s, 16 * rt);
+        load_b2_t<P>(b0, b1, vs, kVLd, 16 * s, 16 * rt);
+        mma_terms<P, P>(x0, a, b0);
+        mma_terms<P, P>(x1, a, b1);
+      }
+      const size_t at = 2 * static_cast<size_t>(p.N) + static_cast<size_t>(w.head0) * V + 16 * rt + g;
+      if ((lane & 3) == (g >> 1) && in_range(p.status, at, 9, part_extent, CHK_SCAN_PARAM)) {
+        part[at] = (g & 1) ? x0[1] : x0[0];
+        part[at + 8] = (g & 1) ? x1[3] : x1[2];
+      }
+    }
 #pragma unroll 1
     for (int h = 0; h < w.heads; ++h) {
-      const float* lo = loc + h * kChunk;
-      const float* lj = locj + h * kChunk;
+      const float* lo = gate + h * 192;
       const int r0 = 16 * rt + g, r1 = r0 + 8;
-      const float dt0 = dts[h * kChunk + r0], dt1 = dts[h * kChunk + r1];
-      const float lj0 = lj[r0], lj1 = lj[r1];
-      float w0, w1;  // 2^S(j,end) dt_j
+      const float end0 = lo[128 + r0], end1 = lo[128 + r1];  // 2^S(j, block's end) dt_j
+      float w0, w1;                                          // 2^S(j, end) dt_j
       {
-        float later = 0.f;
-        for (int i4 = rt + 1; i4 < 4; ++i4) later += lo[16 * i4 + 15];
-        w0 = ex2(later + (lo[16 * rt + 15] - lj0));
-        w1 = ex2(later + (lo[16 * rt + 15] - lj1));
-        if (F32) {
-          w0 *= dt0;
-          w1 *= dt1;
-        }
+        float off = 0.f;
+        for (int i4 = rt + 1; i4 < 4; ++i4) off += lo[16 * i4 + 15];
+        off = ex2(off);
+        w0 = end0 * off;
+        w1 = end1 * off;
       }
-      through(vs, rs, ks, h, w0, w1, dk, Uin);
       // dv through R
       float dv[NT][4];
 #pragma unroll
@@ -309,76 +536,84 @@ __global__ void __launch_bounds__(kThreads, F32 || KT == 16 ? 1 : 2) bwd_kernel(
         load_a<P>(a, ks, ld, 16 * rt, 16 * kk);
 #pragma unroll
         for (int nt = 0; nt < NT; nt += 2) {
-          uint32_t b0[PR][2], b1[PR][2];
-          state_b2<PR>(b0, b1, rs, K, h * NT + nt, kk);
-          mma_terms<P, PR>(dv[nt], a, b0);
-          mma_terms<P, PR>(dv[nt + 1], a, b1);
+          uint32_t b0[PO][2], b1[PO][2];
+          state_b2<PO>(b0, b1, rs, K, h * NT + nt, kk);
+          mma_terms<P, PO>(dv[nt], a, b0);
+          mma_terms<P, PO>(dv[nt + 1], a, b1);
         }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        dv[nt][0] *= w0;
-        dv[nt][1] *= w0;
-        dv[nt][2] *= w1;
-        dv[nt][3] *= w1;
+        set_pair(dv[nt], 0, mul2(pair(dv[nt], 0), both(w0)));
+        set_pair(dv[nt], 1, mul2(pair(dv[nt], 1), both(w1)));
       }
       // within the chunk
       uint32_t va[V / 16][P][4];
 #pragma unroll
       for (int vv = 0; vv < V / 16; ++vv) load_a<P>(va[vv], vs, kVLd, 16 * rt, h * V + 16 * vv);
-      float col[16], ur0 = 0.f, ur1 = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) col[i] = 0.f;
-      float s0 = -lj0, s1 = -lj1;  // sum of l behind j, up to the start of i's block
+      float2 ur0 = make_float2(0.f, 0.f), ur1 = ur0;
+      float between = 0.f;  // sum of l over the blocks between j's and i's
 #pragma unroll
       for (int ib = 0; ib < 4; ++ib) {
         if (ib < rt) continue;
-        if (ib > rt) {
-          s0 += lo[16 * ib - 1];
-          s1 += lo[16 * ib - 1];
-        }
-        float e0[4] = {0.f, 0.f, 0.f, 0.f}, e1[4] = {0.f, 0.f, 0.f, 0.f};
+        if (ib > rt + 1) between += lo[16 * ib - 1];
+        float e[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int vv = 0; vv < V / 16; ++vv) {
           uint32_t b0[P][2], b1[P][2];
           load_b2<P>(b0, b1, us, kVLd, 16 * ib, h * V + 16 * vv);
-          mma_terms<P, P>(e0, va[vv], b0);
-          mma_terms<P, P>(e1, va[vv], b1);
+          mma_terms<P, P>(e[0], va[vv], b0);
+          mma_terms<P, P>(e[1], va[vv], b1);
         }
-        uint32_t a[PW][4];
+        uint32_t a[PO][4];
+        float2 dc[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int nt = 2 * ib + u;
           const float2 li = *reinterpret_cast<const float2*>(lo + 8 * nt + c2);
-          const float4 gg = gs[(g_tile(rt) + 2 * (ib - rt) + u) * 32 + lane];
-          float l0 = ex2(s0 + li.x), l1 = ex2(s0 + li.y);
-          float l2 = ex2(s1 + li.x), l3 = ex2(s1 + li.y);
+          const float4 g4 = tri_load(gs, rt, nt);
+          const float2 g0 = make_float2(g4.x, g4.y), g1 = make_float2(g4.z, g4.w);
+          float2 l0, l1;
+          if (ib == rt) {
+            const float lj0 = lo[r0], lj1 = lo[r1];
+            l0 = mul2(make_float2(ex2(li.x - lj0), ex2(li.y - lj0)), both(lo[64 + r0]));
+            l1 = mul2(make_float2(ex2(li.x - lj1), ex2(li.y - lj1)), both(lo[64 + r1]));
+            const int i = 8 * u + c2;  // i >= j
+            l0.x = i >= g ? l0.x : 0.f;
+            l0.y = i + 1 >= g ? l0.y : 0.f;
+            l1.x = i >= g + 8 ? l1.x : 0.f;
+            l1.y = i + 1 >= g + 8 ? l1.y : 0.f;
+          } else {
+            const float2 s = add2(li, both(between));
+            const float2 r = make_float2(ex2(s.x), ex2(s.y));
+            l0 = mul2(r, both(end0));
+            l1 = mul2(r, both(end1));
+          }
+          const float2 f0 = mul2(pair(e[u], 0), l0), f1 = mul2(pair(e[u], 1), l1);
           if (F32) {
-            l0 *= dt0; l1 *= dt0; l2 *= dt1; l3 *= dt1;
+            set_pair(dsum[nt], 0, add2(pair(dsum[nt], 0), f0));
+            set_pair(dsum[nt], 1, add2(pair(dsum[nt], 1), f1));
+          } else {
+            const float4 s = tri_load(fs, rt, nt);
+            const float2 s0 = add2(make_float2(s.x, s.y), f0), s1 = add2(make_float2(s.z, s.w), f1);
+            tri_store(fs, rt, nt, make_float4(s0.x, s0.y, s1.x, s1.y));
           }
-          if (ib == rt) {  // i >= j
-            const int i = 8 * u + c2;
-            l0 = i >= g ? l0 : 0.f;
-            l1 = i + 1 >= g ? l1 : 0.f;
-            l2 = i >= g + 8 ? l2 : 0.f;
-            l3 = i + 1 >= g + 8 ? l3 : 0.f;
+          float2 d0 = mul2(f0, g0), d1 = mul2(f1, g1);
+          if (ib == rt) {  // the diagonal apart: row g in the first tile, g + 8 in the second
+            float2& d = u ? d1 : d0;
+            if ((lane & 3) == (g >> 1)) {
+              Ddiag[h * kChunk + (u ? r1 : r0)] = (g & 1) ? d.y : d.x;
+              d = (g & 1) ? make_float2(d.x, 0.f) : make_float2(0.f, d.y);
+            }
           }
-          const float* e = u ? e1 : e0;
-          const float f0 = e[0] * l0, f1 = e[1] * l1, f2 = e[2] * l2, f3 = e[3] * l3;
-          dsum[nt][0] += f0;
-          dsum[nt][1] += f1;
-          dsum[nt][2] += f2;
-          dsum[nt][3] += f3;
-          const float d0 = f0 * gg.x, d1 = f1 * gg.y, d2 = f2 * gg.z, d3 = f3 * gg.w;
-          ur0 += d0 + d1;
-          ur1 += d2 + d3;
-          col[2 * nt] = d0 + d2;
-          col[2 * nt + 1] = d1 + d3;
-          uint32_t x0[PW], x1[PW];
-          split<PW>(gg.x * l0, gg.y * l1, x0);
-          split<PW>(gg.z * l2, gg.w * l3, x1);
+          ur0 = add2(ur0, d0);
+          ur1 = add2(ur1, d1);
+          dc[u] = add2(d0, d1);
+          uint32_t x0[PO], x1[PO];
+          split<PO>(mul2(g0, l0), x0);
+          split<PO>(mul2(g1, l1), x1);
 #pragma unroll
-          for (int s = 0; s < PW; ++s) {
+          for (int s = 0; s < PO; ++s) {
             a[s][2 * u] = x0[s];
             a[s][2 * u + 1] = x1[s];
           }
@@ -387,198 +622,77 @@ __global__ void __launch_bounds__(kThreads, F32 || KT == 16 ? 1 : 2) bwd_kernel(
         for (int nt = 0; nt < NT; nt += 2) {
           uint32_t b0[P][2], b1[P][2];
           load_b2_t<P>(b0, b1, us, kVLd, 16 * ib, h * V + 8 * nt);
-          mma_terms<PW, P>(dv[nt], a, b0);
-          mma_terms<PW, P>(dv[nt + 1], a, b1);
+          mma_terms<PO, P>(dv[nt], a, b0);
+          mma_terms<PO, P>(dv[nt + 1], a, b1);
+        }
+        {  // the column sums: 4 values over the 8 lanes that share lane mod 4
+          const bool b4 = lane & 16, b3 = lane & 8;
+          float2 s = b4 ? dc[1] : dc[0], o = b4 ? dc[0] : dc[1];
+          s.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
+          s.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+          float t = b3 ? s.y : s.x;
+          t += __shfl_xor_sync(0xffffffffu, b3 ? s.x : s.y, 8);
+          t += __shfl_xor_sync(0xffffffffu, t, 4);
+          if (!(lane & 4)) Pcol[col_at(rt, h, 16 * ib + (b4 ? 8 : 0) + c2 + (b3 ? 1 : 0))] = t;
         }
       }
-      ur0 = quad_sum(ur0);
-      ur1 = quad_sum(ur1);
+      const float u0 = quad_sum(ur0.x + ur0.y), u1 = quad_sum(ur1.x + ur1.y);
       if ((lane & 3) == 0) {
-        Urow[h * kChunk + r0] = ur0;
-        Urow[h * kChunk + r1] = ur1;
+        Urow[h * kChunk + r0] = u0;
+        Urow[h * kChunk + r1] = u1;
       }
-      const int j8 = column_sums(col, lane);  // this lane: column tile j8
-      *reinterpret_cast<float2*>(Pcol + (warp * HB + h) * kChunk + 8 * j8 + c2) = make_float2(col[0], col[1]);
+      // dv, with w_r (.) u
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; nt += 2) {
+        if (w_r != nullptr) {
+          uint32_t x[P][4];
+          load_a<P>(x, us, kVLd, 16 * rt, h * V + 8 * nt);
+          const E* wr = w_r + static_cast<size_t>(w.head0 + h) * V + 8 * nt + c2;
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int r = hh ? r1 : r0;
-          float y0 = dv[nt][2 * hh], y1 = dv[nt][2 * hh + 1];
-          if (w_r != nullptr) {
-            uint32_t x[P];
+          for (int r = 0; r < 4; ++r) {
+            uint32_t t[P];
 #pragma unroll
-            for (int s = 0; s < P; ++s)
-              x[s] = ptx::lds_u32(us + s * kChunk * kVLd * 2 + (r * kVLd + h * V + 8 * nt + c2) * 2);
-            const float2 uu = join<P>(x);
-            const E* wr = w_r + static_cast<size_t>(w.head0 + h) * V + 8 * nt + c2;
-            y0 = fmaf(to_f32(wr[0]), uu.x, y0);
-            y1 = fmaf(to_f32(wr[1]), uu.y, y1);
+            for (int s = 0; s < P; ++s) t[s] = x[s][r];
+            const float2 wv = make_float2(to_f32(wr[8 * (r >> 1)]), to_f32(wr[8 * (r >> 1) + 1]));
+            float(&o)[4] = dv[nt + (r >> 1)];
+            set_pair(o, r & 1, fma2(wv, join<P>(t), pair(o, r & 1)));
           }
-          const size_t at = ((static_cast<size_t>(b) * p.T + t0 + r) * p.N + w.head0 + h) * V + 8 * nt + c2;
-          if (r < rows && in_range(p.status, at, 2, tok_extent * V, CHK_SCAN_OUT))
-            store2<F32>(static_cast<E*>(p.dv) + at, y0, y1);
         }
-    }
-
-    // dw_r: sum over the chunk of u (.) v, half the rows per 64 threads
-    float ws = 0.f;
-    if (w_r != nullptr) {
-      const int col = threadIdx.x & 63, row0 = (threadIdx.x >> 6) * 32;
-      for (int r = row0; r < row0 + 32; ++r) {
-        const uint32_t at = (r * kVLd + col) * 2;
-        float x = 0.f, y = 0.f;
 #pragma unroll
-        for (int s = P - 1; s >= 0; --s) {
-          x += __uint_as_float(ptx::lds_u16(vs + s * kChunk * kVLd * 2 + at) << 16);
-          y += __uint_as_float(ptx::lds_u16(us + s * kChunk * kVLd * 2 + at) << 16);
+        for (int r = 0; r < 4; ++r) {
+          const int row = (r & 1) ? r1 : r0;
+          const size_t at = ((static_cast<size_t>(b) * p.T + t0 + row) * p.N + w.head0 + h) * V +
+                            8 * (nt + (r >> 1)) + c2;
+          if (row < rows && in_range(p.status, at, 2, tok_extent * V, CHK_SCAN_OUT))
+            store2<F32>(static_cast<E*>(p.dv) + at, dv[nt + (r >> 1)][2 * (r & 1)],
+                        dv[nt + (r >> 1)][2 * (r & 1) + 1]);
         }
-        ws = fmaf(x, y, ws);
       }
-      if (row0) wsum[col] = ws;
+    }
+    if (!F32) {
+      bar_wait(2 * kThreads);  // the other side is done with H
+      if (hb + 1 < hb1) fetch_h(hb + 1, tid, kThreads);
     }
     __syncthreads();
-    const size_t part_extent = static_cast<size_t>(p.N) * (2 + V);
-    if (w_r != nullptr && threadIdx.x < w.heads * V) {
-      const size_t at = 2 * static_cast<size_t>(p.N) + static_cast<size_t>(w.head0) * V + threadIdx.x;
-      if (in_range(p.status, at, 1, part_extent, CHK_SCAN_PARAM)) part[at] = ws + wsum[threadIdx.x];
-    }
-    if (warp < w.heads) {  // the gate: one warp per head, two tokens per lane
-      const int h = warp, n = w.head0 + h, t = 2 * lane;
-      const float* lo = loc + h * kChunk;
-      const float alpha = to_f32(static_cast<const E*>(p.alpha)[n]);
-      const float beta = to_f32(static_cast<const E*>(p.beta)[n]);
-      float x[2];
-      const E* a = static_cast<const E*>(p.a) + b * p.ab + n;
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        x[e] = t + e < rows && in_range(p.status, t0 + t + e, 1, p.T, CHK_SCAN_IN)
-                   ? to_f32(a[(t0 + t + e) * p.at]) + beta : -INFINITY;
-      float fwd[2], bwd[2], uu[2], ui[2];  // Uin; Pin + rows of D - columns of D
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int at = h * kChunk + t + e;
-        ui[e] = Uin[at];
-        uu[e] = ui[e] + Urow[at];
-        bwd[e] = Pin[at] - Urow[at];
-        float pc = 0.f;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) pc += Pcol[(s * HB + h) * kChunk + t + e];
-        bwd[e] += pc;
-        fwd[e] = ui[e];
-      }
-      float inc = fwd[0] + fwd[1], suf = bwd[0] + bwd[1];
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const float up = __shfl_up_sync(0xffffffffu, inc, d);
-        const float dn = __shfl_down_sync(0xffffffffu, suf, d);
-        if (lane >= d) inc += up;
-        if (lane + d < 32) suf += dn;
-      }
-      float before = __shfl_up_sync(0xffffffffu, inc, 1), behind = __shfl_down_sync(0xffffffffu, suf, 1);
-      if (lane == 0) before = 0.f;
-      if (lane == 31) behind = 0.f;
-      float rhs = 0.f;
-#pragma unroll
-      for (int s = 0; s < V / 16; ++s) rhs += rh[h * (V / 16) + s];
-      const float through_all = ex2((lo[15] + lo[31]) + (lo[47] + lo[63])) * rhs;
-      float dl[2];
-      dl[0] = through_all + before + (behind + bwd[1] + bwd[0]);
-      dl[1] = through_all + (before + fwd[0]) + (behind + bwd[1]);
-      float sa = 0.f, sb = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (t + e >= rows) continue;
-        const float dt = dts[h * kChunk + t + e];
-        const float sg = 1.f / (1.f + expf(-x[e]));
-        // sigmoid / softplus -> 1 as both vanish; a token with dt = 0 has no part of U
-        const float ratio = dt > 0.f ? sg / dt : 1.f;
-        const float da = fmaf(ratio, uu[e], -alpha * sg * dl[e]);
-        sa = fmaf(-dt, dl[e], sa);
-        sb += da;
-        const size_t at = (static_cast<size_t>(b) * p.T + t0 + t + e) * p.N + n;
-        if (in_range(p.status, at, 1, tok_extent, CHK_SCAN_OUT)) {
-          if constexpr (F32)
-            static_cast<float*>(p.da)[at] = da;
-          else
-            static_cast<__nv_bfloat16*>(p.da)[at] = __float2bfloat16_rn(da);
-        }
-      }
-#pragma unroll
-      for (int m = 16; m >= 1; m /= 2) {
-        sa += __shfl_xor_sync(0xffffffffu, sa, m);
-        sb += __shfl_xor_sync(0xffffffffu, sb, m);
-      }
-      if (lane == 0 && in_range(p.status, p.N + n, 1, part_extent, CHK_SCAN_PARAM)) {
-        part[n] = sa;
-        part[p.N + n] = sb;
-      }
-    }
-    __syncthreads();
-    if (hb + 1 < hb1) fetch(hb + 1);
+    if (hb + 1 < hb1) fetch_rest(hb + 1);
   }
-
-  // dq and dk within the chunk, from the sum over heads of E L
-  uint32_t x[8][2][PW];
+  // by way of the v tile's place, [j][i], to the other side
+  __syncthreads();
 #pragma unroll
   for (int nt = 0; nt < 8; ++nt) {
-    split<PW>(dsum[nt][0], dsum[nt][1], x[nt][0]);
-    split<PW>(dsum[nt][2], dsum[nt][3], x[nt][1]);
+    if (nt < 2 * rt) continue;
+    const float4 f4 = F32 ? make_float4(dsum[nt][0], dsum[nt][1], dsum[nt][2], dsum[nt][3]) : tri_load(fs, rt, nt);
+    uint32_t x0[PO], x1[PO];
+    split<PO>(make_float2(f4.x, f4.y), x0);
+    split<PO>(make_float2(f4.z, f4.w), x1);
 #pragma unroll
-    for (int s = 0; s < PW; ++s) {  // the v tile's place: [j][i]
+    for (int s = 0; s < PO; ++s) {
       const uint32_t at = vs + s * kChunk * kVLd * 2 + ((16 * rt + g) * kVLd + 8 * nt + c2) * 2;
-      ptx::sts_u32(at, x[nt][0][s]);
-      ptx::sts_u32(at + 8 * kVLd * 2, x[nt][1][s]);
+      ptx::sts_u32(at, x0[s]);
+      ptx::sts_u32(at + 8 * kVLd * 2, x1[s]);
     }
   }
   __syncthreads();
-#pragma unroll
-  for (int ib = 0; ib < 4; ++ib) {
-    if (ib < rt) continue;
-    uint32_t a[PW][4];
-#pragma unroll
-    for (int s = 0; s < PW; ++s) {
-      a[s][0] = x[2 * ib][0][s];
-      a[s][1] = x[2 * ib][1][s];
-      a[s][2] = x[2 * ib + 1][0][s];
-      a[s][3] = x[2 * ib + 1][1][s];
-    }
-#pragma unroll
-    for (int nt = 0; nt < KT; nt += 2) {
-      uint32_t b0[P][2], b1[P][2];
-      load_b2_t<P>(b0, b1, qs, ld, 16 * ib, 8 * nt);
-      mma_terms<PW, P>(dk[nt], a, b0);
-      mma_terms<PW, P>(dk[nt + 1], a, b1);
-    }
-  }
-  for (int jb = 0; jb <= rt; ++jb) {
-    uint32_t a[PW][4];
-    load_a_t<PW>(a, vs, kVLd, 16 * jb, 16 * rt);
-#pragma unroll
-    for (int nt = 0; nt < KT; nt += 2) {
-      uint32_t b0[P][2], b1[P][2];
-      load_b2_t<P>(b0, b1, ks, ld, 16 * jb, 8 * nt);
-      mma_terms<PW, P>(dq[nt], a, b0);
-      mma_terms<PW, P>(dq[nt + 1], a, b1);
-    }
-  }
-  const size_t qk_extent = static_cast<size_t>(p.B) * p.T * p.Nq * K;
-#pragma unroll
-  for (int nt = 0; nt < KT; ++nt)
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const int r = 16 * rt + g + 8 * hh;
-      const size_t at = ((static_cast<size_t>(b) * p.T + t0 + r) * p.Nq + group) * K + 8 * nt + c2;
-      if (r >= rows || !in_range(p.status, at, 2, qk_extent, CHK_SCAN_OUT)) continue;
-      if (p.hsplit > 1) {
-        float* dst = p.dqk + static_cast<size_t>(share) * 2 * qk_extent + at;
-        *reinterpret_cast<float2*>(dst) = make_float2(dq[nt][2 * hh], dq[nt][2 * hh + 1]);
-        *reinterpret_cast<float2*>(dst + qk_extent) = make_float2(dk[nt][2 * hh], dk[nt][2 * hh + 1]);
-      } else {
-        store2<F32>(static_cast<E*>(p.dq) + at, dq[nt][2 * hh], dq[nt][2 * hh + 1]);
-        store2<F32>(static_cast<E*>(p.dk) + at, dk[nt][2 * hh], dk[nt][2 * hh + 1]);
-      }
-    }
 }
 
 template <bool F32, int KT, int V>
@@ -589,7 +703,7 @@ cudaError_t launch_bwd_kt(const ScanParams& p, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(p.B) * p.Nq * p.hsplit * p.nc;
-  kern<<<static_cast<unsigned>(grid), kThreads, bytes, st>>>(p);
+  kern<<<static_cast<unsigned>(grid), 2 * kThreads, bytes, st>>>(p);
   return cudaGetLastError();
 }
 

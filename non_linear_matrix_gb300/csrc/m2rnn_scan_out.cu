@@ -7,69 +7,77 @@
 // formed once, a warp keeping its 16 rows in registers for all heads; then the
 // head blocks pass by, each bringing its v tile and state.  For each head
 // the weights are made in registers from q k^T, in the layout that the next
-// product takes as its A operand.  Warp w of CTA x works on rows 16 ((w + x)
-// mod 4)..: the row blocks differ in causal work, and a warp's place decides
-// which quarter of the SM it runs on.
+// product takes as its A operand.  Between different 16-token blocks the decay
+// is a product of a row's and a column's factor, both at most 1 in size for a
+// decaying gate (the column's made with the states); only the diagonal blocks
+// take a power of two per element.
 #include "m2rnn_scan.cuh"
 
 namespace m2rnn {
 namespace scan {
 namespace {
 
-template <bool F32>
-int out_smem_bytes(int K) {
-  constexpr int P = Terms<F32>::in, PS = Terms<F32>::state;
-  return 2 * P * kChunk * (K + 8) * 2 + P * kChunk * kVLd * 2 + PS * kCols * K * 2 +
-         (F32 ? 0 : kChunk * kVLd * 2) + 3 * 4 * kChunk * 4;
-}
+template <bool F32, int KT, int V>
+struct OutSmem {
+  static constexpr int P = Terms<F32>::in, PO = Terms<F32>::out, K = 8 * KT, HB = kCols / V;
+  static constexpr int key = P * kChunk * (K + 8) * 2, val = P * kChunk * kVLd * 2;
+  // the k tile, and after q k^T the rows of y on their way out
+  static constexpr int ky = key > kChunk * kVLd * 2 ? key : kChunk * kVLd * 2;
+  static constexpr int q = 0, k = key, v = k + ky, h = v + val, gate = h + PO * kCols * K * 2;
+  static constexpr int bytes = gate + HB * 192 * 4;
+};
 
-template <bool F32, int V>
-__global__ void __launch_bounds__(kThreads) out_kernel(const ScanParams p) {
+template <bool F32, int KT, int V>
+__global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_kernel(const ScanParams p) {
   using E = typename Elem<F32>::T;
-  constexpr int P = Terms<F32>::in, PS = Terms<F32>::state, PW = Terms<F32>::prob;
-  constexpr int HB = kCols / V, NT = V / 8;  // heads per block, column tiles per head
+  using S = OutSmem<F32, KT, V>;
+  constexpr int P = S::P, PO = S::PO, K = S::K, ld = K + 8;
+  constexpr int HB = S::HB, NT = V / 8;  // heads per block, column tiles per head
   extern __shared__ __align__(128) unsigned char smem[];
-  const int K = p.K, ld = K + 8;
-  const uint32_t qs = ptx::smem_addr(smem), ks_ = qs + P * kChunk * ld * 2,
-                 vs = ks_ + P * kChunk * ld * 2, hs = vs + P * kChunk * kVLd * 2,
-                 ys = hs + PS * kCols * K * 2;
-  // per head: sum of l from the 16-block's start to the token; the same less
-  // log2 dt (bf16) or as it is (fp32); dt
-  float* loc = reinterpret_cast<float*>(smem + (ys - qs) + (F32 ? 0 : kChunk * kVLd * 2));
-  float* locj = loc + HB * kChunk;
-  float* dts = locj + HB * kChunk;
+  const uint32_t base = ptx::smem_addr(smem), qs = base + S::q, ks = base + S::k, vs = base + S::v,
+                 hs = base + S::h, ys = ks;
+  const float* gate = reinterpret_cast<const float*>(smem + S::gate);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c2 = (lane & 3) * 2;
-  const int rt = (warp + blockIdx.x) & 3;  // the warp's 16 rows
+  const int rt = row_block(warp);  // the warp's 16 rows
   const int c = blockIdx.x % p.nc;
   const int rest = blockIdx.x / p.nc, part = rest % p.hsplit;
   const int group = (rest / p.hsplit) % p.Nq, b = rest / p.hsplit / p.Nq;
-  const int t0 = c * kChunk, rows = min(kChunk, p.T - t0);
+  const int t0 = c * kChunk, rows = min(kChunk, p.T - t0), seg = c / p.cps;
   const int per = (p.nhb + p.hsplit - 1) / p.hsplit;
   const int hb0 = part * per, hb1 = min(p.nhb, hb0 + per);
-  if (hb0 >= hb1) return;
   const E* q = static_cast<const E*>(p.q) + b * p.qb + t0 * p.qt + static_cast<size_t>(group) * K;
   const E* k = static_cast<const E*>(p.k) + b * p.kb + t0 * p.kt + static_cast<size_t>(group) * K;
-  load_tile<F32>(qs, q, p.qt, rows, K, K, ld, p.status, p.T - t0);
-  load_tile<F32>(ks_, k, p.kt, rows, K, K, ld, p.status, p.T - t0);
+  load_tile<F32, K>(threadIdx.x, qs, q, p.qt, rows, K, p.status, p.T - t0);
+  load_tile<F32, K>(threadIdx.x, ks, k, p.kt, rows, K, p.status, p.T - t0);
   ptx::cp_async_commit();
 
-  const size_t sd_extent = static_cast<size_t>(p.B) * p.N * p.nc * kChunk;
-  const size_t hs_extent = state_at(p, PS, p.B, 0, 0);
+  const size_t hl_extent = static_cast<size_t>(p.B) * p.Nq * p.nhb * p.nc * kCols * K;
   auto fetch = [&](int hb) {
-    const Place w = place_of(p, b, group * p.nhb + hb);
+    const Place w = place_in(p, HB, b, group, hb);
     const E* v = static_cast<const E*>(p.v) + b * p.vb + t0 * p.vt + static_cast<size_t>(w.head0) * V;
-    load_tile<F32>(vs, v, p.vt, rows, w.heads * V, kCols, kVLd, p.status, p.T - t0);
-    const size_t at = state_at(p, PS, b, group * p.nhb + hb, c);
-    if (in_range(p.status, at, PS * kCols * K, hs_extent, CHK_SCAN_WS))
-      load_linear(hs, p.Hs + at, PS * kCols * K * 2);
+    load_tile<F32, kCols>(threadIdx.x, vs, v, p.vt, rows, w.heads * V, p.status, p.T - t0);
+    load_gate(threadIdx.x, base + S::gate, p, w, c);
     ptx::cp_async_commit();
-    for (int e = threadIdx.x; e < w.heads * kChunk; e += kThreads) {
-      const size_t sat = (static_cast<size_t>(b) * p.N + w.head0 + e / kChunk) * p.nc * kChunk + t0 + e % kChunk;
-      float2 s = make_float2(0.f, 0.f);
-      if (in_range(p.status, sat, 1, sd_extent, CHK_SCAN_WS)) s = p.sd[sat];
-      loc[e] = s.x;
-      locj[e] = F32 ? s.x : s.x - log2f(s.y);  // dt = 0: +inf, a weight of 0
-      if (F32) dts[e] = s.y;
+    const StateRef r = state_ref(p, p.Hl, p.Hseg, p.cdec, w, c, seg);
+    constexpr int step = kThreads * 8, U = kCols * K >= 2 * step ? 2 : 1;  // rows in flight
+    const int n = w.heads * V * K;
+#pragma unroll 1
+    for (int e0 = threadIdx.x * 8; e0 < n; e0 += U * step) {
+      StateRow x[U];
+      bool on[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int e = e0 + u * step;
+        on[u] = e < n && in_range(p.status, (r.own - p.Hl) + e, 8, hl_extent, CHK_SCAN_WS);
+        if (on[u]) x[u] = state_load<K, V>(p, r, e);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (on[u]) {
+          float2 z[4];
+          state_sum(x[u], z);
+          put_state_row<PO, K>(hs, e0 + u * step, z);
+        }
     }
   };
   fetch(hb0);
@@ -81,14 +89,15 @@ __global__ void __launch_bounds__(kThreads) out_kernel(const ScanParams p) {
   for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) gm[nt][i] = 0.f;
-  for (int kk = 0; kk < K / 16; ++kk) {
+#pragma unroll
+  for (int kk = 0; kk < KT / 2; ++kk) {
     uint32_t a[P][4];
     load_a<P>(a, qs, ld, 16 * rt, 16 * kk);
 #pragma unroll
     for (int jb = 0; jb < 4; ++jb) {
       if (jb > rt) break;
       uint32_t b0[P][2], b1[P][2];
-      load_b2<P>(b0, b1, ks_, ld, 16 * jb, 16 * kk);
+      load_b2<P>(b0, b1, ks, ld, 16 * jb, 16 * kk);
       mma_terms<P, P>(gm[2 * jb], a, b0);
       mma_terms<P, P>(gm[2 * jb + 1], a, b1);
     }
@@ -98,139 +107,164 @@ __global__ void __launch_bounds__(kThreads) out_kernel(const ScanParams p) {
   E* y = static_cast<E*>(p.y);
   const size_t y_extent = static_cast<size_t>(p.B) * p.T * p.N * V;
   for (int hb = hb0; hb < hb1; ++hb) {
-    const Place w = place_of(p, b, group * p.nhb + hb);
+    const Place w = place_in(p, HB, b, group, hb);
     cp_async_wait<0>();
     __syncthreads();
+    if (hb + 1 < hb1) {
+      const Place next = place_in(p, HB, b, group, hb + 1);
+      state_prefetch(threadIdx.x, state_ref(p, p.Hl, p.Hseg, p.cdec, next, c, seg), next.heads * V * K);
+    }
     float acc[8][4];
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
     // from the state: q H
-    for (int kk = 0; kk < K / 16; ++kk) {
+#pragma unroll
+    for (int kk = 0; kk < KT / 2; ++kk) {
       uint32_t a[P][4];
       load_a<P>(a, qs, ld, 16 * rt, 16 * kk);
 #pragma unroll
       for (int v8 = 0; v8 < 8; v8 += 2) {
         if (v8 >= w.heads * NT) break;
-        uint32_t b0[PS][2], b1[PS][2];
-        state_b2<PS>(b0, b1, hs, K, v8, kk);
-        mma_terms<P, PS>(acc[v8], a, b0);
-        mma_terms<P, PS>(acc[v8 + 1], a, b1);
+        uint32_t b0[PO][2], b1[PO][2];
+        state_b2<PO>(b0, b1, hs, K, v8, kk);
+        mma_terms<P, PO>(acc[v8], a, b0);
+        mma_terms<P, PO>(acc[v8 + 1], a, b1);
       }
     }
 #pragma unroll
     for (int h = 0; h < HB; ++h) {
       if (h >= w.heads) break;
-      const float* lo = loc + h * kChunk;
-      const float* lj = locj + h * kChunk;
+      const float* lo = gate + h * 192;
+      const float* end = lo + 128;
       const float li0 = lo[16 * rt + g], li1 = lo[16 * rt + g + 8];
+      const float tot[3] = {lo[15], lo[31], lo[47]};
       {  // decay since the chunk's start
         float off = 0.f;
 #pragma unroll
-        for (int k4 = 0; k4 < 3; ++k4) off += k4 < rt ? lo[16 * k4 + 15] : 0.f;
-        const float e0 = ex2(off + li0), e1 = ex2(off + li1);
+        for (int k4 = 0; k4 < 3; ++k4) off += k4 < rt ? tot[k4] : 0.f;
+        const float2 e0 = both(ex2(off + li0)), e1 = both(ex2(off + li1));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          acc[h * NT + nt][0] *= e0;
-          acc[h * NT + nt][1] *= e0;
-          acc[h * NT + nt][2] *= e1;
-          acc[h * NT + nt][3] *= e1;
+        for (int nt = h * NT; nt < (h + 1) * NT; ++nt) {
+          set_pair(acc[nt], 0, mul2(pair(acc[nt], 0), e0));
+          set_pair(acc[nt], 1, mul2(pair(acc[nt], 1), e1));
         }
       }
-      // within the chunk; s0, s1: sum of l from the start of j's block to i
+      // within the chunk; s0, s1: sum of l from the end of j's block to i
       float s0 = li0, s1 = li1;
 #pragma unroll
       for (int jj = 3; jj >= 0; --jj) {
         if (jj > rt) continue;
-        if (jj < rt) {
-          s0 += lo[16 * jj + 15];
-          s1 += lo[16 * jj + 15];
-        }
-        uint32_t a[PW][4];
+        uint32_t a[PO][4];
+        if (jj == rt) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int nt = 2 * jj + u;
-          const float2 s = *reinterpret_cast<const float2*>(lj + 8 * nt + c2);
-          float m0 = gm[nt][0] * ex2(s0 - s.x), m1 = gm[nt][1] * ex2(s0 - s.y);
-          float m2 = gm[nt][2] * ex2(s1 - s.x), m3 = gm[nt][3] * ex2(s1 - s.y);
-          if (F32) {
-            const float2 d = *reinterpret_cast<const float2*>(dts + h * kChunk + 8 * nt + c2);
-            m0 *= d.x; m1 *= d.y; m2 *= d.x; m3 *= d.y;
-          }
-          if (jj == rt) {  // j <= i
-            const int j = 8 * u + c2;
-            m0 = j <= g ? m0 : 0.f;
-            m1 = j + 1 <= g ? m1 : 0.f;
-            m2 = j <= g + 8 ? m2 : 0.f;
-            m3 = j + 1 <= g + 8 ? m3 : 0.f;
-          }
-          uint32_t t0_[PW], t1_[PW];
-          split<PW>(m0, m1, t0_);
-          split<PW>(m2, m3, t1_);
+          for (int u = 0; u < 2; ++u) {
+            const int nt = 2 * jj + u;
+            const float2 lj = *reinterpret_cast<const float2*>(lo + 8 * nt + c2);
+            const float2 dt = *reinterpret_cast<const float2*>(lo + 64 + 8 * nt + c2);
+            float2 x0 = mul2(make_float2(ex2(li0 - lj.x), ex2(li0 - lj.y)), dt);
+            float2 x1 = mul2(make_float2(ex2(li1 - lj.x), ex2(li1 - lj.y)), dt);
+            const int j = 8 * u + c2;  // j <= i
+            x0.x = j <= g ? x0.x : 0.f;
+            x0.y = j < g ? x0.y : 0.f;
+            x1.x = j <= g + 8 ? x1.x : 0.f;
+            x1.y = j < g + 8 ? x1.y : 0.f;
+            uint32_t y0[PO], y1[PO];
+            split<PO>(mul2(pair(gm[nt], 0), x0), y0);
+            split<PO>(mul2(pair(gm[nt], 1), x1), y1);
 #pragma unroll
-          for (int s2 = 0; s2 < PW; ++s2) {
-            a[s2][2 * u] = t0_[s2];
-            a[s2][2 * u + 1] = t1_[s2];
+            for (int t = 0; t < PO; ++t) {
+              a[t][2 * u] = y0[t];
+              a[t][2 * u + 1] = y1[t];
+            }
+          }
+        } else {
+          if (jj + 1 < rt) {
+            s0 += tot[jj + 1 < 3 ? jj + 1 : 2];
+            s1 += tot[jj + 1 < 3 ? jj + 1 : 2];
+          }
+          const float2 r0 = both(ex2(s0)), r1 = both(ex2(s1));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int nt = 2 * jj + u;
+            const float2 e = *reinterpret_cast<const float2*>(end + 8 * nt + c2);
+            uint32_t y0[PO], y1[PO];
+            split<PO>(mul2(mul2(pair(gm[nt], 0), e), r0), y0);
+            split<PO>(mul2(mul2(pair(gm[nt], 1), e), r1), y1);
+#pragma unroll
+            for (int t = 0; t < PO; ++t) {
+              a[t][2 * u] = y0[t];
+              a[t][2 * u + 1] = y1[t];
+            }
           }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; nt += 2) {
           uint32_t b0[P][2], b1[P][2];
           load_b2_t<P>(b0, b1, vs, kVLd, 16 * jj, h * V + 8 * nt);
-          mma_terms<PW, P>(acc[h * NT + nt], a, b0);
-          mma_terms<PW, P>(acc[h * NT + nt + 1], a, b1);
+          mma_terms<PO, P>(acc[h * NT + nt], a, b0);
+          mma_terms<PO, P>(acc[h * NT + nt + 1], a, b1);
         }
       }
     }
     // + w_r (.) v, and out
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
+    for (int nt = 0; nt < 8; nt += 2) {
       if (nt >= w.heads * NT) break;
-      float2 wr = make_float2(0.f, 0.f);
       if (w_r != nullptr) {
+        uint32_t x[P][4];
+        load_a<P>(x, vs, kVLd, 16 * rt, 8 * nt);
         const E* src = w_r + static_cast<size_t>(w.head0) * V + 8 * nt + c2;
-        wr = make_float2(to_f32(src[0]), to_f32(src[1]));
-      }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 16 * rt + g + 8 * h;
-        uint32_t x[P];
+        for (int r = 0; r < 4; ++r) {
+          uint32_t t[P];
 #pragma unroll
-        for (int s = 0; s < P; ++s)
-          x[s] = ptx::lds_u32(vs + s * kChunk * kVLd * 2 + (r * kVLd + 8 * nt + c2) * 2);
-        const float2 v = join<P>(x);
-        const float y0 = fmaf(wr.x, v.x, acc[nt][2 * h]), y1 = fmaf(wr.y, v.y, acc[nt][2 * h + 1]);
-        if constexpr (F32) {
-          const size_t at = ((static_cast<size_t>(b) * p.T + t0 + r) * p.N + w.head0) * V + 8 * nt + c2;
-          if (r < rows && in_range(p.status, at, 2, y_extent, CHK_SCAN_OUT))
-            *reinterpret_cast<float2*>(y + at) = make_float2(y0, y1);
-        } else {
-          ptx::sts_u32(ys + (r * kVLd + 8 * nt + c2) * 2, ptx::pack_bf16x2(y0, y1));
+          for (int s = 0; s < P; ++s) t[s] = x[s][r];
+          const float2 wr = make_float2(to_f32(src[8 * (r >> 1)]), to_f32(src[8 * (r >> 1) + 1]));
+          set_pair(acc[nt + (r >> 1)], r & 1, fma2(wr, join<P>(t), pair(acc[nt + (r >> 1)], r & 1)));
         }
+      }
+      if constexpr (F32) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * rt + g + 8 * (r & 1);
+          const size_t at = ((static_cast<size_t>(b) * p.T + t0 + row) * p.N + w.head0) * V +
+                            8 * (nt + (r >> 1)) + c2;
+          if (row < rows && in_range(p.status, at, 2, y_extent, CHK_SCAN_OUT))
+            *reinterpret_cast<float2*>(y + at) = pair(acc[nt + (r >> 1)], r & 1);
+        }
+      } else {
+        uint32_t x[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float2 o = pair(acc[nt + (r >> 1)], r & 1);
+          x[r] = ptx::pack_bf16x2(o.x, o.y);
+        }
+        stsm4(piece_rc(ys, kVLd, 16 * rt, 8 * nt), x);
       }
     }
     if constexpr (!F32) {
       __syncwarp();  // the warp's own 16 rows, in 16-byte pieces
+      const int col = (lane & 7) * 8;
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        const int r = 16 * rt + it * 4 + (lane >> 3), col = (lane & 7) * 8;
-        if (r >= rows || col >= w.heads * V) continue;
-        const uint4 u = ptx::lds_u32x4(ys + (r * kVLd + col) * 2);
+        const int r = 16 * rt + it * 4 + (lane >> 3);
         const size_t at = ((static_cast<size_t>(b) * p.T + t0 + r) * p.N + w.head0) * V + col;
-        if (in_range(p.status, at, 8, y_extent, CHK_SCAN_OUT))
-          *reinterpret_cast<uint4*>(y + at) = u;
+        if (r < rows && col < w.heads * V && in_range(p.status, at, 8, y_extent, CHK_SCAN_OUT))
+          *reinterpret_cast<uint4*>(y + at) = ptx::lds_u32x4(ys + (r * kVLd + col) * 2);
       }
     }
-    __syncthreads();  // v, the state and the sums may be overwritten
+    __syncthreads();  // v, the state and the gate may be overwritten
     if (hb + 1 < hb1) fetch(hb + 1);
   }
 }
 
-template <bool F32, int V>
+template <bool F32, int KT, int V>
 cudaError_t run(const ScanParams& p, cudaStream_t st) {
-  const int smem = out_smem_bytes<F32>(p.K);
-  auto kern = out_kernel<F32, V>;
+  constexpr int smem = OutSmem<F32, KT, V>::bytes;
+  static_assert(smem <= 227 * 1024, "shared memory of one CTA");
+  auto kern = out_kernel<F32, KT, V>;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -240,12 +274,22 @@ cudaError_t run(const ScanParams& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <bool F32, int V>
+cudaError_t run_k(const ScanParams& p, cudaStream_t st) {
+  switch (p.K) {
+    case 16: return run<F32, 2, V>(p, st);
+    case 32: return run<F32, 4, V>(p, st);
+    case 64: return run<F32, 8, V>(p, st);
+    default: return run<F32, 16, V>(p, st);
+  }
+}
+
 }  // namespace
 }  // namespace scan
 
 cudaError_t launch_scan_out(const ScanParams& p, bool f32, cudaStream_t st) {
-  if (p.V == 16) return f32 ? scan::run<true, 16>(p, st) : scan::run<false, 16>(p, st);
-  return f32 ? scan::run<true, 32>(p, st) : scan::run<false, 32>(p, st);
+  if (p.V == 16) return f32 ? scan::run_k<true, 16>(p, st) : scan::run_k<false, 16>(p, st);
+  return f32 ? scan::run_k<true, 32>(p, st) : scan::run_k<false, 32>(p, st);
 }
 
 }  // namespace m2rnn

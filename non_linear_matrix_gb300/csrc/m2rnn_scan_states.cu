@@ -8,21 +8,17 @@
 //
 // A CTA walks along a segment of a sequence with the state of one head block
 // (64 value columns x K) in its accumulators, warp w the columns 16 w..; the
-// decayed values are the A operand (two bf16 terms, made in registers), the
-// keys the B operand.  The chain is sequential in chunks, so where there
-// are fewer (sequence, head block) pairs than the SMs take, a sequence is cut
-// into segments: a first launch computes each segment's contribution alone, a
-// small one joins them, and this kernel runs again from the joined states,
-// writing them.  The second reading of k and v costs 36 of the operator's 74
-// bytes per token and head (K = 64, V = 16) and replaces a chain that would
-// leave most SMs idle.
+// decayed values are the A operand (three bf16 terms, made in registers, so the
+// state is good to fp32), the keys the B operand.  Segments run at the same
+// time from zero states; join_kernel then carries the states from segment to
+// segment.
 #include "m2rnn_scan.cuh"
 
 namespace m2rnn {
 namespace scan {
 namespace {
 
-template <bool F32, int KT, bool REV, bool WRITE>
+template <bool F32, int KT, bool REV>
 __global__ void __launch_bounds__(kThreads) states_kernel(const ScanParams p) {
   using E = typename Elem<F32>::T;
   constexpr int P = Terms<F32>::in, PS = Terms<F32>::state, K = 8 * KT, kLd = K + 8;
@@ -31,12 +27,12 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const ScanParams p) {
   float(*weights)[kChunk] = reinterpret_cast<float(*)[kChunk]>(smem);
   const uint32_t key0 = ptx::smem_addr(smem) + 4 * kChunk * 4, val0 = key0 + 2 * kKey;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c2 = (lane & 3) * 2;
-  const int nseg = WRITE ? p.nseg : p.nseg - 1;
-  const int seg = blockIdx.x % nseg, gbx = blockIdx.x / nseg;
+  const int seg = blockIdx.x % p.nseg, gbx = blockIdx.x / p.nseg;
   const int gb = gbx % (p.Nq * p.nhb), b = gbx / (p.Nq * p.nhb);
   const Place w = place_of(p, b, gb);
   const int vh = 16 * warp / p.V;  // the warp's head within the block
   const bool on = vh < w.heads;
+  const bool leads = on && (16 * warp) % p.V == 0;  // writes what a head has once
   const int n = w.head0 + (on ? vh : 0);
   const int first = seg * p.cps, count = min(p.cps, p.nc - first);
   const E* key = static_cast<const E*>(REV ? p.q : p.k) + b * (REV ? p.qb : p.kb) +
@@ -46,33 +42,33 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const ScanParams p) {
                            (static_cast<size_t>(b) * p.T * p.N + w.head0) * p.V
                      : static_cast<const E*>(p.v) + b * p.vb + static_cast<size_t>(w.head0) * p.V;
   const long long val_t = REV ? static_cast<long long>(p.N) * p.V : p.vt;
-  const float alpha = to_f32(static_cast<const E*>(p.alpha)[n]);
   const float beta = to_f32(static_cast<const E*>(p.beta)[n]);
-  const size_t sd_extent = static_cast<size_t>(p.B) * p.N * p.nc * kChunk;
+  const float rate = -to_f32(static_cast<const E*>(p.alpha)[n]) * kLog2e;
+  const size_t head = static_cast<size_t>(b) * p.N + n;
+  const size_t gate_extent = static_cast<size_t>(p.B) * p.N * p.nc * 192;
 
   auto chunk_of = [&](int i) { return REV ? p.nc - 1 - (first + i) : first + i; };
   auto fetch = [&](int i) {  // tiles of the i-th chunk of the segment
     const int t0 = chunk_of(i) * kChunk, rows = min(kChunk, p.T - t0);
-    load_tile<F32>(key0 + (i & 1) * kKey, key + t0 * key_t, key_t, rows, K, K, kLd, p.status, p.T - t0);
-    load_tile<F32>(val0 + (i & 1) * kVal, val + t0 * val_t, val_t, rows, w.heads * p.V, kCols, kVLd,
-                   p.status, p.T - t0);
+    load_tile<F32, K>(threadIdx.x, key0 + (i & 1) * kKey, key + t0 * key_t, key_t, rows, K, p.status, p.T - t0);
+    load_tile<F32, kCols>(threadIdx.x, val0 + (i & 1) * kVal, val + t0 * val_t, val_t, rows, w.heads * p.V,
+                          p.status, p.T - t0);
     ptx::cp_async_commit();
   };
-  float ga[2];  // the lane's two tokens' gate inputs (forward)
-  float4 gs;    // the same tokens' (block sum, dt) pairs (reverse)
+  float2 ga;  // the lane's two tokens: gate inputs (forward) or block sums (reverse)
   auto fetch_gate = [&](int i) {
     const int c = chunk_of(i), t = c * kChunk + 2 * lane;
     if constexpr (REV) {
-      const size_t at = (static_cast<size_t>(b) * p.N + n) * p.nc * kChunk + t;
-      gs = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (in_range(p.status, at, 2, sd_extent, CHK_SCAN_WS))
-        gs = *reinterpret_cast<const float4*>(p.sd + at);
+      const size_t at = (head * p.nc + c) * 192 + 2 * lane;
+      ga = make_float2(0.f, 0.f);
+      if (in_range(p.status, at, 2, gate_extent, CHK_SCAN_WS))
+        ga = *reinterpret_cast<const float2*>(p.gate + at);
     } else {
       const E* a = static_cast<const E*>(p.a) + b * p.ab + n;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        ga[u] = t + u < p.T && in_range(p.status, t + u, 1, p.T, CHK_SCAN_IN)
-                    ? to_f32(a[(t + u) * p.at]) : -INFINITY;
+      ga = make_float2(-INFINITY, -INFINITY);
+      if (t < p.T && in_range(p.status, t, 1, p.T, CHK_SCAN_IN)) ga.x = to_f32(a[t * p.at]);
+      if (t + 1 < p.T && in_range(p.status, t + 1, 1, p.T, CHK_SCAN_IN))
+        ga.y = to_f32(a[(t + 1) * p.at]);
     }
   };
 
@@ -81,115 +77,98 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const ScanParams p) {
   // state: accumulator nt holds (column 16 warp + g [+8], key row 8 nt + c2, +1)
   float acc[KT][4];
   const float* init = REV ? p.dHT : p.H0;
-  const size_t st0 = (static_cast<size_t>(b) * p.N + n) * K * p.V;
-  const size_t st_extent = static_cast<size_t>(p.B) * p.N * K * p.V;
+  const size_t st0 = head * K * p.V, st_extent = static_cast<size_t>(p.B) * p.N * K * p.V;
   const int vcol = (16 * warp) % p.V + g;
-  const size_t seg_extent = static_cast<size_t>(p.B) * p.Nq * p.nhb * p.nseg * kCols * K;
-  auto seg_at = [&](int s) {
-    return ((static_cast<size_t>(b) * p.Nq * p.nhb + gb) * p.nseg + s) * kCols * K +
-           static_cast<size_t>(warp) * KT * 128 + lane;
-  };
 #pragma unroll
   for (int nt = 0; nt < KT; ++nt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       acc[nt][i] = 0.f;
-      if (!on) continue;
-      if (seg == 0) {
-        const size_t at = st0 + static_cast<size_t>(8 * nt + c2 + (i & 1)) * p.V + vcol + (i >> 1) * 8;
-        if (init != nullptr && in_range(p.status, at, 1, st_extent, CHK_SCAN_STATE))
-          acc[nt][i] = init[at];
-      } else if (WRITE) {
-        const size_t at = seg_at(seg - 1) + (nt * 4 + i) * 32;
-        if (in_range(p.status, at, 1, seg_extent, CHK_SCAN_WS)) acc[nt][i] = p.segst[at];
-      }
+      const size_t at = st0 + static_cast<size_t>(8 * nt + c2 + (i & 1)) * p.V + vcol + (i >> 1) * 8;
+      if (on && seg == 0 && init != nullptr && in_range(p.status, at, 1, st_extent, CHK_SCAN_STATE))
+        acc[nt][i] = init[at];
     }
+  // writes the accumulators as a tile's blocks, whole lines at a time
+  auto put = [&](float* base, size_t tiles, size_t tile) {
+#pragma unroll
+    for (int nt = 0; nt < KT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const size_t at = tile * kCols * K + ((2 * warp + h) * KT + nt) * 64 + 2 * lane;
+        if (in_range(p.status, at, 2, tiles * kCols * K, CHK_SCAN_WS))
+          *reinterpret_cast<float2*>(base + at) = pair(acc[nt], h);
+      }
+  };
 
+  const size_t pairs = static_cast<size_t>(p.B) * p.Nq * p.nhb;
   float total = 0.f;  // log2 decay of the segment so far
   for (int i = 0; i < count; ++i) {
     const int c = chunk_of(i);
     // The gate's sums.  Blocks of 16 tokens are 8 lanes; loc: from the block's
     // start up to the lane's tokens, rest: from behind them to its end.
-    float wt[2], chunk_sum;
-    {
-      float l0, l1, dt0 = 0.f, dt1 = 0.f, loc0, loc1;
-      if constexpr (REV) {
-        loc0 = gs.x;
-        loc1 = gs.z;
-      } else {
-        dt0 = gate_softplus(ga[0] + beta);
-        dt1 = gate_softplus(ga[1] + beta);
-        // below 2^-160 a decay is 0 in fp32: the bound keeps sums short
-        l0 = -alpha * kLog2e * dt0;
-        l1 = -alpha * kLog2e * dt1;
-        l0 = l0 < -160.f ? -160.f : l0;
-        l1 = l1 < -160.f ? -160.f : l1;
-        float inc = l0 + l1, suf = inc;
+    float2 loc, rest = make_float2(0.f, 0.f), dt = make_float2(0.f, 0.f), wt;
+    if constexpr (REV) {
+      loc = ga;
+    } else {
+      dt.x = gate_softplus(ga.x + beta);
+      dt.y = gate_softplus(ga.y + beta);
+      float2 l = make_float2(rate * dt.x, rate * dt.y);
+      // below 2^-160 a decay is 0 in fp32: the bound keeps sums short
+      l.x = l.x < -160.f ? -160.f : l.x;
+      l.y = l.y < -160.f ? -160.f : l.y;
+      float inc = l.x + l.y, suf = inc;
 #pragma unroll
-        for (int d = 1; d < 8; d *= 2) {
-          const float up = __shfl_up_sync(0xffffffffu, inc, d, 8);
-          const float dn = __shfl_down_sync(0xffffffffu, suf, d, 8);
-          if ((lane & 7) >= d) inc += up;
-          if ((lane & 7) + d < 8) suf += dn;
-        }
-        loc1 = inc;
-        const float before = __shfl_up_sync(0xffffffffu, inc, 1, 8);
-        loc0 = ((lane & 7) ? before : 0.f) + l0;
-        const float behind = __shfl_down_sync(0xffffffffu, suf, 1, 8);
-        wt[1] = (lane & 7) < 7 ? behind : 0.f;  // after the second token
-        wt[0] = wt[1] + l1;
+      for (int d = 1; d < 8; d *= 2) {
+        const float up = __shfl_up_sync(0xffffffffu, inc, d, 8);
+        const float dn = __shfl_down_sync(0xffffffffu, suf, d, 8);
+        if ((lane & 7) >= d) inc += up;
+        if ((lane & 7) + d < 8) suf += dn;
       }
-      float tot[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tot[k] = __shfl_sync(0xffffffffu, loc1, 8 * k + 7);
-      const int blk = lane >> 3;
-      float off = 0.f;
-      if constexpr (REV) {
-#pragma unroll
-        for (int k = 0; k < 3; ++k) off += k < blk ? tot[k] : 0.f;
-        wt[0] = ex2(off + loc0);
-        wt[1] = ex2(off + loc1);
-      } else {
-#pragma unroll
-        for (int k = 3; k > 0; --k) off += k > blk ? tot[k] : 0.f;
-        wt[0] = ex2(off + wt[0]) * dt0;
-        wt[1] = ex2(off + wt[1]) * dt1;
-        const size_t at = (static_cast<size_t>(b) * p.N + n) * p.nc * kChunk + c * kChunk + 2 * lane;
-        if (WRITE && on && (16 * warp) % p.V == 0 && in_range(p.status, at, 2, sd_extent, CHK_SCAN_WS))
-          *reinterpret_cast<float4*>(p.sd + at) = make_float4(loc0, dt0, loc1, dt1);
-      }
-      chunk_sum = (tot[0] + tot[1]) + (tot[2] + tot[3]);
-      weights[warp][2 * lane] = wt[0];
-      weights[warp][2 * lane + 1] = wt[1];
+      const float before = __shfl_up_sync(0xffffffffu, inc, 1, 8);
+      const float behind = __shfl_down_sync(0xffffffffu, suf, 1, 8);
+      loc.y = inc;
+      loc.x = ((lane & 7) ? before : 0.f) + l.x;
+      rest.y = (lane & 7) < 7 ? behind : 0.f;
+      rest.x = rest.y + l.y;
     }
+    float tot[4], off = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tot[k] = __shfl_sync(0xffffffffu, loc.y, 8 * k + 7);
+    const int blk = lane >> 3;
+    if constexpr (REV) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k) off += k < blk ? tot[k] : 0.f;
+      wt = make_float2(ex2(off + loc.x), ex2(off + loc.y));
+    } else {
+#pragma unroll
+      for (int k = 3; k > 0; --k) off += k > blk ? tot[k] : 0.f;
+      const float2 end = make_float2(ex2(rest.x) * dt.x, ex2(rest.y) * dt.y);
+      wt = make_float2(ex2(off + rest.x) * dt.x, ex2(off + rest.y) * dt.y);
+      const size_t at = (head * p.nc + c) * 192 + 2 * lane;
+      if (leads && in_range(p.status, at, 130, gate_extent, CHK_SCAN_WS)) {
+        *reinterpret_cast<float2*>(p.gate + at) = loc;
+        *reinterpret_cast<float2*>(p.gate + at + 64) = dt;
+        *reinterpret_cast<float2*>(p.gate + at + 128) = end;
+      }
+    }
+    const float chunk_sum = (tot[0] + tot[1]) + (tot[2] + tot[3]);
+    *reinterpret_cast<float2*>(&weights[warp][2 * lane]) = wt;
+    const size_t cat = head * p.nc + c;
+    if (leads && lane == 0 &&
+        in_range(p.status, cat, 1, static_cast<size_t>(p.B) * p.N * p.nc, CHK_SCAN_WS))
+      (REV ? p.rdec : p.cdec)[cat] = total;
     total += chunk_sum;
     if (i + 1 < count) fetch_gate(i + 1);
     cp_async_wait<0>();
     __syncthreads();  // tiles of chunk i are there; everyone is done with chunk i - 1
     if (i + 1 < count) fetch(i + 1);
     if (on) {
-      if (WRITE) {
-        __nv_bfloat16* dst = (REV ? p.Rs : p.Hs) + state_at(p, PS, b, gb, c);
-        const size_t extent = state_at(p, PS, p.B, 0, 0);
-#pragma unroll
-        for (int nt = 0; nt < KT; ++nt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t t[PS];
-            split<PS>(acc[nt][2 * h], acc[nt][2 * h + 1], t);
-#pragma unroll
-            for (int s = 0; s < PS; ++s) {
-              const size_t at = static_cast<size_t>(s) * kCols * K + ((2 * warp + h) * KT + nt) * 64 + 2 * lane;
-              if (in_range(p.status, (dst - (REV ? p.Rs : p.Hs)) + at, 2, extent, CHK_SCAN_WS))
-                *reinterpret_cast<uint32_t*>(dst + at) = t[s];
-            }
-          }
-      }
-      const float dec = ex2(chunk_sum);
+      put(REV ? p.Rl : p.Hl, pairs * p.nc, static_cast<size_t>(gbx) * p.nc + c);
+      const float2 dec = both(ex2(chunk_sum));
 #pragma unroll
       for (int nt = 0; nt < KT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[nt][j] *= dec;
+        for (int h = 0; h < 2; ++h) set_pair(acc[nt], h, mul2(pair(acc[nt], h), dec));
       const uint32_t kt = key0 + (i & 1) * kKey, vt = val0 + (i & 1) * kVal;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
@@ -202,40 +181,34 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const ScanParams p) {
           uint32_t x[P], t[PS];
 #pragma unroll
           for (int s = 0; s < P; ++s) x[s] = raw[s][r];
-          const float2 v = join<P>(x);
-          const float2 ww = r < 2 ? w0 : w1;
-          split<PS>(v.x * ww.x, v.y * ww.y, t);
+          split<PS>(mul2(join<P>(x), r < 2 ? w0 : w1), t);
 #pragma unroll
           for (int s = 0; s < PS; ++s) a[s][r] = t[s];
         }
+        constexpr int NX = KT >= 4 ? 4 : 2;
 #pragma unroll
-        for (int nt = 0; nt < KT; nt += 2) {
-          uint32_t b0[P][2], b1[P][2];
-          load_b2_t<P>(b0, b1, kt, kLd, 16 * ks, 8 * nt);
-          mma_terms<PS, P>(acc[nt], a, b0);
-          mma_terms<PS, P>(acc[nt + 1], a, b1);
+        for (int nt = 0; nt < KT; nt += NX) {
+          uint32_t bb[NX][P][2];
+#pragma unroll
+          for (int n = 0; n < NX; n += 2) load_b2_t<P>(bb[n], bb[n + 1], kt, kLd, 16 * ks, 8 * (nt + n));
+          mma_terms_n<PS, P, NX>(reinterpret_cast<float(&)[NX][4]>(acc[nt]), a, bb);
         }
       }
     }
     __syncwarp();  // the warp's weights may be overwritten
   }
   if (!on) return;
-  if (!WRITE) {
-#pragma unroll
-    for (int nt = 0; nt < KT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const size_t at = seg_at(seg) + (nt * 4 + i) * 32;
-        if (in_range(p.status, at, 1, seg_extent, CHK_SCAN_WS)) p.segst[at] = acc[nt][i];
-      }
-    const size_t at = (static_cast<size_t>(b) * p.N + n) * p.nseg + seg;
-    if (lane == 0 && (16 * warp) % p.V == 0 &&
-        in_range(p.status, at, 1, static_cast<size_t>(p.B) * p.N * p.nseg, CHK_SCAN_WS))
-      p.segdec[at] = total;
+  if (p.nseg > 1) {
+    put(REV ? p.Rseg : p.Hseg, pairs * p.nseg, static_cast<size_t>(gbx) * p.nseg + seg);
+    // the whole segment's decay goes behind its last chunk's
+    const size_t at = static_cast<size_t>(p.B) * p.N * p.nc + head * p.nseg + seg;
+    if (leads && lane == 0 &&
+        in_range(p.status, at, 1, static_cast<size_t>(p.B) * p.N * (p.nc + p.nseg), CHK_SCAN_WS))
+      (REV ? p.rdec : p.cdec)[at] = total;
     return;
   }
   float* fin = REV ? p.dH0 : p.HT;
-  if (seg != p.nseg - 1 || fin == nullptr) return;
+  if (fin == nullptr) return;
 #pragma unroll
   for (int nt = 0; nt < KT; ++nt)
 #pragma unroll
@@ -245,41 +218,54 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const ScanParams p) {
     }
 }
 
-// Joins the segments: turns each segment's own end state into the sequence's,
-// E_g = E_{g-1} 2^dec_g + own_g.  One thread per state element.
-__global__ void __launch_bounds__(256) join_kernel(const ScanParams p) {
-  const int per = kCols * p.K;
-  const long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  if (e >= static_cast<long long>(p.B) * p.Nq * p.nhb * per) return;
-  const long long gbx = e / per;
-  const int at = static_cast<int>(e - gbx * per);
-  const int gb = static_cast<int>(gbx % (p.Nq * p.nhb)), b = static_cast<int>(gbx / (p.Nq * p.nhb));
-  const Place w = place_of(p, b, gb);
-  const int vh = 16 * (at / (16 * p.K)) / p.V;
+// Turns each segment's own end state into the sequence's, E_g = E_{g-1} 2^dec_g
+// + own_g, and writes the last one as the final state.  A thread takes 4
+// neighbouring elements of a tile; grid y runs over the tiles.
+__global__ void __launch_bounds__(256) join_kernel(const ScanParams p, float* ends, const float* cdec,
+                                                   float* fin, int first_pair) {
+  const int per = kCols * p.K, at = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (at >= per) return;
+  const int gbx = first_pair + blockIdx.y, groups = p.Nq * p.nhb;
+  const int b = gbx / groups;
+  const Place w = place_of(p, b, gbx - b * groups);
+  const int blk = at / 64, v = (blk / (p.K / 8)) * 8 + (at % 64) / 8, k = (blk % (p.K / 8)) * 8 + at % 8;
+  const int vh = v / p.V;
   if (vh >= w.heads) return;
-  float* own = p.segst + (gbx * p.nseg) * per + at;
-  const float* dec = p.segdec + (static_cast<size_t>(b) * p.N + w.head0 + vh) * p.nseg;
-  const size_t extent = static_cast<size_t>(p.B) * p.Nq * p.nhb * p.nseg * per;
-  float s = own[0];
+  const size_t head = static_cast<size_t>(b) * p.N + w.head0 + vh;
+  float* own = ends + static_cast<size_t>(gbx) * p.nseg * per + at;
+  const float* dec = cdec + static_cast<size_t>(p.B) * p.N * p.nc + head * p.nseg;
+  const size_t extent = static_cast<size_t>(p.B) * groups * p.nseg * per;
+  float4 s = *reinterpret_cast<const float4*>(own);
   constexpr int U = 8;  // loads in flight
-  for (int g0 = 1; g0 < p.nseg - 1; g0 += U) {
-    float x[U], d[U];
+  for (int g0 = 1; g0 < p.nseg; g0 += U) {
+    float4 x[U];
+    float d[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int g = g0 + u;
-      x[u] = d[u] = 0.f;
-      if (g < p.nseg - 1 && in_range(p.status, (gbx * p.nseg + g) * per + at, 1, extent, CHK_SCAN_WS)) {
-        x[u] = own[static_cast<size_t>(g) * per];
-        d[u] = dec[g];
+      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      d[u] = 0.f;
+      if (g < p.nseg && in_range(p.status, (static_cast<size_t>(gbx) * p.nseg + g) * per + at, 4, extent,
+                                 CHK_SCAN_WS)) {
+        x[u] = *reinterpret_cast<const float4*>(own + static_cast<size_t>(g) * per);
+        d[u] = __ldg(dec + g);
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int g = g0 + u;
-      if (g >= p.nseg - 1) break;
-      s = fmaf(s, ex2(d[u]), x[u]);
-      own[static_cast<size_t>(g) * per] = s;
+      if (g >= p.nseg) break;
+      const float f = ex2(d[u]);
+      s = make_float4(fmaf(s.x, f, x[u].x), fmaf(s.y, f, x[u].y), fmaf(s.z, f, x[u].z), fmaf(s.w, f, x[u].w));
+      *reinterpret_cast<float4*>(own + static_cast<size_t>(g) * per) = s;
     }
+  }
+  if (fin == nullptr) return;
+  const float r[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const size_t to = (head * p.K + k + i) * p.V + v % p.V;
+    if (in_range(p.status, to, 1, static_cast<size_t>(p.B) * p.N * p.K * p.V, CHK_SCAN_STATE)) fin[to] = r[i];
   }
 }
 
@@ -288,20 +274,17 @@ cudaError_t run(const ScanParams& p, cudaStream_t st) {
   constexpr int P = Terms<F32>::in, K = 8 * KT;
   constexpr int smem = 4 * kChunk * 4 + 2 * P * kChunk * (K + 8 + kVLd) * 2;
   const long long pairs = static_cast<long long>(p.B) * p.Nq * p.nhb;
-  auto own = states_kernel<F32, KT, REV, false>;
-  auto write = states_kernel<F32, KT, REV, true>;
+  auto kern = states_kernel<F32, KT, REV>;
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(own, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(write, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  if (p.nseg > 1) {
-    own<<<static_cast<unsigned>(pairs * (p.nseg - 1)), kThreads, smem, st>>>(p);
-    if (p.nseg > 2)
-      join_kernel<<<static_cast<unsigned>((pairs * kCols * K + 255) / 256), 256, 0, st>>>(p);
-  }
-  write<<<static_cast<unsigned>(pairs * p.nseg), kThreads, smem, st>>>(p);
+  kern<<<static_cast<unsigned>(pairs * p.nseg), kThreads, smem, st>>>(p);
+  if (p.nseg > 1)
+    for (long long y0 = 0; y0 < pairs; y0 += 65535)  // (nseg > 1 means few pairs: one launch)
+      join_kernel<<<dim3((kCols * K / 4 + 255) / 256, static_cast<unsigned>(pairs - y0 < 65535 ? pairs - y0 : 65535)),
+                    256, 0, st>>>(p, REV ? p.Rseg : p.Hseg, REV ? p.rdec : p.cdec,
+                                  REV ? p.dH0 : p.HT, static_cast<int>(y0));
   return cudaGetLastError();
 }
 
@@ -317,10 +300,6 @@ cudaError_t run_k(const ScanParams& p, cudaStream_t st) {
 
 }  // namespace
 }  // namespace scan
-
-int scan_state_terms(bool f32) {
-  return f32 ? scan::Terms<true>::state : scan::Terms<false>::state;
-}
 
 cudaError_t launch_scan_states(const ScanParams& p, bool f32, bool reverse, cudaStream_t st) {
   if (f32) return reverse ? scan::run_k<true, true>(p, st) : scan::run_k<true, false>(p, st);
