@@ -91,7 +91,7 @@ int m2rnn_conv_step(const m2rnn_conv_shape *s, const void *x, const m2rnn_rows *
  *   q, qo [B,T,Nq,K], k, ko [B,T,Nk,K] in_dtype (q, k: rows)
  *   wq, wk [K] in_dtype or NULL;  cos, sin [P,R/2] fp32 (NULL if R = 0)
  *   pos [B,T] int32 or NULL (then token t has position t, and T <= P)
- * K a multiple of 8 up to 256; R = 0, 8 or a multiple of 16, R <= K; Nq >= 1,
+ * K a multiple of 8 up to 256; R a multiple of 8, 0 <= R <= K; Nq >= 1,
  * Nk >= 0 (k, ko, wk NULL when 0); eps >= 0 (with eps = 0 a zero row gives
  * NaN, as the formula does).  A position outside [0, P) records
  * M2RNN_ERR_BOUNDS in the device status word (in either build) and gives NaN

@@ -71,7 +71,7 @@ struct QkParams {
   float eps;
   int* status;
 };
-cudaError_t launch_qk_fwd(const QkParams& p, bool f32, int sms, cudaStream_t st);
+cudaError_t launch_qk_fwd(const QkParams& p, bool f32, cudaStream_t st);
 cudaError_t launch_qk_bwd(const QkParams& p, bool f32, bool grad_f32, cudaStream_t st);
 int qk_split(const m2rnn_qk_shape* s);
 int qk_bwd_parts(const m2rnn_qk_shape* s);

@@ -101,7 +101,7 @@ int check_qk(const m2rnn_qk_shape* s, bool backward) {
     return M2RNN_ERR_INVALID_ARG;
   if (backward && s->grad_dtype != M2RNN_F32 && s->grad_dtype != s->in_dtype)
     return M2RNN_ERR_INVALID_ARG;
-  if (s->K % 8 != 0 || s->K > 256 || s->R > s->K || (s->R != 8 && s->R % 16 != 0))
+  if (s->K % 8 != 0 || s->K > 256 || s->R > s->K || s->R % 8 != 0)
     return M2RNN_ERR_UNSUPPORTED_SHAPE;
   if (s->Nq >= (1 << 20) || s->Nk >= (1 << 20)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
   const double tokens = static_cast<double>(s->B) * s->T;
@@ -429,7 +429,7 @@ int m2rnn_qk_norm_fwd(const m2rnn_qk_shape* s, const void* q, const m2rnn_rows* 
   if ((rc = host_check_ptr(ko, dev, s->Nk > 0)) != M2RNN_OK) return rc;
   p.qo = qo;
   p.ko = ko;
-  return status_from_cuda(m2rnn::launch_qk_fwd(p, s->in_dtype == M2RNN_F32, sms,
+  return status_from_cuda(m2rnn::launch_qk_fwd(p, s->in_dtype == M2RNN_F32,
                                                static_cast<cudaStream_t>(stream)));
 }
 

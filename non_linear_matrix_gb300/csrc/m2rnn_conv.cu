@@ -8,13 +8,16 @@
 //
 // with F = [state; x] along time (F[0..W-2] the carried inputs).
 //
-// All three kernels are bound by HBM traffic (2 W + 5 operations for each
-// value read and written).  A thread owns a few neighbouring channels
-// and walks along time with the last W rows of F (backward: and of dz) in
-// registers, so each value is loaded once apart from the W - 1 rows
-// before a thread's run, which its neighbour has just pulled into L2.
-// Neighbouring lanes own neighbouring channels: every row is read in whole
-// 128-byte lines.
+// All three kernels are bound by HBM traffic, the backward one closely followed
+// by instruction issue (about 40 for each pair of values).  A thread owns a few
+// neighbouring channels and walks along time with the last W rows of F
+// (backward: and of dz) in registers, so each value is loaded once apart from the
+// W - 1 rows before a thread's run, which its neighbour has just pulled into
+// L2; the next rows are loaded while these are worked on.  Neighbouring lanes own
+// neighbouring channels: every row is read in whole lines.  Channels are few per
+// thread (4 forward, 2 backward) so that 32 warps fit on an SM: with 8 (16-byte
+// loads) the registers left 16 and the prompt took 77 us instead of FWD_US
+// (B=1 T=65536 C=1152), with 4 backward 110 us instead of BWD_US (B=8 T=4096 C=640).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -54,89 +57,116 @@ __device__ __forceinline__ Raw<F32, VEC> row_of(const ConvParams& p, int b, long
   return raw_load<F32, VEC>(static_cast<const E*>(p.state) + at);
 }
 
-// The taps of VEC channels, w[c][i], and their bias.
+// The taps of VEC channels, as pairs of channels for each tap, and their bias.
 template <bool F32, int VEC, int W>
-__device__ __forceinline__ void load_taps(const ConvParams& p, int c0, float (&w)[VEC][W],
-                                          float (&bias)[VEC]) {
+__device__ __forceinline__ void load_taps(const ConvParams& p, int c0, float2 (&w)[W][VEC / 2],
+                                          float2 (&bias)[VEC / 2]) {
   using E = typename Elem<F32>::T;
+  float t[VEC * W], bb[VEC];
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) bias[j] = 0.f;
-  if (!in_range(p.status, c0, VEC, p.C, CHK_CONV_PARAM)) {
+  for (int j = 0; j < VEC * W; ++j) t[j] = 0.f;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j)
+  for (int j = 0; j < VEC; ++j) bb[j] = 0.f;
+  if (in_range(p.status, c0, VEC, p.C, CHK_CONV_PARAM)) {
+    const E* src = static_cast<const E*>(p.w) + static_cast<size_t>(c0) * W;
 #pragma unroll
-      for (int i = 0; i < W; ++i) w[j][i] = 0.f;
-    return;
+    for (int g = 0; g < W; ++g) {  // VEC * W values, VEC at a time
+      float x[VEC];
+      load_vec<F32, VEC>(src + g * VEC, x);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) t[g * VEC + e] = x[e];
+    }
+    if (p.bias != nullptr) load_vec<F32, VEC>(static_cast<const E*>(p.bias) + c0, bb);
   }
-  const E* src = static_cast<const E*>(p.w) + static_cast<size_t>(c0) * W;
 #pragma unroll
-  for (int g = 0; g < W; ++g) {  // VEC * W values, VEC at a time
-    float t[VEC];
-    load_vec<F32, VEC>(src + g * VEC, t);
+  for (int j = 0; j < VEC / 2; ++j) {
+    bias[j] = make_float2(bb[2 * j], bb[2 * j + 1]);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) w[(g * VEC + e) / W][(g * VEC + e) % W] = t[e];
+    for (int i = 0; i < W; ++i) w[i][j] = make_float2(t[2 * j * W + i], t[(2 * j + 1) * W + i]);
   }
-  if (p.bias != nullptr) load_vec<F32, VEC>(static_cast<const E*>(p.bias) + c0, bias);
 }
 
-template <bool F32, int VEC, int W, bool SILU>
-__device__ __forceinline__ void apply(const float (&f)[W][VEC], const float (&w)[VEC][W],
-                                      const float (&bias)[VEC], float (&y)[VEC]) {
+// z of a thread's channels from the rows f[0..W-1], in pairs.
+template <int VEC, int W>
+__device__ __forceinline__ void filter(const float2 (&f)[W][VEC / 2], const float2 (&w)[W][VEC / 2],
+                                       const float2 (&bias)[VEC / 2], float2 (&z)[VEC / 2]) {
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    float z = bias[j];
+  for (int j = 0; j < VEC / 2; ++j) {
+    z[j] = bias[j];
 #pragma unroll
-    for (int i = 0; i < W; ++i) z = fmaf(w[j][i], f[i][j], z);
-    y[j] = SILU ? z * sigmoid<F32>(z) : z;
+    for (int i = 0; i < W; ++i) z[j] = fma2(w[i][j], f[i][j], z[j]);
   }
+}
+template <bool F32>
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+  return make_float2(sigmoid<F32>(z.x), sigmoid<F32>(z.y));
 }
 
 // One thread: VEC channels x TT tokens.
 template <bool F32, int VEC, int W, bool SILU>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) conv_fwd_kernel(const ConvParams p) {
   using E = typename Elem<F32>::T;
-  constexpr int U = 4;  // rows in flight per thread
+  constexpr int U = 4, H = VEC / 2;  // rows in flight per thread
   const int cv = p.C / VEC;
   const long long item = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   if (item >= static_cast<long long>(p.B) * p.nT * cv) return;
   const int c0 = static_cast<int>(item % cv) * VEC;
-  const int chunk = static_cast<int>((item / cv) % p.nT);
-  const int b = static_cast<int>(item / cv / p.nT);
-  const int t0 = chunk * p.TT, t1 = min(p.T, t0 + p.TT);
-  float w[VEC][W], bias[VEC], f[W][VEC];
-  Raw<F32, VEC> last[W - 1];  // F[t .. t+W-2] as they lie in memory
+  const long long run = item / cv;
+  const int b = static_cast<int>(run / p.nT);
+  const int t0 = static_cast<int>(run - static_cast<long long>(b) * p.nT) * p.TT, t1 = min(p.T, t0 + p.TT);
+  float2 w[W][H], bias[H], f[W][H];
+  Raw<F32, VEC> next[U], last[W - 1];  // F[t .. t+W-2] as they lie in memory
 #pragma unroll
   for (int i = 0; i < W - 1; ++i) last[i] = row_of<F32, VEC, W>(p, b, t0 + i, c0);
+  const E* x = static_cast<const E*>(p.x) + b * p.xb + t0 * p.xt + c0;
+  auto load = [&](int t) {
+    return t < t1 && in_range(p.status, t, 1, p.T, CHK_CONV_IN) ? raw_load<F32, VEC>(x)
+                                                                : raw_zero<F32, VEC>();
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    next[u] = load(t0 + u);
+    x += p.xt;
+  }
   load_taps<F32, VEC, W>(p, c0, w, bias);
 #pragma unroll
-  for (int i = 0; i < W - 1; ++i) raw_unpack<F32, VEC>(last[i], f[i]);
+  for (int i = 0; i < W - 1; ++i) raw_unpack2<F32, VEC>(last[i], f[i]);
+  size_t at = (static_cast<size_t>(b) * p.T + t0) * p.C + c0;
+  const size_t extent = static_cast<size_t>(p.B) * p.T * p.C;
   E* y = static_cast<E*>(p.y);
   for (int t = t0; t < t1; t += U) {
     Raw<F32, VEC> r[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      r[u] = t + u < t1 ? row_of<F32, VEC, W>(p, b, t + u + W - 1, c0) : raw_zero<F32, VEC>();
+    for (int u = 0; u < U; ++u) {
+      r[u] = next[u];
+      next[u] = load(t + U + u);
+      x += p.xt;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (t + u >= t1) break;
-      raw_unpack<F32, VEC>(r[u], f[W - 1]);
-      float o[VEC];
-      apply<F32, VEC, W, SILU>(f, w, bias, o);
-      const size_t at = (static_cast<size_t>(b) * p.T + t + u) * p.C + c0;
-      if (in_range(p.status, at, VEC, static_cast<size_t>(p.B) * p.T * p.C, CHK_CONV_OUT))
-        store_vec<F32, VEC>(y + at, o);
+      raw_unpack2<F32, VEC>(r[u], f[W - 1]);
+      float2 z[H];
+      filter<VEC, W>(f, w, bias, z);
+      if (SILU) {
+#pragma unroll
+        for (int j = 0; j < H; ++j) z[j] = mul2(z[j], sigmoid2<F32>(z[j]));
+      }
+      if (in_range(p.status, at, VEC, extent, CHK_CONV_OUT))
+        raw_store<F32, VEC>(y + at, raw_pack2<F32, VEC>(z));
+      at += p.C;
 #pragma unroll
       for (int i = 0; i < W - 1; ++i)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) f[i][j] = f[i + 1][j];
+        for (int j = 0; j < H; ++j) f[i][j] = f[i + 1][j];
     }
   }
   if (t1 == p.T && p.state_out != nullptr) {  // f now holds F's last W - 1 rows
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
-      const size_t at = (static_cast<size_t>(b) * (W - 1) + i) * p.C + c0;
-      if (in_range(p.status, at, VEC, static_cast<size_t>(p.B) * (W - 1) * p.C, CHK_CONV_OUT))
-        store_vec<F32, VEC>(static_cast<E*>(p.state_out) + at, f[i]);
+      const size_t sat = (static_cast<size_t>(b) * (W - 1) + i) * p.C + c0;
+      if (in_range(p.status, sat, VEC, static_cast<size_t>(p.B) * (W - 1) * p.C, CHK_CONV_OUT))
+        raw_store<F32, VEC>(static_cast<E*>(p.state_out) + sat, raw_pack2<F32, VEC>(f[i]));
     }
   }
 }
@@ -151,16 +181,20 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvParams p) {
   if (item >= static_cast<long long>(p.B) * cv) return;
   const int c0 = static_cast<int>(item % cv) * VEC, b = static_cast<int>(item / cv);
   Raw<F32, VEC> r[W];
-  float f[W][VEC], w[VEC][W], bias[VEC], o[VEC];
+  float2 f[W][VEC / 2], w[W][VEC / 2], bias[VEC / 2], o[VEC / 2];
 #pragma unroll
   for (int i = 0; i < W; ++i) r[i] = row_of<F32, VEC, W>(p, b, i, c0);
   load_taps<F32, VEC, W>(p, c0, w, bias);
 #pragma unroll
-  for (int i = 0; i < W; ++i) raw_unpack<F32, VEC>(r[i], f[i]);
-  apply<F32, VEC, W, SILU>(f, w, bias, o);
+  for (int i = 0; i < W; ++i) raw_unpack2<F32, VEC>(r[i], f[i]);
+  filter<VEC, W>(f, w, bias, o);
+  if (SILU) {
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) o[j] = mul2(o[j], sigmoid2<F32>(o[j]));
+  }
   const size_t yat = static_cast<size_t>(b) * p.C + c0;
   if (in_range(p.status, yat, VEC, static_cast<size_t>(p.B) * p.C, CHK_CONV_OUT))
-    store_vec<F32, VEC>(static_cast<E*>(p.y) + yat, o);
+    raw_store<F32, VEC>(static_cast<E*>(p.y) + yat, raw_pack2<F32, VEC>(o));
 #pragma unroll
   for (int i = 0; i < W - 1; ++i) {
     const size_t at = (static_cast<size_t>(b) * (W - 1) + i) * p.C + c0;
@@ -169,15 +203,14 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvParams p) {
   }
 }
 
-// A warp takes 128 channels (4 per lane: more would not leave the registers
-// for the taps, the two windows and the sums) and runs of TT rows of F; a run
-// [m0, m0 + TT) writes dF there and adds dz's products for tokens in it.  The
-// eight warps' sums are added in warp order, the CTAs' by sum_parts_kernel.
+// A warp takes 64 channels (2 per lane) and runs of TT rows of F; a run [m0, m0 +
+// TT) writes dF there and adds dz's products for tokens in it.  The eight
+// warps' sums are added in warp order, the CTAs' by sum_parts_kernel.
 template <bool F32, bool G32, int W, bool SILU>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) conv_bwd_kernel(const ConvParams p) {
   using E = typename Elem<F32>::T;
   using G = typename Elem<G32>::T;
-  constexpr int VEC = 4, kWarps = kThreads / 32, U = 2;
+  constexpr int VEC = 2, kWarps = kThreads / 32, U = 2;
   __shared__ float sums[kWarps][32 * VEC * (W + 1)];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c0 = (blockIdx.x * 32 + lane) * VEC;
@@ -185,113 +218,108 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvParams p) 
   const long long rows = static_cast<long long>(p.T) + W - 1;
   const size_t xn = static_cast<size_t>(p.B) * p.T * p.C;
   const size_t sn = static_cast<size_t>(p.B) * (W - 1) * p.C;
-  float dw[VEC][W], db[VEC];
+  float2 dw[W], db = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    db[j] = 0.f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) dw[j][i] = 0.f;
-  }
+  for (int i = 0; i < W; ++i) dw[i] = make_float2(0.f, 0.f);
   if (active) {
-    float w[VEC][W], bias[VEC];
+    float2 w[W][1], bias[1];
     load_taps<F32, VEC, W>(p, c0, w, bias);
     const long long runs = static_cast<long long>(p.B) * p.nT;
     for (long long g = static_cast<long long>(blockIdx.y) * kWarps + warp; g < runs;
          g += static_cast<long long>(gridDim.y) * kWarps) {
       const int b = static_cast<int>(g / p.nT);
-      const long long m0 = (g % p.nT) * p.TT;
-      const long long m1 = m0 + p.TT < rows ? m0 + p.TT : rows;
-      const long long first = m0 - (W - 1) > 0 ? m0 - (W - 1) : 0;
-      float f[W][VEC], dz[W][VEC];  // dz[i]: of token t - (W-1) + i
+      const long long m0 = (g - static_cast<long long>(b) * p.nT) * p.TT;
+      const int m1 = static_cast<int>(m0 + p.TT < rows ? m0 + p.TT : rows);
+      const int first = static_cast<int>(m0 - (W - 1) > 0 ? m0 - (W - 1) : 0);
+      const int tend = min(p.T, m1);  // tokens to be read
+      float2 f[W][1], dz[W];          // dz[i]: of token t - (W-1) + i
 #pragma unroll
-      for (int i = 0; i < W; ++i)
+      for (int i = 0; i < W; ++i) f[i][0] = dz[i] = make_float2(0.f, 0.f);
+      const E* x = static_cast<const E*>(p.x) + b * p.xb + first * p.xt + c0;
+      const G* dy = static_cast<const G*>(p.dy) + (static_cast<size_t>(b) * p.T + first) * p.C + c0;
+      Raw<F32, VEC> nx[U];
+      Raw<G32, VEC> ng[U];
+      auto load = [&](int t, int u) {
+        const bool on = t < tend && in_range(p.status, t, 1, p.T, CHK_CONV_IN);
+        nx[u] = on ? raw_load<F32, VEC>(x) : raw_zero<F32, VEC>();
+        ng[u] = on ? raw_load<G32, VEC>(dy) : raw_zero<G32, VEC>();
+        x += p.xt;
+        dy += p.C;
+      };
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) f[i][j] = dz[i][j] = 0.f;
+      for (int u = 0; u < U; ++u) load(first + u, u);
 #pragma unroll
       for (int i = 0; i < W - 1; ++i)
-        if (first + i < rows) raw_unpack<F32, VEC>(row_of<F32, VEC, W>(p, b, first + i, c0), f[i]);
-      for (long long t = first; t < m1; t += U) {
+        if (first + i < rows)
+          raw_unpack2<F32, VEC>(row_of<F32, VEC, W>(p, b, first + i, c0), f[i]);
+      for (int t = first; t < m1; t += U) {
         Raw<F32, VEC> rx[U];
         Raw<G32, VEC> rg[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          rx[u] = raw_zero<F32, VEC>();
-          rg[u] = raw_zero<G32, VEC>();
-          if (t + u < p.T && t + u < m1) {
-            rx[u] = row_of<F32, VEC, W>(p, b, t + u + W - 1, c0);
-            const size_t at = (static_cast<size_t>(b) * p.T + t + u) * p.C + c0;
-            if (in_range(p.status, at, VEC, xn, CHK_CONV_IN))
-              rg[u] = raw_load<G32, VEC>(static_cast<const G*>(p.dy) + at);
-          }
+          rx[u] = nx[u];
+          rg[u] = ng[u];
+          load(t + U + u, u);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const long long m = t + u;
+          const int m = t + u;
           if (m >= m1) break;
-          float gy[VEC];
-          raw_unpack<F32, VEC>(rx[u], f[W - 1]);
-          raw_unpack<G32, VEC>(rg[u], gy);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            float d = gy[j];
-            if (SILU) {
-              float z = bias[j];
-#pragma unroll
-              for (int i = 0; i < W; ++i) z = fmaf(w[j][i], f[i][j], z);
-              const float s = sigmoid<F32>(z);
-              d *= s * fmaf(z, 1.f - s, 1.f);
-            }
-            dz[W - 1][j] = m < p.T ? d : 0.f;
+          float2 gy[1];
+          raw_unpack2<F32, VEC>(rx[u], f[W - 1]);
+          raw_unpack2<G32, VEC>(rg[u], gy);
+          float2 d = gy[0];
+          if (SILU) {
+            float2 z[1];
+            filter<VEC, W>(f, w, bias, z);
+            const float2 s = sigmoid2<F32>(z[0]), one = make_float2(1.f, 1.f);
+            // s (1 + z (1 - s)); at z = +-inf the bracket's product is 0 times inf: NaN, as in the formula
+            d = mul2(d, mul2(s, fma2(z[0], fma2(s, make_float2(-1.f, -1.f), one), one)));
           }
+          dz[W - 1] = m < p.T ? d : make_float2(0.f, 0.f);
           if (m >= m0) {
-            float o[VEC];
+            float2 o[1] = {make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-              o[j] = 0.f;
-#pragma unroll
-              for (int i = 0; i < W; ++i) {
-                o[j] = fmaf(w[j][i], dz[W - 1 - i][j], o[j]);
-                dw[j][i] = fmaf(dz[W - 1][j], f[i][j], dw[j][i]);
-              }
-              db[j] += dz[W - 1][j];
+            for (int i = 0; i < W; ++i) {
+              o[0] = fma2(w[i][0], dz[W - 1 - i], o[0]);
+              dw[i] = fma2(dz[W - 1], f[i][0], dw[i]);
             }
+            db = add2(db, dz[W - 1]);
             if (m >= p.T && p.dstate_out != nullptr) {
               const size_t at = (static_cast<size_t>(b) * (W - 1) + (m - p.T)) * p.C + c0;
-              float ds[VEC];
+              float2 ds[1];
               if (in_range(p.status, at, VEC, sn, CHK_CONV_IN)) {
-                load_vec<F32, VEC>(static_cast<const E*>(p.dstate_out) + at, ds);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) o[j] += ds[j];
+                raw_unpack2<F32, VEC>(raw_load<F32, VEC>(static_cast<const E*>(p.dstate_out) + at), ds);
+                o[0] = add2(o[0], ds[0]);
               }
             }
             if (m >= W - 1) {
               const size_t at = (static_cast<size_t>(b) * p.T + (m - (W - 1))) * p.C + c0;
               if (in_range(p.status, at, VEC, xn, CHK_CONV_OUT))
-                store_vec<F32, VEC>(static_cast<E*>(p.dx) + at, o);
+                raw_store<F32, VEC>(static_cast<E*>(p.dx) + at, raw_pack2<F32, VEC>(o));
             } else if (p.dstate != nullptr) {
               const size_t at = (static_cast<size_t>(b) * (W - 1) + m) * p.C + c0;
               if (in_range(p.status, at, VEC, sn, CHK_CONV_OUT))
-                store_vec<F32, VEC>(static_cast<E*>(p.dstate) + at, o);
+                raw_store<F32, VEC>(static_cast<E*>(p.dstate) + at, raw_pack2<F32, VEC>(o));
             }
           }
 #pragma unroll
-          for (int i = 0; i < W - 1; ++i)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-              f[i][j] = f[i + 1][j];
-              dz[i][j] = dz[i + 1][j];
-            }
+          for (int i = 0; i < W - 1; ++i) {
+            f[i][0] = f[i + 1][0];
+            dz[i] = dz[i + 1];
+          }
         }
       }
     }
   }
   // the part's layout: dw [C][W], then dbias [C]
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) sums[warp][(lane * VEC + j) * W + i] = dw[j][i];
-    sums[warp][32 * VEC * W + lane * VEC + j] = db[j];
+  for (int i = 0; i < W; ++i) {
+    sums[warp][lane * VEC * W + i] = dw[i].x;
+    sums[warp][(lane * VEC + 1) * W + i] = dw[i].y;
   }
+  sums[warp][32 * VEC * W + lane * VEC] = db.x;
+  sums[warp][32 * VEC * W + lane * VEC + 1] = db.y;
   __syncthreads();
   const int cols = min(32 * VEC, p.C - static_cast<int>(blockIdx.x) * 32 * VEC);
   float* part = p.part + static_cast<size_t>(blockIdx.y) * p.C * (W + 1);
@@ -310,8 +338,7 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvParams p) 
 
 template <bool F32, int W, bool SILU>
 cudaError_t fwd_w(const ConvParams& p, cudaStream_t st) {
-  // 16-byte loads in both types: 8 channels of bf16, 4 of fp32
-  constexpr int VEC = F32 ? 4 : 8;
+  constexpr int VEC = 4;
   const long long items = static_cast<long long>(p.B) * p.nT * (p.C / VEC);
   const long long grid = (items + kThreads - 1) / kThreads;
   conv_fwd_kernel<F32, VEC, W, SILU><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(p);
@@ -328,7 +355,7 @@ cudaError_t step_w(const ConvParams& p, cudaStream_t st) {
 
 template <bool F32, int W, bool SILU>
 cudaError_t bwd_w(const ConvParams& p, bool grad_f32, cudaStream_t st) {
-  const dim3 grid((p.C + 127) / 128, p.nparts);
+  const dim3 grid((p.C + 63) / 64, p.nparts);
   if (F32 || grad_f32)
     conv_bwd_kernel<F32, true, W, SILU><<<grid, kThreads, 0, st>>>(p);
   else
@@ -355,25 +382,28 @@ cudaError_t bwd_w(const ConvParams& p, bool grad_f32, cudaStream_t st) {
 // TT), short ones give more threads; the longest run that still leaves
 // 2,048 threads for each SM, 4 tokens at least.
 int conv_fwd_tokens(const m2rnn_conv_shape* s, int sms) {
-  const int vec = s->in_dtype == M2RNN_F32 ? 4 : 8;
-  const long long per_token = static_cast<long long>(s->B) * (s->C / vec);
+  const long long per_token = static_cast<long long>(s->B) * (s->C / 4);
   int tt = 32;
   while (tt > 4 && per_token * ((s->T + tt - 1) / tt) < 2048LL * sms) tt /= 2;
   return tt;
 }
 
-// Runs of 32 rows, 16 or 8 where the sequences are short; at most 1,216 CTAs
-// (8 for each of 152 SMs), so that the parts stay a small share of the bytes.
+// CTAs of eight warps for 64 channels each, as many as are resident (456: three
+// for each of 152 SMs) and no more, so that they end together and the parts
+// stay few; the sequences are cut so that each warp has one run, 8 rows at
+// least.
 void conv_bwd_plan(const m2rnn_conv_shape* s, int* TT, int* nT, int* nparts) {
   const long long rows = static_cast<long long>(s->T) + s->W - 1;
-  const int groups = (s->C + 127) / 128;
-  int tt = 32;
-  while (tt > 8 && s->B * ((rows + tt - 1) / tt) * groups < 8LL * 1216) tt /= 2;
-  *TT = tt;
+  const long long groups = (s->C + 63) / 64;
+  const long long parts = 456 / groups > 1 ? 456 / groups : 1;
+  long long per_item = parts * 8 / s->B;  // runs of a sequence
+  if (per_item < 1) per_item = 1;
+  long long tt = (rows + per_item - 1) / per_item;
+  if (tt < 8) tt = 8;
+  *TT = static_cast<int>(tt);
   *nT = static_cast<int>((rows + tt - 1) / tt);
   const long long need = (static_cast<long long>(s->B) * *nT + 7) / 8;
-  const long long most = 1216 / groups > 1 ? 1216 / groups : 1;
-  *nparts = static_cast<int>(need < most ? need : most);
+  *nparts = static_cast<int>(need < parts ? need : parts);
 }
 
 cudaError_t launch_conv_fwd(const ConvParams& p, bool f32, bool silu, cudaStream_t st) {

@@ -8,12 +8,14 @@
 // where Rot turns the pairs of the first R features by the token's angles.
 //
 // Bound by HBM traffic: every row is read once and written once.  K / 8 lanes
-// hold a head's row, 8 features each (one 16-byte load of bf16); the row's
-// sums are shuffles among them.  The rotation's partner feature is in the
-// same lane (interleaved pairs) or in the lane R / 16 further on (one
-// shuffle).  A lane group takes several heads of one token, so that the
-// token's cosines and sines are loaded once for all of them: per head they
-// would be 8 R bytes next to 2 K bytes of row.
+// hold a head's row as two quads of features each; the row's sums are
+// shuffles among them.  A lane's quads are chosen so that both features of a
+// rotated pair are its own (quads i and i + R/2 for pairs at that distance), so
+// that the rotation needs no exchange: with eight neighbouring features per
+// lane it took eight shuffles a row, and the prompt 77 us instead of FWD_US
+// (B=8 T=2048, 64 heads of 64).  A lane group takes several heads of one token,
+// so that the token's cosines and sines are loaded once for all of them: per head
+// they would be 4 R bytes next to 2 K bytes of row.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -34,169 +36,179 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// A lane's share of one token's rotation.
-struct Angles {
-  float c[8], n[8];  // cosine and signed sine of each of the lane's features
-  int src;           // lane (of the row's) that holds the partner features
+// A lane's place in a row: the first features of its two quads, whether they
+// rotate, and the token's angles for them.
+struct Lane {
+  int o[2];
+  bool on, turns;
+  float2 c[2], n[2];  // cosine, sine of angles i .. i + 3
 };
 
-// The partner of feature j (0..7) of the lane, given the lane's own values.
-__device__ __forceinline__ void partners(const QkParams& p, const Angles& a, const float (&u)[8],
-                                         float (&o)[8], int lpr) {
-  if (p.interleaved) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = u[j ^ 1];
-  } else if (p.R == 8) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = u[j ^ 4];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(0xffffffffu, u[j], a.src, lpr);
-  }
+template <int LPR>
+__device__ __forceinline__ Lane lane_of(const QkParams& p) {
+  const int l = threadIdx.x % LPR;
+  Lane a;
+  a.on = 8 * l < p.K;
+  a.turns = 8 * l < p.R;
+  const bool apart = a.turns && !p.interleaved;
+  a.o[0] = apart ? 4 * l : 8 * l;
+  a.o[1] = apart ? 4 * l + p.R / 2 : 8 * l + 4;
+  a.c[0] = a.c[1] = make_float2(1.f, 1.f);
+  a.n[0] = a.n[1] = make_float2(0.f, 0.f);
+  return a;
 }
 
-// Angles of token `token` for row lane l.  The sine carries the sign with
-// which the partner enters: first of a pair -, second +.
-__device__ __forceinline__ void load_angles(const QkParams& p, long long token, int l, bool valid,
-                                            Angles& a) {
-  a.src = l;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    a.c[j] = 1.f;
-    a.n[j] = 0.f;
-  }
-  if (p.R == 0) return;
-  const int half = p.R / 2;
-  if (!p.interleaved && p.R >= 16 && 8 * l < p.R) a.src = 8 * l < half ? l + half / 8 : l - half / 8;
-  if (!valid || 8 * l >= p.R) return;
-  int pos = static_cast<int>(token % p.T);
-  if (p.pos != nullptr) pos = __ldg(p.pos + token);
+// The angles of a token.
+template <int LPR>
+__device__ __forceinline__ void load_angles(const QkParams& p, long long token, int t, bool valid,
+                                            Lane& a) {
+  if (!valid || !a.turns) return;
+  const int pos = p.pos != nullptr ? __ldg(p.pos + token) : t;
   if (pos < 0 || pos >= p.P) {
     if (atomicCAS(&p.status[0], 0, kStatusBounds) == 0) atomicExch(&p.status[1], CHK_QK_POS);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) a.c[j] = a.n[j] = __int_as_float(0x7fffffff);
+    const float nan = __int_as_float(0x7fffffff);
+    a.c[0] = a.c[1] = a.n[0] = a.n[1] = make_float2(nan, nan);
     return;
   }
-  const float* cs = p.cs + static_cast<size_t>(pos) * half;
-  const float* sn = p.sn + static_cast<size_t>(pos) * half;
-  if (p.interleaved || p.R == 8) {  // four angles for the lane's eight features
-    const int i0 = p.interleaved ? 4 * l : 0;
-    const float4 c = __ldg(reinterpret_cast<const float4*>(cs + i0));
-    const float4 n = __ldg(reinterpret_cast<const float4*>(sn + i0));
-    const float cc[4] = {c.x, c.y, c.z, c.w}, nn[4] = {n.x, n.y, n.z, n.w};
+  const size_t at = static_cast<size_t>(pos) * (p.R / 2) + 4 * (threadIdx.x % LPR);
+  const float4 c = __ldg(reinterpret_cast<const float4*>(p.cs + at));
+  const float4 n = __ldg(reinterpret_cast<const float4*>(p.sn + at));
+  a.c[0] = make_float2(c.x, c.y);
+  a.c[1] = make_float2(c.z, c.w);
+  a.n[0] = make_float2(n.x, n.y);
+  a.n[1] = make_float2(n.z, n.w);
+}
+
+// u[0..1], u[2..3]: the lane's quads as pairs; turned in place by the angles
+// (TURN = 1) or back (-1).
+template <int TURN>
+__device__ __forceinline__ void rotate(const QkParams& p, const Lane& a, float2 (&u)[4]) {
+  if (p.R == 0) return;
+  if (p.interleaved) {  // (2i, 2i + 1) is one of the pairs
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int ci = p.interleaved ? j / 2 : j % 4;
-      const bool second = p.interleaved ? (j & 1) : j >= 4;
-      a.c[j] = ci == 0 ? cc[0] : ci == 1 ? cc[1] : ci == 2 ? cc[2] : cc[3];
-      const float s = ci == 0 ? nn[0] : ci == 1 ? nn[1] : ci == 2 ? nn[2] : nn[3];
-      a.n[j] = second ? s : -s;
+    for (int j = 0; j < 4; ++j) {
+      const float c = (j & 1) ? a.c[j / 2].y : a.c[j / 2].x;
+      const float n = TURN * ((j & 1) ? a.n[j / 2].y : a.n[j / 2].x);
+      u[j] = make_float2(fmaf(u[j].x, c, -u[j].y * n), fmaf(u[j].y, c, u[j].x * n));
     }
     return;
   }
-  const bool second = 8 * l >= half;
-  const int i0 = second ? 8 * l - half : 8 * l;
 #pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const float4 c = __ldg(reinterpret_cast<const float4*>(cs + i0) + g);
-    const float4 n = __ldg(reinterpret_cast<const float4*>(sn + i0) + g);
-    a.c[4 * g] = c.x; a.c[4 * g + 1] = c.y; a.c[4 * g + 2] = c.z; a.c[4 * g + 3] = c.w;
-    a.n[4 * g] = second ? n.x : -n.x;
-    a.n[4 * g + 1] = second ? n.y : -n.y;
-    a.n[4 * g + 2] = second ? n.z : -n.z;
-    a.n[4 * g + 3] = second ? n.w : -n.w;
+  for (int j = 0; j < 2; ++j) {  // first quad with second
+    const float2 n = a.n[j], m = make_float2(-n.x, -n.y);
+    const float2 x = u[j], y = u[2 + j];
+    const float2 xr = fma2(y, TURN > 0 ? m : n, mul2(x, a.c[j]));
+    const float2 yr = fma2(x, TURN > 0 ? n : m, mul2(y, a.c[j]));
+    u[j] = a.turns ? xr : x;
+    u[2 + j] = a.turns ? yr : y;
   }
 }
 
-// o = Rot(u) for sign = 1, Rot^T(u) for sign = -1.
-__device__ __forceinline__ void rotate(const QkParams& p, const Angles& a, float sign, int lpr,
-                                       const float (&u)[8], float (&o)[8]) {
-  if (p.R == 0) {
+template <bool F32>
+struct RawRow {
+  Raw<F32, 4> q[2];
+};
+template <bool F32>
+__device__ __forceinline__ RawRow<F32> row_zero() {
+  return RawRow<F32>{{raw_zero<F32, 4>(), raw_zero<F32, 4>()}};
+}
+template <bool F32>
+__device__ __forceinline__ RawRow<F32> row_load(const typename Elem<F32>::T* src, const Lane& a) {
+  return RawRow<F32>{{raw_load<F32, 4>(src + a.o[0]), raw_load<F32, 4>(src + a.o[1])}};
+}
+template <bool F32>
+__device__ __forceinline__ void row_unpack(const RawRow<F32>& r, float2 (&o)[4]) {
+  float2 t[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = u[j];
-    return;
+  for (int i = 0; i < 2; ++i) {
+    raw_unpack2<F32, 4>(r.q[i], t);
+    o[2 * i] = t[0];
+    o[2 * i + 1] = t[1];
   }
-  float v[8];
-  partners(p, a, u, v, lpr);
+}
+template <bool F32>
+__device__ __forceinline__ void row_store(typename Elem<F32>::T* dst, const Lane& a, const float2 (&o)[4]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = fmaf(u[j], a.c[j], sign * a.n[j] * v[j]);
+  for (int i = 0; i < 2; ++i) {
+    const float2 t[2] = {o[2 * i], o[2 * i + 1]};
+    raw_store<F32, 4>(dst + a.o[i], raw_pack2<F32, 4>(t));
+  }
 }
 
 template <bool F32>
-__device__ __forceinline__ void load_weight(const QkParams& p, const void* w, int l, float (&o)[8]) {
+__device__ __forceinline__ void load_weight(const QkParams& p, const void* w, const Lane& a, float2 (&o)[4]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = 1.f;
-  if (w != nullptr && in_range(p.status, 8 * l, 8, p.K, CHK_QK_PARAM))
-    load_vec<F32, 8>(static_cast<const typename Elem<F32>::T*>(w) + 8 * l, o);
+  for (int j = 0; j < 4; ++j) o[j] = make_float2(1.f, 1.f);
+  if (w != nullptr && a.on && in_range(p.status, a.o[0], 4, p.K, CHK_QK_PARAM) &&
+      in_range(p.status, a.o[1], 4, p.K, CHK_QK_PARAM))
+    row_unpack<F32>(row_load<F32>(static_cast<const typename Elem<F32>::T*>(w), a), o);
 }
 
-// Input row of head h (queries first, then keys) of a token.
+// Row of head h (queries first, then keys) of a token in the inputs.
 template <bool F32>
-__device__ __forceinline__ Raw<F32, 8> load_row(const QkParams& p, int b, int t, int h, int l) {
+__device__ __forceinline__ const typename Elem<F32>::T* in_row(const QkParams& p, long long qrow,
+                                                               long long krow, int h) {
   using E = typename Elem<F32>::T;
-  const bool isq = h < p.Nq;
-  const int hh = isq ? h : h - p.Nq;
-  if (!in_range(p.status, static_cast<size_t>(hh) * p.K + 8 * l, 8,
-                static_cast<size_t>(isq ? p.Nq : p.Nk) * p.K, CHK_QK_IN) ||
-      !in_range(p.status, t, 1, p.T, CHK_QK_IN))
-    return raw_zero<F32, 8>();
-  const E* base = isq ? static_cast<const E*>(p.q) + b * p.qb + t * p.qt
-                      : static_cast<const E*>(p.k) + b * p.kb + t * p.kt;
-  return raw_load<F32, 8>(base + hh * p.K + 8 * l);
+  return h < p.Nq ? static_cast<const E*>(p.q) + qrow + static_cast<long long>(h) * p.K
+                  : static_cast<const E*>(p.k) + krow + static_cast<long long>(h - p.Nq) * p.K;
 }
-
-// Offset of head h's row of a token in a contiguous [tokens][Nq or Nk][K].
-__device__ __forceinline__ size_t out_at(const QkParams& p, long long token, int h, int l) {
-  return h < p.Nq ? (static_cast<size_t>(token) * p.Nq + h) * p.K + 8 * l
-                  : (static_cast<size_t>(token) * p.Nk + (h - p.Nq)) * p.K + 8 * l;
+// The same in a contiguous [tokens][Nq or Nk][K].
+__device__ __forceinline__ size_t out_at(const QkParams& p, long long token, int h) {
+  return (h < p.Nq ? static_cast<size_t>(token) * p.Nq + h
+                   : static_cast<size_t>(token) * p.Nk + (h - p.Nq)) * p.K;
 }
-__device__ __forceinline__ size_t out_extent(const QkParams& p, int h) {
-  return static_cast<size_t>(p.tokens) * (h < p.Nq ? p.Nq : p.Nk) * p.K;
+__device__ __forceinline__ bool out_ok(const QkParams& p, size_t at, int h, int site) {
+  return in_range(p.status, at, p.K, static_cast<size_t>(p.tokens) * (h < p.Nq ? p.Nq : p.Nk) * p.K, site);
 }
 
 // A lane group takes heads g, g + split, ... of one token, U at a time.
 template <bool F32, int LPR>
-__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) qk_fwd_kernel(const QkParams p) {
   using E = typename Elem<F32>::T;
-  constexpr int U = F32 ? 2 : 4;  // rows in flight
+  constexpr int U = 4;  // rows in flight
   const long long gid = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / LPR;
-  const int l = threadIdx.x % LPR;
   const long long token = gid / p.split;
-  const int g = static_cast<int>(gid % p.split);
+  const int g = static_cast<int>(gid - token * p.split);
   const int heads = p.Nq + p.Nk;
-  const bool valid = token < p.tokens && 8 * l < p.K;
-  const int b = static_cast<int>(token / p.T), t = static_cast<int>(token % p.T);
-  Angles a;
-  load_angles(p, token, l, valid, a);
-  float wq[8], wk[8];
-  load_weight<F32>(p, 8 * l < p.K ? p.wq : nullptr, l, wq);
-  load_weight<F32>(p, 8 * l < p.K ? p.wk : nullptr, l, wk);
-  const float inv_k = 1.f / static_cast<float>(p.K);
+  Lane a = lane_of<LPR>(p);
+  const bool valid = token < p.tokens && a.on;
+  const int b = static_cast<int>(token / p.T), t = static_cast<int>(token - static_cast<long long>(b) * p.T);
+  const long long qrow = b * p.qb + t * p.qt, krow = b * p.kb + t * p.kt;
   const int steps = (heads + p.split - 1) / p.split;  // the same for every lane: shuffles below
-  for (int s0 = 0; s0 < steps; s0 += U) {
-    Raw<F32, 8> r[U];
+  RawRow<F32> next[U];
+  auto load = [&](int s0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = g + (s0 + u) * p.split;
-      r[u] = valid && h < heads ? load_row<F32>(p, b, t, h, l) : raw_zero<F32, 8>();
+      next[u] = valid && h < heads && in_range(p.status, t, 1, p.T, CHK_QK_IN)
+                    ? row_load<F32>(in_row<F32>(p, qrow, krow, h), a) : row_zero<F32>();
     }
+  };
+  load(0);
+  load_angles<LPR>(p, token, t, valid, a);
+  float2 wq[4], wk[4];
+  load_weight<F32>(p, p.wq, a, wq);
+  load_weight<F32>(p, p.wk, a, wk);
+  const float inv_k = 1.f / static_cast<float>(p.K);
+  for (int s0 = 0; s0 < steps; s0 += U) {
+    RawRow<F32> r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u] = next[u];
+    if (s0 + U < steps) load(s0 + U);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (s0 + u >= steps) break;
       const int h = g + (s0 + u) * p.split;
-      float x[8], o[8], ss = 0.f;
-      raw_unpack<F32, 8>(r[u], x);
+      float2 x[4];
+      row_unpack<F32>(r[u], x);
+      const float2 ss = fma2(x[0], x[0], fma2(x[1], x[1], fma2(x[2], x[2], mul2(x[3], x[3]))));
+      const float2 rs = both(rsqrtf(row_sum<LPR>(ss.x + ss.y) * inv_k + p.eps));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-      const float rs = rsqrtf(row_sum<LPR>(ss) * inv_k + p.eps);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= rs * (h < p.Nq ? wq[j] : wk[j]);
-      rotate(p, a, 1.f, LPR, x, o);
-      if (valid && h < heads) {
-        const size_t at = out_at(p, token, h, l);
-        if (in_range(p.status, at, 8, out_extent(p, h), CHK_QK_OUT))
-          store_vec<F32, 8>(static_cast<E*>(h < p.Nq ? p.qo : p.ko) + at, o);
-      }
+      for (int j = 0; j < 4; ++j) x[j] = mul2(mul2(x[j], rs), h < p.Nq ? wq[j] : wk[j]);
+      rotate<1>(p, a, x);
+      const size_t at = out_at(p, token, h);
+      if (valid && h < heads && out_ok(p, at, h, CHK_QK_OUT))
+        row_store<F32>(static_cast<E*>(h < p.Nq ? p.qo : p.ko) + at, a, x);
     }
   }
 }
@@ -204,20 +216,19 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkParams p) {
 // As the forward kernel, with the groups walking over the tokens: a lane
 // keeps its features' shares of dwq and dwk in registers throughout.
 template <bool F32, bool G32, int LPR>
-__global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const QkParams p) {
   using E = typename Elem<F32>::T;
   using G = typename Elem<G32>::T;
   constexpr int U = 2, kGroups = kThreads / LPR;
   __shared__ float sums[2][kGroups][8 * LPR + 1];
-  const int l = threadIdx.x % LPR;
   const int heads = p.Nq + p.Nk;
   const float inv_k = 1.f / static_cast<float>(p.K);
-  const bool lane_on = 8 * l < p.K;
-  float wq[8], wk[8], dwq[8], dwk[8];
-  load_weight<F32>(p, lane_on ? p.wq : nullptr, l, wq);
-  load_weight<F32>(p, lane_on ? p.wk : nullptr, l, wk);
+  Lane a = lane_of<LPR>(p);
+  float2 wq[4], wk[4], dwq[4], dwk[4];
+  load_weight<F32>(p, p.wq, a, wq);
+  load_weight<F32>(p, p.wk, a, wk);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) dwq[j] = dwk[j] = 0.f;
+  for (int j = 0; j < 4; ++j) dwq[j] = dwk[j] = make_float2(0.f, 0.f);
   const long long items = p.tokens * p.split;
   const int steps = (heads + p.split - 1) / p.split;
   // i0: the CTA's first group, the same for all of its warps
@@ -225,68 +236,81 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkParams p) {
        i0 += static_cast<long long>(gridDim.x) * kGroups) {
     const long long item = i0 + threadIdx.x / LPR;
     const long long token = item / p.split;
-    const int g = static_cast<int>(item % p.split);
-    const bool valid = item < items && lane_on;
-    const int b = static_cast<int>(token / p.T), t = static_cast<int>(token % p.T);
-    Angles a;
-    load_angles(p, token, l, valid, a);
-    for (int s0 = 0; s0 < steps; s0 += U) {
-      Raw<F32, 8> rx[U];
-      Raw<G32, 8> ry[U];
+    const int g = static_cast<int>(item - token * p.split);
+    const bool valid = item < items && a.on;
+    const int b = static_cast<int>(token / p.T), t = static_cast<int>(token - static_cast<long long>(b) * p.T);
+    const long long qrow = b * p.qb + t * p.qt, krow = b * p.kb + t * p.kt;
+    RawRow<F32> nx[U];
+    RawRow<G32> ny[U];
+    auto load = [&](int s0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int h = g + (s0 + u) * p.split;
-        rx[u] = raw_zero<F32, 8>();
-        ry[u] = raw_zero<G32, 8>();
-        if (valid && h < heads) {
-          rx[u] = load_row<F32>(p, b, t, h, l);
-          const size_t at = out_at(p, token, h, l);
-          if (in_range(p.status, at, 8, out_extent(p, h), CHK_QK_IN))
-            ry[u] = raw_load<G32, 8>(static_cast<const G*>(h < p.Nq ? p.dqo : p.dko) + at);
+        nx[u] = row_zero<F32>();
+        ny[u] = row_zero<G32>();
+        if (valid && h < heads && in_range(p.status, t, 1, p.T, CHK_QK_IN)) {
+          nx[u] = row_load<F32>(in_row<F32>(p, qrow, krow, h), a);
+          const size_t at = out_at(p, token, h);
+          if (out_ok(p, at, h, CHK_QK_IN))
+            ny[u] = row_load<G32>(static_cast<const G*>(h < p.Nq ? p.dqo : p.dko) + at, a);
         }
       }
+    };
+    load(0);
+    load_angles<LPR>(p, token, t, valid, a);
+    for (int s0 = 0; s0 < steps; s0 += U) {
+      RawRow<F32> rx[U];
+      RawRow<G32> ry[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        rx[u] = nx[u];
+        ry[u] = ny[u];
+      }
+      if (s0 + U < steps) load(s0 + U);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (s0 + u >= steps) break;
         const int h = g + (s0 + u) * p.split;
         const bool on = valid && h < heads, isq = h < p.Nq;
-        float x[8], y[8], du[8], ss = 0.f;
-        raw_unpack<F32, 8>(rx[u], x);
-        raw_unpack<G32, 8>(ry[u], y);
-        rotate(p, a, -1.f, LPR, y, du);
+        float2 x[4], du[4];
+        row_unpack<F32>(rx[u], x);
+        row_unpack<G32>(ry[u], du);
+        rotate<-1>(p, a, du);
+        const float2 ss = fma2(x[0], x[0], fma2(x[1], x[1], fma2(x[2], x[2], mul2(x[3], x[3]))));
+        const float rs = rsqrtf(row_sum<LPR>(ss.x + ss.y) * inv_k + p.eps);
+        float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-        const float rs = rsqrtf(row_sum<LPR>(ss) * inv_k + p.eps);
-        float dot = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[j] *= rs;  // xh
-          if (on) {    // a head that is not there has x = 0 and, for eps = 0, xh = NaN
+        for (int j = 0; j < 4; ++j) {
+          x[j] = mul2(x[j], both(rs));  // xh
+          if (on) {  // a head that is not there has x = 0 and, for eps = 0, xh = NaN
             if (isq)
-              dwq[j] = fmaf(du[j], x[j], dwq[j]);
+              dwq[j] = fma2(du[j], x[j], dwq[j]);
             else
-              dwk[j] = fmaf(du[j], x[j], dwk[j]);
+              dwk[j] = fma2(du[j], x[j], dwk[j]);
           }
-          du[j] *= isq ? wq[j] : wk[j];  // g
-          dot = fmaf(du[j], x[j], dot);
+          du[j] = mul2(du[j], isq ? wq[j] : wk[j]);  // g
+          dot = fma2(du[j], x[j], dot);
         }
         // Lanes past the row's end hold zeros, or NaN times zero when eps = 0:
         // they must not enter the row's sum.
-        dot = row_sum<LPR>(lane_on ? dot : 0.f) * inv_k;
+        const float2 mean = both(-row_sum<LPR>(a.on ? dot.x + dot.y : 0.f) * inv_k);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = rs * fmaf(-x[j], dot, du[j]);
-        if (on) {
-          const size_t at = out_at(p, token, h, l);
-          if (in_range(p.status, at, 8, out_extent(p, h), CHK_QK_OUT))
-            store_vec<F32, 8>(static_cast<E*>(isq ? p.dq : p.dk) + at, y);
-        }
+        for (int j = 0; j < 4; ++j) du[j] = mul2(both(rs), fma2(x[j], mean, du[j]));
+        const size_t at = out_at(p, token, h);
+        if (on && out_ok(p, at, h, CHK_QK_OUT))
+          row_store<F32>(static_cast<E*>(isq ? p.dq : p.dk) + at, a, du);
       }
     }
   }
+  if (a.on) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    sums[0][threadIdx.x / LPR][8 * l + j] = dwq[j];
-    sums[1][threadIdx.x / LPR][8 * l + j] = dwk[j];
+    for (int j = 0; j < 4; ++j) {
+      const int f = a.o[j / 2] + 2 * (j & 1), grp = threadIdx.x / LPR;
+      sums[0][grp][f] = dwq[j].x;
+      sums[0][grp][f + 1] = dwq[j].y;
+      sums[1][grp][f] = dwk[j].x;
+      sums[1][grp][f + 1] = dwk[j].y;
+    }
   }
   __syncthreads();
   for (int e = threadIdx.x; e < 2 * p.K; e += kThreads) {
@@ -350,15 +374,16 @@ int qk_split(const m2rnn_qk_shape* s) {
   return static_cast<int>(want < 1 ? 1 : want > heads ? heads : want);
 }
 
+// CTAs of the gradient kernel: two resident ones for each of 152 SMs, so that the
+// groups keep their sums of dw through many tokens.
 int qk_bwd_parts(const m2rnn_qk_shape* s) {
   const long long groups = static_cast<long long>(s->B) * s->T * qk_split(s);
   const long long per_cta = kThreads / lanes_per_row(s->K);
   const long long need = (groups + per_cta - 1) / per_cta;
-  return static_cast<int>(need < 152 * 4 ? need : 152 * 4);
+  return static_cast<int>(need < 152 * 2 ? need : 152 * 2);
 }
 
-cudaError_t launch_qk_fwd(const QkParams& p, bool f32, int sms, cudaStream_t st) {
-  (void)sms;
+cudaError_t launch_qk_fwd(const QkParams& p, bool f32, cudaStream_t st) {
   if (f32) {
     M2RNN_QK_DISPATCH(fwd_l, true, p, st)
   }

@@ -24,8 +24,31 @@ struct Elem<false> {
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// VEC (4 or 8) consecutive elements as they lie in memory: 8 or 16 bytes of
-// bf16, 16 or 32 bytes of fp32.
+// Pairs of fp32 values in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// VEC (2, 4 or 8) consecutive elements as they lie in memory: 4, 8 or 16 bytes
+// of bf16, 8, 16 or 32 bytes of fp32.
 template <bool F32, int VEC>
 struct Raw {
   uint32_t w[F32 ? VEC : VEC / 2];
@@ -42,7 +65,9 @@ __device__ __forceinline__ Raw<F32, VEC> raw_zero() {
 template <bool F32, int VEC>
 __device__ __forceinline__ Raw<F32, VEC> raw_load(const typename Elem<F32>::T* src) {
   Raw<F32, VEC> r;
-  if constexpr (sizeof(r.w) == 8) {
+  if constexpr (sizeof(r.w) == 4) {
+    r.w[0] = __ldg(reinterpret_cast<const unsigned int*>(src));
+  } else if constexpr (sizeof(r.w) == 8) {
     const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
     r.w[0] = u.x;
     r.w[1] = u.y;
@@ -61,7 +86,9 @@ __device__ __forceinline__ Raw<F32, VEC> raw_load(const typename Elem<F32>::T* s
 
 template <bool F32, int VEC>
 __device__ __forceinline__ void raw_store(typename Elem<F32>::T* dst, const Raw<F32, VEC>& r) {
-  if constexpr (sizeof(r.w) == 8) {
+  if constexpr (sizeof(r.w) == 4) {
+    *reinterpret_cast<uint32_t*>(dst) = r.w[0];
+  } else if constexpr (sizeof(r.w) == 8) {
     *reinterpret_cast<uint2*>(dst) = make_uint2(r.w[0], r.w[1]);
   } else {
 #pragma unroll
@@ -93,6 +120,25 @@ __device__ __forceinline__ Raw<F32, VEC> raw_pack(const float (&o)[VEC]) {
     for (int i = 0; i < VEC / 2; ++i) r.w[i] = ptx::pack_bf16x2(o[2 * i], o[2 * i + 1]);
   }
   return r;
+}
+
+// The same as pairs.
+template <bool F32, int VEC>
+__device__ __forceinline__ void raw_unpack2(const Raw<F32, VEC>& r, float2 (&o)[VEC / 2]) {
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i)
+    o[i] = F32 ? make_float2(__uint_as_float(r.w[F32 ? 2 * i : 0]), __uint_as_float(r.w[F32 ? 2 * i + 1 : 0]))
+               : make_float2(ptx::bf16x2_lo(r.w[F32 ? 0 : i]), ptx::bf16x2_hi(r.w[F32 ? 0 : i]));
+}
+template <bool F32, int VEC>
+__device__ __forceinline__ Raw<F32, VEC> raw_pack2(const float2 (&o)[VEC / 2]) {
+  float t[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) {
+    t[2 * i] = o[i].x;
+    t[2 * i + 1] = o[i].y;
+  }
+  return raw_pack<F32, VEC>(t);
 }
 
 template <bool F32, int VEC>

@@ -487,15 +487,45 @@ def _rows(t, lead: int) -> Rows:
     return Rows(batch, token)
 
 
+def _row_arg(t, lead: int):
+    """The ``m2rnn_rows`` argument of an input: None where it is contiguous."""
+    if t.is_contiguous() and t.is_cuda:
+        return None
+    return ctypes.byref(_rows(t, lead))
+
+
 def _at(t):
-    """Pointer of a tensor described by ``_rows`` (which checked its layout)."""
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    """Address of a tensor whose layout ``_row_arg`` or ``_rows`` checked."""
+    return None if t is None else t.data_ptr()
+
+
+def _addr(t):
+    """Address of a tensor that must be contiguous (``_ptr`` as a number)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("tensors passed to libm2rnn must be CUDA tensors")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libm2rnn must be contiguous")
+    return t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, t):
+    """Handle of ``stream``, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:  # a tenth of the time that building a Stream object takes
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _expect(name: str, t, shape, *dtypes):
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:  # (a torch.Size equals a tuple)
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
@@ -540,9 +570,9 @@ def conv_fwd(x, w, bias=None, state=None, *, silu: bool = True, want_state: bool
     so = out.get("state")
     if so is not None or want_state:
         so = _out(so, (B, W - 1, C), x.dtype, x.device, "state")
-    s, r = ConvShape(B, T, C, W, _dtype_code(x), 0, int(bool(silu))), _rows(x, 2)
-    rc = lib().m2rnn_conv_fwd(ctypes.byref(s), _at(x), ctypes.byref(r), _ptr(w), _ptr(bias),
-                              _ptr(state), _ptr(y), _ptr(so), _stream(stream))
+    s = ConvShape(B, T, C, W, _dtype_code(x), 0, int(bool(silu)))
+    rc = lib().m2rnn_conv_fwd(ctypes.byref(s), _at(x), _row_arg(x, 2), _addr(w), _addr(bias),
+                              _addr(state), _addr(y), _addr(so), _stream_of(stream, x))
     _check(rc, "m2rnn_conv_fwd")
     return y, so
 
@@ -561,7 +591,7 @@ def conv_bwd(x, w, dy, bias=None, state=None, dstate_out=None, *, silu: bool = T
     _expect("dstate_out", dstate_out, (B, W - 1, C), x.dtype)
     _expect("dy", dy, (B, T, C), torch.float32, x.dtype)
     s = ConvShape(B, T, C, W, _dtype_code(x), _grad_code(dy, x), int(bool(silu)))
-    r, out, dev, f32 = _rows(x, 2), dict(out or {}), x.device, torch.float32
+    out, dev, f32 = dict(out or {}), x.device, torch.float32
     g = {"dx": _out(out.get("dx"), (B, T, C), x.dtype, dev, "dx"),
          "dw": _out(out.get("dw"), (C, W), f32, dev, "dw"),
          "dbias": None if bias is None else _out(out.get("dbias"), (C,), f32, dev, "dbias")}
@@ -569,10 +599,10 @@ def conv_bwd(x, w, dy, bias=None, state=None, dstate_out=None, *, silu: bool = T
     if ds is not None or want_dstate:
         ds = _out(ds, (B, W - 1, C), x.dtype, dev, "dstate")
     ws = _workspace(workspace, int(lib().m2rnn_conv_bwd_workspace_size(ctypes.byref(s))), dev)
-    rc = lib().m2rnn_conv_bwd(ctypes.byref(s), _at(x), ctypes.byref(r), _ptr(w), _ptr(bias),
-                              _ptr(state), _ptr(dy), _ptr(dstate_out), _ptr(g["dx"]),
-                              _ptr(g["dw"]), _ptr(g["dbias"]), _ptr(ds), _ptr(ws), _nbytes(ws),
-                              _stream(stream))
+    rc = lib().m2rnn_conv_bwd(ctypes.byref(s), _at(x), _row_arg(x, 2), _addr(w), _addr(bias),
+                              _addr(state), _addr(dy), _addr(dstate_out), _addr(g["dx"]),
+                              _addr(g["dw"]), _addr(g["dbias"]), _addr(ds), _addr(ws), _nbytes(ws),
+                              _stream_of(stream, x))
     _check(rc, "m2rnn_conv_bwd")
     if ds is not None:
         g["dstate"] = ds
@@ -590,9 +620,9 @@ def conv_step(x, w, state, bias=None, *, silu: bool = True, state_out=None, y=No
     _expect("state", state, (B, W - 1, C), x.dtype)
     y = _out(y, (B, C), x.dtype, x.device, "y")
     so = _out(state_out, (B, W - 1, C), x.dtype, x.device, "state_out")
-    s, r = ConvShape(B, 1, C, W, _dtype_code(x), 0, int(bool(silu))), _rows(x, 1)
-    rc = lib().m2rnn_conv_step(ctypes.byref(s), _at(x), ctypes.byref(r), _ptr(w), _ptr(bias),
-                               _ptr(state), _ptr(y), _ptr(so), _stream(stream))
+    s = ConvShape(B, 1, C, W, _dtype_code(x), 0, int(bool(silu)))
+    rc = lib().m2rnn_conv_step(ctypes.byref(s), _at(x), _row_arg(x, 1), _addr(w), _addr(bias),
+                               _addr(state), _addr(y), _addr(so), _stream_of(stream, x))
     _check(rc, "m2rnn_conv_step")
     return y, so
 
@@ -615,9 +645,7 @@ def _qk_args(q, k, wq, wk, cos, sin, pos, interleaved, grad_code):
     _expect("wq", wq, (K,), q.dtype)
     _expect("wk", wk, (K,), q.dtype)
     s = QkShape(B, T, Nq, Nk, K, R, P, _dtype_code(q), grad_code, int(bool(interleaved)))
-    rq = _rows(q, 2)
-    rk = rq if k is None else _rows(k, 2)
-    return s, rq, rk
+    return s, _row_arg(q, 2), None if k is None else _row_arg(k, 2)
 
 
 def qk_norm_fwd(q, k, wq=None, wk=None, eps: float = 1e-6, *, cos=None, sin=None, pos=None,
@@ -634,10 +662,10 @@ def qk_norm_fwd(q, k, wq=None, wk=None, eps: float = 1e-6, *, cos=None, sin=None
     out = dict(out or {})
     qo = _out(out.get("q"), tuple(q.shape), q.dtype, q.device, "q")
     ko = None if k is None else _out(out.get("k"), tuple(k.shape), q.dtype, q.device, "k")
-    rc = lib().m2rnn_qk_norm_fwd(ctypes.byref(s), _at(q), ctypes.byref(rq), _at(k),
-                                 ctypes.byref(rk), _ptr(wq), _ptr(wk), ctypes.c_float(eps),
-                                 _ptr(cos), _ptr(sin), _ptr(pos), _ptr(qo), _ptr(ko),
-                                 _stream(stream))
+    rc = lib().m2rnn_qk_norm_fwd(ctypes.byref(s), _at(q), rq, _at(k), rk,
+                                  _addr(wq), _addr(wk), eps,
+                                 _addr(cos), _addr(sin), _addr(pos), _addr(qo), _addr(ko),
+                                 _stream_of(stream, q))
     _check(rc, "m2rnn_qk_norm_fwd")
     return qo, ko
 
@@ -659,29 +687,31 @@ def qk_norm_bwd(q, k, wq, wk, dqo, dko, eps: float = 1e-6, *, cos=None, sin=None
          "dwq": None if wq is None else _out(out.get("dwq"), (K,), torch.float32, dev, "dwq"),
          "dwk": None if wk is None else _out(out.get("dwk"), (K,), torch.float32, dev, "dwk")}
     ws = _workspace(workspace, int(lib().m2rnn_qk_norm_bwd_workspace_size(ctypes.byref(s))), dev)
-    rc = lib().m2rnn_qk_norm_bwd(ctypes.byref(s), _at(q), ctypes.byref(rq), _at(k),
-                                 ctypes.byref(rk), _ptr(wq), _ptr(wk), ctypes.c_float(eps),
-                                 _ptr(cos), _ptr(sin), _ptr(pos), _ptr(dqo), _ptr(dko),
-                                 _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dwq"]), _ptr(g["dwk"]),
-                                 _ptr(ws), _nbytes(ws), _stream(stream))
+    rc = lib().m2rnn_qk_norm_bwd(ctypes.byref(s), _at(q), rq, _at(k), rk,
+                                  _addr(wq), _addr(wk), eps,
+                                 _addr(cos), _addr(sin), _addr(pos), _addr(dqo), _addr(dko),
+                                 _addr(g["dq"]), _addr(g["dk"]), _addr(g["dwq"]), _addr(g["dwk"]),
+                                 _addr(ws), _nbytes(ws), _stream_of(stream, q))
     _check(rc, "m2rnn_qk_norm_bwd")
     return g
 
 
 def _scan_args(q, k, v, a, alpha, beta, w_r, lead: int):
     """Shape and rows of a scan call; q, k may lack the group dimension."""
-    if q.dim() == lead + 1:
-        q, k = q.unsqueeze(lead), k.unsqueeze(lead)
-    B, (Nq, K), (N, V) = q.shape[0], q.shape[lead:], v.shape[lead:]
-    T = q.shape[1] if lead == 2 else 1
-    first = (B, T) if lead == 2 else (B,)
-    _expect("k", k, (*first, Nq, K), q.dtype)
+    first = tuple(q.shape[:lead])
+    B, T = first if lead == 2 else (first[0], 1)
+    Nq, K = q.shape[lead:] if q.dim() == lead + 2 else (1, *q.shape[lead:])
+    N, V = v.shape[lead:]
+    _expect("k", k, q.shape, q.dtype)
     _expect("v", v, (*first, N, V), q.dtype)
     _expect("a", a, (*first, N), q.dtype)
     _expect("alpha", alpha, (N,), q.dtype)
     _expect("beta", beta, (N,), q.dtype)
     _expect("w_r", w_r, (N, V), q.dtype)
-    rows = ScanRows(_rows(q, lead), _rows(k, lead), _rows(v, lead), _rows(a, lead))
+    rows = None
+    if not all(t.is_contiguous() and t.is_cuda for t in (q, k, v, a)):
+        rows = ctypes.byref(ScanRows(_rows(q, lead), _rows(k, lead), _rows(v, lead),
+                                     _rows(a, lead)))
     return Shape(B, T, N, K, V, _dtype_code(q), 0, Nq), rows
 
 
@@ -711,9 +741,9 @@ def scan_fwd(q, k, v, a, alpha, beta, w_r=None, H0=None, *, want_HT: bool = True
         raise ValueError("saved is smaller than m2rnn_scan_saved_size")
     ws = _workspace(workspace, int(L.m2rnn_scan_fwd_workspace_size(ctypes.byref(s),
                                                                    int(saved is not None))), dev)
-    rc = L.m2rnn_scan_fwd(ctypes.byref(s), ctypes.byref(rows), _at(q), _at(k), _at(v), _at(a),
-                          _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(H0), _ptr(y), _ptr(HT),
-                          _ptr(saved), _ptr(ws), _nbytes(ws), _stream(stream))
+    rc = L.m2rnn_scan_fwd(ctypes.byref(s), rows, _at(q), _at(k), _at(v), _at(a),
+                          _addr(alpha), _addr(beta), _addr(w_r), _addr(H0), _addr(y), _addr(HT),
+                          _addr(saved), _addr(ws), _nbytes(ws), _stream_of(stream, q))
     _check(rc, "m2rnn_scan_fwd")
     return y, HT, saved
 
@@ -745,11 +775,11 @@ def scan_bwd(q, k, v, a, alpha, beta, dy, w_r=None, H0=None, dHT=None, *, saved=
         raise ValueError("saved is smaller than m2rnn_scan_saved_size")
     ws = _workspace(workspace, int(L.m2rnn_scan_bwd_workspace_size(ctypes.byref(s),
                                                                    int(saved is not None))), dev)
-    rc = L.m2rnn_scan_bwd(ctypes.byref(s), ctypes.byref(rows), _at(q), _at(k), _at(v), _at(a),
-                          _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(H0), _ptr(saved), _ptr(dy),
-                          _ptr(dHT), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["da"]),
-                          _ptr(g["dalpha"]), _ptr(g["dbeta"]), _ptr(g["dw_r"]), _ptr(dH0),
-                          _ptr(ws), _nbytes(ws), _stream(stream))
+    rc = L.m2rnn_scan_bwd(ctypes.byref(s), rows, _at(q), _at(k), _at(v), _at(a),
+                          _addr(alpha), _addr(beta), _addr(w_r), _addr(H0), _addr(saved), _addr(dy),
+                          _addr(dHT), _addr(g["dq"]), _addr(g["dk"]), _addr(g["dv"]), _addr(g["da"]),
+                          _addr(g["dalpha"]), _addr(g["dbeta"]), _addr(g["dw_r"]), _addr(dH0),
+                          _addr(ws), _nbytes(ws), _stream_of(stream, q))
     _check(rc, "m2rnn_scan_bwd")
     if dH0 is not None:
         g["dH0"] = dH0
@@ -767,9 +797,9 @@ def scan_step(q, k, v, a, alpha, beta, H, w_r=None, *, H_out=None, y=None, strea
     _expect("H", H, state, torch.float32)
     H_out = _out(H_out, state, torch.float32, q.device, "H_out")
     y = _out(y, (s.B, s.N, s.V), q.dtype, q.device, "y")
-    rc = lib().m2rnn_scan_step(ctypes.byref(s), ctypes.byref(rows), _at(q), _at(k), _at(v),
-                               _at(a), _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(H), _ptr(H_out),
-                               _ptr(y), _stream(stream))
+    rc = lib().m2rnn_scan_step(ctypes.byref(s), rows, _at(q), _at(k), _at(v),
+                               _at(a), _addr(alpha), _addr(beta), _addr(w_r), _addr(H), _addr(H_out),
+                               _addr(y), _stream_of(stream, q))
     _check(rc, "m2rnn_scan_step")
     return y, H_out
 

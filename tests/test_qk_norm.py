@@ -83,7 +83,7 @@ def rel(got, ref):
 
 SHAPES = [(1, 1, 1, 1, 16, 16), (2, 3, 1, 1, 64, 64), (1, 5, 3, 1, 128, 32), (2, 7, 8, 2, 64, 0),
           (3, 17, 4, 4, 16, 8), (1, 33, 6, 3, 32, 16), (2, 9, 2, 1, 96, 64), (1, 4, 5, 0, 80, 16),
-          (1, 40, 2, 2, 256, 256), (1, 300, 16, 16, 64, 48), (2, 2, 1, 1, 8, 8)]
+          (1, 40, 2, 2, 256, 256), (1, 300, 16, 16, 64, 48), (2, 2, 1, 1, 8, 8), (1, 6, 3, 2, 64, 24), (1, 3, 2, 1, 104, 40)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -239,7 +239,7 @@ def test_refusals(m2rnn):
 
     assert code(lambda: m2rnn.qk_norm_fwd(*a, -1.0, **rot)) == -1
     assert code(lambda: m2rnn.qk_norm_fwd(*a, float("nan"), **rot)) == -1
-    c12 = torch.ones(50, 12, device="cuda")                       # R = 24
+    c12 = torch.ones(50, 10, device="cuda")                       # R = 20
     assert code(lambda: m2rnn.qk_norm_fwd(*a, EPS, cos=c12, sin=c12, pos=d["pos"])) == -2
     c64 = torch.ones(50, 64, device="cuda")                       # R > K
     assert code(lambda: m2rnn.qk_norm_fwd(*a, EPS, cos=c64, sin=c64, pos=d["pos"])) == -2
