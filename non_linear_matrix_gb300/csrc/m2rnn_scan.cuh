@@ -38,6 +38,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "m2rnn_block.h"
@@ -165,6 +166,21 @@ __device__ __forceinline__ void mma_terms_n(float (&acc)[N][4], const uint32_t (
 #pragma unroll
         for (int n = 0; n < N; ++n) ptx::mma_bf16_16816(acc[n], a[i], b[n][j][0], b[n][j][1]);
     }
+}
+
+// Lets a kernel take `bytes` of dynamic shared memory: asked once per kernel
+// and device.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done{0};  // by device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // ---- tiles ------------------------------------------------------------------

@@ -699,11 +699,10 @@ template <bool F32, int KT, int V>
 cudaError_t launch_bwd_kt(const ScanParams& p, cudaStream_t st) {
   constexpr int bytes = BwdSmem<F32, KT, V>::bytes;
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
-  auto kern = bwd_kernel<F32, KT, V>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e = allow_smem<bwd_kernel<F32, KT, V>>(bytes);
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(p.B) * p.Nq * p.hsplit * p.nc;
-  kern<<<static_cast<unsigned>(grid), 2 * kThreads, bytes, st>>>(p);
+  bwd_kernel<F32, KT, V><<<static_cast<unsigned>(grid), 2 * kThreads, bytes, st>>>(p);
   return cudaGetLastError();
 }
 

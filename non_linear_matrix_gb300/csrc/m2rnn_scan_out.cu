@@ -264,13 +264,10 @@ template <bool F32, int KT, int V>
 cudaError_t run(const ScanParams& p, cudaStream_t st) {
   constexpr int smem = OutSmem<F32, KT, V>::bytes;
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
-  auto kern = out_kernel<F32, KT, V>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_smem<out_kernel<F32, KT, V>>(smem);
+  if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(p.B) * p.Nq * p.hsplit * p.nc;
-  kern<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(p);
+  out_kernel<F32, KT, V><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -274,12 +274,9 @@ cudaError_t run(const ScanParams& p, cudaStream_t st) {
   constexpr int P = Terms<F32>::in, K = 8 * KT;
   constexpr int smem = 4 * kChunk * 4 + 2 * P * kChunk * (K + 8 + kVLd) * 2;
   const long long pairs = static_cast<long long>(p.B) * p.Nq * p.nhb;
-  auto kern = states_kernel<F32, KT, REV>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  kern<<<static_cast<unsigned>(pairs * p.nseg), kThreads, smem, st>>>(p);
+  const cudaError_t e = allow_smem<states_kernel<F32, KT, REV>>(smem);
+  if (e != cudaSuccess) return e;
+  states_kernel<F32, KT, REV><<<static_cast<unsigned>(pairs * p.nseg), kThreads, smem, st>>>(p);
   if (p.nseg > 1)
     for (long long y0 = 0; y0 < pairs; y0 += 65535)  // (nseg > 1 means few pairs: one launch)
       join_kernel<<<dim3((kCols * K / 4 + 255) / 256, static_cast<unsigned>(pairs - y0 < 65535 ? pairs - y0 : 65535)),

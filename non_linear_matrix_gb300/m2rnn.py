@@ -476,15 +476,15 @@ def _rows(t, lead: int) -> Rows:
     are batch (and token) and whose remaining ones are packed."""
     if not t.is_cuda:
         raise ValueError("tensors passed to libm2rnn must be CUDA tensors")
-    inner = 1
-    for size, st in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
-        if size != 1 and st != inner:
+    shape, st, inner = t.shape, t.stride(), 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if st[i] != inner and shape[i] != 1:
             raise ValueError("the dimensions after the token must be packed")
-        inner *= size
-    token = t.stride(1) if lead == 2 and t.shape[1] > 1 else inner
-    tokens = t.shape[1] if lead == 2 else 1
-    batch = t.stride(0) if t.shape[0] > 1 else token * tokens
-    return Rows(batch, token)
+        inner *= shape[i]
+    if lead == 1:
+        return Rows(st[0] if shape[0] > 1 else inner, inner)
+    token = st[1] if shape[1] > 1 else inner
+    return Rows(st[0] if shape[0] > 1 else token * shape[1], token)
 
 
 def _row_arg(t, lead: int):
@@ -500,14 +500,13 @@ def _at(t):
 
 
 def _addr(t):
-    """Address of a tensor that must be contiguous (``_ptr`` as a number)."""
+    """Address of a tensor that must be contiguous; that it is device memory
+    the library checks (M2RNN_ERR_POINTER)."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("tensors passed to libm2rnn must be CUDA tensors")
-    if not t.is_contiguous():
-        raise ValueError("tensors passed to libm2rnn must be contiguous")
-    return t.data_ptr()
+    if t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("tensors passed to libm2rnn must be contiguous")
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -529,6 +528,19 @@ def _expect(name: str, t, shape, *dtypes):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+
+
+def _expect_all(dtype, *specs):
+    """``_expect`` for (name, tensor, shape) triples of one dtype; cheap when
+    they are right."""
+    for name, t, shape in specs:
+        if t is not None and (t.dtype is not dtype or t.shape != shape):
+            _expect(name, t, shape, dtype)
+
+
+def _given(out, *names):
+    """The named outputs that the caller supplied (None where not)."""
+    return [None] * len(names) if out is None else [out.get(n) for n in names]
 
 
 def _out(t, shape, dtype, device, name: str = "out"):
@@ -560,14 +572,10 @@ def conv_fwd(x, w, bias=None, state=None, *, silu: bool = True, want_state: bool
     x [B,T,C] (its rows may be a slice of a wider buffer); w [C,W], W = 2..4;
     bias [C] or None; state [B,W-1,C], the inputs before the call, or None
     for zeros; one dtype (bf16 or f32).  ``out`` may supply y and state."""
-    B, T, C = x.shape
-    W = w.shape[1]
-    _expect("w", w, (C, W), x.dtype)
-    _expect("bias", bias, (C,), x.dtype)
-    _expect("state", state, (B, W - 1, C), x.dtype)
-    out = dict(out or {})
-    y = _out(out.get("y"), (B, T, C), x.dtype, x.device, "y")
-    so = out.get("state")
+    (B, T, C), W = x.shape, w.shape[1]
+    _expect_all(x.dtype, ("w", w, (C, W)), ("bias", bias, (C,)), ("state", state, (B, W - 1, C)))
+    y, so = _given(out, "y", "state")
+    y = _out(y, (B, T, C), x.dtype, x.device, "y")
     if so is not None or want_state:
         so = _out(so, (B, W - 1, C), x.dtype, x.device, "state")
     s = ConvShape(B, T, C, W, _dtype_code(x), 0, int(bool(silu)))
@@ -583,19 +591,15 @@ def conv_bwd(x, w, dy, bias=None, state=None, dstate_out=None, *, silu: bool = T
     is float32 or of x's dtype; dstate_out [B,W-1,C] is the gradient of the
     returned state (None = 0).  dx and dstate have x's dtype, dw and dbias
     are fp32 (dbias None without a bias)."""
-    B, T, C = x.shape
-    W = w.shape[1]
-    _expect("w", w, (C, W), x.dtype)
-    _expect("bias", bias, (C,), x.dtype)
-    _expect("state", state, (B, W - 1, C), x.dtype)
-    _expect("dstate_out", dstate_out, (B, W - 1, C), x.dtype)
+    (B, T, C), W = x.shape, w.shape[1]
+    _expect_all(x.dtype, ("w", w, (C, W)), ("bias", bias, (C,)), ("state", state, (B, W - 1, C)),
+                ("dstate_out", dstate_out, (B, W - 1, C)))
     _expect("dy", dy, (B, T, C), torch.float32, x.dtype)
     s = ConvShape(B, T, C, W, _dtype_code(x), _grad_code(dy, x), int(bool(silu)))
-    out, dev, f32 = dict(out or {}), x.device, torch.float32
-    g = {"dx": _out(out.get("dx"), (B, T, C), x.dtype, dev, "dx"),
-         "dw": _out(out.get("dw"), (C, W), f32, dev, "dw"),
-         "dbias": None if bias is None else _out(out.get("dbias"), (C,), f32, dev, "dbias")}
-    ds = out.get("dstate")
+    dev, f32 = x.device, torch.float32
+    dx, dw, db, ds = _given(out, "dx", "dw", "dbias", "dstate")
+    g = {"dx": _out(dx, (B, T, C), x.dtype, dev, "dx"), "dw": _out(dw, (C, W), f32, dev, "dw"),
+         "dbias": None if bias is None else _out(db, (C,), f32, dev, "dbias")}
     if ds is not None or want_dstate:
         ds = _out(ds, (B, W - 1, C), x.dtype, dev, "dstate")
     ws = _workspace(workspace, int(lib().m2rnn_conv_bwd_workspace_size(ctypes.byref(s))), dev)
@@ -613,11 +617,8 @@ def conv_step(x, w, state, bias=None, *, silu: bool = True, state_out=None, y=No
     """One token of the convolution for B sequences: x [B,C], state
     [B,W-1,C].  Returns (y, state_out); pass ``state_out=state`` to update
     the state in place."""
-    B, C = x.shape
-    W = w.shape[1]
-    _expect("w", w, (C, W), x.dtype)
-    _expect("bias", bias, (C,), x.dtype)
-    _expect("state", state, (B, W - 1, C), x.dtype)
+    (B, C), W = x.shape, w.shape[1]
+    _expect_all(x.dtype, ("w", w, (C, W)), ("bias", bias, (C,)), ("state", state, (B, W - 1, C)))
     y = _out(y, (B, C), x.dtype, x.device, "y")
     so = _out(state_out, (B, W - 1, C), x.dtype, x.device, "state_out")
     s = ConvShape(B, 1, C, W, _dtype_code(x), 0, int(bool(silu)))
@@ -627,23 +628,30 @@ def conv_step(x, w, state, bias=None, *, silu: bool = True, state_out=None, y=No
     return y, so
 
 
+def _bad_qk():
+    raise ValueError("q must be [B,T,Nq,K] and k [B,T,Nk,K]")
+
+
 def _qk_args(q, k, wq, wk, cos, sin, pos, interleaved, grad_code):
     """Shape, rows and checked arguments shared by both directions."""
-    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or
-                                           k.shape[3] != q.shape[3])):
-        raise ValueError("q must be [B,T,Nq,K] and k [B,T,Nk,K]")
-    if k is not None and k.dtype != q.dtype:
-        raise TypeError("q and k must share one dtype")
-    B, T, Nq, K = q.shape
-    Nk = 0 if k is None else k.shape[2]
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin come together")
-    R, P = (0, 0) if cos is None else (2 * cos.shape[1], cos.shape[0])
-    _expect("cos", cos, (P, R // 2), torch.float32)
-    _expect("sin", sin, (P, R // 2), torch.float32)
-    _expect("pos", pos, (B, T), torch.int32)
-    _expect("wq", wq, (K,), q.dtype)
-    _expect("wk", wk, (K,), q.dtype)
+    B, T, Nq, K = q.shape if q.dim() == 4 else _bad_qk()
+    Nk = 0
+    if k is not None:
+        if k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != K:
+            _bad_qk()
+        if k.dtype is not q.dtype:
+            raise TypeError("q and k must share one dtype")
+        Nk = k.shape[2]
+    R = P = 0
+    if cos is not None or sin is not None:
+        if cos is None or sin is None:
+            raise ValueError("cos and sin come together")
+        P, half = cos.shape
+        R = 2 * half
+        _expect_all(torch.float32, ("cos", cos, (P, half)), ("sin", sin, (P, half)))
+    if pos is not None:
+        _expect("pos", pos, (B, T), torch.int32)
+    _expect_all(q.dtype, ("wq", wq, (K,)), ("wk", wk, (K,)))
     s = QkShape(B, T, Nq, Nk, K, R, P, _dtype_code(q), grad_code, int(bool(interleaved)))
     return s, _row_arg(q, 2), None if k is None else _row_arg(k, 2)
 
@@ -659,9 +667,9 @@ def qk_norm_fwd(q, k, wq=None, wk=None, eps: float = 1e-6, *, cos=None, sin=None
     (2i, 2i+1) instead of (i, i + R/2).  A position outside the table gives
     NaN and sets M2RNN_ERR_BOUNDS in the device status."""
     s, rq, rk = _qk_args(q, k, wq, wk, cos, sin, pos, interleaved, 0)
-    out = dict(out or {})
-    qo = _out(out.get("q"), tuple(q.shape), q.dtype, q.device, "q")
-    ko = None if k is None else _out(out.get("k"), tuple(k.shape), q.dtype, q.device, "k")
+    qo, ko = _given(out, "q", "k")
+    qo = _out(qo, q.shape, q.dtype, q.device, "q")
+    ko = None if k is None else _out(ko, k.shape, q.dtype, q.device, "k")
     rc = lib().m2rnn_qk_norm_fwd(ctypes.byref(s), _at(q), rq, _at(k), rk,
                                   _addr(wq), _addr(wk), eps,
                                  _addr(cos), _addr(sin), _addr(pos), _addr(qo), _addr(ko),
@@ -676,16 +684,17 @@ def qk_norm_bwd(q, k, wq, wk, dqo, dko, eps: float = 1e-6, *, cos=None, sin=None
     float32 or of q's dtype, dq and dk have q's dtype, dwq and dwk [K] are
     fp32 (None without that weight)."""
     s, rq, rk = _qk_args(q, k, wq, wk, cos, sin, pos, interleaved, _grad_code(dqo, q))
-    _expect("dqo", dqo, tuple(q.shape), torch.float32, q.dtype)
+    _expect("dqo", dqo, q.shape, torch.float32, q.dtype)
     if (k is None) != (dko is None):
         raise ValueError("dko goes with k")
     if k is not None:
-        _expect("dko", dko, tuple(k.shape), dqo.dtype)
-    out, dev, K = dict(out or {}), q.device, q.shape[3]
-    g = {"dq": _out(out.get("dq"), tuple(q.shape), q.dtype, dev, "dq"),
-         "dk": None if k is None else _out(out.get("dk"), tuple(k.shape), q.dtype, dev, "dk"),
-         "dwq": None if wq is None else _out(out.get("dwq"), (K,), torch.float32, dev, "dwq"),
-         "dwk": None if wk is None else _out(out.get("dwk"), (K,), torch.float32, dev, "dwk")}
+        _expect("dko", dko, k.shape, dqo.dtype)
+    dev, K = q.device, q.shape[3]
+    dq, dk, dwq, dwk = _given(out, "dq", "dk", "dwq", "dwk")
+    g = {"dq": _out(dq, q.shape, q.dtype, dev, "dq"),
+         "dk": None if k is None else _out(dk, k.shape, q.dtype, dev, "dk"),
+         "dwq": None if wq is None else _out(dwq, (K,), torch.float32, dev, "dwq"),
+         "dwk": None if wk is None else _out(dwk, (K,), torch.float32, dev, "dwk")}
     ws = _workspace(workspace, int(lib().m2rnn_qk_norm_bwd_workspace_size(ctypes.byref(s))), dev)
     rc = lib().m2rnn_qk_norm_bwd(ctypes.byref(s), _at(q), rq, _at(k), rk,
                                   _addr(wq), _addr(wk), eps,
@@ -702,14 +711,11 @@ def _scan_args(q, k, v, a, alpha, beta, w_r, lead: int):
     B, T = first if lead == 2 else (first[0], 1)
     Nq, K = q.shape[lead:] if q.dim() == lead + 2 else (1, *q.shape[lead:])
     N, V = v.shape[lead:]
-    _expect("k", k, q.shape, q.dtype)
-    _expect("v", v, (*first, N, V), q.dtype)
-    _expect("a", a, (*first, N), q.dtype)
-    _expect("alpha", alpha, (N,), q.dtype)
-    _expect("beta", beta, (N,), q.dtype)
-    _expect("w_r", w_r, (N, V), q.dtype)
+    _expect_all(q.dtype, ("k", k, q.shape), ("v", v, (*first, N, V)), ("a", a, (*first, N)),
+                ("alpha", alpha, (N,)), ("beta", beta, (N,)), ("w_r", w_r, (N, V)))
     rows = None
-    if not all(t.is_contiguous() and t.is_cuda for t in (q, k, v, a)):
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and a.is_contiguous()
+            and q.is_cuda):
         rows = ctypes.byref(ScanRows(_rows(q, lead), _rows(k, lead), _rows(v, lead),
                                      _rows(a, lead)))
     return Shape(B, T, N, K, V, _dtype_code(q), 0, Nq), rows
@@ -728,9 +734,8 @@ def scan_fwd(q, k, v, a, alpha, beta, w_r=None, H0=None, *, want_HT: bool = True
     s, rows = _scan_args(q, k, v, a, alpha, beta, w_r, 2)
     state, dev = (s.B, s.N, s.K, s.V), q.device
     _expect("H0", H0, state, torch.float32)
-    out = dict(out or {})
-    y = _out(out.get("y"), (s.B, s.T, s.N, s.V), q.dtype, dev, "y")
-    HT, saved = out.get("HT"), out.get("saved")
+    y, HT, saved = _given(out, "y", "HT", "saved")
+    y = _out(y, v.shape, q.dtype, dev, "y")
     if HT is not None or want_HT:
         HT = _out(HT, state, torch.float32, dev, "HT")
     L = lib()
@@ -757,18 +762,16 @@ def scan_bwd(q, k, v, a, alpha, beta, dy, w_r=None, H0=None, dHT=None, *, saved=
     states are computed again."""
     s, rows = _scan_args(q, k, v, a, alpha, beta, w_r, 2)
     state, dev, f32 = (s.B, s.N, s.K, s.V), q.device, torch.float32
-    _expect("H0", H0, state, f32)
-    _expect("dHT", dHT, state, f32)
-    _expect("dy", dy, (s.B, s.T, s.N, s.V), q.dtype)
-    out, L = dict(out or {}), lib()
-    g = {"dq": _out(out.get("dq"), tuple(q.shape), q.dtype, dev, "dq"),
-         "dk": _out(out.get("dk"), tuple(q.shape), q.dtype, dev, "dk"),
-         "dv": _out(out.get("dv"), (s.B, s.T, s.N, s.V), q.dtype, dev, "dv"),
-         "da": _out(out.get("da"), (s.B, s.T, s.N), q.dtype, dev, "da"),
-         "dalpha": _out(out.get("dalpha"), (s.N,), f32, dev, "dalpha"),
-         "dbeta": _out(out.get("dbeta"), (s.N,), f32, dev, "dbeta"),
-         "dw_r": None if w_r is None else _out(out.get("dw_r"), (s.N, s.V), f32, dev, "dw_r")}
-    dH0 = out.get("dH0")
+    _expect_all(f32, ("H0", H0, state), ("dHT", dHT, state))
+    _expect("dy", dy, v.shape, q.dtype)
+    L = lib()
+    dq, dk, dv, da, dal, dbe, dw, dH0 = _given(out, "dq", "dk", "dv", "da", "dalpha", "dbeta",
+                                               "dw_r", "dH0")
+    g = {"dq": _out(dq, q.shape, q.dtype, dev, "dq"), "dk": _out(dk, q.shape, q.dtype, dev, "dk"),
+         "dv": _out(dv, v.shape, q.dtype, dev, "dv"), "da": _out(da, a.shape, q.dtype, dev, "da"),
+         "dalpha": _out(dal, alpha.shape, f32, dev, "dalpha"),
+         "dbeta": _out(dbe, beta.shape, f32, dev, "dbeta"),
+         "dw_r": None if w_r is None else _out(dw, w_r.shape, f32, dev, "dw_r")}
     if dH0 is not None or want_dH0:
         dH0 = _out(dH0, state, f32, dev, "dH0")
     if saved is not None and saved.numel() < int(L.m2rnn_scan_saved_size(ctypes.byref(s))):
@@ -796,7 +799,7 @@ def scan_step(q, k, v, a, alpha, beta, H, w_r=None, *, H_out=None, y=None, strea
     state = (s.B, s.N, s.K, s.V)
     _expect("H", H, state, torch.float32)
     H_out = _out(H_out, state, torch.float32, q.device, "H_out")
-    y = _out(y, (s.B, s.N, s.V), q.dtype, q.device, "y")
+    y = _out(y, v.shape, q.dtype, q.device, "y")
     rc = lib().m2rnn_scan_step(ctypes.byref(s), rows, _at(q), _at(k), _at(v),
                                _at(a), _addr(alpha), _addr(beta), _addr(w_r), _addr(H), _addr(H_out),
                                _addr(y), _stream_of(stream, q))
