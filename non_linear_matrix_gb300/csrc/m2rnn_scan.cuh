@@ -402,12 +402,21 @@ __device__ __forceinline__ void put_state_row(uint32_t tile, int e, const float2
 // A chunk's gate values of the block's heads: [heads][3][64] floats.
 __device__ __forceinline__ void load_gate(int tid, uint32_t dst, const ScanParams& p, const Place& w,
                                           int c) {
-  for (int e = tid; e < w.heads * 48; e += kThreads) {
-    const int h = e / 48, o = (e - h * 48) * 4;
+  const int o = (tid & 63) * 4;  // 48 threads bring a head's 768 bytes
+  const size_t extent = static_cast<size_t>(p.B) * p.N * p.nc * 192;
+  if (o >= 192) return;
+  for (int h = tid >> 6; h < w.heads; h += kThreads / 64) {
     const size_t at = ((static_cast<size_t>(w.b) * p.N + w.head0 + h) * p.nc + c) * 192 + o;
-    if (in_range(p.status, at, 4, static_cast<size_t>(p.B) * p.N * p.nc * 192, CHK_SCAN_WS))
-      ptx::cp_async16(dst + (h * 192 + o) * 4, p.gate + at);
+    if (in_range(p.status, at, 4, extent, CHK_SCAN_WS)) ptx::cp_async16(dst + (h * 192 + o) * 4, p.gate + at);
   }
+}
+
+// Two neighbouring values (at an even place).
+template <bool F32>
+__device__ __forceinline__ float2 load_pair(const typename Elem<F32>::T* src) {
+  float2 o[1];
+  raw_unpack2<F32, 2>(raw_load<F32, 2>(src), o);
+  return o[0];
 }
 
 }  // namespace scan

@@ -45,41 +45,21 @@ struct BwdSmem {
   static constexpr int P = Terms<F32>::in, PS = Terms<F32>::state, K = 8 * KT, HB = kCols / V;
   static constexpr int key = P * kChunk * (K + 8) * 2, val = P * kChunk * kVLd * 2;
   static constexpr int state = PS * kCols * K * 2;
-  static constexpr int tri = 18 * 512;  // G, or the sum of E L: see tri_at
-  // D without its diagonal: column sums by row block (from column 16 w on), row
-  // sums; the diagonal
-  static constexpr int cols = 160 * HB, sums = (cols + 2 * HB * kChunk) * 4;
+  static constexpr int tri = 20 * 512;  // G, or the sum of E L: 8 - 2 rt tiles of row block rt
   static constexpr int q = 0, k = q + key, v = k + key, u = v + val, h = u + val;
   static constexpr int r = F32 ? h : h + state;  // fp32: R takes H's place
   static constexpr int KH = KT >= 4 ? 2 : 1;     // parts that the K columns are cut into
   static constexpr int g = r + state, f = g + tri;
   static constexpr int gate = f + (F32 ? 0 : tri);  // fp32 keeps the sum in registers
-  static constexpr int through = gate + HB * 192 * 4;       // Pin, Uin: [HB][64]
-  static constexpr int rh = through + 2 * HB * kChunk * 4;  // shares of <R, H>
-  static constexpr int chunk_sums = rh + 32 * 4;
-  static constexpr int bytes = chunk_sums + sums;
+  // Per head and token, from the first half of the K columns: Pin, Uin [HB][64];
+  // column sums of D without its diagonal by row block, from column 16 rt on;
+  // shares of <R, H>.  What else there is per head and token has its place in the
+  // 16 bytes behind the tiles' rows (see spare).
+  static constexpr int through = gate + HB * 192 * 4;
+  static constexpr int cols = through + 2 * HB * kChunk * 4;
+  static constexpr int rh = cols + 160 * HB * 4;
+  static constexpr int bytes = rh + 32 * 4;
 };
-
-// Where row block rt keeps column tile nt (2 rt on) of a j by i matrix, in floats: 4 per lane,
-// of the first tile only the upper 8 rows' 2 (below, i < j).
-__device__ __forceinline__ int tri_at(int rt, int nt) {
-  const int first = rt * (960 - 128 * (rt - 1));  // sum of 64 + 128 (7 - 2 r) over r < rt
-  return nt == 2 * rt ? first : first + 64 + 128 * (nt - 2 * rt - 1);
-}
-
-__device__ __forceinline__ float4 tri_load(const float* m, int rt, int nt) {
-  const int lane = threadIdx.x & 31;
-  if (nt != 2 * rt) return *reinterpret_cast<const float4*>(m + tri_at(rt, nt) + 4 * lane);
-  const float2 x = *reinterpret_cast<const float2*>(m + tri_at(rt, nt) + 2 * lane);
-  return make_float4(x.x, x.y, 0.f, 0.f);
-}
-__device__ __forceinline__ void tri_store(float* m, int rt, int nt, float4 x) {
-  const int lane = threadIdx.x & 31;
-  if (nt != 2 * rt)
-    *reinterpret_cast<float4*>(m + tri_at(rt, nt) + 4 * lane) = x;
-  else
-    *reinterpret_cast<float2*>(m + tri_at(rt, nt) + 2 * lane) = make_float2(x.x, x.y);
-}
 
 __device__ __forceinline__ float quad_sum(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 1);
@@ -105,15 +85,11 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
   const uint32_t base = ptx::smem_addr(smem);
   const uint32_t qs = base + S::q, ks = base + S::k, vs = base + S::v, us = base + S::u,
                  hs = base + S::h, rs = base + S::r;
-  float* gs = reinterpret_cast<float*>(smem + S::g);
-  float* fs = reinterpret_cast<float*>(smem + S::f);
   const float* gate = reinterpret_cast<const float*>(smem + S::gate);
   float* Pin = reinterpret_cast<float*>(smem + S::through);
   float* Uin = Pin + HB * kChunk;
   float* rh = reinterpret_cast<float*>(smem + S::rh);
-  float* Pcol = reinterpret_cast<float*>(smem + S::chunk_sums);  // see col_at
-  float* Urow = Pcol + S::cols;                                  // [HB][64]
-  float* Ddiag = Urow + HB * kChunk;                             // [HB][64]
+  float* Pcol = reinterpret_cast<float*>(smem + S::cols);  // see col_at
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c2 = (lane & 3) * 2;
   const int rt = row_block(warp & 3);                  // its 16 rows (the chunk's side)
   const bool sside = warp < 4;                         // the states' side
@@ -200,8 +176,13 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
       if (lane == 0) rh[e / 256] = s;
     }
   };
+  // The 16 bytes behind each row of a tile keep bank conflicts away and hold one
+  // value per head: the second half's shares of Pin (u) and Uin (v), the row
+  // sums of D without its diagonal (q) and the diagonal (k).
+  auto spare = [&](int tile, int width, int h, int row) {
+    return reinterpret_cast<float*>(smem + tile + (row * (width + 8) + width) * 2) + h;
+  };
   if (sside) {
-    for (int e = tid; e < 2 * HB * kChunk; e += kThreads) Pin[e] = 0.f;  // and Uin
     fetch_h(hb0, tid, kThreads);
     cp_async_wait<0>();
   } else {
@@ -225,8 +206,9 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
         for (int i = 0; i < 4; ++i) dq[m][nt][i] = dk[m][nt][i] = 0.f;
     // Through a state: out += scale_row (A state^T), and the rows' products with
     // `with`'s rows (q or k), for one head; scale[m]: of rows 16 m + g, + 8.
-    auto through = [&](uint32_t tile, uint32_t state, uint32_t with, int h, const float2 (&scale)[2],
+    auto through = [&](int tile_at, uint32_t state, uint32_t with, int h, const float2 (&scale)[2],
                        float (&out)[2][NK][4], float* sums) {
+      const uint32_t tile = base + tile_at;
       uint32_t a[2][V / 16][P][4];
 #pragma unroll
       for (int m = 0; m < 2; ++m)
@@ -262,10 +244,15 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const float y0 = quad_sum(d[m][0]) * scale[m].x, y1 = quad_sum(d[m][1]) * scale[m].y;
-        float* to = sums + h * kChunk + row0 + 16 * m + g;
-        if ((lane & 3) == 0) {  // at most two shares onto 0: their order does not matter
-          atomicAdd(to, y0);
-          atomicAdd(to + 8, y1);
+        const int r = row0 + 16 * m + g;
+        if ((lane & 3) == 0) {
+          if (n0 == 0) {
+            sums[h * kChunk + r] = y0;
+            sums[h * kChunk + r + 8] = y1;
+          } else {
+            *spare(tile_at, kCols, h, r) = y0;
+            *spare(tile_at, kCols, h, r + 8) = y1;
+          }
         }
       }
     };
@@ -307,7 +294,7 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
             sc[m] = make_float2(ex2(off + lo[row0 + 16 * m + g]), ex2(off + lo[row0 + 16 * m + g + 8]));
             off += lo[row0 + 15];
           }
-          through(us, hs, qs, h, sc, dq, Pin);
+          through(S::u, hs, qs, h, sc, dq, Pin);
         }
       }
       if constexpr (F32) {  // R in H's place
@@ -344,19 +331,21 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
             sc[m] = make_float2(lo[128 + row0 + 16 * m + g] * f, lo[128 + row0 + 16 * m + g + 8] * f);
             off += lo[row0 + 31];
           }
-          through(vs, rs, ks, h, sc, dk, Uin);
+          through(S::v, rs, ks, h, sc, dk, Uin);
         }
       }
       __syncthreads();  // done with it; the others' sums are there
       if (F32 && hb + 1 < hb1) fetch_h(hb + 1, tid, kThreads);
       if (warp < w.heads) {  // the gate: one warp per head, two tokens per lane
         const int h = warp, n = w.head0 + h, t = 2 * lane, blk = lane >> 3;
-        float2& us2 = *reinterpret_cast<float2*>(Uin + h * kChunk + t);
-        float2& ps2 = *reinterpret_cast<float2*>(Pin + h * kChunk + t);
-        const float2 ui = us2, dd = *reinterpret_cast<const float2*>(Ddiag + h * kChunk + t);
-        float2 pi = ps2;
-        us2 = ps2 = make_float2(0.f, 0.f);  // for the next head block
-        const float2 ur = *reinterpret_cast<const float2*>(Urow + h * kChunk + t);
+        float2 ui = *reinterpret_cast<const float2*>(Uin + h * kChunk + t);
+        float2 pi = *reinterpret_cast<const float2*>(Pin + h * kChunk + t);
+        if (KH == 2) {
+          ui = add2(ui, make_float2(*spare(S::v, kCols, h, t), *spare(S::v, kCols, h, t + 1)));
+          pi = add2(pi, make_float2(*spare(S::u, kCols, h, t), *spare(S::u, kCols, h, t + 1)));
+        }
+        const float2 dd = make_float2(*spare(S::k, K, h, t), *spare(S::k, K, h, t + 1));
+        const float2 ur = make_float2(*spare(S::q, K, h, t), *spare(S::q, K, h, t + 1));
 #pragma unroll
         for (int s = 0; s < 4; ++s)
           if (s <= blk) pi = add2(pi, *reinterpret_cast<const float2*>(Pcol + col_at(s, h, t)));
@@ -457,26 +446,32 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
     return;
   }
 
+  // Tile n of the row block (columns 16 rt + 8 n..) of G and of the sum of E L.
+  const int rb = 16 * rt;
+  float4* gt = reinterpret_cast<float4*>(smem + S::g) + rt * (9 - rt) * 32 + lane;
+  float4* ft = reinterpret_cast<float4*>(smem + S::f) + rt * (9 - rt) * 32 + lane;
   // G with j along the rows, for the tiles with i >= j
 #pragma unroll 1
-  for (int ib = rt; ib < 4; ++ib) {
+  for (int k4 = 0; rt + k4 < 4; ++k4) {
     float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kk = 0; kk < KT / 2; ++kk) {
       uint32_t a[P][4], b0[P][2], b1[P][2];
-      load_a<P>(a, ks, ld, 16 * rt, 16 * kk);
-      load_b2<P>(b0, b1, qs, ld, 16 * ib, 16 * kk);
+      load_a<P>(a, ks, ld, rb, 16 * kk);
+      load_b2<P>(b0, b1, qs, ld, rb + 16 * k4, 16 * kk);
       mma_terms<P, P>(x0, a, b0);
       mma_terms<P, P>(x1, a, b1);
     }
-    tri_store(gs, rt, 2 * ib, make_float4(x0[0], x0[1], x0[2], x0[3]));
-    tri_store(gs, rt, 2 * ib + 1, make_float4(x1[0], x1[1], x1[2], x1[3]));
-    if (!F32) {
-      tri_store(fs, rt, 2 * ib, make_float4(0.f, 0.f, 0.f, 0.f));
-      tri_store(fs, rt, 2 * ib + 1, make_float4(0.f, 0.f, 0.f, 0.f));
-    }
+    gt[64 * k4] = make_float4(x0[0], x0[1], x0[2], x0[3]);
+    gt[64 * k4 + 32] = make_float4(x1[0], x1[1], x1[2], x1[3]);
+    if (!F32) ft[64 * k4] = ft[64 * k4 + 32] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  float dsum[8][4];  // sum over heads of E L, rows j
+  E* dv_out = static_cast<E*>(p.dv) + ((static_cast<size_t>(b) * p.T + t0 + rb + g) * p.N +
+                                       static_cast<size_t>(group) * p.hpg) * V + c2;
+  const size_t dv_8 = 8 * static_cast<size_t>(p.N) * V;  // 8 rows further on
+  float* pcol = Pcol + HB * (rt * 64 - 8 * rt * (rt - 1)) + c2;
+  const int pcol_h = 64 - rb;
+  float dsum[8][4];  // sum over heads of E L, tile n (fp32)
 #pragma unroll
   for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
@@ -514,9 +509,9 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
 #pragma unroll 1
     for (int h = 0; h < w.heads; ++h) {
       const float* lo = gate + h * 192;
-      const int r0 = 16 * rt + g, r1 = r0 + 8;
-      const float end0 = lo[128 + r0], end1 = lo[128 + r1];  // 2^S(j, block's end) dt_j
-      float w0, w1;                                          // 2^S(j, end) dt_j
+      const float* lj = lo + rb + g;                   // of rows g; g + 8 further on the others
+      const float end0 = lj[128], end1 = lj[128 + 8];  // 2^S(j, block's end) dt_j
+      float w0, w1;                                    // 2^S(j, end) dt_j
       {
         float off = 0.f;
         for (int i4 = rt + 1; i4 < 4; ++i4) off += lo[16 * i4 + 15];
@@ -552,16 +547,18 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
 #pragma unroll
       for (int vv = 0; vv < V / 16; ++vv) load_a<P>(va[vv], vs, kVLd, 16 * rt, h * V + 16 * vv);
       float2 ur0 = make_float2(0.f, 0.f), ur1 = ur0;
+      float* ph = pcol + h * pcol_h;
+      const float* li_at = lo + rb + c2;
       float between = 0.f;  // sum of l over the blocks between j's and i's
 #pragma unroll
-      for (int ib = 0; ib < 4; ++ib) {
-        if (ib < rt) continue;
-        if (ib > rt + 1) between += lo[16 * ib - 1];
+      for (int k4 = 0; k4 < 4; ++k4) {  // columns i of block rt + k4
+        if (rt + k4 > 3) break;
+        if (k4 > 1) between += lo[rb + 16 * k4 - 1];
         float e[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int vv = 0; vv < V / 16; ++vv) {
           uint32_t b0[P][2], b1[P][2];
-          load_b2<P>(b0, b1, us, kVLd, 16 * ib, h * V + 16 * vv);
+          load_b2<P>(b0, b1, us, kVLd, rb + 16 * k4, h * V + 16 * vv);
           mma_terms<P, P>(e[0], va[vv], b0);
           mma_terms<P, P>(e[1], va[vv], b1);
         }
@@ -569,15 +566,15 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
         float2 dc[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int nt = 2 * ib + u;
-          const float2 li = *reinterpret_cast<const float2*>(lo + 8 * nt + c2);
-          const float4 g4 = tri_load(gs, rt, nt);
+          const int n = 2 * k4 + u;
+          const float2 li = *reinterpret_cast<const float2*>(li_at + 8 * n);
+          const float4 g4 = gt[32 * n];
           const float2 g0 = make_float2(g4.x, g4.y), g1 = make_float2(g4.z, g4.w);
           float2 l0, l1;
-          if (ib == rt) {
-            const float lj0 = lo[r0], lj1 = lo[r1];
-            l0 = mul2(make_float2(ex2(li.x - lj0), ex2(li.y - lj0)), both(lo[64 + r0]));
-            l1 = mul2(make_float2(ex2(li.x - lj1), ex2(li.y - lj1)), both(lo[64 + r1]));
+          if (k4 == 0) {
+            const float lj0 = lj[0], lj1 = lj[8];
+            l0 = mul2(make_float2(ex2(li.x - lj0), ex2(li.y - lj0)), both(lj[64]));
+            l1 = mul2(make_float2(ex2(li.x - lj1), ex2(li.y - lj1)), both(lj[64 + 8]));
             const int i = 8 * u + c2;  // i >= j
             l0.x = i >= g ? l0.x : 0.f;
             l0.y = i + 1 >= g ? l0.y : 0.f;
@@ -591,18 +588,18 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
           }
           const float2 f0 = mul2(pair(e[u], 0), l0), f1 = mul2(pair(e[u], 1), l1);
           if (F32) {
-            set_pair(dsum[nt], 0, add2(pair(dsum[nt], 0), f0));
-            set_pair(dsum[nt], 1, add2(pair(dsum[nt], 1), f1));
+            set_pair(dsum[n], 0, add2(pair(dsum[n], 0), f0));
+            set_pair(dsum[n], 1, add2(pair(dsum[n], 1), f1));
           } else {
-            const float4 s = tri_load(fs, rt, nt);
+            const float4 s = ft[32 * n];
             const float2 s0 = add2(make_float2(s.x, s.y), f0), s1 = add2(make_float2(s.z, s.w), f1);
-            tri_store(fs, rt, nt, make_float4(s0.x, s0.y, s1.x, s1.y));
+            ft[32 * n] = make_float4(s0.x, s0.y, s1.x, s1.y);
           }
           float2 d0 = mul2(f0, g0), d1 = mul2(f1, g1);
-          if (ib == rt) {  // the diagonal apart: row g in the first tile, g + 8 in the second
+          if (k4 == 0) {  // the diagonal apart: row g in the first tile, g + 8 in the second
             float2& d = u ? d1 : d0;
             if ((lane & 3) == (g >> 1)) {
-              Ddiag[h * kChunk + (u ? r1 : r0)] = (g & 1) ? d.y : d.x;
+              *spare(S::k, K, h, rb + g + 8 * u) = (g & 1) ? d.y : d.x;
               d = (g & 1) ? make_float2(d.x, 0.f) : make_float2(0.f, d.y);
             }
           }
@@ -621,7 +618,7 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
 #pragma unroll
         for (int nt = 0; nt < NT; nt += 2) {
           uint32_t b0[P][2], b1[P][2];
-          load_b2_t<P>(b0, b1, us, kVLd, 16 * ib, h * V + 8 * nt);
+          load_b2_t<P>(b0, b1, us, kVLd, rb + 16 * k4, h * V + 8 * nt);
           mma_terms<PO, P>(dv[nt], a, b0);
           mma_terms<PO, P>(dv[nt + 1], a, b1);
         }
@@ -633,39 +630,38 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
           float t = b3 ? s.y : s.x;
           t += __shfl_xor_sync(0xffffffffu, b3 ? s.x : s.y, 8);
           t += __shfl_xor_sync(0xffffffffu, t, 4);
-          if (!(lane & 4)) Pcol[col_at(rt, h, 16 * ib + (b4 ? 8 : 0) + c2 + (b3 ? 1 : 0))] = t;
+          if (!(lane & 4)) ph[16 * k4 + (b4 ? 8 : 0) + (b3 ? 1 : 0)] = t;
         }
       }
       const float u0 = quad_sum(ur0.x + ur0.y), u1 = quad_sum(ur1.x + ur1.y);
       if ((lane & 3) == 0) {
-        Urow[h * kChunk + r0] = u0;
-        Urow[h * kChunk + r1] = u1;
+        *spare(S::q, K, h, rb + g) = u0;
+        *spare(S::q, K, h, rb + g + 8) = u1;
       }
       // dv, with w_r (.) u
+      const int hv = (hb * HB + h) * V;
 #pragma unroll
       for (int nt = 0; nt < NT; nt += 2) {
         if (w_r != nullptr) {
           uint32_t x[P][4];
-          load_a<P>(x, us, kVLd, 16 * rt, h * V + 8 * nt);
+          load_a<P>(x, us, kVLd, rb, h * V + 8 * nt);
           const E* wr = w_r + static_cast<size_t>(w.head0 + h) * V + 8 * nt + c2;
+          const float2 wr0 = load_pair<F32>(wr), wr1 = load_pair<F32>(wr + 8);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             uint32_t t[P];
 #pragma unroll
             for (int s = 0; s < P; ++s) t[s] = x[s][r];
-            const float2 wv = make_float2(to_f32(wr[8 * (r >> 1)]), to_f32(wr[8 * (r >> 1) + 1]));
             float(&o)[4] = dv[nt + (r >> 1)];
-            set_pair(o, r & 1, fma2(wv, join<P>(t), pair(o, r & 1)));
+            set_pair(o, r & 1, fma2(r < 2 ? wr0 : wr1, join<P>(t), pair(o, r & 1)));
           }
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int row = (r & 1) ? r1 : r0;
-          const size_t at = ((static_cast<size_t>(b) * p.T + t0 + row) * p.N + w.head0 + h) * V +
-                            8 * (nt + (r >> 1)) + c2;
-          if (row < rows && in_range(p.status, at, 2, tok_extent * V, CHK_SCAN_OUT))
-            store2<F32>(static_cast<E*>(p.dv) + at, dv[nt + (r >> 1)][2 * (r & 1)],
-                        dv[nt + (r >> 1)][2 * (r & 1) + 1]);
+          E* dst = dv_out + ((r & 1) ? dv_8 : 0) + hv + 8 * (nt + (r >> 1));
+          if (rb + g + 8 * (r & 1) < rows &&
+              in_range(p.status, dst - static_cast<E*>(p.dv), 2, tok_extent * V, CHK_SCAN_OUT))
+            store2<F32>(dst, dv[nt + (r >> 1)][2 * (r & 1)], dv[nt + (r >> 1)][2 * (r & 1) + 1]);
         }
       }
     }
@@ -679,15 +675,15 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
   // by way of the v tile's place, [j][i], to the other side
   __syncthreads();
 #pragma unroll
-  for (int nt = 0; nt < 8; ++nt) {
-    if (nt < 2 * rt) continue;
-    const float4 f4 = F32 ? make_float4(dsum[nt][0], dsum[nt][1], dsum[nt][2], dsum[nt][3]) : tri_load(fs, rt, nt);
+  for (int n = 0; n < 8; ++n) {
+    if (2 * rt + n > 7) break;
+    const float4 f4 = F32 ? make_float4(dsum[n][0], dsum[n][1], dsum[n][2], dsum[n][3]) : ft[32 * n];
     uint32_t x0[PO], x1[PO];
     split<PO>(make_float2(f4.x, f4.y), x0);
     split<PO>(make_float2(f4.z, f4.w), x1);
 #pragma unroll
     for (int s = 0; s < PO; ++s) {
-      const uint32_t at = vs + s * kChunk * kVLd * 2 + ((16 * rt + g) * kVLd + 8 * nt + c2) * 2;
+      const uint32_t at = vs + s * kChunk * kVLd * 2 + ((rb + g) * kVLd + rb + 8 * n + c2) * 2;
       ptx::sts_u32(at, x0[s]);
       ptx::sts_u32(at + 8 * kVLd * 2, x1[s]);
     }

@@ -216,12 +216,13 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_ke
         uint32_t x[P][4];
         load_a<P>(x, vs, kVLd, 16 * rt, 8 * nt);
         const E* src = w_r + static_cast<size_t>(w.head0) * V + 8 * nt + c2;
+        const float2 wr0 = load_pair<F32>(src), wr1 = load_pair<F32>(src + 8);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           uint32_t t[P];
 #pragma unroll
           for (int s = 0; s < P; ++s) t[s] = x[s][r];
-          const float2 wr = make_float2(to_f32(src[8 * (r >> 1)]), to_f32(src[8 * (r >> 1) + 1]));
+          const float2 wr = r < 2 ? wr0 : wr1;
           set_pair(acc[nt + (r >> 1)], r & 1, fma2(wr, join<P>(t), pair(acc[nt + (r >> 1)], r & 1)));
         }
       }
@@ -246,13 +247,14 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_ke
     }
     if constexpr (!F32) {
       __syncwarp();  // the warp's own 16 rows, in 16-byte pieces
-      const int col = (lane & 7) * 8;
+      const int col = (lane & 7) * 8, r0 = 16 * rt + (lane >> 3);
+      size_t at = ((static_cast<size_t>(b) * p.T + t0 + r0) * p.N + w.head0) * V + col;
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        const int r = 16 * rt + it * 4 + (lane >> 3);
-        const size_t at = ((static_cast<size_t>(b) * p.T + t0 + r) * p.N + w.head0) * V + col;
+        const int r = r0 + 4 * it;
         if (r < rows && col < w.heads * V && in_range(p.status, at, 8, y_extent, CHK_SCAN_OUT))
           *reinterpret_cast<uint4*>(y + at) = ptx::lds_u32x4(ys + (r * kVLd + col) * 2);
+        at += 4 * static_cast<size_t>(p.N) * V;
       }
     }
     __syncthreads();  // v, the state and the gate may be overwritten
