@@ -297,6 +297,23 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
           through(S::u, hs, qs, h, sc, dq, Pin);
         }
       }
+      // dw_r: the diagonal of u^T v over the chunk, 16 columns per warp
+      if (w_r != nullptr && 16 * warp < w.heads * V) {
+        float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          uint32_t a[P][4], b0[P][2], b1[P][2];
+          load_a_t<P>(a, us, kVLd, 16 * s, 16 * warp);
+          load_b2_t<P>(b0, b1, vs, kVLd, 16 * s, 16 * warp);
+          mma_terms<P, P>(x0, a, b0);
+          mma_terms<P, P>(x1, a, b1);
+        }
+        const size_t at = 2 * static_cast<size_t>(p.N) + static_cast<size_t>(w.head0) * V + 16 * warp + g;
+        if ((lane & 3) == (g >> 1) && in_range(p.status, at, 9, part_extent, CHK_SCAN_PARAM)) {
+          part[at] = (g & 1) ? x0[1] : x0[0];
+          part[at + 8] = (g & 1) ? x1[3] : x1[2];
+        }
+      }
       if constexpr (F32) {  // R in H's place
         __syncthreads();
         __syncthreads();
@@ -488,23 +505,6 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
     if (hb + 1 < hb1) {
       const Place next = place_in(p, HB, b, group, hb + 1);
       state_prefetch(tid, ref_r(next), next.heads * V * K);
-    }
-    // dw_r: the diagonal of u^T v over the chunk, 16 columns per warp
-    if (w_r != nullptr && 16 * rt < w.heads * V) {
-      float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        uint32_t a[P][4], b0[P][2], b1[P][2];
-        load_a_t<P>(a, us, kVLd, 16 * s, 16 * rt);
-        load_b2_t<P>(b0, b1, vs, kVLd, 16 * s, 16 * rt);
-        mma_terms<P, P>(x0, a, b0);
-        mma_terms<P, P>(x1, a, b1);
-      }
-      const size_t at = 2 * static_cast<size_t>(p.N) + static_cast<size_t>(w.head0) * V + 16 * rt + g;
-      if ((lane & 3) == (g >> 1) && in_range(p.status, at, 9, part_extent, CHK_SCAN_PARAM)) {
-        part[at] = (g & 1) ? x0[1] : x0[0];
-        part[at + 8] = (g & 1) ? x1[3] : x1[2];
-      }
     }
 #pragma unroll 1
     for (int h = 0; h < w.heads; ++h) {

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(256) join_kernel(const ScanParams p, float* en
   const float* dec = cdec + static_cast<size_t>(p.B) * p.N * p.nc + head * p.nseg;
   const size_t extent = static_cast<size_t>(p.B) * groups * p.nseg * per;
   float4 s = *reinterpret_cast<const float4*>(own);
-  constexpr int U = 8;  // loads in flight
+  constexpr int U = 14;  // loads in flight
   for (int g0 = 1; g0 < p.nseg; g0 += U) {
     float4 x[U];
     float d[U];
