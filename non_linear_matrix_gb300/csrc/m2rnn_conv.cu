@@ -30,13 +30,21 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// sigmoid(z) from e = exp(-z): e = inf gives 0.
+// sigmoid(z) = 1 / (1 + e^-z); e^-z = inf gives 0.
 template <bool F32>
-__device__ __forceinline__ float sigmoid(float z) {
-  if constexpr (F32)
-    return 1.f / (1.f + expf(-z));
-  else  // the fast forms' error (about 2^-21) is far below the output's rounding (2^-9)
-    return __fdividef(1.f, 1.f + __expf(-z));
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+  if constexpr (F32) {
+    return make_float2(1.f / (1.f + expf(-z.x)), 1.f / (1.f + expf(-z.y)));
+  } else {  // the approximations' error (about 2^-21) is far below the output's rounding (2^-9)
+    const float2 x = mul2(z, both(-1.4426950408889634f));
+    float2 e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(x.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(x.y));
+    e = add2(e, both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+    return r;
+  }
 }
 
 // Row m of F for channels c0.. of batch item b (m in [0, T + W - 1)).
@@ -97,11 +105,6 @@ __device__ __forceinline__ void filter(const float2 (&f)[W][VEC / 2], const floa
     for (int i = 0; i < W; ++i) z[j] = fma2(w[i][j], f[i][j], z[j]);
   }
 }
-template <bool F32>
-__device__ __forceinline__ float2 sigmoid2(float2 z) {
-  return make_float2(sigmoid<F32>(z.x), sigmoid<F32>(z.y));
-}
-
 // One thread: VEC channels x TT tokens.
 template <bool F32, int VEC, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) conv_fwd_kernel(const ConvParams p) {
@@ -119,48 +122,56 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) conv_fwd_kernel(const C
 #pragma unroll
   for (int i = 0; i < W - 1; ++i) last[i] = row_of<F32, VEC, W>(p, b, t0 + i, c0);
   const E* x = static_cast<const E*>(p.x) + b * p.xb + t0 * p.xt + c0;
-  auto load = [&](int t) {
-    return t < t1 && in_range(p.status, t, 1, p.T, CHK_CONV_IN) ? raw_load<F32, VEC>(x)
-                                                                : raw_zero<F32, VEC>();
-  };
+  const size_t extent = static_cast<size_t>(p.B) * p.T * p.C;
+  E* y = static_cast<E*>(p.y) + (static_cast<size_t>(b) * p.T + t0) * p.C + c0;
+  auto load = [&](int t) {  // the rows t .. t + U - 1, as far as they are the run's
+    if (t + U <= t1 && in_range(p.status, t, U, p.T, CHK_CONV_IN)) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    next[u] = load(t0 + u);
-    x += p.xt;
-  }
+      for (int u = 0; u < U; ++u) {
+        next[u] = raw_load<F32, VEC>(x);
+        x += p.xt;
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        next[u] = t + u < t1 && in_range(p.status, t + u, 1, p.T, CHK_CONV_IN) ? raw_load<F32, VEC>(x)
+                                                                               : raw_zero<F32, VEC>();
+        x += p.xt;
+      }
+    }
+  };
+  auto token = [&](const Raw<F32, VEC>& r) {
+    raw_unpack2<F32, VEC>(r, f[W - 1]);
+    float2 z[H];
+    filter<VEC, W>(f, w, bias, z);
+    if (SILU) {
+#pragma unroll
+      for (int j = 0; j < H; ++j) z[j] = mul2(z[j], sigmoid2<F32>(z[j]));
+    }
+    if (in_range(p.status, y - static_cast<E*>(p.y), VEC, extent, CHK_CONV_OUT))
+      raw_store<F32, VEC>(y, raw_pack2<F32, VEC>(z));
+    y += p.C;
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i)
+#pragma unroll
+      for (int j = 0; j < H; ++j) f[i][j] = f[i + 1][j];
+  };
+  load(t0);
   load_taps<F32, VEC, W>(p, c0, w, bias);
 #pragma unroll
   for (int i = 0; i < W - 1; ++i) raw_unpack2<F32, VEC>(last[i], f[i]);
-  size_t at = (static_cast<size_t>(b) * p.T + t0) * p.C + c0;
-  const size_t extent = static_cast<size_t>(p.B) * p.T * p.C;
-  E* y = static_cast<E*>(p.y);
-  for (int t = t0; t < t1; t += U) {
+  int t = t0;
+  for (; t + U <= t1; t += U) {
     Raw<F32, VEC> r[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      r[u] = next[u];
-      next[u] = load(t + U + u);
-      x += p.xt;
-    }
+    for (int u = 0; u < U; ++u) r[u] = next[u];
+    load(t + U);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (t + u >= t1) break;
-      raw_unpack2<F32, VEC>(r[u], f[W - 1]);
-      float2 z[H];
-      filter<VEC, W>(f, w, bias, z);
-      if (SILU) {
-#pragma unroll
-        for (int j = 0; j < H; ++j) z[j] = mul2(z[j], sigmoid2<F32>(z[j]));
-      }
-      if (in_range(p.status, at, VEC, extent, CHK_CONV_OUT))
-        raw_store<F32, VEC>(y + at, raw_pack2<F32, VEC>(z));
-      at += p.C;
-#pragma unroll
-      for (int i = 0; i < W - 1; ++i)
-#pragma unroll
-        for (int j = 0; j < H; ++j) f[i][j] = f[i + 1][j];
-    }
+    for (int u = 0; u < U; ++u) token(r[u]);
   }
+#pragma unroll
+  for (int u = 0; u < U - 1; ++u)
+    if (t + u < t1) token(next[u]);
   if (t1 == p.T && p.state_out != nullptr) {  // f now holds F's last W - 1 rows
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
@@ -210,7 +221,7 @@ template <bool F32, bool G32, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) conv_bwd_kernel(const ConvParams p) {
   using E = typename Elem<F32>::T;
   using G = typename Elem<G32>::T;
-  constexpr int VEC = 2, kWarps = kThreads / 32, U = 2;
+  constexpr int VEC = 2, kWarps = kThreads / 32, U = 4;
   __shared__ float sums[kWarps][32 * VEC * (W + 1)];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c0 = (blockIdx.x * 32 + lane) * VEC;
@@ -237,21 +248,95 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) conv_bwd_kernel(const C
       for (int i = 0; i < W; ++i) f[i][0] = dz[i] = make_float2(0.f, 0.f);
       const E* x = static_cast<const E*>(p.x) + b * p.xb + first * p.xt + c0;
       const G* dy = static_cast<const G*>(p.dy) + (static_cast<size_t>(b) * p.T + first) * p.C + c0;
+      E* dx = static_cast<E*>(p.dx) + (static_cast<size_t>(b) * p.T + first) * p.C + c0;  // row m - (W-1)
+      dx -= static_cast<size_t>(W - 1) * p.C;
       Raw<F32, VEC> nx[U];
       Raw<G32, VEC> ng[U];
-      auto load = [&](int t, int u) {
-        const bool on = t < tend && in_range(p.status, t, 1, p.T, CHK_CONV_IN);
-        nx[u] = on ? raw_load<F32, VEC>(x) : raw_zero<F32, VEC>();
-        ng[u] = on ? raw_load<G32, VEC>(dy) : raw_zero<G32, VEC>();
-        x += p.xt;
-        dy += p.C;
-      };
+      auto load = [&](int t) {  // tokens t .. t + U - 1, as far as they are to be read
+        if (t + U <= tend && in_range(p.status, t, U, p.T, CHK_CONV_IN)) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) load(first + u, u);
+          for (int u = 0; u < U; ++u) {
+            nx[u] = raw_load<F32, VEC>(x);
+            ng[u] = raw_load<G32, VEC>(dy);
+            x += p.xt;
+            dy += p.C;
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const bool on = t + u < tend && in_range(p.status, t + u, 1, p.T, CHK_CONV_IN);
+            nx[u] = on ? raw_load<F32, VEC>(x) : raw_zero<F32, VEC>();
+            ng[u] = on ? raw_load<G32, VEC>(dy) : raw_zero<G32, VEC>();
+            x += p.xt;
+            dy += p.C;
+          }
+        }
+      };
+      // dz of the next token into dz[W - 1], its row into f[W - 1]
+      auto enter = [&](const Raw<F32, VEC>& rx, const Raw<G32, VEC>& rg) {
+        float2 gy[1];
+        raw_unpack2<F32, VEC>(rx, f[W - 1]);
+        raw_unpack2<G32, VEC>(rg, gy);
+        dz[W - 1] = gy[0];
+        if (SILU) {
+          float2 z[1];
+          filter<VEC, W>(f, w, bias, z);
+          const float2 s = sigmoid2<F32>(z[0]);
+          // s (1 + z (1 - s)); at z = +-inf the inner product is 0 times inf: NaN, as in the formula
+          const float2 q = fma2(z[0], fma2(s, both(-1.f), both(1.f)), both(1.f));
+          dz[W - 1] = mul2(gy[0], mul2(s, q));
+        }
+      };
+      auto products = [&](float2 (&o)[1]) {
+        o[0] = mul2(w[0][0], dz[W - 1]);
+        dw[0] = fma2(dz[W - 1], f[0][0], dw[0]);
+#pragma unroll
+        for (int i = 1; i < W; ++i) {
+          o[0] = fma2(w[i][0], dz[W - 1 - i], o[0]);
+          dw[i] = fma2(dz[W - 1], f[i][0], dw[i]);
+        }
+        db = add2(db, dz[W - 1]);
+      };
+      auto leave = [&]() {
+        dx += p.C;
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+          f[i][0] = f[i + 1][0];
+          dz[i] = dz[i + 1];
+        }
+      };
+      // any token of the run, its edges among them
+      auto token = [&](int m, const Raw<F32, VEC>& rx, const Raw<G32, VEC>& rg) {
+        enter(rx, rg);
+        if (m >= p.T) dz[W - 1] = make_float2(0.f, 0.f);
+        if (m >= m0) {
+          float2 o[1];
+          products(o);
+          if (m >= p.T && p.dstate_out != nullptr) {
+            const size_t at = (static_cast<size_t>(b) * (W - 1) + (m - p.T)) * p.C + c0;
+            float2 ds[1];
+            if (in_range(p.status, at, VEC, sn, CHK_CONV_IN)) {
+              raw_unpack2<F32, VEC>(raw_load<F32, VEC>(static_cast<const E*>(p.dstate_out) + at), ds);
+              o[0] = add2(o[0], ds[0]);
+            }
+          }
+          if (m >= W - 1) {
+            if (in_range(p.status, dx - static_cast<E*>(p.dx), VEC, xn, CHK_CONV_OUT))
+              raw_store<F32, VEC>(dx, raw_pack2<F32, VEC>(o));
+          } else if (p.dstate != nullptr) {
+            const size_t at = (static_cast<size_t>(b) * (W - 1) + m) * p.C + c0;
+            if (in_range(p.status, at, VEC, sn, CHK_CONV_OUT))
+              raw_store<F32, VEC>(static_cast<E*>(p.dstate) + at, raw_pack2<F32, VEC>(o));
+          }
+        }
+        leave();
+      };
+      load(first);
 #pragma unroll
       for (int i = 0; i < W - 1; ++i)
         if (first + i < rows)
           raw_unpack2<F32, VEC>(row_of<F32, VEC, W>(p, b, first + i, c0), f[i]);
+      const int inner = m0 > W - 1 ? static_cast<int>(m0) : W - 1;  // from here to tend: no edge
       for (int t = first; t < m1; t += U) {
         Raw<F32, VEC> rx[U];
         Raw<G32, VEC> rg[U];
@@ -259,55 +344,22 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) conv_bwd_kernel(const C
         for (int u = 0; u < U; ++u) {
           rx[u] = nx[u];
           rg[u] = ng[u];
-          load(t + U + u, u);
         }
+        load(t + U);
+        if (t >= inner && t + U <= tend) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int m = t + u;
-          if (m >= m1) break;
-          float2 gy[1];
-          raw_unpack2<F32, VEC>(rx[u], f[W - 1]);
-          raw_unpack2<G32, VEC>(rg[u], gy);
-          float2 d = gy[0];
-          if (SILU) {
-            float2 z[1];
-            filter<VEC, W>(f, w, bias, z);
-            const float2 s = sigmoid2<F32>(z[0]), one = make_float2(1.f, 1.f);
-            // s (1 + z (1 - s)); at z = +-inf the bracket's product is 0 times inf: NaN, as in the formula
-            d = mul2(d, mul2(s, fma2(z[0], fma2(s, make_float2(-1.f, -1.f), one), one)));
+          for (int u = 0; u < U; ++u) {
+            float2 o[1];
+            enter(rx[u], rg[u]);
+            products(o);
+            if (in_range(p.status, dx - static_cast<E*>(p.dx), VEC, xn, CHK_CONV_OUT))
+              raw_store<F32, VEC>(dx, raw_pack2<F32, VEC>(o));
+            leave();
           }
-          dz[W - 1] = m < p.T ? d : make_float2(0.f, 0.f);
-          if (m >= m0) {
-            float2 o[1] = {make_float2(0.f, 0.f)};
+        } else {
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-              o[0] = fma2(w[i][0], dz[W - 1 - i], o[0]);
-              dw[i] = fma2(dz[W - 1], f[i][0], dw[i]);
-            }
-            db = add2(db, dz[W - 1]);
-            if (m >= p.T && p.dstate_out != nullptr) {
-              const size_t at = (static_cast<size_t>(b) * (W - 1) + (m - p.T)) * p.C + c0;
-              float2 ds[1];
-              if (in_range(p.status, at, VEC, sn, CHK_CONV_IN)) {
-                raw_unpack2<F32, VEC>(raw_load<F32, VEC>(static_cast<const E*>(p.dstate_out) + at), ds);
-                o[0] = add2(o[0], ds[0]);
-              }
-            }
-            if (m >= W - 1) {
-              const size_t at = (static_cast<size_t>(b) * p.T + (m - (W - 1))) * p.C + c0;
-              if (in_range(p.status, at, VEC, xn, CHK_CONV_OUT))
-                raw_store<F32, VEC>(static_cast<E*>(p.dx) + at, raw_pack2<F32, VEC>(o));
-            } else if (p.dstate != nullptr) {
-              const size_t at = (static_cast<size_t>(b) * (W - 1) + m) * p.C + c0;
-              if (in_range(p.status, at, VEC, sn, CHK_CONV_OUT))
-                raw_store<F32, VEC>(static_cast<E*>(p.dstate) + at, raw_pack2<F32, VEC>(o));
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < W - 1; ++i) {
-            f[i][0] = f[i + 1][0];
-            dz[i] = dz[i + 1];
-          }
+          for (int u = 0; u < U; ++u)
+            if (t + u < m1) token(t + u, rx[u], rg[u]);
         }
       }
     }

@@ -144,24 +144,8 @@ __device__ __forceinline__ void load_weight(const QkParams& p, const void* w, co
     row_unpack<F32>(row_load<F32>(static_cast<const typename Elem<F32>::T*>(w), a), o);
 }
 
-// Row of head h (queries first, then keys) of a token in the inputs.
-template <bool F32>
-__device__ __forceinline__ const typename Elem<F32>::T* in_row(const QkParams& p, long long qrow,
-                                                               long long krow, int h) {
-  using E = typename Elem<F32>::T;
-  return h < p.Nq ? static_cast<const E*>(p.q) + qrow + static_cast<long long>(h) * p.K
-                  : static_cast<const E*>(p.k) + krow + static_cast<long long>(h - p.Nq) * p.K;
-}
-// The same in a contiguous [tokens][Nq or Nk][K].
-__device__ __forceinline__ size_t out_at(const QkParams& p, long long token, int h) {
-  return (h < p.Nq ? static_cast<size_t>(token) * p.Nq + h
-                   : static_cast<size_t>(token) * p.Nk + (h - p.Nq)) * p.K;
-}
-__device__ __forceinline__ bool out_ok(const QkParams& p, size_t at, int h, int site) {
-  return in_range(p.status, at, p.K, static_cast<size_t>(p.tokens) * (h < p.Nq ? p.Nq : p.Nk) * p.K, site);
-}
-
-// A lane group takes heads g, g + split, ... of one token, U at a time.
+// A lane group takes heads g, g + split, ... of one token, queries first, then
+// keys, U at a time.
 template <bool F32, int LPR>
 __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) qk_fwd_kernel(const QkParams p) {
   using E = typename Elem<F32>::T;
@@ -169,48 +153,53 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) qk_fwd_kernel(const QkP
   const long long gid = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / LPR;
   const long long token = gid / p.split;
   const int g = static_cast<int>(gid - token * p.split);
-  const int heads = p.Nq + p.Nk;
   Lane a = lane_of<LPR>(p);
   const bool valid = token < p.tokens && a.on;
   const int b = static_cast<int>(token / p.T), t = static_cast<int>(token - static_cast<long long>(b) * p.T);
-  const long long qrow = b * p.qb + t * p.qt, krow = b * p.kb + t * p.kt;
-  const int steps = (heads + p.split - 1) / p.split;  // the same for every lane: shuffles below
-  RawRow<F32> next[U];
-  auto load = [&](int s0) {
+  const float inv_k = 1.f / static_cast<float>(p.K);
+  const int step = p.split * p.K;
+  load_angles<LPR>(p, token, t, valid, a);
+  auto heads = [&](const void* src, long long row, int n, const void* weight, void* dst) {
+    const E* in = static_cast<const E*>(src) + row + g * p.K;
+    E* out = static_cast<E*>(dst) + (token * n + g) * p.K;
+    const size_t extent = static_cast<size_t>(p.tokens) * n * p.K;
+    const int steps = (n + p.split - 1) / p.split;  // the same for every lane: shuffles below
+    RawRow<F32> next[U];
+    auto load = [&](int s0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = g + (s0 + u) * p.split;
-      next[u] = valid && h < heads && in_range(p.status, t, 1, p.T, CHK_QK_IN)
-                    ? row_load<F32>(in_row<F32>(p, qrow, krow, h), a) : row_zero<F32>();
+      for (int u = 0; u < U; ++u) {
+        const bool on = valid && g + (s0 + u) * p.split < n && in_range(p.status, t, 1, p.T, CHK_QK_IN);
+        next[u] = on ? row_load<F32>(in, a) : row_zero<F32>();
+        in += step;
+      }
+    };
+    load(0);
+    float2 w[4];
+    load_weight<F32>(p, weight, a, w);
+    for (int s0 = 0; s0 < steps; s0 += U) {
+      RawRow<F32> r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) r[u] = next[u];
+      if (s0 + U < steps) load(s0 + U);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (s0 + u >= steps) break;
+        float2 x[4];
+        row_unpack<F32>(r[u], x);
+        const float2 ss = fma2(x[0], x[0], fma2(x[1], x[1], fma2(x[2], x[2], mul2(x[3], x[3]))));
+        const float2 rs = both(rsqrtf(fmaf(row_sum<LPR>(ss.x + ss.y), inv_k, p.eps)));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = mul2(mul2(x[j], rs), w[j]);
+        rotate<1>(p, a, x);
+        if (valid && g + (s0 + u) * p.split < n &&
+            in_range(p.status, out - static_cast<E*>(dst), p.K, extent, CHK_QK_OUT))
+          row_store<F32>(out, a, x);
+        out += step;
+      }
     }
   };
-  load(0);
-  load_angles<LPR>(p, token, t, valid, a);
-  float2 wq[4], wk[4];
-  load_weight<F32>(p, p.wq, a, wq);
-  load_weight<F32>(p, p.wk, a, wk);
-  const float inv_k = 1.f / static_cast<float>(p.K);
-  for (int s0 = 0; s0 < steps; s0 += U) {
-    RawRow<F32> r[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) r[u] = next[u];
-    if (s0 + U < steps) load(s0 + U);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (s0 + u >= steps) break;
-      const int h = g + (s0 + u) * p.split;
-      float2 x[4];
-      row_unpack<F32>(r[u], x);
-      const float2 ss = fma2(x[0], x[0], fma2(x[1], x[1], fma2(x[2], x[2], mul2(x[3], x[3]))));
-      const float2 rs = both(rsqrtf(row_sum<LPR>(ss.x + ss.y) * inv_k + p.eps));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = mul2(mul2(x[j], rs), h < p.Nq ? wq[j] : wk[j]);
-      rotate<1>(p, a, x);
-      const size_t at = out_at(p, token, h);
-      if (valid && h < heads && out_ok(p, at, h, CHK_QK_OUT))
-        row_store<F32>(static_cast<E*>(h < p.Nq ? p.qo : p.ko) + at, a, x);
-    }
-  }
+  heads(p.q, b * p.qb + t * p.qt, p.Nq, p.wq, p.qo);
+  if (p.Nk > 0) heads(p.k, b * p.kb + t * p.kt, p.Nk, p.wk, p.ko);
 }
 
 // As the forward kernel, with the groups walking over the tokens: a lane
@@ -221,7 +210,6 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const QkParams p) {
   using G = typename Elem<G32>::T;
   constexpr int U = 2, kGroups = kThreads / LPR;
   __shared__ float sums[2][kGroups][8 * LPR + 1];
-  const int heads = p.Nq + p.Nk;
   const float inv_k = 1.f / static_cast<float>(p.K);
   Lane a = lane_of<LPR>(p);
   float2 wq[4], wk[4], dwq[4], dwk[4];
@@ -230,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const QkParams p) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) dwq[j] = dwk[j] = make_float2(0.f, 0.f);
   const long long items = p.tokens * p.split;
-  const int steps = (heads + p.split - 1) / p.split;
+  const int step = p.split * p.K;
   // i0: the CTA's first group, the same for all of its warps
   for (long long i0 = static_cast<long long>(blockIdx.x) * kGroups; i0 < items;
        i0 += static_cast<long long>(gridDim.x) * kGroups) {
@@ -239,68 +227,69 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const QkParams p) {
     const int g = static_cast<int>(item - token * p.split);
     const bool valid = item < items && a.on;
     const int b = static_cast<int>(token / p.T), t = static_cast<int>(token - static_cast<long long>(b) * p.T);
-    const long long qrow = b * p.qb + t * p.qt, krow = b * p.kb + t * p.kt;
-    RawRow<F32> nx[U];
-    RawRow<G32> ny[U];
-    auto load = [&](int s0) {
+    load_angles<LPR>(p, token, t, valid, a);
+    auto heads = [&](const void* src, long long row, const void* grad, int n, const float2 (&w)[4],
+                     float2 (&dw)[4], void* dst) {
+      const E* in = static_cast<const E*>(src) + row + g * p.K;
+      const size_t first = static_cast<size_t>(token * n + g) * p.K;
+      const G* gin = static_cast<const G*>(grad) + first;
+      E* out = static_cast<E*>(dst) + first;
+      const size_t extent = static_cast<size_t>(p.tokens) * n * p.K;
+      const int steps = (n + p.split - 1) / p.split;
+      RawRow<F32> nx[U];
+      RawRow<G32> ny[U];
+      auto load = [&](int s0) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = g + (s0 + u) * p.split;
-        nx[u] = row_zero<F32>();
-        ny[u] = row_zero<G32>();
-        if (valid && h < heads && in_range(p.status, t, 1, p.T, CHK_QK_IN)) {
-          nx[u] = row_load<F32>(in_row<F32>(p, qrow, krow, h), a);
-          const size_t at = out_at(p, token, h);
-          if (out_ok(p, at, h, CHK_QK_IN))
-            ny[u] = row_load<G32>(static_cast<const G*>(h < p.Nq ? p.dqo : p.dko) + at, a);
+        for (int u = 0; u < U; ++u) {
+          const bool on = valid && g + (s0 + u) * p.split < n && in_range(p.status, t, 1, p.T, CHK_QK_IN) &&
+                          in_range(p.status, gin - static_cast<const G*>(grad), p.K, extent, CHK_QK_IN);
+          nx[u] = on ? row_load<F32>(in, a) : row_zero<F32>();
+          ny[u] = on ? row_load<G32>(gin, a) : row_zero<G32>();
+          in += step;
+          gin += step;
+        }
+      };
+      load(0);
+      for (int s0 = 0; s0 < steps; s0 += U) {
+        RawRow<F32> rx[U];
+        RawRow<G32> ry[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          rx[u] = nx[u];
+          ry[u] = ny[u];
+        }
+        if (s0 + U < steps) load(s0 + U);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (s0 + u >= steps) break;
+          const bool on = valid && g + (s0 + u) * p.split < n;
+          float2 x[4], du[4];
+          row_unpack<F32>(rx[u], x);
+          row_unpack<G32>(ry[u], du);
+          rotate<-1>(p, a, du);
+          const float2 ss = fma2(x[0], x[0], fma2(x[1], x[1], fma2(x[2], x[2], mul2(x[3], x[3]))));
+          const float2 rs = both(rsqrtf(fmaf(row_sum<LPR>(ss.x + ss.y), inv_k, p.eps)));
+          float2 dot = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[j] = mul2(x[j], rs);                   // xh
+            if (on) dw[j] = fma2(du[j], x[j], dw[j]);  // a head that is not there has, for eps = 0, xh = NaN
+            du[j] = mul2(du[j], w[j]);               // g
+            dot = fma2(du[j], x[j], dot);
+          }
+          // Lanes past the row's end hold zeros, or NaN times zero when eps = 0:
+          // they must not enter the row's sum.
+          const float2 mean = both(-row_sum<LPR>(a.on ? dot.x + dot.y : 0.f) * inv_k);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) du[j] = mul2(rs, fma2(x[j], mean, du[j]));
+          if (on && in_range(p.status, out - static_cast<E*>(dst), p.K, extent, CHK_QK_OUT))
+            row_store<F32>(out, a, du);
+          out += step;
         }
       }
     };
-    load(0);
-    load_angles<LPR>(p, token, t, valid, a);
-    for (int s0 = 0; s0 < steps; s0 += U) {
-      RawRow<F32> rx[U];
-      RawRow<G32> ry[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        rx[u] = nx[u];
-        ry[u] = ny[u];
-      }
-      if (s0 + U < steps) load(s0 + U);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (s0 + u >= steps) break;
-        const int h = g + (s0 + u) * p.split;
-        const bool on = valid && h < heads, isq = h < p.Nq;
-        float2 x[4], du[4];
-        row_unpack<F32>(rx[u], x);
-        row_unpack<G32>(ry[u], du);
-        rotate<-1>(p, a, du);
-        const float2 ss = fma2(x[0], x[0], fma2(x[1], x[1], fma2(x[2], x[2], mul2(x[3], x[3]))));
-        const float rs = rsqrtf(row_sum<LPR>(ss.x + ss.y) * inv_k + p.eps);
-        float2 dot = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] = mul2(x[j], both(rs));  // xh
-          if (on) {  // a head that is not there has x = 0 and, for eps = 0, xh = NaN
-            if (isq)
-              dwq[j] = fma2(du[j], x[j], dwq[j]);
-            else
-              dwk[j] = fma2(du[j], x[j], dwk[j]);
-          }
-          du[j] = mul2(du[j], isq ? wq[j] : wk[j]);  // g
-          dot = fma2(du[j], x[j], dot);
-        }
-        // Lanes past the row's end hold zeros, or NaN times zero when eps = 0:
-        // they must not enter the row's sum.
-        const float2 mean = both(-row_sum<LPR>(a.on ? dot.x + dot.y : 0.f) * inv_k);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) du[j] = mul2(both(rs), fma2(x[j], mean, du[j]));
-        const size_t at = out_at(p, token, h);
-        if (on && out_ok(p, at, h, CHK_QK_OUT))
-          row_store<F32>(static_cast<E*>(isq ? p.dq : p.dk) + at, a, du);
-      }
-    }
+    heads(p.q, b * p.qb + t * p.qt, p.dqo, p.Nq, wq, dwq, p.dq);
+    if (p.Nk > 0) heads(p.k, b * p.kb + t * p.kt, p.dko, p.Nk, wk, dwk, p.dk);
   }
   if (a.on) {
 #pragma unroll
@@ -368,7 +357,7 @@ cudaError_t bwd_main(const QkParams& p, bool f32, bool grad_f32, cudaStream_t st
 // unless that leaves fewer than 1,024 threads for each of 152 SMs.
 int qk_split(const m2rnn_qk_shape* s) {
   const long long tokens = static_cast<long long>(s->B) * s->T;
-  const int heads = s->Nq + s->Nk, lpr = lanes_per_row(s->K);
+  const int heads = s->Nq > s->Nk ? s->Nq : s->Nk, lpr = lanes_per_row(s->K);
   if (tokens <= 0) return 1;
   const long long want = (152LL * 1024 / lpr + tokens - 1) / tokens;
   return static_cast<int>(want < 1 ? 1 : want > heads ? heads : want);

@@ -167,7 +167,7 @@ static __global__ void __launch_bounds__(1024)
   const int col = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (col < n) {
-#pragma unroll 16
+#pragma unroll 8
     for (int r = warp; r < nparts; r += 32) {
       const size_t at = static_cast<size_t>(r) * n + col;
       if (in_range(status, at, 1, static_cast<size_t>(nparts) * n, site)) s += part[at];
