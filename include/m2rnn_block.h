@@ -48,7 +48,8 @@ typedef struct {
  *   x      [B,T,C] in_dtype (rows)          w     [C,W] in_dtype
  *   bias   [C] in_dtype or NULL (0)         state [B,W-1,C] in_dtype or NULL (0)
  *   y      [B,T,C] in_dtype                 state_out [B,W-1,C] in_dtype or NULL
- * C a multiple of 8, W in {2, 3, 4}, B >= 1, T >= 0, B*T*C < 2^40.
+ * C a multiple of 8 up to 2^24, W in {2, 3, 4}, B >= 1, 0 <= T <= 2^30,
+ * B*T*C < 2^40.
  * T = 0 copies the state. */
 typedef struct {
     int B, T, C, W;
@@ -126,7 +127,8 @@ int m2rnn_qk_norm_bwd(const m2rnn_qk_shape *s, const void *q, const m2rnn_rows *
  *     dt_t = softplus(a_t + beta_n),   f_t = exp(-alpha_n dt_t)
  *     H_t  = f_t H_{t-1} + dt_t k_t v_t^T,     y_t = H_t^T q_t + w_r (.) v_t
  * Shapes, layouts and the sharing of q and k by groups of heads are those of
- * m2rnn_shape (K in {16,32,64,128}, V in {16,32}; ckpt_every is ignored):
+ * m2rnn_shape (K in {16,32,64,128}, V in {16,32}; ckpt_every is ignored), for
+ * whole sequences with T <= 2^30 and N <= 2^20:
  *   q, k [B,T,Nq,K], v [B,T,N,V], a [B,T,N] in_dtype (rows)
  *   alpha, beta [N] in_dtype; w_r [N,V] in_dtype or NULL (0)
  *   H0, H_T [B,N,K,V] fp32 or NULL;   y [B,T,N,V] in_dtype

@@ -65,6 +65,7 @@ int check_conv(const m2rnn_conv_shape* s, bool backward) {
   if (backward && s->grad_dtype != M2RNN_F32 && s->grad_dtype != s->in_dtype)
     return M2RNN_ERR_INVALID_ARG;
   if (s->C % 8 != 0 || s->W < 2 || s->W > 4) return M2RNN_ERR_UNSUPPORTED_SHAPE;
+  if (s->C > (1 << 24) || s->T > (1 << 30)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
   if (static_cast<double>(s->B) * (static_cast<double>(s->T) + s->W) * s->C >= 1099511627776.0)
     return M2RNN_ERR_UNSUPPORTED_SHAPE;  // 2^40
   return M2RNN_OK;
@@ -234,7 +235,7 @@ size_t scan_part_bytes(const m2rnn_shape* s, const ScanPlan& q) {
 int check_scan(const m2rnn_shape* s) {
   const int rc = m2rnn::validate_shape(s);
   if (rc != M2RNN_OK) return rc;
-  if (s->T > (1 << 30)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
+  if (s->T > (1 << 30) || s->N > (1 << 20)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
   const ScanPlan q = scan_plan(s);
   const double ctas = static_cast<double>(s->B) * q.nhb * (s->Nq == 0 ? 1 : s->Nq) * q.nc;
   return ctas < 1073741824.0 ? M2RNN_OK : M2RNN_ERR_UNSUPPORTED_SHAPE;  // 2^30

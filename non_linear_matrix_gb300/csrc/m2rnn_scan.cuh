@@ -53,6 +53,7 @@ namespace scan {
 constexpr int kThreads = 128;  // that fill a tile together
 constexpr int kVLd = kCols + 8;  // shared row of a value tile: 144 bytes, no bank conflicts
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eLo = static_cast<float>(1.4426950408889634 - kLog2e);
 
 template <bool F32>
 struct Terms {
@@ -136,27 +137,27 @@ __device__ __forceinline__ float2 join(const uint32_t (&t)[P]) {
   return v;
 }
 
-// acc += A B over the terms' pairs that matter, smallest first.
-template <int PA, int PB>
-__device__ __forceinline__ void mma_terms(float (&acc)[4], const uint32_t (&a)[PA][4],
-                                          const uint32_t (&b)[PB][2]) {
-  constexpr int most = (PA > PB ? PA : PB) - 1;
-#pragma unroll
-  for (int s = most; s >= 0; --s)
-#pragma unroll
-    for (int i = 0; i < PA; ++i) {
-      const int j = s - i;
-      if (j >= 0 && j < PB) ptx::mma_bf16_16816(acc, a[i], b[j][0], b[j][1]);
-    }
-}
+// A tensor core cuts its sum off where it should round (by 0.37 of the last
+// place on average where the accumulator is much larger or smaller than the
+// products, 0.05 from zero, measured): a long chain drifts towards zero, and one
+// that runs through a state does so from chunk to chunk.  So where both sides
+// have three terms, the leading product and the others' sum start from zero and
+// are added with rounding, and the states' products start from zero per chunk.
 
-// The same for N accumulators that share A, term by term across them: a
-// product's result is ready about 20 clocks after its issue, so consecutive
-// products go to different accumulators.
+// acc += A B over the terms' pairs that matter, smallest first, for N
+// accumulators that share A, term by term across them: a product's result is
+// ready about 20 clocks after its issue, so consecutive products go to different
+// accumulators.
 template <int PA, int PB, int N>
 __device__ __forceinline__ void mma_terms_n(float (&acc)[N][4], const uint32_t (&a)[PA][4],
                                             const uint32_t (&b)[N][PB][2]) {
   constexpr int most = (PA > PB ? PA : PB) - 1;
+  constexpr bool apart = PA == 3 && PB == 3;
+  float top[N][4], rest[N][4];
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top[n][i] = rest[n][i] = 0.f;
 #pragma unroll
   for (int s = most; s >= 0; --s)
 #pragma unroll
@@ -164,8 +165,21 @@ __device__ __forceinline__ void mma_terms_n(float (&acc)[N][4], const uint32_t (
       const int j = s - i;
       if (j >= 0 && j < PB)
 #pragma unroll
-        for (int n = 0; n < N; ++n) ptx::mma_bf16_16816(acc[n], a[i], b[n][j][0], b[n][j][1]);
+        for (int n = 0; n < N; ++n)
+          ptx::mma_bf16_16816(!apart ? acc[n] : s == 0 ? top[n] : rest[n], a[i], b[n][j][0], b[n][j][1]);
     }
+  if (apart)
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        set_pair(acc[n], h, add2(pair(acc[n], h), add2(pair(top[n], h), pair(rest[n], h))));
+}
+template <int PA, int PB>
+__device__ __forceinline__ void mma_terms(float (&acc)[4], const uint32_t (&a)[PA][4],
+                                          const uint32_t (&b)[PB][2]) {
+  mma_terms_n<PA, PB, 1>(reinterpret_cast<float(&)[1][4]>(acc), a,
+                         reinterpret_cast<const uint32_t(&)[1][PB][2]>(b));
 }
 
 // Lets a kernel take `bytes` of dynamic shared memory: asked once per kernel

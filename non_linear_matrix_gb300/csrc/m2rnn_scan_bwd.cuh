@@ -15,9 +15,11 @@
 //     da_t = sigmoid(a + beta) ((Uin_t + sum_i D_it) / dt_t - alpha dl_t)
 //     dalpha = - sum dt dl,  dbeta = sum da,  dw_r = sum u (.) v
 //
-// (dl_t: with respect to the natural logarithm of the decay; its last sum is the
-// row sums of D from t on less its column sums from t on, both without the
-// diagonal, which would cancel and where the decay is strong is most of D.)
+// (dl_t: with respect to the natural logarithm of the decay.)  Its last sum is
+// formed without differences, which would leave errors of the size of all of D in
+// it where the decay is strong: block by block of 16 tokens, from D's row sums and
+// column sums over whole blocks, and within t's own block as [i >= t] D^T on the
+// tensor cores (D in three terms), summed over j < t.
 //
 // A CTA takes one chunk of one group and walks over its head blocks: dq and
 // dk, and the sum over heads of E L, stay in registers, so neither needs a sum
@@ -52,9 +54,10 @@ struct BwdSmem {
   static constexpr int g = r + state, f = g + tri;
   static constexpr int gate = f + (F32 ? 0 : tri);  // fp32 keeps the sum in registers
   // Per head and token, from the first half of the K columns: Pin, Uin [HB][64];
-  // column sums of D without its diagonal by row block, from column 16 rt on;
-  // shares of <R, H>.  What else there is per head and token has its place in the
-  // 16 bytes behind the tiles' rows (see spare).
+  // column sums of D by row block rt: in the columns of its own block the sums over
+  // i >= t > j, then the later blocks' column sums; shares of <R, H>.  What else
+  // there is per head and token has its place in the 16 bytes behind the tiles' rows
+  // (see spare).
   static constexpr int through = gate + HB * 192 * 4;
   static constexpr int cols = through + 2 * HB * kChunk * 4;
   static constexpr int rh = cols + 160 * HB * 4;
@@ -64,6 +67,13 @@ struct BwdSmem {
 __device__ __forceinline__ float quad_sum(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 1);
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+
+// d (16 x 8) += A (16 x 8, a0: rows 0..7, a1: 8..15) B (8 x 8).
+__device__ __forceinline__ void mma_bf16_1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(b));
 }
 
 // Two neighbouring values of an output in its element type.
@@ -178,7 +188,7 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
   };
   // The 16 bytes behind each row of a tile keep bank conflicts away and hold one
   // value per head: the second half's shares of Pin (u) and Uin (v), the row
-  // sums of D without its diagonal (q) and the diagonal (k).
+  // sums of D over later blocks (q) and over the row's own block (k).
   auto spare = [&](int tile, int width, int h, int row) {
     return reinterpret_cast<float*>(smem + tile + (row * (width + 8) + width) * 2) + h;
   };
@@ -361,30 +371,49 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
           ui = add2(ui, make_float2(*spare(S::v, kCols, h, t), *spare(S::v, kCols, h, t + 1)));
           pi = add2(pi, make_float2(*spare(S::u, kCols, h, t), *spare(S::u, kCols, h, t + 1)));
         }
-        const float2 dd = make_float2(*spare(S::k, K, h, t), *spare(S::k, K, h, t + 1));
-        const float2 ur = make_float2(*spare(S::q, K, h, t), *spare(S::q, K, h, t + 1));
+        // sums of D over a token's own block (from itself on) and the later ones, and
+        // what earlier blocks' columns hold for it
+        const float2 own = make_float2(*spare(S::k, K, h, t), *spare(S::k, K, h, t + 1));
+        const float2 later = make_float2(*spare(S::q, K, h, t), *spare(S::q, K, h, t + 1));
+        const float2 within = *reinterpret_cast<const float2*>(Pcol + col_at(blk, h, t));
+        float2 bw = pi;
+        float far[4];  // for the tokens of block 0..3: the parts of tokens of other blocks
+        far[0] = blk > 0 ? pi.x + pi.y : 0.f;
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-          if (s <= blk) pi = add2(pi, *reinterpret_cast<const float2*>(Pcol + col_at(s, h, t)));
-        const float2 bw = make_float2(pi.x - ur.x, pi.y - ur.y);
-        float inc = ui.x + ui.y, suf = bw.x + bw.y;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-          const float up = __shfl_up_sync(0xffffffffu, inc, d);
-          const float dn = __shfl_down_sync(0xffffffffu, suf, d);
-          if (lane >= d) inc += up;
-          if (lane + d < 32) suf += dn;
+        for (int s = 0; s < 3; ++s) {
+          if (s < blk) bw = add2(bw, *reinterpret_cast<const float2*>(Pcol + col_at(s, h, t)));
+          far[s + 1] = blk < s + 1 ? ui.x + ui.y : blk > s + 1 ? bw.x + bw.y : 0.f;
         }
-        float before = __shfl_up_sync(0xffffffffu, inc, 1), behind = __shfl_down_sync(0xffffffffu, suf, 1);
-        if (lane == 0) before = 0.f;
-        if (lane == 31) behind = 0.f;
+        {  // their sums, a lane its own block's
+          const bool b4 = lane & 16, b3 = lane & 8;
+          float x = b4 ? far[2] : far[0], y = b4 ? far[3] : far[1];
+          x += __shfl_xor_sync(0xffffffffu, b4 ? far[0] : far[2], 16);
+          y += __shfl_xor_sync(0xffffffffu, b4 ? far[1] : far[3], 16);
+          far[0] = b3 ? y : x;
+          far[0] += __shfl_xor_sync(0xffffffffu, b3 ? x : y, 8);
+#pragma unroll
+          for (int m = 4; m >= 1; m /= 2) far[0] += __shfl_xor_sync(0xffffffffu, far[0], m);
+        }
+        const float2 fw = add2(ui, later);
+        float inc = fw.x + fw.y, suf = bw.x + bw.y;
+#pragma unroll
+        for (int d = 1; d < 8; d *= 2) {
+          const float up = __shfl_up_sync(0xffffffffu, inc, d, 8);
+          const float dn = __shfl_down_sync(0xffffffffu, suf, d, 8);
+          if ((lane & 7) >= d) inc += up;
+          if ((lane & 7) + d < 8) suf += dn;
+        }
+        float before = __shfl_up_sync(0xffffffffu, inc, 1, 8), behind = __shfl_down_sync(0xffffffffu, suf, 1, 8);
+        if ((lane & 7) == 0) before = 0.f;
+        if ((lane & 7) == 7) behind = 0.f;
         constexpr int shares = F32 ? K * V / 256 : V / 16;
         float all = 0.f;
 #pragma unroll
         for (int e = 0; e < shares; ++e) all += rh[h * shares + e];
-        all *= decay;
-        const float dl[2] = {all + before + (behind + bw.y + bw.x), all + (before + ui.x) + (behind + bw.y)};
-        const float uu[2] = {ui.x + ur.x + dd.x, ui.y + ur.y + dd.y};
+        all = fmaf(all, decay, far[0]);
+        const float dl[2] = {all + within.x + before + (behind + bw.y + bw.x),
+                             all + within.y + (before + fw.x) + (behind + bw.y)};
+        const float uu[2] = {fw.x + own.x, fw.y + own.y};
         float sa = 0.f, sb = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -546,7 +575,8 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
       uint32_t va[V / 16][P][4];
 #pragma unroll
       for (int vv = 0; vv < V / 16; ++vv) load_a<P>(va[vv], vs, kVLd, 16 * rt, h * V + 16 * vv);
-      float2 ur0 = make_float2(0.f, 0.f), ur1 = ur0;
+      float2 ur0 = make_float2(0.f, 0.f), ur1 = ur0;  // row sums of D: later blocks
+      float own0 = 0.f, own1 = 0.f;                   // own block
       float* ph = pcol + h * pcol_h;
       const float* li_at = lo + rb + c2;
       float between = 0.f;  // sum of l over the blocks between j's and i's
@@ -564,6 +594,7 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
         }
         uint32_t a[PO][4];
         float2 dc[2];
+        float z0[4] = {0.f, 0.f, 0.f, 0.f}, z1[4] = {0.f, 0.f, 0.f, 0.f};  // j < 8, j >= 8
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int n = 2 * k4 + u;
@@ -595,17 +626,27 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
             const float2 s0 = add2(make_float2(s.x, s.y), f0), s1 = add2(make_float2(s.z, s.w), f1);
             ft[32 * n] = make_float4(s0.x, s0.y, s1.x, s1.y);
           }
-          float2 d0 = mul2(f0, g0), d1 = mul2(f1, g1);
-          if (k4 == 0) {  // the diagonal apart: row g in the first tile, g + 8 in the second
-            float2& d = u ? d1 : d0;
-            if ((lane & 3) == (g >> 1)) {
-              *spare(S::k, K, h, rb + g + 8 * u) = (g & 1) ? d.y : d.x;
-              d = (g & 1) ? make_float2(d.x, 0.f) : make_float2(0.f, d.y);
+          const float2 d0 = mul2(f0, g0), d1 = mul2(f1, g1);
+          if (k4 == 0) {
+            // sum of D over i >= t > j in the block: z = [i >= t] D^T, then row t's sum
+            // over j < t; D is 0 for j >= 8 > i
+            const uint32_t tri = (c2 >= g ? 0x3f80u : 0u) | (c2 + 1 >= g ? 0x3f800000u : 0u);
+            uint32_t x[3];
+            split<3>(d0, x);
+#pragma unroll
+            for (int s = 2; s >= 0; --s) mma_bf16_1688(z0, u ? 0x3f803f80u : tri, u ? tri : 0u, x[s]);
+            own0 += d0.x + d0.y;
+            if (u) {
+              split<3>(d1, x);
+#pragma unroll
+              for (int s = 2; s >= 0; --s) mma_bf16_1688(z1, 0u, tri, x[s]);
+              own1 = d1.x + d1.y;
             }
+          } else {
+            ur0 = add2(ur0, d0);
+            ur1 = add2(ur1, d1);
+            dc[u] = add2(d0, d1);
           }
-          ur0 = add2(ur0, d0);
-          ur1 = add2(ur1, d1);
-          dc[u] = add2(d0, d1);
           uint32_t x0[PO], x1[PO];
           split<PO>(mul2(g0, l0), x0);
           split<PO>(mul2(g1, l1), x1);
@@ -622,7 +663,15 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
           mma_terms<PO, P>(dv[nt], a, b0);
           mma_terms<PO, P>(dv[nt + 1], a, b1);
         }
-        {  // the column sums: 4 values over the 8 lanes that share lane mod 4
+        if (k4 == 0) {
+          const bool b0 = lane & 1;
+          const float x = (c2 < g ? z0[0] : 0.f) + (c2 + 1 < g ? z0[1] : 0.f);
+          const float y = (z0[2] + z0[3]) + ((c2 < g ? z1[2] : 0.f) + (c2 + 1 < g ? z1[3] : 0.f));
+          float t = b0 ? y : x;
+          t += __shfl_xor_sync(0xffffffffu, b0 ? x : y, 1);
+          t += __shfl_xor_sync(0xffffffffu, t, 2);
+          if (!(lane & 2)) ph[g - c2 + (b0 ? 8 : 0)] = t;
+        } else {  // the column sums: 4 values over the 8 lanes that share lane mod 4
           const bool b4 = lane & 16, b3 = lane & 8;
           float2 s = b4 ? dc[1] : dc[0], o = b4 ? dc[0] : dc[1];
           s.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
@@ -633,10 +682,14 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
           if (!(lane & 4)) ph[16 * k4 + (b4 ? 8 : 0) + (b3 ? 1 : 0)] = t;
         }
       }
-      const float u0 = quad_sum(ur0.x + ur0.y), u1 = quad_sum(ur1.x + ur1.y);
-      if ((lane & 3) == 0) {
-        *spare(S::q, K, h, rb + g) = u0;
-        *spare(S::q, K, h, rb + g + 8) = u1;
+      {  // the rows' values over 4 lanes
+        const bool b0 = lane & 1, b1 = lane & 2;
+        const float u0 = ur0.x + ur0.y, u1 = ur1.x + ur1.y;
+        float x = b0 ? u1 : u0, y = b0 ? own1 : own0;
+        x += __shfl_xor_sync(0xffffffffu, b0 ? u0 : u1, 1);
+        y += __shfl_xor_sync(0xffffffffu, b0 ? own0 : own1, 1);
+        const float t = (b1 ? y : x) + __shfl_xor_sync(0xffffffffu, b1 ? x : y, 2);
+        *spare(b1 ? S::k : S::q, K, h, rb + g + (b0 ? 8 : 0)) = t;
       }
       // dv, with w_r (.) u
       const int hv = (hb * HB + h) * V;

@@ -43,7 +43,10 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const ScanParams p) {
                      : static_cast<const E*>(p.v) + b * p.vb + static_cast<size_t>(w.head0) * p.V;
   const long long val_t = REV ? static_cast<long long>(p.N) * p.V : p.vt;
   const float beta = to_f32(static_cast<const E*>(p.beta)[n]);
-  const float rate = -to_f32(static_cast<const E*>(p.alpha)[n]) * kLog2e;
+  // -alpha log2(e) to twice fp32: an error here would be the same for all of a
+  // head's tokens, which dalpha (a sum that nearly cancels) shows ten times over
+  const float alpha = -to_f32(static_cast<const E*>(p.alpha)[n]);
+  const float rate = alpha * kLog2e, rate_lo = fmaf(alpha, kLog2e, -rate) + alpha * kLog2eLo;
   const size_t head = static_cast<size_t>(b) * p.N + n;
   const size_t gate_extent = static_cast<size_t>(p.B) * p.N * p.nc * 192;
 
@@ -112,7 +115,7 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const ScanParams p) {
     } else {
       dt.x = gate_softplus(ga.x + beta);
       dt.y = gate_softplus(ga.y + beta);
-      float2 l = make_float2(rate * dt.x, rate * dt.y);
+      float2 l = make_float2(fmaf(rate, dt.x, rate_lo * dt.x), fmaf(rate, dt.y, rate_lo * dt.y));
       // below 2^-160 a decay is 0 in fp32: the bound keeps sums short
       l.x = l.x < -160.f ? -160.f : l.x;
       l.y = l.y < -160.f ? -160.f : l.y;
@@ -165,33 +168,50 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const ScanParams p) {
     if (on) {
       put(REV ? p.Rl : p.Hl, pairs * p.nc, static_cast<size_t>(gbx) * p.nc + c);
       const float2 dec = both(ex2(chunk_sum));
-#pragma unroll
-      for (int nt = 0; nt < KT; ++nt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) set_pair(acc[nt], h, mul2(pair(acc[nt], h), dec));
       const uint32_t kt = key0 + (i & 1) * kKey, vt = val0 + (i & 1) * kVal;
+      constexpr int G = F32 ? 1 : 4;  // steps of 16 tokens at a time (fp32 has more terms to hold)
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        uint32_t raw[P][4], a[PS][4];
-        load_a_t<P>(raw, vt, kVLd, 16 * ks, 16 * warp);
-        const float2 w0 = *reinterpret_cast<const float2*>(&weights[warp][16 * ks + c2]);
-        const float2 w1 = *reinterpret_cast<const float2*>(&weights[warp][16 * ks + 8 + c2]);
+      for (int k0 = 0; k0 < 4; k0 += G) {
+        uint32_t a[G][PS][4];  // the decayed values
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          uint32_t x[P], t[PS];
+        for (int ks = 0; ks < G; ++ks) {
+          const int t = 16 * (k0 + ks);
+          uint32_t raw[P][4];
+          load_a_t<P>(raw, vt, kVLd, t, 16 * warp);
+          const float2 w0 = *reinterpret_cast<const float2*>(&weights[warp][t + c2]);
+          const float2 w1 = *reinterpret_cast<const float2*>(&weights[warp][t + 8 + c2]);
 #pragma unroll
-          for (int s = 0; s < P; ++s) x[s] = raw[s][r];
-          split<PS>(mul2(join<P>(x), r < 2 ? w0 : w1), t);
+          for (int r = 0; r < 4; ++r) {
+            uint32_t x[P], y[PS];
 #pragma unroll
-          for (int s = 0; s < PS; ++s) a[s][r] = t[s];
+            for (int s = 0; s < P; ++s) x[s] = raw[s][r];
+            split<PS>(mul2(join<P>(x), r < 2 ? w0 : w1), y);
+#pragma unroll
+            for (int s = 0; s < PS; ++s) a[ks][s][r] = y[s];
+          }
         }
         constexpr int NX = KT >= 4 ? 4 : 2;
+        const float2 old = k0 == 0 ? dec : both(1.f);
 #pragma unroll
         for (int nt = 0; nt < KT; nt += NX) {
-          uint32_t bb[NX][P][2];
+          float x[NX][4];  // what these tokens add
 #pragma unroll
-          for (int n = 0; n < NX; n += 2) load_b2_t<P>(bb[n], bb[n + 1], kt, kLd, 16 * ks, 8 * (nt + n));
-          mma_terms_n<PS, P, NX>(reinterpret_cast<float(&)[NX][4]>(acc[nt]), a, bb);
+          for (int n = 0; n < NX; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+#pragma unroll
+          for (int ks = 0; ks < G; ++ks) {
+            uint32_t bb[NX][P][2];
+#pragma unroll
+            for (int n = 0; n < NX; n += 2)
+              load_b2_t<P>(bb[n], bb[n + 1], kt, kLd, 16 * (k0 + ks), 8 * (nt + n));
+            mma_terms_n<PS, P, NX>(x, a[ks], bb);
+          }
+#pragma unroll
+          for (int n = 0; n < NX; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              set_pair(acc[nt + n], h, fma2(pair(acc[nt + n], h), old, pair(x[n], h)));
         }
       }
     }

@@ -27,6 +27,8 @@ def m():
     ((1, 8, 64, 1, 1, 1, 1), -2),
     ((1, 8, 64, 4, 7, 1, 1), -1),   # dtype
     ((1, 8, 64, 4, 1, 1, 2), -1),   # activation
+    ((1, 8, 1 << 25, 4, 1, 1, 1), -2),          # C > 2^24
+    ((1, (1 << 30) + 1, 8, 4, 1, 1, 1), -2),    # T > 2^30
 ])
 def test_conv_refuses(m, shape, code):
     s = None if shape is None else ctypes.byref(m.ConvShape(*shape))

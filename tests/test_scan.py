@@ -290,6 +290,34 @@ def test_long_sequence(m2rnn, dtype):
     assert rel(y, ref["y"]) <= OUT_REL[dtype] and rel(HT, ref["HT"]) <= FP32_REL
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sums_do_not_drift(m2rnn, dtype):
+    """A state that hardly decays is a plain sum of many positive parts, where a
+    rounding that always goes one way would add up.  912 head blocks: the whole
+    sequence is one chain of chunks.
+
+    Tolerance: a part (16 tokens' products, or with bf16 inputs a chunk's) is off
+    by half of the last place 12 times at most, 12 * 2^-24 of itself; adding the
+    T/16 = 32 parts rounds the sum so far, on average half of the final one, by
+    2^-24 each time, in either direction: sqrt(32) / 2 * 2^-24.  Together < 15 * 2^-24 <
+    9e-7; the step sizes' and decays' own errors (2^-22 of a step, in either
+    direction over 512 tokens) add 2e-8."""
+    B, T, N, K, V = 912, 512, 2, 16, 32
+    g = torch.Generator(device="cuda").manual_seed(9)
+
+    def ru(*s):
+        return torch.rand(*s, generator=g, device="cuda").to(TD[dtype])
+    q, k, v, a = ru(B, T, 1, K), ru(B, T, 1, K), ru(B, T, N, V), ru(B, T, N)
+    alpha = torch.full((N,), 1e-3, device="cuda").to(TD[dtype])
+    beta = torch.full((N,), -4.0, device="cuda").to(TD[dtype])
+    H = m2rnn.scan_fwd(q, k, v, a, alpha, beta)[1]
+    z = a.double() + beta.double()
+    dt = torch.logaddexp(z, torch.zeros_like(z))
+    tail = (dt.sum(1, keepdim=True) - dt.cumsum(1)) * -alpha.double()
+    ref = torch.einsum("btn,btk,btnv->bnkv", torch.exp(tail) * dt, k[:, :, 0].double(), v.double())
+    assert rel(H, ref) < 9e-7
+
+
 def test_empty_sequence(m2rnn):
     d = make(2, 0, 4, 64, 16, 1, "bf16", 10)
     y, HT, _ = m2rnn.scan_fwd(*args(d), d["w_r"], d["H0"])
