@@ -575,8 +575,7 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
       uint32_t va[V / 16][P][4];
 #pragma unroll
       for (int vv = 0; vv < V / 16; ++vv) load_a<P>(va[vv], vs, kVLd, 16 * rt, h * V + 16 * vv);
-      float2 ur0 = make_float2(0.f, 0.f), ur1 = ur0;  // row sums of D: later blocks
-      float own0 = 0.f, own1 = 0.f;                   // own block
+      float2 ur0 = make_float2(0.f, 0.f), ur1 = ur0;  // row sums of D over later blocks
       float* ph = pcol + h * pcol_h;
       const float* li_at = lo + rb + c2;
       float between = 0.f;  // sum of l over the blocks between j's and i's
@@ -629,18 +628,16 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
           const float2 d0 = mul2(f0, g0), d1 = mul2(f1, g1);
           if (k4 == 0) {
             // sum of D over i >= t > j in the block: z = [i >= t] D^T, then row t's sum
-            // over j < t; D is 0 for j >= 8 > i
+            // over j < t; D is 0 for j >= 8 > i.  Row t = 0 of z is D's row sums.
             const uint32_t tri = (c2 >= g ? 0x3f80u : 0u) | (c2 + 1 >= g ? 0x3f800000u : 0u);
             uint32_t x[3];
             split<3>(d0, x);
 #pragma unroll
             for (int s = 2; s >= 0; --s) mma_bf16_1688(z0, u ? 0x3f803f80u : tri, u ? tri : 0u, x[s]);
-            own0 += d0.x + d0.y;
             if (u) {
               split<3>(d1, x);
 #pragma unroll
-              for (int s = 2; s >= 0; --s) mma_bf16_1688(z1, 0u, tri, x[s]);
-              own1 = d1.x + d1.y;
+              for (int s = 2; s >= 0; --s) mma_bf16_1688(z1, 0x3f803f80u, tri, x[s]);
             }
           } else {
             ur0 = add2(ur0, d0);
@@ -671,6 +668,14 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
           t += __shfl_xor_sync(0xffffffffu, b0 ? x : y, 1);
           t += __shfl_xor_sync(0xffffffffu, t, 2);
           if (!(lane & 2)) ph[g - c2 + (b0 ? 8 : 0)] = t;
+          if (g == 0) {
+            float* own = spare(S::k, K, h, rb + c2);
+            constexpr int row = ld / 2;  // floats
+            own[0] = z0[0];
+            own[row] = z0[1];
+            own[8 * row] = z1[0];
+            own[9 * row] = z1[1];
+          }
         } else {  // the column sums: 4 values over the 8 lanes that share lane mod 4
           const bool b4 = lane & 16, b3 = lane & 8;
           float2 s = b4 ? dc[1] : dc[0], o = b4 ? dc[0] : dc[1];
@@ -682,14 +687,13 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
           if (!(lane & 4)) ph[16 * k4 + (b4 ? 8 : 0) + (b3 ? 1 : 0)] = t;
         }
       }
-      {  // the rows' values over 4 lanes
-        const bool b0 = lane & 1, b1 = lane & 2;
+      {  // the row sums: 2 values over 4 lanes
+        const bool b0 = lane & 1;
         const float u0 = ur0.x + ur0.y, u1 = ur1.x + ur1.y;
-        float x = b0 ? u1 : u0, y = b0 ? own1 : own0;
-        x += __shfl_xor_sync(0xffffffffu, b0 ? u0 : u1, 1);
-        y += __shfl_xor_sync(0xffffffffu, b0 ? own0 : own1, 1);
-        const float t = (b1 ? y : x) + __shfl_xor_sync(0xffffffffu, b1 ? x : y, 2);
-        *spare(b1 ? S::k : S::q, K, h, rb + g + (b0 ? 8 : 0)) = t;
+        float t = b0 ? u1 : u0;
+        t += __shfl_xor_sync(0xffffffffu, b0 ? u0 : u1, 1);
+        t += __shfl_xor_sync(0xffffffffu, t, 2);
+        if (!(lane & 2)) *spare(S::q, K, h, rb + g + (b0 ? 8 : 0)) = t;
       }
       // dv, with w_r (.) u
       const int hv = (hb * HB + h) * V;
