@@ -127,18 +127,18 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
   auto ref_h = [&](const Place& w) { return state_ref(p, p.Hl, p.Hseg, p.cdec, w, c, hseg); };
   auto ref_r = [&](const Place& w) { return state_ref(p, p.Rl, p.Rseg, p.rdec, w, c, rseg); };
   // `threads` threads bring a state's tile, two rows each in flight.
-  auto fetch_state = [&](int thread, int threads, uint32_t dst, const float* base_of, const StateRef& r,
+  auto fetch_state = [&](int thread, int threads, uint32_t dst, const StateRef& r,
                          int n) {
     constexpr int U = 2;
     const int step = threads * 8;
 #pragma unroll 1
     for (int e0 = thread * 8; e0 < n; e0 += U * step) {
-      StateRow x[U];
+      StateRow<false> x[U];
       bool on[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int e = e0 + u * step;
-        on[u] = e < n && in_range(p.status, (r.own - base_of) + e, 8, st_extent, CHK_SCAN_WS);
+        on[u] = e < n && in_range(p.status, r.at + e, 8, st_extent, CHK_SCAN_WS);
         if (on[u]) x[u] = state_load<K, V>(p, r, e);
       }
 #pragma unroll
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
   };
   auto fetch_h = [&](int hb, int thread, int threads) {
     const Place w = place_in(p, HB, b, group, hb);
-    fetch_state(thread, threads, hs, p.Hl, ref_h(w), w.heads * V * K);
+    fetch_state(thread, threads, hs, ref_h(w), w.heads * V * K);
   };
   auto fetch_rest = [&](int hb) {
     const Place w = place_in(p, HB, b, group, hb);
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
     load_tile<F32, kCols>(tid, us, u, ut, rows, w.heads * V, p.status, p.T - t0);
     load_gate(tid, base + S::gate, p, w, c);
     ptx::cp_async_commit();
-    if (!F32) fetch_state(tid, kThreads, rs, p.Rl, ref_r(w), w.heads * V * K);
+    if (!F32) fetch_state(tid, kThreads, rs, ref_r(w), w.heads * V * K);
   };
   // fp32: R in H's place, and <R, H> with H from memory, in shares of 256
   // elements (a warp's pass).
@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
 #pragma unroll 1
     for (int e = tid * 8; e < w.heads * V * K; e += kThreads * 8) {
       // (a warp's 256 elements together: its lanes sum below)
-      if (!in_range(p.status, (fh.own - p.Hl) + e / 256 * 256, 256, st_extent, CHK_SCAN_WS)) continue;
-      const StateRow xr = state_load<K, V>(p, fh, e), yr = state_load<K, V>(p, fr, e);
+      if (!in_range(p.status, fh.at + e / 256 * 256, 256, st_extent, CHK_SCAN_WS)) continue;
+      const StateRow<false> xr = state_load<K, V>(p, fh, e), yr = state_load<K, V>(p, fr, e);
       float2 x[4], y[4];
       state_sum(xr, x);
       state_sum(yr, y);

@@ -27,7 +27,8 @@ struct OutSmem {
   static constexpr int bytes = gate + HB * 192 * 4;
 };
 
-template <bool F32, int KT, int V>
+// SHORT: the states come in bf16.
+template <bool F32, int KT, int V, bool SHORT>
 __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_kernel(const ScanParams p) {
   using E = typename Elem<F32>::T;
   using S = OutSmem<F32, KT, V>;
@@ -58,24 +59,24 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_ke
     load_tile<F32, kCols>(threadIdx.x, vs, v, p.vt, rows, w.heads * V, p.status, p.T - t0);
     load_gate(threadIdx.x, base + S::gate, p, w, c);
     ptx::cp_async_commit();
-    const StateRef r = state_ref(p, p.Hl, p.Hseg, p.cdec, w, c, seg);
+    const StateRef r = state_ref<SHORT>(p, p.Hl, p.Hseg, p.cdec, w, c, seg);
     constexpr int step = kThreads * 8, U = kCols * K >= 2 * step ? 2 : 1;  // rows in flight
     const int n = w.heads * V * K;
 #pragma unroll 1
     for (int e0 = threadIdx.x * 8; e0 < n; e0 += U * step) {
-      StateRow x[U];
+      StateRow<SHORT> x[U];
       bool on[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int e = e0 + u * step;
-        on[u] = e < n && in_range(p.status, (r.own - p.Hl) + e, 8, hl_extent, CHK_SCAN_WS);
-        if (on[u]) x[u] = state_load<K, V>(p, r, e);
+        on[u] = e < n && in_range(p.status, r.at + e, 8, hl_extent, CHK_SCAN_WS);
+        if (on[u]) x[u] = state_load<K, V, SHORT>(p, r, e);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (on[u]) {
           float2 z[4];
-          state_sum(x[u], z);
+          state_sum<!F32>(x[u], z);  // (the same y with and without a saved forward pass)
           put_state_row<PO, K>(hs, e0 + u * step, z);
         }
     }
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_ke
     __syncthreads();
     if (hb + 1 < hb1) {
       const Place next = place_in(p, HB, b, group, hb + 1);
-      state_prefetch(threadIdx.x, state_ref(p, p.Hl, p.Hseg, p.cdec, next, c, seg), next.heads * V * K);
+      state_prefetch<SHORT>(threadIdx.x, state_ref<SHORT>(p, p.Hl, p.Hseg, p.cdec, next, c, seg), next.heads * V * K);
     }
     float acc[8][4];
 #pragma unroll
@@ -262,33 +263,37 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_ke
   }
 }
 
-template <bool F32, int KT, int V>
+template <bool F32, int KT, int V, bool SHORT>
 cudaError_t run(const ScanParams& p, cudaStream_t st) {
   constexpr int smem = OutSmem<F32, KT, V>::bytes;
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
-  const cudaError_t e = allow_smem<out_kernel<F32, KT, V>>(smem);
+  const cudaError_t e = allow_smem<out_kernel<F32, KT, V, SHORT>>(smem);
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(p.B) * p.Nq * p.hsplit * p.nc;
-  out_kernel<F32, KT, V><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(p);
+  out_kernel<F32, KT, V, SHORT><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
-template <bool F32, int V>
+template <bool F32, int V, bool SHORT>
 cudaError_t run_k(const ScanParams& p, cudaStream_t st) {
   switch (p.K) {
-    case 16: return run<F32, 2, V>(p, st);
-    case 32: return run<F32, 4, V>(p, st);
-    case 64: return run<F32, 8, V>(p, st);
-    default: return run<F32, 16, V>(p, st);
+    case 16: return run<F32, 2, V, SHORT>(p, st);
+    case 32: return run<F32, 4, V, SHORT>(p, st);
+    case 64: return run<F32, 8, V, SHORT>(p, st);
+    default: return run<F32, 16, V, SHORT>(p, st);
   }
+}
+template <int V>
+cudaError_t run_type(const ScanParams& p, bool f32, cudaStream_t st) {
+  if (f32) return run_k<true, V, false>(p, st);
+  return p.short_states ? run_k<false, V, true>(p, st) : run_k<false, V, false>(p, st);
 }
 
 }  // namespace
 }  // namespace scan
 
 cudaError_t launch_scan_out(const ScanParams& p, bool f32, cudaStream_t st) {
-  if (p.V == 16) return f32 ? scan::run_k<true, 16>(p, st) : scan::run_k<false, 16>(p, st);
-  return f32 ? scan::run_k<true, 32>(p, st) : scan::run_k<false, 32>(p, st);
+  return p.V == 16 ? scan::run_type<16>(p, f32, st) : scan::run_type<32>(p, f32, st);
 }
 
 }  // namespace m2rnn
