@@ -21,8 +21,8 @@
  *
  * Gradients.  The gradients of activations (dx, dq, dk, dv, da) are summed
  * in fp32 and rounded once to in_dtype, the type the preceding layer takes
- * them in; those of parameters and of fp32 states are fp32.  Every sum runs in a fixed order: the same
- * inputs give the same bits.
+ * them in; those of parameters and of fp32 states are fp32.  Every sum runs
+ * in a fixed order: the same inputs give the same bits.
  */
 #ifndef M2RNN_BLOCK_H_
 #define M2RNN_BLOCK_H_

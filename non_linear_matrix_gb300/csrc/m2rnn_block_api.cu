@@ -200,18 +200,20 @@ ScanPlan scan_plan(const m2rnn_shape* s) {
   return q;
 }
 
-// CTAs that share a chunk's head blocks.  Outputs: enough CTAs (1,824, three
-// times what is resident) that they even out over the SMs; a CTA's own cost, its
-// q and k tiles and their product, is about 0.4 of a head block.
+// CTAs that share a chunk's head blocks.  Outputs: about 1,216 (twice what is
+// resident), so that they even out over the SMs; a CTA's own cost, its q and k tiles
+// and their product, is about 0.4 of a head block.  B=8 T=2048 N=32 (256 chunks, 8
+// head blocks): 52 us, with one CTA per chunk 63, with 3,648 53.
 int scan_out_split(const m2rnn_shape* s, const ScanPlan& q) {
   const long long chunks = static_cast<long long>(s->B) * (s->Nq == 0 ? 1 : s->Nq) * q.nc;
-  long long want = (1824 + chunks - 1) / chunks;
+  long long want = (1216 + chunks - 1) / chunks;
   if (want > q.nhb) want = q.nhb;
   const int per = static_cast<int>((q.nhb + want - 1) / want);
   return (q.nhb + per - 1) / per;
 }
 // Gradients: more than one costs shares of dq and dk in fp32, so only as many as
-// it takes to give each SM its two resident CTAs.
+// it takes to give each SM its two resident CTAs.  A training step at B=1 T=8192
+// N=32 (128 chunks) takes 139 us so, 181 with one CTA per chunk, 144 with 608 CTAs.
 int scan_bwd_split(const m2rnn_shape* s, const ScanPlan& q) {
   const long long chunks = static_cast<long long>(s->B) * (s->Nq == 0 ? 1 : s->Nq) * q.nc;
   long long want = 304 / chunks;

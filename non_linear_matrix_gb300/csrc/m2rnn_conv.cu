@@ -8,16 +8,17 @@
 //
 // with F = [state; x] along time (F[0..W-2] the carried inputs).
 //
-// All three kernels are bound by HBM traffic, the backward one closely followed
-// by instruction issue (about 40 for each pair of values).  A thread owns a few
+// All three kernels are bound by HBM traffic, with instruction issue close behind
+// (the backward kernel takes about 40 for each pair of values).  A thread owns a few
 // neighbouring channels and walks along time with the last W rows of F
 // (backward: and of dz) in registers, so each value is loaded once apart from the
 // W - 1 rows before a thread's run, which its neighbour has just pulled into
 // L2; the next rows are loaded while these are worked on.  Neighbouring lanes own
 // neighbouring channels: every row is read in whole lines.  Channels are few per
-// thread (4 forward, 2 backward) so that 32 warps fit on an SM: with 8 (16-byte
-// loads) the registers left 16 and the prompt took 77 us instead of FWD_US
-// (B=1 T=65536 C=1152), with 4 backward 110 us instead of BWD_US (B=8 T=4096 C=640).
+// thread (4 forward, 2 backward) so that 24 warps fit on an SM: with 8 (16-byte
+// loads) the forward kernel took 77 us instead of 53 (B=1 T=65536 C=1152, 302 MB:
+// 5.7 TB/s), with 4 the backward one 110 us instead of 37 (B=8 T=4096 C=640,
+// 126 MB: 3.4 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -432,7 +433,8 @@ cudaError_t bwd_w(const ConvParams& p, bool grad_f32, cudaStream_t st) {
 
 // Tokens per thread: long runs re-read fewer rows at their start (W - 1 of
 // TT), short ones give more threads; the longest run that still leaves
-// 2,048 threads for each SM, 4 tokens at least.
+// 2,048 threads for each SM, 4 tokens at least.  B=8 T=4096 C=640: 17.2 us, asking
+// for 8,192 26.7, for 512 16.4; T=2048 C=640: 4.7 (4.7, 4.8).
 int conv_fwd_tokens(const m2rnn_conv_shape* s, int sms) {
   const long long per_token = static_cast<long long>(s->B) * (s->C / 4);
   int tt = 32;
@@ -443,7 +445,7 @@ int conv_fwd_tokens(const m2rnn_conv_shape* s, int sms) {
 // CTAs of eight warps for 64 channels each, as many as are resident (456: three
 // for each of 152 SMs) and no more, so that they end together and the parts
 // stay few; the sequences are cut so that each warp has one run, 8 rows at
-// least.
+// least.  B=8 T=4096 C=640: 37 us, with 228 CTAs 57, with 912 41.
 void conv_bwd_plan(const m2rnn_conv_shape* s, int* TT, int* nT, int* nparts) {
   const long long rows = static_cast<long long>(s->T) + s->W - 1;
   const long long groups = (s->C + 63) / 64;
