@@ -222,6 +222,7 @@ template <bool F32, bool G32, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) conv_bwd_kernel(const ConvParams p) {
   using E = typename Elem<F32>::T;
   using G = typename Elem<G32>::T;
+  let_next_begin();
   constexpr int VEC = 2, kWarps = kThreads / 32, U = 4;
   __shared__ float sums[kWarps][32 * VEC * (W + 1)];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -209,6 +209,7 @@ template <bool F32, bool G32, int LPR>
 __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const QkParams p) {
   using E = typename Elem<F32>::T;
   using G = typename Elem<G32>::T;
+  let_next_begin();
   constexpr int U = 2, kGroups = kThreads / LPR;
   __shared__ float sums[2][kGroups][8 * LPR + 1];
   const float inv_k = 1.f / static_cast<float>(p.K);

@@ -16,6 +16,8 @@ namespace {
 template <bool F32>
 __global__ void __launch_bounds__(256) add_shares_kernel(const ScanParams p) {
   using E = typename Elem<F32>::T;
+  let_next_begin();
+  await_before();
   const size_t n = static_cast<size_t>(p.B) * p.T * p.Nq * p.K;
   const size_t at = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (at >= 2 * n) return;
@@ -43,12 +45,10 @@ cudaError_t launch_scan_bwd(const ScanParams& p, bool f32, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (p.hsplit > 1) {
     const size_t n4 = static_cast<size_t>(p.B) * p.T * p.Nq * p.K / 2;  // 2 n / 4
-    const unsigned grid = static_cast<unsigned>((n4 + 255) / 256);
-    if (f32)
-      add_shares_kernel<true><<<grid, 256, 0, st>>>(p);
-    else
-      add_shares_kernel<false><<<grid, 256, 0, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>((n4 + 255) / 256));
+    e = f32 ? launch_after(add_shares_kernel<true>, grid, 256, 0, st, p)
+            : launch_after(add_shares_kernel<false>, grid, 256, 0, st, p);
+    if (e != cudaSuccess) return e;
   }
   const SumOut o{{p.dalpha, p.dbeta, p.dw_r}, {p.N, p.N, p.N * p.V}};
   return launch_sum_parts(p.part, p.B * p.nc, o, p.status, CHK_SCAN_PARAM, st);

@@ -199,6 +199,8 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
   auto spare = [&](int tile, int width, int h, int row) {
     return reinterpret_cast<float*>(smem + tile + (row * (width + 8) + width) * 2) + h;
   };
+  let_next_begin();
+  await_before();  // (q and k are inputs)
   if (sside) {
     fetch_h(hb0, tid, kThreads);
     cp_async_wait<0>();
@@ -762,8 +764,7 @@ cudaError_t launch_bwd_kt(const ScanParams& p, cudaStream_t st) {
   const cudaError_t e = allow_smem<bwd_kernel<F32, KT, V>>(bytes);
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(p.B) * p.Nq * p.hsplit * p.nc;
-  bwd_kernel<F32, KT, V><<<static_cast<unsigned>(grid), 2 * kThreads, bytes, st>>>(p);
-  return cudaGetLastError();
+  return launch_after(bwd_kernel<F32, KT, V>, dim3(static_cast<unsigned>(grid)), 2 * kThreads, bytes, st, p);
 }
 
 }  // namespace

@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_ke
         }
     }
   };
+  await_before();  // (q and k are inputs)
   fetch(hb0);
   cp_async_wait<1>();
   __syncthreads();
@@ -277,8 +278,7 @@ cudaError_t run(const ScanParams& p, cudaStream_t st) {
   const cudaError_t e = allow_smem<out_kernel<F32, KT, V, SHORT>>(smem);
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(p.B) * p.Nq * p.hsplit * p.nc;
-  out_kernel<F32, KT, V, SHORT><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_after(out_kernel<F32, KT, V, SHORT>, dim3(static_cast<unsigned>(grid)), kThreads, smem, st, p);
 }
 
 template <bool F32, int V, bool SHORT>

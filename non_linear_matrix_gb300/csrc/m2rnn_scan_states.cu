@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? (KT == 16 ? 2 : 3) : KT == 16 
     }
   };
 
+  let_next_begin();
   fetch_gate(0);
   fetch(0);
   // state: accumulator nt holds (column 16 warp + g [+8], key row 8 nt + c2, +1)
@@ -267,6 +268,8 @@ __global__ void __launch_bounds__(kThreads, F32 ? (KT == 16 ? 2 : 3) : KT == 16 
 // neighbouring elements of a tile; grid y runs over the tiles.
 __global__ void __launch_bounds__(256) join_kernel(const ScanParams p, float* ends, const float* cdec,
                                                    float* fin, int first_pair) {
+  let_next_begin();
+  await_before();
   const int per = kCols * p.K, at = (blockIdx.x * 256 + threadIdx.x) * 4;
   if (at >= per) return;
   const int gbx = first_pair + blockIdx.y, groups = p.Nq * p.nhb;
@@ -323,9 +326,12 @@ cudaError_t run(const ScanParams& p, cudaStream_t st) {
   states_kernel<F32, KT, REV, SHORT><<<static_cast<unsigned>(pairs * p.nseg), kThreads, smem, st>>>(p);
   if (p.nseg > 1)
     for (long long y0 = 0; y0 < pairs; y0 += 65535)  // (nseg > 1 means few pairs: one launch)
-      join_kernel<<<dim3((kCols * K / 4 + 255) / 256, static_cast<unsigned>(pairs - y0 < 65535 ? pairs - y0 : 65535)),
-                    256, 0, st>>>(p, REV ? p.Rseg : p.Hseg, REV ? p.rdec : p.cdec,
-                                  REV ? p.dH0 : p.HT, static_cast<int>(y0));
+    {
+      const dim3 grid((kCols * K / 4 + 255) / 256, static_cast<unsigned>(pairs - y0 < 65535 ? pairs - y0 : 65535));
+      const cudaError_t j = launch_after(join_kernel, grid, 256, 0, st, p, REV ? p.Rseg : p.Hseg,
+                                         REV ? p.rdec : p.cdec, REV ? p.dH0 : p.HT, static_cast<int>(y0));
+      if (j != cudaSuccess) return j;
+    }
   return cudaGetLastError();
 }
 

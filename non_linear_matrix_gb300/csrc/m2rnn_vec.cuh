@@ -151,6 +151,29 @@ __device__ __forceinline__ void store_vec(typename Elem<F32>::T* dst, const floa
   raw_store<F32, VEC>(dst, raw_pack<F32, VEC>(o));
 }
 
+// A kernel launched by launch_after may begin while the one before it in the
+// stream still runs (once all of that one's CTAs have called let_next_begin or
+// ended); await_before returns when it has ended and its writes are seen.  Such a
+// kernel calls await_before before it touches anything but the call's inputs.
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void await_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                         const A&... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 // Sums part[nparts][n0 + n1 + n2] over the parts, always in the same order,
 // into up to three outputs (NULL: skipped).  A CTA takes 32 columns, its 32
 // warps every 32nd part each; the warps' sums are added in warp order.
@@ -166,6 +189,7 @@ static __global__ void __launch_bounds__(1024)
   const int n = o.n[0] + o.n[1] + o.n[2];
   const int col = blockIdx.x * 32 + lane;
   float s = 0.f;
+  await_before();
   if (col < n) {
 #pragma unroll 8
     for (int r = warp; r < nparts; r += 32) {
@@ -193,8 +217,7 @@ static __global__ void __launch_bounds__(1024)
 static cudaError_t launch_sum_parts(const float* part, int nparts, const SumOut& o, int* status,
                                     int site, cudaStream_t st) {
   const int n = o.n[0] + o.n[1] + o.n[2];
-  sum_parts_kernel<<<(n + 31) / 32, 1024, 0, st>>>(part, nparts, o, status, site);
-  return cudaGetLastError();
+  return launch_after(sum_parts_kernel, dim3((n + 31) / 32), 1024, 0, st, part, nparts, o, status, site);
 }
 
 }  // namespace m2rnn
