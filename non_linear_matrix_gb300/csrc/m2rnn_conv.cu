@@ -48,8 +48,8 @@ __device__ __forceinline__ float2 sigmoid2(float2 z) {
   }
 }
 
-// Row m of F for channels c0.. of batch item b (m in [0, T + W - 1)).
-template <bool F32, int VEC, int W>
+// Row m of F for channels c0.. of batch item b (m in [0, T + W - 1)).  CONST: see raw_load.
+template <bool F32, int VEC, int W, bool CONST = true>
 __device__ __forceinline__ Raw<F32, VEC> row_of(const ConvParams& p, int b, long long m, int c0) {
   using E = typename Elem<F32>::T;
   if (m >= W - 1) {
@@ -57,13 +57,13 @@ __device__ __forceinline__ Raw<F32, VEC> row_of(const ConvParams& p, int b, long
     if (!in_range(p.status, static_cast<size_t>(t), 1, p.T, CHK_CONV_IN) ||
         !in_range(p.status, c0, VEC, p.C, CHK_CONV_IN))
       return raw_zero<F32, VEC>();
-    return raw_load<F32, VEC>(static_cast<const E*>(p.x) + b * p.xb + t * p.xt + c0);
+    return raw_load<F32, VEC, CONST>(static_cast<const E*>(p.x) + b * p.xb + t * p.xt + c0);
   }
   if (p.state == nullptr) return raw_zero<F32, VEC>();
   const size_t at = (static_cast<size_t>(b) * (W - 1) + m) * p.C + c0;
   if (!in_range(p.status, at, VEC, static_cast<size_t>(p.B) * (W - 1) * p.C, CHK_CONV_IN))
     return raw_zero<F32, VEC>();
-  return raw_load<F32, VEC>(static_cast<const E*>(p.state) + at);
+  return raw_load<F32, VEC, CONST>(static_cast<const E*>(p.state) + at);
 }
 
 // The taps of VEC channels, as pairs of channels for each tap, and their bias.
@@ -183,7 +183,8 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) conv_fwd_kernel(const C
   }
 }
 
-// One thread: 4 channels of one sequence; the state may be updated in place.
+// One thread: 4 channels of one sequence; the state may be updated in place, so it
+// is read by plain loads.
 template <bool F32, int W, bool SILU>
 __global__ void __launch_bounds__(128) conv_step_kernel(const ConvParams p) {
   using E = typename Elem<F32>::T;
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvParams p) {
   Raw<F32, VEC> r[W];
   float2 f[W][VEC / 2], w[W][VEC / 2], bias[VEC / 2], o[VEC / 2];
 #pragma unroll
-  for (int i = 0; i < W; ++i) r[i] = row_of<F32, VEC, W>(p, b, i, c0);
+  for (int i = 0; i < W; ++i) r[i] = row_of<F32, VEC, W, false>(p, b, i, c0);
   load_taps<F32, VEC, W>(p, c0, w, bias);
 #pragma unroll
   for (int i = 0; i < W; ++i) raw_unpack2<F32, VEC>(r[i], f[i]);

@@ -371,7 +371,10 @@ __device__ __forceinline__ StateRef state_ref(const ScanParams& p, const float* 
 }
 
 // Eight values of a state (a row of a block), element e of the tile: the loads,
-// and apart from them the sum, so that several rows' loads can be in flight.
+// and apart from them the sum, so that several rows' loads can be in flight.  Plain
+// loads, never the read-only path: a kernel that await_before holds back is resident
+// while its predecessors still write the states and decays, and a load that
+// promises read-only memory may be moved in front of the wait.
 template <bool SHORT>
 struct StateRow {
   float4 a, b, s, t;  // SHORT: a holds the eight values
@@ -381,17 +384,17 @@ template <int K, int V, bool SHORT = false>
 __device__ __forceinline__ StateRow<SHORT> state_load(const ScanParams& p, const StateRef& r, int e) {
   StateRow<SHORT> x;
   if constexpr (SHORT) {
-    x.a = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const __nv_bfloat16*>(r.own) + e));
+    x.a = *reinterpret_cast<const float4*>(reinterpret_cast<const __nv_bfloat16*>(r.own) + e);
   } else {
-    x.a = __ldg(reinterpret_cast<const float4*>(r.own + e));
-    x.b = __ldg(reinterpret_cast<const float4*>(r.own + e) + 1);
+    x.a = *reinterpret_cast<const float4*>(r.own + e);
+    x.b = reinterpret_cast<const float4*>(r.own + e)[1];
   }
   x.s = x.t = make_float4(0.f, 0.f, 0.f, 0.f);
   x.dec = 0.f;
   if (r.start != nullptr) {
-    x.s = __ldg(reinterpret_cast<const float4*>(r.start + e));
-    x.t = __ldg(reinterpret_cast<const float4*>(r.start + e) + 1);
-    x.dec = __ldg(r.dec + static_cast<size_t>(e / (K * V)) * p.nc);
+    x.s = *reinterpret_cast<const float4*>(r.start + e);
+    x.t = reinterpret_cast<const float4*>(r.start + e)[1];
+    x.dec = r.dec[static_cast<size_t>(e / (K * V)) * p.nc];
   }
   return x;
 }

@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(256) join_kernel(const ScanParams p, float* en
       if (g < p.nseg && in_range(p.status, (static_cast<size_t>(gbx) * p.nseg + g) * per + at, 4, extent,
                                  CHK_SCAN_WS)) {
         x[u] = *reinterpret_cast<const float4*>(own + static_cast<size_t>(g) * per);
-        d[u] = __ldg(dec + g);
+        d[u] = dec[g];  // (written by the kernel before: not read-only memory)
       }
     }
 #pragma unroll

@@ -62,19 +62,27 @@ __device__ __forceinline__ Raw<F32, VEC> raw_zero() {
   return r;
 }
 
-template <bool F32, int VEC>
+// CONST: through the read-only path, for memory that nobody writes while the kernel
+// is resident (a call's inputs, unless the call may update them in place).
+template <bool F32, int VEC, bool CONST = true>
 __device__ __forceinline__ Raw<F32, VEC> raw_load(const typename Elem<F32>::T* src) {
+  const auto get = [](const auto* p) {
+    if constexpr (CONST)
+      return __ldg(p);
+    else
+      return *p;
+  };
   Raw<F32, VEC> r;
   if constexpr (sizeof(r.w) == 4) {
-    r.w[0] = __ldg(reinterpret_cast<const unsigned int*>(src));
+    r.w[0] = get(reinterpret_cast<const unsigned int*>(src));
   } else if constexpr (sizeof(r.w) == 8) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
+    const uint2 u = get(reinterpret_cast<const uint2*>(src));
     r.w[0] = u.x;
     r.w[1] = u.y;
   } else {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(r.w) / 16); ++i) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + i);
+      const uint4 u = get(reinterpret_cast<const uint4*>(src) + i);
       r.w[4 * i] = u.x;
       r.w[4 * i + 1] = u.y;
       r.w[4 * i + 2] = u.z;
