@@ -5,10 +5,14 @@ output tensors with torch, passes raw device pointers and the current CUDA
 stream to the C ABI and turns non-zero status codes into exceptions.  Every
 step of the recurrence runs in the library's CUDA kernels; if the library is
 not built this module raises instead of computing anything itself.
+
+A call with ``stream=`` behaves as under ``torch.cuda.stream(stream)``: it is queued
+there, and what it allocates is that stream's memory.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -146,6 +150,36 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _tensors(r):
+    """The tensors of a call's result (a tensor, a dict or a tuple)."""
+    if isinstance(r, (dict, tuple)):
+        for x in r.values() if isinstance(r, dict) else r:
+            yield from _tensors(x)
+    elif r is not None:
+        yield r
+
+
+def _on_stream(call):
+    """``call`` with ``stream=``: what it allocates (scratch that it drops on return,
+    results) comes from that stream's own memory.  Taken from the current
+    stream's, the scratch could go to the next allocation there while the call still
+    works in it, or still be in use by what was queued there before.  The
+    results are marked as used on the current stream too, so that the caller may drop
+    them while work that was queued there reads them."""
+    @functools.wraps(call)
+    def on_stream(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        caller = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            r = call(*args, stream=stream, **kw)
+        if stream != caller:
+            for t in _tensors(r):
+                t.record_stream(caller)
+        return r
+    return on_stream
+
+
 def make_shape(q, v, ckpt_every: int = 0) -> Shape:
     """Shape of a call; q is [B,T,K] (shared by all heads) or [B,T,Nq,K]
     (Nq query/key groups)."""
@@ -161,6 +195,7 @@ def num_checkpoints(shape: Shape) -> int:
     return int(lib().m2rnn_num_checkpoints(ctypes.byref(shape)))
 
 
+@_on_stream
 def fwd(q, k, v, f, W, w_r, H0=None, *, ckpt_every: int = 0, want_HT: bool = True,
         out=None, stream=None):
     """Forward pass.  Returns (y, H_T or None, ckpt or None).
@@ -189,6 +224,7 @@ def fwd(q, k, v, f, W, w_r, H0=None, *, ckpt_every: int = 0, want_HT: bool = Tru
     return y, HT, ck
 
 
+@_on_stream
 def fwd_gated(q, k, v, a, alpha, beta, W, w_r, H0=None, *, ckpt_every: int = 0,
               want_HT: bool = True, out=None, stream=None):
     """Forward pass with the fused input gate f = exp(-alpha softplus(a + beta)),
@@ -216,6 +252,7 @@ def fwd_gated(q, k, v, a, alpha, beta, W, w_r, H0=None, *, ckpt_every: int = 0,
     return y, HT, ck
 
 
+@_on_stream
 def decode(q, k, v, f, W, w_r, H, *, H_out=None, y=None, stream=None):
     """One decode step for B sequences.  Returns (y, H_out).
 
@@ -242,6 +279,7 @@ def decode(q, k, v, f, W, w_r, H, *, H_out=None, y=None, stream=None):
     return y, H_out
 
 
+@_on_stream
 def decode_gated(q, k, v, a, alpha, beta, W, w_r, H, *, H_out=None, y=None, stream=None):
     """One decode step with the fused input gate: a [B,N], alpha and beta
     [N] replace f; otherwise as ``decode``.  Returns (y, H_out)."""
@@ -269,6 +307,7 @@ def bwd_workspace_size(shape: Shape, ckpt_given: bool) -> int:
     return int(lib().m2rnn_bwd_workspace_size(ctypes.byref(shape), int(bool(ckpt_given))))
 
 
+@_on_stream
 def bwd(q, k, v, f, W, w_r, dy, H0=None, ckpt=None, dHT=None, *, ckpt_every: int = 64,
         want_dH0: bool = False, want_dckpt: bool = False, workspace=None, out=None,
         stream=None):
@@ -310,6 +349,7 @@ def bwd(q, k, v, f, W, w_r, dy, H0=None, ckpt=None, dHT=None, *, ckpt_every: int
     return g
 
 
+@_on_stream
 def bwd_noalloc(q, k, v, f, W, w_r, dy, H0=None, dHT=None, *, ckpt_every: int = 64,
                 want_dH0: bool = False, out=None, stream=None):
     """Backward pass that allocates nothing inside the library (checkpoints
@@ -336,6 +376,7 @@ def bwd_noalloc(q, k, v, f, W, w_r, dy, H0=None, dHT=None, *, ckpt_every: int = 
     return g
 
 
+@_on_stream
 def bwd_gated(q, k, v, a, alpha, beta, W, w_r, dy, H0=None, ckpt=None, dHT=None, *,
               ckpt_every: int = 64, want_dH0: bool = False, want_dckpt: bool = False,
               workspace=None, out=None, stream=None):
@@ -373,6 +414,7 @@ def bwd_gated(q, k, v, a, alpha, beta, W, w_r, dy, H0=None, ckpt=None, dHT=None,
     return g
 
 
+@_on_stream
 def fwd_norm(q, k, v, f, W, w_r, g, w_norm, eps: float = 0.0, H0=None, *, gate=None,
              ckpt_every: int = 0, want_HT: bool = True, out=None, stream=None):
     """Forward pass with the readout epilogue out = w_norm (.) (y (.) g) rstd,
@@ -403,6 +445,7 @@ def fwd_norm(q, k, v, f, W, w_r, g, w_norm, eps: float = 0.0, H0=None, *, gate=N
     return r
 
 
+@_on_stream
 def bwd_norm(q, k, v, f, W, w_r, g, w_norm, y, rstd, dout, H0=None, ckpt=None, dHT=None, *,
              gate=None, ckpt_every: int = 64, want_dH0: bool = False, want_dckpt: bool = False,
              workspace=None, out=None, stream=None):
@@ -564,6 +607,7 @@ def _grad_code(dy, x) -> int:
     return _dtype_code(dy)
 
 
+@_on_stream
 def conv_fwd(x, w, bias=None, state=None, *, silu: bool = True, want_state: bool = True,
              out=None, stream=None):
     """Short causal convolution along time with SiLU (or none, silu=False).
@@ -585,6 +629,7 @@ def conv_fwd(x, w, bias=None, state=None, *, silu: bool = True, want_state: bool
     return y, so
 
 
+@_on_stream
 def conv_bwd(x, w, dy, bias=None, state=None, dstate_out=None, *, silu: bool = True,
              want_dstate: bool = False, workspace=None, out=None, stream=None):
     """Gradient of ``conv_fwd``: dict(dx, dw, dbias[, dstate]).  dy [B,T,C]
@@ -613,6 +658,7 @@ def conv_bwd(x, w, dy, bias=None, state=None, dstate_out=None, *, silu: bool = T
     return g
 
 
+@_on_stream
 def conv_step(x, w, state, bias=None, *, silu: bool = True, state_out=None, y=None, stream=None):
     """One token of the convolution for B sequences: x [B,C], state
     [B,W-1,C].  Returns (y, state_out); pass ``state_out=state`` to update
@@ -656,6 +702,7 @@ def _qk_args(q, k, wq, wk, cos, sin, pos, interleaved, grad_code):
     return s, _row_arg(q, 2), None if k is None else _row_arg(k, 2)
 
 
+@_on_stream
 def qk_norm_fwd(q, k, wq=None, wk=None, eps: float = 1e-6, *, cos=None, sin=None, pos=None,
                 interleaved: bool = False, out=None, stream=None):
     """RMS norm of every query and key head over its K features, times wq /
@@ -678,6 +725,7 @@ def qk_norm_fwd(q, k, wq=None, wk=None, eps: float = 1e-6, *, cos=None, sin=None
     return qo, ko
 
 
+@_on_stream
 def qk_norm_bwd(q, k, wq, wk, dqo, dko, eps: float = 1e-6, *, cos=None, sin=None, pos=None,
                 interleaved: bool = False, workspace=None, out=None, stream=None):
     """Gradient of ``qk_norm_fwd``: dict(dq, dk, dwq, dwk); dqo, dko are
@@ -721,6 +769,7 @@ def _scan_args(q, k, v, a, alpha, beta, w_r, lead: int):
     return Shape(B, T, N, K, V, _dtype_code(q), 0, Nq), rows
 
 
+@_on_stream
 def scan_fwd(q, k, v, a, alpha, beta, w_r=None, H0=None, *, want_HT: bool = True,
              save: bool = False, workspace=None, out=None, stream=None):
     """Selective scan H_t = exp(-alpha dt_t) H_{t-1} + dt_t k_t v_t^T, dt =
@@ -753,6 +802,7 @@ def scan_fwd(q, k, v, a, alpha, beta, w_r=None, H0=None, *, want_HT: bool = True
     return y, HT, saved
 
 
+@_on_stream
 def scan_bwd(q, k, v, a, alpha, beta, dy, w_r=None, H0=None, dHT=None, *, saved=None,
              want_dH0: bool = False, workspace=None, out=None, stream=None):
     """Gradient of ``scan_fwd`` for dL/dy = dy (v's dtype) and dL/dH_T = dHT
@@ -789,6 +839,7 @@ def scan_bwd(q, k, v, a, alpha, beta, dy, w_r=None, H0=None, dHT=None, *, saved=
     return g
 
 
+@_on_stream
 def scan_step(q, k, v, a, alpha, beta, H, w_r=None, *, H_out=None, y=None, stream=None):
     """One token of the selective scan for B sequences.  Returns (y, H_out).
 
