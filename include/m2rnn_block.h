@@ -142,8 +142,11 @@ typedef struct {
  * state before every 64th token and the gate's sums).  0 when T = 0. */
 size_t m2rnn_scan_saved_size(const m2rnn_shape *s);
 
-/* Bytes of workspace of m2rnn_scan_fwd; saved_given = 1 when `saved` is
- * passed. */
+/* Least bytes of workspace of m2rnn_scan_fwd; saved_given = 1 when `saved` is
+ * passed (0 then).  With fewer than m2rnn_scan_saved_size bytes, which bf16
+ * inputs allow (room for the fp32 states of half of the sequences), the call runs
+ * the sequences in two parts, one after the other, with the same results;
+ * m2rnn_scan_saved_size bytes let it run them at once. */
 size_t m2rnn_scan_fwd_workspace_size(const m2rnn_shape *s, int saved_given);
 
 /* saved: m2rnn_scan_saved_size(s) bytes, or NULL. */

@@ -113,7 +113,6 @@ struct ScanParams {
   float* cdec;    // [B][N][nc]: log2 decay from the segment's start to the chunk
   float* Hl;      // [B][Nq * nhb][nc][64 x K]: states before each chunk, without what
                   // came before their segment
-  bool short_states;  // Hl holds bf16: bf16 inputs and only the outputs read it
   float* Hseg;    // [B][Nq * nhb][nseg][64 x K]: states at the segments' ends
   float* rdec;    // cdec, Hl and Hseg of the reverse states
   float* Rl;

@@ -169,7 +169,7 @@ int qk_common(const m2rnn_qk_shape* s, const void* q, const m2rnn_rows* q_rows, 
 
 struct ScanPlan {
   int nc, hpg, nhb, nseg, cps;
-  size_t gate, dec, states, ends;  // bytes
+  size_t gate, dec, states, ends;  // bytes, for B sequences (sized_for)
   size_t saved() const { return gate + one_way(); }
   size_t one_way() const { return dec + states + ends; }
 };
@@ -178,6 +178,7 @@ struct ScanPlan {
 // where there are fewer (sequence, head block) pairs than 608 CTAs (the four that
 // are resident on each of 152 SMs), into runs of two chunks at least.  With 912 the
 // kernel took 115 us instead of 99 and the join 9.5 instead of 7.7 (B=1 T=65536 N=64).
+ScanPlan sized_for(ScanPlan q, const m2rnn_shape* s, int B);
 ScanPlan scan_plan(const m2rnn_shape* s) {
   ScanPlan q;
   const int Nq = s->Nq == 0 ? 1 : s->Nq;
@@ -191,8 +192,14 @@ ScanPlan scan_plan(const m2rnn_shape* s) {
   q.cps = static_cast<int>((q.nc + seg - 1) / seg);
   if (q.cps < 1) q.cps = 1;
   q.nseg = (q.nc + q.cps - 1) / q.cps;
+  return sized_for(q, s, s->B);
+}
+
+// The plan's buffers for `B` of the sequences.
+ScanPlan sized_for(ScanPlan q, const m2rnn_shape* s, int B) {
   const size_t tile = static_cast<size_t>(m2rnn::kCols) * s->K * sizeof(float);
-  const size_t heads = static_cast<size_t>(s->B) * s->N;
+  const size_t heads = static_cast<size_t>(B) * s->N;
+  const size_t pairs = static_cast<size_t>(B) * (s->Nq == 0 ? 1 : s->Nq) * q.nhb;
   q.gate = align256(heads * q.nc * 3 * m2rnn::kChunk * sizeof(float));
   q.dec = align256(heads * (q.nc + q.nseg) * sizeof(float));
   q.states = align256(pairs * q.nc * tile);
@@ -302,6 +309,23 @@ int scan_common(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void* q
   return M2RNN_OK;
 }
 
+// The parameters of `count` sequences from b0 on.
+m2rnn::ScanParams items_from(m2rnn::ScanParams p, int b0, int count, size_t e) {
+  const auto in = [&](const void* x, long long elems) {
+    return static_cast<const char*>(x) + b0 * elems * static_cast<long long>(e);
+  };
+  const long long state = static_cast<long long>(b0) * p.N * p.K * p.V;
+  p.q = in(p.q, p.qb);
+  p.k = in(p.k, p.kb);
+  p.v = in(p.v, p.vb);
+  p.a = in(p.a, p.ab);
+  p.y = const_cast<char*>(in(p.y, static_cast<long long>(p.T) * p.N * p.V));
+  if (p.H0 != nullptr) p.H0 += state;
+  if (p.HT != nullptr) p.HT += state;
+  p.B = count;
+  return p;
+}
+
 // Hands out pieces of the workspace.
 struct Carve {
   char* at;
@@ -311,6 +335,18 @@ struct Carve {
     return r;
   }
 };
+
+int scan_fwd_part(m2rnn::ScanParams p, const m2rnn_shape* s, const ScanPlan& plan, void* buffer,
+                  bool f32, cudaStream_t st) {
+  Carve keep{static_cast<char*>(buffer)};
+  p.gate = keep.take(plan.gate);
+  p.cdec = keep.take(plan.dec);
+  p.Hl = keep.take(plan.states);
+  p.Hseg = keep.take(plan.ends);
+  p.hsplit = scan_out_split(s, plan);
+  if (m2rnn::launch_scan_states(p, f32, false, st) != cudaSuccess) return M2RNN_ERR_CUDA;
+  return status_from_cuda(m2rnn::launch_scan_out(p, f32, st));
+}
 
 }  // namespace
 
@@ -491,7 +527,8 @@ size_t m2rnn_scan_fwd_workspace_size(const m2rnn_shape* s, int saved_given) {
   if (check_scan(s) != M2RNN_OK || s->T == 0) return 0;
   const ScanPlan q = scan_plan(s);
   if (saved_given) return 0;
-  return s->in_dtype == M2RNN_F32 ? q.saved() : q.saved() - q.states / 2;  // states in bf16
+  // with the states of half of the sequences the call runs in two parts
+  return s->in_dtype == M2RNN_F32 ? q.saved() : q.saved() - sized_for(q, s, s->B / 2).states;
 }
 
 int m2rnn_scan_fwd(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void* q,
@@ -518,18 +555,20 @@ int m2rnn_scan_fwd(const m2rnn_shape* s, const m2rnn_scan_rows* rows, const void
     if (workspace == nullptr || ws_bytes < need) return M2RNN_ERR_WORKSPACE;
     if ((rc = host_check_ptr(workspace, dev, true)) != M2RNN_OK) return rc;
   }
-  Carve keep{static_cast<char*>(saved ? saved : workspace)};
   p.y = y;
   p.HT = H_T;
-  p.gate = keep.take(plan.gate);
-  p.cdec = keep.take(plan.dec);
   const bool f32 = s->in_dtype == M2RNN_F32;
-  p.short_states = !f32 && saved == nullptr;
-  p.Hl = keep.take(p.short_states ? plan.states / 2 : plan.states);
-  p.Hseg = keep.take(plan.ends);
-  p.hsplit = scan_out_split(s, plan);
-  if (m2rnn::launch_scan_states(p, f32, false, st) != cudaSuccess) return M2RNN_ERR_CUDA;
-  return status_from_cuda(m2rnn::launch_scan_out(p, f32, st));
+  // All sequences at once, or in two parts where the workspace has the states of the
+  // larger one only; the segments are the same, and so are the results' bits.
+  const int most = saved != nullptr || ws_bytes >= plan.saved() ? s->B : s->B - s->B / 2;
+  for (int b0 = 0; b0 < s->B; b0 += most) {
+    m2rnn_shape part = *s;
+    part.B = s->B - b0 < most ? s->B - b0 : most;
+    const ScanPlan size = sized_for(plan, s, part.B);
+    const m2rnn::ScanParams x = items_from(p, b0, part.B, esize(s->in_dtype));
+    if ((rc = scan_fwd_part(x, &part, size, saved ? saved : workspace, f32, st)) != M2RNN_OK) return rc;
+  }
+  return M2RNN_OK;
 }
 
 size_t m2rnn_scan_bwd_workspace_size(const m2rnn_shape* s, int saved_given) {

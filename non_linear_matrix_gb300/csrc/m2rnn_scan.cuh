@@ -350,21 +350,19 @@ __device__ __forceinline__ Place place_of(const ScanParams& p, int b, int gb) {
 // A segment's first state is the one its predecessor ended with; the first
 // segment starts from the given state itself.
 struct StateRef {
-  const float* own;    // 64 x K, before the chunk, from the segment's start (bf16 if short)
+  const float* own;    // 64 x K, before the chunk, from the segment's start
   size_t at;           // its first element's place
   const float* start;  // 64 x K, at the segment's start (NULL: nothing to add)
   const float* dec;    // [heads * nc]: log2 decay from there, head h's at h * nc
 };
 // seg: the segment that made the chunk's state.
-template <bool SHORT = false>
 __device__ __forceinline__ StateRef state_ref(const ScanParams& p, const float* local,
                                               const float* ends, const float* dec, const Place& w,
                                               int c, int seg) {
   const size_t pair = (static_cast<size_t>(w.b) * p.Nq + w.group) * p.nhb + w.hb, tile = kCols * p.K;
   StateRef r;
   r.at = (pair * p.nc + c) * tile;
-  r.own = SHORT ? reinterpret_cast<const float*>(reinterpret_cast<const __nv_bfloat16*>(local) + r.at)
-                : local + r.at;
+  r.own = local + r.at;
   r.start = seg == 0 ? nullptr : ends + (pair * p.nseg + seg - 1) * tile;
   r.dec = dec + (static_cast<size_t>(w.b) * p.N + w.head0) * p.nc + c;
   return r;
@@ -375,20 +373,15 @@ __device__ __forceinline__ StateRef state_ref(const ScanParams& p, const float* 
 // loads, never the read-only path: a kernel that await_before holds back is resident
 // while its predecessors still write the states and decays, and a load that
 // promises read-only memory may be moved in front of the wait.
-template <bool SHORT>
 struct StateRow {
-  float4 a, b, s, t;  // SHORT: a holds the eight values
+  float4 a, b, s, t;
   float dec;
 };
-template <int K, int V, bool SHORT = false>
-__device__ __forceinline__ StateRow<SHORT> state_load(const ScanParams& p, const StateRef& r, int e) {
-  StateRow<SHORT> x;
-  if constexpr (SHORT) {
-    x.a = *reinterpret_cast<const float4*>(reinterpret_cast<const __nv_bfloat16*>(r.own) + e);
-  } else {
-    x.a = *reinterpret_cast<const float4*>(r.own + e);
-    x.b = reinterpret_cast<const float4*>(r.own + e)[1];
-  }
+template <int K, int V>
+__device__ __forceinline__ StateRow state_load(const ScanParams& p, const StateRef& r, int e) {
+  StateRow x;
+  x.a = *reinterpret_cast<const float4*>(r.own + e);
+  x.b = reinterpret_cast<const float4*>(r.own + e)[1];
   x.s = x.t = make_float4(0.f, 0.f, 0.f, 0.f);
   x.dec = 0.f;
   if (r.start != nullptr) {
@@ -398,29 +391,12 @@ __device__ __forceinline__ StateRow<SHORT> state_load(const ScanParams& p, const
   }
   return x;
 }
-// ROUND: the own part as SHORT holds it.
-template <bool ROUND = false, bool SHORT>
-__device__ __forceinline__ void state_sum(const StateRow<SHORT>& r, float2 (&x)[4]) {
+__device__ __forceinline__ void state_sum(const StateRow& r, float2 (&x)[4]) {
   const float2 d = both(ex2(r.dec));
-  if constexpr (SHORT) {
-    const float raw[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t u = __float_as_uint(raw[i]);
-      x[i] = make_float2(ptx::bf16x2_lo(u), ptx::bf16x2_hi(u));
-    }
-  } else {
-    x[0] = make_float2(r.a.x, r.a.y);
-    x[1] = make_float2(r.a.z, r.a.w);
-    x[2] = make_float2(r.b.x, r.b.y);
-    x[3] = make_float2(r.b.z, r.b.w);
-    if (ROUND)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t u = ptx::pack_bf16x2(x[i].x, x[i].y);
-        x[i] = make_float2(ptx::bf16x2_lo(u), ptx::bf16x2_hi(u));
-      }
-  }
+  x[0] = make_float2(r.a.x, r.a.y);
+  x[1] = make_float2(r.a.z, r.a.w);
+  x[2] = make_float2(r.b.x, r.b.y);
+  x[3] = make_float2(r.b.z, r.b.w);
   x[0] = fma2(make_float2(r.s.x, r.s.y), d, x[0]);
   x[1] = fma2(make_float2(r.s.z, r.s.w), d, x[1]);
   x[2] = fma2(make_float2(r.t.x, r.t.y), d, x[2]);
@@ -428,9 +404,7 @@ __device__ __forceinline__ void state_sum(const StateRow<SHORT>& r, float2 (&x)[
 }
 
 // Asks for a state's own tile to be in L2 by the time it is fetched.
-template <bool SHORT = false>
 __device__ __forceinline__ void state_prefetch(int tid, const StateRef& r, int n) {
-  if (SHORT) n /= 2;
   for (int e = tid * 32; e < n; e += kThreads * 32)
     asm volatile("prefetch.global.L2 [%0];" ::"l"(r.own + e));
 }

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
     const int step = threads * 8;
 #pragma unroll 1
     for (int e0 = thread * 8; e0 < n; e0 += U * step) {
-      StateRow<false> x[U];
+      StateRow x[U];
       bool on[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
     for (int e = tid * 8; e < w.heads * V * K; e += kThreads * 8) {
       // (a warp's 256 elements together: its lanes sum below)
       if (!in_range(p.status, fh.at + e / 256 * 256, 256, st_extent, CHK_SCAN_WS)) continue;
-      const StateRow<false> xr = state_load<K, V>(p, fh, e), yr = state_load<K, V>(p, fr, e);
+      const StateRow xr = state_load<K, V>(p, fh, e), yr = state_load<K, V>(p, fr, e);
       float2 x[4], y[4];
       state_sum(xr, x);
       state_sum(yr, y);

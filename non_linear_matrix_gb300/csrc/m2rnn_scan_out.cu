@@ -14,8 +14,7 @@
 //
 // Bound by latency: each head block waits for its state, converts it and passes
 // two barriers, at four CTAs per SM (registers, shared memory).  B=1 T=65536 N=64
-// K=64 V=16: 173 us with the states in bf16, 182 in fp32; B=8 T=4096 N=32, fp32
-// states: 53 us, of which without the state's fetch 40 remain and without the
+// K=64 V=16: 182 us; B=8 T=4096 N=32: 53 us, of which without the state's fetch 40 remain and without the
 // products within the chunk 48.  Double-buffered tiles (three CTAs) took 63, five
 // CTAs (spills) 61.
 #include "m2rnn_scan.cuh"
@@ -34,8 +33,7 @@ struct OutSmem {
   static constexpr int bytes = gate + HB * 192 * 4;
 };
 
-// SHORT: the states come in bf16.
-template <bool F32, int KT, int V, bool SHORT>
+template <bool F32, int KT, int V>
 __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_kernel(const ScanParams p) {
   using E = typename Elem<F32>::T;
   using S = OutSmem<F32, KT, V>;
@@ -66,24 +64,24 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_ke
     load_tile<F32, kCols>(threadIdx.x, vs, v, p.vt, rows, w.heads * V, p.status, p.T - t0);
     load_gate(threadIdx.x, base + S::gate, p, w, c);
     ptx::cp_async_commit();
-    const StateRef r = state_ref<SHORT>(p, p.Hl, p.Hseg, p.cdec, w, c, seg);
+    const StateRef r = state_ref(p, p.Hl, p.Hseg, p.cdec, w, c, seg);
     constexpr int step = kThreads * 8, U = kCols * K >= 2 * step ? 2 : 1;  // rows in flight
     const int n = w.heads * V * K;
 #pragma unroll 1
     for (int e0 = threadIdx.x * 8; e0 < n; e0 += U * step) {
-      StateRow<SHORT> x[U];
+      StateRow x[U];
       bool on[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int e = e0 + u * step;
         on[u] = e < n && in_range(p.status, r.at + e, 8, hl_extent, CHK_SCAN_WS);
-        if (on[u]) x[u] = state_load<K, V, SHORT>(p, r, e);
+        if (on[u]) x[u] = state_load<K, V>(p, r, e);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (on[u]) {
           float2 z[4];
-          state_sum<!F32>(x[u], z);  // (the same y with and without a saved forward pass)
+          state_sum(x[u], z);
           put_state_row<PO, K>(hs, e0 + u * step, z);
         }
     }
@@ -121,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_ke
     __syncthreads();
     if (hb + 1 < hb1) {
       const Place next = place_in(p, HB, b, group, hb + 1);
-      state_prefetch<SHORT>(threadIdx.x, state_ref<SHORT>(p, p.Hl, p.Hseg, p.cdec, next, c, seg), next.heads * V * K);
+      state_prefetch(threadIdx.x, state_ref(p, p.Hl, p.Hseg, p.cdec, next, c, seg), next.heads * V * K);
     }
     float acc[8][4];
 #pragma unroll
@@ -271,29 +269,28 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_ke
   }
 }
 
-template <bool F32, int KT, int V, bool SHORT>
+template <bool F32, int KT, int V>
 cudaError_t run(const ScanParams& p, cudaStream_t st) {
   constexpr int smem = OutSmem<F32, KT, V>::bytes;
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
-  const cudaError_t e = allow_smem<out_kernel<F32, KT, V, SHORT>>(smem);
+  const cudaError_t e = allow_smem<out_kernel<F32, KT, V>>(smem);
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(p.B) * p.Nq * p.hsplit * p.nc;
-  return launch_after(out_kernel<F32, KT, V, SHORT>, dim3(static_cast<unsigned>(grid)), kThreads, smem, st, p);
+  return launch_after(out_kernel<F32, KT, V>, dim3(static_cast<unsigned>(grid)), kThreads, smem, st, p);
 }
 
-template <bool F32, int V, bool SHORT>
+template <bool F32, int V>
 cudaError_t run_k(const ScanParams& p, cudaStream_t st) {
   switch (p.K) {
-    case 16: return run<F32, 2, V, SHORT>(p, st);
-    case 32: return run<F32, 4, V, SHORT>(p, st);
-    case 64: return run<F32, 8, V, SHORT>(p, st);
-    default: return run<F32, 16, V, SHORT>(p, st);
+    case 16: return run<F32, 2, V>(p, st);
+    case 32: return run<F32, 4, V>(p, st);
+    case 64: return run<F32, 8, V>(p, st);
+    default: return run<F32, 16, V>(p, st);
   }
 }
 template <int V>
 cudaError_t run_type(const ScanParams& p, bool f32, cudaStream_t st) {
-  if (f32) return run_k<true, V, false>(p, st);
-  return p.short_states ? run_k<false, V, true>(p, st) : run_k<false, V, false>(p, st);
+  return f32 ? run_k<true, V>(p, st) : run_k<false, V>(p, st);
 }
 
 }  // namespace

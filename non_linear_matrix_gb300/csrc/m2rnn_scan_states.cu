@@ -14,9 +14,8 @@
 // segment.
 //
 // Bound by the three-term products (44 % of the tensor pipe's cycles) and the
-// instructions around them (48 % of issue slots), not by the states' traffic: with
-// the states in bf16 (only outputs read them) B=1 T=65536 N=64 K=64 V=16 takes
-// 95 us, in fp32 99.  B=8 T=4096 N=32: 33 us forwards, 28 in reverse; the join
+// instructions around them (48 % of issue slots), not by the states' traffic:
+// B=1 T=65536 N=64 K=64 V=16 takes 99 us.  B=8 T=4096 N=32: 33 us forwards, 28 in reverse; the join
 // 5 to 8.  Four CTAs per SM: without that bound on the registers 107 us, with five
 // (spills) 151.
 #include "m2rnn_scan.cuh"
@@ -25,8 +24,7 @@ namespace m2rnn {
 namespace scan {
 namespace {
 
-// SHORT: the chunks' states are written in bf16.
-template <bool F32, int KT, bool REV, bool SHORT>
+template <bool F32, int KT, bool REV>
 __global__ void __launch_bounds__(kThreads, F32 ? (KT == 16 ? 2 : 3) : KT == 16 ? 3 : 4) states_kernel(const ScanParams p) {
   using E = typename Elem<F32>::T;
   constexpr int P = Terms<F32>::in, PS = Terms<F32>::state, K = 8 * KT, kLd = K + 8;
@@ -112,19 +110,6 @@ __global__ void __launch_bounds__(kThreads, F32 ? (KT == 16 ? 2 : 3) : KT == 16 
       }
   };
 
-  auto put_short = [&](float* to, size_t tiles, size_t tile) {
-    __nv_bfloat16* base = reinterpret_cast<__nv_bfloat16*>(to);
-#pragma unroll
-    for (int nt = 0; nt < KT; ++nt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const size_t at = tile * kCols * K + ((2 * warp + h) * KT + nt) * 64 + 2 * lane;
-        const float2 x = pair(acc[nt], h);
-        if (in_range(p.status, at, 2, tiles * kCols * K, CHK_SCAN_WS))
-          *reinterpret_cast<uint32_t*>(base + at) = ptx::pack_bf16x2(x.x, x.y);
-      }
-  };
-
   const size_t pairs = static_cast<size_t>(p.B) * p.Nq * p.nhb;
   float total = 0.f;  // log2 decay of the segment so far
   for (int i = 0; i < count; ++i) {
@@ -188,10 +173,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? (KT == 16 ? 2 : 3) : KT == 16 
     __syncthreads();  // tiles of chunk i are there; everyone is done with chunk i - 1
     if (i + 1 < count) fetch(i + 1);
     if (on) {
-      if constexpr (SHORT)
-        put_short(p.Hl, pairs * p.nc, static_cast<size_t>(gbx) * p.nc + c);
-      else
-        put(REV ? p.Rl : p.Hl, pairs * p.nc, static_cast<size_t>(gbx) * p.nc + c);
+      put(REV ? p.Rl : p.Hl, pairs * p.nc, static_cast<size_t>(gbx) * p.nc + c);
       const float2 dec = both(ex2(chunk_sum));
       const uint32_t kt = key0 + (i & 1) * kKey, vt = val0 + (i & 1) * kVal;
       constexpr int G = F32 ? 1 : 4;  // steps of 16 tokens at a time (fp32 has more terms to hold)
@@ -316,14 +298,14 @@ __global__ void __launch_bounds__(256) join_kernel(const ScanParams p, float* en
   }
 }
 
-template <bool F32, int KT, bool REV, bool SHORT>
+template <bool F32, int KT, bool REV>
 cudaError_t run(const ScanParams& p, cudaStream_t st) {
   constexpr int P = Terms<F32>::in, K = 8 * KT;
   constexpr int smem = 4 * kChunk * 4 + 2 * P * kChunk * (K + 8 + kVLd) * 2;
   const long long pairs = static_cast<long long>(p.B) * p.Nq * p.nhb;
-  const cudaError_t e = allow_smem<states_kernel<F32, KT, REV, SHORT>>(smem);
+  const cudaError_t e = allow_smem<states_kernel<F32, KT, REV>>(smem);
   if (e != cudaSuccess) return e;
-  states_kernel<F32, KT, REV, SHORT><<<static_cast<unsigned>(pairs * p.nseg), kThreads, smem, st>>>(p);
+  states_kernel<F32, KT, REV><<<static_cast<unsigned>(pairs * p.nseg), kThreads, smem, st>>>(p);
   if (p.nseg > 1)
     for (long long y0 = 0; y0 < pairs; y0 += 65535)  // (nseg > 1 means few pairs: one launch)
     {
@@ -335,13 +317,13 @@ cudaError_t run(const ScanParams& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <bool F32, bool REV, bool SHORT = false>
+template <bool F32, bool REV>
 cudaError_t run_k(const ScanParams& p, cudaStream_t st) {
   switch (p.K) {
-    case 16: return run<F32, 2, REV, SHORT>(p, st);
-    case 32: return run<F32, 4, REV, SHORT>(p, st);
-    case 64: return run<F32, 8, REV, SHORT>(p, st);
-    default: return run<F32, 16, REV, SHORT>(p, st);
+    case 16: return run<F32, 2, REV>(p, st);
+    case 32: return run<F32, 4, REV>(p, st);
+    case 64: return run<F32, 8, REV>(p, st);
+    default: return run<F32, 16, REV>(p, st);
   }
 }
 
@@ -350,8 +332,7 @@ cudaError_t run_k(const ScanParams& p, cudaStream_t st) {
 
 cudaError_t launch_scan_states(const ScanParams& p, bool f32, bool reverse, cudaStream_t st) {
   if (f32) return reverse ? scan::run_k<true, true>(p, st) : scan::run_k<true, false>(p, st);
-  if (reverse) return scan::run_k<false, true>(p, st);
-  return p.short_states ? scan::run_k<false, false, true>(p, st) : scan::run_k<false, false>(p, st);
+  return reverse ? scan::run_k<false, true>(p, st) : scan::run_k<false, false>(p, st);
 }
 
 }  // namespace m2rnn

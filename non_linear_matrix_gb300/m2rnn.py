@@ -779,7 +779,9 @@ def scan_fwd(q, k, v, a, alpha, beta, w_r=None, H0=None, *, want_HT: bool = True
     q, k [B,T,K] or [B,T,Nq,K]; v [B,T,N,V]; a [B,T,N] (rows may be slices
     of a wider buffer); alpha, beta [N]; w_r [N,V] or None; H0 [B,N,K,V] fp32
     or None.  save=True keeps what ``scan_bwd`` would otherwise recompute (an
-    opaque buffer).  ``out`` may supply y, HT and saved."""
+    opaque buffer).  ``out`` may supply y, HT and saved.  ``workspace``: at
+    least m2rnn_scan_fwd_workspace_size bytes (none when saved is kept); with
+    m2rnn_scan_saved_size bytes the call runs in one part."""
     s, rows = _scan_args(q, k, v, a, alpha, beta, w_r, 2)
     state, dev = (s.B, s.N, s.K, s.V), q.device
     _expect("H0", H0, state, torch.float32)
@@ -793,8 +795,9 @@ def scan_fwd(q, k, v, a, alpha, beta, w_r=None, H0=None, *, want_HT: bool = True
                             dtype=torch.uint8)
     elif saved is not None and saved.numel() < int(L.m2rnn_scan_saved_size(ctypes.byref(s))):
         raise ValueError("saved is smaller than m2rnn_scan_saved_size")
-    ws = _workspace(workspace, int(L.m2rnn_scan_fwd_workspace_size(ctypes.byref(s),
-                                                                   int(saved is not None))), dev)
+    # (as much as runs in one part; m2rnn_scan_fwd_workspace_size is the least)
+    need = int(L.m2rnn_scan_saved_size(ctypes.byref(s))) if saved is None and workspace is None else 0
+    ws = _workspace(workspace, need, dev)
     rc = L.m2rnn_scan_fwd(ctypes.byref(s), rows, _at(q), _at(k), _at(v), _at(a),
                           _addr(alpha), _addr(beta), _addr(w_r), _addr(H0), _addr(y), _addr(HT),
                           _addr(saved), _addr(ws), _nbytes(ws), _stream_of(stream, q))
