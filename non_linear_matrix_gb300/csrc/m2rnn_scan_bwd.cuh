@@ -34,7 +34,7 @@
 // along the rows, which leaves G L in the registers as the A operand of dv.
 // Between different 16-token blocks L is a product of a row's and a column's
 // factor, as in the forward pass.  States enter with three bf16 terms where a
-// value that stays in fp32 depends on them (dl) and with one for dv.
+// value that stays in fp32 depends on them (dl) and with two for dv.
 //
 // Bound by latency and the shared-memory pipe (55 % of its cycles; 36 % of issue
 // slots, 17 % of the tensor pipe's): B=8 T=4096 N=32 K=64 V=16 takes 235 us.  At
@@ -738,7 +738,8 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
     __syncthreads();
     if (hb + 1 < hb1) fetch_rest(hb + 1);
   }
-  // by way of the v tile's place, [j][i], to the other side
+  // by way of the v tile's place (bf16 inputs: and the u tile's), [j][i], to the other side
+  static_assert(PO * kChunk * kVLd * 2 <= 2 * S::val, "the terms of the sum of E L");
   __syncthreads();
 #pragma unroll
   for (int n = 0; n < 8; ++n) {

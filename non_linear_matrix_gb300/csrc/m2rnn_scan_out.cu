@@ -25,19 +25,19 @@ namespace {
 
 template <bool F32, int KT, int V>
 struct OutSmem {
-  static constexpr int P = Terms<F32>::in, PO = Terms<F32>::out, K = 8 * KT, HB = kCols / V;
+  static constexpr int P = Terms<F32>::in, PS = Terms<F32>::state, K = 8 * KT, HB = kCols / V;
   static constexpr int key = P * kChunk * (K + 8) * 2, val = P * kChunk * kVLd * 2;
   // the k tile, and after q k^T the rows of y on their way out
   static constexpr int ky = key > kChunk * kVLd * 2 ? key : kChunk * kVLd * 2;
-  static constexpr int q = 0, k = key, v = k + ky, h = v + val, gate = h + PO * kCols * K * 2;
+  static constexpr int q = 0, k = key, v = k + ky, h = v + val, gate = h + PS * kCols * K * 2;
   static constexpr int bytes = gate + HB * 192 * 4;
 };
 
 template <bool F32, int KT, int V>
-__global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 2 : 4)) out_kernel(const ScanParams p) {
   using E = typename Elem<F32>::T;
   using S = OutSmem<F32, KT, V>;
-  constexpr int P = S::P, PO = S::PO, K = S::K, ld = K + 8;
+  constexpr int P = S::P, PS = S::PS, PO = Terms<F32>::out, K = S::K, ld = K + 8;
   constexpr int HB = S::HB, NT = V / 8;  // heads per block, column tiles per head
   extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t base = ptx::smem_addr(smem), qs = base + S::q, ks = base + S::k, vs = base + S::v,
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_ke
         if (on[u]) {
           float2 z[4];
           state_sum(x[u], z);
-          put_state_row<PO, K>(hs, e0 + u * step, z);
+          put_state_row<PS, K>(hs, e0 + u * step, z);
         }
     }
   };
@@ -134,10 +134,10 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 3 : 4)) out_ke
 #pragma unroll
       for (int v8 = 0; v8 < 8; v8 += 2) {
         if (v8 >= w.heads * NT) break;
-        uint32_t b0[PO][2], b1[PO][2];
-        state_b2<PO>(b0, b1, hs, K, v8, kk);
-        mma_terms<P, PO>(acc[v8], a, b0);
-        mma_terms<P, PO>(acc[v8 + 1], a, b1);
+        uint32_t b0[PS][2], b1[PS][2];
+        state_b2<PS>(b0, b1, hs, K, v8, kk);
+        mma_terms<P, PS>(acc[v8], a, b0);
+        mma_terms<P, PS>(acc[v8 + 1], a, b1);
       }
     }
 #pragma unroll

@@ -79,3 +79,36 @@ def test_least_workspace(m, B, T, N, K, V, Nq, dtype):
         assert (buf[given:] == 165).all()
     with pytest.raises(m.M2RNNError):
         m.scan_fwd(*args(d), d["w_r"], d["H0"], workspace=buf[:need - 16])
+
+
+# B, T, N, K, V, Nq
+SHAPES = [(2, 512, 8, 64, 16, 1), (1, 333, 6, 128, 32, 2), (3, 130, 5, 32, 16, 5), (1, 1500, 4, 16, 32, 1)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,T,N,K,V,Nq", SHAPES)
+def test_outputs_are_rounded_once(m, B, T, N, K, V, Nq):
+    """Without the skip term, which would hide the scan's own part.  Tolerance: the
+    exact values' rounding to bf16, and 2^-14: operands of two bf16 terms (2^-17
+    each), their sums' cancellation (a factor of 8)."""
+    for sliced, state in [(False, True), (True, False)]:
+        d = make(B, T, N, K, V, Nq, "bf16", T + K + 2, sliced, state)
+        d["w_r"] = None
+        ref = plain(d)["y"]
+        for save in (False, True):
+            y = m.scan_fwd(*args(d), None, d["H0"], save=save)[0]
+            assert rel(y, ref) <= rounding(ref) + 2.0 ** -14, (sliced, save, rel(y, ref), rounding(ref))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,T,N,K,V,Nq", SHAPES)
+def test_gradients_are_rounded_once(m, B, T, N, K, V, Nq):
+    """As the outputs: dq, dk, dv, da."""
+    for sliced, state in [(False, True), (True, False)]:
+        d = make(B, T, N, K, V, Nq, "bf16", T + K + 3, sliced, state)
+        d["w_r"] = None
+        ref = plain(d, backward=True)
+        g = m.scan_bwd(*args(d), d["dy"], None, d["H0"], d["dHT"])
+        bad = {n: (rel(g[n], ref[n]), rounding(ref[n])) for n in ("dq", "dk", "dv", "da")
+               if not rel(g[n], ref[n]) <= rounding(ref[n]) + 2.0 ** -14}
+        assert not bad, (sliced, bad)
