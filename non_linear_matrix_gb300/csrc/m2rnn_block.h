@@ -90,6 +90,7 @@ cudaError_t launch_scan_step(const ScanStepParams& p, int V, bool f32, cudaStrea
 // Selective scan over whole sequences (m2rnn_scan_*.cu).
 constexpr int kChunk = 64;    // tokens per chunk
 constexpr int kCols = 64;     // value columns per head block: 64 / V heads
+constexpr int kGate = 4 * kChunk;  // gate values of a chunk and head
 
 struct ScanParams {
   const void *q, *k, *v, *a, *alpha, *beta, *w_r;
@@ -106,9 +107,9 @@ struct ScanParams {
   int hpg, nhb;   // heads per group, head blocks per group
   int nseg, cps;  // segments of a sequence in the state kernels, chunks in each
   int hsplit;     // CTAs that share a chunk's head blocks
-  // The gate's values of a chunk, [B][N][nc][3][64]: sums of log2 decay from the
+  // The gate's values of a chunk, [B][N][nc][4][64]: sums of log2 decay from the
   // token's 16-block's start (loc); dt; the token's weight at its block's end,
-  // dt 2^(block's sum - loc).
+  // dt 2^(block's sum - loc); what loc's rounding leaves of its sum.
   float* gate;
   float* cdec;    // [B][N][nc]: log2 decay from the segment's start to the chunk
   float* Hl;      // [B][Nq * nhb][nc][64 x K]: states before each chunk, without what

@@ -200,7 +200,7 @@ ScanPlan sized_for(ScanPlan q, const m2rnn_shape* s, int B) {
   const size_t tile = static_cast<size_t>(m2rnn::kCols) * s->K * sizeof(float);
   const size_t heads = static_cast<size_t>(B) * s->N;
   const size_t pairs = static_cast<size_t>(B) * (s->Nq == 0 ? 1 : s->Nq) * q.nhb;
-  q.gate = align256(heads * q.nc * 3 * m2rnn::kChunk * sizeof(float));
+  q.gate = align256(heads * q.nc * m2rnn::kGate * sizeof(float));
   q.dec = align256(heads * (q.nc + q.nseg) * sizeof(float));
   q.states = align256(pairs * q.nc * tile);
   q.ends = q.nseg > 1 ? align256(pairs * q.nseg * tile) : 0;

@@ -9,8 +9,10 @@
 //
 // so a chunk is a handful of small matrix products.  Decays are powers of two
 // of sums over (j, i] that are formed from sums over 16-token blocks: exact
-// to a few 2^-24 of the sum itself, however long the sequence, never as
-// differences of two long sums.
+// to a few 2^-24 of the sum itself, however long the sequence.  Between blocks only
+// sums of parts are formed.  Within a block S(j,i) is a difference of two sums from
+// the block's start, which a token that forgets (l near -160) makes large: each is
+// held as a rounded sum and what the rounding left, and so is the difference.
 //
 // Operands.  Products run on the tensor cores (mma.sync) in bf16 with fp32
 // accumulation.  A value of more than 8 bits enters as a sum of bf16 terms,
@@ -71,6 +73,13 @@ __device__ __forceinline__ float2 pair(const float (&x)[4], int half) {
 __device__ __forceinline__ void set_pair(float (&x)[4], int half, float2 v) {
   x[2 * half] = v.x;
   x[2 * half + 1] = v.y;
+}
+
+// a + b rounded, and what the rounding left of it (Knuth's two-sum; exact).
+__device__ __forceinline__ float two_sum(float a, float b, float& left) {
+  const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+  left = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
+  return s;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -425,15 +434,14 @@ __device__ __forceinline__ void put_state_row(uint32_t tile, int e, const float2
                  : "memory");
 }
 
-// A chunk's gate values of the block's heads: [heads][3][64] floats.
+// A chunk's gate values of the block's heads: [heads][4][64] floats.
 __device__ __forceinline__ void load_gate(int tid, uint32_t dst, const ScanParams& p, const Place& w,
                                           int c) {
-  const int o = (tid & 63) * 4;  // 48 threads bring a head's 768 bytes
-  const size_t extent = static_cast<size_t>(p.B) * p.N * p.nc * 192;
-  if (o >= 192) return;
+  const int o = (tid & 63) * 4;  // 64 threads bring a head's 1,024 bytes
+  const size_t extent = static_cast<size_t>(p.B) * p.N * p.nc * kGate;
   for (int h = tid >> 6; h < w.heads; h += kThreads / 64) {
-    const size_t at = ((static_cast<size_t>(w.b) * p.N + w.head0 + h) * p.nc + c) * 192 + o;
-    if (in_range(p.status, at, 4, extent, CHK_SCAN_WS)) ptx::cp_async16(dst + (h * 192 + o) * 4, p.gate + at);
+    const size_t at = ((static_cast<size_t>(w.b) * p.N + w.head0 + h) * p.nc + c) * kGate + o;
+    if (in_range(p.status, at, 4, extent, CHK_SCAN_WS)) ptx::cp_async16(dst + (h * kGate + o) * 4, p.gate + at);
   }
 }
 

@@ -65,7 +65,7 @@ struct BwdSmem {
   // i >= t > j, then the later blocks' column sums; shares of <R, H>.  What else
   // there is per head and token has its place in the 16 bytes behind the tiles' rows
   // (see spare).
-  static constexpr int through = gate + HB * 192 * 4;
+  static constexpr int through = gate + HB * kGate * 4;
   static constexpr int cols = through + 2 * HB * kChunk * 4;
   static constexpr int rh = cols + 160 * HB * 4;
   static constexpr int bytes = rh + 32 * 4;
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
       float decay = 0.f, alpha = 0.f, dt[2], sg[2], ratio[2];
       if (warp < w.heads) {
         const int n = w.head0 + warp;
-        const float* lo = gate + warp * 192;
+        const float* lo = gate + warp * kGate;
         decay = ex2((lo[15] + lo[31]) + (lo[47] + lo[63]));
         const E* a = static_cast<const E*>(p.a) + b * p.ab + n;
         alpha = to_f32(static_cast<const E*>(p.alpha)[n]);
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
       if (works) {
 #pragma unroll 1
         for (int h = 0; h < w.heads; ++h) {  // dq through H: 2^S(start,i)
-          const float* lo = gate + h * 192;
+          const float* lo = gate + h * kGate;
           float2 sc[2];
           float off = row0 ? lo[15] + lo[31] : 0.f;
 #pragma unroll
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
       if (works) {
 #pragma unroll 1
         for (int h = 0; h < w.heads; ++h) {  // dk through R: 2^S(j,end) dt_j
-          const float* lo = gate + h * 192;
+          const float* lo = gate + h * kGate;
           float2 sc[2];
           float off = row0 ? 0.f : lo[47] + lo[63];
 #pragma unroll
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
     }
 #pragma unroll 1
     for (int h = 0; h < w.heads; ++h) {
-      const float* lo = gate + h * 192;
+      const float* lo = gate + h * kGate;
       const float* lj = lo + rb + g;                   // of rows g; g + 8 further on the others
       const float end0 = lj[128], end1 = lj[128 + 8];  // 2^S(j, block's end) dt_j
       float w0, w1;                                    // 2^S(j, end) dt_j
@@ -611,9 +611,10 @@ __global__ void __launch_bounds__(2 * kThreads, F32 || KT == 16 ? 1 : 2) bwd_ker
           const float2 g0 = make_float2(g4.x, g4.y), g1 = make_float2(g4.z, g4.w);
           float2 l0, l1;
           if (k4 == 0) {
-            const float lj0 = lj[0], lj1 = lj[8];
-            l0 = mul2(make_float2(ex2(li.x - lj0), ex2(li.y - lj0)), both(lj[64]));
-            l1 = mul2(make_float2(ex2(li.x - lj1), ex2(li.y - lj1)), both(lj[64 + 8]));
+            const float lj0 = lj[0], lj1 = lj[8], ej0 = lj[192], ej1 = lj[192 + 8];
+            const float2 ei = *reinterpret_cast<const float2*>(li_at + 192 + 8 * n);
+            l0 = mul2(make_float2(ex2((li.x - lj0) + (ei.x - ej0)), ex2((li.y - lj0) + (ei.y - ej0))), both(lj[64]));
+            l1 = mul2(make_float2(ex2((li.x - lj1) + (ei.x - ej1)), ex2((li.y - lj1) + (ei.y - ej1))), both(lj[64 + 8]));
             const int i = 8 * u + c2;  // i >= j
             l0.x = i >= g ? l0.x : 0.f;
             l0.y = i + 1 >= g ? l0.y : 0.f;

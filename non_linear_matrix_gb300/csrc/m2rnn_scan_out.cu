@@ -30,7 +30,7 @@ struct OutSmem {
   // the k tile, and after q k^T the rows of y on their way out
   static constexpr int ky = key > kChunk * kVLd * 2 ? key : kChunk * kVLd * 2;
   static constexpr int q = 0, k = key, v = k + ky, h = v + val, gate = h + PS * kCols * K * 2;
-  static constexpr int bytes = gate + HB * 192 * 4;
+  static constexpr int bytes = gate + HB * kGate * 4;
 };
 
 template <bool F32, int KT, int V>
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 2 : 4)) out_ke
 #pragma unroll
     for (int h = 0; h < HB; ++h) {
       if (h >= w.heads) break;
-      const float* lo = gate + h * 192;
+      const float* lo = gate + h * kGate;
       const float* end = lo + 128;
       const float li0 = lo[16 * rt + g], li1 = lo[16 * rt + g + 8];
       const float tot[3] = {lo[15], lo[31], lo[47]};
@@ -170,8 +170,10 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 2 : 4)) out_ke
             const int nt = 2 * jj + u;
             const float2 lj = *reinterpret_cast<const float2*>(lo + 8 * nt + c2);
             const float2 dt = *reinterpret_cast<const float2*>(lo + 64 + 8 * nt + c2);
-            float2 x0 = mul2(make_float2(ex2(li0 - lj.x), ex2(li0 - lj.y)), dt);
-            float2 x1 = mul2(make_float2(ex2(li1 - lj.x), ex2(li1 - lj.y)), dt);
+            const float2 ej = *reinterpret_cast<const float2*>(lo + 192 + 8 * nt + c2);
+            const float ei0 = lo[192 + 16 * rt + g], ei1 = lo[192 + 16 * rt + g + 8];
+            float2 x0 = mul2(make_float2(ex2((li0 - lj.x) + (ei0 - ej.x)), ex2((li0 - lj.y) + (ei0 - ej.y))), dt);
+            float2 x1 = mul2(make_float2(ex2((li1 - lj.x) + (ei1 - ej.x)), ex2((li1 - lj.y) + (ei1 - ej.y))), dt);
             const int j = 8 * u + c2;  // j <= i
             x0.x = j <= g ? x0.x : 0.f;
             x0.y = j < g ? x0.y : 0.f;

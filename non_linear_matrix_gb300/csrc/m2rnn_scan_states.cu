@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? (KT == 16 ? 2 : 3) : KT == 16 
   const float alpha = -to_f32(static_cast<const E*>(p.alpha)[n]);
   const float rate = alpha * kLog2e, rate_lo = fmaf(alpha, kLog2e, -rate) + alpha * kLog2eLo;
   const size_t head = static_cast<size_t>(b) * p.N + n;
-  const size_t gate_extent = static_cast<size_t>(p.B) * p.N * p.nc * 192;
+  const size_t gate_extent = static_cast<size_t>(p.B) * p.N * p.nc * kGate;
 
   auto chunk_of = [&](int i) { return REV ? p.nc - 1 - (first + i) : first + i; };
   auto fetch = [&](int i) {  // tiles of the i-th chunk of the segment
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? (KT == 16 ? 2 : 3) : KT == 16 
   auto fetch_gate = [&](int i) {
     const int c = chunk_of(i), t = c * kChunk + 2 * lane;
     if constexpr (REV) {
-      const size_t at = (head * p.nc + c) * 192 + 2 * lane;
+      const size_t at = (head * p.nc + c) * kGate + 2 * lane;
       ga = make_float2(0.f, 0.f);
       if (in_range(p.status, at, 2, gate_extent, CHK_SCAN_WS))
         ga = *reinterpret_cast<const float2*>(p.gate + at);
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? (KT == 16 ? 2 : 3) : KT == 16 
     const int c = chunk_of(i);
     // The gate's sums.  Blocks of 16 tokens are 8 lanes; loc: from the block's
     // start up to the lane's tokens, rest: from behind them to its end.
-    float2 loc, rest = make_float2(0.f, 0.f), dt = make_float2(0.f, 0.f), wt;
+    float2 loc, left, rest = make_float2(0.f, 0.f), dt = make_float2(0.f, 0.f), wt;
     if constexpr (REV) {
       loc = ga;
     } else {
@@ -126,18 +126,26 @@ __global__ void __launch_bounds__(kThreads, F32 ? (KT == 16 ? 2 : 3) : KT == 16 
       // below 2^-160 a decay is 0 in fp32: the bound keeps sums short
       l.x = l.x < -160.f ? -160.f : l.x;
       l.y = l.y < -160.f ? -160.f : l.y;
-      float inc = l.x + l.y, suf = inc;
+      float low, inc = two_sum(l.x, l.y, low), suf = inc;  // inc + low: the sum so far
 #pragma unroll
       for (int d = 1; d < 8; d *= 2) {
         const float up = __shfl_up_sync(0xffffffffu, inc, d, 8);
+        const float up_low = __shfl_up_sync(0xffffffffu, low, d, 8);
         const float dn = __shfl_down_sync(0xffffffffu, suf, d, 8);
-        if ((lane & 7) >= d) inc += up;
+        if ((lane & 7) >= d) {
+          float e;
+          inc = two_sum(up, inc, e);
+          low += up_low + e;
+        }
         if ((lane & 7) + d < 8) suf += dn;
       }
       const float before = __shfl_up_sync(0xffffffffu, inc, 1, 8);
+      const float before_low = __shfl_up_sync(0xffffffffu, low, 1, 8);
       const float behind = __shfl_down_sync(0xffffffffu, suf, 1, 8);
       loc.y = inc;
-      loc.x = ((lane & 7) ? before : 0.f) + l.x;
+      left.y = low;
+      loc.x = two_sum((lane & 7) ? before : 0.f, l.x, left.x);
+      if (lane & 7) left.x += before_low;
       rest.y = (lane & 7) < 7 ? behind : 0.f;
       rest.x = rest.y + l.y;
     }
@@ -154,11 +162,12 @@ __global__ void __launch_bounds__(kThreads, F32 ? (KT == 16 ? 2 : 3) : KT == 16 
       for (int k = 3; k > 0; --k) off += k > blk ? tot[k] : 0.f;
       const float2 end = make_float2(ex2(rest.x) * dt.x, ex2(rest.y) * dt.y);
       wt = make_float2(ex2(off + rest.x) * dt.x, ex2(off + rest.y) * dt.y);
-      const size_t at = (head * p.nc + c) * 192 + 2 * lane;
-      if (leads && in_range(p.status, at, 130, gate_extent, CHK_SCAN_WS)) {
+      const size_t at = (head * p.nc + c) * kGate + 2 * lane;
+      if (leads && in_range(p.status, at, 194, gate_extent, CHK_SCAN_WS)) {
         *reinterpret_cast<float2*>(p.gate + at) = loc;
         *reinterpret_cast<float2*>(p.gate + at + 64) = dt;
         *reinterpret_cast<float2*>(p.gate + at + 128) = end;
+        *reinterpret_cast<float2*>(p.gate + at + 192) = left;
       }
     }
     const float chunk_sum = (tot[0] + tot[1]) + (tot[2] + tot[3]);
