@@ -133,7 +133,10 @@ int m2rnn_qk_norm_bwd(const m2rnn_qk_shape *s, const void *q, const m2rnn_rows *
  *   alpha, beta [N] in_dtype; w_r [N,V] in_dtype or NULL (0)
  *   H0, H_T [B,N,K,V] fp32 or NULL;   y [B,T,N,V] in_dtype
  * alpha < 0 is not rejected (the formula is evaluated as given).  a = -inf
- * gives dt = 0: the token leaves the state as it is (padding). */
+ * gives dt = 0: the token leaves the state as it is (padding; its k and v have to
+ * be finite).  y_t depends on no later token, whatever that holds; of its own and
+ * earlier tokens an infinity may come out as NaN.  In gradients a value that is not
+ * finite spreads over its neighbours. */
 typedef struct {
     m2rnn_rows q, k, v, a;
 } m2rnn_scan_rows;

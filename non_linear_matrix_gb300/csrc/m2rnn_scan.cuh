@@ -137,6 +137,15 @@ __device__ __forceinline__ void split(float2 v, uint32_t (&t)[P]) {
   }
 }
 
+// Which of two packed bf16 values are infinite or NaN: their sign bits' places.
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+  return ((x & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
+}
+// The pair with those values replaced by 0.
+__device__ __forceinline__ uint32_t finite_only(uint32_t x) {
+  return x & ~((not_finite(x) >> 15) * 0xffffu);
+}
+
 // The pair of values that packed terms stand for (exact for an input's terms).
 template <int P>
 __device__ __forceinline__ float2 join(const uint32_t (&t)[P]) {

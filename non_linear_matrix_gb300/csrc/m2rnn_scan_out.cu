@@ -17,6 +17,8 @@
 // K=64 V=16: 182 us; B=8 T=4096 N=32: 53 us, of which without the state's fetch 40 remain and without the
 // products within the chunk 48.  Double-buffered tiles (three CTAs) took 63, five
 // CTAs (spills) 61.
+#include <type_traits>
+
 #include "m2rnn_scan.cuh"
 
 namespace m2rnn {
@@ -32,6 +34,39 @@ struct OutSmem {
   static constexpr int q = 0, k = key, v = k + ky, h = v + val, gate = h + PS * kCols * K * 2;
   static constexpr int bytes = gate + HB * kGate * 4;
 };
+
+// acc (16 rows i x 8 columns) += A (rows i, tokens j of the same 16) times those values
+// of v that are infinite or NaN, for j <= i only: what a product with masked
+// weights cannot do.  v: shared address of token 0's 8 columns.  Rare, so one token
+// at a time.
+template <int PA>
+__device__ __forceinline__ void add_not_finite(float (&acc)[4], const uint32_t (&a)[PA][4], uint32_t v) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c2 = (lane & 3) * 2;
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll 1
+    for (int jj = 0; jj < 8; ++jj) {
+      const int j = 8 * u + jj, from = (lane & 28) | (jj >> 1);
+      float w0 = 0.f, w1 = 0.f;  // rows g, g + 8
+#pragma unroll
+      for (int t = PA - 1; t >= 0; --t) {
+        const uint32_t x0 = __shfl_sync(0xffffffffu, a[t][2 * u], from);
+        const uint32_t x1 = __shfl_sync(0xffffffffu, a[t][2 * u + 1], from);
+        w0 += (jj & 1) ? ptx::bf16x2_hi(x0) : ptx::bf16x2_lo(x0);
+        w1 += (jj & 1) ? ptx::bf16x2_hi(x1) : ptx::bf16x2_lo(x1);
+      }
+      const uint32_t x = ptx::lds_u32(v + (j * kVLd + c2) * 2), bad = not_finite(x);
+      const float lo = ptx::bf16x2_lo(x), hi = ptx::bf16x2_hi(x);
+      if (bad & 0x8000u) {
+        if (j <= g) acc[0] = fmaf(w0, lo, acc[0]);
+        if (j <= g + 8) acc[2] = fmaf(w1, lo, acc[2]);
+      }
+      if (bad & 0x80000000u) {
+        if (j <= g) acc[1] = fmaf(w0, hi, acc[1]);
+        if (j <= g + 8) acc[3] = fmaf(w1, hi, acc[3]);
+      }
+    }
+}
 
 template <bool F32, int KT, int V>
 __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 2 : 4)) out_kernel(const ScanParams p) {
@@ -122,100 +157,126 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : (KT == 16 ? 2 : 4)) out_ke
       state_prefetch(threadIdx.x, state_ref(p, p.Hl, p.Hseg, p.cdec, next, c, seg), next.heads * V * K);
     }
     float acc[8][4];
+    // The rows' outputs but for w_r (.) v.  CAREFUL: a value of v that is not finite
+    // is kept out of the product with the weights of its own 16 tokens, where a
+    // masked weight of 0 would make NaN of it for the tokens before.
+    auto form = [&](auto careful) {
+      constexpr bool CAREFUL = decltype(careful)::value;
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
+      for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
-    // from the state: q H
+        for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
+      // from the state: q H
 #pragma unroll
-    for (int kk = 0; kk < KT / 2; ++kk) {
-      uint32_t a[P][4];
-      load_a<P>(a, qs, ld, 16 * rt, 16 * kk);
+      for (int kk = 0; kk < KT / 2; ++kk) {
+        uint32_t a[P][4];
+        load_a<P>(a, qs, ld, 16 * rt, 16 * kk);
 #pragma unroll
-      for (int v8 = 0; v8 < 8; v8 += 2) {
-        if (v8 >= w.heads * NT) break;
-        uint32_t b0[PS][2], b1[PS][2];
-        state_b2<PS>(b0, b1, hs, K, v8, kk);
-        mma_terms<P, PS>(acc[v8], a, b0);
-        mma_terms<P, PS>(acc[v8 + 1], a, b1);
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < HB; ++h) {
-      if (h >= w.heads) break;
-      const float* lo = gate + h * kGate;
-      const float* end = lo + 128;
-      const float li0 = lo[16 * rt + g], li1 = lo[16 * rt + g + 8];
-      const float tot[3] = {lo[15], lo[31], lo[47]};
-      {  // decay since the chunk's start
-        float off = 0.f;
-#pragma unroll
-        for (int k4 = 0; k4 < 3; ++k4) off += k4 < rt ? tot[k4] : 0.f;
-        const float2 e0 = both(ex2(off + li0)), e1 = both(ex2(off + li1));
-#pragma unroll
-        for (int nt = h * NT; nt < (h + 1) * NT; ++nt) {
-          set_pair(acc[nt], 0, mul2(pair(acc[nt], 0), e0));
-          set_pair(acc[nt], 1, mul2(pair(acc[nt], 1), e1));
+        for (int v8 = 0; v8 < 8; v8 += 2) {
+          if (v8 >= w.heads * NT) break;
+          uint32_t b0[PS][2], b1[PS][2];
+          state_b2<PS>(b0, b1, hs, K, v8, kk);
+          mma_terms<P, PS>(acc[v8], a, b0);
+          mma_terms<P, PS>(acc[v8 + 1], a, b1);
         }
       }
-      // within the chunk; s0, s1: sum of l from the end of j's block to i
-      float s0 = li0, s1 = li1;
 #pragma unroll
-      for (int jj = 3; jj >= 0; --jj) {
-        if (jj > rt) continue;
-        uint32_t a[PO][4];
-        if (jj == rt) {
+      for (int h = 0; h < HB; ++h) {
+        if (h >= w.heads) break;
+        const float* lo = gate + h * kGate;
+        const float* end = lo + 128;
+        const float li0 = lo[16 * rt + g], li1 = lo[16 * rt + g + 8];
+        const float tot[3] = {lo[15], lo[31], lo[47]};
+        {  // decay since the chunk's start
+          float off = 0.f;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int nt = 2 * jj + u;
-            const float2 lj = *reinterpret_cast<const float2*>(lo + 8 * nt + c2);
-            const float2 dt = *reinterpret_cast<const float2*>(lo + 64 + 8 * nt + c2);
-            const float2 ej = *reinterpret_cast<const float2*>(lo + 192 + 8 * nt + c2);
-            const float ei0 = lo[192 + 16 * rt + g], ei1 = lo[192 + 16 * rt + g + 8];
-            float2 x0 = mul2(make_float2(ex2((li0 - lj.x) + (ei0 - ej.x)), ex2((li0 - lj.y) + (ei0 - ej.y))), dt);
-            float2 x1 = mul2(make_float2(ex2((li1 - lj.x) + (ei1 - ej.x)), ex2((li1 - lj.y) + (ei1 - ej.y))), dt);
-            const int j = 8 * u + c2;  // j <= i
-            x0.x = j <= g ? x0.x : 0.f;
-            x0.y = j < g ? x0.y : 0.f;
-            x1.x = j <= g + 8 ? x1.x : 0.f;
-            x1.y = j < g + 8 ? x1.y : 0.f;
-            uint32_t y0[PO], y1[PO];
-            split<PO>(mul2(pair(gm[nt], 0), x0), y0);
-            split<PO>(mul2(pair(gm[nt], 1), x1), y1);
+          for (int k4 = 0; k4 < 3; ++k4) off += k4 < rt ? tot[k4] : 0.f;
+          const float2 e0 = both(ex2(off + li0)), e1 = both(ex2(off + li1));
 #pragma unroll
-            for (int t = 0; t < PO; ++t) {
-              a[t][2 * u] = y0[t];
-              a[t][2 * u + 1] = y1[t];
+          for (int nt = h * NT; nt < (h + 1) * NT; ++nt) {
+            set_pair(acc[nt], 0, mul2(pair(acc[nt], 0), e0));
+            set_pair(acc[nt], 1, mul2(pair(acc[nt], 1), e1));
+          }
+        }
+        // within the chunk; s0, s1: sum of l from the end of j's block to i
+        float s0 = li0, s1 = li1;
+#pragma unroll
+        for (int jj = 3; jj >= 0; --jj) {
+          if (jj > rt) continue;
+          uint32_t a[PO][4];
+          if (jj == rt) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int nt = 2 * jj + u;
+              const float2 lj = *reinterpret_cast<const float2*>(lo + 8 * nt + c2);
+              const float2 dt = *reinterpret_cast<const float2*>(lo + 64 + 8 * nt + c2);
+              const float2 ej = *reinterpret_cast<const float2*>(lo + 192 + 8 * nt + c2);
+              const float ei0 = lo[192 + 16 * rt + g], ei1 = lo[192 + 16 * rt + g + 8];
+              float2 x0 = mul2(make_float2(ex2((li0 - lj.x) + (ei0 - ej.x)), ex2((li0 - lj.y) + (ei0 - ej.y))), dt);
+              float2 x1 = mul2(make_float2(ex2((li1 - lj.x) + (ei1 - ej.x)), ex2((li1 - lj.y) + (ei1 - ej.y))), dt);
+              x0 = mul2(pair(gm[nt], 0), x0);
+              x1 = mul2(pair(gm[nt], 1), x1);
+              const int j = 8 * u + c2;  // j <= i (the product is cut: a later k_j may be NaN)
+              x0.x = j <= g ? x0.x : 0.f;
+              x0.y = j < g ? x0.y : 0.f;
+              x1.x = j <= g + 8 ? x1.x : 0.f;
+              x1.y = j < g + 8 ? x1.y : 0.f;
+              uint32_t y0[PO], y1[PO];
+              split<PO>(x0, y0);
+              split<PO>(x1, y1);
+#pragma unroll
+              for (int t = 0; t < PO; ++t) {
+                a[t][2 * u] = y0[t];
+                a[t][2 * u + 1] = y1[t];
+              }
+            }
+          } else {
+            if (jj + 1 < rt) {
+              s0 += tot[jj + 1 < 3 ? jj + 1 : 2];
+              s1 += tot[jj + 1 < 3 ? jj + 1 : 2];
+            }
+            const float2 r0 = both(ex2(s0)), r1 = both(ex2(s1));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int nt = 2 * jj + u;
+              const float2 e = *reinterpret_cast<const float2*>(end + 8 * nt + c2);
+              uint32_t y0[PO], y1[PO];
+              split<PO>(mul2(mul2(pair(gm[nt], 0), e), r0), y0);
+              split<PO>(mul2(mul2(pair(gm[nt], 1), e), r1), y1);
+#pragma unroll
+              for (int t = 0; t < PO; ++t) {
+                a[t][2 * u] = y0[t];
+                a[t][2 * u + 1] = y1[t];
+              }
             }
           }
-        } else {
-          if (jj + 1 < rt) {
-            s0 += tot[jj + 1 < 3 ? jj + 1 : 2];
-            s1 += tot[jj + 1 < 3 ? jj + 1 : 2];
-          }
-          const float2 r0 = both(ex2(s0)), r1 = both(ex2(s1));
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int nt = 2 * jj + u;
-            const float2 e = *reinterpret_cast<const float2*>(end + 8 * nt + c2);
-            uint32_t y0[PO], y1[PO];
-            split<PO>(mul2(mul2(pair(gm[nt], 0), e), r0), y0);
-            split<PO>(mul2(mul2(pair(gm[nt], 1), e), r1), y1);
+          for (int nt = 0; nt < NT; nt += 2) {
+            uint32_t b0[P][2], b1[P][2];
+            load_b2_t<P>(b0, b1, vs, kVLd, 16 * jj, h * V + 8 * nt);
+            if (CAREFUL && jj == rt) {
+              add_not_finite<PO>(acc[h * NT + nt], a, vs + (16 * rt * kVLd + h * V + 8 * nt) * 2);
+              add_not_finite<PO>(acc[h * NT + nt + 1], a, vs + (16 * rt * kVLd + h * V + 8 * nt + 8) * 2);
 #pragma unroll
-            for (int t = 0; t < PO; ++t) {
-              a[t][2 * u] = y0[t];
-              a[t][2 * u + 1] = y1[t];
+              for (int t = 0; t < P; ++t)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  b0[t][r] = finite_only(b0[t][r]);
+                  b1[t][r] = finite_only(b1[t][r]);
+                }
             }
+            mma_terms<PO, P>(acc[h * NT + nt], a, b0);
+            mma_terms<PO, P>(acc[h * NT + nt + 1], a, b1);
           }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; nt += 2) {
-          uint32_t b0[P][2], b1[P][2];
-          load_b2_t<P>(b0, b1, vs, kVLd, 16 * jj, h * V + 8 * nt);
-          mma_terms<PO, P>(acc[h * NT + nt], a, b0);
-          mma_terms<PO, P>(acc[h * NT + nt + 1], a, b1);
         }
       }
+    };
+    form(std::false_type{});
+    {  // rare: once more, with care (a NaN of an earlier token stays one)
+      float2 z = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt) z = fma2(pair(acc[nt], 0), z, mul2(pair(acc[nt], 1), make_float2(0.f, 0.f)));
+      if (__any_sync(0xffffffffu, !(z.x + z.y == 0.f))) form(std::true_type{});
     }
     // + w_r (.) v, and out
 #pragma unroll
