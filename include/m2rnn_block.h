@@ -17,7 +17,8 @@
  * What follows the token (channels, or heads x features) is packed.  Both
  * are >= 0 and, except for the scan's `a`, multiples of 16 bytes
  * (M2RNN_ERR_MISALIGNED otherwise).  A null m2rnn_rows pointer means a
- * contiguous tensor.  Outputs are always contiguous.
+ * contiguous tensor.  Outputs are always contiguous.  An output must not overlap
+ * an input or another output except where a function says that it may.
  *
  * Gradients.  The gradients of activations (dx, dq, dk, dv, da) are summed
  * in fp32 and rounded once to in_dtype, the type the preceding layer takes
@@ -58,7 +59,8 @@ typedef struct {
     int silu;       /* 1: SiLU after the convolution, 0: none */
 } m2rnn_conv_shape;
 
-/* state_out must not overlap state. */
+/* y and state_out must overlap neither x, state nor each other: other tokens' runs
+ * still read those (M2RNN_ERR_INVALID_ARG; so for dx and dstate below). */
 int m2rnn_conv_fwd(const m2rnn_conv_shape *s, const void *x, const m2rnn_rows *x_rows,
                    const void *w, const void *bias, const void *state, void *y,
                    void *state_out, void *stream);

@@ -35,9 +35,29 @@ int read_rows(const m2rnn_rows* r, int T, long long width, int dtype, long long 
   return M2RNN_OK;
 }
 
-bool overlap(const void* a, const void* b, size_t bytes) {
+bool overlap_spans(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + bytes && y < x + bytes;
+  return x < y + b_bytes && y < x + a_bytes;
+}
+bool overlap(const void* a, const void* b, size_t bytes) { return overlap_spans(a, bytes, b, bytes); }
+
+// Whether any of the rows ([B][T] of `width` elements of e bytes) overlaps the
+// `bytes` at y.
+bool rows_overlap(const void* x, const m2rnn_rows& r, long long B, long long T, long long width, size_t e,
+                  const void* y, size_t bytes) {
+  if (x == nullptr || y == nullptr || T == 0 || bytes == 0) return false;
+  const long long n = static_cast<long long>(e);
+  const long long token = r.token * n, row = width * n, item = (T - 1) * token + row;
+  if (!overlap_spans(x, (B - 1) * r.batch * n + item, y, bytes)) return false;
+  for (long long b = 0; b < B; ++b) {
+    const char* xb = static_cast<const char*>(x) + b * r.batch * n;
+    if (!overlap_spans(xb, item, y, bytes)) continue;
+    // the first row that ends behind y's start
+    const long long gap = static_cast<const char*>(y) - xb - row;
+    const long long t = gap < 0 || token == 0 ? 0 : gap / token + 1;
+    if (t < T && overlap_spans(xb + t * token, row, y, bytes)) return true;
+  }
+  return false;
 }
 
 int check_all(const void* const* ptrs, int n, int dev, bool required) {
@@ -73,6 +93,24 @@ int check_conv(const m2rnn_conv_shape* s, bool backward) {
 
 size_t conv_state_bytes(const m2rnn_conv_shape* s) {
   return static_cast<size_t>(s->B) * (s->W - 1) * s->C * esize(s->in_dtype);
+}
+
+// The outputs of a whole sequence's convolution (`y`, like x in size, and `so`, like
+// the state) over what neighbouring runs still read: x's rows and the others of `in`
+// (of the type's or, dy, of ge bytes).
+bool conv_outputs_overlap(const m2rnn_conv_shape* s, const m2rnn_rows& xr, const void* x, const void* dy,
+                          size_t ge, const void* state, const void* state2, const void* y, const void* so) {
+  const size_t e = esize(s->in_dtype), sb = conv_state_bytes(s);
+  const size_t n = static_cast<size_t>(s->B) * s->T * s->C;
+  const struct { const void* p; size_t bytes; } outs[] = {{y, n * e}, {so, sb}};
+  for (const auto& o : outs) {
+    if (o.p == nullptr || o.bytes == 0) continue;
+    if (rows_overlap(x, xr, s->B, s->T, s->C, e, o.p, o.bytes)) return true;
+    if (dy != nullptr && n > 0 && overlap_spans(dy, n * ge, o.p, o.bytes)) return true;
+    for (const void* st : {state, state2})
+      if (st != nullptr && overlap_spans(st, sb, o.p, o.bytes)) return true;
+  }
+  return y != nullptr && so != nullptr && overlap_spans(y, n * e, so, sb) && n > 0;
 }
 
 m2rnn::ConvParams conv_params(const m2rnn_conv_shape* s, const m2rnn_rows& xr, const void* x,
@@ -359,14 +397,13 @@ int m2rnn_conv_fwd(const m2rnn_conv_shape* s, const void* x, const m2rnn_rows* x
   if (rc != M2RNN_OK) return rc;
   m2rnn_rows xr;
   if ((rc = read_rows(x_rows, s->T, s->C, s->in_dtype, 16, &xr)) != M2RNN_OK) return rc;
+  if (conv_outputs_overlap(s, xr, x, nullptr, 0, state, nullptr, y, state_out)) return M2RNN_ERR_INVALID_ARG;
   int dev, sms, *status;
   if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
   const void* req[] = {w};
   const void* opt[] = {bias, state, state_out};
   if ((rc = require(req, dev)) != M2RNN_OK || (rc = allow(opt, dev)) != M2RNN_OK) return rc;
   const size_t sb = conv_state_bytes(s);
-  if (state != nullptr && state_out != nullptr && overlap(state, state_out, sb))
-    return M2RNN_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (s->T == 0) {
     if (state_out == nullptr) return M2RNN_OK;
@@ -398,6 +435,8 @@ int m2rnn_conv_bwd(const m2rnn_conv_shape* s, const void* x, const m2rnn_rows* x
   if (rc != M2RNN_OK) return rc;
   m2rnn_rows xr;
   if ((rc = read_rows(x_rows, s->T, s->C, s->in_dtype, 16, &xr)) != M2RNN_OK) return rc;
+  if (conv_outputs_overlap(s, xr, x, dy, esize(s->grad_dtype), state, dstate_out, dx, dstate))
+    return M2RNN_ERR_INVALID_ARG;
   int dev, sms, *status;
   if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
   const void* req[] = {w, dw};
