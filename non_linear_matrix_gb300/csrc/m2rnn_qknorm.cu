@@ -90,7 +90,8 @@ __device__ __forceinline__ void rotate(const QkParams& p, const Lane& a, float2 
     for (int j = 0; j < 4; ++j) {
       const float c = (j & 1) ? a.c[j / 2].y : a.c[j / 2].x;
       const float n = TURN * ((j & 1) ? a.n[j / 2].y : a.n[j / 2].x);
-      u[j] = make_float2(fmaf(u[j].x, c, -u[j].y * n), fmaf(u[j].y, c, u[j].x * n));
+      const float2 r = make_float2(fmaf(u[j].x, c, -u[j].y * n), fmaf(u[j].y, c, u[j].x * n));
+      u[j] = a.turns ? r : u[j];  // (1 and 0 in place of c and n would make NaN of a partner's inf)
     }
     return;
   }
