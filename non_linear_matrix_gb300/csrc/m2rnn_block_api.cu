@@ -248,7 +248,7 @@ ScanPlan sized_for(ScanPlan q, const m2rnn_shape* s, int B) {
 // CTAs that share a chunk's head blocks.  Outputs: about 1,216 (twice what is
 // resident), so that they even out over the SMs; a CTA's own cost, its q and k tiles
 // and their product, is about 0.4 of a head block.  B=8 T=2048 N=32 (256 chunks, 8
-// head blocks): 52 us, with one CTA per chunk 63, with 3,648 53.
+// head blocks): the call takes 64 us, with one CTA per chunk 100, with 3,648 67.
 int scan_out_split(const m2rnn_shape* s, const ScanPlan& q) {
   const long long chunks = static_cast<long long>(s->B) * (s->Nq == 0 ? 1 : s->Nq) * q.nc;
   long long want = (1216 + chunks - 1) / chunks;
@@ -258,7 +258,8 @@ int scan_out_split(const m2rnn_shape* s, const ScanPlan& q) {
 }
 // Gradients: more than one costs shares of dq and dk in fp32, so only as many as
 // it takes to give each SM its two resident CTAs.  A training step at B=1 T=8192
-// N=32 (128 chunks) takes 139 us so, 181 with one CTA per chunk, 144 with 608 CTAs.
+// N=32 (128 chunks) takes 134 us so, 139 with 608 CTAs (and, when it took 139, 181
+// with one CTA per chunk).
 int scan_bwd_split(const m2rnn_shape* s, const ScanPlan& q) {
   const long long chunks = static_cast<long long>(s->B) * (s->Nq == 0 ? 1 : s->Nq) * q.nc;
   long long want = 304 / chunks;

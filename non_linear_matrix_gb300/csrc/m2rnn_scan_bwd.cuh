@@ -30,15 +30,15 @@
 // dw_r and the gate; warps 4 to 7 dv and everything within the chunk, 16 rows j
 // each, and the fetching of the next head block.  G and the sum of E L wait in
 // shared memory, in the order of the accumulators' lanes (in registers they
-// spill: 336 us instead of 235).  The products within the chunk are formed with j
+// spilled: 336 us instead of 245).  The products within the chunk are formed with j
 // along the rows, which leaves G L in the registers as the A operand of dv.
 // Between different 16-token blocks L is a product of a row's and a column's
 // factor, as in the forward pass.  States enter with three bf16 terms where a
 // value that stays in fp32 depends on them (dl) and with two for dv.
 //
-// Bound by latency and the shared-memory pipe (55 % of its cycles; 36 % of issue
-// slots, 17 % of the tensor pipe's): B=8 T=4096 N=32 K=64 V=16 takes 235 us.  At
-// 248 us, before the last steps, it took 173 without the products within the chunk,
+// Bound by latency and the shared-memory pipe (54 % of its cycles; 37 % of issue
+// slots, 18 % of the tensor pipe's): B=8 T=4096 N=32 K=64 V=16 takes 250 us (235 with
+// one-term weights).  An earlier state of it, 248 us, took 173 without the products within the chunk,
 // 206 without the fetching, 222 without the states' side and 241 without the gate.
 // The chunk's side is uneven (row block 0 has four blocks, row block 3 one), yet
 // handing one over to row block 3's warp gained nothing (269 us: more spills).

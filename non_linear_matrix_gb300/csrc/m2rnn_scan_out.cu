@@ -14,9 +14,10 @@
 //
 // Bound by latency: each head block waits for its state, converts it and passes
 // two barriers, at four CTAs per SM (registers, shared memory).  B=1 T=65536 N=64
-// K=64 V=16: 182 us; B=8 T=4096 N=32: 53 us, of which without the state's fetch 40 remain and without the
-// products within the chunk 48.  Double-buffered tiles (three CTAs) took 63, five
-// CTAs (spills) 61.
+// K=64 V=16: 285 us (issue 40 %, shared-memory pipe 50 %, tensor pipe 21 %); B=8 T=4096
+// N=32: 79 us.  With one-term weights and states it was 182 and 53, of which
+// without the state's fetch 40 remained and without the products within the chunk 48;
+// double-buffered tiles (three CTAs) took 63 then, five CTAs (spills) 61.
 #include <type_traits>
 
 #include "m2rnn_scan.cuh"

@@ -13,9 +13,9 @@
 // time from zero states; join_kernel then carries the states from segment to
 // segment.
 //
-// Bound by the three-term products (44 % of the tensor pipe's cycles) and the
-// instructions around them (48 % of issue slots), not by the states' traffic:
-// B=1 T=65536 N=64 K=64 V=16 takes 99 us.  B=8 T=4096 N=32: 33 us forwards, 28 in reverse; the join
+// Bound by the three-term products (42 % of the tensor pipe's cycles), the
+// instructions around them (46 % of issue slots) and the states' traffic (54 % of
+// DRAM's): B=1 T=65536 N=64 K=64 V=16 takes 101 us.  B=8 T=4096 N=32: 33 us forwards, 28 in reverse; the join
 // 5 to 8.  Four CTAs per SM: without that bound on the registers 107 us, with five
 // (spills) 151.
 #include "m2rnn_scan.cuh"
