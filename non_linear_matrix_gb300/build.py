@@ -30,7 +30,9 @@ SOURCES = ["m2rnn_api.cu", "m2rnn_fwd.cu", "m2rnn_bwd.cu", "m2rnn_bwd_pipe.cu", 
            "m2rnn_noalloc.cu", "m2rnn_norm.cu", "m2rnn_block_api.cu", "m2rnn_conv.cu",
            "m2rnn_qknorm.cu", "m2rnn_scan_step.cu", "m2rnn_scan_states.cu",
            "m2rnn_scan_out.cu", "m2rnn_scan_bwd.cu", "m2rnn_scan_bwd_bf16_lo.cu",
-           "m2rnn_scan_bwd_bf16_hi.cu", "m2rnn_scan_bwd_f32_lo.cu", "m2rnn_scan_bwd_f32_hi.cu"]
+           "m2rnn_scan_bwd_bf16_hi.cu", "m2rnn_scan_bwd_f32_lo.cu", "m2rnn_scan_bwd_f32_hi.cu",
+           "m2rnn_ffn_api.cu", "m2rnn_addnorm.cu", "m2rnn_few.cu", "m2rnn_gemm_pair.cu",
+           "m2rnn_gemm_grad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -1,0 +1,351 @@
+// m2rnn_addnorm.cu -- the residual's addition with the RMS norm behind it, its
+// gradient, its 8-bit output, and the quantiser of rows.
+//
+// A row belongs to a group of 1 to 16 warps whose threads hold it in registers
+// (vectors of 8 elements, `NV` each): one pass over memory, the mean square between
+// load and store.  Bound by HBM: 4 D e bytes per row forward (e the element's size),
+// 4 D e backward.
+#include "m2rnn_ffn.h"
+#include "m2rnn_vec.cuh"
+
+namespace m2rnn {
+namespace {
+
+constexpr float kE4m3Max = 448.f;
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// The larger one; NaN if either is.
+__device__ __forceinline__ float nan_max(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = nan_max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Two e4m3 codes (round to nearest even, saturating; NaN stays NaN), lo in bits 0..7.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 8 codes of o / scale.
+__device__ __forceinline__ uint2 codes8(const float (&o)[8], float scale) {
+  float c[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c[j] = scale == 0.f ? 0.f : __fdiv_rn(o[j], scale);
+  return make_uint2(e4m3x2(c[0], c[1]) | (e4m3x2(c[2], c[3]) << 16), e4m3x2(c[4], c[5]) | (e4m3x2(c[6], c[7]) << 16));
+}
+
+// Sums (or maxima) over a row's warps, in warp order; a CTA of more than one warp per row
+// holds one row.
+template <int N, bool MAX>
+__device__ __forceinline__ void row_reduce(float (&v)[N], int warps, float* sm) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = MAX ? warp_max(v[i]) : warp_sum(v[i]);
+  if (warps == 1) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) sm[warp * N + i] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float s = sm[i];
+    for (int w = 1; w < warps; ++w) s = MAX ? nan_max(s, sm[w * N + i]) : s + sm[w * N + i];
+    v[i] = s;
+  }
+  __syncthreads();
+}
+
+// ADD: r = x + res is stored.  Q8: the output as codes and a scale.  NORM = false:
+// the quantiser of x alone.
+template <bool F32, int NV, bool ADD, bool Q8>
+__global__ void __launch_bounds__(512) add_norm_kernel(Norm2Params p, int warps, int rows_per_cta) {
+  using T = typename Elem<F32>::T;
+  __shared__ float sm[32];
+  const int group = warps * 32, vecs = p.D / 8;
+  const int lane = warps == 1 ? threadIdx.x & 31 : threadIdx.x;
+  const long long row = static_cast<long long>(blockIdx.x) * rows_per_cta + (warps == 1 ? threadIdx.x >> 5 : 0);
+  if (row >= p.M) return;  // (whole warps; CTAs of several warps per row hold one row)
+  const size_t D = p.D, n = static_cast<size_t>(p.M) * D, at = static_cast<size_t>(row) * D;
+  const T* x = static_cast<const T*>(p.x) + row * p.x_row;
+  const T* res = ADD ? static_cast<const T*>(p.res) + row * p.res_row : nullptr;
+  const size_t x_ext = static_cast<size_t>(p.M - 1) * p.x_row + D;
+  const size_t res_ext = static_cast<size_t>(p.M - 1) * p.res_row + D;
+  Raw<F32, 8> xv[NV], rv[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = lane + i * group;
+    xv[i] = rv[i] = raw_zero<F32, 8>();
+    if (v < vecs) {
+      if (in_range(p.status, static_cast<size_t>(row) * p.x_row + 8 * v, 8, x_ext, CHK_NORM2_IN))
+        xv[i] = raw_load<F32, 8, false>(x + 8 * v);
+      if (ADD && in_range(p.status, static_cast<size_t>(row) * p.res_row + 8 * v, 8, res_ext, CHK_NORM2_IN))
+        rv[i] = raw_load<F32, 8, false>(res + 8 * v);
+    }
+  }
+  float ss[1] = {0.f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = lane + i * group;
+    float o[8];
+    raw_unpack<F32, 8>(xv[i], o);
+    if constexpr (ADD) {
+      float b[8];
+      raw_unpack<F32, 8>(rv[i], b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] += b[j];
+      // rounded as it is stored: the norm acts on the stream that the next layer reads
+      xv[i] = raw_pack<F32, 8>(o);
+      raw_unpack<F32, 8>(xv[i], o);
+      if (v < vecs && in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
+        raw_store<F32, 8>(static_cast<T*>(p.r) + at + 8 * v, xv[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss[0] = fmaf(o[j], o[j], ss[0]);
+  }
+  row_reduce<1, false>(ss, warps, sm);
+  const float rstd = 1.f / sqrtf(ss[0] / static_cast<float>(p.D) + p.eps);
+  float top[1] = {0.f};
+  float keep[Q8 ? NV : 1][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = lane + i * group;
+    float o[8], w[8];
+    raw_unpack<F32, 8>(xv[i], o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 1.f;
+    if (p.w != nullptr && v < vecs && in_range(p.status, 8 * v, 8, D, CHK_NORM2_PARAM))
+      load_vec<F32, 8>(static_cast<const T*>(p.w) + 8 * v, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = o[j] * rstd * w[j];
+    if constexpr (Q8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        keep[i][j] = o[j];
+        if (v < vecs) top[0] = nan_max(top[0], fabsf(o[j]));
+      }
+    } else {
+      if (v < vecs && in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
+        store_vec<F32, 8>(static_cast<T*>(p.y) + at + 8 * v, o);
+    }
+  }
+  if constexpr (Q8) {
+    row_reduce<1, true>(top, warps, sm);
+    const float scale = __fdiv_rn(top[0], kE4m3Max);
+    if (lane == 0 && in_range(p.status, row, 1, p.M, CHK_NORM2_OUT)) p.scale[row] = scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = lane + i * group;
+      if (v < vecs && in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
+        *reinterpret_cast<uint2*>(p.q + at + 8 * v) = codes8(keep[i], scale);
+    }
+  }
+}
+
+// The quantiser: a CTA per row, which reads the row twice (its second time from L1 or L2).
+template <bool F32>
+__global__ void __launch_bounds__(256) quant_rows_kernel(Norm2Params p) {
+  using T = typename Elem<F32>::T;
+  __shared__ float sm[32];
+  const int vecs = p.D / 8;
+  const long long row = blockIdx.x;
+  const size_t n = static_cast<size_t>(p.M) * p.D, at = static_cast<size_t>(row) * p.D;
+  const size_t x0 = static_cast<size_t>(row) * p.x_row, x_ext = static_cast<size_t>(p.M - 1) * p.x_row + p.D;
+  const T* x = static_cast<const T*>(p.x) + x0;
+  float top[1] = {0.f};
+  for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (in_range(p.status, x0 + 8 * v, 8, x_ext, CHK_NORM2_IN)) load_vec<F32, 8>(x + 8 * v, o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top[0] = nan_max(top[0], fabsf(o[j]));
+  }
+  row_reduce<1, true>(top, blockDim.x / 32, sm);
+  const float scale = __fdiv_rn(top[0], kE4m3Max);
+  if (threadIdx.x == 0 && in_range(p.status, row, 1, p.M, CHK_NORM2_OUT)) p.scale[row] = scale;
+  for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (in_range(p.status, x0 + 8 * v, 8, x_ext, CHK_NORM2_IN)) load_vec<F32, 8>(x + 8 * v, o);
+    if (in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
+      *reinterpret_cast<uint2*>(p.q + at + 8 * v) = codes8(o, scale);
+  }
+}
+
+// Backward: with n = r rstd, p = w dy:  dx = dr + rstd (p - n mean(p n)),  dw = sum dy n.
+// A group walks over rows (p.nparts groups in all) with its share of dw in registers and
+// writes it to `part`; sum_parts adds the shares in order.
+template <bool F32, int NV>
+__global__ void __launch_bounds__(512) add_norm_bwd_kernel(Norm2Params p, int warps) {
+  using T = typename Elem<F32>::T;
+  __shared__ float sm[64];
+  const int group = warps * 32, vecs = p.D / 8;
+  const int lane = warps == 1 ? threadIdx.x & 31 : threadIdx.x;
+  const int part = warps == 1 ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  let_next_begin();
+  if (part >= p.nparts) return;
+  const size_t D = p.D, n = static_cast<size_t>(p.M) * D;
+  const size_t r_ext = static_cast<size_t>(p.M - 1) * p.x_row + D;
+  float dw[NV][8], w[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = lane + i * group;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      dw[i][j] = 0.f;
+      w[i][j] = 1.f;
+    }
+    if (p.w != nullptr && v < vecs && in_range(p.status, 8 * v, 8, D, CHK_NORM2_PARAM))
+      load_vec<F32, 8>(static_cast<const T*>(p.w) + 8 * v, w[i]);
+  }
+  for (long long row = part; row < p.M; row += p.nparts) {
+    const size_t at = static_cast<size_t>(row) * D, r0 = static_cast<size_t>(row) * p.x_row;
+    Raw<F32, 8> rv[NV], yv[NV], gv[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = lane + i * group;
+      rv[i] = yv[i] = gv[i] = raw_zero<F32, 8>();
+      if (v < vecs) {
+        if (in_range(p.status, r0 + 8 * v, 8, r_ext, CHK_NORM2_IN))
+          rv[i] = raw_load<F32, 8>(static_cast<const T*>(p.x) + r0 + 8 * v);
+        if (in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_IN)) {
+          yv[i] = raw_load<F32, 8, false>(static_cast<const T*>(p.dy) + at + 8 * v);
+          if (p.dr != nullptr) gv[i] = raw_load<F32, 8, false>(static_cast<const T*>(p.dr) + at + 8 * v);
+        }
+      }
+    }
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float r[8], dy[8];
+      raw_unpack<F32, 8>(rv[i], r);
+      raw_unpack<F32, 8>(yv[i], dy);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[0] = fmaf(r[j], r[j], s[0]);
+        s[1] = fmaf(r[j], dy[j] * w[i][j], s[1]);
+      }
+    }
+    row_reduce<2, false>(s, warps, sm);
+    const float rstd = 1.f / sqrtf(s[0] / static_cast<float>(p.D) + p.eps);
+    const float c = s[1] * rstd / static_cast<float>(p.D);  // mean(p n)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = lane + i * group;
+      float r[8], dy[8], o[8];
+      raw_unpack<F32, 8>(rv[i], r);
+      raw_unpack<F32, 8>(yv[i], dy);
+      raw_unpack<F32, 8>(gv[i], o);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float nj = r[j] * rstd;
+        o[j] += rstd * (w[i][j] * dy[j] - nj * c);
+        dw[i][j] = fmaf(dy[j], nj, dw[i][j]);
+      }
+      if (v < vecs && in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
+        store_vec<F32, 8>(static_cast<T*>(p.dx) + at + 8 * v, o);
+    }
+  }
+  if (p.part == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = lane + i * group;
+    const size_t at = static_cast<size_t>(part) * D + 8 * v;
+    if (v < vecs && in_range(p.status, at, 8, static_cast<size_t>(p.nparts) * D, CHK_NORM2_PARAM))
+      store_vec<true, 8>(p.part + at, dw[i]);
+  }
+}
+
+// Vectors per thread and warps per row: the fewest warps (1, 2, 4, 8, 16) whose threads
+// hold the row in four vectors each, and then as few vectors as that takes.
+struct RowPlan {
+  int nv, warps;
+};
+RowPlan row_plan(int D, int most) {
+  const int vecs = D / 8;
+  int warps = 1;
+  while (warps < 16 && warps * 32 * most < vecs) warps *= 2;
+  const int nv = (vecs + warps * 32 - 1) / (warps * 32);
+  return {nv <= 1 ? 1 : nv <= 2 ? 2 : 4, warps};
+}
+
+template <bool F32, int NV>
+cudaError_t launch_nv(const Norm2Params& p, int warps, cudaStream_t st) {
+  const int per = warps == 1 ? 4 : 1;
+  const dim3 grid(static_cast<unsigned>((p.M + per - 1) / per));
+  const int threads = warps == 1 ? 128 : 32 * warps;
+  const bool add = p.res != nullptr, q8 = p.q != nullptr;
+  if (add && q8)
+    add_norm_kernel<F32, NV, true, true><<<grid, threads, 0, st>>>(p, warps, per);
+  else if (add)
+    add_norm_kernel<F32, NV, true, false><<<grid, threads, 0, st>>>(p, warps, per);
+  else if (q8)
+    add_norm_kernel<F32, NV, false, true><<<grid, threads, 0, st>>>(p, warps, per);
+  else
+    add_norm_kernel<F32, NV, false, false><<<grid, threads, 0, st>>>(p, warps, per);
+  return cudaGetLastError();
+}
+
+template <bool F32>
+cudaError_t launch_fwd_t(const Norm2Params& p, int sms, cudaStream_t st) {
+  // Few rows: one vector per thread, the row's loads all at once.
+  const RowPlan r = row_plan(p.D, p.M <= 2 * sms ? 1 : 4);
+  return r.nv == 1 ? launch_nv<F32, 1>(p, r.warps, st)
+         : r.nv == 2 ? launch_nv<F32, 2>(p, r.warps, st)
+                     : launch_nv<F32, 4>(p, r.warps, st);
+}
+
+template <bool F32, int NV>
+cudaError_t launch_bwd_nv(const Norm2Params& p, int warps, cudaStream_t st) {
+  const int per = warps == 1 ? 4 : 1;
+  const int grid = (p.nparts + per - 1) / per, threads = warps == 1 ? 128 : 32 * warps;
+  add_norm_bwd_kernel<F32, NV><<<grid, threads, 0, st>>>(p, warps);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || p.part == nullptr) return e;
+  const SumOut o = {{p.dw, nullptr, nullptr}, {p.D, 0, 0}};
+  return launch_sum_parts(p.part, p.nparts, o, p.status, CHK_NORM2_PARAM, st);
+}
+template <bool F32>
+cudaError_t launch_bwd_t(const Norm2Params& p, cudaStream_t st) {
+  const RowPlan r = row_plan(p.D, 4);
+  return r.nv == 1 ? launch_bwd_nv<F32, 1>(p, r.warps, st)
+         : r.nv == 2 ? launch_bwd_nv<F32, 2>(p, r.warps, st)
+                     : launch_bwd_nv<F32, 4>(p, r.warps, st);
+}
+
+}  // namespace
+
+// Groups of the backward kernel: as many as are resident on 152 SMs, and a row each at least.
+int add_norm_bwd_parts(const m2rnn_norm_shape* s) {
+  const RowPlan r = row_plan(s->D, 4);
+  const long long most = 152LL * 16 / r.warps;
+  return static_cast<int>(s->M < most ? s->M : most);
+}
+
+cudaError_t launch_add_norm(const Norm2Params& p, bool f32, int sms, cudaStream_t st) {
+  return f32 ? launch_fwd_t<true>(p, sms, st) : launch_fwd_t<false>(p, sms, st);
+}
+cudaError_t launch_add_norm_bwd(const Norm2Params& p, bool f32, cudaStream_t st) {
+  return f32 ? launch_bwd_t<true>(p, st) : launch_bwd_t<false>(p, st);
+}
+cudaError_t launch_quant_rows(const Norm2Params& p, bool f32, int sms, cudaStream_t st) {
+  (void)sms;
+  int threads = 32;
+  while (threads < 256 && threads * 8 < p.D) threads *= 2;
+  if (f32)
+    quant_rows_kernel<true><<<static_cast<unsigned>(p.M), threads, 0, st>>>(p);
+  else
+    quant_rows_kernel<false><<<static_cast<unsigned>(p.M), threads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace m2rnn

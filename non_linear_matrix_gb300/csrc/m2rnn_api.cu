@@ -79,6 +79,7 @@ int check_shape(const m2rnn_shape* s) { return m2rnn::validate_shape(s); }
 namespace m2rnn {
 int host_device_info(int* dev, int** status, int* sms) { return device_info(dev, status, sms); }
 int host_check_ptr(const void* p, int dev, bool required) { return check_ptr(p, dev, required); }
+unsigned long long host_wait_limit_ns() { return static_cast<unsigned long long>(g_wait_limit_ns.load()); }
 int host_check_elem_ptr(const void* p, int dev, size_t unit) {
   if (p == nullptr) return M2RNN_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(p) % unit != 0) return M2RNN_ERR_MISALIGNED;
@@ -509,7 +510,7 @@ int decode_impl(const m2rnn_shape* s, const void* q, const void* k, const void* 
 
 extern "C" {
 
-int m2rnn_version(void) { return 202; }
+int m2rnn_version(void) { return 203; }
 
 int m2rnn_checked(void) { return M2RNN_CHECK ? 1 : 0; }
 

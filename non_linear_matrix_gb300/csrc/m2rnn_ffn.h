@@ -1,0 +1,111 @@
+// m2rnn_ffn.h (internal) -- launch parameters of the feed-forward operators
+// (residual and norm, gated products, 8-bit product).  Not part of the public ABI.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/m2rnn_ffn.h"
+#include "m2rnn_block.h"
+
+namespace m2rnn {
+
+// m2rnn_api.cu: the time limit of waits inside kernels.
+unsigned long long host_wait_limit_ns();
+
+// Location codes of the index checks and of waits that gave up.
+enum FfnCheckSite : int {
+  CHK_NORM2_IN = 801,     // x, res, r, dy, dr loads
+  CHK_NORM2_OUT = 802,    // r, y, q, scale, dx stores
+  CHK_NORM2_PARAM = 803,  // w loads, dw partials and sums
+  CHK_GLU_IN = 901,       // x, weights, scales, dh, res loads
+  CHK_GLU_OUT = 902,      // h, y, dx, dwg, dwu stores
+  CHK_GLU_WS = 903,       // bf16 terms and the gradients of g and u
+  SITE_GEMM_COPY = 951,   // waits of the product kernel
+  SITE_GEMM_MMA = 952,
+  SITE_GEMM_OUT = 953,
+  SITE_GEMM_DRAIN = 954,
+};
+
+struct Norm2Params {
+  const void *x, *res, *w, *dy, *dr;
+  void *r, *y, *dx;
+  uint8_t* q;
+  float* scale;
+  float* part;  // backward: [nparts][D]
+  float* dw;
+  long long x_row, res_row;
+  long long M;
+  int D;
+  int nparts;
+  float eps;
+  int* status;
+};
+cudaError_t launch_add_norm(const Norm2Params& p, bool f32, int sms, cudaStream_t st);
+cudaError_t launch_add_norm_bwd(const Norm2Params& p, bool f32, cudaStream_t st);
+int add_norm_bwd_parts(const m2rnn_norm_shape* s);
+cudaError_t launch_quant_rows(const Norm2Params& p, bool f32, int sms, cudaStream_t st);
+
+// Products on the 5th-generation tensor core: out[m][n] = sum over segments and k of
+// A[z][m][k] B[z][n][k], A and B as tensor maps of three dimensions.
+enum GemmEpi : int {
+  EPI_GLU,    // act(g) (.) u of a pair of products
+  EPI_DGLU,   // gradients of g and u, in bf16 (1 term) or as 3 bf16 terms (fp32)
+  EPI_STORE,  // the product itself
+  EPI_GLU8,   // act(g) (.) u with scales
+  EPI_LIN8,   // the product with scales, plus res
+};
+constexpr int kMaxSeg = 12;
+struct GemmParams {
+  CUtensorMap a, b0, b1;  // b1: of a pair, or of the second operand
+  int nseg;
+  int8_t az[kMaxSeg], bi[kMaxSeg], bz[kMaxSeg];  // a segment's plane of A, its B and plane
+  int kt;                   // K tiles of a segment
+  int kc;                   // K tiles of a chunk (fp32: what one chain of sums takes)
+  int mt, nt, nbatch;       // tiles; products that share B (A's planes az_step apart)
+  int az_step;
+  long long M;              // rows and columns of out
+  int N;
+  void* out[2];             // one for each of nbatch
+  const void* in;           // dh, res
+  long long in_row;
+  const float *sa, *sb0, *sb1;
+  int act;
+  int* status;
+  unsigned long long limit_ns;
+};
+// kind: operands' element (0 bf16, 1 e4m3); a_mn, b_mn: whether M or N runs fastest in memory.
+struct GemmKind {
+  int epi;
+  bool e4m3, f32, a_mn, b_mn;
+  int bn;  // accumulator columns of a tile: 128 or 256
+};
+cudaError_t launch_gemm(const GemmParams& p, const GemmKind& k, int sms, cudaStream_t st);
+int gemm_bn(int epi, bool f32, long long m, int n, int nbatch, int sms);
+
+// Few tokens: the weights stream through registers (mma.sync).
+struct FewParams {
+  const void *x, *w0, *w1, *res;
+  long long x_row, res_row;
+  const float *sa, *sb0, *sb1;
+  void* out;
+  int M, D, F, act;
+  int* status;
+};
+constexpr int kFewMost = 64;
+cudaError_t launch_few(const FewParams& p, int epi, bool e4m3, bool f32, cudaStream_t st);
+
+// fp32 matrices into three bf16 terms [3][M][D] each.
+struct SplitParams {
+  const float* src[3];
+  long long row[3], M[3];
+  __nv_bfloat16* dst[3];
+  int D, n;
+  int* status;
+};
+cudaError_t launch_split(const SplitParams& p, cudaStream_t st);
+
+}  // namespace m2rnn

@@ -1,0 +1,550 @@
+// m2rnn_ffn_api.cu -- the extern "C" entry points declared in
+// include/m2rnn_ffn.h: argument validation, tensor maps and launch planning of the
+// residual and norm, the gated products and the 8-bit product.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "m2rnn_ffn.h"
+
+namespace {
+
+using m2rnn::host_check_ptr;
+using m2rnn::host_device_info;
+
+int status_from_cuda(cudaError_t e) { return e == cudaSuccess ? M2RNN_OK : M2RNN_ERR_CUDA; }
+bool is_dtype(int d) { return d == M2RNN_F32 || d == M2RNN_BF16; }
+size_t esize(int dtype) { return dtype == M2RNN_F32 ? 4 : 2; }
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+constexpr double kMostElems = 1099511627776.0;  // 2^40
+
+template <int N>
+int check(const void* const (&ptrs)[N], int dev, bool required) {
+  for (const void* p : ptrs) {
+    const int rc = host_check_ptr(p, dev, required);
+    if (rc != M2RNN_OK) return rc;
+  }
+  return M2RNN_OK;
+}
+
+// A row distance (in elements of e bytes) keeps rows on 16-byte boundaries, and M rows stay
+// below 2^40 elements.
+int check_row(long long row, size_t e, long long M, long long least) {
+  if (row < 0 || row < least) return M2RNN_ERR_INVALID_ARG;
+  if ((row * static_cast<long long>(e)) % 16 != 0) return M2RNN_ERR_MISALIGNED;
+  if (static_cast<double>(row) * (M > 0 ? M : 1) >= kMostElems) return M2RNN_ERR_UNSUPPORTED_SHAPE;
+  return M2RNN_OK;
+}
+
+// ---- residual and norm ---------------------------------------------------------
+
+int check_norm(const m2rnn_norm_shape* s, int most_d) {
+  if (s == nullptr) return M2RNN_ERR_INVALID_ARG;
+  if (s->M < 0 || s->D < 1 || !is_dtype(s->in_dtype)) return M2RNN_ERR_INVALID_ARG;
+  if (s->D % 8 != 0 || s->D > most_d || s->M >= (1LL << 31)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
+  if (static_cast<double>(s->M) * s->D >= kMostElems) return M2RNN_ERR_UNSUPPORTED_SHAPE;
+  return M2RNN_OK;
+}
+constexpr int kNormMostD = 16384, kMostD = 1 << 20;
+
+// Whether the rows of x overlap `bytes` at y (by their whole span: a false alarm only for
+// outputs between the rows of a wider buffer, which contiguous outputs never are).
+bool spans_overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  if (a == nullptr || b == nullptr || a_bytes == 0 || b_bytes == 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+size_t rows_bytes(long long M, long long row, long long D, size_t e) {
+  return M == 0 ? 0 : (static_cast<size_t>(M - 1) * row + D) * e;
+}
+
+int add_norm(const m2rnn_norm_shape* s, const void* x, long long x_row, const void* res, long long res_row,
+             const void* w, float eps, void* r, void* y, void* q, float* scale, bool q8, void* stream) {
+  int rc = check_norm(s, kNormMostD);
+  if (rc != M2RNN_OK) return rc;
+  if (!(eps >= 0.f)) return M2RNN_ERR_INVALID_ARG;  // also rejects NaN
+  const size_t e = esize(s->in_dtype);
+  if ((rc = check_row(x_row, e, s->M, 0)) != M2RNN_OK) return rc;
+  if (res != nullptr && (rc = check_row(res_row, e, s->M, 0)) != M2RNN_OK) return rc;
+  if ((res == nullptr) != (r == nullptr) && s->M > 0) return M2RNN_ERR_INVALID_ARG;
+  // outputs apart from inputs and each other; r may be x or res itself
+  const size_t n = static_cast<size_t>(s->M) * s->D * e;
+  const size_t xb = rows_bytes(s->M, x_row, s->D, e), rb = rows_bytes(s->M, res_row, s->D, e);
+  const struct { const void* p; size_t bytes; } outs[] = {
+      {r, n}, {y, n}, {q, static_cast<size_t>(s->M) * s->D}, {scale, static_cast<size_t>(s->M) * 4}};
+  for (int i = 0; i < 4; ++i) {
+    const bool in_place_x = i == 0 && r == x && x_row == s->D, in_place_r = i == 0 && r == res && res_row == s->D;
+    if (!in_place_x && spans_overlap(x, xb, outs[i].p, outs[i].bytes)) return M2RNN_ERR_INVALID_ARG;
+    if (!in_place_r && res != nullptr && spans_overlap(res, rb, outs[i].p, outs[i].bytes))
+      return M2RNN_ERR_INVALID_ARG;
+    if (spans_overlap(w, static_cast<size_t>(s->D) * e, outs[i].p, outs[i].bytes)) return M2RNN_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (spans_overlap(outs[j].p, outs[j].bytes, outs[i].p, outs[i].bytes)) return M2RNN_ERR_INVALID_ARG;
+  }
+  int dev, sms, *status;
+  if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
+  if (s->M == 0) return M2RNN_OK;
+  const void* opt[] = {res, w, r};
+  if ((rc = check(opt, dev, false)) != M2RNN_OK) return rc;
+  const void* req[] = {x, q8 ? q : y, q8 ? static_cast<const void*>(scale) : x};
+  if ((rc = check(req, dev, true)) != M2RNN_OK) return rc;
+  m2rnn::Norm2Params p{};
+  p.x = x;
+  p.res = res;
+  p.w = w;
+  p.r = r;
+  p.y = y;
+  p.q = static_cast<uint8_t*>(q);
+  p.scale = scale;
+  p.x_row = x_row;
+  p.res_row = res_row;
+  p.M = s->M;
+  p.D = s->D;
+  p.eps = eps;
+  p.status = status;
+  return status_from_cuda(
+      m2rnn::launch_add_norm(p, s->in_dtype == M2RNN_F32, sms, static_cast<cudaStream_t>(stream)));
+}
+
+// ---- products --------------------------------------------------------------------
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder of tensor maps, looked up once.
+EncodeFn encoder() {
+  static std::atomic<void*> fn{nullptr};
+  void* f = fn.load();
+  if (f == nullptr) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    fn.store(f);
+  }
+  return reinterpret_cast<EncodeFn>(f);
+}
+
+// [planes][outer][inner] elements of e bytes (1: e4m3, 2: bf16), rows `row` elements and
+// planes `plane` elements apart, read in boxes of 128 bytes by `box` rows.
+bool make_map(CUtensorMap* m, const void* base, size_t e, long long inner, long long outer, long long planes,
+              long long row, long long plane, int box) {
+  const EncodeFn f = encoder();
+  if (f == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                              static_cast<cuuint64_t>(planes)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row) * e, static_cast<cuuint64_t>(plane) * e};
+  const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(128 / e), static_cast<cuuint32_t>(box), 1};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return f(m, e == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+           dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int check_glu(const m2rnn_glu_shape* s, bool q8) {
+  if (s == nullptr) return M2RNN_ERR_INVALID_ARG;
+  if (s->M < 0 || s->D < 1 || s->F < 1 || !is_dtype(s->in_dtype)) return M2RNN_ERR_INVALID_ARG;
+  if (s->act != 0 && s->act != 1) return M2RNN_ERR_INVALID_ARG;
+  if (q8 && s->in_dtype != M2RNN_BF16) return M2RNN_ERR_INVALID_ARG;
+  if (s->D % (q8 ? 16 : 8) != 0 || s->F % 8 != 0 || s->D > kMostD || s->F > kMostD || s->M >= (1LL << 31))
+    return M2RNN_ERR_UNSUPPORTED_SHAPE;
+  const double M = static_cast<double>(s->M);
+  if (M * s->D >= kMostElems || M * s->F >= kMostElems || static_cast<double>(s->D) * s->F >= kMostElems / 4)
+    return M2RNN_ERR_UNSUPPORTED_SHAPE;
+  return M2RNN_OK;
+}
+
+// The products of bf16 terms that make up one fp32 product, small ones first.
+constexpr int kPairs = 6;
+constexpr int8_t kPairA[kPairs] = {2, 1, 0, 1, 0, 0}, kPairB[kPairs] = {0, 1, 2, 0, 1, 0};
+// fp32: K tiles whose products one chain of sums takes (256 k).
+constexpr int kChunkTiles = 4;
+
+m2rnn::GemmParams gemm_params(long long M, int N, long long K, size_t e, bool f32, int* status) {
+  m2rnn::GemmParams p{};
+  p.M = M;
+  p.N = N;
+  p.kt = static_cast<int>((K * static_cast<long long>(e) + 127) / 128);
+  p.kc = f32 ? kChunkTiles : p.kt;
+  p.nseg = f32 ? kPairs : 1;
+  for (int i = 0; f32 && i < kPairs; ++i) {
+    p.az[i] = kPairA[i];
+    p.bz[i] = kPairB[i];
+  }
+  p.nbatch = 1;
+  p.status = status;
+  p.limit_ns = m2rnn::host_wait_limit_ns();
+  return p;
+}
+
+int run_gemm(m2rnn::GemmParams& p, const m2rnn::GemmKind& k, int sms, cudaStream_t st) {
+  const bool pair = k.epi == m2rnn::EPI_GLU || k.epi == m2rnn::EPI_DGLU || k.epi == m2rnn::EPI_GLU8;
+  const int cols = pair ? k.bn / 2 : k.bn;
+  p.mt = static_cast<int>((p.M + 127) / 128);
+  p.nt = (p.N + cols - 1) / cols;
+  return status_from_cuda(m2rnn::launch_gemm(p, k, sms, st));
+}
+
+// Hands out pieces of the workspace.
+struct Pieces {
+  char* at;
+  __nv_bfloat16* take(size_t elems) {
+    __nv_bfloat16* r = reinterpret_cast<__nv_bfloat16*>(at);
+    at += align256(elems * 2);
+    return r;
+  }
+};
+size_t terms_bytes(const m2rnn_glu_shape* s) {  // of x, wg and wu
+  const size_t x = static_cast<size_t>(s->M) * s->D, w = static_cast<size_t>(s->F) * s->D;
+  return s->in_dtype == M2RNN_F32 ? align256(6 * x) + 2 * align256(6 * w) : 0;
+}
+size_t dgu_bytes(const m2rnn_glu_shape* s) {  // the gradients of g and u
+  return align256(static_cast<size_t>(s->M) * s->F * (s->in_dtype == M2RNN_F32 ? 12 : 4));
+}
+
+// What the products read: the caller's bf16 matrices, or their terms.
+struct Operands {
+  const void *x, *wg, *wu;
+  long long x_row;
+  int terms;
+};
+int make_operands(const m2rnn_glu_shape* s, const void* x, long long x_row, const void* wg, const void* wu,
+                  Pieces* ws, int* status, cudaStream_t st, Operands* o) {
+  if (s->in_dtype == M2RNN_BF16) {
+    *o = {x, wg, wu, x_row, 1};
+    return M2RNN_OK;
+  }
+  m2rnn::SplitParams q{};
+  const void* src[3] = {x, wg, wu};
+  for (int i = 0; i < 3; ++i) {
+    q.src[i] = static_cast<const float*>(src[i]);
+    q.row[i] = i == 0 ? x_row : s->D;
+    q.M[i] = i == 0 ? s->M : s->F;
+    q.dst[i] = ws->take(static_cast<size_t>(3 * q.M[i]) * s->D);
+  }
+  q.D = s->D;
+  q.n = 3;
+  q.status = status;
+  *o = {q.dst[0], q.dst[1], q.dst[2], s->D, 3};
+  return status_from_cuda(m2rnn::launch_split(q, st));
+}
+
+// g and u of every token (EPI_GLU: h; EPI_DGLU: their gradients).
+int run_pair(const m2rnn_glu_shape* s, const Operands& o, int epi, const void* dh, void* out, int* status, int sms,
+             cudaStream_t st) {
+  const bool f32 = o.terms == 3;
+  m2rnn::GemmParams p = gemm_params(s->M, s->F, s->D, 2, f32, status);
+  const int bn = m2rnn::gemm_bn(epi, f32, s->M, s->F, 1, sms);
+  const long long x_plane = static_cast<long long>(s->M) * s->D, w_plane = static_cast<long long>(s->F) * s->D;
+  if (!make_map(&p.a, o.x, 2, s->D, s->M, o.terms, o.x_row, f32 ? x_plane : o.x_row, 128) ||
+      !make_map(&p.b0, o.wg, 2, s->D, s->F, o.terms, s->D, f32 ? w_plane : s->D, bn / 2) ||
+      !make_map(&p.b1, o.wu, 2, s->D, s->F, o.terms, s->D, f32 ? w_plane : s->D, bn / 2))
+    return M2RNN_ERR_CUDA;
+  p.out[0] = out;
+  p.in = dh;
+  p.act = s->act;
+  return run_gemm(p, {epi, false, f32, false, false, bn}, sms, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+int m2rnn_add_norm_fwd(const m2rnn_norm_shape* s, const void* x, long long x_row, const void* res,
+                       long long res_row, const void* w, float eps, void* r, void* y, void* stream) {
+  return add_norm(s, x, x_row, res, res_row, w, eps, r, y, nullptr, nullptr, false, stream);
+}
+
+int m2rnn_add_norm_q8(const m2rnn_norm_shape* s, const void* x, long long x_row, const void* res,
+                      long long res_row, const void* w, float eps, void* r, void* q, float* scale, void* stream) {
+  return add_norm(s, x, x_row, res, res_row, w, eps, r, nullptr, q, scale, true, stream);
+}
+
+size_t m2rnn_add_norm_bwd_workspace_size(const m2rnn_norm_shape* s) {
+  if (check_norm(s, kNormMostD) != M2RNN_OK || s->M == 0) return 0;
+  return align256(static_cast<size_t>(m2rnn::add_norm_bwd_parts(s)) * s->D * sizeof(float));
+}
+
+int m2rnn_add_norm_bwd(const m2rnn_norm_shape* s, const void* r, long long r_row, const void* w, float eps,
+                       const void* dy, const void* dr, void* dx, float* dw, void* workspace, size_t ws_bytes,
+                       void* stream) {
+  int rc = check_norm(s, kNormMostD);
+  if (rc != M2RNN_OK) return rc;
+  if (!(eps >= 0.f)) return M2RNN_ERR_INVALID_ARG;
+  const size_t e = esize(s->in_dtype);
+  if ((rc = check_row(r_row, e, s->M, 0)) != M2RNN_OK) return rc;
+  const size_t n = static_cast<size_t>(s->M) * s->D * e, db = static_cast<size_t>(s->D) * 4;
+  const size_t rb = rows_bytes(s->M, r_row, s->D, e), wb = static_cast<size_t>(s->D) * e;
+  if (spans_overlap(r, rb, dx, n) || spans_overlap(w, wb, dx, n) || (dx != dy && spans_overlap(dy, n, dx, n)) ||
+      (dx != dr && spans_overlap(dr, n, dx, n)) || spans_overlap(dw, db, dx, n) || spans_overlap(dw, db, r, rb) ||
+      spans_overlap(dw, db, dy, n) || spans_overlap(dw, db, dr, n) || spans_overlap(dw, db, w, wb))
+    return M2RNN_ERR_INVALID_ARG;
+  int dev, sms, *status;
+  if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const void* opt[] = {w, dr, dw};
+  if ((rc = check(opt, dev, false)) != M2RNN_OK) return rc;
+  if (s->M == 0) return dw == nullptr ? M2RNN_OK : status_from_cuda(cudaMemsetAsync(dw, 0, db, st));
+  const void* req[] = {r, dy, dx};
+  if ((rc = check(req, dev, true)) != M2RNN_OK) return rc;
+  if (dw != nullptr) {
+    if (workspace == nullptr || ws_bytes < m2rnn_add_norm_bwd_workspace_size(s)) return M2RNN_ERR_WORKSPACE;
+    if ((rc = host_check_ptr(workspace, dev, true)) != M2RNN_OK) return rc;
+  }
+  m2rnn::Norm2Params p{};
+  p.x = r;
+  p.x_row = r_row;
+  p.w = w;
+  p.dy = dy;
+  p.dr = dr;
+  p.dx = dx;
+  p.dw = dw;
+  p.part = dw == nullptr ? nullptr : static_cast<float*>(workspace);
+  p.nparts = m2rnn::add_norm_bwd_parts(s);
+  p.M = s->M;
+  p.D = s->D;
+  p.eps = eps;
+  p.status = status;
+  return status_from_cuda(m2rnn::launch_add_norm_bwd(p, s->in_dtype == M2RNN_F32, st));
+}
+
+int m2rnn_quant_rows(const m2rnn_norm_shape* s, const void* x, long long x_row, void* q, float* scale,
+                     void* stream) {
+  int rc = check_norm(s, kMostD);
+  if (rc != M2RNN_OK) return rc;
+  const size_t e = esize(s->in_dtype);
+  if ((rc = check_row(x_row, e, s->M, 0)) != M2RNN_OK) return rc;
+  const size_t xb = rows_bytes(s->M, x_row, s->D, e), qb = static_cast<size_t>(s->M) * s->D;
+  const size_t sb = static_cast<size_t>(s->M) * 4;
+  if (spans_overlap(x, xb, q, qb) || spans_overlap(x, xb, scale, sb) || spans_overlap(q, qb, scale, sb))
+    return M2RNN_ERR_INVALID_ARG;
+  int dev, sms, *status;
+  if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
+  if (s->M == 0) return M2RNN_OK;
+  const void* req[] = {x, q, scale};
+  if ((rc = check(req, dev, true)) != M2RNN_OK) return rc;
+  m2rnn::Norm2Params p{};
+  p.x = x;
+  p.x_row = x_row;
+  p.q = static_cast<uint8_t*>(q);
+  p.scale = scale;
+  p.M = s->M;
+  p.D = s->D;
+  p.status = status;
+  return status_from_cuda(
+      m2rnn::launch_quant_rows(p, s->in_dtype == M2RNN_F32, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t m2rnn_glu_fwd_workspace_size(const m2rnn_glu_shape* s) {
+  if (check_glu(s, false) != M2RNN_OK || s->M <= m2rnn::kFewMost) return 0;
+  return terms_bytes(s);
+}
+
+int m2rnn_glu_fwd(const m2rnn_glu_shape* s, const void* x, long long x_row, const void* wg, const void* wu, void* h,
+                  void* workspace, size_t ws_bytes, void* stream) {
+  int rc = check_glu(s, false);
+  if (rc != M2RNN_OK) return rc;
+  const size_t e = esize(s->in_dtype);
+  if ((rc = check_row(x_row, e, s->M, s->D)) != M2RNN_OK) return rc;
+  const size_t hb = static_cast<size_t>(s->M) * s->F * e, wb = static_cast<size_t>(s->F) * s->D * e;
+  if (spans_overlap(x, rows_bytes(s->M, x_row, s->D, e), h, hb) || spans_overlap(wg, wb, h, hb) ||
+      spans_overlap(wu, wb, h, hb))
+    return M2RNN_ERR_INVALID_ARG;
+  int dev, sms, *status;
+  if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
+  if (s->M == 0) return M2RNN_OK;
+  const void* req[] = {x, wg, wu, h};
+  if ((rc = check(req, dev, true)) != M2RNN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s->M <= m2rnn::kFewMost) {
+    m2rnn::FewParams p{};
+    p.x = x;
+    p.x_row = x_row;
+    p.w0 = wg;
+    p.w1 = wu;
+    p.out = h;
+    p.M = static_cast<int>(s->M);
+    p.D = s->D;
+    p.F = s->F;
+    p.act = s->act;
+    p.status = status;
+    return status_from_cuda(m2rnn::launch_few(p, m2rnn::EPI_GLU, false, s->in_dtype == M2RNN_F32, st));
+  }
+  const size_t need = m2rnn_glu_fwd_workspace_size(s);
+  if (need > 0) {
+    if (workspace == nullptr || ws_bytes < need) return M2RNN_ERR_WORKSPACE;
+    if ((rc = host_check_ptr(workspace, dev, true)) != M2RNN_OK) return rc;
+  }
+  Pieces ws{static_cast<char*>(workspace)};
+  Operands o;
+  if ((rc = make_operands(s, x, x_row, wg, wu, &ws, status, st, &o)) != M2RNN_OK) return rc;
+  return run_pair(s, o, m2rnn::EPI_GLU, nullptr, h, status, sms, st);
+}
+
+size_t m2rnn_glu_bwd_workspace_size(const m2rnn_glu_shape* s) {
+  if (check_glu(s, false) != M2RNN_OK || s->M == 0) return 0;
+  return terms_bytes(s) + dgu_bytes(s);
+}
+
+int m2rnn_glu_bwd(const m2rnn_glu_shape* s, const void* x, long long x_row, const void* wg, const void* wu,
+                  const void* dh, void* dx, void* dwg, void* dwu, void* workspace, size_t ws_bytes, void* stream) {
+  int rc = check_glu(s, false);
+  if (rc != M2RNN_OK) return rc;
+  const size_t e = esize(s->in_dtype);
+  if ((rc = check_row(x_row, e, s->M, s->D)) != M2RNN_OK) return rc;
+  if ((dwg == nullptr) != (dwu == nullptr)) return M2RNN_ERR_INVALID_ARG;
+  const size_t xb = static_cast<size_t>(s->M) * s->D * e, wb = static_cast<size_t>(s->F) * s->D * e;
+  const size_t hb = static_cast<size_t>(s->M) * s->F * e, xr = rows_bytes(s->M, x_row, s->D, e);
+  const struct { const void* p; size_t bytes; } outs[] = {{dx, xb}, {dwg, wb}, {dwu, wb}},
+                                                ins[] = {{x, xr}, {wg, wb}, {wu, wb}, {dh, hb}};
+  for (int i = 0; i < 3; ++i) {
+    for (const auto& in : ins)
+      if (spans_overlap(in.p, in.bytes, outs[i].p, outs[i].bytes)) return M2RNN_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (spans_overlap(outs[j].p, outs[j].bytes, outs[i].p, outs[i].bytes)) return M2RNN_ERR_INVALID_ARG;
+  }
+  int dev, sms, *status;
+  if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
+  const void* opt[] = {dx, dwg, dwu};
+  if ((rc = check(opt, dev, false)) != M2RNN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dx == nullptr && dwg == nullptr) return M2RNN_OK;
+  if (s->M == 0) {
+    if (dwg == nullptr) return M2RNN_OK;
+    const cudaError_t a = cudaMemsetAsync(dwg, 0, wb, st);
+    return status_from_cuda(a != cudaSuccess ? a : cudaMemsetAsync(dwu, 0, wb, st));
+  }
+  const void* req[] = {x, wg, wu, dh};
+  if ((rc = check(req, dev, true)) != M2RNN_OK) return rc;
+  if (workspace == nullptr || ws_bytes < m2rnn_glu_bwd_workspace_size(s)) return M2RNN_ERR_WORKSPACE;
+  if ((rc = host_check_ptr(workspace, dev, true)) != M2RNN_OK) return rc;
+  Pieces ws{static_cast<char*>(workspace)};
+  Operands o;
+  if ((rc = make_operands(s, x, x_row, wg, wu, &ws, status, st, &o)) != M2RNN_OK) return rc;
+  const bool f32 = o.terms == 3;
+  const long long hp = s->M * s->F;
+  __nv_bfloat16* dgu = ws.take(static_cast<size_t>(2 * o.terms) * hp);
+  if ((rc = run_pair(s, o, m2rnn::EPI_DGLU, dh, dgu, status, sms, st)) != M2RNN_OK) return rc;
+  const long long xp = s->M * s->D, wp = static_cast<long long>(s->F) * s->D;
+  if (dx != nullptr) {  // dg wg + du wu
+    m2rnn::GemmParams p = gemm_params(s->M, s->D, s->F, 2, f32, status);
+    const int bn = m2rnn::gemm_bn(m2rnn::EPI_STORE, f32, s->M, s->D, 1, sms);
+    // of both products, the small segments before the leading ones
+    p.nseg = 0;
+    for (int i = 0; i < (f32 ? kPairs : 1); ++i)
+      for (int which = 0; which < 2; ++which, ++p.nseg) {
+        p.az[p.nseg] = static_cast<int8_t>((f32 ? kPairA[i] : 0) + which * o.terms);
+        p.bi[p.nseg] = static_cast<int8_t>(which);
+        p.bz[p.nseg] = f32 ? kPairB[i] : 0;
+      }
+    if (!make_map(&p.a, dgu, 2, s->F, s->M, 2 * o.terms, s->F, hp, 128) ||
+        !make_map(&p.b0, o.wg, 2, s->D, s->F, o.terms, s->D, f32 ? wp : s->D, 64) ||
+        !make_map(&p.b1, o.wu, 2, s->D, s->F, o.terms, s->D, f32 ? wp : s->D, 64))
+      return M2RNN_ERR_CUDA;
+    p.out[0] = dx;
+    if ((rc = run_gemm(p, {m2rnn::EPI_STORE, false, f32, false, true, bn}, sms, st)) != M2RNN_OK) return rc;
+  }
+  if (dwg != nullptr) {  // dg^T x and du^T x, which share x
+    m2rnn::GemmParams p = gemm_params(s->F, s->D, s->M, 2, f32, status);
+    const int bn = m2rnn::gemm_bn(m2rnn::EPI_STORE, f32, s->F, s->D, 2, sms);
+    p.nbatch = 2;
+    p.az_step = o.terms;
+    if (!make_map(&p.a, dgu, 2, s->F, s->M, 2 * o.terms, s->F, hp, 64) ||
+        !make_map(&p.b0, o.x, 2, s->D, s->M, o.terms, o.x_row, f32 ? xp : o.x_row, 64))
+      return M2RNN_ERR_CUDA;
+    p.b1 = p.b0;
+    p.out[0] = dwg;
+    p.out[1] = dwu;
+    if ((rc = run_gemm(p, {m2rnn::EPI_STORE, false, f32, true, true, bn}, sms, st)) != M2RNN_OK) return rc;
+  }
+  return M2RNN_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Both 8-bit products: the arguments, then few tokens or tiles.
+int product_q8(const m2rnn_glu_shape* s, const void* x, long long x_row, const float* xs, const void* w0,
+               const float* s0, const void* w1, const float* s1, const void* res, long long res_row, void* out,
+               bool pair, void* stream) {
+  int rc = check_glu(s, true);
+  if (rc != M2RNN_OK) return rc;
+  if ((rc = check_row(x_row, 1, s->M, s->D)) != M2RNN_OK) return rc;
+  if (res != nullptr && (rc = check_row(res_row, 2, s->M, 0)) != M2RNN_OK) return rc;
+  const size_t ob = static_cast<size_t>(s->M) * s->F * 2, wb = static_cast<size_t>(s->F) * s->D;
+  const size_t fb = static_cast<size_t>(s->F) * 4;
+  const bool in_place = res == out && res_row == s->F;
+  if (spans_overlap(x, rows_bytes(s->M, x_row, s->D, 1), out, ob) || spans_overlap(w0, wb, out, ob) ||
+      spans_overlap(w1, wb, out, ob) || spans_overlap(xs, static_cast<size_t>(s->M) * 4, out, ob) ||
+      spans_overlap(s0, fb, out, ob) || spans_overlap(s1, fb, out, ob) ||
+      (!in_place && spans_overlap(res, rows_bytes(s->M, res_row, s->F, 2), out, ob)))
+    return M2RNN_ERR_INVALID_ARG;
+  int dev, sms, *status;
+  if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
+  if (s->M == 0) return M2RNN_OK;
+  const void* req[] = {x, xs, w0, s0, out};
+  if ((rc = check(req, dev, true)) != M2RNN_OK) return rc;
+  const void* more[] = {w1, s1};
+  if ((rc = check(more, dev, pair)) != M2RNN_OK) return rc;
+  if ((rc = host_check_ptr(res, dev, false)) != M2RNN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int epi = pair ? m2rnn::EPI_GLU8 : m2rnn::EPI_LIN8;
+  if (s->M <= m2rnn::kFewMost) {
+    m2rnn::FewParams p{};
+    p.x = x;
+    p.x_row = x_row;
+    p.w0 = w0;
+    p.w1 = w1;
+    p.res = res;
+    p.res_row = res_row;
+    p.sa = xs;
+    p.sb0 = s0;
+    p.sb1 = s1;
+    p.out = out;
+    p.M = static_cast<int>(s->M);
+    p.D = s->D;
+    p.F = s->F;
+    p.act = s->act;
+    p.status = status;
+    return status_from_cuda(m2rnn::launch_few(p, epi, true, false, st));
+  }
+  m2rnn::GemmParams p = gemm_params(s->M, s->F, s->D, 1, false, status);
+  const int bn = m2rnn::gemm_bn(epi, false, s->M, s->F, 1, sms);
+  if (!make_map(&p.a, x, 1, s->D, s->M, 1, x_row, x_row, 128) ||
+      !make_map(&p.b0, w0, 1, s->D, s->F, 1, s->D, s->D, bn / 2))
+    return M2RNN_ERR_CUDA;
+  if (!pair)
+    p.b1 = p.b0;
+  else if (!make_map(&p.b1, w1, 1, s->D, s->F, 1, s->D, s->D, bn / 2))
+    return M2RNN_ERR_CUDA;
+  p.out[0] = out;
+  p.in = res;
+  p.in_row = res_row;
+  p.sa = xs;
+  p.sb0 = s0;
+  p.sb1 = s1;
+  p.act = s->act;
+  return run_gemm(p, {epi, true, false, false, false, bn}, sms, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+int m2rnn_glu_q8(const m2rnn_glu_shape* s, const void* x, long long x_row, const float* xs, const void* wg,
+                 const float* wgs, const void* wu, const float* wus, void* h, void* stream) {
+  return product_q8(s, x, x_row, xs, wg, wgs, wu, wus, nullptr, 0, h, true, stream);
+}
+
+int m2rnn_linear_q8(const m2rnn_glu_shape* s, const void* x, long long x_row, const float* xs, const void* w,
+                    const float* ws, const void* res, long long res_row, void* y, void* stream) {
+  return product_q8(s, x, x_row, xs, w, ws, nullptr, nullptr, res, res_row, y, false, stream);
+}
+
+}  // extern "C"

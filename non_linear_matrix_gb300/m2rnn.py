@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libm2rnn.so (include/m2rnn.h and m2rnn_block.h).
+"""Thin ctypes binding of libm2rnn.so (include/m2rnn.h, m2rnn_block.h and
+m2rnn_ffn.h).
 
 Argument marshalling only: it checks tensor placement and dtypes, allocates
 output tensors with torch, passes raw device pointers and the current CUDA
@@ -34,7 +35,7 @@ STATUS = {
 _lock = threading.Lock()
 _lib = None
 
-_VP = ctypes.c_void_p
+_VP, _LL = ctypes.c_void_p, ctypes.c_longlong
 _EXPORTS = {
     "m2rnn_version": (ctypes.c_int, []),
     "m2rnn_checked": (ctypes.c_int, []),
@@ -68,6 +69,18 @@ _EXPORTS = {
     "m2rnn_scan_bwd_workspace_size": (ctypes.c_size_t, [_VP, ctypes.c_int]),
     "m2rnn_scan_bwd": (ctypes.c_int, [_VP] * 22 + [ctypes.c_size_t, _VP]),
     "m2rnn_scan_step": (ctypes.c_int, [_VP] * 13),
+    "m2rnn_add_norm_fwd": (ctypes.c_int, [_VP, _VP, _LL, _VP, _LL, _VP, ctypes.c_float] + [_VP] * 3),
+    "m2rnn_add_norm_q8": (ctypes.c_int, [_VP, _VP, _LL, _VP, _LL, _VP, ctypes.c_float] + [_VP] * 4),
+    "m2rnn_add_norm_bwd_workspace_size": (ctypes.c_size_t, [_VP]),
+    "m2rnn_add_norm_bwd": (ctypes.c_int, [_VP, _VP, _LL, _VP, ctypes.c_float] + [_VP] * 5 +
+                           [ctypes.c_size_t, _VP]),
+    "m2rnn_quant_rows": (ctypes.c_int, [_VP, _VP, _LL, _VP, _VP, _VP]),
+    "m2rnn_glu_fwd_workspace_size": (ctypes.c_size_t, [_VP]),
+    "m2rnn_glu_fwd": (ctypes.c_int, [_VP, _VP, _LL] + [_VP] * 4 + [ctypes.c_size_t, _VP]),
+    "m2rnn_glu_bwd_workspace_size": (ctypes.c_size_t, [_VP]),
+    "m2rnn_glu_bwd": (ctypes.c_int, [_VP, _VP, _LL] + [_VP] * 7 + [ctypes.c_size_t, _VP]),
+    "m2rnn_glu_q8": (ctypes.c_int, [_VP, _VP, _LL] + [_VP] * 7),
+    "m2rnn_linear_q8": (ctypes.c_int, [_VP, _VP, _LL] + [_VP] * 4 + [_LL, _VP, _VP]),
 }
 
 
@@ -859,6 +872,247 @@ def scan_step(q, k, v, a, alpha, beta, H, w_r=None, *, H_out=None, y=None, strea
                                _addr(y), _stream_of(stream, q))
     _check(rc, "m2rnn_scan_step")
     return y, H_out
+
+
+# ---- the feed-forward half of a layer (include/m2rnn_ffn.h) ------------------
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_longlong), ("D", ctypes.c_int), ("in_dtype", ctypes.c_int)]
+
+
+class GluShape(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_longlong), ("D", ctypes.c_int), ("F", ctypes.c_int),
+                ("in_dtype", ctypes.c_int), ("act", ctypes.c_int)]
+
+
+_ACTS = {"silu": 0, "gelu": 1}
+
+
+def _act(act: str) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, not {act!r}")
+    return _ACTS[act]
+
+
+def _token_rows(name: str, t):
+    """Number of rows of t [..., D] and the distance between them: its features packed,
+    its tokens evenly spaced."""
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have a feature dimension")
+    D = t.shape[-1]
+    if t.is_contiguous():
+        return t.numel() // D if D else 0, D
+    if not t.is_cuda:
+        raise ValueError("tensors passed to libm2rnn must be CUDA tensors")
+    shape, st = t.shape, t.stride()
+    if 0 in shape:
+        return 0, D
+    if st[-1] != 1 and D != 1:
+        raise ValueError(f"{name}'s features must be packed")
+    row, span, M = None, None, 1
+    for i in range(len(shape) - 2, -1, -1):  # from the innermost token dimension out
+        M *= shape[i]
+        if shape[i] == 1:
+            continue
+        if row is None:
+            row = st[i]
+        elif st[i] != span:
+            raise ValueError(f"{name}'s rows must be evenly spaced")
+        span = st[i] * shape[i]
+    return M, D if row is None else row
+
+
+def _bf16_or_f32(name: str, t):
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, not {t.dtype}")
+
+
+def _norm_args(x, res, w):
+    _bf16_or_f32("x", x)
+    M, x_row = _token_rows("x", x)
+    D, res_row = x.shape[-1], 0
+    if res is not None:
+        _expect("res", res, x.shape, x.dtype)
+        res_row = _token_rows("res", res)[1]
+    _expect_all(x.dtype, ("w", w, (D,)))
+    return NormShape(M, D, _dtype_code(x)), x_row, res_row
+
+
+@_on_stream
+def add_norm_fwd(x, res=None, w=None, eps: float = 1e-6, *, out=None, stream=None):
+    """r = x + res, stored in x's dtype, and y = w (.) r (mean r^2 + eps)^(-1/2) over the
+    features of what is stored.  Returns (y, r); r is None without ``res``.
+
+    x, res [..., D] (rows may be evenly spaced slices); w [D] or None (1); one dtype (bf16
+    or f32).  ``out`` may supply y and r; r may be ``res`` or x itself (in place)."""
+    s, x_row, res_row = _norm_args(x, res, w)
+    y, r = _given(out, "y", "r")
+    y = _out(y, x.shape, x.dtype, x.device, "y")
+    if res is None:
+        if r is not None:
+            raise ValueError("r goes with res")
+    else:
+        r = _out(r, x.shape, x.dtype, x.device, "r")
+    rc = lib().m2rnn_add_norm_fwd(ctypes.byref(s), _at(x), x_row, _at(res), res_row, _addr(w), eps,
+                                  _addr(r), _addr(y), _stream_of(stream, x))
+    _check(rc, "m2rnn_add_norm_fwd")
+    return y, r
+
+
+@_on_stream
+def add_norm_q8(x, res=None, w=None, eps: float = 1e-6, *, out=None, stream=None):
+    """``add_norm_fwd`` with y in 8 bits: returns (q [..., D] float8_e4m3fn, scale [...]
+    fp32, r), y about q * scale.  ``out`` may supply q, scale and r."""
+    s, x_row, res_row = _norm_args(x, res, w)
+    q, scale, r = _given(out, "q", "scale", "r")
+    q = _out(q, x.shape, torch.float8_e4m3fn, x.device, "q")
+    scale = _out(scale, x.shape[:-1], torch.float32, x.device, "scale")
+    if res is None:
+        if r is not None:
+            raise ValueError("r goes with res")
+    else:
+        r = _out(r, x.shape, x.dtype, x.device, "r")
+    rc = lib().m2rnn_add_norm_q8(ctypes.byref(s), _at(x), x_row, _at(res), res_row, _addr(w), eps,
+                                 _addr(r), _addr(q), _addr(scale), _stream_of(stream, x))
+    _check(rc, "m2rnn_add_norm_q8")
+    return q, scale, r
+
+
+@_on_stream
+def add_norm_bwd(r, dy, w=None, dr=None, eps: float = 1e-6, *, want_dw: bool = True, workspace=None,
+                 out=None, stream=None):
+    """Gradient of ``add_norm_fwd`` at r [..., D], its stored sum (or x, without
+    ``res``): dict(dx, dw).  dy is dL/dy and dr dL/dr past the norm (None = 0), of r's
+    dtype; dx (r's dtype) is the gradient of x and of res alike; dw [D] is fp32
+    (None without a weight or with want_dw=False).  dx may be dr or dy itself."""
+    _bf16_or_f32("r", r)
+    M, row = _token_rows("r", r)
+    D, dev = r.shape[-1], r.device
+    _expect_all(r.dtype, ("w", w, (D,)), ("dy", dy, r.shape), ("dr", dr, r.shape))
+    s = NormShape(M, D, _dtype_code(r))
+    dx, dw = _given(out, "dx", "dw")
+    dx = _out(dx, r.shape, r.dtype, dev, "dx")
+    dw = _out(dw, (D,), torch.float32, dev, "dw") if w is not None and want_dw else None
+    need = int(lib().m2rnn_add_norm_bwd_workspace_size(ctypes.byref(s))) if dw is not None else 0
+    ws = _workspace(workspace, need, dev)
+    rc = lib().m2rnn_add_norm_bwd(ctypes.byref(s), _at(r), row, _addr(w), eps, _addr(dy), _addr(dr),
+                                  _addr(dx), _addr(dw), _addr(ws), _nbytes(ws), _stream_of(stream, r))
+    _check(rc, "m2rnn_add_norm_bwd")
+    return {"dx": dx, "dw": dw}
+
+
+@_on_stream
+def quant_rows(x, *, out=None, stream=None):
+    """x [..., D] (bf16 or f32; rows may be evenly spaced slices) in 8 bits with a scale per
+    row: (q float8_e4m3fn, scale [...] fp32), scale = max|row| / 448, q the nearest
+    code of row / scale.  ``out`` may supply q and scale."""
+    _bf16_or_f32("x", x)
+    M, row = _token_rows("x", x)
+    s = NormShape(M, x.shape[-1], _dtype_code(x))
+    q, scale = _given(out, "q", "scale")
+    q = _out(q, x.shape, torch.float8_e4m3fn, x.device, "q")
+    scale = _out(scale, x.shape[:-1], torch.float32, x.device, "scale")
+    rc = lib().m2rnn_quant_rows(ctypes.byref(s), _at(x), row, _addr(q), _addr(scale),
+                                _stream_of(stream, x))
+    _check(rc, "m2rnn_quant_rows")
+    return q, scale
+
+
+def _glu_args(x, wg, wu, act):
+    _bf16_or_f32("x", x)
+    M, row = _token_rows("x", x)
+    if wg.dim() != 2:
+        raise ValueError("wg must be [F,D]")
+    F, D = wg.shape[0], x.shape[-1]
+    _expect_all(x.dtype, ("wg", wg, (F, D)), ("wu", wu, (F, D)))
+    return GluShape(M, D, F, _dtype_code(x), _act(act)), row
+
+
+@_on_stream
+def glu_fwd(x, wg, wu, *, act: str = "silu", workspace=None, out=None, stream=None):
+    """Gated feed-forward products h = act(x wg^T) (.) (x wu^T), [..., F].
+
+    x [..., D] (rows may be evenly spaced slices); wg, wu [F,D]; one dtype (bf16 or f32);
+    act "silu" or "gelu" (the tanh form).  ``out`` may supply h."""
+    s, row = _glu_args(x, wg, wu, act)
+    h = _out(_given(out, "h")[0], (*x.shape[:-1], s.F), x.dtype, x.device, "h")
+    need = int(lib().m2rnn_glu_fwd_workspace_size(ctypes.byref(s)))
+    ws = _workspace(workspace, need, x.device) if need or workspace is not None else None
+    rc = lib().m2rnn_glu_fwd(ctypes.byref(s), _at(x), row, _addr(wg), _addr(wu), _addr(h),
+                             _addr(ws), ctypes.c_size_t(0) if ws is None else _nbytes(ws),
+                             _stream_of(stream, x))
+    _check(rc, "m2rnn_glu_fwd")
+    return h
+
+
+@_on_stream
+def glu_bwd(x, wg, wu, dh, *, act: str = "silu", want_dx: bool = True, want_dw: bool = True,
+            workspace=None, out=None, stream=None):
+    """Gradient of ``glu_fwd``: dict(dx, dwg, dwu), all of x's dtype, for dL/dh = dh
+    [..., F]; None for what is not wanted.  The products of the forward pass are formed
+    again: nothing is kept between the two."""
+    s, row = _glu_args(x, wg, wu, act)
+    _expect("dh", dh, (*x.shape[:-1], s.F), x.dtype)
+    dx, dwg, dwu = _given(out, "dx", "dwg", "dwu")
+    dev = x.device
+    g = {"dx": _out(dx, x.shape, x.dtype, dev, "dx") if want_dx else None,
+         "dwg": _out(dwg, wg.shape, x.dtype, dev, "dwg") if want_dw else None,
+         "dwu": _out(dwu, wu.shape, x.dtype, dev, "dwu") if want_dw else None}
+    ws = _workspace(workspace, int(lib().m2rnn_glu_bwd_workspace_size(ctypes.byref(s))), dev)
+    rc = lib().m2rnn_glu_bwd(ctypes.byref(s), _at(x), row, _addr(wg), _addr(wu), _addr(dh),
+                             _addr(g["dx"]), _addr(g["dwg"]), _addr(g["dwu"]), _addr(ws), _nbytes(ws),
+                             _stream_of(stream, x))
+    _check(rc, "m2rnn_glu_bwd")
+    return g
+
+
+def _q8_args(x, xs, weights):
+    """Rows of e4m3 x [..., D] and the width of weights [(w [F,D], scales [F]), ...]."""
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    if weights[0][0].dim() != 2:
+        raise ValueError("weights must be [F,D]")
+    F, D = weights[0][0].shape[0], x.shape[-1]
+    _expect("x", x, x.shape, e4m3)
+    _expect("xs", xs, x.shape[:-1], f32)
+    for w, ws in weights:
+        _expect("w", w, (F, D), e4m3)
+        _expect("ws", ws, (F,), f32)
+    M, row = _token_rows("x", x)
+    return M, row, D, F
+
+
+@_on_stream
+def glu_q8(x, xs, wg, wgs, wu, wus, *, act: str = "silu", out=None, stream=None):
+    """``glu_fwd`` on 8-bit operands: x [..., D] e4m3 with scales xs [...] (from
+    ``add_norm_q8`` or ``quant_rows``), wg, wu [F,D] e4m3 with scales [F] (``quant_rows``
+    of the weights).  Returns h [..., F] in bf16; ``out`` may supply it."""
+    M, row, D, F = _q8_args(x, xs, ((wg, wgs), (wu, wus)))
+    s = GluShape(M, D, F, M2RNN_BF16, _act(act))
+    h = _out(_given(out, "h")[0], (*x.shape[:-1], F), torch.bfloat16, x.device, "h")
+    rc = lib().m2rnn_glu_q8(ctypes.byref(s), _at(x), row, _addr(xs), _addr(wg), _addr(wgs), _addr(wu),
+                            _addr(wus), _addr(h), _stream_of(stream, x))
+    _check(rc, "m2rnn_glu_q8")
+    return h
+
+
+@_on_stream
+def linear_q8(x, xs, w, ws, res=None, *, out=None, stream=None):
+    """y = x w^T with both operands' scales, plus ``res``: x [..., D] e4m3 with scales
+    xs [...], w [F,D] e4m3 with scales ws [F], res [..., F] bf16 (rows may be evenly
+    spaced slices) or None.  Returns y [..., F] in bf16; ``out`` may supply y, also res
+    itself (in place)."""
+    M, row, D, F = _q8_args(x, xs, ((w, ws),))
+    res_row = 0
+    if res is not None:
+        _expect("res", res, (*x.shape[:-1], F), torch.bfloat16)
+        res_row = _token_rows("res", res)[1]
+    s = GluShape(M, D, F, M2RNN_BF16, 0)
+    y = _out(_given(out, "y")[0], (*x.shape[:-1], F), torch.bfloat16, x.device, "y")
+    rc = lib().m2rnn_linear_q8(ctypes.byref(s), _at(x), row, _addr(xs), _addr(w), _addr(ws), _at(res),
+                               res_row, _addr(y), _stream_of(stream, x))
+    _check(rc, "m2rnn_linear_q8")
+    return y
 
 
 def device_status(clear: bool = True, stream=None):
