@@ -185,7 +185,8 @@ m2rnn::GemmParams gemm_params(long long M, int N, long long K, size_t e, bool f3
 int run_gemm(m2rnn::GemmParams& p, const m2rnn::GemmKind& k, int sms, cudaStream_t st) {
   const bool pair = k.epi == m2rnn::EPI_GLU || k.epi == m2rnn::EPI_DGLU || k.epi == m2rnn::EPI_GLU8;
   const int cols = pair ? k.bn / 2 : k.bn;
-  p.mt = static_cast<int>((p.M + 127) / 128);
+  const int rows = k.bn == 256 ? 256 : 128;  // (of a pair of CTAs, or of one)
+  p.mt = static_cast<int>((p.M + rows - 1) / rows);
   p.nt = (p.N + cols - 1) / cols;
   return status_from_cuda(m2rnn::launch_gemm(p, k, sms, st));
 }
@@ -517,7 +518,7 @@ int product_q8(const m2rnn_glu_shape* s, const void* x, long long x_row, const f
   m2rnn::GemmParams p = gemm_params(s->M, s->F, s->D, 1, false, status);
   const int bn = m2rnn::gemm_bn(epi, false, s->M, s->F, 1, sms);
   if (!make_map(&p.a, x, 1, s->D, s->M, 1, x_row, x_row, 128) ||
-      !make_map(&p.b0, w0, 1, s->D, s->F, 1, s->D, s->D, bn / 2))
+      !make_map(&p.b0, w0, 1, s->D, s->F, 1, s->D, s->D, pair ? bn / 2 : 128))
     return M2RNN_ERR_CUDA;
   if (!pair)
     p.b1 = p.b0;

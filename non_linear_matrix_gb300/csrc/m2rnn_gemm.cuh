@@ -1,6 +1,8 @@
 // m2rnn_gemm.cuh -- the product kernel of the feed-forward operators.
 //
-// out = sum over segments and K of A B^T, 128 rows x BN accumulator columns per tile.
+// out = sum over segments and K of A B^T.  A tile is 128 rows x BN accumulator columns of
+// one CTA, or 256 x BN of a pair of CTAs (CG = 2), each of which holds half of the rows of A
+// and of B, so that a byte of B in shared memory serves twice as many rows.
 // One persistent CTA per SM: a warp that issues the tensor-map copies into a ring of
 // K tiles (128 bytes of K each), a warp whose elected thread issues tcgen05.mma, and four
 // warps that turn finished accumulators into outputs.  Tensor memory holds two
@@ -22,15 +24,16 @@
 
 namespace m2rnn {
 
-template <int EPI_, bool E4M3_, bool F32_, bool A_MN_, bool B_MN_, int BN_>
+template <int EPI_, bool E4M3_, bool F32_, bool A_MN_, bool B_MN_, int BN_, int CG_>
 struct GemmCfg {
-  static constexpr int EPI = EPI_, BN = BN_;
+  static constexpr int EPI = EPI_, BN = BN_, CG = CG_;
+  static constexpr int BM = 128 * CG, BR = BN / CG;  // rows of a tile; B's rows in a CTA
   static constexpr bool E4M3 = E4M3_, F32 = F32_, A_MN = A_MN_, B_MN = B_MN_;
   static constexpr bool PAIR = EPI == EPI_GLU || EPI == EPI_DGLU || EPI == EPI_GLU8;
   static constexpr int OUT_N = PAIR ? BN / 2 : BN;  // output columns of a tile
   static constexpr int KT = E4M3 ? 128 : 64;        // elements of a K tile
-  static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN == 256 ? 4 : 6;
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = BR * 128, STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = 6;
   static constexpr int SMEM = STAGES * STAGE + 1024;
   static constexpr int TCOLS = 2 * BN;
   static constexpr int THREADS = 192;
@@ -59,29 +62,34 @@ __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
 }
 
 template <class C>
-__device__ __forceinline__ void issue_tile(const GemmParams& p, uint32_t dst, uint32_t bar, const TileAt& t, int seg,
-                                           int kt) {
+__device__ __forceinline__ void issue_tile(const GemmParams& p, uint32_t dst, uint32_t bar, const TileAt& t, int rank,
+                                           int seg, int kt) {
   const int k = kt * C::KT;
   const int az = p.az[seg] + t.batch * p.az_step, bz = p.bz[seg];
-  const int m = t.m * 128, n = t.n * C::OUT_N;
+  const int m = t.m * C::BM + rank * 128;
   if constexpr (C::A_MN) {
-    tc5::copy_box(dst, &p.a, m, k, az, bar);
-    tc5::copy_box(dst + 8192, &p.a, m + 64, k, az, bar);
+    tc5::copy_box<C::CG>(dst, &p.a, m, k, az, bar);
+    tc5::copy_box<C::CG>(dst + 8192, &p.a, m + 64, k, az, bar);
   } else {
-    tc5::copy_box(dst, &p.a, k, m, az, bar);
+    tc5::copy_box<C::CG>(dst, &p.a, k, m, az, bar);
   }
   const uint32_t b = dst + C::A_BYTES;
   if constexpr (C::PAIR) {
-    tc5::copy_box(b, &p.b0, k, n, bz, bar);
-    tc5::copy_box(b + C::B_BYTES / 2, &p.b1, k, n, bz, bar);
+    const int n = t.n * C::OUT_N;
+    if constexpr (C::CG == 2) {  // a weight to each CTA
+      tc5::copy_box<2>(b, rank ? &p.b1 : &p.b0, k, n, bz, bar);
+    } else {
+      tc5::copy_box<1>(b, &p.b0, k, n, bz, bar);
+      tc5::copy_box<1>(b + C::B_BYTES / 2, &p.b1, k, n, bz, bar);
+    }
   } else {
+    const int n = t.n * C::OUT_N + rank * C::BR;
     const CUtensorMap* map = p.bi[seg] ? &p.b1 : &p.b0;
     if constexpr (C::B_MN) {
 #pragma unroll
-      for (int i = 0; i < C::BN / 64; ++i) tc5::copy_box(b + 8192 * i, map, n + 64 * i, k, bz, bar);
+      for (int i = 0; i < C::BR / 64; ++i) tc5::copy_box<C::CG>(b + 8192 * i, map, n + 64 * i, k, bz, bar);
     } else {
-      tc5::copy_box(b, map, k, n, bz, bar);
-      tc5::copy_box(b + C::B_BYTES / 2, map, k, n + C::BN / 2, bz, bar);
+      tc5::copy_box<C::CG>(b, map, k, n, bz, bar);
     }
   }
 }
@@ -202,6 +210,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
   const uint32_t full = ptx::smem_addr(&bars[0]), empty = full + 8 * C::STAGES;
   const uint32_t tfull = empty + 8 * C::STAGES, tempty = tfull + 16, drain = tempty + 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = C::CG == 2 ? static_cast<int>(tc5::cta_rank()) : 0;
+  const int first = blockIdx.x / C::CG, stride = gridDim.x / C::CG;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       ptx::mbar_init(full + 8 * i, 1);
@@ -209,14 +219,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(tfull + 8 * i, 1);
-      ptx::mbar_init(tempty + 8 * i, 4);
+      ptx::mbar_init(tempty + 8 * i, 4 * C::CG);
     }
     ptx::mbar_init(drain, 1);
     ptx::mbar_init_fence();
   }
-  if (warp == 5) tc5::alloc(ptx::smem_addr(&tslot), C::TCOLS);
+  if (warp == 5) tc5::alloc<C::CG>(ptx::smem_addr(&tslot), C::TCOLS);
   tc5::fence_before();
   __syncthreads();
+  if constexpr (C::CG == 2) tc5::cluster_sync();
   tc5::fence_after();
   const uint32_t tm = tslot;
   let_next_begin();
@@ -228,9 +239,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
       tc5::prefetch_map(&p.a);
       tc5::prefetch_map(&p.b0);
       tc5::prefetch_map(&p.b1);
+      const uint32_t full0 = C::CG == 2 ? tc5::map_to(full, 0) : full;
       int it = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      for (int t = first; t < tiles && ok; t += stride) {
         const TileAt at = tile_at(p, t);
         for (int c = 0; c < nchunk && ok; ++c)
           for (int s = 0; s < p.nseg && ok; ++s)
@@ -240,28 +252,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
                 ok = false;
                 break;
               }
-              tc5::arrive_expect(full + 8 * st, C::STAGE);
-              issue_tile<C>(p, base + st * C::STAGE, full + 8 * st, at, s, k);
+              // (the pair's copies are counted in the first CTA, whose thread issues the products)
+              if (rank == 0) tc5::arrive_expect(full + 8 * st, C::CG * C::STAGE);
+              issue_tile<C>(p, base + st * C::STAGE, full0 + 8 * st, at, rank, s, k);
             }
       }
+      // The last products have been done, and have said so, before a CTA of a pair goes.
+      for (int i = max(0, it - C::STAGES); i < it && ok && C::CG == 2; ++i)
+        ok = ptx::mbar_wait(empty + 8 * (i % C::STAGES), (i / C::STAGES) & 1, p.limit_ns);
       if (!ok) {  // copies in flight land before the CTA goes
         gave_up(p.status, SITE_GEMM_COPY);
-        for (int i = max(0, it - C::STAGES); i < it; ++i)
+        for (int i = max(0, it - C::STAGES); i < it && rank == 0; ++i)
           ptx::mbar_wait(full + 8 * (i % C::STAGES), (i / C::STAGES) & 1, p.limit_ns);
       }
     }
     __syncwarp();
   } else if (warp == 5) {
-    if (tc5::elect_one()) {
-      constexpr uint32_t id = tc5::idesc(128, C::BN, C::E4M3, C::A_MN, C::B_MN);
+    if (rank == 0 && tc5::elect_one()) {
+      constexpr uint32_t id = tc5::idesc(C::BM, C::BN, C::E4M3, C::A_MN, C::B_MN);
       constexpr uint32_t a_step = C::A_MN ? 2048 : 32, b_step = C::B_MN ? 2048 : 32;
       int it = 0, acc = 0;
       bool ok = true;
       int site = SITE_GEMM_MMA;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x)
+      for (int t = first; t < tiles && ok; t += stride)
         for (int c = 0; c < nchunk && ok; ++c, ++acc) {
           const int ab = acc & 1;
-          if (!ptx::mbar_wait(tempty + 8 * ab, ((acc >> 1) & 1) ^ 1, p.limit_ns)) {
+          if (!tc5::wait_released<C::CG>(tempty + 8 * ab, ((acc >> 1) & 1) ^ 1, p.limit_ns)) {
             ok = false;
             break;
           }
@@ -278,28 +294,39 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
               const uint32_t sa = base + st * C::STAGE, sb = sa + C::A_BYTES;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                tc5::mma<C::E4M3>(tm + ab * C::BN, tc5::sdesc(sa + i * a_step, C::A_MN ? 8192 : 16, 1024),
+                tc5::mma<C::E4M3, C::CG>(tm + ab * C::BN, tc5::sdesc(sa + i * a_step, C::A_MN ? 8192 : 16, 1024),
                                   tc5::sdesc(sb + i * b_step, C::B_MN ? 8192 : 16, 1024), id, add);
                 add = true;
               }
-              tc5::commit(empty + 8 * st);
+              tc5::commit<C::CG>(empty + 8 * st);
             }
-          if (ok) tc5::commit(tfull + 8 * ab);
+          if (ok) tc5::commit<C::CG>(tfull + 8 * ab);
         }
       if (!ok) {
         gave_up(p.status, site);
-        tc5::commit(drain);
+        tc5::commit<C::CG>(drain);
         if (!ptx::mbar_wait(drain, 0, p.limit_ns)) gave_up(p.status, SITE_GEMM_DRAIN);
       }
     }
     __syncwarp();
   } else {
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t tempty0 = C::CG == 2 ? tc5::map_to(tempty, 0) : tempty;
+    const auto release = [&](int ab) {  // the accumulator has been read
+      tc5::fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (C::CG == 2)
+          tc5::arrive_cluster(tempty0 + 8 * ab);
+        else
+          ptx::mbar_arrive(tempty0 + 8 * ab);
+      }
+    };
     int acc = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    for (int t = first; t < tiles && ok; t += stride) {
       const TileAt at = tile_at(p, t);
-      const long long row = static_cast<long long>(at.m) * 128 + warp * 32 + lane;
+      const long long row = static_cast<long long>(at.m) * C::BM + rank * 128 + warp * 32 + lane;
       const int col0 = at.n * C::OUT_N;
       if constexpr (C::F32) {
         float sum[C::BN / 32][32];
@@ -319,9 +346,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
 #pragma unroll
             for (int i = 0; i < 32; ++i) sum[b][i] = c == 0 ? v[i] : sum[b][i] + v[i];
           }
-          tc5::fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(tempty + 8 * ab);
+          release(ab);
         }
         if (ok) {
 #pragma unroll
@@ -343,11 +368,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
             if constexpr (C::PAIR) tc5::ld32(ta + C::OUT_N + 32 * b, u);
             tc5::wait_ld(g);
             if constexpr (C::PAIR) tc5::wait_ld(u);
-            if (b == C::OUT_N / 32 - 1) {  // the accumulator is free
-              tc5::fence_before();
-              __syncwarp();
-              if (lane == 0) ptx::mbar_arrive(tempty + 8 * ab);
-            }
+            if (b == C::OUT_N / 32 - 1) release(ab);
             finish32<C>(p, at, row, col0 + 32 * b, g, u);
           }
         }
@@ -358,8 +379,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
   }
   tc5::fence_before();
   __syncthreads();
+  if constexpr (C::CG == 2) tc5::cluster_sync();
   tc5::fence_after();
-  if (warp == 5) tc5::dealloc(tm, C::TCOLS);
+  if (warp == 5) tc5::dealloc<C::CG>(tm, C::TCOLS);
 }
 
 template <class C>
@@ -373,9 +395,21 @@ cudaError_t launch_cfg(const GemmParams& p, int sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
   }
-  const long long tiles = static_cast<long long>(p.mt) * p.nt * p.nbatch;
-  const int grid = static_cast<int>(tiles < sms ? tiles : sms);
-  return launch_after(gemm_kernel<C>, dim3(grid), C::THREADS, C::SMEM, st, p);
+  const long long tiles = static_cast<long long>(p.mt) * p.nt * p.nbatch, most = sms / C::CG;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = C::CG;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(static_cast<unsigned>(C::CG * (tiles < most ? tiles : most)));
+  c.blockDim = dim3(C::THREADS);
+  c.dynamicSmemBytes = C::SMEM;
+  c.stream = st;
+  c.attrs = at;
+  c.numAttrs = C::CG == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&c, gemm_kernel<C>, p);
 }
 
 }  // namespace m2rnn
