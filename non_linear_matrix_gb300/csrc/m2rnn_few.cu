@@ -230,12 +230,12 @@ __global__ void __launch_bounds__(256) split_kernel(SplitParams p) {
   let_next_begin();
   const int which = blockIdx.y, vecs = p.D / 8;
   const long long total = p.M[which] * vecs;
-  const size_t plane = static_cast<size_t>(p.M[which]) * p.D;
+  const size_t plane = static_cast<size_t>(p.M[which]) * p.pitch;
   const size_t extent = static_cast<size_t>(p.M[which] - 1) * p.row[which] + p.D;
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
     const long long r = i / vecs;
     const int v = static_cast<int>(i - r * vecs);
-    const size_t src = static_cast<size_t>(r) * p.row[which] + 8 * v, at = static_cast<size_t>(r) * p.D + 8 * v;
+    const size_t src = static_cast<size_t>(r) * p.row[which] + 8 * v, at = static_cast<size_t>(r) * p.pitch + 8 * v;
     if (!in_range(p.status, src, 8, extent, CHK_GLU_IN)) continue;
     const Raw<true, 8> x = raw_load<true, 8>(p.src[which] + src);
     uint32_t t[3][4];

@@ -58,19 +58,20 @@ enum GemmEpi : int {
   EPI_GLU8,   // act(g) (.) u with scales
   EPI_LIN8,   // the product with scales, plus res
 };
-constexpr int kMaxSeg = 12;
 struct GemmParams {
-  CUtensorMap a, b0, b1;  // b1: of a pair, or of the second operand
-  int nseg;
-  int8_t az[kMaxSeg], bi[kMaxSeg], bz[kMaxSeg];  // a segment's plane of A, its B and plane
-  int kt;                   // K tiles of a segment
-  int kc;                   // K tiles of a chunk (fp32: what one chain of sums takes)
-  int mt, nt, nbatch;       // tiles; products that share B (A's planes az_step apart)
-  int az_step;
-  long long M;              // rows and columns of out
+  CUtensorMap a, b0, b1;  // b1: of a pair, or of the second segment
+  int nseg;               // products that are added up: A's planes with b0, then b1
+  int kt;                 // K tiles of a segment
+  int kc;                 // K tiles of a chunk (fp32: what one chain of sums takes)
+  int mt, nt, nbatch;     // tiles; products that share B, of A's planes one after the other
+  int whole;              // tiles that one unit of work takes each
+  int split, nparts;      // parts of each other tile, and of all of them
+  float* parts;           // their sums
+  long long M;            // rows and columns of out
   int N;
-  void* out[2];             // one for each of nbatch
-  const void* in;           // dh, res
+  int pitch;              // EPI_DGLU: elements from a row of out to the next
+  void* out[2];           // one for each of nbatch
+  const void* in;         // dh, res
   long long in_row;
   const float *sa, *sb0, *sb1;
   int act;
@@ -84,7 +85,12 @@ struct GemmKind {
   int bn;  // accumulator columns of a tile: 128 or 256
 };
 cudaError_t launch_gemm(const GemmParams& p, const GemmKind& k, int sms, cudaStream_t st);
-int gemm_bn(int epi, bool f32, long long m, int n, int nbatch, int sms);
+struct GemmPlan {
+  int bn, rows;  // accumulator columns and rows of a tile
+  int mt, nt, nbatch, whole, split, nparts;
+  size_t parts_bytes;
+};
+GemmPlan gemm_plan(int epi, bool f32, long long m, int n, int nbatch, int nseg, int kt);
 
 // Few tokens: the weights stream through registers (mma.sync).
 struct FewParams {
@@ -98,12 +104,12 @@ struct FewParams {
 constexpr int kFewMost = 64;
 cudaError_t launch_few(const FewParams& p, int epi, bool e4m3, bool f32, cudaStream_t st);
 
-// fp32 matrices into three bf16 terms [3][M][D] each.
+// fp32 matrices into three bf16 terms [3][M][pitch] each.
 struct SplitParams {
   const float* src[3];
   long long row[3], M[3];
   __nv_bfloat16* dst[3];
-  int D, n;
+  int D, pitch, n;
   int* status;
 };
 cudaError_t launch_split(const SplitParams& p, cudaStream_t st);

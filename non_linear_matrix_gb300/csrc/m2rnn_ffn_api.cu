@@ -159,37 +159,31 @@ int check_glu(const m2rnn_glu_shape* s, bool q8) {
   return M2RNN_OK;
 }
 
-// The products of bf16 terms that make up one fp32 product, small ones first.
-constexpr int kPairs = 6;
-constexpr int8_t kPairA[kPairs] = {2, 1, 0, 1, 0, 0}, kPairB[kPairs] = {0, 1, 2, 0, 1, 0};
 // fp32: K tiles whose products one chain of sums takes (256 k).
 constexpr int kChunkTiles = 4;
 
-m2rnn::GemmParams gemm_params(long long M, int N, long long K, size_t e, bool f32, int* status) {
+// Rows of what lies in the workspace start on 128 bytes: a copied row of 128 bytes then is one
+// line of L2 (rows of 1,040 and 2,800 bytes took twice the time).
+int pitch_of(int n) { return (n + 63) / 64 * 64; }
+
+m2rnn::GemmParams gemm_params(const m2rnn::GemmPlan& q, long long M, int N, int nseg, int kt, bool f32, int* status) {
   m2rnn::GemmParams p{};
   p.M = M;
   p.N = N;
-  p.kt = static_cast<int>((K * static_cast<long long>(e) + 127) / 128);
-  p.kc = f32 ? kChunkTiles : p.kt;
-  p.nseg = f32 ? kPairs : 1;
-  for (int i = 0; f32 && i < kPairs; ++i) {
-    p.az[i] = kPairA[i];
-    p.bz[i] = kPairB[i];
-  }
-  p.nbatch = 1;
+  p.kt = kt;
+  p.kc = f32 ? kChunkTiles : kt;
+  p.nseg = nseg;
+  p.mt = q.mt;
+  p.nt = q.nt;
+  p.nbatch = q.nbatch;
+  p.whole = q.whole;
+  p.split = q.split;
+  p.nparts = q.nparts;
   p.status = status;
   p.limit_ns = m2rnn::host_wait_limit_ns();
   return p;
 }
-
-int run_gemm(m2rnn::GemmParams& p, const m2rnn::GemmKind& k, int sms, cudaStream_t st) {
-  const bool pair = k.epi == m2rnn::EPI_GLU || k.epi == m2rnn::EPI_DGLU || k.epi == m2rnn::EPI_GLU8;
-  const int cols = pair ? k.bn / 2 : k.bn;
-  const int rows = k.bn == 256 ? 256 : 128;  // (of a pair of CTAs, or of one)
-  p.mt = static_cast<int>((p.M + rows - 1) / rows);
-  p.nt = (p.N + cols - 1) / cols;
-  return status_from_cuda(m2rnn::launch_gemm(p, k, sms, st));
-}
+int k_tiles(long long K, size_t e) { return static_cast<int>((K * static_cast<long long>(e) + 127) / 128); }
 
 // Hands out pieces of the workspace.
 struct Pieces {
@@ -201,23 +195,30 @@ struct Pieces {
   }
 };
 size_t terms_bytes(const m2rnn_glu_shape* s) {  // of x, wg and wu
-  const size_t x = static_cast<size_t>(s->M) * s->D, w = static_cast<size_t>(s->F) * s->D;
-  return s->in_dtype == M2RNN_F32 ? align256(6 * x) + 2 * align256(6 * w) : 0;
+  if (s->in_dtype != M2RNN_F32) return 0;
+  const size_t pitch = pitch_of(s->D);
+  return align256(6 * s->M * pitch) + 2 * align256(6 * s->F * pitch);
 }
 size_t dgu_bytes(const m2rnn_glu_shape* s) {  // the gradients of g and u
-  return align256(static_cast<size_t>(s->M) * s->F * (s->in_dtype == M2RNN_F32 ? 12 : 4));
+  return align256(static_cast<size_t>(s->M) * pitch_of(s->F) * (s->in_dtype == M2RNN_F32 ? 12 : 4));
+}
+m2rnn::GemmPlan dx_plan(const m2rnn_glu_shape* s) {
+  return m2rnn::gemm_plan(m2rnn::EPI_STORE, s->in_dtype == M2RNN_F32, s->M, s->D, 1, 2, k_tiles(s->F, 2));
+}
+m2rnn::GemmPlan dw_plan(const m2rnn_glu_shape* s) {
+  return m2rnn::gemm_plan(m2rnn::EPI_STORE, s->in_dtype == M2RNN_F32, s->F, s->D, 2, 1, k_tiles(s->M, 2));
 }
 
 // What the products read: the caller's bf16 matrices, or their terms.
 struct Operands {
   const void *x, *wg, *wu;
-  long long x_row;
+  long long x_row, w_row;
   int terms;
 };
 int make_operands(const m2rnn_glu_shape* s, const void* x, long long x_row, const void* wg, const void* wu,
                   Pieces* ws, int* status, cudaStream_t st, Operands* o) {
   if (s->in_dtype == M2RNN_BF16) {
-    *o = {x, wg, wu, x_row, 1};
+    *o = {x, wg, wu, x_row, s->D, 1};
     return M2RNN_OK;
   }
   m2rnn::SplitParams q{};
@@ -226,12 +227,13 @@ int make_operands(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
     q.src[i] = static_cast<const float*>(src[i]);
     q.row[i] = i == 0 ? x_row : s->D;
     q.M[i] = i == 0 ? s->M : s->F;
-    q.dst[i] = ws->take(static_cast<size_t>(3 * q.M[i]) * s->D);
+    q.dst[i] = ws->take(static_cast<size_t>(3 * q.M[i]) * pitch_of(s->D));
   }
   q.D = s->D;
+  q.pitch = pitch_of(s->D);
   q.n = 3;
   q.status = status;
-  *o = {q.dst[0], q.dst[1], q.dst[2], s->D, 3};
+  *o = {q.dst[0], q.dst[1], q.dst[2], q.pitch, q.pitch, 3};
   return status_from_cuda(m2rnn::launch_split(q, st));
 }
 
@@ -239,17 +241,19 @@ int make_operands(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
 int run_pair(const m2rnn_glu_shape* s, const Operands& o, int epi, const void* dh, void* out, int* status, int sms,
              cudaStream_t st) {
   const bool f32 = o.terms == 3;
-  m2rnn::GemmParams p = gemm_params(s->M, s->F, s->D, 2, f32, status);
-  const int bn = m2rnn::gemm_bn(epi, f32, s->M, s->F, 1, sms);
-  const long long x_plane = static_cast<long long>(s->M) * s->D, w_plane = static_cast<long long>(s->F) * s->D;
+  const int kt = k_tiles(s->D, 2);
+  const m2rnn::GemmPlan q = m2rnn::gemm_plan(epi, f32, s->M, s->F, 1, 1, kt);
+  m2rnn::GemmParams p = gemm_params(q, s->M, s->F, 1, kt, f32, status);
+  const long long x_plane = s->M * o.x_row, w_plane = s->F * o.w_row;
   if (!make_map(&p.a, o.x, 2, s->D, s->M, o.terms, o.x_row, f32 ? x_plane : o.x_row, 128) ||
-      !make_map(&p.b0, o.wg, 2, s->D, s->F, o.terms, s->D, f32 ? w_plane : s->D, bn / 2) ||
-      !make_map(&p.b1, o.wu, 2, s->D, s->F, o.terms, s->D, f32 ? w_plane : s->D, bn / 2))
+      !make_map(&p.b0, o.wg, 2, s->D, s->F, o.terms, o.w_row, f32 ? w_plane : o.w_row, q.bn / 2) ||
+      !make_map(&p.b1, o.wu, 2, s->D, s->F, o.terms, o.w_row, f32 ? w_plane : o.w_row, q.bn / 2))
     return M2RNN_ERR_CUDA;
   p.out[0] = out;
+  p.pitch = epi == m2rnn::EPI_DGLU ? pitch_of(s->F) : s->F;
   p.in = dh;
   p.act = s->act;
-  return run_gemm(p, {epi, false, f32, false, false, bn}, sms, st);
+  return status_from_cuda(m2rnn::launch_gemm(p, {epi, false, f32, false, false, q.bn}, sms, st));
 }
 
 }  // namespace
@@ -389,7 +393,8 @@ int m2rnn_glu_fwd(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
 
 size_t m2rnn_glu_bwd_workspace_size(const m2rnn_glu_shape* s) {
   if (check_glu(s, false) != M2RNN_OK || s->M == 0) return 0;
-  return terms_bytes(s) + dgu_bytes(s);
+  const size_t dx = dx_plan(s).parts_bytes, dw = dw_plan(s).parts_bytes;
+  return terms_bytes(s) + dgu_bytes(s) + align256(dx > dw ? dx : dw);
 }
 
 int m2rnn_glu_bwd(const m2rnn_glu_shape* s, const void* x, long long x_row, const void* wg, const void* wu,
@@ -428,40 +433,35 @@ int m2rnn_glu_bwd(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
   Operands o;
   if ((rc = make_operands(s, x, x_row, wg, wu, &ws, status, st, &o)) != M2RNN_OK) return rc;
   const bool f32 = o.terms == 3;
-  const long long hp = s->M * s->F;
+  const int hrow = pitch_of(s->F);
+  const long long hp = s->M * hrow;
   __nv_bfloat16* dgu = ws.take(static_cast<size_t>(2 * o.terms) * hp);
+  float* parts = reinterpret_cast<float*>(ws.at);
   if ((rc = run_pair(s, o, m2rnn::EPI_DGLU, dh, dgu, status, sms, st)) != M2RNN_OK) return rc;
-  const long long xp = s->M * s->D, wp = static_cast<long long>(s->F) * s->D;
+  const long long xp = s->M * o.x_row, wp = s->F * o.w_row;
   if (dx != nullptr) {  // dg wg + du wu
-    m2rnn::GemmParams p = gemm_params(s->M, s->D, s->F, 2, f32, status);
-    const int bn = m2rnn::gemm_bn(m2rnn::EPI_STORE, f32, s->M, s->D, 1, sms);
-    // of both products, the small segments before the leading ones
-    p.nseg = 0;
-    for (int i = 0; i < (f32 ? kPairs : 1); ++i)
-      for (int which = 0; which < 2; ++which, ++p.nseg) {
-        p.az[p.nseg] = static_cast<int8_t>((f32 ? kPairA[i] : 0) + which * o.terms);
-        p.bi[p.nseg] = static_cast<int8_t>(which);
-        p.bz[p.nseg] = f32 ? kPairB[i] : 0;
-      }
-    if (!make_map(&p.a, dgu, 2, s->F, s->M, 2 * o.terms, s->F, hp, 128) ||
-        !make_map(&p.b0, o.wg, 2, s->D, s->F, o.terms, s->D, f32 ? wp : s->D, 64) ||
-        !make_map(&p.b1, o.wu, 2, s->D, s->F, o.terms, s->D, f32 ? wp : s->D, 64))
+    const m2rnn::GemmPlan q = dx_plan(s);
+    m2rnn::GemmParams p = gemm_params(q, s->M, s->D, 2, k_tiles(s->F, 2), f32, status);
+    if (!make_map(&p.a, dgu, 2, s->F, s->M, 2 * o.terms, hrow, hp, 128) ||
+        !make_map(&p.b0, o.wg, 2, s->D, s->F, o.terms, o.w_row, f32 ? wp : o.w_row, 64) ||
+        !make_map(&p.b1, o.wu, 2, s->D, s->F, o.terms, o.w_row, f32 ? wp : o.w_row, 64))
       return M2RNN_ERR_CUDA;
     p.out[0] = dx;
-    if ((rc = run_gemm(p, {m2rnn::EPI_STORE, false, f32, false, true, bn}, sms, st)) != M2RNN_OK) return rc;
+    p.parts = parts;
+    rc = status_from_cuda(m2rnn::launch_gemm(p, {m2rnn::EPI_STORE, false, f32, false, true, q.bn}, sms, st));
+    if (rc != M2RNN_OK) return rc;
   }
   if (dwg != nullptr) {  // dg^T x and du^T x, which share x
-    m2rnn::GemmParams p = gemm_params(s->F, s->D, s->M, 2, f32, status);
-    const int bn = m2rnn::gemm_bn(m2rnn::EPI_STORE, f32, s->F, s->D, 2, sms);
-    p.nbatch = 2;
-    p.az_step = o.terms;
-    if (!make_map(&p.a, dgu, 2, s->F, s->M, 2 * o.terms, s->F, hp, 64) ||
+    const m2rnn::GemmPlan q = dw_plan(s);
+    m2rnn::GemmParams p = gemm_params(q, s->F, s->D, 1, k_tiles(s->M, 2), f32, status);
+    if (!make_map(&p.a, dgu, 2, s->F, s->M, 2 * o.terms, hrow, hp, 64) ||
         !make_map(&p.b0, o.x, 2, s->D, s->M, o.terms, o.x_row, f32 ? xp : o.x_row, 64))
       return M2RNN_ERR_CUDA;
     p.b1 = p.b0;
     p.out[0] = dwg;
     p.out[1] = dwu;
-    if ((rc = run_gemm(p, {m2rnn::EPI_STORE, false, f32, true, true, bn}, sms, st)) != M2RNN_OK) return rc;
+    p.parts = parts;
+    return status_from_cuda(m2rnn::launch_gemm(p, {m2rnn::EPI_STORE, false, f32, true, true, q.bn}, sms, st));
   }
   return M2RNN_OK;
 }
@@ -515,14 +515,16 @@ int product_q8(const m2rnn_glu_shape* s, const void* x, long long x_row, const f
     p.status = status;
     return status_from_cuda(m2rnn::launch_few(p, epi, true, false, st));
   }
-  m2rnn::GemmParams p = gemm_params(s->M, s->F, s->D, 1, false, status);
-  const int bn = m2rnn::gemm_bn(epi, false, s->M, s->F, 1, sms);
+  const int kt = k_tiles(s->D, 1);
+  const m2rnn::GemmPlan q = m2rnn::gemm_plan(epi, false, s->M, s->F, 1, 1, kt);
+  m2rnn::GemmParams p = gemm_params(q, s->M, s->F, 1, kt, false, status);
+  const int box = pair ? q.bn / 2 : 128;
   if (!make_map(&p.a, x, 1, s->D, s->M, 1, x_row, x_row, 128) ||
-      !make_map(&p.b0, w0, 1, s->D, s->F, 1, s->D, s->D, pair ? bn / 2 : 128))
+      !make_map(&p.b0, w0, 1, s->D, s->F, 1, s->D, s->D, box))
     return M2RNN_ERR_CUDA;
   if (!pair)
     p.b1 = p.b0;
-  else if (!make_map(&p.b1, w1, 1, s->D, s->F, 1, s->D, s->D, bn / 2))
+  else if (!make_map(&p.b1, w1, 1, s->D, s->F, 1, s->D, s->D, box))
     return M2RNN_ERR_CUDA;
   p.out[0] = out;
   p.in = res;
@@ -531,7 +533,7 @@ int product_q8(const m2rnn_glu_shape* s, const void* x, long long x_row, const f
   p.sb0 = s0;
   p.sb1 = s1;
   p.act = s->act;
-  return run_gemm(p, {epi, true, false, false, false, bn}, sms, st);
+  return status_from_cuda(m2rnn::launch_gemm(p, {epi, true, false, false, false, q.bn}, sms, st));
 }
 
 }  // namespace

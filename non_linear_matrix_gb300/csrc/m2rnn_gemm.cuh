@@ -4,18 +4,21 @@
 // one CTA, or 256 x BN of a pair of CTAs (CG = 2), each of which holds half of the rows of A
 // and of B, so that a byte of B in shared memory serves twice as many rows.
 // One persistent CTA per SM: a warp that issues the tensor-map copies into a ring of
-// K tiles (128 bytes of K each), a warp whose elected thread issues tcgen05.mma, and four
-// warps that turn finished accumulators into outputs.  Tensor memory holds two
+// K tiles (128 bytes of K each), a warp whose elected thread issues tcgen05.mma, and eight
+// warps that turn finished accumulators into outputs.  Tensor memory holds two sets of
 // accumulators, so that the products of the next tile run meanwhile.
 //
 // PAIR (gated products): the accumulator's halves are the products with two weights'
 // rows of the same numbers, so g and u of an output meet in one thread.
 //
 // fp32: operands come as three bf16 terms each (x = x0 + x1 + x2, |x1| <= 2^-9 |x|,
-// |x2| <= 2^-18 |x|), and the six products down to 2^-27 are segments of one sum, the
-// small ones first.  The tensor core cuts its sums off where it should round, which
-// drifts along a long sum; so K is taken in chunks whose accumulators are added with
-// rounding in registers.
+// |x2| <= 2^-18 |x|); a K tile holds all terms of both, and the six products down to
+// 2^-27 are formed from it.  The tensor core cuts its sums off where it should round, which
+// drifts along a long sum; so the leading products and the small ones have accumulators of
+// their own, and K is taken in chunks whose sums are added with rounding in registers.
+//
+// A last wave of few tiles is cut along K (`split` parts each, fp32 sums in memory that
+// join_parts_kernel adds in order), so that it takes 1/split of a wave.
 #pragma once
 #include "m2rnn_act.cuh"
 #include "m2rnn_ffn.h"
@@ -32,25 +35,40 @@ struct GemmCfg {
   static constexpr bool PAIR = EPI == EPI_GLU || EPI == EPI_DGLU || EPI == EPI_GLU8;
   static constexpr int OUT_N = PAIR ? BN / 2 : BN;  // output columns of a tile
   static constexpr int KT = E4M3 ? 128 : 64;        // elements of a K tile
-  static constexpr int A_BYTES = 128 * 128, B_BYTES = BR * 128, STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 6;
+  static constexpr int TERMS = F32 ? 3 : 1;
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = BR * 128;  // of a term
+  static constexpr int STAGE = TERMS * (A_BYTES + B_BYTES);
+  static constexpr int STAGES = 220 * 1024 / STAGE;  // (6 of 32 KB, 3 of 72 KB)
   static constexpr int SMEM = STAGES * STAGE + 1024;
-  static constexpr int TCOLS = 2 * BN;
-  static constexpr int THREADS = 192;
+  static constexpr int ACC = F32 ? 2 * BN : BN;  // columns of a set of accumulators
+  static constexpr int TCOLS = 2 * ACC;
+  static constexpr int OUT_WARPS = 8, THREADS = 32 * (OUT_WARPS + 2);
+  static constexpr int BLOCKS = OUT_N / 32 / 2;  // blocks of 32 output columns of a warp
 };
 
 __device__ __forceinline__ void gave_up(int* status, int site) {
   if (atomicCAS(&status[0], 0, kStatusTimeout) == 0) atomicExch(&status[1], site);
 }
 
+// A unit of work: a tile, or the part `part` of a tile of the last wave.
 struct TileAt {
-  int batch, m, n;
+  int batch, m, n, k0, k1, part;  // part < 0: the whole tile
 };
 // Tiles in groups of 16 rows of tiles, rows fastest: what runs at the same time shares
 // its B columns and, between neighbours, its A rows in L2.
 __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
-  const int per = p.mt * p.nt;
   TileAt r;
+  r.k0 = 0;
+  r.k1 = p.kt;
+  r.part = -1;
+  if (t >= p.whole) {
+    r.part = t - p.whole;
+    t = p.whole + r.part / p.split;
+    const int i = r.part % p.split;
+    r.k0 = static_cast<int>(static_cast<long long>(p.kt) * i / p.split);
+    r.k1 = static_cast<int>(static_cast<long long>(p.kt) * (i + 1) / p.split);
+  }
+  const int per = p.mt * p.nt;
   r.batch = t / per;
   t -= r.batch * per;
   const int group = t / (16 * p.nt), first = group * 16;
@@ -65,31 +83,35 @@ template <class C>
 __device__ __forceinline__ void issue_tile(const GemmParams& p, uint32_t dst, uint32_t bar, const TileAt& t, int rank,
                                            int seg, int kt) {
   const int k = kt * C::KT;
-  const int az = p.az[seg] + t.batch * p.az_step, bz = p.bz[seg];
   const int m = t.m * C::BM + rank * 128;
-  if constexpr (C::A_MN) {
-    tc5::copy_box<C::CG>(dst, &p.a, m, k, az, bar);
-    tc5::copy_box<C::CG>(dst + 8192, &p.a, m + 64, k, az, bar);
-  } else {
-    tc5::copy_box<C::CG>(dst, &p.a, k, m, az, bar);
-  }
-  const uint32_t b = dst + C::A_BYTES;
-  if constexpr (C::PAIR) {
-    const int n = t.n * C::OUT_N;
-    if constexpr (C::CG == 2) {  // a weight to each CTA
-      tc5::copy_box<2>(b, rank ? &p.b1 : &p.b0, k, n, bz, bar);
-    } else {
-      tc5::copy_box<1>(b, &p.b0, k, n, bz, bar);
-      tc5::copy_box<1>(b + C::B_BYTES / 2, &p.b1, k, n, bz, bar);
-    }
-  } else {
-    const int n = t.n * C::OUT_N + rank * C::BR;
-    const CUtensorMap* map = p.bi[seg] ? &p.b1 : &p.b0;
-    if constexpr (C::B_MN) {
 #pragma unroll
-      for (int i = 0; i < C::BR / 64; ++i) tc5::copy_box<C::CG>(b + 8192 * i, map, n + 64 * i, k, bz, bar);
+  for (int term = 0; term < C::TERMS; ++term) {
+    const uint32_t a = dst + term * C::A_BYTES;
+    const int az = (seg + t.batch) * C::TERMS + term;  // (one of the two counts at a time)
+    if constexpr (C::A_MN) {
+      tc5::copy_box<C::CG>(a, &p.a, m, k, az, bar);
+      tc5::copy_box<C::CG>(a + 8192, &p.a, m + 64, k, az, bar);
     } else {
-      tc5::copy_box<C::CG>(b, map, k, n, bz, bar);
+      tc5::copy_box<C::CG>(a, &p.a, k, m, az, bar);
+    }
+    const uint32_t b = dst + C::TERMS * C::A_BYTES + term * C::B_BYTES;
+    if constexpr (C::PAIR) {
+      const int n = t.n * C::OUT_N;
+      if constexpr (C::CG == 2) {  // a weight to each CTA
+        tc5::copy_box<2>(b, rank ? &p.b1 : &p.b0, k, n, term, bar);
+      } else {
+        tc5::copy_box<1>(b, &p.b0, k, n, term, bar);
+        tc5::copy_box<1>(b + C::B_BYTES / 2, &p.b1, k, n, term, bar);
+      }
+    } else {
+      const int n = t.n * C::OUT_N + rank * C::BR;
+      const CUtensorMap* map = seg ? &p.b1 : &p.b0;
+      if constexpr (C::B_MN) {
+#pragma unroll
+        for (int i = 0; i < C::BR / 64; ++i) tc5::copy_box<C::CG>(b + 8192 * i, map, n + 64 * i, k, term, bar);
+      } else {
+        tc5::copy_box<C::CG>(b, map, k, n, term, bar);
+      }
     }
   }
 }
@@ -123,6 +145,18 @@ __device__ __forceinline__ void load32(const void* in, size_t at, int cols, floa
   }
 }
 
+// 32 scales (the same ones for the whole warp).
+__device__ __forceinline__ void load32_const(const float* in, int at, int cols, float (&v)[32], size_t extent,
+                                             int* status) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (8 * i < cols && in_range(status, at + 8 * i, 8, extent, CHK_GLU_IN)) load_vec<true, 8>(in + at + 8 * i, o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[8 * i + j] = o[j];
+  }
+}
+
 // The bf16 terms of fp32 values: each the rounding of what the ones before leave.  A
 // value that is not finite is its own first term.
 __device__ __forceinline__ void next_term(float (&v)[32], float (&t)[32]) {
@@ -139,6 +173,13 @@ __device__ __forceinline__ void finish32(const GemmParams& p, const TileAt& t, l
                                          float (&u)[32]) {
   const int cols = min(32, p.N - col);
   if (row >= p.M || cols <= 0) return;
+  if (C::EPI == EPI_STORE && t.part >= 0) {  // fp32 sums of a part: [part][rows of a tile][BN]
+    const size_t tile = static_cast<size_t>(C::BM) * C::BN;
+    const size_t at = t.part * tile + static_cast<size_t>(row - static_cast<long long>(t.m) * C::BM) * C::BN +
+                      (col - t.n * C::BN);
+    store32<true>(p.parts, at, 32, g, tile * p.nparts, p.status, CHK_GLU_WS);
+    return;
+  }
   const size_t at = static_cast<size_t>(row) * p.N + col, extent = static_cast<size_t>(p.M) * p.N;
   if constexpr (C::EPI == EPI_GLU) {
 #pragma unroll
@@ -162,14 +203,15 @@ __device__ __forceinline__ void finish32(const GemmParams& p, const TileAt& t, l
     for (int which = 0; which < 2; ++which) {
 #pragma unroll
       for (int k = 0; k < terms; ++k) {
-        const size_t plane = static_cast<size_t>(which * terms + k) * extent;
+        const size_t plane = static_cast<size_t>(which * terms + k) * p.M * p.pitch;
         if constexpr (C::F32)
           next_term(which ? u : g, d);
         else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) d[i] = which ? u[i] : g[i];
         }
-        store32<false>(out, plane + at, cols, d, 2 * terms * extent, p.status, CHK_GLU_WS);
+        store32<false>(out, plane + static_cast<size_t>(row) * p.pitch + col, cols, d,
+                       2 * terms * static_cast<size_t>(p.M) * p.pitch, p.status, CHK_GLU_WS);
       }
     }
   } else if constexpr (C::EPI == EPI_STORE) {
@@ -177,19 +219,16 @@ __device__ __forceinline__ void finish32(const GemmParams& p, const TileAt& t, l
   } else {
     const float sa = __ldg(p.sa + row);
     const size_t n = static_cast<size_t>(p.N);
+    float s0[32];
+    load32_const(p.sb0, col, cols, s0, n, p.status);
     if constexpr (C::EPI == EPI_GLU8) {
+      float s1[32];
+      load32_const(p.sb1, col, cols, s1, n, p.status);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const bool in = i < cols && in_range(p.status, col + i, 1, n, CHK_GLU_IN);
-        const float s0 = in ? __ldg(p.sb0 + col + i) : 0.f, s1 = in ? __ldg(p.sb1 + col + i) : 0.f;
-        g[i] = act_of<false>(g[i] * (sa * s0), p.act) * (u[i] * (sa * s1));
-      }
+      for (int i = 0; i < 32; ++i) g[i] = act_of<false>(g[i] * (sa * s0[i]), p.act) * (u[i] * (sa * s1[i]));
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const bool in = i < cols && in_range(p.status, col + i, 1, n, CHK_GLU_IN);
-        g[i] *= sa * (in ? __ldg(p.sb0 + col + i) : 0.f);
-      }
+      for (int i = 0; i < 32; ++i) g[i] *= sa * s0[i];
       if (p.in != nullptr) {
         load32<false>(p.in, static_cast<size_t>(row) * p.in_row + col, cols, u,
                       static_cast<size_t>(p.M - 1) * p.in_row + n, p.status, CHK_GLU_IN);
@@ -219,12 +258,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(tfull + 8 * i, 1);
-      ptx::mbar_init(tempty + 8 * i, 4 * C::CG);
+      ptx::mbar_init(tempty + 8 * i, C::OUT_WARPS * C::CG);
     }
     ptx::mbar_init(drain, 1);
     ptx::mbar_init_fence();
   }
-  if (warp == 5) tc5::alloc<C::CG>(ptx::smem_addr(&tslot), C::TCOLS);
+  if (warp == C::OUT_WARPS + 1) tc5::alloc<C::CG>(ptx::smem_addr(&tslot), C::TCOLS);
   tc5::fence_before();
   __syncthreads();
   if constexpr (C::CG == 2) tc5::cluster_sync();
@@ -233,8 +272,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
   let_next_begin();
   await_before();
 
-  const int tiles = p.mt * p.nt * p.nbatch, nchunk = (p.kt + p.kc - 1) / p.kc;
-  if (warp == 4) {
+  const int tiles = p.whole + p.nparts;
+  if (warp == C::OUT_WARPS) {
     if (tc5::elect_one()) {
       tc5::prefetch_map(&p.a);
       tc5::prefetch_map(&p.b0);
@@ -244,9 +283,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
       bool ok = true;
       for (int t = first; t < tiles && ok; t += stride) {
         const TileAt at = tile_at(p, t);
-        for (int c = 0; c < nchunk && ok; ++c)
+        for (int c = at.k0; c < at.k1 && ok; c += p.kc)
           for (int s = 0; s < p.nseg && ok; ++s)
-            for (int k = c * p.kc; k < min(p.kt, (c + 1) * p.kc); ++k, ++it) {
+            for (int k = c; k < min(at.k1, c + p.kc); ++k, ++it) {
               const int st = it % C::STAGES, round = it / C::STAGES;
               if (!ptx::mbar_wait(empty + 8 * st, (round & 1) ^ 1, p.limit_ns)) {
                 ok = false;
@@ -267,41 +306,56 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
       }
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == C::OUT_WARPS + 1) {
     if (rank == 0 && tc5::elect_one()) {
       constexpr uint32_t id = tc5::idesc(C::BM, C::BN, C::E4M3, C::A_MN, C::B_MN);
       constexpr uint32_t a_step = C::A_MN ? 2048 : 32, b_step = C::B_MN ? 2048 : 32;
       int it = 0, acc = 0;
       bool ok = true;
       int site = SITE_GEMM_MMA;
-      for (int t = first; t < tiles && ok; t += stride)
-        for (int c = 0; c < nchunk && ok; ++c, ++acc) {
+      for (int t = first; t < tiles && ok; t += stride) {
+        const TileAt at = tile_at(p, t);
+        for (int c = at.k0; c < at.k1 && ok; c += p.kc, ++acc) {
           const int ab = acc & 1;
           if (!tc5::wait_released<C::CG>(tempty + 8 * ab, ((acc >> 1) & 1) ^ 1, p.limit_ns)) {
             ok = false;
             break;
           }
           tc5::fence_after();
+          const uint32_t lead = tm + ab * C::ACC, small = lead + C::BN;
           bool add = false;
           for (int s = 0; s < p.nseg && ok; ++s)
-            for (int k = c * p.kc; k < min(p.kt, (c + 1) * p.kc); ++k, ++it) {
+            for (int k = c; k < min(at.k1, c + p.kc); ++k, ++it) {
               const int st = it % C::STAGES;
               if (!ptx::mbar_wait(full + 8 * st, (it / C::STAGES) & 1, p.limit_ns)) {
                 ok = false;
                 break;
               }
               tc5::fence_after();
-              const uint32_t sa = base + st * C::STAGE, sb = sa + C::A_BYTES;
+              const uint32_t sa = base + st * C::STAGE, sb = sa + C::TERMS * C::A_BYTES;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                tc5::mma<C::E4M3, C::CG>(tm + ab * C::BN, tc5::sdesc(sa + i * a_step, C::A_MN ? 8192 : 16, 1024),
-                                  tc5::sdesc(sb + i * b_step, C::B_MN ? 8192 : 16, 1024), id, add);
+                const auto ad = [&](int term) {
+                  return tc5::sdesc(sa + term * C::A_BYTES + i * a_step, C::A_MN ? 8192 : 16, 1024);
+                };
+                const auto bd = [&](int term) {
+                  return tc5::sdesc(sb + term * C::B_BYTES + i * b_step, C::B_MN ? 8192 : 16, 1024);
+                };
+                tc5::mma<C::E4M3, C::CG>(lead, ad(0), bd(0), id, add);
+                if constexpr (C::F32) {
+                  tc5::mma<C::E4M3, C::CG>(small, ad(2), bd(0), id, add);
+                  tc5::mma<C::E4M3, C::CG>(small, ad(1), bd(1), id, true);
+                  tc5::mma<C::E4M3, C::CG>(small, ad(0), bd(2), id, true);
+                  tc5::mma<C::E4M3, C::CG>(small, ad(1), bd(0), id, true);
+                  tc5::mma<C::E4M3, C::CG>(small, ad(0), bd(1), id, true);
+                }
                 add = true;
               }
               tc5::commit<C::CG>(empty + 8 * st);
             }
           if (ok) tc5::commit<C::CG>(tfull + 8 * ab);
         }
+      }
       if (!ok) {
         gave_up(p.status, site);
         tc5::commit<C::CG>(drain);
@@ -310,7 +364,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
     }
     __syncwarp();
   } else {
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int half = (warp >> 2) * C::BLOCKS;  // this warp's first block of columns
     const uint32_t tempty0 = C::CG == 2 ? tc5::map_to(tempty, 0) : tempty;
     const auto release = [&](int ab) {  // the accumulator has been read
       tc5::fence_before();
@@ -326,32 +381,35 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
     bool ok = true;
     for (int t = first; t < tiles && ok; t += stride) {
       const TileAt at = tile_at(p, t);
-      const long long row = static_cast<long long>(at.m) * C::BM + rank * 128 + warp * 32 + lane;
+      const long long row = static_cast<long long>(at.m) * C::BM + rank * 128 + (warp & 3) * 32 + lane;
       const int col0 = at.n * C::OUT_N;
       if constexpr (C::F32) {
-        float sum[C::BN / 32][32];
-        for (int c = 0; c < nchunk; ++c, ++acc) {
+        float sum[C::PAIR ? 2 : 1][C::BLOCKS][32];
+        for (int c = at.k0; c < at.k1; c += p.kc, ++acc) {
           const int ab = acc & 1;
           ok = ptx::mbar_wait(tfull + 8 * ab, (acc >> 1) & 1, p.limit_ns);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc5::fence_after();
 #pragma unroll
-          for (int b = 0; b < C::BN / 32; ++b) {
-            float v[32];
-            tc5::ld32(tm + lanes + ab * C::BN + 32 * b, v);
-            tc5::wait_ld(v);
+          for (int w = 0; w < (C::PAIR ? 2 : 1); ++w)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sum[b][i] = c == 0 ? v[i] : sum[b][i] + v[i];
-          }
+            for (int b = 0; b < C::BLOCKS; ++b) {
+              float v[32], r[32];
+              const uint32_t ta = tm + lanes + ab * C::ACC + w * C::OUT_N + 32 * (half + b);
+              tc5::ld32(ta, v);
+              tc5::ld32(ta + C::BN, r);
+              tc5::wait_ld(v);
+              tc5::wait_ld(r);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sum[w][b][i] = c == at.k0 ? v[i] + r[i] : sum[w][b][i] + (v[i] + r[i]);
+            }
           release(ab);
         }
         if (ok) {
 #pragma unroll
-          for (int b = 0; b < C::OUT_N / 32; ++b)
-            finish32<C>(p, at, row, col0 + 32 * b, sum[b], sum[C::PAIR ? b + C::OUT_N / 32 : b]);
+          for (int b = 0; b < C::BLOCKS; ++b)
+            finish32<C>(p, at, row, col0 + 32 * (half + b), sum[0][b], sum[C::PAIR ? 1 : 0][b]);
         }
       } else {
         const int ab = acc & 1;
@@ -359,17 +417,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
           tc5::fence_after();
-          const uint32_t ta = tm + lanes + ab * C::BN;
+          const uint32_t ta = tm + lanes + ab * C::ACC + 32 * half;
 #pragma unroll 1
-          for (int b = 0; b < C::OUT_N / 32; ++b) {
+          for (int b = 0; b < C::BLOCKS; ++b) {
             float g[32], u[32];
             __syncwarp();
             tc5::ld32(ta + 32 * b, g);
             if constexpr (C::PAIR) tc5::ld32(ta + C::OUT_N + 32 * b, u);
             tc5::wait_ld(g);
             if constexpr (C::PAIR) tc5::wait_ld(u);
-            if (b == C::OUT_N / 32 - 1) release(ab);
-            finish32<C>(p, at, row, col0 + 32 * b, g, u);
+            if (b == C::BLOCKS - 1) release(ab);
+            finish32<C>(p, at, row, col0 + 32 * (half + b), g, u);
           }
         }
         ++acc;
@@ -381,7 +439,35 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
   __syncthreads();
   if constexpr (C::CG == 2) tc5::cluster_sync();
   tc5::fence_after();
-  if (warp == 5) tc5::dealloc<C::CG>(tm, C::TCOLS);
+  if (warp == C::OUT_WARPS + 1) tc5::dealloc<C::CG>(tm, C::TCOLS);
+}
+
+// The parts of the last wave's tiles, added in order: out = sum over i of parts[t][i].  A thread
+// takes 8 columns.
+template <class C>
+__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ GemmParams p) {
+  await_before();
+  constexpr int VECS = C::BN / 8;
+  const size_t tile = static_cast<size_t>(C::BM) * C::BN;
+  const int t = blockIdx.y, v = blockIdx.x * 256 + threadIdx.x;
+  const int r = v / VECS, c = v % VECS * 8;
+  if (r >= C::BM) return;
+  const TileAt at = tile_at(p, p.whole + t * p.split);
+  const long long row = static_cast<long long>(at.m) * C::BM + r;
+  const int col = at.n * C::BN + c;
+  if (row >= p.M || col >= p.N) return;
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < p.split; ++i) {
+    const size_t from = (static_cast<size_t>(t) * p.split + i) * tile + static_cast<size_t>(r) * C::BN + c;
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (in_range(p.status, from, 8, tile * p.nparts, CHK_GLU_WS))
+      raw_unpack<true, 8>(raw_load<true, 8, false>(p.parts + from), o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] += o[j];
+  }
+  const size_t to = static_cast<size_t>(row) * p.N + col;
+  if (in_range(p.status, to, 8, static_cast<size_t>(p.M) * p.N, CHK_GLU_OUT))
+    store_vec<C::F32, 8>(static_cast<typename Elem<C::F32>::T*>(at.batch ? p.out[1] : p.out[0]) + to, s);
 }
 
 template <class C>
@@ -395,7 +481,7 @@ cudaError_t launch_cfg(const GemmParams& p, int sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
   }
-  const long long tiles = static_cast<long long>(p.mt) * p.nt * p.nbatch, most = sms / C::CG;
+  const int tiles = p.whole + p.nparts, most = sms / C::CG;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -409,7 +495,12 @@ cudaError_t launch_cfg(const GemmParams& p, int sms, cudaStream_t st) {
   c.stream = st;
   c.attrs = at;
   c.numAttrs = C::CG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&c, gemm_kernel<C>, p);
+  e = cudaLaunchKernelEx(&c, gemm_kernel<C>, p);
+  if constexpr (C::EPI == EPI_STORE) {
+    if (e == cudaSuccess && p.nparts > 0)
+      e = launch_after(join_parts_kernel<C>, dim3(C::BM * C::BN / 8 / 256, p.nparts / p.split), 256, 0, st, p);
+  }
+  return e;
 }
 
 }  // namespace m2rnn

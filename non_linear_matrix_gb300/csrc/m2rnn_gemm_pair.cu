@@ -9,7 +9,7 @@ cudaError_t launch_gemm_grad(const GemmParams& p, const GemmKind& k, int sms, cu
 cudaError_t launch_gemm(const GemmParams& p, const GemmKind& k, int sms, cudaStream_t st) {
   switch (k.epi) {
     case EPI_GLU:
-      if (k.f32) return launch_cfg<GemmCfg<EPI_GLU, false, true, false, false, 128, 1>>(p, sms, st);
+      if (k.f32) return launch_cfg<GemmCfg<EPI_GLU, false, true, false, false, 128, 2>>(p, sms, st);
       return k.bn == 256 ? launch_cfg<GemmCfg<EPI_GLU, false, false, false, false, 256, 2>>(p, sms, st)
                          : launch_cfg<GemmCfg<EPI_GLU, false, false, false, false, 128, 1>>(p, sms, st);
     case EPI_GLU8:
@@ -23,15 +23,43 @@ cudaError_t launch_gemm(const GemmParams& p, const GemmKind& k, int sms, cudaStr
   }
 }
 
-// Accumulator columns of a tile: 256, by a pair of CTAs over 256 rows, where there are
-// as many tiles as pairs; otherwise 128, by a CTA over 128 rows.  fp32: 128, whose sums fit
-// the registers.
-int gemm_bn(int epi, bool f32, long long m, int n, int nbatch, int sms) {
-  if (f32) return 128;
+// Tiles of 256 x 256 by a pair of CTAs where there are as many as pairs (76, two to each of
+// 152 SMs); otherwise 128 x 128 by a CTA.  fp32: 256 x 128 by a pair, whose terms and sums fit.
+// The tiles beyond whole waves are cut along K into as many parts as leave every pair or
+// CTA one, each of 8 K tiles at least.
+GemmPlan gemm_plan(int epi, bool f32, long long m, int n, int nbatch, int nseg, int kt) {
+  constexpr int kSms = 152;
   const bool pair = epi == EPI_GLU || epi == EPI_DGLU || epi == EPI_GLU8;
-  const int cols = pair ? 128 : 256;
-  const long long tiles = (m + 255) / 256 * ((n + cols - 1) / cols) * nbatch;
-  return 2 * tiles >= sms ? 256 : 128;
+  GemmPlan q{};
+  const auto tiles = [&](int rows, int bn) {
+    const int cols = pair ? bn / 2 : bn;
+    q.bn = bn;
+    q.rows = rows;
+    q.mt = static_cast<int>((m + rows - 1) / rows);
+    q.nt = (n + cols - 1) / cols;
+    q.nbatch = nbatch;
+    return q.mt * q.nt * nbatch;
+  };
+  int count, at_once = kSms / 2;
+  if (f32) {
+    count = tiles(256, 128);
+  } else if ((count = tiles(256, 256)) < at_once) {
+    count = tiles(128, 128);
+    at_once = kSms;
+  }
+  q.whole = count;
+  q.split = 1;
+  const int rest = count % at_once;
+  if (epi != EPI_STORE || rest == 0) return q;
+  int split = at_once / rest;
+  if (split > nseg * kt / 8) split = nseg * kt / 8;
+  if (split > kt) split = kt;
+  if (split < 2) return q;
+  q.whole = count - rest;
+  q.split = split;
+  q.nparts = rest * split;
+  q.parts_bytes = static_cast<size_t>(q.nparts) * q.rows * q.bn * sizeof(float);
+  return q;
 }
 
 }  // namespace m2rnn
