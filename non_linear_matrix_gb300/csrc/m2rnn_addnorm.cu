@@ -37,11 +37,17 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// 8 codes of o / scale.
-__device__ __forceinline__ uint2 codes8(const float (&o)[8], float scale) {
+// 8 codes of o / scale.  The quotient is o times the rounded reciprocal (2^-23 off, against e4m3's
+// half step of 2^-4), a true division only where the reciprocal might overflow: the divisions
+// took 13 of 38 us of the 8-bit norm at 12,001 rows of 2,000.
+__device__ __forceinline__ uint2 codes8(const float (&o)[8], float scale, float inv) {
   float c[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) c[j] = scale == 0.f ? 0.f : __fdiv_rn(o[j], scale);
+  for (int j = 0; j < 8; ++j) c[j] = o[j] * inv;
+  if (!(scale > 1e-30f)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = scale == 0.f ? 0.f : __fdiv_rn(o[j], scale);
+  }
   return make_uint2(e4m3x2(c[0], c[1]) | (e4m3x2(c[2], c[3]) << 16), e4m3x2(c[4], c[5]) | (e4m3x2(c[6], c[7]) << 16));
 }
 
@@ -142,79 +148,99 @@ __global__ void __launch_bounds__(512) add_norm_kernel(Norm2Params p, int warps,
   }
   if constexpr (Q8) {
     row_reduce<1, true>(top, warps, sm);
-    const float scale = __fdiv_rn(top[0], kE4m3Max);
+    const float scale = __fdiv_rn(top[0], kE4m3Max), inv = 1.f / scale;
     if (lane == 0 && in_range(p.status, row, 1, p.M, CHK_NORM2_OUT)) p.scale[row] = scale;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = lane + i * group;
       if (v < vecs && in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
-        *reinterpret_cast<uint2*>(p.q + at + 8 * v) = codes8(keep[i], scale);
+        *reinterpret_cast<uint2*>(p.q + at + 8 * v) = codes8(keep[i], scale, inv);
     }
   }
 }
 
-// The quantiser: a CTA per row, which reads the row twice (its second time from L1 or L2).
+// The quantiser: a CTA per row, whose threads keep four vectors each; what is behind those is
+// read a second time.
 template <bool F32>
 __global__ void __launch_bounds__(256) quant_rows_kernel(Norm2Params p) {
   using T = typename Elem<F32>::T;
+  constexpr int NV = 4;
   __shared__ float sm[32];
-  const int vecs = p.D / 8;
+  const int vecs = p.D / 8, step = blockDim.x;
   const long long row = blockIdx.x;
   const size_t n = static_cast<size_t>(p.M) * p.D, at = static_cast<size_t>(row) * p.D;
   const size_t x0 = static_cast<size_t>(row) * p.x_row, x_ext = static_cast<size_t>(p.M - 1) * p.x_row + p.D;
   const T* x = static_cast<const T*>(p.x) + x0;
+  const auto load = [&](int v) {
+    return v < vecs && in_range(p.status, x0 + 8 * v, 8, x_ext, CHK_NORM2_IN) ? raw_load<F32, 8>(x + 8 * v)
+                                                                              : raw_zero<F32, 8>();
+  };
+  Raw<F32, 8> keep[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) keep[i] = load(threadIdx.x + i * step);
   float top[1] = {0.f};
-  for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
-    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (in_range(p.status, x0 + 8 * v, 8, x_ext, CHK_NORM2_IN)) load_vec<F32, 8>(x + 8 * v, o);
+  const auto take = [&](const Raw<F32, 8>& r) {
+    float o[8];
+    raw_unpack<F32, 8>(r, o);
 #pragma unroll
     for (int j = 0; j < 8; ++j) top[0] = nan_max(top[0], fabsf(o[j]));
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) take(keep[i]);
+  for (int v = threadIdx.x + NV * step; v < vecs; v += step) take(load(v));
   row_reduce<1, true>(top, blockDim.x / 32, sm);
-  const float scale = __fdiv_rn(top[0], kE4m3Max);
+  const float scale = __fdiv_rn(top[0], kE4m3Max), inv = 1.f / scale;
   if (threadIdx.x == 0 && in_range(p.status, row, 1, p.M, CHK_NORM2_OUT)) p.scale[row] = scale;
-  for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
-    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (in_range(p.status, x0 + 8 * v, 8, x_ext, CHK_NORM2_IN)) load_vec<F32, 8>(x + 8 * v, o);
-    if (in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
-      *reinterpret_cast<uint2*>(p.q + at + 8 * v) = codes8(o, scale);
-  }
+  const auto put = [&](int v, const Raw<F32, 8>& r) {
+    float o[8];
+    raw_unpack<F32, 8>(r, o);
+    if (v < vecs && in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
+      *reinterpret_cast<uint2*>(p.q + at + 8 * v) = codes8(o, scale, inv);
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) put(threadIdx.x + i * step, keep[i]);
+  for (int v = threadIdx.x + NV * step; v < vecs; v += step) put(v, load(v));
 }
 
 // Backward: with n = r rstd, p = w dy:  dx = dr + rstd (p - n mean(p n)),  dw = sum dy n.
-// A group walks over rows (p.nparts groups in all) with its share of dw in registers and
-// writes it to `part`; sum_parts adds the shares in order.
+// A CTA holds several groups of warps, each of which walks over rows with its share of dw in
+// registers and the next row's loads in flight.  The groups' shares are added in order, then
+// the CTAs' by sum_parts.
 template <bool F32, int NV>
-__global__ void __launch_bounds__(512) add_norm_bwd_kernel(Norm2Params p, int warps) {
+__global__ void __launch_bounds__(NV == 4 ? 512 : 256, NV == 4 || (F32 && NV == 2) ? 1 : 2)
+    add_norm_bwd_kernel(Norm2Params p, int warps) {
   using T = typename Elem<F32>::T;
-  __shared__ float sm[64];
-  const int group = warps * 32, vecs = p.D / 8;
-  const int lane = warps == 1 ? threadIdx.x & 31 : threadIdx.x;
-  const int part = warps == 1 ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  constexpr int CTA = NV == 4 ? 512 : 256;
+  __shared__ float2 sums[2][CTA / 32];
+  __shared__ float share[NV == 4 ? 1 : CTA * NV * 8];  // [groups][D]
+  const int group = warps * 32, vecs = p.D / 8, groups = CTA / group;
+  const int lane = threadIdx.x % group, mine = threadIdx.x / group;
   let_next_begin();
-  if (part >= p.nparts) return;
   const size_t D = p.D, n = static_cast<size_t>(p.M) * D;
   const size_t r_ext = static_cast<size_t>(p.M - 1) * p.x_row + D;
-  float dw[NV][8], w[NV][8];
+  float dw[NV][8];
+  Raw<F32, 8> w[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = lane + i * group;
+    float one[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       dw[i][j] = 0.f;
-      w[i][j] = 1.f;
+      one[j] = 1.f;
     }
+    w[i] = raw_pack<F32, 8>(one);
     if (p.w != nullptr && v < vecs && in_range(p.status, 8 * v, 8, D, CHK_NORM2_PARAM))
-      load_vec<F32, 8>(static_cast<const T*>(p.w) + 8 * v, w[i]);
+      w[i] = raw_load<F32, 8>(static_cast<const T*>(p.w) + 8 * v);
   }
-  for (long long row = part; row < p.M; row += p.nparts) {
+  Raw<F32, 8> rv[NV], yv[NV], gv[NV];
+  const auto load = [&](long long row) {
     const size_t at = static_cast<size_t>(row) * D, r0 = static_cast<size_t>(row) * p.x_row;
-    Raw<F32, 8> rv[NV], yv[NV], gv[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = lane + i * group;
       rv[i] = yv[i] = gv[i] = raw_zero<F32, 8>();
-      if (v < vecs) {
+      if (v < vecs && row < p.M) {
         if (in_range(p.status, r0 + 8 * v, 8, r_ext, CHK_NORM2_IN))
           rv[i] = raw_load<F32, 8>(static_cast<const T*>(p.x) + r0 + 8 * v);
         if (in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_IN)) {
@@ -223,45 +249,91 @@ __global__ void __launch_bounds__(512) add_norm_bwd_kernel(Norm2Params p, int wa
         }
       }
     }
+  };
+  const long long step = static_cast<long long>(gridDim.x) * groups;
+  long long row = static_cast<long long>(blockIdx.x) * groups + mine;
+  load(row);
+  for (int turn = 0; row < p.M; row += step, turn ^= 1) {  // (the same count in all warps of a group)
+    const size_t at = static_cast<size_t>(row) * D;
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float r[8], dy[8];
+      float r[8], dy[8], wf[8];
       raw_unpack<F32, 8>(rv[i], r);
       raw_unpack<F32, 8>(yv[i], dy);
+      raw_unpack<F32, 8>(w[i], wf);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         s[0] = fmaf(r[j], r[j], s[0]);
-        s[1] = fmaf(r[j], dy[j] * w[i][j], s[1]);
+        s[1] = fmaf(r[j], dy[j] * wf[j], s[1]);
       }
     }
-    row_reduce<2, false>(s, warps, sm);
+    Raw<F32, 8> r0[NV], y0[NV], g0[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      r0[i] = rv[i];
+      y0[i] = yv[i];
+      g0[i] = gv[i];
+    }
+    if (NV < 4) load(row + step);
+    s[0] = warp_sum(s[0]);
+    s[1] = warp_sum(s[1]);
+    if (warps > 1) {
+      float2* mem = sums[turn] + mine * warps;
+      if ((threadIdx.x & 31) == 0) mem[lane >> 5] = make_float2(s[0], s[1]);
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + mine), "r"(group) : "memory");
+      s[0] = s[1] = 0.f;
+      for (int i = 0; i < warps; ++i) {
+        s[0] += mem[i].x;
+        s[1] += mem[i].y;
+      }
+    }
     const float rstd = 1.f / sqrtf(s[0] / static_cast<float>(p.D) + p.eps);
     const float c = s[1] * rstd / static_cast<float>(p.D);  // mean(p n)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = lane + i * group;
-      float r[8], dy[8], o[8];
-      raw_unpack<F32, 8>(rv[i], r);
-      raw_unpack<F32, 8>(yv[i], dy);
-      raw_unpack<F32, 8>(gv[i], o);
+      float r[8], dy[8], wf[8], o[8];
+      raw_unpack<F32, 8>(r0[i], r);
+      raw_unpack<F32, 8>(y0[i], dy);
+      raw_unpack<F32, 8>(w[i], wf);
+      raw_unpack<F32, 8>(g0[i], o);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float nj = r[j] * rstd;
-        o[j] += rstd * (w[i][j] * dy[j] - nj * c);
+        o[j] += rstd * (wf[j] * dy[j] - nj * c);
         dw[i][j] = fmaf(dy[j], nj, dw[i][j]);
       }
       if (v < vecs && in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
         store_vec<F32, 8>(static_cast<T*>(p.dx) + at + 8 * v, o);
     }
+    if (NV == 4) load(row + step);
   }
   if (p.part == nullptr) return;
+  if constexpr (NV == 4) {  // (one group)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = lane + i * group;
+      const size_t at = static_cast<size_t>(blockIdx.x) * D + 8 * v;
+      if (v < vecs && in_range(p.status, at, 8, static_cast<size_t>(p.nparts) * D, CHK_NORM2_PARAM))
+        store_vec<true, 8>(p.part + at, dw[i]);
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = lane + i * group;
-    const size_t at = static_cast<size_t>(part) * D + 8 * v;
-    if (v < vecs && in_range(p.status, at, 8, static_cast<size_t>(p.nparts) * D, CHK_NORM2_PARAM))
-      store_vec<true, 8>(p.part + at, dw[i]);
+    if (v < vecs) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) share[NV == 4 ? 0 : mine * p.D + 8 * v + j] = dw[i][j];
+    }
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < p.D; d += CTA) {
+    float s = 0.f;
+    for (int g = 0; g < groups; ++g) s += share[NV == 4 ? 0 : g * p.D + d];
+    const size_t at = static_cast<size_t>(blockIdx.x) * D + d;
+    if (in_range(p.status, at, 1, static_cast<size_t>(p.nparts) * D, CHK_NORM2_PARAM)) p.part[at] = s;
   }
 }
 
@@ -306,17 +378,24 @@ cudaError_t launch_fwd_t(const Norm2Params& p, int sms, cudaStream_t st) {
 
 template <bool F32, int NV>
 cudaError_t launch_bwd_nv(const Norm2Params& p, int warps, cudaStream_t st) {
-  const int per = warps == 1 ? 4 : 1;
-  const int grid = (p.nparts + per - 1) / per, threads = warps == 1 ? 128 : 32 * warps;
-  add_norm_bwd_kernel<F32, NV><<<grid, threads, 0, st>>>(p, warps);
+  add_norm_bwd_kernel<F32, NV><<<p.nparts, NV == 4 ? 512 : 256, 0, st>>>(p, warps);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.part == nullptr) return e;
   const SumOut o = {{p.dw, nullptr, nullptr}, {p.D, 0, 0}};
   return launch_sum_parts(p.part, p.nparts, o, p.status, CHK_NORM2_PARAM, st);
 }
+// Two vectors per thread (the next row's are in flight beside them), four only where 16 warps
+// would not hold the row otherwise.
+RowPlan bwd_plan(int D) {
+  const int vecs = D / 8;
+  int warps = 1;
+  while (warps < 8 && warps * 64 < vecs) warps *= 2;
+  if (warps * 64 < vecs) return {4, 16};
+  return {vecs <= warps * 32 ? 1 : 2, warps};
+}
 template <bool F32>
 cudaError_t launch_bwd_t(const Norm2Params& p, cudaStream_t st) {
-  const RowPlan r = row_plan(p.D, 4);
+  const RowPlan r = bwd_plan(p.D);
   return r.nv == 1 ? launch_bwd_nv<F32, 1>(p, r.warps, st)
          : r.nv == 2 ? launch_bwd_nv<F32, 2>(p, r.warps, st)
                      : launch_bwd_nv<F32, 4>(p, r.warps, st);
@@ -324,11 +403,13 @@ cudaError_t launch_bwd_t(const Norm2Params& p, cudaStream_t st) {
 
 }  // namespace
 
-// Groups of the backward kernel: as many as are resident on 152 SMs, and a row each at least.
+// CTAs of the backward kernel: two to each of 152 SMs (one of the 512-thread ones), and a
+// row for each group at least.
 int add_norm_bwd_parts(const m2rnn_norm_shape* s) {
-  const RowPlan r = row_plan(s->D, 4);
-  const long long most = 152LL * 16 / r.warps;
-  return static_cast<int>(s->M < most ? s->M : most);
+  const RowPlan r = bwd_plan(s->D);
+  const int groups = (r.nv == 4 ? 16 : 8) / r.warps;
+  const long long most = r.nv == 4 ? 152 : 304, need = (s->M + groups - 1) / groups;
+  return static_cast<int>(need < most ? need : most);
 }
 
 cudaError_t launch_add_norm(const Norm2Params& p, bool f32, int sms, cudaStream_t st) {

@@ -226,25 +226,27 @@ cudaError_t launch_t(const FewParams& p, cudaStream_t st) {
                      : launch_nt<EPI, E4M3, F32, 8>(p, st);
 }
 
-__global__ void __launch_bounds__(256) split_kernel(SplitParams p) {
+// A row to 64 threads (of D = 520, one vector each); blockIdx.y: the matrix.
+__global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ SplitParams p) {
   let_next_begin();
   const int which = blockIdx.y, vecs = p.D / 8;
-  const long long total = p.M[which] * vecs;
-  const size_t plane = static_cast<size_t>(p.M[which]) * p.pitch;
-  const size_t extent = static_cast<size_t>(p.M[which] - 1) * p.row[which] + p.D;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
-    const long long r = i / vecs;
-    const int v = static_cast<int>(i - r * vecs);
-    const size_t src = static_cast<size_t>(r) * p.row[which] + 8 * v, at = static_cast<size_t>(r) * p.pitch + 8 * v;
-    if (!in_range(p.status, src, 8, extent, CHK_GLU_IN)) continue;
-    const Raw<true, 8> x = raw_load<true, 8>(p.src[which] + src);
-    uint32_t t[3][4];
-    split8(x.w, t);
+  const float* src = which == 0 ? p.src[0] : which == 1 ? p.src[1] : p.src[2];
+  __nv_bfloat16* dst = which == 0 ? p.dst[0] : which == 1 ? p.dst[1] : p.dst[2];
+  const long long M = which == 0 ? p.M[0] : which == 1 ? p.M[1] : p.M[2];
+  const long long from = which == 0 ? p.row[0] : which == 1 ? p.row[1] : p.row[2];
+  const size_t plane = static_cast<size_t>(M) * p.pitch, extent = static_cast<size_t>(M - 1) * from + p.D;
+  for (long long r = blockIdx.x * 4LL + (threadIdx.x >> 6); r < M; r += gridDim.x * 4LL)
+    for (int v = threadIdx.x & 63; v < vecs; v += 64) {
+      const size_t at = static_cast<size_t>(r) * from + 8 * v, to = static_cast<size_t>(r) * p.pitch + 8 * v;
+      if (!in_range(p.status, at, 8, extent, CHK_GLU_IN)) continue;
+      const Raw<true, 8> x = raw_load<true, 8>(src + at);
+      uint32_t t[3][4];
+      split8(x.w, t);
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
-      if (in_range(p.status, k * plane + at, 8, 3 * plane, CHK_GLU_WS))
-        *reinterpret_cast<uint4*>(p.dst[which] + k * plane + at) = make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
-  }
+      for (int k = 0; k < 3; ++k)
+        if (in_range(p.status, k * plane + to, 8, 3 * plane, CHK_GLU_WS))
+          *reinterpret_cast<uint4*>(dst + k * plane + to) = make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
+    }
 }
 
 }  // namespace
@@ -256,7 +258,7 @@ cudaError_t launch_few(const FewParams& p, int epi, bool e4m3, bool f32, cudaStr
 }
 
 cudaError_t launch_split(const SplitParams& p, cudaStream_t st) {
-  split_kernel<<<dim3(608, p.n), 256, 0, st>>>(p);
+  split_kernel<<<dim3(912, p.n), 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 

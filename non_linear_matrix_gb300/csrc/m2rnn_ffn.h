@@ -101,7 +101,10 @@ struct FewParams {
   int M, D, F, act;
   int* status;
 };
-constexpr int kFewMost = 64;
+// Up to 16 tokens (fp32: 64) go this way.  us at D=2048 F=5632, gated products, bf16: 8 tokens
+// 10.0 against 17.9 of the tiles, 16 tokens 12.1 against 18.6, 32 tokens 28 against 11.7; e4m3: 16 tokens
+// 9.3 against 10.9, 32 16.1 against 10.5; fp32 at D=1024 F=2816: 32 tokens 20 against 33, 64 30 against 34.
+inline int few_most(bool f32) { return f32 ? 64 : 16; }
 cudaError_t launch_few(const FewParams& p, int epi, bool e4m3, bool f32, cudaStream_t st);
 
 // fp32 matrices into three bf16 terms [3][M][pitch] each.

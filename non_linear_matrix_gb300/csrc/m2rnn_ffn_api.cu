@@ -346,7 +346,7 @@ int m2rnn_quant_rows(const m2rnn_norm_shape* s, const void* x, long long x_row, 
 }
 
 size_t m2rnn_glu_fwd_workspace_size(const m2rnn_glu_shape* s) {
-  if (check_glu(s, false) != M2RNN_OK || s->M <= m2rnn::kFewMost) return 0;
+  if (check_glu(s, false) != M2RNN_OK || s->M <= m2rnn::few_most(s->in_dtype == M2RNN_F32)) return 0;
   return terms_bytes(s);
 }
 
@@ -366,7 +366,7 @@ int m2rnn_glu_fwd(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
   const void* req[] = {x, wg, wu, h};
   if ((rc = check(req, dev, true)) != M2RNN_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (s->M <= m2rnn::kFewMost) {
+  if (s->M <= m2rnn::few_most(s->in_dtype == M2RNN_F32)) {
     m2rnn::FewParams p{};
     p.x = x;
     p.x_row = x_row;
@@ -496,7 +496,7 @@ int product_q8(const m2rnn_glu_shape* s, const void* x, long long x_row, const f
   if ((rc = host_check_ptr(res, dev, false)) != M2RNN_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int epi = pair ? m2rnn::EPI_GLU8 : m2rnn::EPI_LIN8;
-  if (s->M <= m2rnn::kFewMost) {
+  if (s->M <= m2rnn::few_most(false)) {
     m2rnn::FewParams p{};
     p.x = x;
     p.x_row = x_row;

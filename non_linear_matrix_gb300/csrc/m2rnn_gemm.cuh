@@ -38,8 +38,10 @@ struct GemmCfg {
   static constexpr int TERMS = F32 ? 3 : 1;
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BR * 128;  // of a term
   static constexpr int STAGE = TERMS * (A_BYTES + B_BYTES);
-  static constexpr int STAGES = 220 * 1024 / STAGE;  // (6 of 32 KB, 3 of 72 KB)
-  static constexpr int SMEM = STAGES * STAGE + 1024;
+  static constexpr int STAGES = 216 * 1024 / STAGE;  // (6 of 32 KB, 3 of 72 KB)
+  // bf16 outputs and what they read pass through 2 KB of each output warp
+  static constexpr int STAGED = F32 ? 0 : 2048;
+  static constexpr int SMEM = STAGES * STAGE + 1024 + 8 * STAGED;
   static constexpr int ACC = F32 ? 2 * BN : BN;  // columns of a set of accumulators
   static constexpr int TCOLS = 2 * ACC;
   static constexpr int OUT_WARPS = 8, THREADS = 32 * (OUT_WARPS + 2);
@@ -167,76 +169,176 @@ __device__ __forceinline__ void next_term(float (&v)[32], float (&t)[32]) {
   }
 }
 
-// One row's 32 columns from their accumulators (g, u: the pair, or the product in g).
-template <class C>
-__device__ __forceinline__ void finish32(const GemmParams& p, const TileAt& t, long long row, int col, float (&g)[32],
-                                         float (&u)[32]) {
-  const int cols = min(32, p.N - col);
-  if (row >= p.M || cols <= 0) return;
-  if (C::EPI == EPI_STORE && t.part >= 0) {  // fp32 sums of a part: [part][rows of a tile][BN]
-    const size_t tile = static_cast<size_t>(C::BM) * C::BN;
-    const size_t at = t.part * tile + static_cast<size_t>(row - static_cast<long long>(t.m) * C::BM) * C::BN +
-                      (col - t.n * C::BN);
-    store32<true>(p.parts, at, 32, g, tile * p.nparts, p.status, CHK_GLU_WS);
-    return;
+// A warp's block of 32 rows of 32 bf16 columns on its way between memory, where four lanes
+// hold a row's 64 bytes (eight rows to an instruction), and a row per lane.  In the warp's 2 KB
+// the 16-byte pieces of a row are exchanged by its number, so that neither side has
+// bank conflicts.
+__device__ __forceinline__ uint32_t piece_at(uint32_t buf, int row, int piece) {
+  return buf + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+struct Block {  // rows and columns of the matrix that the block covers, from `at` on
+  size_t at, row;
+  long long rows;
+  int cols;
+  size_t extent;
+};
+__device__ __forceinline__ void block_load(uint4 (&v)[4], const __nv_bfloat16* src, const Block& k, int lane,
+                                           int* status) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2), c = lane & 3;
+    const size_t at = k.at + r * k.row + 8 * c;
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < k.rows && 8 * c < k.cols && in_range(status, at, 8, k.extent, CHK_GLU_IN))
+      v[i] = *reinterpret_cast<const uint4*>(src + at);
   }
-  const size_t at = static_cast<size_t>(row) * p.N + col, extent = static_cast<size_t>(p.M) * p.N;
+}
+// What block_load took, as the lane's row.
+__device__ __forceinline__ void block_rows(const uint4 (&v)[4], uint32_t buf, int lane, float (&o)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sts128(piece_at(buf, 8 * i + (lane >> 2), lane & 3), v[i]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 u = ptx::lds_u32x4(piece_at(buf, lane, i));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      o[8 * i + 2 * j] = ptx::bf16x2_lo(w[j]);
+      o[8 * i + 2 * j + 1] = ptx::bf16x2_hi(w[j]);
+    }
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void block_store(__nv_bfloat16* dst, const Block& k, uint32_t buf, int lane,
+                                            const float (&o)[32], int* status, int site) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    sts128(piece_at(buf, lane, i),
+           make_uint4(ptx::pack_bf16x2(o[8 * i], o[8 * i + 1]), ptx::pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                      ptx::pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), ptx::pack_bf16x2(o[8 * i + 6], o[8 * i + 7])));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2), c = lane & 3;
+    const size_t at = k.at + r * k.row + 8 * c;
+    const uint4 u = ptx::lds_u32x4(piece_at(buf, r, c));
+    if (r < k.rows && 8 * c < k.cols && in_range(status, at, 8, k.extent, site))
+      *reinterpret_cast<uint4*>(dst + at) = u;
+  }
+  __syncwarp();
+}
+
+// fp32 sums of a part of a tile: [part][rows of a tile][BN].
+template <class C>
+__device__ __forceinline__ void store_part(const GemmParams& p, const TileAt& t, long long row, int col,
+                                           const float (&g)[32]) {
+  if (row >= p.M || col >= p.N) return;
+  const size_t tile = static_cast<size_t>(C::BM) * C::BN;
+  const size_t at = t.part * tile + static_cast<size_t>(row - static_cast<long long>(t.m) * C::BM) * C::BN +
+                    (col - t.n * C::BN);
+  store32<true>(p.parts, at, 32, g, tile * p.nparts, p.status, CHK_GLU_WS);
+}
+
+// Where the output's block of a warp's 32 rows from row0 on lies, with `pitch` elements to a row.
+__device__ __forceinline__ Block block_of(const GemmParams& p, long long row0, int col, long long pitch) {
+  Block k;
+  k.row = static_cast<size_t>(pitch);
+  k.at = static_cast<size_t>(row0) * k.row + col;
+  k.rows = p.M - row0;
+  k.cols = min(32, p.N - col);
+  k.extent = static_cast<size_t>(p.M - 1) * k.row + p.N;
+  return k;
+}
+
+// A block's outputs from its accumulators (g, u: the pair, or the product in g); `in`: what
+// block_load took of dh or res.
+template <class C>
+__device__ __forceinline__ void finish_bf16(const GemmParams& p, const TileAt& t, long long row0, int col, int lane,
+                                            uint32_t buf, float (&g)[32], float (&u)[32], const uint4 (&in)[4]) {
+  const Block k = block_of(p, row0, col, C::EPI == EPI_DGLU ? p.pitch : p.N);
   if constexpr (C::EPI == EPI_GLU) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) g[i] = act_of<C::F32>(g[i], p.act) * u[i];
-    store32<C::F32>(p.out[0], at, cols, g, extent, p.status, CHK_GLU_OUT);
+    for (int i = 0; i < 32; ++i) g[i] = act_of<false>(g[i], p.act) * u[i];
+    block_store(static_cast<__nv_bfloat16*>(p.out[0]), k, buf, lane, g, p.status, CHK_GLU_OUT);
   } else if constexpr (C::EPI == EPI_DGLU) {
     float d[32];
-    load32<C::F32>(p.in, at, cols, d, extent, p.status, CHK_GLU_IN);
+    block_rows(in, buf, lane, d);
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       float a, s;
-      act_grad<C::F32>(g[i], p.act, a, s);
+      act_grad<false>(g[i], p.act, a, s);
       g[i] = d[i] * u[i] * s;
       u[i] = d[i] * a;
     }
-    // Rounded to bf16 (bf16 inputs): they are operands of the products to come.  fp32 inputs:
-    // three terms, which hold the value.
-    constexpr int terms = C::F32 ? 3 : 1;
+    // Rounded to bf16: they are operands of the products to come.
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out[0]);
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-#pragma unroll
-      for (int k = 0; k < terms; ++k) {
-        const size_t plane = static_cast<size_t>(which * terms + k) * p.M * p.pitch;
-        if constexpr (C::F32)
-          next_term(which ? u : g, d);
-        else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) d[i] = which ? u[i] : g[i];
-        }
-        store32<false>(out, plane + static_cast<size_t>(row) * p.pitch + col, cols, d,
-                       2 * terms * static_cast<size_t>(p.M) * p.pitch, p.status, CHK_GLU_WS);
-      }
-    }
+    block_store(out, k, buf, lane, g, p.status, CHK_GLU_WS);
+    block_store(out + static_cast<size_t>(p.M) * p.pitch, k, buf, lane, u, p.status, CHK_GLU_WS);
   } else if constexpr (C::EPI == EPI_STORE) {
-    store32<C::F32>(t.batch ? p.out[1] : p.out[0], at, cols, g, extent, p.status, CHK_GLU_OUT);
+    if (t.part >= 0)
+      store_part<C>(p, t, row0 + lane, col, g);
+    else
+      block_store(static_cast<__nv_bfloat16*>(t.batch ? p.out[1] : p.out[0]), k, buf, lane, g, p.status, CHK_GLU_OUT);
   } else {
-    const float sa = __ldg(p.sa + row);
+    const float sa = lane < k.rows ? __ldg(p.sa + row0 + lane) : 0.f;
     const size_t n = static_cast<size_t>(p.N);
-    float s0[32];
-    load32_const(p.sb0, col, cols, s0, n, p.status);
+    float s[32];
+    load32_const(p.sb0, col, k.cols, s, n, p.status);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) g[i] *= sa * s[i];
     if constexpr (C::EPI == EPI_GLU8) {
-      float s1[32];
-      load32_const(p.sb1, col, cols, s1, n, p.status);
+      load32_const(p.sb1, col, k.cols, s, n, p.status);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) g[i] = act_of<false>(g[i] * (sa * s0[i]), p.act) * (u[i] * (sa * s1[i]));
-    } else {
+      for (int i = 0; i < 32; ++i) g[i] = act_of<false>(g[i], p.act) * (u[i] * (sa * s[i]));
+    } else if (p.in != nullptr) {
+      block_rows(in, buf, lane, s);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) g[i] *= sa * s0[i];
-      if (p.in != nullptr) {
-        load32<false>(p.in, static_cast<size_t>(row) * p.in_row + col, cols, u,
-                      static_cast<size_t>(p.M - 1) * p.in_row + n, p.status, CHK_GLU_IN);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) g[i] += u[i];
-      }
+      for (int i = 0; i < 32; ++i) g[i] += s[i];
     }
-    store32<false>(p.out[0], at, cols, g, extent, p.status, CHK_GLU_OUT);
+    block_store(static_cast<__nv_bfloat16*>(p.out[0]), k, buf, lane, g, p.status, CHK_GLU_OUT);
+  }
+}
+
+// fp32: one row's 32 columns.
+template <class C>
+__device__ __forceinline__ void finish_f32(const GemmParams& p, const TileAt& t, long long row, int col, float (&g)[32],
+                                           float (&u)[32]) {
+  const int cols = min(32, p.N - col);
+  if (row >= p.M || cols <= 0) return;
+  const size_t at = static_cast<size_t>(row) * p.N + col, extent = static_cast<size_t>(p.M) * p.N;
+  if constexpr (C::EPI == EPI_GLU) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) g[i] = act_of<true>(g[i], p.act) * u[i];
+    store32<true>(p.out[0], at, cols, g, extent, p.status, CHK_GLU_OUT);
+  } else if constexpr (C::EPI == EPI_DGLU) {
+    float d[32];
+    load32<true>(p.in, at, cols, d, extent, p.status, CHK_GLU_IN);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      float a, s;
+      act_grad<true>(g[i], p.act, a, s);
+      g[i] = d[i] * u[i] * s;
+      u[i] = d[i] * a;
+    }
+    // as the three terms that the products to come take
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out[0]);
+    const size_t plane = static_cast<size_t>(p.M) * p.pitch, to = static_cast<size_t>(row) * p.pitch + col;
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        next_term(which ? u : g, d);
+        store32<false>(out, (which * 3 + k) * plane + to, cols, d, 6 * plane, p.status, CHK_GLU_WS);
+      }
+  } else {
+    if (t.part >= 0)
+      store_part<C>(p, t, row, col, g);
+    else
+      store32<true>(t.batch ? p.out[1] : p.out[0], at, cols, g, extent, p.status, CHK_GLU_OUT);
   }
 }
 
@@ -381,7 +483,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
     bool ok = true;
     for (int t = first; t < tiles && ok; t += stride) {
       const TileAt at = tile_at(p, t);
-      const long long row = static_cast<long long>(at.m) * C::BM + rank * 128 + (warp & 3) * 32 + lane;
+      const long long row0 = static_cast<long long>(at.m) * C::BM + rank * 128 + (warp & 3) * 32;
       const int col0 = at.n * C::OUT_N;
       if constexpr (C::F32) {
         float sum[C::PAIR ? 2 : 1][C::BLOCKS][32];
@@ -409,10 +511,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
         if (ok) {
 #pragma unroll
           for (int b = 0; b < C::BLOCKS; ++b)
-            finish32<C>(p, at, row, col0 + 32 * (half + b), sum[0][b], sum[C::PAIR ? 1 : 0][b]);
+            finish_f32<C>(p, at, row0 + lane, col0 + 32 * (half + b), sum[0][b], sum[C::PAIR ? 1 : 0][b]);
         }
       } else {
         const int ab = acc & 1;
+        const uint32_t buf = base + C::STAGES * C::STAGE + warp * C::STAGED;
+        const bool reads = C::EPI == EPI_DGLU || (C::EPI == EPI_LIN8 && p.in != nullptr);
+        const long long in_row = C::EPI == EPI_DGLU ? p.N : p.in_row;
+        const __nv_bfloat16* in = static_cast<const __nv_bfloat16*>(p.in);
+        uint4 next[4];  // of dh or res: in flight while the accumulators are waited for
+        if (reads) block_load(next, in, block_of(p, row0, col0 + 32 * half, in_row), lane, p.status);
         ok = ptx::mbar_wait(tfull + 8 * ab, (acc >> 1) & 1, p.limit_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
@@ -421,13 +529,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
 #pragma unroll 1
           for (int b = 0; b < C::BLOCKS; ++b) {
             float g[32], u[32];
+            uint4 now[4];
+            const int col = col0 + 32 * (half + b);
             __syncwarp();
             tc5::ld32(ta + 32 * b, g);
             if constexpr (C::PAIR) tc5::ld32(ta + C::OUT_N + 32 * b, u);
+            if (reads) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) now[i] = next[i];
+              if (b + 1 < C::BLOCKS) block_load(next, in, block_of(p, row0, col + 32, in_row), lane, p.status);
+            }
             tc5::wait_ld(g);
             if constexpr (C::PAIR) tc5::wait_ld(u);
             if (b == C::BLOCKS - 1) release(ab);
-            finish32<C>(p, at, row, col0 + 32 * (half + b), g, u);
+            finish_bf16<C>(p, at, row0, col, lane, buf, g, u, now);
           }
         }
         ++acc;
