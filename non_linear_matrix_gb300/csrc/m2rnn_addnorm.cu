@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(512) add_norm_kernel(Norm2Params p, int warps,
 // The quantiser: a CTA per row, whose threads keep four vectors each; what is behind those is
 // read a second time.
 template <bool F32>
-__global__ void __launch_bounds__(256) quant_rows_kernel(Norm2Params p) {
+__global__ void __launch_bounds__(256, F32 ? 4 : 5) quant_rows_kernel(Norm2Params p) {
   using T = typename Elem<F32>::T;
   constexpr int NV = 4;
   __shared__ float sm[32];
@@ -204,15 +204,26 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(Norm2Params p) {
 
 // Backward: with n = r rstd, p = w dy:  dx = dr + rstd (p - n mean(p n)),  dw = sum dy n.
 // A CTA holds several groups of warps, each of which walks over rows with its share of dw in
-// registers and the next row's loads in flight.  The groups' shares are added in order, then
-// the CTAs' by sum_parts.
+// registers.  A thread copies its vectors of the next S rows into its own places of shared
+// memory (asynchronously, so they take no registers while they are in flight: 96 KB to a
+// CTA), and reads them twice, for the two sums and for dx.  The groups' shares of dw are
+// added in order, then the CTAs' by sum_parts.  M=32768 D=2048: 111 us with the next row in
+// registers.
 template <bool F32, int NV>
-__global__ void __launch_bounds__(NV == 4 ? 512 : 256, NV == 4 || (F32 && NV == 2) ? 1 : 2)
-    add_norm_bwd_kernel(Norm2Params p, int warps) {
+struct BwdCfg {
+  static constexpr int CTA = NV == 4 ? 512 : 256;
+  static constexpr int U = F32 ? 2 : 1;  // 16-byte units of a vector
+  static constexpr int S = NV == 4 ? (F32 ? 1 : 2) : NV * U == 4 ? 2 : 4;
+  static constexpr int SMEM = S * 3 * NV * U * CTA * 16;
+};
+
+template <bool F32, int NV>
+__global__ void __launch_bounds__(BwdCfg<F32, NV>::CTA, NV == 4 ? 1 : 2) add_norm_bwd_kernel(Norm2Params p, int warps) {
   using T = typename Elem<F32>::T;
-  constexpr int CTA = NV == 4 ? 512 : 256;
+  using C = BwdCfg<F32, NV>;
+  constexpr int CTA = C::CTA, U = C::U, S = C::S;
+  extern __shared__ __align__(16) uint8_t ring[];  // [S][3][NV][U][CTA] 16-byte units, then [groups][D]
   __shared__ float2 sums[2][CTA / 32];
-  __shared__ float share[NV == 4 ? 1 : CTA * NV * 8];  // [groups][D]
   const int group = warps * 32, vecs = p.D / 8, groups = CTA / group;
   const int lane = threadIdx.x % group, mine = threadIdx.x / group;
   let_next_begin();
@@ -233,34 +244,56 @@ __global__ void __launch_bounds__(NV == 4 ? 512 : 256, NV == 4 || (F32 && NV == 
     if (p.w != nullptr && v < vecs && in_range(p.status, 8 * v, 8, D, CHK_NORM2_PARAM))
       w[i] = raw_load<F32, 8>(static_cast<const T*>(p.w) + 8 * v);
   }
-  Raw<F32, 8> rv[NV], yv[NV], gv[NV];
-  const auto load = [&](long long row) {
+  const uint32_t base = ptx::smem_addr(ring) + threadIdx.x * 16;
+  const auto place = [&](int slot, int which, int i) { return base + ((slot * 3 + which) * NV + i) * U * CTA * 16; };
+  const auto fetch = [&](int slot, long long row) {
     const size_t at = static_cast<size_t>(row) * D, r0 = static_cast<size_t>(row) * p.x_row;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = lane + i * group;
-      rv[i] = yv[i] = gv[i] = raw_zero<F32, 8>();
       if (v < vecs && row < p.M) {
-        if (in_range(p.status, r0 + 8 * v, 8, r_ext, CHK_NORM2_IN))
-          rv[i] = raw_load<F32, 8>(static_cast<const T*>(p.x) + r0 + 8 * v);
-        if (in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_IN)) {
-          yv[i] = raw_load<F32, 8, false>(static_cast<const T*>(p.dy) + at + 8 * v);
-          if (p.dr != nullptr) gv[i] = raw_load<F32, 8, false>(static_cast<const T*>(p.dr) + at + 8 * v);
+        const bool r_in = in_range(p.status, r0 + 8 * v, 8, r_ext, CHK_NORM2_IN);
+        const bool in = in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_IN);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          constexpr int E = 16 / sizeof(T);
+          if (r_in) ptx::cp_async16(place(slot, 0, i) + u * CTA * 16, static_cast<const T*>(p.x) + r0 + 8 * v + u * E);
+          if (in) ptx::cp_async16(place(slot, 1, i) + u * CTA * 16, static_cast<const T*>(p.dy) + at + 8 * v + u * E);
+          if (in && p.dr != nullptr)
+            ptx::cp_async16(place(slot, 2, i) + u * CTA * 16, static_cast<const T*>(p.dr) + at + 8 * v + u * E);
         }
       }
     }
+    ptx::cp_async_commit();
+  };
+  const auto read = [&](int slot, int which, int i, float (&o)[8]) {
+    Raw<F32, 8> r = raw_zero<F32, 8>();
+    if (lane + i * group < vecs) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint4 q = ptx::lds_u32x4(place(slot, which, i) + u * CTA * 16);
+        r.w[4 * u] = q.x;
+        r.w[4 * u + 1] = q.y;
+        r.w[4 * u + 2] = q.z;
+        r.w[4 * u + 3] = q.w;
+      }
+    }
+    raw_unpack<F32, 8>(r, o);
   };
   const long long step = static_cast<long long>(gridDim.x) * groups;
   long long row = static_cast<long long>(blockIdx.x) * groups + mine;
-  load(row);
+#pragma unroll
+  for (int k = 0; k < S; ++k) fetch(k, row + k * step);
+  int slot = 0;
   for (int turn = 0; row < p.M; row += step, turn ^= 1) {  // (the same count in all warps of a group)
     const size_t at = static_cast<size_t>(row) * D;
+    ptx::cp_async_wait<S - 1>();
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float r[8], dy[8], wf[8];
-      raw_unpack<F32, 8>(rv[i], r);
-      raw_unpack<F32, 8>(yv[i], dy);
+      read(slot, 0, i, r);
+      read(slot, 1, i, dy);
       raw_unpack<F32, 8>(w[i], wf);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -268,14 +301,6 @@ __global__ void __launch_bounds__(NV == 4 ? 512 : 256, NV == 4 || (F32 && NV == 
         s[1] = fmaf(r[j], dy[j] * wf[j], s[1]);
       }
     }
-    Raw<F32, 8> r0[NV], y0[NV], g0[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      r0[i] = rv[i];
-      y0[i] = yv[i];
-      g0[i] = gv[i];
-    }
-    if (NV < 4) load(row + step);
     s[0] = warp_sum(s[0]);
     s[1] = warp_sum(s[1]);
     if (warps > 1) {
@@ -294,10 +319,12 @@ __global__ void __launch_bounds__(NV == 4 ? 512 : 256, NV == 4 || (F32 && NV == 
     for (int i = 0; i < NV; ++i) {
       const int v = lane + i * group;
       float r[8], dy[8], wf[8], o[8];
-      raw_unpack<F32, 8>(r0[i], r);
-      raw_unpack<F32, 8>(y0[i], dy);
+      read(slot, 0, i, r);
+      read(slot, 1, i, dy);
       raw_unpack<F32, 8>(w[i], wf);
-      raw_unpack<F32, 8>(g0[i], o);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = 0.f;
+      if (p.dr != nullptr) read(slot, 2, i, o);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float nj = r[j] * rstd;
@@ -307,8 +334,10 @@ __global__ void __launch_bounds__(NV == 4 ? 512 : 256, NV == 4 || (F32 && NV == 
       if (v < vecs && in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
         store_vec<F32, 8>(static_cast<T*>(p.dx) + at + 8 * v, o);
     }
-    if (NV == 4) load(row + step);
+    fetch(slot, row + S * step);  // (the thread has read its places)
+    slot = slot + 1 == S ? 0 : slot + 1;
   }
+  ptx::cp_async_wait_all();
   if (p.part == nullptr) return;
   if constexpr (NV == 4) {  // (one group)
 #pragma unroll
@@ -320,18 +349,20 @@ __global__ void __launch_bounds__(NV == 4 ? 512 : 256, NV == 4 || (F32 && NV == 
     }
     return;
   }
+  float* share = reinterpret_cast<float*>(ring);
+  __syncthreads();  // (the rows in the ring have been read)
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = lane + i * group;
     if (v < vecs) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) share[NV == 4 ? 0 : mine * p.D + 8 * v + j] = dw[i][j];
+      for (int j = 0; j < 8; ++j) share[mine * p.D + 8 * v + j] = dw[i][j];
     }
   }
   __syncthreads();
   for (int d = threadIdx.x; d < p.D; d += CTA) {
     float s = 0.f;
-    for (int g = 0; g < groups; ++g) s += share[NV == 4 ? 0 : g * p.D + d];
+    for (int g = 0; g < groups; ++g) s += share[g * p.D + d];
     const size_t at = static_cast<size_t>(blockIdx.x) * D + d;
     if (in_range(p.status, at, 1, static_cast<size_t>(p.nparts) * D, CHK_NORM2_PARAM)) p.part[at] = s;
   }
@@ -378,8 +409,18 @@ cudaError_t launch_fwd_t(const Norm2Params& p, int sms, cudaStream_t st) {
 
 template <bool F32, int NV>
 cudaError_t launch_bwd_nv(const Norm2Params& p, int warps, cudaStream_t st) {
-  add_norm_bwd_kernel<F32, NV><<<p.nparts, NV == 4 ? 512 : 256, 0, st>>>(p, warps);
-  cudaError_t e = cudaGetLastError();
+  using C = BwdCfg<F32, NV>;
+  static bool ready[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev]) {
+    e = cudaFuncSetAttribute(add_norm_bwd_kernel<F32, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev] = true;
+  }
+  add_norm_bwd_kernel<F32, NV><<<p.nparts, C::CTA, C::SMEM, st>>>(p, warps);
+  e = cudaGetLastError();
   if (e != cudaSuccess || p.part == nullptr) return e;
   const SumOut o = {{p.dw, nullptr, nullptr}, {p.D, 0, 0}};
   return launch_sum_parts(p.part, p.nparts, o, p.status, CHK_NORM2_PARAM, st);

@@ -923,20 +923,26 @@ def _token_rows(name: str, t):
     return M, D if row is None else row
 
 
-def _bf16_or_f32(name: str, t):
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, not {t.dtype}")
+def _like(t, x, name: str):
+    """An output of x's shape and dtype."""
+    if t is not None:
+        _expect(name, t, x.shape, x.dtype)
+        return t
+    if x.is_contiguous():
+        return torch.empty_like(x)  # (cheaper than by shape)
+    return torch.empty(x.shape, device=x.device, dtype=x.dtype)
 
 
 def _norm_args(x, res, w):
-    _bf16_or_f32("x", x)
-    M, x_row = _token_rows("x", x)
+    code, (M, x_row) = _dtype_code(x), _token_rows("x", x)
     D, res_row = x.shape[-1], 0
     if res is not None:
-        _expect("res", res, x.shape, x.dtype)
+        if res.dtype is not x.dtype or res.shape != x.shape:
+            _expect("res", res, x.shape, x.dtype)
         res_row = _token_rows("res", res)[1]
-    _expect_all(x.dtype, ("w", w, (D,)))
-    return NormShape(M, D, _dtype_code(x)), x_row, res_row
+    if w is not None and (w.dtype is not x.dtype or w.shape != (D,)):
+        _expect("w", w, (D,), x.dtype)
+    return NormShape(M, D, code), x_row, res_row
 
 
 @_on_stream
@@ -948,12 +954,11 @@ def add_norm_fwd(x, res=None, w=None, eps: float = 1e-6, *, out=None, stream=Non
     or f32).  ``out`` may supply y and r; r may be ``res`` or x itself (in place)."""
     s, x_row, res_row = _norm_args(x, res, w)
     y, r = _given(out, "y", "r")
-    y = _out(y, x.shape, x.dtype, x.device, "y")
-    if res is None:
-        if r is not None:
-            raise ValueError("r goes with res")
-    else:
-        r = _out(r, x.shape, x.dtype, x.device, "r")
+    y = _like(y, x, "y")
+    if res is not None:
+        r = _like(r, x, "r")
+    elif r is not None:
+        raise ValueError("r goes with res")
     rc = lib().m2rnn_add_norm_fwd(ctypes.byref(s), _at(x), x_row, _at(res), res_row, _addr(w), eps,
                                   _addr(r), _addr(y), _stream_of(stream, x))
     _check(rc, "m2rnn_add_norm_fwd")
@@ -968,11 +973,10 @@ def add_norm_q8(x, res=None, w=None, eps: float = 1e-6, *, out=None, stream=None
     q, scale, r = _given(out, "q", "scale", "r")
     q = _out(q, x.shape, torch.float8_e4m3fn, x.device, "q")
     scale = _out(scale, x.shape[:-1], torch.float32, x.device, "scale")
-    if res is None:
-        if r is not None:
-            raise ValueError("r goes with res")
-    else:
-        r = _out(r, x.shape, x.dtype, x.device, "r")
+    if res is not None:
+        r = _like(r, x, "r")
+    elif r is not None:
+        raise ValueError("r goes with res")
     rc = lib().m2rnn_add_norm_q8(ctypes.byref(s), _at(x), x_row, _at(res), res_row, _addr(w), eps,
                                  _addr(r), _addr(q), _addr(scale), _stream_of(stream, x))
     _check(rc, "m2rnn_add_norm_q8")
@@ -986,13 +990,12 @@ def add_norm_bwd(r, dy, w=None, dr=None, eps: float = 1e-6, *, want_dw: bool = T
     ``res``): dict(dx, dw).  dy is dL/dy and dr dL/dr past the norm (None = 0), of r's
     dtype; dx (r's dtype) is the gradient of x and of res alike; dw [D] is fp32
     (None without a weight or with want_dw=False).  dx may be dr or dy itself."""
-    _bf16_or_f32("r", r)
-    M, row = _token_rows("r", r)
+    code, (M, row) = _dtype_code(r), _token_rows("r", r)
     D, dev = r.shape[-1], r.device
     _expect_all(r.dtype, ("w", w, (D,)), ("dy", dy, r.shape), ("dr", dr, r.shape))
-    s = NormShape(M, D, _dtype_code(r))
+    s = NormShape(M, D, code)
     dx, dw = _given(out, "dx", "dw")
-    dx = _out(dx, r.shape, r.dtype, dev, "dx")
+    dx = _like(dx, r, "dx")
     dw = _out(dw, (D,), torch.float32, dev, "dw") if w is not None and want_dw else None
     need = int(lib().m2rnn_add_norm_bwd_workspace_size(ctypes.byref(s))) if dw is not None else 0
     ws = _workspace(workspace, need, dev)
@@ -1007,9 +1010,8 @@ def quant_rows(x, *, out=None, stream=None):
     """x [..., D] (bf16 or f32; rows may be evenly spaced slices) in 8 bits with a scale per
     row: (q float8_e4m3fn, scale [...] fp32), scale = max|row| / 448, q the nearest
     code of row / scale.  ``out`` may supply q and scale."""
-    _bf16_or_f32("x", x)
-    M, row = _token_rows("x", x)
-    s = NormShape(M, x.shape[-1], _dtype_code(x))
+    code, (M, row) = _dtype_code(x), _token_rows("x", x)
+    s = NormShape(M, x.shape[-1], code)
     q, scale = _given(out, "q", "scale")
     q = _out(q, x.shape, torch.float8_e4m3fn, x.device, "q")
     scale = _out(scale, x.shape[:-1], torch.float32, x.device, "scale")
@@ -1020,13 +1022,12 @@ def quant_rows(x, *, out=None, stream=None):
 
 
 def _glu_args(x, wg, wu, act):
-    _bf16_or_f32("x", x)
-    M, row = _token_rows("x", x)
+    code, (M, row) = _dtype_code(x), _token_rows("x", x)
     if wg.dim() != 2:
         raise ValueError("wg must be [F,D]")
     F, D = wg.shape[0], x.shape[-1]
     _expect_all(x.dtype, ("wg", wg, (F, D)), ("wu", wu, (F, D)))
-    return GluShape(M, D, F, _dtype_code(x), _act(act)), row
+    return GluShape(M, D, F, code, _act(act)), row
 
 
 @_on_stream
@@ -1037,11 +1038,12 @@ def glu_fwd(x, wg, wu, *, act: str = "silu", workspace=None, out=None, stream=No
     act "silu" or "gelu" (the tanh form).  ``out`` may supply h."""
     s, row = _glu_args(x, wg, wu, act)
     h = _out(_given(out, "h")[0], (*x.shape[:-1], s.F), x.dtype, x.device, "h")
-    need = int(lib().m2rnn_glu_fwd_workspace_size(ctypes.byref(s)))
-    ws = _workspace(workspace, need, x.device) if need or workspace is not None else None
-    rc = lib().m2rnn_glu_fwd(ctypes.byref(s), _at(x), row, _addr(wg), _addr(wu), _addr(h),
-                             _addr(ws), ctypes.c_size_t(0) if ws is None else _nbytes(ws),
-                             _stream_of(stream, x))
+    L, ws = lib(), workspace
+    if ws is None:
+        need = L.m2rnn_glu_fwd_workspace_size(ctypes.byref(s))
+        ws = _workspace(None, need, x.device) if need else None
+    rc = L.m2rnn_glu_fwd(ctypes.byref(s), _at(x), row, _addr(wg), _addr(wu), _addr(h), _addr(ws),
+                         0 if ws is None else _nbytes(ws), _stream_of(stream, x))
     _check(rc, "m2rnn_glu_fwd")
     return h
 
@@ -1073,11 +1075,11 @@ def _q8_args(x, xs, weights):
     if weights[0][0].dim() != 2:
         raise ValueError("weights must be [F,D]")
     F, D = weights[0][0].shape[0], x.shape[-1]
-    _expect("x", x, x.shape, e4m3)
-    _expect("xs", xs, x.shape[:-1], f32)
+    _expect_all(e4m3, ("x", x, x.shape))
+    _expect_all(f32, ("xs", xs, x.shape[:-1]))
     for w, ws in weights:
-        _expect("w", w, (F, D), e4m3)
-        _expect("ws", ws, (F,), f32)
+        _expect_all(e4m3, ("w", w, (F, D)))
+        _expect_all(f32, ("ws", ws, (F,)))
     M, row = _token_rows("x", x)
     return M, row, D, F
 
@@ -1104,11 +1106,14 @@ def linear_q8(x, xs, w, ws, res=None, *, out=None, stream=None):
     itself (in place)."""
     M, row, D, F = _q8_args(x, xs, ((w, ws),))
     res_row = 0
+    y = _given(out, "y")[0]
     if res is not None:
-        _expect("res", res, (*x.shape[:-1], F), torch.bfloat16)
+        _expect_all(torch.bfloat16, ("res", res, (*x.shape[:-1], F)))
         res_row = _token_rows("res", res)[1]
+        y = _like(y, res, "y")
+    else:
+        y = _out(y, (*x.shape[:-1], F), torch.bfloat16, x.device, "y")
     s = GluShape(M, D, F, M2RNN_BF16, 0)
-    y = _out(_given(out, "y")[0], (*x.shape[:-1], F), torch.bfloat16, x.device, "y")
     rc = lib().m2rnn_linear_q8(ctypes.byref(s), _at(x), row, _addr(xs), _addr(w), _addr(ws), _at(res),
                                res_row, _addr(y), _stream_of(stream, x))
     _check(rc, "m2rnn_linear_q8")
