@@ -37,16 +37,32 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// 8 codes of o / scale.  The quotient is o times the rounded reciprocal (2^-23 off, against e4m3's
-// half step of 2^-4), a true division only where the reciprocal might overflow: the divisions
-// took 13 of 38 us of the 8-bit norm at 12,001 rows of 2,000.
-__device__ __forceinline__ uint2 codes8(const float (&o)[8], float scale, float inv) {
+// 8 codes of o / scale.  The reciprocal is held to twice fp32 (hi + lo, 2^-47 off), so the
+// product, rounded once by the fma, is the rounded quotient: quotients of bf16 values do
+// fall on the middle between two codes, and the rounded reciprocal alone changed the codes of 1
+// in 10^3 of them.  True divisions only where the parts might leave fp32's range.
+struct Reciprocal {
+  float scale, hi, lo;
+};
+__device__ __forceinline__ Reciprocal reciprocal_of(float scale) {
+  Reciprocal r;
+  r.scale = scale;
+  r.hi = 1.f / scale;
+  r.lo = fmaf(-scale, r.hi, 1.f) * r.hi;
+  return r;
+}
+__device__ __forceinline__ uint2 codes8(const float (&o)[8], const Reciprocal& r) {
   float c[8];
+  if (r.scale > 1e-30f && r.scale < 1e30f) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) c[j] = o[j] * inv;
-  if (!(scale > 1e-30f)) {
+    for (int j = 0; j < 8; j += 2) {
+      const float2 x = make_float2(o[j], o[j + 1]), q = fma2(x, both(r.hi), mul2(x, both(r.lo)));
+      c[j] = q.x;
+      c[j + 1] = q.y;
+    }
+  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = scale == 0.f ? 0.f : __fdiv_rn(o[j], scale);
+    for (int j = 0; j < 8; ++j) c[j] = r.scale == 0.f ? 0.f : __fdiv_rn(o[j], r.scale);
   }
   return make_uint2(e4m3x2(c[0], c[1]) | (e4m3x2(c[2], c[3]) << 16), e4m3x2(c[4], c[5]) | (e4m3x2(c[6], c[7]) << 16));
 }
@@ -148,13 +164,14 @@ __global__ void __launch_bounds__(512) add_norm_kernel(Norm2Params p, int warps,
   }
   if constexpr (Q8) {
     row_reduce<1, true>(top, warps, sm);
-    const float scale = __fdiv_rn(top[0], kE4m3Max), inv = 1.f / scale;
+    const float scale = __fdiv_rn(top[0], kE4m3Max);
+    const Reciprocal inv = reciprocal_of(scale);
     if (lane == 0 && in_range(p.status, row, 1, p.M, CHK_NORM2_OUT)) p.scale[row] = scale;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = lane + i * group;
       if (v < vecs && in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
-        *reinterpret_cast<uint2*>(p.q + at + 8 * v) = codes8(keep[i], scale, inv);
+        *reinterpret_cast<uint2*>(p.q + at + 8 * v) = codes8(keep[i], inv);
     }
   }
 }
@@ -179,23 +196,32 @@ __global__ void __launch_bounds__(256, F32 ? 4 : 5) quant_rows_kernel(Norm2Param
 #pragma unroll
   for (int i = 0; i < NV; ++i) keep[i] = load(threadIdx.x + i * step);
   float top[1] = {0.f};
+  __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);  // bf16: the largest of packed pairs, exact
   const auto take = [&](const Raw<F32, 8>& r) {
-    float o[8];
-    raw_unpack<F32, 8>(r, o);
+    if constexpr (F32) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top[0] = nan_max(top[0], fabsf(o[j]));
+      for (int j = 0; j < 8; ++j) top[0] = nan_max(top[0], fabsf(__uint_as_float(r.w[j])));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a = r.w[j] & 0x7FFF7FFFu;
+        top2 = __hmax2_nan(top2, reinterpret_cast<const __nv_bfloat162&>(a));
+      }
+    }
   };
 #pragma unroll
   for (int i = 0; i < NV; ++i) take(keep[i]);
   for (int v = threadIdx.x + NV * step; v < vecs; v += step) take(load(v));
+  if constexpr (!F32) top[0] = nan_max(__low2float(top2), __high2float(top2));
   row_reduce<1, true>(top, blockDim.x / 32, sm);
-  const float scale = __fdiv_rn(top[0], kE4m3Max), inv = 1.f / scale;
+  const float scale = __fdiv_rn(top[0], kE4m3Max);
+  const Reciprocal inv = reciprocal_of(scale);
   if (threadIdx.x == 0 && in_range(p.status, row, 1, p.M, CHK_NORM2_OUT)) p.scale[row] = scale;
   const auto put = [&](int v, const Raw<F32, 8>& r) {
     float o[8];
     raw_unpack<F32, 8>(r, o);
     if (v < vecs && in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
-      *reinterpret_cast<uint2*>(p.q + at + 8 * v) = codes8(o, scale, inv);
+      *reinterpret_cast<uint2*>(p.q + at + 8 * v) = codes8(o, inv);
   };
 #pragma unroll
   for (int i = 0; i < NV; ++i) put(threadIdx.x + i * step, keep[i]);
