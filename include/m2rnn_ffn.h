@@ -7,12 +7,12 @@
  * outputs overwritten; no allocation; no pointer kept; argument errors found
  * on the host before anything is launched.
  *
- * Rows.  Operators here act on each token by itself: M rows (tokens) of D
- * features.  An input that is a slice of a wider buffer is described by its
- * row distance in elements (`x_row` and so on), a multiple of 16 bytes and at
- * least 0 (0: every row is the same one).  Weights, scales and outputs are contiguous.  An
+ * Rows.  Operators here act on each token by itself.  The inputs of the norm and of the
+ * quantiser are [B,T,D] with the row description of m2rnn_block.h (NULL: contiguous); the
+ * products take M tokens whose rows are `x_row` (and so on) elements apart.  Distances are
+ * multiples of 16 bytes.  Weights, scales and outputs are contiguous.  An
  * output must not overlap an input or another output except where a function
- * says that it may.
+ * says that it may (M2RNN_ERR_INVALID_ARG).
  *
  * 8 bits.  M2RNN_E4M3 codes (1 sign, 4 exponent, 3 mantissa bits; largest 448)
  * with one fp32 scale per row: scale = max|row| / 448, code = the nearest e4m3
@@ -26,7 +26,7 @@
 #ifndef M2RNN_FFN_H_
 #define M2RNN_FFN_H_
 
-#include "m2rnn.h"
+#include "m2rnn_block.h" /* m2rnn_rows */
 
 #ifdef __cplusplus
 extern "C" {
@@ -38,44 +38,44 @@ extern "C" {
  *
  * The sum is rounded to in_dtype as it is stored, and y is the norm of what is
  * stored.  res NULL: r = x and the argument `r` must be NULL.
- *   x, res [M,D] in_dtype (rows)     w [D] in_dtype or NULL (1)
- *   r, y [M,D] in_dtype;  q [M,D] e4m3 and scale [M] fp32 (the 8-bit form of y)
- * D a multiple of 8 up to 16384, 0 <= M < 2^31, M*D < 2^40; eps >= 0 (with eps = 0 a
- * zero row gives NaN, as the formula does).  `r` may be `res` or `x` itself (in
+ *   x, res [B,T,D] in_dtype (rows)   w [D] in_dtype or NULL (1)
+ *   r, y [B,T,D] in_dtype;  q [B,T,D] e4m3 and scale [B,T] fp32 (the 8-bit form of y)
+ * D a multiple of 8 up to 16384, B, T >= 0, B*T < 2^31, B*T*D < 2^40; eps >= 0 (with eps = 0
+ * a zero row gives NaN, as the formula does).  `r` may be `res` or `x` itself (in
  * place, contiguous). */
 typedef struct {
-    long long M;
-    int D;
+    int B, T, D;
     int in_dtype; /* m2rnn_dtype of x, res, w, r, y, dy, dr, dx */
 } m2rnn_norm_shape;
 
-int m2rnn_add_norm_fwd(const m2rnn_norm_shape *s, const void *x, long long x_row,
-                       const void *res, long long res_row, const void *w, float eps, void *r,
-                       void *y, void *stream);
+int m2rnn_add_norm_fwd(const m2rnn_norm_shape *s, const void *x, const m2rnn_rows *x_rows,
+                       const void *res, const m2rnn_rows *res_rows, const void *w, float eps,
+                       void *r, void *y, void *stream);
 
-int m2rnn_add_norm_q8(const m2rnn_norm_shape *s, const void *x, long long x_row, const void *res,
-                      long long res_row, const void *w, float eps, void *r, void *q,
-                      float *scale, void *stream);
+int m2rnn_add_norm_q8(const m2rnn_norm_shape *s, const void *x, const m2rnn_rows *x_rows,
+                      const void *res, const m2rnn_rows *res_rows, const void *w, float eps,
+                      void *r, void *q, float *scale, void *stream);
 
 size_t m2rnn_add_norm_bwd_workspace_size(const m2rnn_norm_shape *s);
 
-/* Gradients for dL/dy = dy and dL/dr = dr past the norm (NULL = 0), both [M,D] in_dtype:
- * dx [M,D] in_dtype, which is the gradient of x and of res alike, and dw [D]
- * fp32 (NULL: not wanted).  r (rows) is the norm's input.  dx may be dr or dy itself. */
-int m2rnn_add_norm_bwd(const m2rnn_norm_shape *s, const void *r, long long r_row, const void *w,
-                       float eps, const void *dy, const void *dr, void *dx, float *dw,
-                       void *workspace, size_t ws_bytes, void *stream);
+/* Gradients for dL/dy = dy and dL/dr = dr past the norm (NULL = 0), both [B,T,D] in_dtype:
+ * dx [B,T,D] in_dtype, which is the gradient of x and of res alike, and dw [D]
+ * fp32 (NULL: not wanted, and no workspace needed).  r (rows) is the norm's input.  dx may
+ * be dr or dy itself. */
+int m2rnn_add_norm_bwd(const m2rnn_norm_shape *s, const void *r, const m2rnn_rows *r_rows,
+                       const void *w, float eps, const void *dy, const void *dr, void *dx,
+                       float *dw, void *workspace, size_t ws_bytes, void *stream);
 
 /* Codes and scales of x's rows (an activation, or a weight matrix laid out once): s->D up
  * to 2^20. */
-int m2rnn_quant_rows(const m2rnn_norm_shape *s, const void *x, long long x_row, void *q,
+int m2rnn_quant_rows(const m2rnn_norm_shape *s, const void *x, const m2rnn_rows *x_rows, void *q,
                      float *scale, void *stream);
 
 /* ---- gated feed-forward products -------------------------------------------
  *
  *     g = x wg^T,  u = x wu^T,  h = act(g) (.) u
  *
- *   x [M,D] (rows), wg, wu [F,D], h, dh [M,F], dx [M,D], dwg, dwu [F,D], all in_dtype
+ *   x [M,D] (rows x_row >= D apart), wg, wu [F,D], h, dh [M,F], dx [M,D], dwg, dwu [F,D], all in_dtype
  * act: 0 SiLU g / (1 + e^-g), 1 GELU in its tanh form.  D and F multiples of 8
  * up to 2^20, 0 <= M < 2^31, M*D and M*F < 2^40.  Products are summed in fp32; with fp32 inputs
  * every operand is held whole (three bf16 terms), and where a product meets a

@@ -36,7 +36,8 @@ __device__ __forceinline__ void act_grad(float g, int act, float& a, float& d) {
   } else {
     const float s = gelu_gate<EXACT>(g), c = 0.7978845608028654f;
     a = g * s;
-    d = s + a * (1.f - s) * (2.f * c) * (1.f + 3.f * 0.044715f * g * g);
+    const float t = a * (1.f - s);  // 0 where the gate is 0 or 1, whatever g^2 overflows to
+    d = s + (t == 0.f ? 0.f : t * (2.f * c) * (1.f + 3.f * 0.044715f * g * g));
   }
 }
 

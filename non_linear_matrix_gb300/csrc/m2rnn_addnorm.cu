@@ -89,6 +89,16 @@ __device__ __forceinline__ void row_reduce(float (&v)[N], int warps, float* sm) 
   __syncthreads();
 }
 
+// Offset of a row, and the elements that the rows span.
+__device__ __forceinline__ size_t row_at(const Norm2Params& p, long long row, long long batch, long long token) {
+  if (p.T == p.M) return static_cast<size_t>(row) * token;
+  const unsigned b = static_cast<unsigned>(row) / static_cast<unsigned>(p.T);
+  return static_cast<size_t>(b) * batch + static_cast<size_t>(row - static_cast<long long>(b) * p.T) * token;
+}
+__device__ __forceinline__ size_t rows_span(const Norm2Params& p, long long batch, long long token) {
+  return static_cast<size_t>(p.M / p.T - 1) * batch + static_cast<size_t>(p.T - 1) * token + p.D;
+}
+
 // ADD: r = x + res is stored.  Q8: the output as codes and a scale.  NORM = false:
 // the quantiser of x alone.
 template <bool F32, int NV, bool ADD, bool Q8>
@@ -100,19 +110,19 @@ __global__ void __launch_bounds__(512) add_norm_kernel(Norm2Params p, int warps,
   const long long row = static_cast<long long>(blockIdx.x) * rows_per_cta + (warps == 1 ? threadIdx.x >> 5 : 0);
   if (row >= p.M) return;  // (whole warps; CTAs of several warps per row hold one row)
   const size_t D = p.D, n = static_cast<size_t>(p.M) * D, at = static_cast<size_t>(row) * D;
-  const T* x = static_cast<const T*>(p.x) + row * p.x_row;
-  const T* res = ADD ? static_cast<const T*>(p.res) + row * p.res_row : nullptr;
-  const size_t x_ext = static_cast<size_t>(p.M - 1) * p.x_row + D;
-  const size_t res_ext = static_cast<size_t>(p.M - 1) * p.res_row + D;
+  const size_t x0 = row_at(p, row, p.xb, p.xt), r0 = ADD ? row_at(p, row, p.rb, p.rt) : 0;
+  const T* x = static_cast<const T*>(p.x) + x0;
+  const T* res = ADD ? static_cast<const T*>(p.res) + r0 : nullptr;
+  const size_t x_ext = rows_span(p, p.xb, p.xt), res_ext = ADD ? rows_span(p, p.rb, p.rt) : 0;
   Raw<F32, 8> xv[NV], rv[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = lane + i * group;
     xv[i] = rv[i] = raw_zero<F32, 8>();
     if (v < vecs) {
-      if (in_range(p.status, static_cast<size_t>(row) * p.x_row + 8 * v, 8, x_ext, CHK_NORM2_IN))
+      if (in_range(p.status, x0 + 8 * v, 8, x_ext, CHK_NORM2_IN))
         xv[i] = raw_load<F32, 8, false>(x + 8 * v);
-      if (ADD && in_range(p.status, static_cast<size_t>(row) * p.res_row + 8 * v, 8, res_ext, CHK_NORM2_IN))
+      if (ADD && in_range(p.status, r0 + 8 * v, 8, res_ext, CHK_NORM2_IN))
         rv[i] = raw_load<F32, 8, false>(res + 8 * v);
     }
   }
@@ -186,7 +196,7 @@ __global__ void __launch_bounds__(256, F32 ? 4 : 5) quant_rows_kernel(Norm2Param
   const int vecs = p.D / 8, step = blockDim.x;
   const long long row = blockIdx.x;
   const size_t n = static_cast<size_t>(p.M) * p.D, at = static_cast<size_t>(row) * p.D;
-  const size_t x0 = static_cast<size_t>(row) * p.x_row, x_ext = static_cast<size_t>(p.M - 1) * p.x_row + p.D;
+  const size_t x0 = row_at(p, row, p.xb, p.xt), x_ext = rows_span(p, p.xb, p.xt);
   const T* x = static_cast<const T*>(p.x) + x0;
   const auto load = [&](int v) {
     return v < vecs && in_range(p.status, x0 + 8 * v, 8, x_ext, CHK_NORM2_IN) ? raw_load<F32, 8>(x + 8 * v)
@@ -254,7 +264,7 @@ __global__ void __launch_bounds__(BwdCfg<F32, NV>::CTA, NV == 4 ? 1 : 2) add_nor
   const int lane = threadIdx.x % group, mine = threadIdx.x / group;
   let_next_begin();
   const size_t D = p.D, n = static_cast<size_t>(p.M) * D;
-  const size_t r_ext = static_cast<size_t>(p.M - 1) * p.x_row + D;
+  const size_t r_ext = rows_span(p, p.xb, p.xt);
   float dw[NV][8];
   Raw<F32, 8> w[NV];
 #pragma unroll
@@ -273,7 +283,7 @@ __global__ void __launch_bounds__(BwdCfg<F32, NV>::CTA, NV == 4 ? 1 : 2) add_nor
   const uint32_t base = ptx::smem_addr(ring) + threadIdx.x * 16;
   const auto place = [&](int slot, int which, int i) { return base + ((slot * 3 + which) * NV + i) * U * CTA * 16; };
   const auto fetch = [&](int slot, long long row) {
-    const size_t at = static_cast<size_t>(row) * D, r0 = static_cast<size_t>(row) * p.x_row;
+    const size_t at = static_cast<size_t>(row) * D, r0 = row_at(p, row, p.xb, p.xt);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = lane + i * group;
@@ -475,7 +485,8 @@ cudaError_t launch_bwd_t(const Norm2Params& p, cudaStream_t st) {
 int add_norm_bwd_parts(const m2rnn_norm_shape* s) {
   const RowPlan r = bwd_plan(s->D);
   const int groups = (r.nv == 4 ? 16 : 8) / r.warps;
-  const long long most = r.nv == 4 ? 152 : 304, need = (s->M + groups - 1) / groups;
+  const long long rows = static_cast<long long>(s->B) * s->T;
+  const long long most = r.nv == 4 ? 152 : 304, need = (rows + groups - 1) / groups;
   return static_cast<int>(need < most ? need : most);
 }
 

@@ -80,6 +80,7 @@ namespace m2rnn {
 int host_device_info(int* dev, int** status, int* sms) { return device_info(dev, status, sms); }
 int host_check_ptr(const void* p, int dev, bool required) { return check_ptr(p, dev, required); }
 unsigned long long host_wait_limit_ns() { return static_cast<unsigned long long>(g_wait_limit_ns.load()); }
+int host_fault_injection() { return g_fault_injection.load(); }
 int host_check_elem_ptr(const void* p, int dev, size_t unit) {
   if (p == nullptr) return M2RNN_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(p) % unit != 0) return M2RNN_ERR_MISALIGNED;

@@ -20,6 +20,46 @@ int host_check_ptr(const void* p, int dev, bool required);
 // `unit` bytes only).
 int host_check_elem_ptr(const void* p, int dev, size_t unit);
 
+// A row description (NULL: contiguous rows of `width` elements); distances
+// must keep rows on `unit`-byte boundaries.
+inline int read_rows(const m2rnn_rows* r, int T, long long width, int dtype, long long unit,
+              m2rnn_rows* out) {
+  if (r == nullptr) {
+    out->token = width;
+    out->batch = width * T;
+    return M2RNN_OK;
+  }
+  if (r->batch < 0 || r->token < 0) return M2RNN_ERR_INVALID_ARG;
+  const long long e = dtype == M2RNN_F32 ? 4 : 2;
+  if ((r->batch * e) % unit != 0 || (r->token * e) % unit != 0) return M2RNN_ERR_MISALIGNED;
+  *out = *r;
+  return M2RNN_OK;
+}
+
+inline bool overlap_spans(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
+// Whether any of the rows ([B][T] of `width` elements of e bytes) overlaps the
+// `bytes` at y.
+inline bool rows_overlap(const void* x, const m2rnn_rows& r, long long B, long long T, long long width, size_t e,
+                  const void* y, size_t bytes) {
+  if (x == nullptr || y == nullptr || T == 0 || bytes == 0) return false;
+  const long long n = static_cast<long long>(e);
+  const long long token = r.token * n, row = width * n, item = (T - 1) * token + row;
+  if (!overlap_spans(x, (B - 1) * r.batch * n + item, y, bytes)) return false;
+  for (long long b = 0; b < B; ++b) {
+    const char* xb = static_cast<const char*>(x) + b * r.batch * n;
+    if (!overlap_spans(xb, item, y, bytes)) continue;
+    // the first row that ends behind y's start
+    const long long gap = static_cast<const char*>(y) - xb - row;
+    const long long t = gap < 0 || token == 0 ? 0 : gap / token + 1;
+    if (t < T && overlap_spans(xb + t * token, row, y, bytes)) return true;
+  }
+  return false;
+}
+
 // Location codes of the block operators' index checks.
 enum BlockCheckSite : int {
   CHK_CONV_IN = 501,     // x, state, dy, dstate_out loads

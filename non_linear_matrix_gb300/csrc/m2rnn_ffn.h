@@ -15,6 +15,7 @@ namespace m2rnn {
 
 // m2rnn_api.cu: the time limit of waits inside kernels.
 unsigned long long host_wait_limit_ns();
+int host_fault_injection();  // 1: kernels start no input transfers (a test hook)
 
 // Location codes of the index checks and of waits that gave up.
 enum FfnCheckSite : int {
@@ -37,9 +38,9 @@ struct Norm2Params {
   float* scale;
   float* part;  // backward: [nparts][D]
   float* dw;
-  long long x_row, res_row;
-  long long M;
-  int D;
+  long long xb, xt, rb, rt;  // rows of x (r in the backward pass) and res
+  long long M;               // B * T rows of
+  int T, D;                  // T per item (M where the rows are evenly spaced)
   int nparts;
   float eps;
   int* status;
@@ -77,6 +78,7 @@ struct GemmParams {
   int act;
   int* status;
   unsigned long long limit_ns;
+  int inject_stall;       // test hook: no copies are issued
 };
 // kind: operands' element (0 bf16, 1 e4m3); a_mn, b_mn: whether M or N runs fastest in memory.
 struct GemmKind {

@@ -14,7 +14,11 @@ namespace {
 using m2rnn::host_check_ptr;
 using m2rnn::host_device_info;
 
-int status_from_cuda(cudaError_t e) { return e == cudaSuccess ? M2RNN_OK : M2RNN_ERR_CUDA; }
+int status_from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return M2RNN_OK;
+  cudaGetLastError();  // (not left for the next call to find)
+  return M2RNN_ERR_CUDA;
+}
 bool is_dtype(int d) { return d == M2RNN_F32 || d == M2RNN_BF16; }
 size_t esize(int dtype) { return dtype == M2RNN_F32 ? 4 : 2; }
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -42,54 +46,85 @@ int check_row(long long row, size_t e, long long M, long long least) {
 
 int check_norm(const m2rnn_norm_shape* s, int most_d) {
   if (s == nullptr) return M2RNN_ERR_INVALID_ARG;
-  if (s->M < 0 || s->D < 1 || !is_dtype(s->in_dtype)) return M2RNN_ERR_INVALID_ARG;
-  if (s->D % 8 != 0 || s->D > most_d || s->M >= (1LL << 31)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
-  if (static_cast<double>(s->M) * s->D >= kMostElems) return M2RNN_ERR_UNSUPPORTED_SHAPE;
+  if (s->B < 0 || s->T < 0 || s->D < 1 || !is_dtype(s->in_dtype)) return M2RNN_ERR_INVALID_ARG;
+  const double rows = static_cast<double>(s->B) * s->T;
+  if (s->D % 8 != 0 || s->D > most_d || rows >= 2147483648.0 || rows * s->D >= kMostElems)
+    return M2RNN_ERR_UNSUPPORTED_SHAPE;
   return M2RNN_OK;
 }
 constexpr int kNormMostD = 16384, kMostD = 1 << 20;
+long long rows_of(const m2rnn_norm_shape* s) { return static_cast<long long>(s->B) * s->T; }
 
-// Whether the rows of x overlap `bytes` at y (by their whole span: a false alarm only for
-// outputs between the rows of a wider buffer, which contiguous outputs never are).
+// Rows of x, whose distances keep every offset below 2^40 elements.
+int norm_rows(const m2rnn_norm_shape* s, const m2rnn_rows* rows, m2rnn_rows* out) {
+  const int rc = m2rnn::read_rows(rows, s->T, s->D, s->in_dtype, 16, out);
+  if (rc != M2RNN_OK) return rc;
+  const double span = static_cast<double>(out->batch) * s->B + static_cast<double>(out->token) * s->T;
+  return span >= 2.0 * kMostElems ? M2RNN_ERR_UNSUPPORTED_SHAPE : M2RNN_OK;
+}
+bool contiguous(const m2rnn_norm_shape* s, const m2rnn_rows& r) {
+  return (s->T <= 1 || r.token == s->D) && (s->B <= 1 || r.batch == static_cast<long long>(s->T) * s->D);
+}
+bool norm_overlap(const m2rnn_norm_shape* s, const void* x, const m2rnn_rows& r, const void* y, size_t bytes) {
+  return s->B > 0 && m2rnn::rows_overlap(x, r, s->B, s->T, s->D, esize(s->in_dtype), y, bytes);
+}
+
 bool spans_overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
-  if (a == nullptr || b == nullptr || a_bytes == 0 || b_bytes == 0) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + b_bytes && y < x + a_bytes;
+  return a != nullptr && b != nullptr && a_bytes > 0 && b_bytes > 0 && m2rnn::overlap_spans(a, a_bytes, b, b_bytes);
 }
-size_t rows_bytes(long long M, long long row, long long D, size_t e) {
-  return M == 0 ? 0 : (static_cast<size_t>(M - 1) * row + D) * e;
+// The same for M rows of the products' inputs.
+bool row_overlap(const void* x, long long row, long long M, long long D, size_t e, const void* y, size_t bytes) {
+  const m2rnn_rows r = {0, row};
+  return M > 0 && m2rnn::rows_overlap(x, r, 1, M, D, e, y, bytes);
 }
 
-int add_norm(const m2rnn_norm_shape* s, const void* x, long long x_row, const void* res, long long res_row,
-             const void* w, float eps, void* r, void* y, void* q, float* scale, bool q8, void* stream) {
+// Rows that are evenly spaced over all items need no division in the kernels.
+void set_rows(const m2rnn_norm_shape* s, const m2rnn_rows& x, const m2rnn_rows* res, m2rnn::Norm2Params* p) {
+  const auto even = [&](const m2rnn_rows& r) { return r.batch == r.token * s->T; };
+  p->M = rows_of(s);
+  p->T = s->B == 1 || (even(x) && (res == nullptr || even(*res))) ? static_cast<int>(p->M) : s->T;
+  p->xb = x.batch;
+  p->xt = x.token;
+  if (res != nullptr) {
+    p->rb = res->batch;
+    p->rt = res->token;
+  }
+  if (s->T == 1 && s->B > 1) {  // items are the rows
+    p->T = static_cast<int>(p->M);
+    p->xt = x.batch;
+    if (res != nullptr) p->rt = res->batch;
+  }
+  p->D = s->D;
+}
+
+int add_norm(const m2rnn_norm_shape* s, const void* x, const m2rnn_rows* x_rows, const void* res,
+             const m2rnn_rows* res_rows, const void* w, float eps, void* r, void* y, void* q, float* scale, bool q8,
+             void* stream) {
   int rc = check_norm(s, kNormMostD);
   if (rc != M2RNN_OK) return rc;
   if (!(eps >= 0.f)) return M2RNN_ERR_INVALID_ARG;  // also rejects NaN
-  const size_t e = esize(s->in_dtype);
-  if ((rc = check_row(x_row, e, s->M, 0)) != M2RNN_OK) return rc;
-  if (res != nullptr && (rc = check_row(res_row, e, s->M, 0)) != M2RNN_OK) return rc;
-  if ((res == nullptr) != (r == nullptr) && s->M > 0) return M2RNN_ERR_INVALID_ARG;
+  const size_t e = esize(s->in_dtype), M = static_cast<size_t>(rows_of(s));
+  m2rnn_rows xr, rr;
+  if ((rc = norm_rows(s, x_rows, &xr)) != M2RNN_OK || (rc = norm_rows(s, res_rows, &rr)) != M2RNN_OK) return rc;
+  if ((res == nullptr) != (r == nullptr) && M > 0) return M2RNN_ERR_INVALID_ARG;
   // outputs apart from inputs and each other; r may be x or res itself
-  const size_t n = static_cast<size_t>(s->M) * s->D * e;
-  const size_t xb = rows_bytes(s->M, x_row, s->D, e), rb = rows_bytes(s->M, res_row, s->D, e);
   const struct { const void* p; size_t bytes; } outs[] = {
-      {r, n}, {y, n}, {q, static_cast<size_t>(s->M) * s->D}, {scale, static_cast<size_t>(s->M) * 4}};
+      {r, M * s->D * e}, {y, M * s->D * e}, {q, M * s->D}, {scale, M * 4}};
   for (int i = 0; i < 4; ++i) {
-    const bool in_place_x = i == 0 && r == x && x_row == s->D, in_place_r = i == 0 && r == res && res_row == s->D;
-    if (!in_place_x && spans_overlap(x, xb, outs[i].p, outs[i].bytes)) return M2RNN_ERR_INVALID_ARG;
-    if (!in_place_r && res != nullptr && spans_overlap(res, rb, outs[i].p, outs[i].bytes))
-      return M2RNN_ERR_INVALID_ARG;
+    const bool here_x = i == 0 && r == x && contiguous(s, xr), here_res = i == 0 && r == res && contiguous(s, rr);
+    if (!here_x && norm_overlap(s, x, xr, outs[i].p, outs[i].bytes)) return M2RNN_ERR_INVALID_ARG;
+    if (!here_res && norm_overlap(s, res, rr, outs[i].p, outs[i].bytes)) return M2RNN_ERR_INVALID_ARG;
     if (spans_overlap(w, static_cast<size_t>(s->D) * e, outs[i].p, outs[i].bytes)) return M2RNN_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)
       if (spans_overlap(outs[j].p, outs[j].bytes, outs[i].p, outs[i].bytes)) return M2RNN_ERR_INVALID_ARG;
   }
   int dev, sms, *status;
   if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
-  if (s->M == 0) return M2RNN_OK;
+  if (M == 0) return M2RNN_OK;
   const void* opt[] = {res, w, r};
   if ((rc = check(opt, dev, false)) != M2RNN_OK) return rc;
-  const void* req[] = {x, q8 ? q : y, q8 ? static_cast<const void*>(scale) : x};
-  if ((rc = check(req, dev, true)) != M2RNN_OK) return rc;
+  const void* req[] = {x, q8 ? q : y};
+  if ((rc = check(req, dev, true)) != M2RNN_OK || (rc = host_check_ptr(scale, dev, q8)) != M2RNN_OK) return rc;
   m2rnn::Norm2Params p{};
   p.x = x;
   p.res = res;
@@ -98,10 +133,7 @@ int add_norm(const m2rnn_norm_shape* s, const void* x, long long x_row, const vo
   p.y = y;
   p.q = static_cast<uint8_t*>(q);
   p.scale = scale;
-  p.x_row = x_row;
-  p.res_row = res_row;
-  p.M = s->M;
-  p.D = s->D;
+  set_rows(s, xr, res == nullptr ? nullptr : &rr, &p);
   p.eps = eps;
   p.status = status;
   return status_from_cuda(
@@ -181,6 +213,7 @@ m2rnn::GemmParams gemm_params(const m2rnn::GemmPlan& q, long long M, int N, int 
   p.nparts = q.nparts;
   p.status = status;
   p.limit_ns = m2rnn::host_wait_limit_ns();
+  p.inject_stall = m2rnn::host_fault_injection() == 1;
   return p;
 }
 int k_tiles(long long K, size_t e) { return static_cast<int>((K * static_cast<long long>(e) + 127) / 128); }
@@ -260,33 +293,34 @@ int run_pair(const m2rnn_glu_shape* s, const Operands& o, int epi, const void* d
 
 extern "C" {
 
-int m2rnn_add_norm_fwd(const m2rnn_norm_shape* s, const void* x, long long x_row, const void* res,
-                       long long res_row, const void* w, float eps, void* r, void* y, void* stream) {
-  return add_norm(s, x, x_row, res, res_row, w, eps, r, y, nullptr, nullptr, false, stream);
+int m2rnn_add_norm_fwd(const m2rnn_norm_shape* s, const void* x, const m2rnn_rows* x_rows, const void* res,
+                       const m2rnn_rows* res_rows, const void* w, float eps, void* r, void* y, void* stream) {
+  return add_norm(s, x, x_rows, res, res_rows, w, eps, r, y, nullptr, nullptr, false, stream);
 }
 
-int m2rnn_add_norm_q8(const m2rnn_norm_shape* s, const void* x, long long x_row, const void* res,
-                      long long res_row, const void* w, float eps, void* r, void* q, float* scale, void* stream) {
-  return add_norm(s, x, x_row, res, res_row, w, eps, r, nullptr, q, scale, true, stream);
+int m2rnn_add_norm_q8(const m2rnn_norm_shape* s, const void* x, const m2rnn_rows* x_rows, const void* res,
+                      const m2rnn_rows* res_rows, const void* w, float eps, void* r, void* q, float* scale,
+                      void* stream) {
+  return add_norm(s, x, x_rows, res, res_rows, w, eps, r, nullptr, q, scale, true, stream);
 }
 
 size_t m2rnn_add_norm_bwd_workspace_size(const m2rnn_norm_shape* s) {
-  if (check_norm(s, kNormMostD) != M2RNN_OK || s->M == 0) return 0;
+  if (check_norm(s, kNormMostD) != M2RNN_OK || rows_of(s) == 0) return 0;
   return align256(static_cast<size_t>(m2rnn::add_norm_bwd_parts(s)) * s->D * sizeof(float));
 }
 
-int m2rnn_add_norm_bwd(const m2rnn_norm_shape* s, const void* r, long long r_row, const void* w, float eps,
+int m2rnn_add_norm_bwd(const m2rnn_norm_shape* s, const void* r, const m2rnn_rows* r_rows, const void* w, float eps,
                        const void* dy, const void* dr, void* dx, float* dw, void* workspace, size_t ws_bytes,
                        void* stream) {
   int rc = check_norm(s, kNormMostD);
   if (rc != M2RNN_OK) return rc;
   if (!(eps >= 0.f)) return M2RNN_ERR_INVALID_ARG;
-  const size_t e = esize(s->in_dtype);
-  if ((rc = check_row(r_row, e, s->M, 0)) != M2RNN_OK) return rc;
-  const size_t n = static_cast<size_t>(s->M) * s->D * e, db = static_cast<size_t>(s->D) * 4;
-  const size_t rb = rows_bytes(s->M, r_row, s->D, e), wb = static_cast<size_t>(s->D) * e;
-  if (spans_overlap(r, rb, dx, n) || spans_overlap(w, wb, dx, n) || (dx != dy && spans_overlap(dy, n, dx, n)) ||
-      (dx != dr && spans_overlap(dr, n, dx, n)) || spans_overlap(dw, db, dx, n) || spans_overlap(dw, db, r, rb) ||
+  m2rnn_rows rr;
+  if ((rc = norm_rows(s, r_rows, &rr)) != M2RNN_OK) return rc;
+  const size_t e = esize(s->in_dtype), M = static_cast<size_t>(rows_of(s));
+  const size_t n = M * s->D * e, db = static_cast<size_t>(s->D) * 4, wb = static_cast<size_t>(s->D) * e;
+  if (norm_overlap(s, r, rr, dx, n) || spans_overlap(w, wb, dx, n) || (dx != dy && spans_overlap(dy, n, dx, n)) ||
+      (dx != dr && spans_overlap(dr, n, dx, n)) || spans_overlap(dw, db, dx, n) || norm_overlap(s, r, rr, dw, db) ||
       spans_overlap(dw, db, dy, n) || spans_overlap(dw, db, dr, n) || spans_overlap(dw, db, w, wb))
     return M2RNN_ERR_INVALID_ARG;
   int dev, sms, *status;
@@ -294,7 +328,7 @@ int m2rnn_add_norm_bwd(const m2rnn_norm_shape* s, const void* r, long long r_row
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const void* opt[] = {w, dr, dw};
   if ((rc = check(opt, dev, false)) != M2RNN_OK) return rc;
-  if (s->M == 0) return dw == nullptr ? M2RNN_OK : status_from_cuda(cudaMemsetAsync(dw, 0, db, st));
+  if (M == 0) return dw == nullptr ? M2RNN_OK : status_from_cuda(cudaMemsetAsync(dw, 0, db, st));
   const void* req[] = {r, dy, dx};
   if ((rc = check(req, dev, true)) != M2RNN_OK) return rc;
   if (dw != nullptr) {
@@ -303,7 +337,7 @@ int m2rnn_add_norm_bwd(const m2rnn_norm_shape* s, const void* r, long long r_row
   }
   m2rnn::Norm2Params p{};
   p.x = r;
-  p.x_row = r_row;
+  set_rows(s, rr, nullptr, &p);
   p.w = w;
   p.dy = dy;
   p.dr = dr;
@@ -311,35 +345,30 @@ int m2rnn_add_norm_bwd(const m2rnn_norm_shape* s, const void* r, long long r_row
   p.dw = dw;
   p.part = dw == nullptr ? nullptr : static_cast<float*>(workspace);
   p.nparts = m2rnn::add_norm_bwd_parts(s);
-  p.M = s->M;
-  p.D = s->D;
   p.eps = eps;
   p.status = status;
   return status_from_cuda(m2rnn::launch_add_norm_bwd(p, s->in_dtype == M2RNN_F32, st));
 }
 
-int m2rnn_quant_rows(const m2rnn_norm_shape* s, const void* x, long long x_row, void* q, float* scale,
+int m2rnn_quant_rows(const m2rnn_norm_shape* s, const void* x, const m2rnn_rows* x_rows, void* q, float* scale,
                      void* stream) {
   int rc = check_norm(s, kMostD);
   if (rc != M2RNN_OK) return rc;
-  const size_t e = esize(s->in_dtype);
-  if ((rc = check_row(x_row, e, s->M, 0)) != M2RNN_OK) return rc;
-  const size_t xb = rows_bytes(s->M, x_row, s->D, e), qb = static_cast<size_t>(s->M) * s->D;
-  const size_t sb = static_cast<size_t>(s->M) * 4;
-  if (spans_overlap(x, xb, q, qb) || spans_overlap(x, xb, scale, sb) || spans_overlap(q, qb, scale, sb))
+  m2rnn_rows xr;
+  if ((rc = norm_rows(s, x_rows, &xr)) != M2RNN_OK) return rc;
+  const size_t M = static_cast<size_t>(rows_of(s)), qb = M * s->D, sb = M * 4;
+  if (norm_overlap(s, x, xr, q, qb) || norm_overlap(s, x, xr, scale, sb) || spans_overlap(q, qb, scale, sb))
     return M2RNN_ERR_INVALID_ARG;
   int dev, sms, *status;
   if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;
-  if (s->M == 0) return M2RNN_OK;
+  if (M == 0) return M2RNN_OK;
   const void* req[] = {x, q, scale};
   if ((rc = check(req, dev, true)) != M2RNN_OK) return rc;
   m2rnn::Norm2Params p{};
   p.x = x;
-  p.x_row = x_row;
+  set_rows(s, xr, nullptr, &p);
   p.q = static_cast<uint8_t*>(q);
   p.scale = scale;
-  p.M = s->M;
-  p.D = s->D;
   p.status = status;
   return status_from_cuda(
       m2rnn::launch_quant_rows(p, s->in_dtype == M2RNN_F32, sms, static_cast<cudaStream_t>(stream)));
@@ -357,7 +386,7 @@ int m2rnn_glu_fwd(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
   const size_t e = esize(s->in_dtype);
   if ((rc = check_row(x_row, e, s->M, s->D)) != M2RNN_OK) return rc;
   const size_t hb = static_cast<size_t>(s->M) * s->F * e, wb = static_cast<size_t>(s->F) * s->D * e;
-  if (spans_overlap(x, rows_bytes(s->M, x_row, s->D, e), h, hb) || spans_overlap(wg, wb, h, hb) ||
+  if (row_overlap(x, x_row, s->M, s->D, e, h, hb) || spans_overlap(wg, wb, h, hb) ||
       spans_overlap(wu, wb, h, hb))
     return M2RNN_ERR_INVALID_ARG;
   int dev, sms, *status;
@@ -405,10 +434,11 @@ int m2rnn_glu_bwd(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
   if ((rc = check_row(x_row, e, s->M, s->D)) != M2RNN_OK) return rc;
   if ((dwg == nullptr) != (dwu == nullptr)) return M2RNN_ERR_INVALID_ARG;
   const size_t xb = static_cast<size_t>(s->M) * s->D * e, wb = static_cast<size_t>(s->F) * s->D * e;
-  const size_t hb = static_cast<size_t>(s->M) * s->F * e, xr = rows_bytes(s->M, x_row, s->D, e);
+  const size_t hb = static_cast<size_t>(s->M) * s->F * e;
   const struct { const void* p; size_t bytes; } outs[] = {{dx, xb}, {dwg, wb}, {dwu, wb}},
-                                                ins[] = {{x, xr}, {wg, wb}, {wu, wb}, {dh, hb}};
+                                                ins[] = {{wg, wb}, {wu, wb}, {dh, hb}};
   for (int i = 0; i < 3; ++i) {
+    if (row_overlap(x, x_row, s->M, s->D, e, outs[i].p, outs[i].bytes)) return M2RNN_ERR_INVALID_ARG;
     for (const auto& in : ins)
       if (spans_overlap(in.p, in.bytes, outs[i].p, outs[i].bytes)) return M2RNN_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)
@@ -481,10 +511,10 @@ int product_q8(const m2rnn_glu_shape* s, const void* x, long long x_row, const f
   const size_t ob = static_cast<size_t>(s->M) * s->F * 2, wb = static_cast<size_t>(s->F) * s->D;
   const size_t fb = static_cast<size_t>(s->F) * 4;
   const bool in_place = res == out && res_row == s->F;
-  if (spans_overlap(x, rows_bytes(s->M, x_row, s->D, 1), out, ob) || spans_overlap(w0, wb, out, ob) ||
+  if (row_overlap(x, x_row, s->M, s->D, 1, out, ob) || spans_overlap(w0, wb, out, ob) ||
       spans_overlap(w1, wb, out, ob) || spans_overlap(xs, static_cast<size_t>(s->M) * 4, out, ob) ||
       spans_overlap(s0, fb, out, ob) || spans_overlap(s1, fb, out, ob) ||
-      (!in_place && spans_overlap(res, rows_bytes(s->M, res_row, s->F, 2), out, ob)))
+      (!in_place && row_overlap(res, res_row, s->M, s->F, 2, out, ob)))
     return M2RNN_ERR_INVALID_ARG;
   int dev, sms, *status;
   if ((rc = host_device_info(&dev, &status, &sms)) != M2RNN_OK) return rc;

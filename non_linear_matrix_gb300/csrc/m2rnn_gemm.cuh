@@ -48,6 +48,9 @@ struct GemmCfg {
   static constexpr int BLOCKS = OUT_N / 32 / 2;  // blocks of 32 output columns of a warp
 };
 
+// How long a kernel that gave up waits for its own copies and products.
+constexpr uint64_t kDrainNs = 1000000000ull;
+
 __device__ __forceinline__ void gave_up(int* status, int site) {
   if (atomicCAS(&status[0], 0, kStatusTimeout) == 0) atomicExch(&status[1], site);
 }
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
       const uint32_t full0 = C::CG == 2 ? tc5::map_to(full, 0) : full;
       int it = 0;
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += stride) {
+      for (int t = p.inject_stall ? tiles : first; t < tiles && ok; t += stride) {
         const TileAt at = tile_at(p, t);
         for (int c = at.k0; c < at.k1 && ok; c += p.kc)
           for (int s = 0; s < p.nseg && ok; ++s)
@@ -403,8 +406,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
         ok = ptx::mbar_wait(empty + 8 * (i % C::STAGES), (i / C::STAGES) & 1, p.limit_ns);
       if (!ok) {  // copies in flight land before the CTA goes
         gave_up(p.status, SITE_GEMM_COPY);
-        for (int i = max(0, it - C::STAGES); i < it && rank == 0; ++i)
-          ptx::mbar_wait(full + 8 * (i % C::STAGES), (i / C::STAGES) & 1, p.limit_ns);
+        if (rank == 0) {
+          for (int i = max(0, it - C::STAGES); i < it; ++i)
+            ptx::mbar_wait(full + 8 * (i % C::STAGES), (i / C::STAGES) & 1, kDrainNs);
+        } else {  // (they are counted in the other CTA: a thousand times what a copy takes)
+          const uint64_t t0 = ptx::globaltimer_ns();
+          while (ptx::globaltimer_ns() - t0 < 1000000) __nanosleep(1000);
+        }
       }
     }
     __syncwarp();
@@ -461,7 +469,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
       if (!ok) {
         gave_up(p.status, site);
         tc5::commit<C::CG>(drain);
-        if (!ptx::mbar_wait(drain, 0, p.limit_ns)) gave_up(p.status, SITE_GEMM_DRAIN);
+        if (!ptx::mbar_wait(drain, 0, kDrainNs)) gave_up(p.status, SITE_GEMM_DRAIN);
       }
     }
     __syncwarp();
@@ -585,8 +593,9 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__
     store_vec<C::F32, 8>(static_cast<typename Elem<C::F32>::T*>(at.batch ? p.out[1] : p.out[0]) + to, s);
 }
 
+// (static: the `ready` of another build of the library in the same process is not this one's)
 template <class C>
-cudaError_t launch_cfg(const GemmParams& p, int sms, cudaStream_t st) {
+static cudaError_t launch_cfg(const GemmParams& p, int sms, cudaStream_t st) {
   static bool ready[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -69,12 +69,12 @@ _EXPORTS = {
     "m2rnn_scan_bwd_workspace_size": (ctypes.c_size_t, [_VP, ctypes.c_int]),
     "m2rnn_scan_bwd": (ctypes.c_int, [_VP] * 22 + [ctypes.c_size_t, _VP]),
     "m2rnn_scan_step": (ctypes.c_int, [_VP] * 13),
-    "m2rnn_add_norm_fwd": (ctypes.c_int, [_VP, _VP, _LL, _VP, _LL, _VP, ctypes.c_float] + [_VP] * 3),
-    "m2rnn_add_norm_q8": (ctypes.c_int, [_VP, _VP, _LL, _VP, _LL, _VP, ctypes.c_float] + [_VP] * 4),
+    "m2rnn_add_norm_fwd": (ctypes.c_int, [_VP] * 6 + [ctypes.c_float] + [_VP] * 3),
+    "m2rnn_add_norm_q8": (ctypes.c_int, [_VP] * 6 + [ctypes.c_float] + [_VP] * 4),
     "m2rnn_add_norm_bwd_workspace_size": (ctypes.c_size_t, [_VP]),
-    "m2rnn_add_norm_bwd": (ctypes.c_int, [_VP, _VP, _LL, _VP, ctypes.c_float] + [_VP] * 5 +
+    "m2rnn_add_norm_bwd": (ctypes.c_int, [_VP] * 4 + [ctypes.c_float] + [_VP] * 5 +
                            [ctypes.c_size_t, _VP]),
-    "m2rnn_quant_rows": (ctypes.c_int, [_VP, _VP, _LL, _VP, _VP, _VP]),
+    "m2rnn_quant_rows": (ctypes.c_int, [_VP] * 6),
     "m2rnn_glu_fwd_workspace_size": (ctypes.c_size_t, [_VP]),
     "m2rnn_glu_fwd": (ctypes.c_int, [_VP, _VP, _LL] + [_VP] * 4 + [ctypes.c_size_t, _VP]),
     "m2rnn_glu_bwd_workspace_size": (ctypes.c_size_t, [_VP]),
@@ -878,7 +878,8 @@ def scan_step(q, k, v, a, alpha, beta, H, w_r=None, *, H_out=None, y=None, strea
 
 
 class NormShape(ctypes.Structure):
-    _fields_ = [("M", ctypes.c_longlong), ("D", ctypes.c_int), ("in_dtype", ctypes.c_int)]
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int),
+                ("in_dtype", ctypes.c_int)]
 
 
 class GluShape(ctypes.Structure):
@@ -933,16 +934,36 @@ def _like(t, x, name: str):
     return torch.empty(x.shape, device=x.device, dtype=x.dtype)
 
 
+def _norm_shape(x, *others):
+    """Shape of a call on x [..., D], and the row arguments of x and ``others`` (None
+    among them allowed).  Items and tokens of three dimensions may lie at any distance; rows
+    of other numbers of dimensions are evenly spaced."""
+    if x.dim() < 1:
+        raise ValueError("there must be a feature dimension")
+    code, D = _dtype_code(x), x.shape[-1]
+    if x.dim() == 3:
+        s = NormShape(x.shape[0], x.shape[1], D, code)
+    else:
+        s = NormShape(1, x.numel() // D if D else 0, D, code)
+    rows = []
+    for t in (x, *others):
+        if t is None or (t.is_contiguous() and t.is_cuda):
+            rows.append(None)
+        elif t.dim() == 3:
+            rows.append(ctypes.byref(_rows(t, 2)))
+        else:
+            M, row = _token_rows("an input", t)
+            rows.append(ctypes.byref(Rows(M * row, row)))
+    return s, rows
+
+
 def _norm_args(x, res, w):
-    code, (M, x_row) = _dtype_code(x), _token_rows("x", x)
-    D, res_row = x.shape[-1], 0
-    if res is not None:
-        if res.dtype is not x.dtype or res.shape != x.shape:
-            _expect("res", res, x.shape, x.dtype)
-        res_row = _token_rows("res", res)[1]
-    if w is not None and (w.dtype is not x.dtype or w.shape != (D,)):
-        _expect("w", w, (D,), x.dtype)
-    return NormShape(M, D, code), x_row, res_row
+    if res is not None and (res.dtype is not x.dtype or res.shape != x.shape):
+        _expect("res", res, x.shape, x.dtype)
+    s, rows = _norm_shape(x, res)
+    if w is not None and (w.dtype is not x.dtype or w.shape != (s.D,)):
+        _expect("w", w, (s.D,), x.dtype)
+    return s, rows
 
 
 @_on_stream
@@ -950,16 +971,16 @@ def add_norm_fwd(x, res=None, w=None, eps: float = 1e-6, *, out=None, stream=Non
     """r = x + res, stored in x's dtype, and y = w (.) r (mean r^2 + eps)^(-1/2) over the
     features of what is stored.  Returns (y, r); r is None without ``res``.
 
-    x, res [..., D] (rows may be evenly spaced slices); w [D] or None (1); one dtype (bf16
+    x, res [..., D] (rows may be slices of wider buffers); w [D] or None (1); one dtype (bf16
     or f32).  ``out`` may supply y and r; r may be ``res`` or x itself (in place)."""
-    s, x_row, res_row = _norm_args(x, res, w)
+    s, (x_rows, res_rows) = _norm_args(x, res, w)
     y, r = _given(out, "y", "r")
     y = _like(y, x, "y")
     if res is not None:
         r = _like(r, x, "r")
     elif r is not None:
         raise ValueError("r goes with res")
-    rc = lib().m2rnn_add_norm_fwd(ctypes.byref(s), _at(x), x_row, _at(res), res_row, _addr(w), eps,
+    rc = lib().m2rnn_add_norm_fwd(ctypes.byref(s), _at(x), x_rows, _at(res), res_rows, _addr(w), eps,
                                   _addr(r), _addr(y), _stream_of(stream, x))
     _check(rc, "m2rnn_add_norm_fwd")
     return y, r
@@ -969,7 +990,7 @@ def add_norm_fwd(x, res=None, w=None, eps: float = 1e-6, *, out=None, stream=Non
 def add_norm_q8(x, res=None, w=None, eps: float = 1e-6, *, out=None, stream=None):
     """``add_norm_fwd`` with y in 8 bits: returns (q [..., D] float8_e4m3fn, scale [...]
     fp32, r), y about q * scale.  ``out`` may supply q, scale and r."""
-    s, x_row, res_row = _norm_args(x, res, w)
+    s, (x_rows, res_rows) = _norm_args(x, res, w)
     q, scale, r = _given(out, "q", "scale", "r")
     q = _out(q, x.shape, torch.float8_e4m3fn, x.device, "q")
     scale = _out(scale, x.shape[:-1], torch.float32, x.device, "scale")
@@ -977,7 +998,7 @@ def add_norm_q8(x, res=None, w=None, eps: float = 1e-6, *, out=None, stream=None
         r = _like(r, x, "r")
     elif r is not None:
         raise ValueError("r goes with res")
-    rc = lib().m2rnn_add_norm_q8(ctypes.byref(s), _at(x), x_row, _at(res), res_row, _addr(w), eps,
+    rc = lib().m2rnn_add_norm_q8(ctypes.byref(s), _at(x), x_rows, _at(res), res_rows, _addr(w), eps,
                                  _addr(r), _addr(q), _addr(scale), _stream_of(stream, x))
     _check(rc, "m2rnn_add_norm_q8")
     return q, scale, r
@@ -990,16 +1011,15 @@ def add_norm_bwd(r, dy, w=None, dr=None, eps: float = 1e-6, *, want_dw: bool = T
     ``res``): dict(dx, dw).  dy is dL/dy and dr dL/dr past the norm (None = 0), of r's
     dtype; dx (r's dtype) is the gradient of x and of res alike; dw [D] is fp32
     (None without a weight or with want_dw=False).  dx may be dr or dy itself."""
-    code, (M, row) = _dtype_code(r), _token_rows("r", r)
-    D, dev = r.shape[-1], r.device
+    s, (rows,) = _norm_shape(r)
+    D, dev = s.D, r.device
     _expect_all(r.dtype, ("w", w, (D,)), ("dy", dy, r.shape), ("dr", dr, r.shape))
-    s = NormShape(M, D, code)
     dx, dw = _given(out, "dx", "dw")
     dx = _like(dx, r, "dx")
     dw = _out(dw, (D,), torch.float32, dev, "dw") if w is not None and want_dw else None
     need = int(lib().m2rnn_add_norm_bwd_workspace_size(ctypes.byref(s))) if dw is not None else 0
     ws = _workspace(workspace, need, dev)
-    rc = lib().m2rnn_add_norm_bwd(ctypes.byref(s), _at(r), row, _addr(w), eps, _addr(dy), _addr(dr),
+    rc = lib().m2rnn_add_norm_bwd(ctypes.byref(s), _at(r), rows, _addr(w), eps, _addr(dy), _addr(dr),
                                   _addr(dx), _addr(dw), _addr(ws), _nbytes(ws), _stream_of(stream, r))
     _check(rc, "m2rnn_add_norm_bwd")
     return {"dx": dx, "dw": dw}
@@ -1007,15 +1027,14 @@ def add_norm_bwd(r, dy, w=None, dr=None, eps: float = 1e-6, *, want_dw: bool = T
 
 @_on_stream
 def quant_rows(x, *, out=None, stream=None):
-    """x [..., D] (bf16 or f32; rows may be evenly spaced slices) in 8 bits with a scale per
+    """x [..., D] (bf16 or f32; rows may be slices of wider buffers) in 8 bits with a scale per
     row: (q float8_e4m3fn, scale [...] fp32), scale = max|row| / 448, q the nearest
     code of row / scale.  ``out`` may supply q and scale."""
-    code, (M, row) = _dtype_code(x), _token_rows("x", x)
-    s = NormShape(M, x.shape[-1], code)
+    s, (rows,) = _norm_shape(x)
     q, scale = _given(out, "q", "scale")
     q = _out(q, x.shape, torch.float8_e4m3fn, x.device, "q")
     scale = _out(scale, x.shape[:-1], torch.float32, x.device, "scale")
-    rc = lib().m2rnn_quant_rows(ctypes.byref(s), _at(x), row, _addr(q), _addr(scale),
+    rc = lib().m2rnn_quant_rows(ctypes.byref(s), _at(x), rows, _addr(q), _addr(scale),
                                 _stream_of(stream, x))
     _check(rc, "m2rnn_quant_rows")
     return q, scale
