@@ -84,7 +84,7 @@ struct GemmParams {
 struct GemmKind {
   int epi;
   bool e4m3, f32, a_mn, b_mn;
-  int bn;  // accumulator columns of a tile: 128 or 256
+  int bn, rows;  // a tile's accumulator columns and rows: 128 or 256
 };
 cudaError_t launch_gemm(const GemmParams& p, const GemmKind& k, int sms, cudaStream_t st);
 struct GemmPlan {

@@ -38,9 +38,9 @@ struct GemmCfg {
   static constexpr int TERMS = F32 ? 3 : 1;
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BR * 128;  // of a term
   static constexpr int STAGE = TERMS * (A_BYTES + B_BYTES);
-  static constexpr int STAGES = 216 * 1024 / STAGE;  // (6 of 32 KB, 3 of 72 KB)
-  // bf16 outputs and what they read pass through 2 KB of each output warp
-  static constexpr int STAGED = F32 ? 0 : 2048;
+  static constexpr int STAGES = 216 * 1024 / STAGE;  // (6 of 32 KB, 3 of 72 KB, 2 of 96 KB)
+  // bf16 outputs and what they read pass through 2 KB of each output warp (where there is room)
+  static constexpr int STAGED = F32 && CG == 2 ? 0 : 2048;
   static constexpr int SMEM = STAGES * STAGE + 1024 + 8 * STAGED;
   static constexpr int ACC = F32 ? 2 * BN : BN;  // columns of a set of accumulators
   static constexpr int TCOLS = 2 * ACC;
@@ -306,12 +306,13 @@ __device__ __forceinline__ void finish_bf16(const GemmParams& p, const TileAt& t
   }
 }
 
-// fp32: one row's 32 columns.
+// fp32: one row's 32 columns (all lanes of the warp are here).
 template <class C>
-__device__ __forceinline__ void finish_f32(const GemmParams& p, const TileAt& t, long long row, int col, float (&g)[32],
-                                           float (&u)[32]) {
-  const int cols = min(32, p.N - col);
-  if (row >= p.M || cols <= 0) return;
+__device__ __forceinline__ void finish_f32(const GemmParams& p, const TileAt& t, long long row0, int col, int lane,
+                                           uint32_t buf, float (&g)[32], float (&u)[32]) {
+  const long long row = row0 + lane;
+  const int cols = row < p.M ? min(32, p.N - col) : 0;  // of the lane's row
+  if (C::EPI != EPI_DGLU && cols <= 0) return;
   const size_t at = static_cast<size_t>(row) * p.N + col, extent = static_cast<size_t>(p.M) * p.N;
   if constexpr (C::EPI == EPI_GLU) {
 #pragma unroll
@@ -335,7 +336,10 @@ __device__ __forceinline__ void finish_f32(const GemmParams& p, const TileAt& t,
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
         next_term(which ? u : g, d);
-        store32<false>(out, (which * 3 + k) * plane + to, cols, d, 6 * plane, p.status, CHK_GLU_WS);
+        if constexpr (C::STAGED > 0)
+          block_store(out + (which * 3 + k) * plane, block_of(p, row0, col, p.pitch), buf, lane, d, p.status, CHK_GLU_WS);
+        else
+          store32<false>(out, (which * 3 + k) * plane + to, cols, d, 6 * plane, p.status, CHK_GLU_WS);
       }
   } else {
     if (t.part >= 0)
@@ -494,6 +498,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
       const long long row0 = static_cast<long long>(at.m) * C::BM + rank * 128 + (warp & 3) * 32;
       const int col0 = at.n * C::OUT_N;
       if constexpr (C::F32) {
+        const uint32_t buf = base + C::STAGES * C::STAGE + warp * C::STAGED;
         float sum[C::PAIR ? 2 : 1][C::BLOCKS][32];
         for (int c = at.k0; c < at.k1; c += p.kc, ++acc) {
           const int ab = acc & 1;
@@ -519,7 +524,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
         if (ok) {
 #pragma unroll
           for (int b = 0; b < C::BLOCKS; ++b)
-            finish_f32<C>(p, at, row0 + lane, col0 + 32 * (half + b), sum[0][b], sum[C::PAIR ? 1 : 0][b]);
+            finish_f32<C>(p, at, row0, col0 + 32 * (half + b), lane, buf, sum[0][b], sum[C::PAIR ? 1 : 0][b]);
         }
       } else {
         const int ab = acc & 1;

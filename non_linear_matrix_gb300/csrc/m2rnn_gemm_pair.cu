@@ -9,7 +9,9 @@ cudaError_t launch_gemm_grad(const GemmParams& p, const GemmKind& k, int sms, cu
 cudaError_t launch_gemm(const GemmParams& p, const GemmKind& k, int sms, cudaStream_t st) {
   switch (k.epi) {
     case EPI_GLU:
-      if (k.f32) return launch_cfg<GemmCfg<EPI_GLU, false, true, false, false, 128, 2>>(p, sms, st);
+      if (k.f32)
+        return k.rows == 256 ? launch_cfg<GemmCfg<EPI_GLU, false, true, false, false, 128, 2>>(p, sms, st)
+                             : launch_cfg<GemmCfg<EPI_GLU, false, true, false, false, 128, 1>>(p, sms, st);
       return k.bn == 256 ? launch_cfg<GemmCfg<EPI_GLU, false, false, false, false, 256, 2>>(p, sms, st)
                          : launch_cfg<GemmCfg<EPI_GLU, false, false, false, false, 128, 1>>(p, sms, st);
     case EPI_GLU8:
@@ -24,7 +26,9 @@ cudaError_t launch_gemm(const GemmParams& p, const GemmKind& k, int sms, cudaStr
 }
 
 // Tiles of 256 x 256 by a pair of CTAs where there are as many as pairs (76, two to each of
-// 152 SMs); otherwise 128 x 128 by a CTA.  fp32: 256 x 128 by a pair, whose terms and sums fit.
+// 152 SMs); otherwise 128 x 128 by a CTA.  fp32: 256 x 128 by a pair, whose
+// terms and sums fit, or 128 x 128 by a CTA, which takes a fifth longer for its tile (shared memory
+// feeds the products), where that makes fewer waves.
 // The tiles beyond whole waves are cut along K into as many parts as leave every pair or
 // CTA one, each of 8 K tiles at least.
 GemmPlan gemm_plan(int epi, bool f32, long long m, int n, int nbatch, int nseg, int kt) {
@@ -42,7 +46,12 @@ GemmPlan gemm_plan(int epi, bool f32, long long m, int n, int nbatch, int nseg, 
   };
   int count, at_once = kSms / 2;
   if (f32) {
+    const int singles = tiles(128, 128), waves = (singles + kSms - 1) / kSms;
     count = tiles(256, 128);
+    if (5 * waves < 4 * ((count + at_once - 1) / at_once)) {
+      count = tiles(128, 128);
+      at_once = kSms;
+    }
   } else if ((count = tiles(256, 256)) < at_once) {
     count = tiles(128, 128);
     at_once = kSms;
