@@ -14,8 +14,6 @@
 namespace m2rnn {
 namespace {
 
-constexpr int kWarps = 8;
-
 __device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -68,14 +66,14 @@ __device__ __forceinline__ void split8(const uint32_t (&w)[8], uint32_t (&t)[3][
 }
 
 // NT: groups of 8 tokens; PAIR: two weights; UN: pieces in flight.
-template <int EPI, bool E4M3, bool F32, int NT>
-__global__ void __launch_bounds__(kWarps * 32) few_kernel(FewParams p) {
+template <int EPI, bool E4M3, bool F32, int NT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) few_kernel(FewParams p) {
   constexpr bool PAIR = EPI != EPI_LIN8;
   constexpr int NW = PAIR ? 2 : 1, TOK = 8 * NT;
   constexpr int UN = F32 ? 1 : NT <= 2 ? 4 : 2;
   using P = Piece<E4M3, F32>;
   constexpr int STEP = 4 * P::ELEMS;  // k of a piece of a warp
-  extern __shared__ float sums[];     // [kWarps][NW][TOK][17]
+  extern __shared__ float sums[];     // [WARPS][NW][TOK][17]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int f0 = blockIdx.x * 16;
   const size_t w_ext = static_cast<size_t>(p.F) * p.D, x_ext = static_cast<size_t>(p.M - 1) * p.x_row + p.D;
@@ -93,7 +91,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(FewParams p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[s][m][t][i] = 0.f;
   const bool r0 = f0 + g < p.F, r1 = f0 + g + 8 < p.F;
-  for (int k0 = warp * UN * STEP; k0 < p.D; k0 += kWarps * UN * STEP) {
+  for (int k0 = warp * UN * STEP; k0 < p.D; k0 += WARPS * UN * STEP) {
     P a[UN][NW][2];
 #pragma unroll
     for (int q = 0; q < UN; ++q) {
@@ -166,7 +164,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(FewParams p) {
         sums[((warp * NW + m) * TOK + 8 * t + 2 * c + (i & 1)) * 17 + g + 8 * (i >> 1)] = v;
       }
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * TOK; i += kWarps * 32) {
+  for (int i = threadIdx.x; i < 16 * TOK; i += WARPS * 32) {
     const int r = i & 15, tok = i >> 4, f = f0 + r;
     if (f >= p.F || tok >= p.M) continue;
     float s[NW];
@@ -174,7 +172,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(FewParams p) {
     for (int m = 0; m < NW; ++m) {
       s[m] = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s[m] += sums[((w * NW + m) * TOK + tok) * 17 + r];
+      for (int w = 0; w < WARPS; ++w) s[m] += sums[((w * NW + m) * TOK + tok) * 17 + r];
     }
     float o;
     if constexpr (E4M3) {
@@ -200,23 +198,35 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(FewParams p) {
   }
 }
 
-template <int EPI, bool E4M3, bool F32, int NT>
-cudaError_t launch_nt(const FewParams& p, cudaStream_t st) {
+template <int EPI, bool E4M3, bool F32, int NT, int WARPS>
+cudaError_t launch_warps(const FewParams& p, cudaStream_t st) {
   constexpr int NW = EPI != EPI_LIN8 ? 2 : 1;
-  constexpr int smem = kWarps * NW * 8 * NT * 17 * 4;
+  constexpr int smem = WARPS * NW * 8 * NT * 17 * 4;
   if (smem > 48 * 1024) {
     static bool ready[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !ready[dev]) {
-      e = cudaFuncSetAttribute(few_kernel<EPI, E4M3, F32, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      e = cudaFuncSetAttribute(few_kernel<EPI, E4M3, F32, NT, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
       if (dev < 64) ready[dev] = true;
     }
   }
-  few_kernel<EPI, E4M3, F32, NT><<<(p.F + 15) / 16, kWarps * 32, smem, st>>>(p);
+  few_kernel<EPI, E4M3, F32, NT, WARPS><<<(p.F + 15) / 16, WARPS * 32, smem, st>>>(p);
   return cudaGetLastError();
+}
+// 16 warps where each of 152 SMs gets one CTA at most and a row has 4 KB, so that every warp has
+// a run of pieces; 8 otherwise.  us for 8 tokens, 8 and 16 warps: the 8-bit product D=5632
+// F=2048 8.1, 6.5; gated, bf16, D=2048 F=2432 7.4, 6.8, D=1024 F=2048 (2 KB) 4.8, 5.2; D=2048
+// F=5632 (352 CTAs) 10.3, 13.7.
+template <int EPI, bool E4M3, bool F32, int NT>
+cudaError_t launch_nt(const FewParams& p, cudaStream_t st) {
+  constexpr int E = E4M3 ? 1 : F32 ? 4 : 2;
+  if constexpr (NT <= 2) {
+    if (p.F <= 16 * 152 && p.D * E >= 4096) return launch_warps<EPI, E4M3, F32, NT, 16>(p, st);
+  }
+  return launch_warps<EPI, E4M3, F32, NT, 8>(p, st);
 }
 template <int EPI, bool E4M3, bool F32>
 cudaError_t launch_t(const FewParams& p, cudaStream_t st) {
