@@ -186,15 +186,18 @@ __global__ void __launch_bounds__(512) add_norm_kernel(Norm2Params p, int warps,
   }
 }
 
-// The quantiser: a CTA per row, whose threads keep four vectors each; what is behind those is
-// read a second time.
-template <bool F32>
-__global__ void __launch_bounds__(256, F32 ? 4 : 5) quant_rows_kernel(Norm2Params p) {
+// The quantiser: a CTA per row (four rows where one warp holds a row), whose threads keep NV
+// vectors each; what is behind those is read a second time.  Bound by HBM where enough
+// is in flight: M=16384 D=5632 bf16 42 us (floor 41), 51 with 256 threads of four vectors.
+template <bool F32, int NV>
+__global__ void __launch_bounds__(256, F32 ? (NV == 4 ? 4 : NV == 6 ? 3 : 2) : (NV == 8 ? 3 : 4))
+    quant_rows_kernel(Norm2Params p, int threads) {
   using T = typename Elem<F32>::T;
-  constexpr int NV = 4;
   __shared__ float sm[32];
-  const int vecs = p.D / 8, step = blockDim.x;
-  const long long row = blockIdx.x;
+  const int vecs = p.D / 8, step = threads;
+  const int lane = threads == 32 ? threadIdx.x & 31 : threadIdx.x;
+  const long long row = threads == 32 ? static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  if (row >= p.M) return;  // (whole warps)
   const size_t n = static_cast<size_t>(p.M) * p.D, at = static_cast<size_t>(row) * p.D;
   const size_t x0 = row_at(p, row, p.xb, p.xt), x_ext = rows_span(p, p.xb, p.xt);
   const T* x = static_cast<const T*>(p.x) + x0;
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(256, F32 ? 4 : 5) quant_rows_kernel(Norm2Param
   };
   Raw<F32, 8> keep[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) keep[i] = load(threadIdx.x + i * step);
+  for (int i = 0; i < NV; ++i) keep[i] = load(lane + i * step);
   float top[1] = {0.f};
   __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);  // bf16: the largest of packed pairs, exact
   const auto take = [&](const Raw<F32, 8>& r) {
@@ -221,12 +224,12 @@ __global__ void __launch_bounds__(256, F32 ? 4 : 5) quant_rows_kernel(Norm2Param
   };
 #pragma unroll
   for (int i = 0; i < NV; ++i) take(keep[i]);
-  for (int v = threadIdx.x + NV * step; v < vecs; v += step) take(load(v));
+  for (int v = lane + NV * step; v < vecs; v += step) take(load(v));
   if constexpr (!F32) top[0] = nan_max(__low2float(top2), __high2float(top2));
-  row_reduce<1, true>(top, blockDim.x / 32, sm);
+  row_reduce<1, true>(top, threads / 32, sm);
   const float scale = __fdiv_rn(top[0], kE4m3Max);
   const Reciprocal inv = reciprocal_of(scale);
-  if (threadIdx.x == 0 && in_range(p.status, row, 1, p.M, CHK_NORM2_OUT)) p.scale[row] = scale;
+  if (lane == 0 && in_range(p.status, row, 1, p.M, CHK_NORM2_OUT)) p.scale[row] = scale;
   const auto put = [&](int v, const Raw<F32, 8>& r) {
     float o[8];
     raw_unpack<F32, 8>(r, o);
@@ -234,8 +237,8 @@ __global__ void __launch_bounds__(256, F32 ? 4 : 5) quant_rows_kernel(Norm2Param
       *reinterpret_cast<uint2*>(p.q + at + 8 * v) = codes8(o, inv);
   };
 #pragma unroll
-  for (int i = 0; i < NV; ++i) put(threadIdx.x + i * step, keep[i]);
-  for (int v = threadIdx.x + NV * step; v < vecs; v += step) put(v, load(v));
+  for (int i = 0; i < NV; ++i) put(lane + i * step, keep[i]);
+  for (int v = lane + NV * step; v < vecs; v += step) put(v, load(v));
 }
 
 // Backward: with n = r rstd, p = w dy:  dx = dr + rstd (p - n mean(p n)),  dw = sum dy n.
@@ -496,15 +499,24 @@ cudaError_t launch_add_norm(const Norm2Params& p, bool f32, int sms, cudaStream_
 cudaError_t launch_add_norm_bwd(const Norm2Params& p, bool f32, cudaStream_t st) {
   return f32 ? launch_bwd_t<true>(p, st) : launch_bwd_t<false>(p, st);
 }
-cudaError_t launch_quant_rows(const Norm2Params& p, bool f32, int sms, cudaStream_t st) {
-  (void)sms;
+template <bool F32>
+static cudaError_t launch_quant_t(const Norm2Params& p, cudaStream_t st) {
+  // the fewest threads that hold the row in six vectors each (256: as many as it takes)
+  const int vecs = p.D / 8;
   int threads = 32;
-  while (threads < 256 && threads * 8 < p.D) threads *= 2;
-  if (f32)
-    quant_rows_kernel<true><<<static_cast<unsigned>(p.M), threads, 0, st>>>(p);
+  while (threads < 256 && threads * 6 < vecs) threads *= 2;
+  const int per = threads == 32 ? 4 : 1, cta = threads * per;
+  const unsigned grid = static_cast<unsigned>((p.M + per - 1) / per);
+  if (vecs <= 4 * threads)
+    quant_rows_kernel<F32, 4><<<grid, cta, 0, st>>>(p, threads);
+  else if (vecs <= 6 * threads)
+    quant_rows_kernel<F32, 6><<<grid, cta, 0, st>>>(p, threads);
   else
-    quant_rows_kernel<false><<<static_cast<unsigned>(p.M), threads, 0, st>>>(p);
+    quant_rows_kernel<F32, 8><<<grid, cta, 0, st>>>(p, threads);
   return cudaGetLastError();
+}
+cudaError_t launch_quant_rows(const Norm2Params& p, bool f32, cudaStream_t st) {
+  return f32 ? launch_quant_t<true>(p, st) : launch_quant_t<false>(p, st);
 }
 
 }  // namespace m2rnn

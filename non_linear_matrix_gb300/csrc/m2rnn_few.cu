@@ -176,9 +176,10 @@ __global__ void __launch_bounds__(WARPS * 32) few_kernel(FewParams p) {
     }
     float o;
     if constexpr (E4M3) {
-      const float sa = __ldg(p.sa + tok);
-      s[0] *= sa * __ldg(p.sb0 + f);
-      if constexpr (PAIR) s[NW - 1] *= sa * __ldg(p.sb1 + f);
+      const float sa = in_range(p.status, tok, 1, p.M, CHK_GLU_IN) ? __ldg(p.sa + tok) : 0.f;
+      const bool in = in_range(p.status, f, 1, p.F, CHK_GLU_IN);
+      s[0] *= sa * (in ? __ldg(p.sb0 + f) : 0.f);
+      if constexpr (PAIR) s[NW - 1] *= sa * (in ? __ldg(p.sb1 + f) : 0.f);
     }
     if constexpr (PAIR) {
       o = act_of<F32>(s[0], p.act) * s[NW - 1];

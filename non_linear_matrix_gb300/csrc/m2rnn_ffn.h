@@ -48,7 +48,7 @@ struct Norm2Params {
 cudaError_t launch_add_norm(const Norm2Params& p, bool f32, int sms, cudaStream_t st);
 cudaError_t launch_add_norm_bwd(const Norm2Params& p, bool f32, cudaStream_t st);
 int add_norm_bwd_parts(const m2rnn_norm_shape* s);
-cudaError_t launch_quant_rows(const Norm2Params& p, bool f32, int sms, cudaStream_t st);
+cudaError_t launch_quant_rows(const Norm2Params& p, bool f32, cudaStream_t st);
 
 // Products on the 5th-generation tensor core: out[m][n] = sum over segments and k of
 // A[z][m][k] B[z][n][k], A and B as tensor maps of three dimensions.

@@ -371,7 +371,7 @@ int m2rnn_quant_rows(const m2rnn_norm_shape* s, const void* x, const m2rnn_rows*
   p.scale = scale;
   p.status = status;
   return status_from_cuda(
-      m2rnn::launch_quant_rows(p, s->in_dtype == M2RNN_F32, sms, static_cast<cudaStream_t>(stream)));
+      m2rnn::launch_quant_rows(p, s->in_dtype == M2RNN_F32, static_cast<cudaStream_t>(stream)));
 }
 
 size_t m2rnn_glu_fwd_workspace_size(const m2rnn_glu_shape* s) {

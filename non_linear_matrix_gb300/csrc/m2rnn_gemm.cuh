@@ -150,13 +150,15 @@ __device__ __forceinline__ void load32(const void* in, size_t at, int cols, floa
   }
 }
 
-// 32 scales (the same ones for the whole warp).
-__device__ __forceinline__ void load32_const(const float* in, int at, int cols, float (&v)[32], size_t extent,
+// 32 scales (the same ones for the whole warp).  Plain loads, as of everything here: a kernel
+// before may still write what this one reads when it becomes resident (await_before).
+__device__ __forceinline__ void load32_scales(const float* in, int at, int cols, float (&v)[32], size_t extent,
                                              int* status) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (8 * i < cols && in_range(status, at + 8 * i, 8, extent, CHK_GLU_IN)) load_vec<true, 8>(in + at + 8 * i, o);
+    if (8 * i < cols && in_range(status, at + 8 * i, 8, extent, CHK_GLU_IN))
+      raw_unpack<true, 8>(raw_load<true, 8, false>(in + at + 8 * i), o);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[8 * i + j] = o[j];
   }
@@ -287,14 +289,14 @@ __device__ __forceinline__ void finish_bf16(const GemmParams& p, const TileAt& t
     else
       block_store(static_cast<__nv_bfloat16*>(t.batch ? p.out[1] : p.out[0]), k, buf, lane, g, p.status, CHK_GLU_OUT);
   } else {
-    const float sa = lane < k.rows ? __ldg(p.sa + row0 + lane) : 0.f;
+    const float sa = lane < k.rows && in_range(p.status, row0 + lane, 1, p.M, CHK_GLU_IN) ? p.sa[row0 + lane] : 0.f;
     const size_t n = static_cast<size_t>(p.N);
     float s[32];
-    load32_const(p.sb0, col, k.cols, s, n, p.status);
+    load32_scales(p.sb0, col, k.cols, s, n, p.status);
 #pragma unroll
     for (int i = 0; i < 32; ++i) g[i] *= sa * s[i];
     if constexpr (C::EPI == EPI_GLU8) {
-      load32_const(p.sb1, col, k.cols, s, n, p.status);
+      load32_scales(p.sb1, col, k.cols, s, n, p.status);
 #pragma unroll
       for (int i = 0; i < 32; ++i) g[i] = act_of<false>(g[i], p.act) * (u[i] * (sa * s[i]));
     } else if (p.in != nullptr) {

@@ -111,6 +111,8 @@ def _load(path: str, how: str) -> ctypes.CDLL:
 def lib() -> ctypes.CDLL:
     """The loaded native library (raises if it was never built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if os.environ.get("M2RNN_LIBRARY") == "checked":
