@@ -61,7 +61,8 @@ enum GemmEpi : int {
 };
 struct GemmParams {
   CUtensorMap a, b0, b1;  // b1: of a pair, or of the second segment
-  int nseg;               // products that are added up: A's planes with b0, then b1
+  int nseg;               // products that are added up: A's planes one after the other
+  int aterms;             // bf16: planes of A that belong to one of B (b0, then b1)
   int kt;                 // K tiles of a segment
   int kc;                 // K tiles of a chunk (fp32: what one chain of sums takes)
   int mt, nt, nbatch;     // tiles; products that share B, of A's planes one after the other

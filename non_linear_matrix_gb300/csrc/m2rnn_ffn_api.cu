@@ -205,6 +205,7 @@ m2rnn::GemmParams gemm_params(const m2rnn::GemmPlan& q, long long M, int N, int 
   p.kt = kt;
   p.kc = f32 ? kChunkTiles : kt;
   p.nseg = nseg;
+  p.aterms = 1;
   p.mt = q.mt;
   p.nt = q.nt;
   p.nbatch = q.nbatch;
@@ -232,14 +233,26 @@ size_t terms_bytes(const m2rnn_glu_shape* s) {  // of x, wg and wu
   const size_t pitch = pitch_of(s->D);
   return align256(6 * s->M * pitch) + 2 * align256(6 * s->F * pitch);
 }
-size_t dgu_bytes(const m2rnn_glu_shape* s) {  // the gradients of g and u
-  return align256(static_cast<size_t>(s->M) * pitch_of(s->F) * (s->in_dtype == M2RNN_F32 ? 12 : 4));
+// bf16 terms that hold each gradient of g and u between the products: 3 with fp32 inputs.  With bf16
+// inputs 1, whose rounding (2^-9 of each of many terms of a sum) adds as much error to dx, dwg and
+// dwu as their own rounding does (relative 2-norm 2.3e-3 instead of 1.7e-3); a second one
+// costs as much again as the first, 2 x 218 of 870 us at M=32768 D=1024 F=2816, so it is taken
+// up to M D F = 2^30, where that is below 5 us.
+int grad_terms(const m2rnn_glu_shape* s) {
+  if (s->in_dtype == M2RNN_F32) return 3;
+  return static_cast<double>(s->M) * s->D * s->F <= 1073741824.0 ? 2 : 1;
 }
+size_t dgu_bytes(const m2rnn_glu_shape* s) {  // the gradients of g and u
+  return align256(static_cast<size_t>(s->M) * pitch_of(s->F) * (4 * grad_terms(s)));
+}
+// Segments of dx's products; of each weight's gradient half as many.
+int dx_segments(const m2rnn_glu_shape* s) { return s->in_dtype == M2RNN_F32 ? 2 : 2 * grad_terms(s); }
 m2rnn::GemmPlan dx_plan(const m2rnn_glu_shape* s) {
-  return m2rnn::gemm_plan(m2rnn::EPI_STORE, s->in_dtype == M2RNN_F32, s->M, s->D, 1, 2, k_tiles(s->F, 2));
+  return m2rnn::gemm_plan(m2rnn::EPI_STORE, s->in_dtype == M2RNN_F32, s->M, s->D, 1, dx_segments(s), k_tiles(s->F, 2));
 }
 m2rnn::GemmPlan dw_plan(const m2rnn_glu_shape* s) {
-  return m2rnn::gemm_plan(m2rnn::EPI_STORE, s->in_dtype == M2RNN_F32, s->F, s->D, 2, 1, k_tiles(s->M, 2));
+  return m2rnn::gemm_plan(m2rnn::EPI_STORE, s->in_dtype == M2RNN_F32, s->F, s->D, 2, dx_segments(s) / 2,
+                          k_tiles(s->M, 2));
 }
 
 // What the products read: the caller's bf16 matrices, or their terms.
@@ -284,6 +297,7 @@ int run_pair(const m2rnn_glu_shape* s, const Operands& o, int epi, const void* d
     return M2RNN_ERR_CUDA;
   p.out[0] = out;
   p.pitch = epi == m2rnn::EPI_DGLU ? pitch_of(s->F) : s->F;
+  p.aterms = grad_terms(s);
   p.in = dh;
   p.act = s->act;
   return status_from_cuda(m2rnn::launch_gemm(p, {epi, false, f32, false, false, q.bn, q.rows}, sms, st));
@@ -463,16 +477,17 @@ int m2rnn_glu_bwd(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
   Operands o;
   if ((rc = make_operands(s, x, x_row, wg, wu, &ws, status, st, &o)) != M2RNN_OK) return rc;
   const bool f32 = o.terms == 3;
-  const int hrow = pitch_of(s->F);
+  const int hrow = pitch_of(s->F), gt = grad_terms(s), segs = dx_segments(s);
   const long long hp = s->M * hrow;
-  __nv_bfloat16* dgu = ws.take(static_cast<size_t>(2 * o.terms) * hp);
+  __nv_bfloat16* dgu = ws.take(static_cast<size_t>(2 * gt) * hp);
   float* parts = reinterpret_cast<float*>(ws.at);
   if ((rc = run_pair(s, o, m2rnn::EPI_DGLU, dh, dgu, status, sms, st)) != M2RNN_OK) return rc;
   const long long xp = s->M * o.x_row, wp = s->F * o.w_row;
   if (dx != nullptr) {  // dg wg + du wu
     const m2rnn::GemmPlan q = dx_plan(s);
-    m2rnn::GemmParams p = gemm_params(q, s->M, s->D, 2, k_tiles(s->F, 2), f32, status);
-    if (!make_map(&p.a, dgu, 2, s->F, s->M, 2 * o.terms, hrow, hp, 128) ||
+    m2rnn::GemmParams p = gemm_params(q, s->M, s->D, segs, k_tiles(s->F, 2), f32, status);
+    p.aterms = gt;
+    if (!make_map(&p.a, dgu, 2, s->F, s->M, 2 * gt, hrow, hp, 128) ||
         !make_map(&p.b0, o.wg, 2, s->D, s->F, o.terms, o.w_row, f32 ? wp : o.w_row, 64) ||
         !make_map(&p.b1, o.wu, 2, s->D, s->F, o.terms, o.w_row, f32 ? wp : o.w_row, 64))
       return M2RNN_ERR_CUDA;
@@ -483,8 +498,9 @@ int m2rnn_glu_bwd(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
   }
   if (dwg != nullptr) {  // dg^T x and du^T x, which share x
     const m2rnn::GemmPlan q = dw_plan(s);
-    m2rnn::GemmParams p = gemm_params(q, s->F, s->D, 1, k_tiles(s->M, 2), f32, status);
-    if (!make_map(&p.a, dgu, 2, s->F, s->M, 2 * o.terms, hrow, hp, 64) ||
+    m2rnn::GemmParams p = gemm_params(q, s->F, s->D, segs / 2, k_tiles(s->M, 2), f32, status);
+    p.aterms = gt;
+    if (!make_map(&p.a, dgu, 2, s->F, s->M, 2 * gt, hrow, hp, 64) ||
         !make_map(&p.b0, o.x, 2, s->D, s->M, o.terms, o.x_row, f32 ? xp : o.x_row, 64))
       return M2RNN_ERR_CUDA;
     p.b1 = p.b0;

@@ -92,7 +92,7 @@ __device__ __forceinline__ void issue_tile(const GemmParams& p, uint32_t dst, ui
 #pragma unroll
   for (int term = 0; term < C::TERMS; ++term) {
     const uint32_t a = dst + term * C::A_BYTES;
-    const int az = (seg + t.batch) * C::TERMS + term;  // (one of the two counts at a time)
+    const int az = C::F32 ? (seg + t.batch) * 3 + term : seg + t.batch * p.aterms;
     if constexpr (C::A_MN) {
       tc5::copy_box<C::CG>(a, &p.a, m, k, az, bar);
       tc5::copy_box<C::CG>(a + 8192, &p.a, m + 64, k, az, bar);
@@ -110,7 +110,7 @@ __device__ __forceinline__ void issue_tile(const GemmParams& p, uint32_t dst, ui
       }
     } else {
       const int n = t.n * C::OUT_N + rank * C::BR;
-      const CUtensorMap* map = seg ? &p.b1 : &p.b0;
+      const CUtensorMap* map = seg >= (C::F32 ? 1 : p.aterms) ? &p.b1 : &p.b0;
       if constexpr (C::B_MN) {
 #pragma unroll
         for (int i = 0; i < C::BR / 64; ++i) tc5::copy_box<C::CG>(b + 8192 * i, map, n + 64 * i, k, term, bar);
@@ -279,10 +279,18 @@ __device__ __forceinline__ void finish_bf16(const GemmParams& p, const TileAt& t
       g[i] = d[i] * u[i] * s;
       u[i] = d[i] * a;
     }
-    // Rounded to bf16: they are operands of the products to come.
+    // Rounded to bf16, as operands of the products to come; where those are small, what the
+    // rounding leaves follows as a second term.
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out[0]);
+    const size_t plane = static_cast<size_t>(p.M) * p.pitch;
     block_store(out, k, buf, lane, g, p.status, CHK_GLU_WS);
-    block_store(out + static_cast<size_t>(p.M) * p.pitch, k, buf, lane, u, p.status, CHK_GLU_WS);
+    block_store(out + p.aterms * plane, k, buf, lane, u, p.status, CHK_GLU_WS);
+    if (p.aterms == 2) {
+      next_term(g, d);
+      block_store(out + plane, k, buf, lane, g, p.status, CHK_GLU_WS);
+      next_term(u, d);
+      block_store(out + 3 * plane, k, buf, lane, u, p.status, CHK_GLU_WS);
+    }
   } else if constexpr (C::EPI == EPI_STORE) {
     if (t.part >= 0)
       store_part<C>(p, t, row0 + lane, col, g);
