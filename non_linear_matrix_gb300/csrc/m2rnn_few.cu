@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(WARPS * 32) few_kernel(FewParams p) {
       if constexpr (PAIR) s[NW - 1] *= sa * (in ? __ldg(p.sb1 + f) : 0.f);
     }
     if constexpr (PAIR) {
-      o = act_of<F32>(s[0], p.act) * s[NW - 1];
+      o = (F32 ? act_of(s[0], p.act) : act2(both(s[0]), p.act).x) * s[NW - 1];
     } else {
       o = s[0];
       const size_t at = static_cast<size_t>(tok) * p.res_row + f;

@@ -267,17 +267,25 @@ __device__ __forceinline__ void finish_bf16(const GemmParams& p, const TileAt& t
   const Block k = block_of(p, row0, col, C::EPI == EPI_DGLU ? p.pitch : p.N);
   if constexpr (C::EPI == EPI_GLU) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) g[i] = act_of<false>(g[i], p.act) * u[i];
+    for (int i = 0; i < 32; i += 2) {
+      const float2 h = mul2(act2(make_float2(g[i], g[i + 1]), p.act), make_float2(u[i], u[i + 1]));
+      g[i] = h.x;
+      g[i + 1] = h.y;
+    }
     block_store(static_cast<__nv_bfloat16*>(p.out[0]), k, buf, lane, g, p.status, CHK_GLU_OUT);
   } else if constexpr (C::EPI == EPI_DGLU) {
     float d[32];
     block_rows(in, buf, lane, d);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      float a, s;
-      act_grad<false>(g[i], p.act, a, s);
-      g[i] = d[i] * u[i] * s;
-      u[i] = d[i] * a;
+    for (int i = 0; i < 32; i += 2) {
+      const float2 dh = make_float2(d[i], d[i + 1]);
+      float2 a, s;
+      act_grad2(make_float2(g[i], g[i + 1]), p.act, a, s);
+      const float2 dg = mul2(mul2(dh, make_float2(u[i], u[i + 1])), s), du = mul2(dh, a);
+      g[i] = dg.x;
+      g[i + 1] = dg.y;
+      u[i] = du.x;
+      u[i + 1] = du.y;
     }
     // Rounded to bf16, as operands of the products to come; where those are small, what the
     // rounding leaves follows as a second term.
@@ -302,11 +310,20 @@ __device__ __forceinline__ void finish_bf16(const GemmParams& p, const TileAt& t
     float s[32];
     load32_scales(p.sb0, col, k.cols, s, n, p.status);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) g[i] *= sa * s[i];
+    for (int i = 0; i < 32; i += 2) {
+      const float2 v = mul2(make_float2(g[i], g[i + 1]), mul2(both(sa), make_float2(s[i], s[i + 1])));
+      g[i] = v.x;
+      g[i + 1] = v.y;
+    }
     if constexpr (C::EPI == EPI_GLU8) {
       load32_scales(p.sb1, col, k.cols, s, n, p.status);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) g[i] = act_of<false>(g[i], p.act) * (u[i] * (sa * s[i]));
+      for (int i = 0; i < 32; i += 2) {
+        const float2 v = mul2(make_float2(u[i], u[i + 1]), mul2(both(sa), make_float2(s[i], s[i + 1])));
+        const float2 h = mul2(act2(make_float2(g[i], g[i + 1]), p.act), v);
+        g[i] = h.x;
+        g[i + 1] = h.y;
+      }
     } else if (p.in != nullptr) {
       block_rows(in, buf, lane, s);
 #pragma unroll
@@ -326,7 +343,7 @@ __device__ __forceinline__ void finish_f32(const GemmParams& p, const TileAt& t,
   const size_t at = static_cast<size_t>(row) * p.N + col, extent = static_cast<size_t>(p.M) * p.N;
   if constexpr (C::EPI == EPI_GLU) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) g[i] = act_of<true>(g[i], p.act) * u[i];
+    for (int i = 0; i < 32; ++i) g[i] = act_of(g[i], p.act) * u[i];
     store32<true>(p.out[0], at, cols, g, extent, p.status, CHK_GLU_OUT);
   } else if constexpr (C::EPI == EPI_DGLU) {
     float d[32];
@@ -334,7 +351,7 @@ __device__ __forceinline__ void finish_f32(const GemmParams& p, const TileAt& t,
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       float a, s;
-      act_grad<true>(g[i], p.act, a, s);
+      act_grad(g[i], p.act, a, s);
       g[i] = d[i] * u[i] * s;
       u[i] = d[i] * a;
     }
