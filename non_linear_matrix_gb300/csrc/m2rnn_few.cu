@@ -57,9 +57,8 @@ __device__ __forceinline__ void split8(const uint32_t (&w)[8], uint32_t (&t)[3][
   for (int k = 0; k < 3; ++k)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t p = ptx::pack_bf16x2(v[2 * i], v[2 * i + 1]);
-      t[k][i] = p;
-      const float lo = ptx::bf16x2_lo(p), hi = ptx::bf16x2_hi(p);
+      const float lo = bf16_term(v[2 * i]), hi = bf16_term(v[2 * i + 1]);
+      t[k][i] = ptx::pack_bf16x2(lo, hi);
       v[2 * i] = isfinite(lo) ? v[2 * i] - lo : 0.f;
       v[2 * i + 1] = isfinite(hi) ? v[2 * i + 1] - hi : 0.f;
     }

@@ -33,12 +33,13 @@ int check(const void* const (&ptrs)[N], int dev, bool required) {
   return M2RNN_OK;
 }
 
-// A row distance (in elements of e bytes) keeps rows on 16-byte boundaries, and M rows stay
-// below 2^40 elements.
+// A row distance (in elements of e bytes) keeps rows on 16-byte boundaries and is below 2^40
+// bytes (a tensor map's limit), and M rows stay below 2^40 elements.
 int check_row(long long row, size_t e, long long M, long long least) {
   if (row < 0 || row < least) return M2RNN_ERR_INVALID_ARG;
   if ((row * static_cast<long long>(e)) % 16 != 0) return M2RNN_ERR_MISALIGNED;
-  if (static_cast<double>(row) * (M > 0 ? M : 1) >= kMostElems) return M2RNN_ERR_UNSUPPORTED_SHAPE;
+  if (static_cast<double>(row) * (M > 0 ? M : 1) >= kMostElems || static_cast<double>(row) * e >= kMostElems)
+    return M2RNN_ERR_UNSUPPORTED_SHAPE;
   return M2RNN_OK;
 }
 

@@ -164,12 +164,13 @@ __device__ __forceinline__ void load32_scales(const float* in, int at, int cols,
   }
 }
 
-// The bf16 terms of fp32 values: each the rounding of what the ones before leave.  A
-// value that is not finite is its own first term.
+// The next bf16 term of fp32 values: the rounding of what the terms before leave (cut off
+// where rounding would pass bf16's largest value).  A value that is not finite is its
+// own first term.
 __device__ __forceinline__ void next_term(float (&v)[32], float (&t)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    t[i] = __bfloat162float(__float2bfloat16_rn(v[i]));
+    t[i] = bf16_term(v[i]);
     v[i] = isfinite(t[i]) ? v[i] - t[i] : 0.f;
   }
 }
@@ -346,6 +347,7 @@ __device__ __forceinline__ void finish_f32(const GemmParams& p, const TileAt& t,
     for (int i = 0; i < 32; ++i) g[i] = act_of(g[i], p.act) * u[i];
     store32<true>(p.out[0], at, cols, g, extent, p.status, CHK_GLU_OUT);
   } else if constexpr (C::EPI == EPI_DGLU) {
+    static_assert(C::STAGED > 0, "the terms pass through shared memory");
     float d[32];
     load32<true>(p.in, at, cols, d, extent, p.status, CHK_GLU_IN);
 #pragma unroll
@@ -357,16 +359,13 @@ __device__ __forceinline__ void finish_f32(const GemmParams& p, const TileAt& t,
     }
     // as the three terms that the products to come take
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out[0]);
-    const size_t plane = static_cast<size_t>(p.M) * p.pitch, to = static_cast<size_t>(row) * p.pitch + col;
+    const size_t plane = static_cast<size_t>(p.M) * p.pitch;
 #pragma unroll
     for (int which = 0; which < 2; ++which)
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
         next_term(which ? u : g, d);
-        if constexpr (C::STAGED > 0)
-          block_store(out + (which * 3 + k) * plane, block_of(p, row0, col, p.pitch), buf, lane, d, p.status, CHK_GLU_WS);
-        else
-          store32<false>(out, (which * 3 + k) * plane + to, cols, d, 6 * plane, p.status, CHK_GLU_WS);
+        block_store(out + (which * 3 + k) * plane, block_of(p, row0, col, p.pitch), buf, lane, d, p.status, CHK_GLU_WS);
       }
   } else {
     if (t.part >= 0)
@@ -453,7 +452,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
       constexpr uint32_t a_step = C::A_MN ? 2048 : 32, b_step = C::B_MN ? 2048 : 32;
       int it = 0, acc = 0;
       bool ok = true;
-      int site = SITE_GEMM_MMA;
       for (int t = first; t < tiles && ok; t += stride) {
         const TileAt at = tile_at(p, t);
         for (int c = at.k0; c < at.k1 && ok; c += p.kc, ++acc) {
@@ -498,7 +496,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
         }
       }
       if (!ok) {
-        gave_up(p.status, site);
+        gave_up(p.status, SITE_GEMM_MMA);
         tc5::commit<C::CG>(drain);
         if (!ptx::mbar_wait(drain, 0, kDrainNs)) gave_up(p.status, SITE_GEMM_DRAIN);
       }

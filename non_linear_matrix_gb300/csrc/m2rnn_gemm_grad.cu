@@ -6,9 +6,7 @@ namespace m2rnn {
 
 cudaError_t launch_gemm_grad(const GemmParams& p, const GemmKind& k, int sms, cudaStream_t st) {
   if (k.epi == EPI_DGLU) {
-    if (k.f32)
-      return k.rows == 256 ? launch_cfg<GemmCfg<EPI_DGLU, false, true, false, false, 128, 2>>(p, sms, st)
-                           : launch_cfg<GemmCfg<EPI_DGLU, false, true, false, false, 128, 1>>(p, sms, st);
+    if (k.f32) return launch_cfg<GemmCfg<EPI_DGLU, false, true, false, false, 128, 1>>(p, sms, st);
     return k.bn == 256 ? launch_cfg<GemmCfg<EPI_DGLU, false, false, false, false, 256, 2>>(p, sms, st)
                        : launch_cfg<GemmCfg<EPI_DGLU, false, false, false, false, 128, 1>>(p, sms, st);
   }

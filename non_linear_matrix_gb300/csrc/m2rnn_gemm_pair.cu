@@ -28,7 +28,9 @@ cudaError_t launch_gemm(const GemmParams& p, const GemmKind& k, int sms, cudaStr
 // Tiles of 256 x 256 by a pair of CTAs where there are as many as pairs (76, two to each of
 // 152 SMs); otherwise 128 x 128 by a CTA.  fp32: 256 x 128 by a pair, whose
 // terms and sums fit, or 128 x 128 by a CTA, which takes a fifth longer for its tile (shared memory
-// feeds the products), where that makes fewer waves.
+// feeds the products), where that makes fewer waves, and for the gradients of g and u, whose six
+// planes then find room to pass through shared memory (backward pass M=8192 D=512 F=2048 432
+// -> 408 us, M=4096 D=2048 F=4096 equal).
 // The tiles beyond whole waves are cut along K into as many parts as leave every pair or
 // CTA one, each of 8 K tiles at least.
 GemmPlan gemm_plan(int epi, bool f32, long long m, int n, int nbatch, int nseg, int kt) {
@@ -48,7 +50,7 @@ GemmPlan gemm_plan(int epi, bool f32, long long m, int n, int nbatch, int nseg, 
   if (f32) {
     const int singles = tiles(128, 128), waves = (singles + kSms - 1) / kSms;
     count = tiles(256, 128);
-    if (5 * waves < 4 * ((count + at_once - 1) / at_once)) {
+    if (epi == EPI_DGLU || 5 * waves < 4 * ((count + at_once - 1) / at_once)) {
       count = tiles(128, 128);
       at_once = kSms;
     }

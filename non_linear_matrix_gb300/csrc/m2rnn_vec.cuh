@@ -47,6 +47,11 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// The bf16 value that an fp32 value rounds to, or is cut off to where it would round to infinity.
+__device__ __forceinline__ float bf16_term(float v) {
+  const float t = __bfloat162float(__float2bfloat16_rn(v));
+  return isinf(t) && isfinite(v) ? __uint_as_float(__float_as_uint(v) & 0xffff0000u) : t;
+}
 // VEC (2, 4 or 8) consecutive elements as they lie in memory: 4, 8 or 16 bytes
 // of bf16, 8, 16 or 32 bytes of fp32.
 template <bool F32, int VEC>

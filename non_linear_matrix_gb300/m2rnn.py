@@ -1019,10 +1019,12 @@ def add_norm_bwd(r, dy, w=None, dr=None, eps: float = 1e-6, *, want_dw: bool = T
     dx, dw = _given(out, "dx", "dw")
     dx = _like(dx, r, "dx")
     dw = _out(dw, (D,), torch.float32, dev, "dw") if w is not None and want_dw else None
-    need = int(lib().m2rnn_add_norm_bwd_workspace_size(ctypes.byref(s))) if dw is not None else 0
-    ws = _workspace(workspace, need, dev)
-    rc = lib().m2rnn_add_norm_bwd(ctypes.byref(s), _at(r), rows, _addr(w), eps, _addr(dy), _addr(dr),
-                                  _addr(dx), _addr(dw), _addr(ws), _nbytes(ws), _stream_of(stream, r))
+    L, ws = lib(), workspace
+    if ws is None and dw is not None:
+        ws = _workspace(None, L.m2rnn_add_norm_bwd_workspace_size(ctypes.byref(s)), dev)
+    rc = L.m2rnn_add_norm_bwd(ctypes.byref(s), _at(r), rows, _addr(w), eps, _addr(dy), _addr(dr),
+                              _addr(dx), _addr(dw), _addr(ws), 0 if ws is None else _nbytes(ws),
+                              _stream_of(stream, r))
     _check(rc, "m2rnn_add_norm_bwd")
     return {"dx": dx, "dw": dw}
 

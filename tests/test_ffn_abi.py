@@ -97,6 +97,8 @@ def test_glu_refuses_arguments(m):
     fwd = lambda row=64, h=A[3]: L.m2rnn_glu_fwd(s, A[0], row, A[1], A[2], h, None, 0, None)  # noqa: E731
     assert fwd(row=56) == -1 and fwd(row=0) == -1 and fwd(row=68) == -3 and fwd(row=1 << 39) == -2
     assert all(fwd(h=a) == -1 for a in A[:3])
+    one = ctypes.byref(m.GluShape(1, 64, 64, 1, 0))  # a row distance beyond a tensor map's
+    assert L.m2rnn_glu_fwd(one, A[0], 1 << 39, A[1], A[2], A[3], None, 0, None) == -2
     bwd = lambda dx=A[4], dwg=A[5], dwu=A[6]: L.m2rnn_glu_bwd(  # noqa: E731
         s, A[0], 64, A[1], A[2], A[3], dx, dwg, dwu, A[7], SZ, None)
     assert bwd(dwu=None) == -1 and bwd(dwg=None) == -1  # together

@@ -217,6 +217,25 @@ def test_far_arguments_of_the_activation(m, act, dtype):
     assert ((dw - M * da).abs() <= M * (da.abs() * 2.0 ** -6 + 1e-6)).all()
 
 
+@pytest.mark.parametrize("M", [9, 100])
+def test_fp32_values_at_the_end_of_the_range(m, M):
+    """fp32 operands up to the largest value (which bf16's rounding would pass) and down to
+    2^-100, one product to a sum, are held whole: u = x w within four roundings."""
+    top = torch.finfo(torch.float32).max
+    vals = torch.tensor([top, -top, 3.3953e38, 1e30, 1.0, 2.0 ** -60 * 1.2345678, 2.0 ** -100 * 1.7654321, 0.0], device="cuda")
+    D = F = 16
+    x = torch.zeros(M, D, device="cuda")
+    x[:, 0] = 1.0
+    wu = torch.zeros(F, D, device="cuda")
+    wu[:8, 0] = vals
+    wg = torch.zeros(F, D, device="cuda")
+    wg[:, 0] = 1.25
+    h = m.glu_fwd(x, wg, wu)
+    ref = (torch.nn.functional.silu(torch.tensor(1.25, dtype=torch.float64)).item() * wu[:, 0].double()).expand(M, F)
+    fits = ref.abs() <= top
+    assert ((h.double() - ref).abs()[fits] <= ref.abs()[fits] * 2.0 ** -20).all() and torch.isinf(h[~fits]).all()
+
+
 def test_against_differences(m):
     """fp32: the slope of sum(h dh) along a direction of all leaves, central differences
     with step 2^-7: third derivatives of the sum along the unit-scale direction are below
