@@ -901,14 +901,15 @@ def _act(act: str) -> int:
 def _token_rows(name: str, t):
     """Number of rows of t [..., D] and the distance between them: its features packed,
     its tokens evenly spaced."""
-    if t.dim() < 1:
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{name} must have a feature dimension")
-    D = t.shape[-1]
+    D = shape[-1]
     if t.is_contiguous():
-        return t.numel() // D if D else 0, D
+        return (shape[0] if len(shape) == 2 else t.numel() // D if D else 0), D
     if not t.is_cuda:
         raise ValueError("tensors passed to libm2rnn must be CUDA tensors")
-    shape, st = t.shape, t.stride()
+    st = t.stride()
     if 0 in shape:
         return 0, D
     if st[-1] != 1 and D != 1:
@@ -940,23 +941,34 @@ def _norm_shape(x, *others):
     """Shape of a call on x [..., D], and the row arguments of x and ``others`` (None
     among them allowed).  Items and tokens of three dimensions may lie at any distance; rows
     of other numbers of dimensions are evenly spaced."""
-    if x.dim() < 1:
-        raise ValueError("there must be a feature dimension")
-    code, D = _dtype_code(x), x.shape[-1]
-    if x.dim() == 3:
-        s = NormShape(x.shape[0], x.shape[1], D, code)
+    shape, code = x.shape, _dtype_code(x)
+    if len(shape) == 2:
+        s = NormShape(1, shape[0], shape[1], code)
+    elif len(shape) == 3:
+        s = NormShape(*shape, code)
+    elif shape:
+        s = NormShape(1, x.numel() // shape[-1] if shape[-1] else 0, shape[-1], code)
     else:
-        s = NormShape(1, x.numel() // D if D else 0, D, code)
-    rows = []
-    for t in (x, *others):
-        if t is None or (t.is_contiguous() and t.is_cuda):
-            rows.append(None)
-        elif t.dim() == 3:
-            rows.append(ctypes.byref(_rows(t, 2)))
+        raise ValueError("there must be a feature dimension")
+    if x.is_contiguous():
+        for t in others:
+            if t is not None and not t.is_contiguous():
+                break
         else:
-            M, row = _token_rows("an input", t)
-            rows.append(ctypes.byref(Rows(M * row, row)))
-    return s, rows
+            return s, _NO_ROWS
+    return s, [_norm_rows(t) for t in (x, *others)] + [None]
+
+
+_NO_ROWS = (None, None)
+
+
+def _norm_rows(t):
+    if t is None or t.is_contiguous():
+        return None
+    if t.dim() == 3:
+        return ctypes.byref(_rows(t, 2))
+    M, row = _token_rows("an input", t)
+    return ctypes.byref(Rows(M * row, row))
 
 
 def _norm_args(x, res, w):
@@ -975,14 +987,14 @@ def add_norm_fwd(x, res=None, w=None, eps: float = 1e-6, *, out=None, stream=Non
 
     x, res [..., D] (rows may be slices of wider buffers); w [D] or None (1); one dtype (bf16
     or f32).  ``out`` may supply y and r; r may be ``res`` or x itself (in place)."""
-    s, (x_rows, res_rows) = _norm_args(x, res, w)
-    y, r = _given(out, "y", "r")
+    s, rows = _norm_args(x, res, w)
+    y, r = (None, None) if out is None else _given(out, "y", "r")
     y = _like(y, x, "y")
     if res is not None:
         r = _like(r, x, "r")
     elif r is not None:
         raise ValueError("r goes with res")
-    rc = lib().m2rnn_add_norm_fwd(ctypes.byref(s), _at(x), x_rows, _at(res), res_rows, _addr(w), eps,
+    rc = lib().m2rnn_add_norm_fwd(ctypes.byref(s), _at(x), rows[0], _at(res), rows[1], _addr(w), eps,
                                   _addr(r), _addr(y), _stream_of(stream, x))
     _check(rc, "m2rnn_add_norm_fwd")
     return y, r
@@ -992,7 +1004,7 @@ def add_norm_fwd(x, res=None, w=None, eps: float = 1e-6, *, out=None, stream=Non
 def add_norm_q8(x, res=None, w=None, eps: float = 1e-6, *, out=None, stream=None):
     """``add_norm_fwd`` with y in 8 bits: returns (q [..., D] float8_e4m3fn, scale [...]
     fp32, r), y about q * scale.  ``out`` may supply q, scale and r."""
-    s, (x_rows, res_rows) = _norm_args(x, res, w)
+    s, rows = _norm_args(x, res, w)
     q, scale, r = _given(out, "q", "scale", "r")
     q = _out(q, x.shape, torch.float8_e4m3fn, x.device, "q")
     scale = _out(scale, x.shape[:-1], torch.float32, x.device, "scale")
@@ -1000,7 +1012,7 @@ def add_norm_q8(x, res=None, w=None, eps: float = 1e-6, *, out=None, stream=None
         r = _like(r, x, "r")
     elif r is not None:
         raise ValueError("r goes with res")
-    rc = lib().m2rnn_add_norm_q8(ctypes.byref(s), _at(x), x_rows, _at(res), res_rows, _addr(w), eps,
+    rc = lib().m2rnn_add_norm_q8(ctypes.byref(s), _at(x), rows[0], _at(res), rows[1], _addr(w), eps,
                                  _addr(r), _addr(q), _addr(scale), _stream_of(stream, x))
     _check(rc, "m2rnn_add_norm_q8")
     return q, scale, r
@@ -1013,7 +1025,7 @@ def add_norm_bwd(r, dy, w=None, dr=None, eps: float = 1e-6, *, want_dw: bool = T
     ``res``): dict(dx, dw).  dy is dL/dy and dr dL/dr past the norm (None = 0), of r's
     dtype; dx (r's dtype) is the gradient of x and of res alike; dw [D] is fp32
     (None without a weight or with want_dw=False).  dx may be dr or dy itself."""
-    s, (rows,) = _norm_shape(r)
+    s, rows = _norm_shape(r)
     D, dev = s.D, r.device
     _expect_all(r.dtype, ("w", w, (D,)), ("dy", dy, r.shape), ("dr", dr, r.shape))
     dx, dw = _given(out, "dx", "dw")
@@ -1022,7 +1034,7 @@ def add_norm_bwd(r, dy, w=None, dr=None, eps: float = 1e-6, *, want_dw: bool = T
     L, ws = lib(), workspace
     if ws is None and dw is not None:
         ws = _workspace(None, L.m2rnn_add_norm_bwd_workspace_size(ctypes.byref(s)), dev)
-    rc = L.m2rnn_add_norm_bwd(ctypes.byref(s), _at(r), rows, _addr(w), eps, _addr(dy), _addr(dr),
+    rc = L.m2rnn_add_norm_bwd(ctypes.byref(s), _at(r), rows[0], _addr(w), eps, _addr(dy), _addr(dr),
                               _addr(dx), _addr(dw), _addr(ws), 0 if ws is None else _nbytes(ws),
                               _stream_of(stream, r))
     _check(rc, "m2rnn_add_norm_bwd")
@@ -1034,11 +1046,11 @@ def quant_rows(x, *, out=None, stream=None):
     """x [..., D] (bf16 or f32; rows may be slices of wider buffers) in 8 bits with a scale per
     row: (q float8_e4m3fn, scale [...] fp32), scale = max|row| / 448, q the nearest
     code of row / scale.  ``out`` may supply q and scale."""
-    s, (rows,) = _norm_shape(x)
+    s, rows = _norm_shape(x)
     q, scale = _given(out, "q", "scale")
     q = _out(q, x.shape, torch.float8_e4m3fn, x.device, "q")
     scale = _out(scale, x.shape[:-1], torch.float32, x.device, "scale")
-    rc = lib().m2rnn_quant_rows(ctypes.byref(s), _at(x), rows, _addr(q), _addr(scale),
+    rc = lib().m2rnn_quant_rows(ctypes.byref(s), _at(x), rows[0], _addr(q), _addr(scale),
                                 _stream_of(stream, x))
     _check(rc, "m2rnn_quant_rows")
     return q, scale
@@ -1046,11 +1058,19 @@ def quant_rows(x, *, out=None, stream=None):
 
 def _glu_args(x, wg, wu, act):
     code, (M, row) = _dtype_code(x), _token_rows("x", x)
-    if wg.dim() != 2:
+    weight, td = wg.shape, x.dtype
+    if len(weight) != 2:
         raise ValueError("wg must be [F,D]")
-    F, D = wg.shape[0], x.shape[-1]
-    _expect_all(x.dtype, ("wg", wg, (F, D)), ("wu", wu, (F, D)))
+    F, D = weight
+    if D != x.shape[-1] or wu.shape != weight or wg.dtype is not td or wu.dtype is not td:
+        _expect_all(td, ("wg", wg, (F, x.shape[-1])), ("wu", wu, (F, x.shape[-1])))
     return GluShape(M, D, F, code, _act(act)), row
+
+
+def _wide(x, F: int):
+    """The shape of x [..., D] with F features."""
+    shape = x.shape
+    return (shape[0], F) if len(shape) == 2 else (*shape[:-1], F)
 
 
 @_on_stream
@@ -1060,9 +1080,9 @@ def glu_fwd(x, wg, wu, *, act: str = "silu", workspace=None, out=None, stream=No
     x [..., D] (rows may be evenly spaced slices); wg, wu [F,D]; one dtype (bf16 or f32);
     act "silu" or "gelu" (the tanh form).  ``out`` may supply h."""
     s, row = _glu_args(x, wg, wu, act)
-    h = _out(_given(out, "h")[0], (*x.shape[:-1], s.F), x.dtype, x.device, "h")
+    h = _out(None if out is None else out.get("h"), _wide(x, s.F), x.dtype, x.device, "h")
     L, ws = lib(), workspace
-    if ws is None:
+    if ws is None and s.in_dtype == M2RNN_F32:  # (bf16 operands need none)
         need = L.m2rnn_glu_fwd_workspace_size(ctypes.byref(s))
         ws = _workspace(None, need, x.device) if need else None
     rc = L.m2rnn_glu_fwd(ctypes.byref(s), _at(x), row, _addr(wg), _addr(wu), _addr(h), _addr(ws),
@@ -1078,7 +1098,7 @@ def glu_bwd(x, wg, wu, dh, *, act: str = "silu", want_dx: bool = True, want_dw: 
     [..., F]; None for what is not wanted.  The products of the forward pass are formed
     again: nothing is kept between the two."""
     s, row = _glu_args(x, wg, wu, act)
-    _expect("dh", dh, (*x.shape[:-1], s.F), x.dtype)
+    _expect("dh", dh, _wide(x, s.F), x.dtype)
     dx, dwg, dwu = _given(out, "dx", "dwg", "dwu")
     dev = x.device
     g = {"dx": _out(dx, x.shape, x.dtype, dev, "dx") if want_dx else None,
@@ -1095,15 +1115,19 @@ def glu_bwd(x, wg, wu, dh, *, act: str = "silu", want_dx: bool = True, want_dw: 
 def _q8_args(x, xs, weights):
     """Rows of e4m3 x [..., D] and the width of weights [(w [F,D], scales [F]), ...]."""
     e4m3, f32 = torch.float8_e4m3fn, torch.float32
-    if weights[0][0].dim() != 2:
+    weight = weights[0][0].shape
+    if len(weight) != 2:
         raise ValueError("weights must be [F,D]")
-    F, D = weights[0][0].shape[0], x.shape[-1]
-    _expect_all(e4m3, ("x", x, x.shape))
-    _expect_all(f32, ("xs", xs, x.shape[:-1]))
-    for w, ws in weights:
-        _expect_all(e4m3, ("w", w, (F, D)))
-        _expect_all(f32, ("ws", ws, (F,)))
+    shape = x.shape
     M, row = _token_rows("x", x)
+    F, D = weight[0], shape[-1]
+    if x.dtype is not e4m3 or xs.dtype is not f32 or xs.shape != shape[:-1]:
+        _expect_all(e4m3, ("x", x, shape))
+        _expect_all(f32, ("xs", xs, shape[:-1]))
+    for w, ws in weights:
+        if w.dtype is not e4m3 or ws.dtype is not f32 or w.shape != (F, D) or ws.shape != (F,):
+            _expect_all(e4m3, ("w", w, (F, D)))
+            _expect_all(f32, ("ws", ws, (F,)))
     return M, row, D, F
 
 
@@ -1114,7 +1138,7 @@ def glu_q8(x, xs, wg, wgs, wu, wus, *, act: str = "silu", out=None, stream=None)
     of the weights).  Returns h [..., F] in bf16; ``out`` may supply it."""
     M, row, D, F = _q8_args(x, xs, ((wg, wgs), (wu, wus)))
     s = GluShape(M, D, F, M2RNN_BF16, _act(act))
-    h = _out(_given(out, "h")[0], (*x.shape[:-1], F), torch.bfloat16, x.device, "h")
+    h = _out(None if out is None else out.get("h"), _wide(x, F), torch.bfloat16, x.device, "h")
     rc = lib().m2rnn_glu_q8(ctypes.byref(s), _at(x), row, _addr(xs), _addr(wg), _addr(wgs), _addr(wu),
                             _addr(wus), _addr(h), _stream_of(stream, x))
     _check(rc, "m2rnn_glu_q8")
@@ -1129,13 +1153,13 @@ def linear_q8(x, xs, w, ws, res=None, *, out=None, stream=None):
     itself (in place)."""
     M, row, D, F = _q8_args(x, xs, ((w, ws),))
     res_row = 0
-    y = _given(out, "y")[0]
+    y = None if out is None else out.get("y")
     if res is not None:
-        _expect_all(torch.bfloat16, ("res", res, (*x.shape[:-1], F)))
+        _expect_all(torch.bfloat16, ("res", res, _wide(x, F)))
         res_row = _token_rows("res", res)[1]
         y = _like(y, res, "y")
     else:
-        y = _out(y, (*x.shape[:-1], F), torch.bfloat16, x.device, "y")
+        y = _out(y, _wide(x, F), torch.bfloat16, x.device, "y")
     s = GluShape(M, D, F, M2RNN_BF16, 0)
     rc = lib().m2rnn_linear_q8(ctypes.byref(s), _at(x), row, _addr(xs), _addr(w), _addr(ws), _at(res),
                                res_row, _addr(y), _stream_of(stream, x))
