@@ -37,8 +37,9 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// 8 codes of o / scale.  The reciprocal is held to twice fp32 (hi + lo, 2^-47 off), so the
-// product, rounded once by the fma, is the rounded quotient: quotients of bf16 values do
+// 8 codes of o / scale.  The reciprocal is held to twice fp32 (hi + lo, 2^-47 off; Brisebarre and
+// Muller's multiplication by a constant of two parts), so the product, rounded once by the fma,
+// is the rounded quotient: quotients of bf16 values do
 // fall on the middle between two codes, and the rounded reciprocal alone changed the codes of 1
 // in 10^3 of them.  True divisions only where the parts might leave fp32's range.
 struct Reciprocal {
@@ -245,15 +246,19 @@ __global__ void __launch_bounds__(256, F32 ? (NV == 4 ? 4 : NV == 6 ? 3 : 2) : (
 // A CTA holds several groups of warps, each of which walks over rows with its share of dw in
 // registers.  A thread copies its vectors of the next S rows into its own places of shared
 // memory (asynchronously, so they take no registers while they are in flight: 96 KB to a
-// CTA), and reads them twice, for the two sums and for dx.  The groups' shares of dw are
-// added in order, then the CTAs' by sum_parts.  M=32768 D=2048: 111 us with the next row in
-// registers.
+// CTA), and reads them twice, for the two sums and for dx.  dw is summed over runs of kRun
+// rows, and those apart, so that long sums do not drift; then over groups, then over CTAs
+// (sum_parts), always in the same order.  M=32768 D=2048: 88 us, 111 with the next row in
+// registers instead.
+constexpr int kRun = 64;
 template <bool F32, int NV>
 struct BwdCfg {
   static constexpr int CTA = NV == 4 ? 512 : 256;
   static constexpr int U = F32 ? 2 : 1;  // 16-byte units of a vector
   static constexpr int S = NV == 4 ? (F32 ? 1 : 2) : NV * U == 4 ? 2 : 4;
-  static constexpr int SMEM = S * 3 * NV * U * CTA * 16;
+  static constexpr int RING = S * 3 * NV * U * CTA * 16;
+  // the runs' sums of dw (NV = 4, whose CTA is one group: in its part in memory instead)
+  static constexpr int SMEM = RING + (NV == 4 ? 0 : CTA * NV * 8 * 4);
 };
 
 template <bool F32, int NV>
@@ -261,7 +266,8 @@ __global__ void __launch_bounds__(BwdCfg<F32, NV>::CTA, NV == 4 ? 1 : 2) add_nor
   using T = typename Elem<F32>::T;
   using C = BwdCfg<F32, NV>;
   constexpr int CTA = C::CTA, U = C::U, S = C::S;
-  extern __shared__ __align__(16) uint8_t ring[];  // [S][3][NV][U][CTA] 16-byte units, then [groups][D]
+  // [S][3][NV][U][CTA] 16-byte units (in the end [groups][D] floats), [NV][8][CTA] floats
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 sums[2][CTA / 32];
   const int group = warps * 32, vecs = p.D / 8, groups = CTA / group;
   const int lane = threadIdx.x % group, mine = threadIdx.x / group;
@@ -319,11 +325,41 @@ __global__ void __launch_bounds__(BwdCfg<F32, NV>::CTA, NV == 4 ? 1 : 2) add_nor
     }
     raw_unpack<F32, 8>(r, o);
   };
+  // Moves a run's sums of dw to those of the runs before (thread by thread).
+  float* runs = reinterpret_cast<float*>(ring + C::RING) + threadIdx.x;
+  bool first = true;
+  const auto end_run = [&]() {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = lane + i * group;
+      if constexpr (NV == 4) {
+        const size_t at = static_cast<size_t>(blockIdx.x) * D + 8 * v;
+        if (v < vecs && in_range(p.status, at, 8, static_cast<size_t>(p.nparts) * D, CHK_NORM2_PARAM)) {
+          float o[8];
+          if (!first) {
+            raw_unpack<true, 8>(raw_load<true, 8, false>(p.part + at), o);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dw[i][j] += o[j];
+          }
+          store_vec<true, 8>(p.part + at, dw[i]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float& sum = runs[(i * 8 + j) * CTA];
+          sum = first ? dw[i][j] : sum + dw[i][j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+    }
+    first = false;
+  };
   const long long step = static_cast<long long>(gridDim.x) * groups;
   long long row = static_cast<long long>(blockIdx.x) * groups + mine;
 #pragma unroll
   for (int k = 0; k < S; ++k) fetch(k, row + k * step);
-  int slot = 0;
+  int slot = 0, rows = 0;
   for (int turn = 0; row < p.M; row += step, turn ^= 1) {  // (the same count in all warps of a group)
     const size_t at = static_cast<size_t>(row) * D;
     ptx::cp_async_wait<S - 1>();
@@ -375,19 +411,12 @@ __global__ void __launch_bounds__(BwdCfg<F32, NV>::CTA, NV == 4 ? 1 : 2) add_nor
     }
     fetch(slot, row + S * step);  // (the thread has read its places)
     slot = slot + 1 == S ? 0 : slot + 1;
+    if (++rows % kRun == 0 && p.part != nullptr) end_run();
   }
   ptx::cp_async_wait_all();
   if (p.part == nullptr) return;
-  if constexpr (NV == 4) {  // (one group)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = lane + i * group;
-      const size_t at = static_cast<size_t>(blockIdx.x) * D + 8 * v;
-      if (v < vecs && in_range(p.status, at, 8, static_cast<size_t>(p.nparts) * D, CHK_NORM2_PARAM))
-        store_vec<true, 8>(p.part + at, dw[i]);
-    }
-    return;
-  }
+  end_run();
+  if constexpr (NV == 4) return;
   float* share = reinterpret_cast<float*>(ring);
   __syncthreads();  // (the rows in the ring have been read)
 #pragma unroll
@@ -395,7 +424,7 @@ __global__ void __launch_bounds__(BwdCfg<F32, NV>::CTA, NV == 4 ? 1 : 2) add_nor
     const int v = lane + i * group;
     if (v < vecs) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) share[mine * p.D + 8 * v + j] = dw[i][j];
+      for (int j = 0; j < 8; ++j) share[mine * p.D + 8 * v + j] = runs[(i * 8 + j) * CTA];
     }
   }
   __syncthreads();

@@ -107,6 +107,22 @@ def test_gradient(m, M, D, with_dr, dtype):
     assert m.add_norm_bwd(r, dy, None, dr, EPS)["dw"] is None
 
 
+@pytest.mark.parametrize("M,D", [(400_000, 64), (60_000, 1032), (20_000, 8200)])
+def test_long_sums_of_the_weights_gradient(m, M, D):
+    """dw over many rows of one sign, whose sum drifts if it is formed in one run: a run of
+    64 rows, then M / (64 groups) runs, then at most 2,432 groups and parts, 8 in a row or in a
+    tree: (64 + M / (64 * 152) + 400) u of the sum, and as each rounding is as often up as
+    down, a hundredth of what a single run of M rows could lose."""
+    r, dy = rn(1, M, D).abs(), rn(2, M, D).abs()
+    w = torch.ones(D, device="cuda").bfloat16()
+    dw = m.add_norm_bwd(r, dy, w, None, EPS)["dw"]
+    ref = torch.zeros(D, dtype=torch.float64, device="cuda")
+    for i in range(0, M, 20_000):
+        ref += (norm64(r[i:i + 20_000], None, EPS)[0] * dy[i:i + 20_000].double()).sum(0)
+    assert (dw.double() - ref).norm() <= 1e-6 * ref.norm()
+    within(dw, ref, ref.abs() * (464 + M / 9728) * U, "dw")
+
+
 def test_gradient_against_differences(m):
     """Central differences of sum(y dy) in fp32 along a direction: the step 2^-6 has a
     curvature term of 2^-12 / 6 of third derivatives of size about one per row, and
