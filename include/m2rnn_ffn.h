@@ -76,11 +76,12 @@ int m2rnn_quant_rows(const m2rnn_norm_shape *s, const void *x, const m2rnn_rows 
  *     g = x wg^T,  u = x wu^T,  h = act(g) (.) u
  *
  *   x [M,D] (rows x_row >= D apart), wg, wu [F,D], h, dh [M,F], dx [M,D], dwg, dwu [F,D], all in_dtype
- * act: 0 SiLU g / (1 + e^-g), 1 GELU in its tanh form.  D and F multiples of 8
- * up to 2^20, 0 <= M < 2^31, M*D and M*F < 2^40.  Products are summed in fp32; with fp32 inputs
- * every operand is held whole (three bf16 terms), and where a product meets a
- * value that is not finite the result may be NaN in place of an infinity.  Neither g
- * nor u leaves the chip: the backward pass forms them again. */
+ * act: 0 SiLU g / (1 + e^-g), 1 GELU in its tanh form.  D a multiple of 8 up to 2^16, F
+ * of 8 up to 2^20, 0 <= M < 2^31, M*D and M*F < 2^40, D*F < 2^38.  Products are summed in
+ * fp32; with fp32 inputs every operand is held whole (three bf16 terms), and where a product
+ * meets a value that is not finite the result may be NaN in place of an infinity.  With bf16
+ * inputs the gradients of g and u are rounded to bf16 between the products (to two bf16 terms
+ * up to M*D*F = 2^30).  Neither g nor u leaves the chip: the backward pass forms them again. */
 typedef struct {
     long long M;
     int D, F;

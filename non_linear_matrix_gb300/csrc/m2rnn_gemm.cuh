@@ -18,7 +18,8 @@
 // their own, and K is taken in chunks whose sums are added with rounding in registers.
 //
 // A last wave of few tiles is cut along K (`split` parts each, fp32 sums in memory that
-// join_parts_kernel adds in order), so that it takes 1/split of a wave.
+// join_parts_kernel adds in order), so that it takes 1/split of a wave; so are all tiles of
+// very long sums.
 #pragma once
 #include "m2rnn_act.cuh"
 #include "m2rnn_ffn.h"
@@ -602,7 +603,8 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__
   await_before();
   constexpr int VECS = C::BN / 8;
   const size_t tile = static_cast<size_t>(C::BM) * C::BN;
-  const int t = blockIdx.y, v = blockIdx.x * 256 + threadIdx.x;
+  constexpr int PER = C::BM * C::BN / 8 / 256;  // CTAs of a tile
+  const int t = blockIdx.x / PER, v = blockIdx.x % PER * 256 + threadIdx.x;
   const int r = v / VECS, c = v % VECS * 8;
   if (r >= C::BM) return;
   const TileAt at = tile_at(p, p.whole + t * p.split);
@@ -652,7 +654,7 @@ static cudaError_t launch_cfg(const GemmParams& p, int sms, cudaStream_t st) {
   e = cudaLaunchKernelEx(&c, gemm_kernel<C>, p);
   if constexpr (C::EPI == EPI_STORE) {
     if (e == cudaSuccess && p.nparts > 0)
-      e = launch_after(join_parts_kernel<C>, dim3(C::BM * C::BN / 8 / 256, p.nparts / p.split), 256, 0, st, p);
+      e = launch_after(join_parts_kernel<C>, dim3(C::BM * C::BN / 8 / 256 * (p.nparts / p.split)), 256, 0, st, p);
   }
   return e;
 }

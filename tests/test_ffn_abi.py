@@ -75,10 +75,10 @@ GLU_BAD = [
     ((4, 64, 64, 1, 2), -1),             # activation
     ((4, 60, 64, 1, 0), -2),
     ((4, 64, 60, 1, 0), -2),
-    ((4, (1 << 20) + 8, 64, 1, 0), -2),
+    ((4, (1 << 16) + 16, 64, 1, 0), -2), # D
+    ((4, 64, (1 << 20) + 8, 1, 0), -2),  # F
     ((1 << 31, 64, 64, 1, 0), -2),
     ((1 << 30, 64, 2048, 1, 0), -2),     # M * F
-    ((4, 1 << 20, 1 << 20, 1, 0), -2),   # D * F
 ]
 
 
