@@ -6,6 +6,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
 
 #include "m2rnn_ffn.h"
 
@@ -192,11 +193,12 @@ int check_glu(const m2rnn_glu_shape* s, bool q8) {
   return M2RNN_OK;
 }
 
-// fp32: K tiles whose products one chain of sums takes, over all segments (128 k, eight steps
+// fp32: K tiles whose products one chain of sums takes, over all segments (256 k, 16 steps
 // of the tensor core, each of which cuts its sum off: 3.1 2^-24 of it where all terms have one
-// sign, measured).  Relative 2-norm of dx of one sign 5.9e-7 with two tiles, 1.3e-6 with four, for
-// 5 % of the time.
-constexpr int kChunkTiles = 2;
+// sign, measured).  Relative 2-norm, terms of both signs and of one: h 4.7e-7, 8.1e-7, gradients at most
+// 5.6e-7, 7.9e-7; with 128 k 2.6e-7, 3.7e-7, for 5 to 14 % of the time (M=4096 D=2048, M=8192
+// D=512).  The formula in plain fp32: 7e-7 to 9e-7.
+constexpr int kChunkTiles = 4;
 
 // Rows of what lies in the workspace start on 128 bytes: a copied row of 128 bytes then is one
 // line of L2 (rows of 1,040 and 2,800 bytes took twice the time).
@@ -251,6 +253,9 @@ size_t dgu_bytes(const m2rnn_glu_shape* s) {  // the gradients of g and u
 }
 // Segments of dx's products; of each weight's gradient half as many.
 int dx_segments(const m2rnn_glu_shape* s) { return s->in_dtype == M2RNN_F32 ? 2 : 2 * grad_terms(s); }
+m2rnn::GemmPlan pair_plan(const m2rnn_glu_shape* s, int epi) {
+  return m2rnn::gemm_plan(epi, s->in_dtype == M2RNN_F32, s->M, s->F, 1, 1, k_tiles(s->D, 2));
+}
 m2rnn::GemmPlan dx_plan(const m2rnn_glu_shape* s) {
   return m2rnn::gemm_plan(m2rnn::EPI_STORE, s->in_dtype == M2RNN_F32, s->M, s->D, 1, dx_segments(s), k_tiles(s->F, 2));
 }
@@ -288,12 +293,12 @@ int make_operands(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
 }
 
 // g and u of every token (EPI_GLU: h; EPI_DGLU: their gradients).
-int run_pair(const m2rnn_glu_shape* s, const Operands& o, int epi, const void* dh, void* out, int* status, int sms,
-             cudaStream_t st) {
+int run_pair(const m2rnn_glu_shape* s, const Operands& o, int epi, const void* dh, void* out, float* parts,
+             int* status, int sms, cudaStream_t st) {
   const bool f32 = o.terms == 3;
-  const int kt = k_tiles(s->D, 2);
-  const m2rnn::GemmPlan q = m2rnn::gemm_plan(epi, f32, s->M, s->F, 1, 1, kt);
-  m2rnn::GemmParams p = gemm_params(q, s->M, s->F, 1, kt, f32, status);
+  const m2rnn::GemmPlan q = pair_plan(s, epi);
+  m2rnn::GemmParams p = gemm_params(q, s->M, s->F, 1, k_tiles(s->D, 2), f32, status);
+  p.parts = parts;
   const long long x_plane = s->M * o.x_row, w_plane = s->F * o.w_row;
   if (!make_map(&p.a, o.x, 2, s->D, s->M, o.terms, o.x_row, f32 ? x_plane : o.x_row, 128) ||
       !make_map(&p.b0, o.wg, 2, s->D, s->F, o.terms, o.w_row, f32 ? w_plane : o.w_row, q.bn / 2) ||
@@ -394,7 +399,7 @@ int m2rnn_quant_rows(const m2rnn_norm_shape* s, const void* x, const m2rnn_rows*
 
 size_t m2rnn_glu_fwd_workspace_size(const m2rnn_glu_shape* s) {
   if (check_glu(s, false) != M2RNN_OK || s->M <= m2rnn::few_most(s->in_dtype == M2RNN_F32)) return 0;
-  return terms_bytes(s);
+  return terms_bytes(s) + align256(pair_plan(s, m2rnn::EPI_GLU).parts_bytes);
 }
 
 int m2rnn_glu_fwd(const m2rnn_glu_shape* s, const void* x, long long x_row, const void* wg, const void* wu, void* h,
@@ -435,13 +440,14 @@ int m2rnn_glu_fwd(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
   Pieces ws{static_cast<char*>(workspace)};
   Operands o;
   if ((rc = make_operands(s, x, x_row, wg, wu, &ws, status, st, &o)) != M2RNN_OK) return rc;
-  return run_pair(s, o, m2rnn::EPI_GLU, nullptr, h, status, sms, st);
+  return run_pair(s, o, m2rnn::EPI_GLU, nullptr, h, reinterpret_cast<float*>(ws.at), status, sms, st);
 }
 
 size_t m2rnn_glu_bwd_workspace_size(const m2rnn_glu_shape* s) {
   if (check_glu(s, false) != M2RNN_OK || s->M == 0) return 0;
-  const size_t dx = dx_plan(s).parts_bytes, dw = dw_plan(s).parts_bytes;
-  return terms_bytes(s) + dgu_bytes(s) + align256(dx > dw ? dx : dw);
+  size_t parts = pair_plan(s, m2rnn::EPI_DGLU).parts_bytes;  // (one after the other in the same place)
+  for (size_t more : {dx_plan(s).parts_bytes, dw_plan(s).parts_bytes}) parts = more > parts ? more : parts;
+  return terms_bytes(s) + dgu_bytes(s) + align256(parts);
 }
 
 int m2rnn_glu_bwd(const m2rnn_glu_shape* s, const void* x, long long x_row, const void* wg, const void* wu,
@@ -485,7 +491,7 @@ int m2rnn_glu_bwd(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
   const long long hp = s->M * hrow;
   __nv_bfloat16* dgu = ws.take(static_cast<size_t>(2 * gt) * hp);
   float* parts = reinterpret_cast<float*>(ws.at);
-  if ((rc = run_pair(s, o, m2rnn::EPI_DGLU, dh, dgu, status, sms, st)) != M2RNN_OK) return rc;
+  if ((rc = run_pair(s, o, m2rnn::EPI_DGLU, dh, dgu, parts, status, sms, st)) != M2RNN_OK) return rc;
   const long long xp = s->M * o.x_row, wp = s->F * o.w_row;
   if (dx != nullptr) {  // dg wg + du wu
     const m2rnn::GemmPlan q = dx_plan(s);

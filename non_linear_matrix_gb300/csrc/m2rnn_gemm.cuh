@@ -239,14 +239,15 @@ __device__ __forceinline__ void block_store(__nv_bfloat16* dst, const Block& k, 
   __syncwarp();
 }
 
-// fp32 sums of a part of a tile: [part][rows of a tile][BN].
+// fp32 sums of a part of a tile: [part][rows of a tile][BN], `col` of the output (a pair's second
+// product behind the first).
 template <class C>
 __device__ __forceinline__ void store_part(const GemmParams& p, const TileAt& t, long long row, int col,
-                                           const float (&g)[32]) {
+                                           const float (&g)[32], int second = 0) {
   if (row >= p.M || col >= p.N) return;
   const size_t tile = static_cast<size_t>(C::BM) * C::BN;
   const size_t at = t.part * tile + static_cast<size_t>(row - static_cast<long long>(t.m) * C::BM) * C::BN +
-                    (col - t.n * C::BN);
+                    (col - t.n * C::OUT_N + second * C::OUT_N);
   store32<true>(p.parts, at, 32, g, tile * p.nparts, p.status, CHK_GLU_WS);
 }
 
@@ -343,6 +344,11 @@ __device__ __forceinline__ void finish_f32(const GemmParams& p, const TileAt& t,
   const int cols = row < p.M ? min(32, p.N - col) : 0;  // of the lane's row
   if (C::EPI != EPI_DGLU && cols <= 0) return;
   const size_t at = static_cast<size_t>(row) * p.N + col, extent = static_cast<size_t>(p.M) * p.N;
+  if (t.part >= 0) {
+    store_part<C>(p, t, row, col, g);
+    if constexpr (C::PAIR) store_part<C>(p, t, row, col, u, 1);
+    return;
+  }
   if constexpr (C::EPI == EPI_GLU) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) g[i] = act_of(g[i], p.act) * u[i];
@@ -369,10 +375,7 @@ __device__ __forceinline__ void finish_f32(const GemmParams& p, const TileAt& t,
         block_store(out + (which * 3 + k) * plane, block_of(p, row0, col, p.pitch), buf, lane, d, p.status, CHK_GLU_WS);
       }
   } else {
-    if (t.part >= 0)
-      store_part<C>(p, t, row, col, g);
-    else
-      store32<true>(t.batch ? p.out[1] : p.out[0], at, cols, g, extent, p.status, CHK_GLU_OUT);
+    store32<true>(t.batch ? p.out[1] : p.out[0], at, cols, g, extent, p.status, CHK_GLU_OUT);
   }
 }
 
@@ -596,33 +599,67 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
   if (warp == C::OUT_WARPS + 1) tc5::dealloc<C::CG>(tm, C::TCOLS);
 }
 
-// The parts of the last wave's tiles, added in order: out = sum over i of parts[t][i].  A thread
-// takes 8 columns.
+// The parts of tiles that were cut, added in order, and (fp32 pairs) what finish_f32 makes of
+// them.  A thread takes 8 columns of the output.
 template <class C>
 __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ GemmParams p) {
   await_before();
-  constexpr int VECS = C::BN / 8;
+  constexpr int VECS = C::OUT_N / 8;
+  constexpr int PER = C::BM * VECS / 256;  // CTAs of a tile
   const size_t tile = static_cast<size_t>(C::BM) * C::BN;
-  constexpr int PER = C::BM * C::BN / 8 / 256;  // CTAs of a tile
   const int t = blockIdx.x / PER, v = blockIdx.x % PER * 256 + threadIdx.x;
   const int r = v / VECS, c = v % VECS * 8;
-  if (r >= C::BM) return;
   const TileAt at = tile_at(p, p.whole + t * p.split);
   const long long row = static_cast<long long>(at.m) * C::BM + r;
-  const int col = at.n * C::BN + c;
+  const int col = at.n * C::OUT_N + c;
   if (row >= p.M || col >= p.N) return;
-  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float s[C::PAIR ? 2 : 1][8] = {};
   for (int i = 0; i < p.split; ++i) {
     const size_t from = (static_cast<size_t>(t) * p.split + i) * tile + static_cast<size_t>(r) * C::BN + c;
-    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (in_range(p.status, from, 8, tile * p.nparts, CHK_GLU_WS))
-      raw_unpack<true, 8>(raw_load<true, 8, false>(p.parts + from), o);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] += o[j];
+    for (int w = 0; w < (C::PAIR ? 2 : 1); ++w) {
+      float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (in_range(p.status, from + w * C::OUT_N, 8, tile * p.nparts, CHK_GLU_WS))
+        raw_unpack<true, 8>(raw_load<true, 8, false>(p.parts + from + w * C::OUT_N), o);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[w][j] += o[j];
+    }
   }
-  const size_t to = static_cast<size_t>(row) * p.N + col;
-  if (in_range(p.status, to, 8, static_cast<size_t>(p.M) * p.N, CHK_GLU_OUT))
-    store_vec<C::F32, 8>(static_cast<typename Elem<C::F32>::T*>(at.batch ? p.out[1] : p.out[0]) + to, s);
+  const size_t to = static_cast<size_t>(row) * p.N + col, extent = static_cast<size_t>(p.M) * p.N;
+  if constexpr (C::EPI == EPI_DGLU) {
+    float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (in_range(p.status, to, 8, extent, CHK_GLU_IN))
+      raw_unpack<true, 8>(raw_load<true, 8, false>(static_cast<const float*>(p.in) + to), d);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float a, e;
+      act_grad(s[0][j], p.act, a, e);
+      s[0][j] = d[j] * s[C::PAIR ? 1 : 0][j] * e;
+      s[C::PAIR ? 1 : 0][j] = d[j] * a;
+    }
+    const size_t plane = static_cast<size_t>(p.M) * p.pitch, at8 = static_cast<size_t>(row) * p.pitch + col;
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float& x = s[C::PAIR ? w : 0][j];
+          o[j] = bf16_term(x);
+          x = isfinite(o[j]) ? x - o[j] : 0.f;
+        }
+        if (in_range(p.status, (w * 3 + k) * plane + at8, 8, 6 * plane, CHK_GLU_WS))
+          store_vec<false, 8>(static_cast<__nv_bfloat16*>(p.out[0]) + (w * 3 + k) * plane + at8, o);
+      }
+  } else {
+    if constexpr (C::EPI == EPI_GLU) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[0][j] = act_of(s[0][j], p.act) * s[C::PAIR ? 1 : 0][j];
+    }
+    if (in_range(p.status, to, 8, extent, CHK_GLU_OUT))
+      store_vec<C::F32, 8>(static_cast<typename Elem<C::F32>::T*>(at.batch ? p.out[1] : p.out[0]) + to, s[0]);
+  }
 }
 
 // (static: the `ready` of another build of the library in the same process is not this one's)
@@ -652,9 +689,9 @@ static cudaError_t launch_cfg(const GemmParams& p, int sms, cudaStream_t st) {
   c.attrs = at;
   c.numAttrs = C::CG == 2 ? 2 : 1;
   e = cudaLaunchKernelEx(&c, gemm_kernel<C>, p);
-  if constexpr (C::EPI == EPI_STORE) {
+  if constexpr (C::EPI == EPI_STORE || C::F32) {
     if (e == cudaSuccess && p.nparts > 0)
-      e = launch_after(join_parts_kernel<C>, dim3(C::BM * C::BN / 8 / 256 * (p.nparts / p.split)), 256, 0, st, p);
+      e = launch_after(join_parts_kernel<C>, dim3(C::BM * C::OUT_N / 8 / 256 * (p.nparts / p.split)), 256, 0, st, p);
   }
   return e;
 }
