@@ -32,7 +32,9 @@ cudaError_t launch_gemm(const GemmParams& p, const GemmKind& k, int sms, cudaStr
 // planes then find room to pass through shared memory (backward pass M=8192 D=512 F=2048 432
 // -> 408 us, M=4096 D=2048 F=4096 equal).
 // The tiles beyond whole waves are cut along K into as many parts as leave every pair or
-// CTA one, each of 8 K tiles at least.  With bf16 operands all tiles are cut where one chain of
+// CTA one, each of 16 K tiles (fp32, whose K tiles are six products: 4) at least, and not where
+// the whole is shorter than three of those: joining the parts takes 2 us and a launch of the
+// host's, 16 K tiles 2 to 4.  With bf16 operands all tiles are cut where one chain of
 // sums would be longer than 512 K tiles (32,768 tokens in a weight's gradient): each of its four steps
 // per K tile cuts the sum off, by up to 3.1 2^-24 of it (measured, terms of one sign), so that a
 // chain loses at most 2^-12.3 of its sum.  The gated products themselves are cut only in fp32 and where
@@ -77,8 +79,10 @@ GemmPlan gemm_plan(int epi, bool f32, long long m, int n, int nbatch, int nseg, 
   }
   const int rest = count % at_once;
   if (rest == 0) return q;
+  const int least = f32 ? 4 : 16;  // K tiles of a part
+  if (chain < 3 * least) return q;
   int split = at_once / rest;
-  if (split > nseg * kt / 8) split = nseg * kt / 8;
+  if (split > chain / least) split = static_cast<int>(chain / least);
   if (split > kt) split = kt;
   if (split < 2) return q;
   q.whole = count - rest;
