@@ -100,8 +100,8 @@ __device__ __forceinline__ size_t rows_span(const Norm2Params& p, long long batc
   return static_cast<size_t>(p.M / p.T - 1) * batch + static_cast<size_t>(p.T - 1) * token + p.D;
 }
 
-// ADD: r = x + res is stored.  Q8: the output as codes and a scale.  NORM = false:
-// the quantiser of x alone.
+// ADD: r = x + res is stored.  Q8: the output as codes and a scale.  us by itself (floor):
+// M=65536 D=1024 79.0 (78.9), 8 bits 70.1 (69.0).
 template <bool F32, int NV, bool ADD, bool Q8>
 __global__ void __launch_bounds__(512) add_norm_kernel(Norm2Params p, int warps, int rows_per_cta) {
   using T = typename Elem<F32>::T;
