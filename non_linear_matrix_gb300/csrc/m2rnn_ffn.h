@@ -81,11 +81,12 @@ struct GemmParams {
   unsigned long long limit_ns;
   int inject_stall;       // test hook: no copies are issued
 };
-// kind: operands' element (0 bf16, 1 e4m3); a_mn, b_mn: whether M or N runs fastest in memory.
+// Which instance: fp32 operands as terms; A with M fastest in memory (the weights' gradients); the
+// tile's accumulator columns and rows (128 or 256).
 struct GemmKind {
   int epi;
-  bool e4m3, f32, a_mn, b_mn;
-  int bn, rows;  // a tile's accumulator columns and rows: 128 or 256
+  bool f32, a_mn;
+  int bn, rows;
 };
 cudaError_t launch_gemm(const GemmParams& p, const GemmKind& k, int sms, cudaStream_t st);
 struct GemmPlan {

@@ -309,7 +309,7 @@ int run_pair(const m2rnn_glu_shape* s, const Operands& o, int epi, const void* d
   p.aterms = grad_terms(s);
   p.in = dh;
   p.act = s->act;
-  return status_from_cuda(m2rnn::launch_gemm(p, {epi, false, f32, false, false, q.bn, q.rows}, sms, st));
+  return status_from_cuda(m2rnn::launch_gemm(p, {epi, f32, false, q.bn, q.rows}, sms, st));
 }
 
 }  // namespace
@@ -503,7 +503,7 @@ int m2rnn_glu_bwd(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
       return M2RNN_ERR_CUDA;
     p.out[0] = dx;
     p.parts = parts;
-    rc = status_from_cuda(m2rnn::launch_gemm(p, {m2rnn::EPI_STORE, false, f32, false, true, q.bn, q.rows}, sms, st));
+    rc = status_from_cuda(m2rnn::launch_gemm(p, {m2rnn::EPI_STORE, f32, false, q.bn, q.rows}, sms, st));
     if (rc != M2RNN_OK) return rc;
   }
   if (dwg != nullptr) {  // dg^T x and du^T x, which share x
@@ -517,7 +517,7 @@ int m2rnn_glu_bwd(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
     p.out[0] = dwg;
     p.out[1] = dwu;
     p.parts = parts;
-    return status_from_cuda(m2rnn::launch_gemm(p, {m2rnn::EPI_STORE, false, f32, true, true, q.bn, q.rows}, sms, st));
+    return status_from_cuda(m2rnn::launch_gemm(p, {m2rnn::EPI_STORE, f32, true, q.bn, q.rows}, sms, st));
   }
   return M2RNN_OK;
 }
@@ -589,7 +589,7 @@ int product_q8(const m2rnn_glu_shape* s, const void* x, long long x_row, const f
   p.sb0 = s0;
   p.sb1 = s1;
   p.act = s->act;
-  return status_from_cuda(m2rnn::launch_gemm(p, {epi, true, false, false, false, q.bn, q.rows}, sms, st));
+  return status_from_cuda(m2rnn::launch_gemm(p, {epi, false, false, q.bn, q.rows}, sms, st));
 }
 
 }  // namespace

@@ -122,30 +122,26 @@ __device__ __forceinline__ void issue_tile(const GemmParams& p, uint32_t dst, ui
   }
 }
 
-// 32 outputs of one row, `cols` of them inside the matrix (a multiple of 8).
-template <bool F32>
+// 32 fp32 values of one row, `cols` of them inside the matrix (a multiple of 8).
 __device__ __forceinline__ void store32(void* out, size_t at, int cols, const float (&v)[32], size_t extent,
                                         int* status, int site) {
-  using T = typename Elem<F32>::T;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (8 * i < cols && in_range(status, at + 8 * i, 8, extent, site)) {
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = v[8 * i + j];
-      store_vec<F32, 8>(static_cast<T*>(out) + at + 8 * i, o);
+      store_vec<true, 8>(static_cast<float*>(out) + at + 8 * i, o);
     }
   }
 }
-template <bool F32>
 __device__ __forceinline__ void load32(const void* in, size_t at, int cols, float (&v)[32], size_t extent,
                                        int* status, int site) {
-  using T = typename Elem<F32>::T;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (8 * i < cols && in_range(status, at + 8 * i, 8, extent, site))
-      raw_unpack<F32, 8>(raw_load<F32, 8, false>(static_cast<const T*>(in) + at + 8 * i), o);
+      raw_unpack<true, 8>(raw_load<true, 8, false>(static_cast<const float*>(in) + at + 8 * i), o);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[8 * i + j] = o[j];
   }
@@ -248,7 +244,7 @@ __device__ __forceinline__ void store_part(const GemmParams& p, const TileAt& t,
   const size_t tile = static_cast<size_t>(C::BM) * C::BN;
   const size_t at = t.part * tile + static_cast<size_t>(row - static_cast<long long>(t.m) * C::BM) * C::BN +
                     (col - t.n * C::OUT_N + second * C::OUT_N);
-  store32<true>(p.parts, at, 32, g, tile * p.nparts, p.status, CHK_GLU_WS);
+  store32(p.parts, at, 32, g, tile * p.nparts, p.status, CHK_GLU_WS);
 }
 
 // Where the output's block of a warp's 32 rows from row0 on lies, with `pitch` elements to a row.
@@ -352,11 +348,11 @@ __device__ __forceinline__ void finish_f32(const GemmParams& p, const TileAt& t,
   if constexpr (C::EPI == EPI_GLU) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) g[i] = act_of(g[i], p.act) * u[i];
-    store32<true>(p.out[0], at, cols, g, extent, p.status, CHK_GLU_OUT);
+    store32(p.out[0], at, cols, g, extent, p.status, CHK_GLU_OUT);
   } else if constexpr (C::EPI == EPI_DGLU) {
     static_assert(C::STAGED > 0, "the terms pass through shared memory");
     float d[32];
-    load32<true>(p.in, at, cols, d, extent, p.status, CHK_GLU_IN);
+    load32(p.in, at, cols, d, extent, p.status, CHK_GLU_IN);
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       float a, s;
@@ -375,7 +371,7 @@ __device__ __forceinline__ void finish_f32(const GemmParams& p, const TileAt& t,
         block_store(out + (which * 3 + k) * plane, block_of(p, row0, col, p.pitch), buf, lane, d, p.status, CHK_GLU_WS);
       }
   } else {
-    store32<true>(t.batch ? p.out[1] : p.out[0], at, cols, g, extent, p.status, CHK_GLU_OUT);
+    store32(t.batch ? p.out[1] : p.out[0], at, cols, g, extent, p.status, CHK_GLU_OUT);
   }
 }
 
@@ -484,13 +480,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_kernel(const __grid_consta
                 const auto bd = [&](int term) {
                   return tc5::sdesc(sb + term * C::B_BYTES + i * b_step, C::B_MN ? 8192 : 16, 1024);
                 };
-                tc5::mma<C::E4M3, C::CG>(lead, ad(0), bd(0), id, add);
-                if constexpr (C::F32) {
-                  tc5::mma<C::E4M3, C::CG>(small, ad(2), bd(0), id, add);
-                  tc5::mma<C::E4M3, C::CG>(small, ad(1), bd(1), id, true);
-                  tc5::mma<C::E4M3, C::CG>(small, ad(0), bd(2), id, true);
-                  tc5::mma<C::E4M3, C::CG>(small, ad(1), bd(0), id, true);
-                  tc5::mma<C::E4M3, C::CG>(small, ad(0), bd(1), id, true);
+                if constexpr (C::F32) {  // (a term of A is read once for its products)
+                  tc5::mma<C::E4M3, C::CG, tc5::KEEP_FILL>(lead, ad(0), bd(0), id, add);
+                  tc5::mma<C::E4M3, C::CG, tc5::KEEP_USE>(small, ad(0), bd(2), id, add);
+                  tc5::mma<C::E4M3, C::CG, tc5::KEEP_LAST>(small, ad(0), bd(1), id, true);
+                  tc5::mma<C::E4M3, C::CG, tc5::KEEP_FILL>(small, ad(1), bd(1), id, true);
+                  tc5::mma<C::E4M3, C::CG, tc5::KEEP_LAST>(small, ad(1), bd(0), id, true);
+                  tc5::mma<C::E4M3, C::CG>(small, ad(2), bd(0), id, true);
+                } else {
+                  tc5::mma<C::E4M3, C::CG>(lead, ad(0), bd(0), id, add);
                 }
                 add = true;
               }

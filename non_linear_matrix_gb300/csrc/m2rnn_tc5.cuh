@@ -43,25 +43,41 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool e4m3, bool a_mn,
 // product: each holds half of A's rows, half of B's, and the accumulators of its rows.  The
 // first CTA's thread issues for both; descriptors are offsets that hold in both.
 
+// What becomes of an mma's A operand in the collector: read and forgotten, kept for the next mma, taken
+// from there and kept, taken for the last time.
+enum Keep { KEEP_NONE, KEEP_FILL, KEEP_USE, KEEP_LAST };
+
 // D (+)= A B for one K step; one thread issues it.
-template <bool E4M3, int CG>
+template <bool E4M3, int CG, Keep K = KEEP_NONE>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
-#define M2RNN_TC5_MMA(GROUP, KIND)                                                               \
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                 \
-               "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(d), \
-               "l"(a), "l"(b), "r"(id), "r"(static_cast<uint32_t>(add))                           \
+#define M2RNN_TC5_MMA(GROUP, KIND, COLLECT)                                                         \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                    \
+               "tcgen05.mma.cta_group::" GROUP ".kind::" KIND COLLECT " [%0], %1, %2, %3, p;\n\t}" :: \
+               "r"(d), "l"(a), "l"(b), "r"(id), "r"(static_cast<uint32_t>(add))                      \
                : "memory")
+#define M2RNN_TC5_KEEP(GROUP, KIND)                              \
+  if constexpr (K == KEEP_FILL)                                  \
+    M2RNN_TC5_MMA(GROUP, KIND, ".collector::a::fill");           \
+  else if constexpr (K == KEEP_USE)                              \
+    M2RNN_TC5_MMA(GROUP, KIND, ".collector::a::use");            \
+  else if constexpr (K == KEEP_LAST)                             \
+    M2RNN_TC5_MMA(GROUP, KIND, ".collector::a::lastuse");        \
+  else                                                           \
+    M2RNN_TC5_MMA(GROUP, KIND, "")
   if constexpr (CG == 2) {
-    if constexpr (E4M3)
-      M2RNN_TC5_MMA("2", "f8f6f4");
-    else
-      M2RNN_TC5_MMA("2", "f16");
+    if constexpr (E4M3) {
+      M2RNN_TC5_KEEP("2", "f8f6f4");
+    } else {
+      M2RNN_TC5_KEEP("2", "f16");
+    }
   } else {
-    if constexpr (E4M3)
-      M2RNN_TC5_MMA("1", "f8f6f4");
-    else
-      M2RNN_TC5_MMA("1", "f16");
+    if constexpr (E4M3) {
+      M2RNN_TC5_KEEP("1", "f8f6f4");
+    } else {
+      M2RNN_TC5_KEEP("1", "f16");
+    }
   }
+#undef M2RNN_TC5_KEEP
 #undef M2RNN_TC5_MMA
 }
 
