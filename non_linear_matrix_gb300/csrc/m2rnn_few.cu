@@ -54,13 +54,19 @@ __device__ __forceinline__ void split8(const uint32_t (&w)[8], uint32_t (&t)[3][
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
 #pragma unroll
-  for (int k = 0; k < 3; ++k)
+  for (int i = 0; i < 4; ++i) {  // (only the first can pass bf16's range)
+    const float lo = bf16_term(v[2 * i]), hi = bf16_term(v[2 * i + 1]);
+    t[0][i] = ptx::pack_bf16x2(lo, hi);
+    v[2 * i] = isfinite(lo) ? v[2 * i] - lo : 0.f;
+    v[2 * i + 1] = isfinite(hi) ? v[2 * i + 1] - hi : 0.f;
+  }
+#pragma unroll
+  for (int k = 1; k < 3; ++k)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float lo = bf16_term(v[2 * i]), hi = bf16_term(v[2 * i + 1]);
-      t[k][i] = ptx::pack_bf16x2(lo, hi);
-      v[2 * i] = isfinite(lo) ? v[2 * i] - lo : 0.f;
-      v[2 * i + 1] = isfinite(hi) ? v[2 * i + 1] - hi : 0.f;
+      t[k][i] = ptx::pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      v[2 * i] -= ptx::bf16x2_lo(t[k][i]);
+      v[2 * i + 1] -= ptx::bf16x2_hi(t[k][i]);
     }
 }
 

@@ -161,14 +161,15 @@ __device__ __forceinline__ void load32_scales(const float* in, int at, int cols,
   }
 }
 
-// The next bf16 term of fp32 values: the rounding of what the terms before leave (cut off
-// where rounding would pass bf16's largest value).  A value that is not finite is its
-// own first term.
+// The next bf16 term of fp32 values: the rounding of what the terms before leave (the first one cut
+// off where rounding would pass bf16's largest value; a value that is not finite is its own
+// first term).
+template <bool FIRST>
 __device__ __forceinline__ void next_term(float (&v)[32], float (&t)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    t[i] = bf16_term(v[i]);
-    v[i] = isfinite(t[i]) ? v[i] - t[i] : 0.f;
+    t[i] = FIRST ? bf16_term(v[i]) : __bfloat162float(__float2bfloat16_rn(v[i]));
+    v[i] = !FIRST || isfinite(t[i]) ? v[i] - t[i] : 0.f;
   }
 }
 
@@ -293,9 +294,9 @@ __device__ __forceinline__ void finish_bf16(const GemmParams& p, const TileAt& t
     block_store(out, k, buf, lane, g, p.status, CHK_GLU_WS);
     block_store(out + p.aterms * plane, k, buf, lane, u, p.status, CHK_GLU_WS);
     if (p.aterms == 2) {
-      next_term(g, d);
+      next_term<true>(g, d);
       block_store(out + plane, k, buf, lane, g, p.status, CHK_GLU_WS);
-      next_term(u, d);
+      next_term<true>(u, d);
       block_store(out + 3 * plane, k, buf, lane, u, p.status, CHK_GLU_WS);
     }
   } else if constexpr (C::EPI == EPI_STORE) {
@@ -367,7 +368,10 @@ __device__ __forceinline__ void finish_f32(const GemmParams& p, const TileAt& t,
     for (int which = 0; which < 2; ++which)
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
-        next_term(which ? u : g, d);
+        if (k == 0)
+          next_term<true>(which ? u : g, d);
+        else
+          next_term<false>(which ? u : g, d);
         block_store(out + (which * 3 + k) * plane, block_of(p, row0, col, p.pitch), buf, lane, d, p.status, CHK_GLU_WS);
       }
   } else {
