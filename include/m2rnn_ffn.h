@@ -79,14 +79,21 @@ int m2rnn_quant_rows(const m2rnn_norm_shape *s, const void *x, const m2rnn_rows 
  * act: 0 SiLU g / (1 + e^-g), 1 GELU in its tanh form.  D a multiple of 8 up to 2^16, F
  * of 8 up to 2^20, 0 <= M < 2^31, M*D and M*F < 2^40, D*F < 2^38.  Products are summed in
  * fp32; with fp32 inputs every operand is held whole (three bf16 terms), and where a product
- * meets a value that is not finite the result may be NaN in place of an infinity.  With bf16
- * inputs the gradients of g and u are rounded to bf16 between the products (to two bf16 terms
- * up to M*D*F = 2^30).  Neither g nor u leaves the chip: the backward pass forms them again. */
+ * meets a value that is not finite the result may be NaN in place of an infinity.  The backward
+ * pass forms g and u again.  Between its products their gradients are held in bf16 terms: three
+ * with fp32 inputs, two with bf16 ones, so that every gradient of the call is rounded once, at
+ * all sizes.
+ *
+ * act | M2RNN_GLU_ROUND (bf16 only): they are rounded to one bf16 value there, as separate bf16
+ * operations would leave them.  The backward pass then takes 55 to 65 % of the time and half of
+ * that workspace, and dx, dwg and dwu are off by two roundings (relative 2-norm 2.35e-3, not
+ * 1.66e-3).  The other functions take the flag and do nothing else for it. */
+#define M2RNN_GLU_ROUND 16
 typedef struct {
     long long M;
     int D, F;
     int in_dtype; /* m2rnn_dtype of x, wg, wu, h and the gradients */
-    int act;
+    int act;      /* 0 or 1, also with M2RNN_GLU_ROUND */
 } m2rnn_glu_shape;
 
 /* Workspace of the forward pass (0 with bf16 inputs). */

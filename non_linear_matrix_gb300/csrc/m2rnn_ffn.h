@@ -54,7 +54,7 @@ cudaError_t launch_quant_rows(const Norm2Params& p, bool f32, cudaStream_t st);
 // A[z][m][k] B[z][n][k], A and B as tensor maps of three dimensions.
 enum GemmEpi : int {
   EPI_GLU,    // act(g) (.) u of a pair of products
-  EPI_DGLU,   // gradients of g and u, in bf16 (1 term) or as 3 bf16 terms (fp32)
+  EPI_DGLU,   // gradients of g and u, as bf16 terms (1 or 2, fp32 3)
   EPI_STORE,  // the product itself
   EPI_GLU8,   // act(g) (.) u with scales
   EPI_LIN8,   // the product with scales, plus res

@@ -180,10 +180,12 @@ bool make_map(CUtensorMap* m, const void* base, size_t e, long long inner, long 
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+int act_of(const m2rnn_glu_shape* s) { return s->act & ~M2RNN_GLU_ROUND; }
 int check_glu(const m2rnn_glu_shape* s, bool q8) {
   if (s == nullptr) return M2RNN_ERR_INVALID_ARG;
   if (s->M < 0 || s->D < 1 || s->F < 1 || !is_dtype(s->in_dtype)) return M2RNN_ERR_INVALID_ARG;
-  if (s->act != 0 && s->act != 1) return M2RNN_ERR_INVALID_ARG;
+  if (act_of(s) != 0 && act_of(s) != 1) return M2RNN_ERR_INVALID_ARG;
+  if (act_of(s) != s->act && s->in_dtype != M2RNN_BF16) return M2RNN_ERR_INVALID_ARG;
   if (q8 && s->in_dtype != M2RNN_BF16) return M2RNN_ERR_INVALID_ARG;
   if (s->D % (q8 ? 16 : 8) != 0 || s->F % 8 != 0 || s->D > kMostSum || s->F > kMostD || s->M >= (1LL << 31))
     return M2RNN_ERR_UNSUPPORTED_SHAPE;
@@ -239,14 +241,14 @@ size_t terms_bytes(const m2rnn_glu_shape* s) {  // of x, wg and wu
   const size_t pitch = pitch_of(s->D);
   return align256(6 * s->M * pitch) + 2 * align256(6 * s->F * pitch);
 }
-// bf16 terms that hold each gradient of g and u between the products: 3 with fp32 inputs.  With bf16
-// inputs 1, whose rounding (2^-9 of each of many terms of a sum) adds as much error to dx, dwg and
-// dwu as their own rounding does (relative 2-norm 2.3e-3 instead of 1.7e-3); a second one
-// costs as much again as the first, 2 x 218 of 870 us at M=32768 D=1024 F=2816, so it is taken
-// up to M D F = 2^30, where that is below 5 us.
+// bf16 terms that hold each gradient of g and u between the products: 3 with fp32 inputs, 2 with
+// bf16 ones.  With 1 (the caller's choice) its rounding (2^-9 of each of many terms of a sum) adds as
+// much error to dx, dwg and dwu as their own rounding does: relative 2-norm 2.35e-3 instead of
+// 1.66e-3.  With 2 the products that take them are twice as long: backward pass 1199 against 661 us at
+// M=32768 D=1024 F=2816, 185 against 107 at M=4096.
 int grad_terms(const m2rnn_glu_shape* s) {
   if (s->in_dtype == M2RNN_F32) return 3;
-  return static_cast<double>(s->M) * s->D * s->F <= 1073741824.0 ? 2 : 1;
+  return act_of(s) != s->act ? 1 : 2;
 }
 size_t dgu_bytes(const m2rnn_glu_shape* s) {  // the gradients of g and u
   return align256(static_cast<size_t>(s->M) * pitch_of(s->F) * (4 * grad_terms(s)));
@@ -308,7 +310,7 @@ int run_pair(const m2rnn_glu_shape* s, const Operands& o, int epi, const void* d
   p.pitch = epi == m2rnn::EPI_DGLU ? pitch_of(s->F) : s->F;
   p.aterms = grad_terms(s);
   p.in = dh;
-  p.act = s->act;
+  p.act = act_of(s);
   return status_from_cuda(m2rnn::launch_gemm(p, {epi, f32, false, q.bn, q.rows}, sms, st));
 }
 
@@ -428,7 +430,7 @@ int m2rnn_glu_fwd(const m2rnn_glu_shape* s, const void* x, long long x_row, cons
     p.M = static_cast<int>(s->M);
     p.D = s->D;
     p.F = s->F;
-    p.act = s->act;
+    p.act = act_of(s);
     p.status = status;
     return status_from_cuda(m2rnn::launch_few(p, m2rnn::EPI_GLU, false, s->in_dtype == M2RNN_F32, st));
   }
@@ -567,7 +569,7 @@ int product_q8(const m2rnn_glu_shape* s, const void* x, long long x_row, const f
     p.M = static_cast<int>(s->M);
     p.D = s->D;
     p.F = s->F;
-    p.act = s->act;
+    p.act = act_of(s);
     p.status = status;
     return status_from_cuda(m2rnn::launch_few(p, epi, true, false, st));
   }
@@ -588,7 +590,7 @@ int product_q8(const m2rnn_glu_shape* s, const void* x, long long x_row, const f
   p.sa = xs;
   p.sb0 = s0;
   p.sb1 = s1;
-  p.act = s->act;
+  p.act = act_of(s);
   return status_from_cuda(m2rnn::launch_gemm(p, {epi, false, false, q.bn, q.rows}, sms, st));
 }
 

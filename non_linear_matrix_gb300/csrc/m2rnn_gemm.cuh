@@ -287,8 +287,8 @@ __device__ __forceinline__ void finish_bf16(const GemmParams& p, const TileAt& t
       u[i] = du.x;
       u[i + 1] = du.y;
     }
-    // Rounded to bf16, as operands of the products to come; where those are small, what the
-    // rounding leaves follows as a second term.
+    // Rounded to bf16, as operands of the products to come; what the rounding leaves follows as a
+    // second term.
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out[0]);
     const size_t plane = static_cast<size_t>(p.M) * p.pitch;
     block_store(out, k, buf, lane, g, p.status, CHK_GLU_WS);

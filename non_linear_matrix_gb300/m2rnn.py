@@ -890,6 +890,7 @@ class GluShape(ctypes.Structure):
 
 
 _ACTS = {"silu": 0, "gelu": 1}
+M2RNN_GLU_ROUND = 16
 
 
 def _act(act: str) -> int:
@@ -1093,11 +1094,16 @@ def glu_fwd(x, wg, wu, *, act: str = "silu", workspace=None, out=None, stream=No
 
 @_on_stream
 def glu_bwd(x, wg, wu, dh, *, act: str = "silu", want_dx: bool = True, want_dw: bool = True,
-            workspace=None, out=None, stream=None):
+            round_between: bool = False, workspace=None, out=None, stream=None):
     """Gradient of ``glu_fwd``: dict(dx, dwg, dwu), all of x's dtype, for dL/dh = dh
-    [..., F]; None for what is not wanted.  The products of the forward pass are formed
-    again: nothing is kept between the two."""
+    [..., F] (contiguous); None for what is not wanted.  The products of the forward pass are
+    formed again: nothing is kept between the two.  Each gradient is rounded once;
+    round_between=True (bf16 only) rounds those of the two products to bf16 on their way too, as
+    separate bf16 operations would: 55 to 65 % of the time, relative 2-norm 2.35e-3 instead of
+    1.66e-3."""
     s, row = _glu_args(x, wg, wu, act)
+    if round_between:
+        s.act |= M2RNN_GLU_ROUND
     _expect("dh", dh, _wide(x, s.F), x.dtype)
     dx, dwg, dwu = _given(out, "dx", "dwg", "dwu")
     dev = x.device
