@@ -39,7 +39,9 @@ extern "C" {
  * The sum is rounded to in_dtype as it is stored, and y is the norm of what is
  * stored.  res NULL: r = x and the argument `r` must be NULL.
  *   x, res [B,T,D] in_dtype (rows)   w [D] in_dtype or NULL (1)
- *   r, y [B,T,D] in_dtype;  q [B,T,D] e4m3 and scale [B,T] fp32 (the 8-bit form of y)
+ *   r, y [B,T,D] in_dtype;  q [B,T,D] e4m3 and scale [B,T] fp32 (the 8-bit form of y, before
+ *   y is rounded; the root leaves y / scale = 448 w r / max|w r|, so with bf16 inputs the codes are
+ *   the formula's, ties included)
  * D a multiple of 8 up to 16384, B, T >= 0, B*T < 2^31, B*T*D < 2^40; eps >= 0 (with eps = 0
  * a zero row gives NaN, as the formula does).  `r` may be `res` or `x` itself (in
  * place, contiguous). */

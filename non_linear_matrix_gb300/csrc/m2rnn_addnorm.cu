@@ -149,38 +149,61 @@ __global__ void __launch_bounds__(512) add_norm_kernel(Norm2Params p, int warps,
   }
   row_reduce<1, false>(ss, warps, sm);
   const float rstd = 1.f / sqrtf(ss[0] / static_cast<float>(p.D) + p.eps);
-  float top[1] = {0.f};
-  float keep[Q8 ? NV : 1][8];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = lane + i * group;
-    float o[8], w[8];
-    raw_unpack<F32, 8>(xv[i], o);
+  const auto weights = [&](int v, float (&w)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = 1.f;
     if (p.w != nullptr && v < vecs && in_range(p.status, 8 * v, 8, D, CHK_NORM2_PARAM))
       load_vec<F32, 8>(static_cast<const T*>(p.w) + 8 * v, w);
+  };
+  if constexpr (!Q8) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = o[j] * rstd * w[j];
-    if constexpr (Q8) {
+    for (int i = 0; i < NV; ++i) {
+      const int v = lane + i * group;
+      float o[8], w[8];
+      raw_unpack<F32, 8>(xv[i], o);
+      weights(v, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        keep[i][j] = o[j];
-        if (v < vecs) top[0] = nan_max(top[0], fabsf(o[j]));
-      }
-    } else {
+      for (int j = 0; j < 8; ++j) o[j] = o[j] * rstd * w[j];
       if (v < vecs && in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
         store_vec<F32, 8>(static_cast<T*>(p.y) + at + 8 * v, o);
     }
-  }
-  if constexpr (Q8) {
-    row_reduce<1, true>(top, warps, sm);
-    const float scale = __fdiv_rn(top[0], kE4m3Max);
-    const Reciprocal inv = reciprocal_of(scale);
+  } else {
+    // rstd leaves the quotient y / scale, which is 448 w r / max|w r|.  From bf16, w r has 16 bits and
+    // 448 w r 19, both exact, so the codes are the formula's; through y and the scale, each of them
+    // rounded, 1 in 10^4 lay on the other side of a middle that the formula meets.
+    float top[1] = {0.f};
+    float keep[NV][8];
+    const auto form = [&](float factor) {  // w r (times rstd), and the largest
+      top[0] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = lane + i * group;
+        float o[8], w[8];
+        raw_unpack<F32, 8>(xv[i], o);
+        weights(v, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          keep[i][j] = o[j] * factor * w[j];
+          if (v < vecs) top[0] = nan_max(top[0], fabsf(keep[i][j]));
+        }
+      }
+      row_reduce<1, true>(top, warps, sm);
+    };
+    form(1.f);
+    float scale = __fdiv_rn(top[0] * rstd, kE4m3Max), by = top[0], times = kE4m3Max;
+    // (the same choice in the whole row; outside, products or squares may have left fp32's range)
+    if (!(top[0] > 1e-25f && top[0] < 1e25f && scale > 1e-30f && scale < 1e30f)) {
+      form(rstd);
+      by = scale = __fdiv_rn(top[0], kE4m3Max);
+      times = 1.f;
+    }
+    const Reciprocal inv = reciprocal_of(by);
     if (lane == 0 && in_range(p.status, row, 1, p.M, CHK_NORM2_OUT)) p.scale[row] = scale;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = lane + i * group;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) keep[i][j] *= times;
       if (v < vecs && in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
         *reinterpret_cast<uint2*>(p.q + at + 8 * v) = codes8(keep[i], inv);
     }
