@@ -37,9 +37,12 @@ cudaError_t launch_gemm(const GemmParams& p, const GemmKind& k, int sms, cudaStr
 // host's, 16 K tiles 2 to 4.  With bf16 operands all tiles are cut where one chain of
 // sums would be longer than 512 K tiles (32,768 tokens in a weight's gradient): each of its four steps
 // per K tile cuts the sum off, by up to 3.1 2^-24 of it (measured, terms of one sign), so that a
-// chain loses at most 2^-12.3 of its sum.  The gated products themselves are cut only in fp32 and where
+// chain loses at most 2^-12.3 of its sum.  So are they with fp32 operands (unless few tiles are cut into more
+// parts anyway): there 512 K tiles are 128 chunks, whose sums are rounded as they are added one
+// after the other, and the roundings of longer runs show (weights' gradients over a million
+// tokens 1.26e-6 instead of 8e-7).  The gated products themselves are cut only in fp32 and where
 // the tiles are at most half as many as run at once: their parts want g and u in memory (M=169
-// D=1888 F=136 36 -> 23 us forward, 72 -> 49 backward).
+// D=1888 F=136 36 -> 23 us forward, 72 -> 49 backward); their longest run is D = 2^16, 256 chunks.
 GemmPlan gemm_plan(int epi, bool f32, long long m, int n, int nbatch, int nseg, int kt) {
   constexpr int kSms = 152;
   const bool pair = epi == EPI_GLU || epi == EPI_DGLU || epi == EPI_GLU8;
@@ -70,20 +73,18 @@ GemmPlan gemm_plan(int epi, bool f32, long long m, int n, int nbatch, int nseg, 
   if (epi != EPI_STORE && !(f32 && 2 * count <= at_once)) return q;
   constexpr long long kChain = 512;
   const long long chain = static_cast<long long>(nseg) * kt;
-  if (!f32 && chain > kChain) {
+  const int rest = count % at_once, least = f32 ? 4 : 16;  // (K tiles of a part)
+  int split = rest == 0 || chain < 3 * least ? 1 : at_once / rest;
+  if (split > chain / least) split = static_cast<int>(chain / least);
+  if (split > kt) split = kt;
+  const int need = static_cast<int>((chain + kChain - 1) / kChain);
+  if (need > 1 && !(f32 && rest == count && split >= need)) {
     q.whole = 0;
-    q.split = static_cast<int>((chain + kChain - 1) / kChain);
+    q.split = need;
     q.nparts = count * q.split;
     q.parts_bytes = static_cast<size_t>(q.nparts) * q.rows * q.bn * sizeof(float);
     return q;
   }
-  const int rest = count % at_once;
-  if (rest == 0) return q;
-  const int least = f32 ? 4 : 16;  // K tiles of a part
-  if (chain < 3 * least) return q;
-  int split = at_once / rest;
-  if (split > chain / least) split = static_cast<int>(chain / least);
-  if (split > kt) split = kt;
   if (split < 2) return q;
   q.whole = count - rest;
   q.split = split;
