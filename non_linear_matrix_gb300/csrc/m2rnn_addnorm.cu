@@ -173,40 +173,65 @@ __global__ void __launch_bounds__(512) add_norm_kernel(Norm2Params p, int warps,
     // rounded, 1 in 10^4 lay on the other side of a middle that the formula meets.
     float top[1] = {0.f};
     float keep[NV][8];
-    const auto form = [&](float factor) {  // w r (times rstd), and the largest
-      top[0] = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = lane + i * group;
-        float o[8], w[8];
-        raw_unpack<F32, 8>(xv[i], o);
-        weights(v, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          keep[i][j] = o[j] * factor * w[j];
-          if (v < vecs) top[0] = nan_max(top[0], fabsf(keep[i][j]));
-        }
-      }
-      row_reduce<1, true>(top, warps, sm);
-    };
-    form(1.f);
-    float scale = __fdiv_rn(top[0] * rstd, kE4m3Max), by = top[0], times = kE4m3Max;
-    // (the same choice in the whole row; outside, products or squares may have left fp32's range)
-    if (!(top[0] > 1e-25f && top[0] < 1e25f && scale > 1e-30f && scale < 1e30f)) {
-      form(rstd);
-      by = scale = __fdiv_rn(top[0], kE4m3Max);
-      times = 1.f;
-    }
-    const Reciprocal inv = reciprocal_of(by);
-    if (lane == 0 && in_range(p.status, row, 1, p.M, CHK_NORM2_OUT)) p.scale[row] = scale;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = lane + i * group;
+      float w[8];
+      raw_unpack<F32, 8>(xv[i], keep[i]);
+      weights(v, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) keep[i][j] *= times;
-      if (v < vecs && in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
-        *reinterpret_cast<uint2*>(p.q + at + 8 * v) = codes8(keep[i], inv);
+      for (int j = 0; j < 8; ++j) {
+        keep[i][j] *= w[j];
+        if (v < vecs) top[0] = nan_max(top[0], fabsf(keep[i][j]));
+      }
     }
+    row_reduce<1, true>(top, warps, sm);
+    float scale = __fdiv_rn(top[0] * rstd, kE4m3Max);
+    const auto put = [&](int v, const float (&o)[8], const Reciprocal& inv) {
+      if (v < vecs && in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT))
+        *reinterpret_cast<uint2*>(p.q + at + 8 * v) = codes8(o, inv);
+    };
+    // (the whole row takes the same way)
+    if (top[0] > 1e-25f && top[0] < 1e25f && scale > 1e-30f && scale < 1e30f) {
+      const Reciprocal inv = reciprocal_of(top[0]);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) keep[i][j] *= kE4m3Max;
+        put(lane + i * group, keep[i], inv);
+      }
+    } else {
+      // Products or squares may have left fp32's range: the codes of y as it is, from r in memory
+      // (a rare row: its registers would be every row's).
+      const auto y_of = [&](int v, float (&o)[8]) {
+        Raw<F32, 8> r = raw_zero<F32, 8>();
+        if (ADD ? in_range(p.status, at + 8 * v, 8, n, CHK_NORM2_OUT) : in_range(p.status, x0 + 8 * v, 8, x_ext, CHK_NORM2_IN))
+          r = raw_load<F32, 8, false>((ADD ? static_cast<const T*>(p.r) + at : x) + 8 * v);
+        float w[8];
+        raw_unpack<F32, 8>(r, o);
+        weights(v, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = o[j] * rstd * w[j];
+      };
+      top[0] = 0.f;
+#pragma unroll 1
+      for (int v = lane; v < vecs; v += group) {
+        float o[8];
+        y_of(v, o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top[0] = nan_max(top[0], fabsf(o[j]));
+      }
+      row_reduce<1, true>(top, warps, sm);
+      scale = __fdiv_rn(top[0], kE4m3Max);
+      const Reciprocal inv = reciprocal_of(scale);
+#pragma unroll 1
+      for (int v = lane; v < vecs; v += group) {
+        float o[8];
+        y_of(v, o);
+        put(v, o, inv);
+      }
+    }
+    if (lane == 0 && in_range(p.status, row, 1, p.M, CHK_NORM2_OUT)) p.scale[row] = scale;
   }
 }
 

@@ -120,3 +120,30 @@ def test_rows_of_zeros_and_not_finite(m, D, dtype):
     q, s, _ = m.add_norm_q8(torch.full_like(r, 1e3), None, huge)
     assert (s == s[0]).all() and (q.float() == 448).all() and abs(s[0].item() * 448 / 3e38 - 1) < 2.0 ** -8
     assert m.device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,D", [(5, 72), (9, 2000), (400, 520), (7, 8200)])
+def test_far_rows_under_the_index_checks(m, M, D, dtype):
+    """Rows that leave fp32's range, with the sum in place, alone and as slices of a wider
+    buffer: the checked build finds no index outside, and both builds agree."""
+    from non_linear_matrix_gb300 import build as b
+    b.build(checked=True)
+    sizes = torch.tensor([1e-30, 1.0, 1e19, 1e25], device="cuda")[torch.arange(M, device="cuda") % 4]
+    wide = (rn(10, M, D + 16, dtype="f32") * sizes[:, None]).to(TD[dtype])
+    x, res, w = wide[:, 8:8 + D], rn(11, M, D, dtype=dtype), (rn(12, D, dtype="f32") * 1e12).to(TD[dtype])
+    got = {}
+    for which in ("normal", "checked"):
+        m.use_library(which)
+        try:
+            m.device_status(clear=True)
+            stream = res.clone()
+            got[which] = [*m.add_norm_q8(x, stream, w, out={"r": stream}), *m.add_norm_q8(x, None, w)[:2],
+                          *m.add_norm_q8(x, res, w)]
+            assert m.device_status(clear=True) == (0, 0)
+        finally:
+            m.use_library("normal")
+    raw = [[t.view(torch.uint8) for t in g] for g in got.values()]
+    assert all(torch.equal(a, b) for a, b in zip(*raw))
+    g = got["normal"]
+    assert torch.equal(g[0].view(torch.uint8), g[5].view(torch.uint8)) and torch.equal(g[2], g[7])
