@@ -87,7 +87,7 @@ int m2rnn_quant_rows(const m2rnn_norm_shape *s, const void *x, const m2rnn_rows 
  * all sizes.
  *
  * act | M2RNN_GLU_ROUND (bf16 only): they are rounded to one bf16 value there, as separate bf16
- * operations would leave them.  The backward pass then takes 55 to 65 % of the time and half of
+ * operations would leave them.  The backward pass then takes 50 to 65 % of the time and half of
  * that workspace, and dx, dwg and dwu are off by two roundings (relative 2-norm 2.35e-3, not
  * 1.66e-3).  The other functions take the flag and do nothing else for it. */
 #define M2RNN_GLU_ROUND 16

@@ -173,6 +173,17 @@ __device__ __forceinline__ void next_term(float (&v)[32], float (&t)[32]) {
   }
 }
 
+// What the rounding to bf16 leaves of v (0 where that is infinite or NaN, which stays so in the sum).
+__device__ __forceinline__ void leave_rest(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const uint32_t w = ptx::pack_bf16x2(v[i], v[i + 1]);
+    const float2 r = fma2(make_float2(ptx::bf16x2_lo(w), ptx::bf16x2_hi(w)), both(-1.f), make_float2(v[i], v[i + 1]));
+    v[i] = isfinite(r.x) ? r.x : 0.f;
+    v[i + 1] = isfinite(r.y) ? r.y : 0.f;
+  }
+}
+
 // A warp's block of 32 rows of 32 bf16 columns on its way between memory, where four lanes
 // hold a row's 64 bytes (eight rows to an instruction), and a row per lane.  In the warp's 2 KB
 // the 16-byte pieces of a row are exchanged by its number, so that neither side has
@@ -291,12 +302,15 @@ __device__ __forceinline__ void finish_bf16(const GemmParams& p, const TileAt& t
     // second term.
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out[0]);
     const size_t plane = static_cast<size_t>(p.M) * p.pitch;
-    block_store(out, k, buf, lane, g, p.status, CHK_GLU_WS);
-    block_store(out + p.aterms * plane, k, buf, lane, u, p.status, CHK_GLU_WS);
-    if (p.aterms == 2) {
-      next_term<true>(g, d);
+    if (p.aterms == 1) {
+      block_store(out, k, buf, lane, g, p.status, CHK_GLU_WS);
+      block_store(out + plane, k, buf, lane, u, p.status, CHK_GLU_WS);
+    } else {
+      block_store(out, k, buf, lane, g, p.status, CHK_GLU_WS);
+      leave_rest(g);
       block_store(out + plane, k, buf, lane, g, p.status, CHK_GLU_WS);
-      next_term<true>(u, d);
+      block_store(out + 2 * plane, k, buf, lane, u, p.status, CHK_GLU_WS);
+      leave_rest(u);
       block_store(out + 3 * plane, k, buf, lane, u, p.status, CHK_GLU_WS);
     }
   } else if constexpr (C::EPI == EPI_STORE) {
