@@ -95,7 +95,8 @@ typedef struct {
 /* Library version (major*10000 + minor*100 + patch). */
 int m2rnn_version(void);  /* 200 and later: m2rnn_shape carries Nq; 201: M2RNN_ERR_BOUNDS;
                                  202: the operators of m2rnn_block.h;
-                                 203: those of m2rnn_ffn.h */
+                                 203: those of m2rnn_ffn.h;
+                                 204: M2RNN_GLU_ROUND */
 
 /* 1 for the checked build (libm2rnn_check.so), 0 for the normal one.  The
  * checked build compiles the same kernels with an index check in front of

@@ -10,7 +10,8 @@
  * Rows.  Operators here act on each token by itself.  The inputs of the norm and of the
  * quantiser are [B,T,D] with the row description of m2rnn_block.h (NULL: contiguous); the
  * products take M tokens whose rows are `x_row` (and so on) elements apart.  Distances are
- * multiples of 16 bytes.  Weights, scales and outputs are contiguous.  An
+ * multiples of 16 bytes.  Weights, scales, incoming gradients (dy, dr, dh) and outputs are
+ * contiguous.  An
  * output must not overlap an input or another output except where a function
  * says that it may (M2RNN_ERR_INVALID_ARG).
  *
@@ -122,7 +123,7 @@ int m2rnn_glu_q8(const m2rnn_glu_shape *s, const void *x, long long x_row, const
  *     y[m,f] = xs[m] ws[f] sum_d x[m,d] w[f,d] + res[m,f]
  *
  *   x [M,D] e4m3 (rows), xs [M], w [F,D] e4m3, ws [F], res [M,F] (rows) or NULL (0) and
- *   y [M,F] in in_dtype, which must be M2RNN_BF16.  Sizes as for m2rnn_glu_q8; act is ignored.
+ *   y [M,F] in in_dtype, which must be M2RNN_BF16.  Sizes as for m2rnn_glu_q8; act has no effect (0).
  * y may be res itself (in place, contiguous). */
 int m2rnn_linear_q8(const m2rnn_glu_shape *s, const void *x, long long x_row, const float *xs,
                     const void *w, const float *ws, const void *res, long long res_row, void *y,

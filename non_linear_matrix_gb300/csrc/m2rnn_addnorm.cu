@@ -100,8 +100,10 @@ __device__ __forceinline__ size_t rows_span(const Norm2Params& p, long long batc
   return static_cast<size_t>(p.M / p.T - 1) * batch + static_cast<size_t>(p.T - 1) * token + p.D;
 }
 
-// ADD: r = x + res is stored.  Q8: the output as codes and a scale.  us by itself (floor):
-// M=65536 D=1024 79.0 (78.9), 8 bits 70.1 (69.0).
+// ADD: r = x + res is stored.  Q8: the output as codes and a scale.  us in a loop (floor), bf16, fp32:
+// M=65536 D=1024 80.3 (78.9), 157 (158), 8 bits 72.3 (69.0), 126 (128); M=4096 D=16384 81.1 (78.9),
+// 175 (158), 8 bits 80.0 (69.0), 159 (128).  Rows just above 4,096 fill little more than half of 8 warps'
+// four vectors: M=16384 D=4104 90 (79), 160 (158), 8 bits 116 (69), 186 (128).
 template <bool F32, int NV, bool ADD, bool Q8>
 __global__ void __launch_bounds__(512) add_norm_kernel(Norm2Params p, int warps, int rows_per_cta) {
   using T = typename Elem<F32>::T;
@@ -294,10 +296,13 @@ __global__ void __launch_bounds__(256, F32 ? (NV == 4 ? 4 : NV == 6 ? 3 : 2) : (
 // A CTA holds several groups of warps, each of which walks over rows with its share of dw in
 // registers.  A thread copies its vectors of the next S rows into its own places of shared
 // memory (asynchronously, so they take no registers while they are in flight: 96 KB to a
-// CTA), and reads them twice, for the two sums and for dx.  dw is summed over runs of kRun
+// CTA of 256 threads, 48 KB with one vector of bf16, 192 KB to one of 512), and reads them twice,
+// for the two sums and for dx.  dw is summed over runs of kRun
 // rows, and those apart, so that long sums do not drift; then over groups, then over CTAs
 // (sum_parts), always in the same order.  M=32768 D=2048: 88 us, 111 with the next row in
-// registers instead.
+// registers instead.  With dw, in a loop, TB/s of bf16, fp32: D=1024 6.1, 4.0, D=4096 6.0, 4.1.  Above
+// 4,096 there is one CTA to an SM, in fp32 with one slot, so that a row's copies and
+// arithmetic take turns: D=4104 2.2, 2.6, D=8192 4.2, 3.3, D=16384 5.9, 3.6.
 constexpr int kRun = 64;
 template <bool F32, int NV>
 struct BwdCfg {
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(BwdCfg<F32, NV>::CTA, NV == 4 ? 1 : 2) add_nor
 }
 
 // Vectors per thread and warps per row: the fewest warps (1, 2, 4, 8, 16) whose threads
-// hold the row in four vectors each, and then as few vectors as that takes.
+// hold the row in `most` vectors each (four where 16 warps do not), and then as few vectors as that takes.
 struct RowPlan {
   int nv, warps;
 };
@@ -541,8 +546,8 @@ cudaError_t launch_bwd_nv(const Norm2Params& p, int warps, cudaStream_t st) {
   const SumOut o = {{p.dw, nullptr, nullptr}, {p.D, 0, 0}};
   return launch_sum_parts(p.part, p.nparts, o, p.status, CHK_NORM2_PARAM, st);
 }
-// Two vectors per thread (the next row's are in flight beside them), four only where 16 warps
-// would not hold the row otherwise.
+// Up to 8 warps of two vectors per thread (the next rows' are in flight beside them); rows of more than
+// 4,096 go to 16 warps of four, of which those up to 8,192 leave half of the places empty.
 RowPlan bwd_plan(int D) {
   const int vecs = D / 8;
   int warps = 1;

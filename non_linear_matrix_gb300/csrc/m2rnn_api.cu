@@ -511,7 +511,7 @@ int decode_impl(const m2rnn_shape* s, const void* q, const void* k, const void* 
 
 extern "C" {
 
-int m2rnn_version(void) { return 203; }
+int m2rnn_version(void) { return 204; }
 
 int m2rnn_checked(void) { return M2RNN_CHECK ? 1 : 0; }
 

@@ -242,7 +242,7 @@ cudaError_t launch_t(const FewParams& p, cudaStream_t st) {
                      : launch_nt<EPI, E4M3, F32, 8>(p, st);
 }
 
-// A row to 64 threads (of D = 520, one vector each); blockIdx.y: the matrix.
+// A row to 64 threads, 8 elements of each at a turn; blockIdx.y: the matrix.
 __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ SplitParams p) {
   let_next_begin();
   const int which = blockIdx.y, vecs = p.D / 8;

@@ -39,7 +39,7 @@ struct Norm2Params {
   float* part;  // backward: [nparts][D]
   float* dw;
   long long xb, xt, rb, rt;  // rows of x (r in the backward pass) and res
-  long long M;               // B * T rows of
+  long long M;               // B * T rows of D elements
   int T, D;                  // T per item (M where the rows are evenly spaced)
   int nparts;
   float eps;
@@ -105,9 +105,15 @@ struct FewParams {
   int M, D, F, act;
   int* status;
 };
-// Up to 16 tokens (fp32: 64) go this way.  us at D=2048 F=5632, gated products, bf16: 8 tokens
-// 10.0 against 17.9 of the tiles, 16 tokens 12.1 against 18.6, 32 tokens 28 against 11.7; e4m3: 16 tokens
-// 9.3 against 10.9, 32 16.1 against 10.5; fp32 at D=1024 F=2816: 32 tokens 20 against 33, 64 30 against 34.
+// Up to 16 tokens (fp32: 64) go this way.  us in a CUDA graph over 450 MB of weights, so from HBM,
+// 16 tokens this way | 17 by the tiles:
+//   D, F             gated bf16    gated e4m3    8-bit product (F to D)
+//   1024, 2816       6.3 |  7.3    5.4 |  5.8    6.8 |  9.0
+//   2048, 5632      12.7 | 18.0   10.9 | 11.4    7.2 | 13.5
+//   4096, 11008     43.6 | 47.8   28.1 | 28.8   16.5 | 23.0
+// fp32, 64 | 65 tokens: D=512 F=1408 12.0 | 17.4, D=1024 F=2816 38.1 | 27.7 (32 tokens 26.5).
+// At D=2048 the tiles take 17.4 to 18.5 for 17 to 31 bf16 tokens and 12.3 from 32 on, for e4m3 10.6 to 11.5
+// below 64 and 8.6 from there: the products are the same; why is not known.
 inline int few_most(bool f32) { return f32 ? 64 : 16; }
 cudaError_t launch_few(const FewParams& p, int epi, bool e4m3, bool f32, cudaStream_t st);
 

@@ -1023,8 +1023,8 @@ def add_norm_q8(x, res=None, w=None, eps: float = 1e-6, *, out=None, stream=None
 def add_norm_bwd(r, dy, w=None, dr=None, eps: float = 1e-6, *, want_dw: bool = True, workspace=None,
                  out=None, stream=None):
     """Gradient of ``add_norm_fwd`` at r [..., D], its stored sum (or x, without
-    ``res``): dict(dx, dw).  dy is dL/dy and dr dL/dr past the norm (None = 0), of r's
-    dtype; dx (r's dtype) is the gradient of x and of res alike; dw [D] is fp32
+    ``res``): dict(dx, dw).  dy is dL/dy and dr dL/dr past the norm (None = 0), contiguous, of
+    r's dtype; dx (r's dtype) is the gradient of x and of res alike; dw [D] is fp32
     (None without a weight or with want_dw=False).  dx may be dr or dy itself."""
     s, rows = _norm_shape(r)
     D, dev = s.D, r.device
