@@ -35,7 +35,8 @@ cudaError_t launch_gemm(const GemmParams& p, const GemmKind& k, int sms, cudaStr
 // CTA one, each of 16 K tiles (fp32, whose K tiles are six products: 4) at least, and not where
 // the whole is shorter than three of those: joining the parts takes 2 us and a launch of the
 // host's, 16 K tiles 2 to 4.  With bf16 operands all tiles are cut where one chain of
-// sums would be longer than 512 K tiles (32,768 tokens in a weight's gradient): each of its four steps
+// sums over all segments would be longer than 512 K tiles (16,384 tokens in a weight's gradient,
+// 32,768 with one term): each of its four steps
 // per K tile cuts the sum off, by up to 3.1 2^-24 of it (measured, terms of one sign), so that a
 // chain loses at most 2^-12.3 of its sum.  So are they with fp32 operands (unless few tiles are cut into more
 // parts anyway): there 512 K tiles are 128 chunks, whose sums are rounded as they are added one
